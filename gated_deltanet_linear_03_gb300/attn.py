@@ -1,0 +1,237 @@
+"""The 8-bit paged key/value cache and attention over it (include/gdn.h: gdn_kv_append, gdn_kv_read, gdn_attend).
+
+    from gated_deltanet_linear_03_gb300 import attn
+    cache = attn.alloc_cache(n_pages, hkv, page_size, d, n_slots)            # pages, scales, open blocks
+    q, _ = attn.kv_append(k, v, cos, sin, cu_seqlens, past_lens, block_table, *cache, q=q, open_out=cache[-1])
+    out = attn.attend(q, *cache[:4], block_table, cu_seqlens, kv_lens, max_q_len=..., max_kv_len=...)
+
+Argument marshalling only, like :mod:`gdn`: the kernels run in ``libgdn.so``, there is no CPU fallback, and a
+call only enqueues work on the current stream of the tensors' device (or ``stream``).
+"""
+from __future__ import annotations
+
+import math
+from typing import Optional, Tuple
+
+import torch
+
+from .gdn import DTYPE, GDN_OK, GdnError, load_library
+
+KV_BLOCK = 16                                             # tokens that share a scale
+FORMAT = {torch.int8: 0, torch.float8_e4m3fn: 1}
+
+
+def _contiguous(name: str, t: torch.Tensor, dtype, ndim: int, device) -> int:
+    """Check a tensor and return its address."""
+    if t.dtype is not dtype or t.dim() != ndim or t.device != device or not t.is_contiguous():
+        _refuse(name, t, dtype, ndim, device)
+    return t.data_ptr()
+
+
+def _refuse(name, t, dtype, ndim, device):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must be a contiguous {ndim}-d tensor")
+
+
+def _device(t: torch.Tensor, name: str) -> torch.device:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    return t.device
+
+
+def _launch(fn, name, device, stream, *args):
+    """Call ``fn(*args, stream)`` with the tensors' device current."""
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        handle = stream.cuda_stream
+    if torch._C._cuda_getDevice() == device.index:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, handle)
+    if st != GDN_OK:
+        raise GdnError(st, name)
+
+
+def _token_rows(name: str, t: torch.Tensor, heads: int, d: int, device) -> Tuple[int, int]:
+    """Address and token stride of a bf16 [T, heads, d] tensor whose head vectors are contiguous."""
+    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.device != device:
+        _refuse(name, t, torch.bfloat16, 3, device)
+    if t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {tuple(t.shape)}")
+    stride = t.stride()
+    if stride[2] != 1 or (heads > 1 and stride[1] != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), max(stride[0], heads * d) if t.shape[0] <= 1 else stride[0]
+
+
+def _pool(k_pages, v_pages, k_scales, v_scales, block_table, device):
+    """Checked (addresses, (table address, max_pages, n_pages, page_size, format), hkv, d) of a cache."""
+    if k_pages.dtype not in FORMAT:
+        raise ValueError(f"k_pages must be int8 or float8_e4m3fn, got {k_pages.dtype}")
+    kp = _contiguous("k_pages", k_pages, k_pages.dtype, 4, device)
+    vp = _contiguous("v_pages", v_pages, k_pages.dtype, 4, device)
+    ks = _contiguous("k_scales", k_scales, torch.float32, 3, device)
+    vs = _contiguous("v_scales", v_scales, torch.float32, 3, device)
+    table = _contiguous("block_table", block_table, torch.int32, 2, device)
+    n_pages, hkv, page, d = k_pages.shape
+    if v_pages.shape != k_pages.shape:
+        raise ValueError("v_pages must have the shape of k_pages")
+    want = (n_pages, hkv, page // KV_BLOCK)
+    if k_scales.shape != want or v_scales.shape != want:
+        raise ValueError(f"k_scales and v_scales must be {want}")
+    return (kp, vp, ks, vs), (table, block_table.shape[1], n_pages, page, FORMAT[k_pages.dtype]), hkv, d
+
+
+def alloc_cache(n_pages: int, hkv: int, page_size: int, d: int, n_slots: int, dtype=torch.int8, device="cuda"):
+    """An empty cache: ``(k_pages, v_pages, k_scales, v_scales, open_blocks)`` in the layouts of include/gdn.h."""
+    pages = [torch.zeros(n_pages, hkv, page_size, d, dtype=torch.int8, device=device).view(dtype) for _ in range(2)]
+    scales = [torch.zeros(n_pages, hkv, page_size // KV_BLOCK, dtype=torch.float32, device=device) for _ in range(2)]
+    return (*pages, *scales, torch.zeros(n_slots, 2, hkv, KV_BLOCK, d, dtype=torch.bfloat16, device=device))
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, cos: Optional[torch.Tensor], sin: Optional[torch.Tensor],
+              cu_seqlens: torch.Tensor, past_lens: torch.Tensor, block_table: torch.Tensor, k_pages: torch.Tensor,
+              v_pages: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor, open_in: torch.Tensor, *,
+              open_out: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+              q_out: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None, interleaved: bool = False,
+              stream=None) -> Tuple[Optional[torch.Tensor], torch.Tensor]:
+    """Run ``gdn_kv_append``: rotate ``k`` (and ``q``) to positions ``past_lens[n], past_lens[n] + 1, ...`` and put
+    ``k`` and ``v`` into the cache (updated in place).  Returns ``(rotated q or None, open_out)``.
+
+    ``k``, ``v``, ``q`` are bf16 [T, heads, d]; they may be slices of one projection (head vectors contiguous, any
+    token stride that is a multiple of 8).  ``cos`` / ``sin``: fp32 [positions, rot / 2], or None for no rotation.
+    ``open_in`` (bf16 [slots, 2, hkv, 16, d]) holds each sequence's unfinished block; ``open_out`` defaults to
+    updating it in place.  ``q_out`` may be ``q``."""
+    lib = load_library()
+    dev = _device(k, "k")
+    pages, pool, hkv, d = _pool(k_pages, v_pages, k_scales, v_scales, block_table, dev)
+    T = k.shape[0]
+    kp, k_stride = _token_rows("k", k, hkv, d, dev)
+    vp, v_stride = _token_rows("v", v, hkv, d, dev)
+    if v.shape[0] != T:
+        raise ValueError("k and v must have the same tokens")
+    cu = _contiguous("cu_seqlens", cu_seqlens, torch.int32, 1, dev)
+    past = _contiguous("past_lens", past_lens, torch.int32, 1, dev)
+    n = past_lens.shape[0]
+    if cu_seqlens.shape[0] != n + 1 or block_table.shape[0] != n:
+        raise ValueError("cu_seqlens, past_lens and block_table must describe the same sequences")
+    rot = positions = cp = sp = 0
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    if cos is not None:
+        cp = _contiguous("cos", cos, torch.float32, 2, dev)
+        sp = _contiguous("sin", sin, torch.float32, 2, dev)
+        if cos.shape != sin.shape:
+            raise ValueError("cos and sin must have the same shape")
+        positions, rot = cos.shape[0], 2 * cos.shape[1]
+    op = _contiguous("open_in", open_in, torch.bfloat16, 5, dev)
+    if open_in.shape[1:] != (2, hkv, KV_BLOCK, d):
+        raise ValueError(f"open_in must be [slots, 2, {hkv}, {KV_BLOCK}, {d}]")
+    if open_out is None:
+        open_out = open_in
+    oo = _contiguous("open_out", open_out, torch.bfloat16, 5, dev)
+    if open_out.shape != open_in.shape:
+        raise ValueError("open_out must have the shape of open_in")
+    sl = 0
+    if slots is not None:
+        sl = _contiguous("slots", slots, torch.int32, 1, dev)
+        if slots.shape[0] != n:
+            raise ValueError("slots must name one slot for each sequence")
+    hq = qp = q_stride = qo = 0
+    if q is not None:
+        hq = q.shape[1] if q.dim() == 3 else 0
+        qp, q_stride = _token_rows("q", q, hq, d, dev)
+        if q.shape[0] != T:
+            raise ValueError("q and k must have the same tokens")
+        if q_out is None:
+            q_out = torch.empty(T, hq, d, dtype=torch.bfloat16, device=dev)
+        qo = _contiguous("q_out", q_out, torch.bfloat16, 3, dev)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have the shape of q")
+        if T == 0:
+            qp = qo = 0
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _launch(lib.gdn_kv_append, "gdn_kv_append", dev, stream, n, T, hq, hkv, d, rot, qp, q_stride, kp, k_stride, vp,
+            v_stride, cp, sp, positions, int(bool(interleaved)), cu, past, *pool, *pages, op, oo, sl,
+            open_in.shape[0], qo)
+    return q_out, open_out
+
+
+def kv_read(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+            block_table: torch.Tensor, cu_tokens: torch.Tensor, total_tokens: int, *, out_dtype=torch.bfloat16,
+            stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Run ``gdn_kv_read``: the values of the first ``cu_tokens[n + 1] - cu_tokens[n]`` tokens of every sequence,
+    packed: ``(k, v)``, each [total_tokens, hkv, d].  ``total_tokens`` is ``cu_tokens``'s last entry, known on the
+    host."""
+    lib = load_library()
+    dev = _device(k_pages, "k_pages")
+    pages, pool, hkv, d = _pool(k_pages, v_pages, k_scales, v_scales, block_table, dev)
+    cu = _contiguous("cu_tokens", cu_tokens, torch.int32, 1, dev)
+    n = cu_tokens.shape[0] - 1
+    if block_table.shape[0] != n:
+        raise ValueError("cu_tokens and block_table must describe the same sequences")
+    k = torch.empty(total_tokens, hkv, d, dtype=out_dtype, device=dev)
+    v = torch.empty(total_tokens, hkv, d, dtype=out_dtype, device=dev)
+    _launch(lib.gdn_kv_read, "gdn_kv_read", dev, stream, n, total_tokens, hkv, d, cu, *pool, *pages, k.data_ptr(),
+            v.data_ptr(), DTYPE[out_dtype])
+    return k, v
+
+
+def attend_workspace_size(n_seqs: int, total_tokens: int, hq: int, hkv: int, d: int, max_q_len: int,
+                          max_kv_len: int) -> int:
+    """Bytes of workspace that :func:`attend` needs for this problem (``gdn_attend_workspace_size``)."""
+    import ctypes
+    st = ctypes.c_int(0)
+    need = load_library().gdn_attend_workspace_size(n_seqs, total_tokens, hq, hkv, d, max_q_len, max_kv_len, st)
+    if st.value != GDN_OK:
+        raise GdnError(st.value, "gdn_attend_workspace_size")
+    return int(need)
+
+
+def attend(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Tensor,
+           v_scales: torch.Tensor, block_table: torch.Tensor, cu_seqlens: torch.Tensor, kv_lens: torch.Tensor, *,
+           max_q_len: int, max_kv_len: int, sm_scale: Optional[float] = None, window: int = 0, sinks: int = 0,
+           out: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16, workspace: Optional[torch.Tensor] = None,
+           stream=None) -> torch.Tensor:
+    """Run ``gdn_attend``: causal attention of the queries ``q`` (bf16 [T, hq, d], rotated) over the cache, which
+    already holds their own keys and values.  ``kv_lens`` (int32 [n]) counts each sequence's cached tokens;
+    ``max_q_len`` and ``max_kv_len`` bound the device values.  With ``window`` a query sees the last ``window``
+    tokens (its own included) and the first ``sinks``.  ``sm_scale`` defaults to 1 / sqrt(d)."""
+    lib = load_library()
+    dev = _device(q, "q")
+    pages, pool, hkv, d = _pool(k_pages, v_pages, k_scales, v_scales, block_table, dev)
+    qp = _contiguous("q", q, torch.bfloat16, 3, dev)
+    T, hq = q.shape[0], q.shape[1]
+    if q.shape[2] != d:
+        raise ValueError(f"q must be [tokens, heads, {d}], got {tuple(q.shape)}")
+    cu = _contiguous("cu_seqlens", cu_seqlens, torch.int32, 1, dev)
+    lens = _contiguous("kv_lens", kv_lens, torch.int32, 1, dev)
+    n = kv_lens.shape[0]
+    if cu_seqlens.shape[0] != n + 1 or block_table.shape[0] != n:
+        raise ValueError("cu_seqlens, kv_lens and block_table must describe the same sequences")
+    if out is None:
+        out = torch.empty(T, hq, d, dtype=out_dtype, device=dev)
+    op = _contiguous("out", out, out.dtype, 3, dev)
+    if out.shape != q.shape or out.dtype not in DTYPE:
+        raise ValueError("out must have the shape of q, in bf16 or fp32")
+    max_q_len = min(max_q_len, T)
+    if workspace is None:
+        need = attend_workspace_size(n, T, hq, hkv, d, max_q_len, max_kv_len)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the other tensors' device")
+    table, max_pages, n_pages, page, fmt = pool
+    _launch(lib.gdn_attend, "gdn_attend", dev, stream, n, T, hq, hkv, d, qp, *pages, table, max_pages, n_pages, page,
+            fmt, cu, lens, max_q_len, max_kv_len, 1.0 / math.sqrt(d) if sm_scale is None else sm_scale, window, sinks,
+            op, DTYPE[out.dtype], workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return out

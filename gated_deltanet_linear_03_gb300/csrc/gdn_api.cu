@@ -130,9 +130,16 @@ __global__ void selftest_wait_kernel(uint64_t limit_ns, unsigned int *err) {
 
 }  // namespace
 
+// The host helpers that the other entry-point files share.
+namespace gdn {
+unsigned int *error_word() { return device_error_ptr(); }
+gdn_status on_current_device(const void *p, cudaStream_t stream) { return check_on_current_device(p, stream); }
+int multiprocessor_count() { return sm_count(); }
+}  // namespace gdn
+
 extern "C" {
 
-int gdn_version(void) { return 200; }
+int gdn_version(void) { return 210; }
 
 const char *gdn_status_string(gdn_status s) {
     switch (s) {

@@ -1,0 +1,329 @@
+// gdn_kv_append and gdn_kv_read: the paged 8-bit cache's writer and reader.
+//
+// Append.  For a 16-token block of one head, with rows x_0 .. x_15 in bf16 (keys after their rotation),
+//     A = max(max |x|, 2^-60),   scale = A / Q,   code = round(x * (Q / A)).
+// A block is quantised as a whole, so its scale needs all of its rows; a sequence's unfinished block keeps its
+// rows in bf16 (open_in / open_out) and is quantised afresh from them whenever it grows.  That costs at most
+// 15 rows a head and call, and makes the cache independent of how tokens were divided into calls.
+// One CTA takes one (block, head): D threads hold K and V, two 8-element pieces of each per thread, so the
+// rows are read once, the maximum is a CTA reduction, and codes leave as 8-byte pieces of full lines.  The
+// queries' rotation, most of the bytes with grouped heads, runs in the same launch on further CTAs.
+// Bound by memory: T (hq + 2 hkv) d 2-byte reads, T hq d 2-byte and 2 T hkv d 1-byte writes.
+#include "kv_cache.cuh"
+
+namespace gdn {
+namespace {
+
+__device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
+    x[0] = bf16_lo(u.x); x[1] = bf16_hi(u.x); x[2] = bf16_lo(u.y); x[3] = bf16_hi(u.y);
+    x[4] = bf16_lo(u.z); x[5] = bf16_hi(u.z); x[6] = bf16_lo(u.w); x[7] = bf16_hi(u.w);
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+    return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+}
+
+// 8 consecutive table entries.
+__device__ __forceinline__ void load8(const float *__restrict__ p, float (&x)[8]) {
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+
+// Interleaved pairs inside one piece of 8 elements: cos and sin of its four pairs.
+__device__ __forceinline__ void rotate_pairs(float (&x)[8], const float *__restrict__ cos, const float *__restrict__ sin) {
+    const float4 c = __ldg(reinterpret_cast<const float4 *>(cos)), s = __ldg(reinterpret_cast<const float4 *>(sin));
+    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = x[2 * i], b = x[2 * i + 1];
+        x[2 * i] = a * cc[i] - b * ss[i];
+        x[2 * i + 1] = b * cc[i] + a * ss[i];
+    }
+}
+
+// Piece c (8 elements) of a key head vector `row`, rotated.
+__device__ __forceinline__ uint4 rotated_piece(const __nv_bfloat16 *__restrict__ row, int c, int rot, int interleaved,
+                                               const float *__restrict__ cos, const float *__restrict__ sin) {
+    const uint4 raw = *reinterpret_cast<const uint4 *>(row + 8 * c);
+    if (8 * c >= rot) return raw;
+    float x[8];
+    unpack8(raw, x);
+    if (interleaved) {
+        rotate_pairs(x, cos + 4 * c, sin + 4 * c);
+    } else {
+        const bool first = 16 * c < rot;                     // the a-half of the pairs
+        const int other = first ? c + rot / 16 : c - rot / 16;
+        float y[8], cc[8], ss[8];
+        unpack8(*reinterpret_cast<const uint4 *>(row + 8 * other), y);
+        const int at = 8 * (first ? c : other);
+        load8(cos + at, cc);
+        load8(sin + at, ss);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = first ? x[i] * cc[i] - y[i] * ss[i] : x[i] * cc[i] + y[i] * ss[i];
+    }
+    return pack8(x);
+}
+
+// Largest magnitude of 8 bf16 values as the bits of a float: ordered like the magnitudes, with infinity above
+// every finite number and NaN above infinity.
+__device__ __forceinline__ uint32_t amax_bits(const uint4 &u) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, max((w[i] << 16) & 0x7fff0000u, w[i] & 0x7fff0000u));
+    return m;
+}
+
+template <int FMT>
+__device__ __forceinline__ uint2 quantise8(const uint4 &u, float inv) {
+    float x[8];
+    unpack8(u, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] *= inv;
+    return make_uint2(values_to_codes<FMT>(x[0], x[1], x[2], x[3]), values_to_codes<FMT>(x[4], x[5], x[6], x[7]));
+}
+
+// Query CTAs: each thread rotates one pair of pieces (or one interleaved piece, or copies one past rot).  Both
+// pieces of a pair are read before either is written, so q_out may be q.
+__device__ __forceinline__ void rotate_queries(const AppendProblem &p, long first, int threads) {
+    const int pieces = p.d / 8;
+    const bool in_place = p.q_out == p.q;
+    const int turned = p.interleaved ? p.rot / 8 : p.rot / 16;      // units that rotate
+    const int units = turned + (in_place ? 0 : pieces - p.rot / 8);
+    if (units == 0) return;
+    const long all = (long)p.total * p.hq * units;
+    for (long i = first; i < all; i += threads) {
+        const int u = (int)(i % units);
+        const long row = i / units;
+        const int t = (int)(row / p.hq), h = (int)(row % p.hq);
+        const __nv_bfloat16 *src = p.q + t * p.q_stride + (long)h * p.d;
+        __nv_bfloat16 *dst = p.q_out + row * p.d;
+        if (u >= turned) {
+            const int c = p.rot / 8 + u - turned;
+            *reinterpret_cast<uint4 *>(dst + 8 * c) = *reinterpret_cast<const uint4 *>(src + 8 * c);
+            continue;
+        }
+        const int n = sequence_of(p.cu, p.n_seqs, t);
+        const int pos = p.past[n] + t - p.cu[n];
+        if (pos < 0 || pos >= p.n_positions) {
+            raise_error(p.err, kErrInternal);
+            continue;
+        }
+        const float *cos = p.cos + (size_t)pos * (p.rot / 2), *sin = p.sin + (size_t)pos * (p.rot / 2);
+        if (p.interleaved) {
+            float x[8];
+            unpack8(*reinterpret_cast<const uint4 *>(src + 8 * u), x);
+            rotate_pairs(x, cos + 4 * u, sin + 4 * u);
+            *reinterpret_cast<uint4 *>(dst + 8 * u) = pack8(x);
+        } else {
+            const int v = u + p.rot / 16;
+            float a[8], b[8], cc[8], ss[8];
+            unpack8(*reinterpret_cast<const uint4 *>(src + 8 * u), a);
+            unpack8(*reinterpret_cast<const uint4 *>(src + 8 * v), b);
+            load8(cos + 8 * u, cc);
+            load8(sin + 8 * u, ss);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float x = a[e] * cc[e] - b[e] * ss[e];
+                b[e] = b[e] * cc[e] + a[e] * ss[e];
+                a[e] = x;
+            }
+            *reinterpret_cast<uint4 *>(dst + 8 * u) = pack8(a);
+            *reinterpret_cast<uint4 *>(dst + 8 * v) = pack8(b);
+        }
+    }
+}
+
+// CTAs that hold blocks: sequence n's blocks start at slot cu[n] / 16 + 2 n, which leaves room for
+// ceil((past % 16 + new) / 16) <= floor(new / 16) + 2 of them without a scan over the sequences.
+__host__ __device__ inline long block_slots(int n_seqs, int total) { return total / kKvBlock + 2L * n_seqs; }
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(D) kv_append_kernel(const __grid_constant__ AppendProblem p) {
+    constexpr int PIECES = D / 8, ROWS = D / PIECES;   // 8 rows per pass of the CTA, two passes
+    __shared__ uint32_t part[2][D / 32];
+    const long kv_ctas = block_slots(p.n_seqs, p.total) * p.pool.hkv;
+    if (blockIdx.x >= kv_ctas) {
+        rotate_queries(p, ((long)blockIdx.x - kv_ctas) * D + threadIdx.x, (int)(gridDim.x - kv_ctas) * D);
+        return;
+    }
+    const int slot = blockIdx.x / p.pool.hkv, h = blockIdx.x % p.pool.hkv;
+    // the sequence whose slots hold this one
+    int n = 0;
+    for (int hi = p.n_seqs; hi - n > 1;) {
+        const int mid = (n + hi) >> 1;
+        if (p.cu[mid] / kKvBlock + 2 * mid <= slot) n = mid;
+        else hi = mid;
+    }
+    const int c0 = min(max(p.cu[n], 0), p.total), c1 = min(max(p.cu[n + 1], c0), p.total), len = c1 - c0;
+    const int past = p.past[n];
+    const int end = past <= 0x7fffffff - len ? past + len : -1;
+    const int local = slot - (p.cu[n] / kKvBlock + 2 * n);
+    if (len == 0 && past >= 0 && past % kKvBlock == 0) return;
+    const int os = p.slots ? p.slots[n] : n;
+    const int first = past / kKvBlock, last = (end - 1) / kKvBlock;
+    if (past < 0 || end < 0 || (p.rot > 0 && end > p.n_positions) || (long)end > (long)p.pool.max_pages * p.pool.page_size ||
+        os < 0 || os >= p.n_slots) {
+        if (threadIdx.x == 0) raise_error(p.err, kErrInternal);
+        return;
+    }
+    if (local > last - first) return;
+    // The first block reads open_in, the last writes open_out, which may be the same memory: when they are
+    // different blocks, one CTA does both, in that order.
+    const bool open = end % kKvBlock != 0;
+    if (open && local > 0 && local == last - first) return;
+    const int c = threadIdx.x % PIECES, r0 = threadIdx.x / PIECES;
+
+    for (int blk = first + local;; blk = last) {
+        uint4 x[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = r0 + i * ROWS, at = blk * kKvBlock + row;
+            x[0][i] = x[1][i] = make_uint4(0, 0, 0, 0);
+            if (at < past) {
+                const __nv_bfloat16 *o = p.open_in + (((size_t)os * 2 * p.pool.hkv + h) * kKvBlock + row) * D + 8 * c;
+                x[0][i] = *reinterpret_cast<const uint4 *>(o);
+                x[1][i] = *reinterpret_cast<const uint4 *>(o + (size_t)p.pool.hkv * kKvBlock * D);
+            } else if (at < end) {
+                const long t = c0 + at - past;
+                x[1][i] = *reinterpret_cast<const uint4 *>(p.v + t * p.v_stride + (long)h * D + 8 * c);
+                x[0][i] = rotated_piece(p.k + t * p.k_stride + (long)h * D, c, p.rot, p.interleaved,
+                                        p.cos + (size_t)at * (p.rot / 2), p.sin + (size_t)at * (p.rot / 2));
+            }
+        }
+        uint32_t m[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            m[j] = __reduce_max_sync(0xffffffffu, max(amax_bits(x[j][0]), amax_bits(x[j][1])));
+            if (threadIdx.x % 32 == 0) part[j][threadIdx.x / 32] = m[j];
+        }
+        __syncthreads();
+        float amax[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t a = 0;
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) a = max(a, part[j][w]);
+            amax[j] = __uint_as_float(max(a, __float_as_uint(kAmaxFloor)));
+        }
+        const int page = p.pool.table[(size_t)n * p.pool.max_pages + blk * kKvBlock / p.pool.page_size];
+        const int in_page = blk * kKvBlock % p.pool.page_size;
+        if (page < 0 || page >= p.pool.n_pages) {
+            if (threadIdx.x == 0) raise_error(p.err, kErrInternal);
+        } else {
+            const size_t head = (size_t)page * p.pool.hkv + h;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const bool finite = amax[j] <= 3.4028234e38f;     // false for infinity and NaN: codes 0, scale as it is
+                const float inv = kv_code_max<FMT>() / amax[j];
+                uint8_t *dst = (j ? p.v_pages : p.k_pages) + (head * p.pool.page_size + in_page) * D;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    *reinterpret_cast<uint2 *>(dst + (size_t)(r0 + i * ROWS) * D + 8 * c) =
+                        finite ? quantise8<FMT>(x[j][i], inv) : make_uint2(0, 0);
+                if (threadIdx.x == 0)
+                    (j ? p.v_scales : p.k_scales)[head * (p.pool.page_size / kKvBlock) + in_page / kKvBlock] =
+                        amax[j] / kv_code_max<FMT>();
+            }
+        }
+        if (open && blk == last) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int row = r0 + i * ROWS;
+                if (row >= end % kKvBlock) continue;
+                __nv_bfloat16 *o = p.open_out + (((size_t)os * 2 * p.pool.hkv + h) * kKvBlock + row) * D + 8 * c;
+                *reinterpret_cast<uint4 *>(o) = x[0][i];
+                *reinterpret_cast<uint4 *>(o + (size_t)p.pool.hkv * kKvBlock * D) = x[1][i];
+            }
+        }
+        if (!open || local > 0 || blk == last) return;
+        __syncthreads();   // part is free again
+    }
+}
+
+// One thread reads 16 codes of K and of V (one 16-byte load each) and writes 16 values of each.
+template <int FMT, bool F32>
+__global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ ReadProblem p) {
+    const int units = p.d / 16;
+    const long i = (long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= (long)p.total * p.pool.hkv * units) return;
+    const int u = (int)(i % units);
+    const long row = i / units;                       // (token, head)
+    const int t = (int)(row / p.pool.hkv), h = (int)(row % p.pool.hkv);
+    const int n = sequence_of(p.cu, p.n_seqs, t);
+    const int at = t - p.cu[n];
+    int page = -1;
+    if (at >= 0 && at < (long)p.pool.max_pages * p.pool.page_size)
+        page = p.pool.table[(size_t)n * p.pool.max_pages + at / p.pool.page_size];
+    const bool ok = page >= 0 && page < p.pool.n_pages;
+    if (!ok) raise_error(p.err, kErrInternal);
+    const size_t head = (size_t)(ok ? page : 0) * p.pool.hkv + h;
+    const int in_page = at % p.pool.page_size;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        uint4 codes = make_uint4(0, 0, 0, 0);
+        float scale = 0.f;
+        if (ok) {
+            codes = __ldg(reinterpret_cast<const uint4 *>((j ? p.v_pages : p.k_pages) + (head * p.pool.page_size + in_page) * p.d + 16 * u));
+            scale = __ldg((j ? p.v_scales : p.k_scales) + head * (p.pool.page_size / kKvBlock) + in_page / kKvBlock);
+        }
+        const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+        float x[16];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            uint32_t lo, hi;
+            codes_to_f16x2<FMT>(w[e], lo, hi);
+            const float2 a = f16x2_to_float2(lo), b = f16x2_to_float2(hi);
+            x[4 * e] = a.x * scale; x[4 * e + 1] = a.y * scale; x[4 * e + 2] = b.x * scale; x[4 * e + 3] = b.y * scale;
+        }
+        void *out = j ? p.v_out : p.k_out;
+        const size_t o = (size_t)row * p.d + 16 * u;
+        if (F32) {
+            float4 *f = reinterpret_cast<float4 *>(static_cast<float *>(out) + o);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+        } else {
+            uint4 *b = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + o);
+            b[0] = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+            b[1] = make_uint4(pack2(x[8], x[9]), pack2(x[10], x[11]), pack2(x[12], x[13]), pack2(x[14], x[15]));
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const AppendProblem &p) {
+    const long kv_ctas = block_slots(p.n_seqs, p.total) * p.pool.hkv;
+    long q_ctas = 0;
+    if (p.q) {
+        const long units = (p.interleaved ? p.rot / 8 : p.rot / 16) + (p.q_out == p.q ? 0 : p.d / 8 - p.rot / 8);
+        q_ctas = ((long)p.total * p.hq * units + 2 * p.d - 1) / (2 * p.d);   // two units a thread
+    }
+    if (kv_ctas + q_ctas > 2147483647L) return cudaErrorInvalidValue;
+    using Fn = void (*)(const AppendProblem);
+    const bool e4m3 = p.format == GDN_KV_E4M3;
+    const Fn fn = p.d == 64 ? (e4m3 ? kv_append_kernel<64, GDN_KV_E4M3> : kv_append_kernel<64, GDN_KV_INT8>)
+                  : p.d == 128 ? (e4m3 ? kv_append_kernel<128, GDN_KV_E4M3> : kv_append_kernel<128, GDN_KV_INT8>)
+                               : (e4m3 ? kv_append_kernel<256, GDN_KV_E4M3> : kv_append_kernel<256, GDN_KV_INT8>);
+    fn<<<(unsigned)(kv_ctas + q_ctas), p.d, 0, p.stream>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_kv_read(const ReadProblem &p) {
+    const long ctas = ((long)p.total * p.pool.hkv * (p.d / 16) + 255) / 256;
+    if (ctas == 0) return cudaSuccess;
+    if (ctas > 2147483647L) return cudaErrorInvalidValue;
+    using Fn = void (*)(const ReadProblem);
+    const bool e4m3 = p.format == GDN_KV_E4M3;
+    const Fn fn = p.out_f32 ? (e4m3 ? kv_read_kernel<GDN_KV_E4M3, true> : kv_read_kernel<GDN_KV_INT8, true>)
+                            : (e4m3 ? kv_read_kernel<GDN_KV_E4M3, false> : kv_read_kernel<GDN_KV_INT8, false>);
+    fn<<<(unsigned)ctas, 256, 0, p.stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace gdn

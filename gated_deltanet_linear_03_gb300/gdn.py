@@ -25,7 +25,8 @@ DTYPE = {torch.bfloat16: 0, torch.float32: 1}
 EXPORTS = ("gdn_prefill", "gdn_prefill_chunked_phase", "gdn_prefill_workspace_size", "gdn_decode_step",
            "gdn_device_error", "gdn_status_string", "gdn_version", "gdn_prefill_noalloc", "gdn_prefill_algo",
            "gdn_prefill_host", "gdn_prefill_host_staging_size", "gdn_selftest_bounded_wait",
-           "gdn_prefill_pass_plan")
+           "gdn_prefill_pass_plan", "gdn_kv_append", "gdn_kv_read", "gdn_attend", "gdn_attend_workspace_size",
+           "gdn_block_norm")
 NOALLOC_SCRATCH_BYTES = 97 * 1024 * 1024
 PHASE = {"prep": 1, "pass": 2}
 
@@ -85,6 +86,18 @@ def bind(path: str) -> ctypes.CDLL:
     lib.gdn_status_string.argtypes = [I]
     lib.gdn_status_string.restype = ctypes.c_char_p
     lib.gdn_version.restype = I
+    L = ctypes.c_longlong
+    lib.gdn_kv_append.argtypes = [I, I, I, I, I, I, P, L, P, L, P, L, P, P, I, I, P, P, P, I, I, I, I, P, P, P, P, P, P,
+                                  P, I, P, P]
+    lib.gdn_kv_append.restype = I
+    lib.gdn_kv_read.argtypes = [I, I, I, I, P, P, I, I, I, I, P, P, P, P, P, P, I, P]
+    lib.gdn_kv_read.restype = I
+    lib.gdn_attend_workspace_size.argtypes = [I, I, I, I, I, I, I, ctypes.POINTER(I)]
+    lib.gdn_attend_workspace_size.restype = Z
+    lib.gdn_attend.argtypes = [I, I, I, I, I, P, P, P, P, P, P, I, I, I, I, P, P, I, I, F, I, I, P, I, P, Z, P]
+    lib.gdn_attend.restype = I
+    lib.gdn_block_norm.argtypes = [I, I, P, P, I, P, I, P, P, P, F, F, P, P, P]
+    lib.gdn_block_norm.restype = I
     return lib
 
 

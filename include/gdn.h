@@ -367,6 +367,142 @@ GDN_API gdn_status gdn_prefill_host(int n_seqs, int total_tokens, int hk, int hv
                                     const float *gate_scale, const float *gate_bias,
                                     int algo, void *staging, size_t staging_bytes, void *stream);
 
+/*
+ * The layers around the recurrence.  A hybrid model interleaves Gated DeltaNet layers with grouped-query
+ * attention layers ("Optimizing on-device inference for Apple Silicon", section "Qwen creates three workload
+ * shapes": 30 of the former, 10 of the latter), whose context is a cache of keys and values instead of a
+ * fixed-size state.  The calls below keep that cache in 8 bits, attend over it, and join a block's output to
+ * the residual stream.  Conventions are the ones above (device pointers of the caller, 16-byte aligned bases,
+ * asynchronous on `stream`, argument errors before any launch); what differs is said at each call.
+ *
+ * The cache.  A pool of n_pages pages, each holding page_size tokens (a multiple of GDN_KV_BLOCK = 16, at most
+ * 4096) of every key/value head, 8 bits an element:
+ *   k_pages, v_pages    [n_pages, hkv, page_size, d], gdn_kv_format elements
+ *   k_scales, v_scales  fp32 [n_pages, hkv, page_size / 16]: one scale for 16 consecutive tokens of one head;
+ *                       an element stands for code * scale
+ *   block_table         int32 [n_seqs, max_pages]: the page of tokens [i * page_size, (i + 1) * page_size) of
+ *                       sequence n is block_table[n, i].  Entries that no token of the sequence reaches are
+ *                       not read.  An entry outside [0, n_pages) that is reached records GDN_ERR_INTERNAL in
+ *                       the device error word (gdn_device_error): nothing is written there, and its tokens
+ *                       read as zeros.
+ * d is 64, 128 or 256; a pool has fewer than 2^31 token rows (n_pages * hkv * page_size).
+ */
+typedef enum {
+    GDN_KV_INT8 = 0,   /* two's complement, codes -127 .. 127 */
+    GDN_KV_E4M3 = 1    /* 8-bit floats: 4 exponent bits, 3 mantissa bits, largest 448 */
+} gdn_kv_format;
+
+#define GDN_KV_BLOCK 16
+
+/*
+ * gdn_kv_append: put new keys and values of n_seqs sequences into the cache, rotated to their positions.
+ *
+ *   n_seqs, total_tokens  sequences, and new tokens T of all of them together (>= 0)
+ *   hq, hkv, d, rot       query heads (0 when q is NULL), key/value heads, head size; the first rot components
+ *                         of every query and key head are rotated (0 <= rot <= d, a multiple of 16)
+ *   q, k, v               bf16 [T, h, d]: head vectors contiguous, tokens q_stride, k_stride, v_stride elements
+ *                         apart (multiples of 8, at least h * d), so they may be slices of one projection.
+ *                         q may be NULL (no queries to rotate)
+ *   cos, sin              fp32 [n_positions, rot / 2] tables, row = position (may be NULL when rot is 0)
+ *   interleaved           0: component i pairs with i + rot/2; 1: component 2i pairs with 2i + 1.  A pair (a, b)
+ *                         with table entry i becomes (a cos - b sin, b cos + a sin), in fp32, rounded to bf16
+ *   cu_seqlens            int32 [n_seqs + 1] on the device: sequence n's new tokens are [cu[n], cu[n + 1])
+ *   past_lens             int32 [n_seqs] on the device: tokens of each sequence that the cache already holds;
+ *                         the new ones get positions past_lens[n], past_lens[n] + 1, ...
+ *   open_in, open_out     bf16 [n_slots, 2, hkv, 16, d]: the tokens (keys, rotated; values) of each sequence's
+ *                         unfinished 16-token block before quantisation.  Sequence n uses slot slots[n] (int32
+ *                         [n_seqs] on the device, all different), or slot n when slots is NULL.  On entry rows
+ *                         [0, past_lens[n] % 16) of open_in are that block's earlier tokens; on return rows
+ *                         [0, new length % 16) of open_out are its tokens now, other rows untouched.  open_out
+ *                         may be open_in (any other overlap is an error).
+ *   q_out                 bf16 [T, hq, d], contiguous: the rotated queries; may be q when q is contiguous
+ *
+ * Every 16-token block that holds a new token is quantised as a whole, from bf16 values: per head
+ *     A = max(largest magnitude, 2^-60),  scale = A / Q,  code = round(x * (Q / A))   (Q = 127 or 448, ties to even)
+ * with zeros in the places of tokens still to come.  An unfinished block is quantised again from its bf16
+ * tokens as it grows, so the cache does not depend on how a prompt was divided into calls.  A block with an
+ * infinity or NaN gets that as its scale and codes 0: it reads as NaN, its neighbours are unharmed.
+ * A token whose position is negative, or outside the cos/sin tables or the block table, records
+ * GDN_ERR_INTERNAL and its sequence is left out.
+ */
+GDN_API gdn_status gdn_kv_append(int n_seqs, int total_tokens, int hq, int hkv, int d, int rot,
+                                 const void *q, long long q_stride, const void *k, long long k_stride,
+                                 const void *v, long long v_stride, const float *cos, const float *sin,
+                                 int n_positions, int interleaved, const int32_t *cu_seqlens,
+                                 const int32_t *past_lens, const int32_t *block_table, int max_pages,
+                                 int n_pages, int page_size, int format, void *k_pages, void *v_pages,
+                                 float *k_scales, float *v_scales, const void *open_in, void *open_out,
+                                 const int32_t *slots, int n_slots, void *q_out, void *stream);
+
+/*
+ * gdn_kv_read: the values that the cache holds, for moving a sequence out of it.
+ *
+ *   cu_tokens      int32 [n_seqs + 1] on the device: tokens 0 .. cu_tokens[n + 1] - cu_tokens[n] of sequence n go
+ *                  to rows [cu_tokens[n], cu_tokens[n + 1]) of the outputs; ends at total_tokens
+ *   k_out, v_out   [total_tokens, hkv, d], dtype out_dtype: code * scale
+ */
+GDN_API gdn_status gdn_kv_read(int n_seqs, int total_tokens, int hkv, int d, const int32_t *cu_tokens,
+                               const int32_t *block_table, int max_pages, int n_pages, int page_size, int format,
+                               const void *k_pages, const void *v_pages, const float *k_scales,
+                               const float *v_scales, void *k_out, void *v_out, int out_dtype, void *stream);
+
+/*
+ * gdn_attend: causal attention of new queries over the cache (which already holds their own keys and values).
+ *
+ *   q              bf16 [T, hq, d], rotated (gdn_kv_append's q_out); query head h reads key/value head
+ *                  h / (hq / hkv)
+ *   cu_seqlens     int32 [n_seqs + 1] on the device: sequence n's queries are tokens [cu[n], cu[n + 1])
+ *   kv_lens        int32 [n_seqs] on the device: tokens of each sequence in the cache.  Its m queries stand at
+ *                  positions kv_lens[n] - m .. kv_lens[n] - 1
+ *   max_q_len,     upper bounds of the device values, known on the host: they choose the kernel and size the
+ *   max_kv_len     workspace.  A sequence beyond a bound records GDN_ERR_INTERNAL and is cut to it.  A CUDA
+ *                  graph may be captured with generous bounds and replayed as the lengths grow.
+ *   sm_scale       multiplies the products q.k (finite; usually 1/sqrt(d))
+ *   window, sinks  a query at position p sees token j when j <= p and (window == 0, or j > p - window, or
+ *                  j < sinks): a sliding window of `window` tokens, its own included, whose first `sinks`
+ *                  tokens stay visible.  A query that sees nothing gets zeros.
+ *   out            [T, hq, d], dtype out_dtype
+ *   workspace      at least gdn_attend_workspace_size() bytes, 256-byte aligned; contents do not matter
+ *
+ * Products and sums are accumulated in fp32, codes enter them exactly; queries are rounded to fp16 after an
+ * exact scaling by a power of two per row, softmax weights to fp16.
+ */
+GDN_API size_t gdn_attend_workspace_size(int n_seqs, int total_tokens, int hq, int hkv, int d, int max_q_len,
+                                         int max_kv_len, gdn_status *status);
+
+GDN_API gdn_status gdn_attend(int n_seqs, int total_tokens, int hq, int hkv, int d, const void *q,
+                              const void *k_pages, const void *v_pages, const float *k_scales,
+                              const float *v_scales, const int32_t *block_table, int max_pages, int n_pages,
+                              int page_size, int format, const int32_t *cu_seqlens, const int32_t *kv_lens,
+                              int max_q_len, int max_kv_len, float sm_scale, int window, int sinks,
+                              void *out, int out_dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * gdn_block_norm: join a block's output to the residual stream and normalise for the next block.  Per row:
+ *     y  = x / sqrt(mean(x^2) + eps) * post_weight      (y = x when post_weight is NULL)
+ *     y  = y * act(gate)                                (when gate is not NULL)
+ *     r' = residual + scale * y                         (scale_weight[i] per channel when given, else scale)
+ *     h  = r' / sqrt(mean(r'^2) + eps) * pre_weight
+ * in fp32; r' and h are rounded once, h from the unrounded r'.
+ *
+ *   rows, dim               dim a multiple of 8, 8 .. 16384
+ *   x, gate                 bf16 [rows, dim]; gate may be NULL
+ *   gate_act                GDN_GATE_SIGMOID (act(g) = 1 / (1 + e^-g)) or GDN_GATE_SILU (g / (1 + e^-g))
+ *   residual, residual_out  [rows, dim], dtype residual_dtype; residual_out may be residual (in place)
+ *   post_weight, pre_weight, scale_weight   fp32 [dim]; post_weight and scale_weight may be NULL
+ *   scale, eps              finite; eps >= 0
+ *   out                     bf16 [rows, dim]: h.  It may be x or gate (in place).
+ */
+typedef enum {
+    GDN_GATE_SIGMOID = 0,
+    GDN_GATE_SILU = 1
+} gdn_gate_act;
+
+GDN_API gdn_status gdn_block_norm(int rows, int dim, const void *x, const void *gate, int gate_act,
+                                  const void *residual, int residual_dtype, const float *post_weight,
+                                  const float *pre_weight, const float *scale_weight, float scale, float eps,
+                                  void *residual_out, void *out, void *stream);
+
 /* Static, human-readable name of a status code. */
 GDN_API const char *gdn_status_string(gdn_status status);
 
