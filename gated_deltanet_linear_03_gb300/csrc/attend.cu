@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D>()) attend_split_kerne
                 const int u = (2 * warp + j) ^ (row & 7);
                 *reinterpret_cast<__half2 *>(reinterpret_cast<uint8_t *>(sm.p) + row * 128 + u * 16 + 4 * t) = h;
             }
-            l[r] = l[r] * corr[r] + sum * rv;
+            l[r] = l[r] * corr[r] + (sum == 0.f ? 0.f : sum * rv);   // a block that the row does not see may have any scale
         }
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
@@ -534,19 +534,24 @@ cudaError_t launch_split(const AttendProblem &p) {
     attend_split_kernel<D, FMT><<<ctas, kThreads, sizeof(Smem<D>), p.stream>>>(p, plan);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (ctas == 1 || bound == items) return cudaSuccess;   // no item crosses CTAs
-    return launch_after(p.stream, dim3((unsigned)(plan.meta_by_item ? items : ctas), kRows), kMergeThreads,
+    return launch_after(p.stream, dim3((unsigned)(plan.meta_by_item ? items : ctas), kRows), kMergeThreads, 0,
                         attend_merge_kernel<D, kRows>, p, plan);
 }
+
+// The tensor-core kernel (attend_tc.cu) for more query rows than four of this kernel's items.
+bool use_tensor_kernel(int group, int max_q_len) { return (long long)group * max_q_len > 64; }
 
 }  // namespace
 
 size_t attend_workspace_bytes(int n_seqs, int total, int hq, int hkv, int d, int max_q_len, int max_kv_len) {
     if (n_seqs == 0 || total == 0) return 0;
+    if (use_tensor_kernel(hq / hkv, max_q_len)) return attend_tc_workspace_bytes(n_seqs, total, hq, hkv, d);
     const long long slots = 2 * min(unit_bound(n_seqs, hq, hkv, max_q_len, max_kv_len), (long long)kMaxSplitCtas);
     return kMetaBytes + (size_t)slots * (kRows * d + 2 * kRows) * sizeof(float);
 }
 
 cudaError_t launch_attend(const AttendProblem &p) {
+    if (use_tensor_kernel(p.hq / p.pool.hkv, p.max_q_len)) return launch_attend_tc(p);
     const bool e4m3 = p.format == GDN_KV_E4M3;
     switch (p.d) {
         case 64: return e4m3 ? launch_split<64, GDN_KV_E4M3>(p) : launch_split<64, GDN_KV_INT8>(p);

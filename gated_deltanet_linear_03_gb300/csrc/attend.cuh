@@ -7,7 +7,8 @@
 namespace gdn {
 namespace attend {
 
-constexpr int kMaxSplitCtas = 1024;
+constexpr int kMaxSplitCtas = 1024;   // CTAs of the split kernel, and
+constexpr int kMaxTcCtas = 256;       // of the tensor-core kernel, that workspaces have room for
 
 // One entry a merge CTA reads: the item's first CTA and the slot it used there, and its last CTA (-1: the item
 // did not cross CTAs).
@@ -147,13 +148,14 @@ __device__ __forceinline__ void store_row(const AttendProblem &p, size_t at, con
 // Launch as the programmatic dependent of the stream's last kernel: its CTAs may become resident early and wait
 // for that kernel's end with grid_dependency_wait.
 template <typename... P, typename... A>
-cudaError_t launch_after(cudaStream_t stream, dim3 grid, int threads, void (*fn)(P...), const A &...args) {
+cudaError_t launch_after(cudaStream_t stream, dim3 grid, int threads, size_t smem, void (*fn)(P...), const A &...args) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;

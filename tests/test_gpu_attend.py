@@ -215,6 +215,24 @@ def test_nonfinite_scales_reach_only_who_sees_them(attn, bad, m):
     check(out[~sees], want[~sees], tol[~sees])
 
 
+@pytest.mark.parametrize("m", [1, 70])
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+def test_nonfinite_scales_behind_the_mask_of_a_loaded_tile(attn, bad, m):
+    """The spoilt blocks share a 64-token tile with visible ones: before the window, and after the last token of the page."""
+    lens = [m + 194]
+    cache = ref.make_cache(lens, 1, 128, 64, I8, 13)
+    clean = ref.Cache(*[x.clone() for x in (cache.table, *cache.args)])
+    first = lens[0] - m - 31                       # the first token that the first query sees
+    assert first // 16 % 4 != 0
+    for j in (first // 16 - 1, -(-lens[0] // 16)):
+        page = int(cache.table[0, j * 16 // 64])
+        cache.k_scales[page, :, j % 4] = bad
+        cache.v_scales[page, :, j % 4] = bad
+    q = torch.randn(m, 2, 128, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    out, cu = run(attn, q, cache, [m], lens, window=32)
+    check(out, *ref.attend(q, clean, cu, lens, 32))
+
+
 def test_bad_pages_and_lengths_are_recorded(attn):
     """Table entries outside the pool read as zeros and record GDN_ERR_INTERNAL; so do lengths beyond the bounds."""
     from gated_deltanet_linear_03_gb300 import gdn
