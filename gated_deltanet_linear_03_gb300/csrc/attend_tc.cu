@@ -1,0 +1,759 @@
+// gdn_attend for many query rows per key/value head (prompts and pieces of prompts): tcgen05.
+//
+// The mathematics is attend.cu's: x_j = s_j log2 e + log2 V_b, weights w_j = 2^{x_j - M}, o = sum w_j v_j / sum_b
+// (1 / V_b) sum_{j in b} w_j.  An item is (sequence, key/value head, NQ * 128 query rows), a row being a head of the
+// group at a token, so all heads of a group share every loaded and converted tile.  A unit is 64 tokens of an item.
+// attend_plan_kernel lists the items and cuts their units into equal runs, one per CTA (one CTA per SM); an item
+// that crosses CTAs is joined by attend_join_kernel.
+//
+// Warps of a CTA, each following the same run of units through mbarriers:
+//   softmax (4 NQ)  thread = row.  Load the query rows, scale each exactly by a power of two, and put them into TMEM
+//                   as the fp16 A operand of the score products; per unit read 64 scores, keep maximum and sum in
+//                   registers, write the fp16 weights over the scores in TMEM as the A operand of the output
+//                   products; rescale O in TMEM only when the row's maximum has grown by more than 2^8 (weights
+//                   then stay at most 2^8: fp16 holds them, and few units pay the pass over O); store the outputs.
+//   loaders (8)     codes from global memory to registers (a unit ahead), turned to fp16 exactly, into 128B-swizzled
+//                   shared-memory tiles: the same layout serves K (K-major B) and V (MN-major B).
+//   MMA (1)         S = Q K^T of the next unit before O += W V of this one, so the tensor pipe works while the
+//                   softmax does.
+//   scales (1)      the unit's four block scales, their logarithms and reciprocals.
+// Queries and weights as TMEM operands leave shared memory to K and V: per unit 2 x 64 x D x 2 bytes written by the
+// loaders and read once by the MMAs.
+// Bound by the tensor pipe (4 D FLOP a row and token).
+#include "attend.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace attend;
+using namespace sm100;
+
+constexpr int kTile = 64;
+constexpr int kStages = 3;
+constexpr int kScaleSlots = 4;
+constexpr int kLoaderWarps = 8;
+
+template <int D>
+struct Tc {
+    static constexpr int NQ = D == 256 ? 1 : 2;              // 128-row tiles of a CTA
+    static constexpr int ROWS = 128 * NQ;
+    static constexpr int SB = NQ * (D + D / 2 + 128) <= 512 ? 2 : 1;   // score buffers of a tile
+    static constexpr int O = 0, Q = NQ * D, S = NQ * (D + D / 2);      // TMEM columns
+    static constexpr int SOFTMAX_WARPS = 4 * NQ;
+    static constexpr int WARPS = SOFTMAX_WARPS + kLoaderWarps + 4;     // the last four: MMA, scales, two idle
+    static constexpr int THREADS = 32 * WARPS;
+    // Registers a thread: at launch (the most that WARPS warps can have, a multiple of 8), then per role.  The roles'
+    // shares add up to what the CTA was launched with: 512 x 128 = 128 x 208 + 256 x 104 + 128 x 96 and
+    // 640 x 96 >= 256 x 152 + 256 x 56 + 128 x 56.
+    static constexpr int REGS_LAUNCH = NQ == 1 ? 128 : 96;
+    static constexpr int REGS_SOFTMAX = NQ == 1 ? 208 : 152, REGS_LOADER = NQ == 1 ? 104 : 56, REGS_OTHER = NQ == 1 ? 96 : 56;
+    static_assert(32 * (SOFTMAX_WARPS * REGS_SOFTMAX + kLoaderWarps * REGS_LOADER + 4 * REGS_OTHER) <= THREADS * REGS_LAUNCH, "registers");
+    static constexpr int TILE_BYTES = kTile * D * 2;
+};
+
+template <int D>
+struct __align__(1024) TcSmem {
+    uint8_t k[kStages][Tc<D>::TILE_BYTES];
+    uint8_t v[kStages][Tc<D>::TILE_BYTES];
+    float scale[kScaleSlots][12];        // K scales, log2 of V scales, reciprocals of V scales
+    uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+    uint64_t s_full[Tc<D>::NQ][2], p_full[Tc<D>::NQ][2], pv_done[Tc<D>::NQ], q_full[Tc<D>::NQ];
+    uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots], drain;
+    uint32_t tmem;
+    int abort;
+};
+
+// Where a run begins: unit j of an item, and that unit's number in the whole call.
+struct RunStart {
+    int item, j;
+    long long unit;
+};
+
+// Workspace of a call: the merge entries, the runs' starts, the item list, the parts.
+struct TcPlan {
+    MergeMeta *meta;       // [ctas]
+    RunStart *start;       // [ctas + 1]
+    long long *per;        // cost of a run
+    int4 *items;           // (sequence, head, row tile, units)
+    float *parts;
+    int ctas;
+};
+
+__host__ __device__ inline size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+
+constexpr int kPlanThreads = 1024;
+// What an item costs beside its units, in units: its queries' way into TMEM, the pipeline's fill, its outputs.
+constexpr int kItemCost = 4;
+
+// Exclusive prefix of v over the CTA, and the sum.
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T &sum, T *part) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    T x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const T y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) part[warp] = x;
+    __syncthreads();
+    T before = 0;
+    sum = 0;
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) {
+        if (w < warp) before += part[w];
+        sum += part[w];
+    }
+    return before + x - v;
+}
+
+// One CTA lists the items (sequence-major, heads inside, row tiles inside) and finds where every run begins.
+template <int ROWS>
+__global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_constant__ AttendProblem p,
+                                                                   const __grid_constant__ TcPlan plan) {
+    __shared__ long long part[kPlanThreads / 32];
+    const int tid = threadIdx.x, group = p.hq / p.pool.hkv;
+    grid_launch_dependents();
+    for (int n = tid; n < p.n_seqs; n += kPlanThreads)
+        if (__ldg(p.cu + n + 1) - __ldg(p.cu + n) > p.max_q_len || __ldg(p.kv_lens + n) > p.max_kv_len || __ldg(p.kv_lens + n) < 0 ||
+            __ldg(p.cu + n + 1) > p.total || __ldg(p.cu + n) < 0 || __ldg(p.cu + n + 1) < __ldg(p.cu + n))
+            raise_error(p.err, kErrInternal);
+    // the items, written by the threads that hold their sequences
+    long long items = 0, total = 0;
+    for (int n0 = 0; n0 < p.n_seqs; n0 += kPlanThreads) {
+        const int n = n0 + tid;
+        Sequence s{};
+        if (n < p.n_seqs) s = load_sequence(p, n);
+        long long mine = (long long)row_tiles<ROWS>(s.qlen, group) * p.pool.hkv, sum;
+        mine = block_scan(mine, sum, part) + items;
+        items += sum;
+        // long sequences are written by the whole CTA below, one after another
+        if (n < p.n_seqs) {
+            const int mts = row_tiles<ROWS>(s.qlen, group);
+            if (mts <= 4)
+                for (int h = 0; h < p.pool.hkv; ++h)
+                    for (int mt = 0; mt < mts; ++mt) plan.items[mine + h * mts + mt] = make_int4(n, h, mt, make_item<ROWS, kTile>(p, s, group, mt).tiles);
+        }
+        __shared__ int long_n[kPlanThreads], longs;
+        __shared__ long long long_at[kPlanThreads];
+        if (tid == 0) longs = 0;
+        __syncthreads();
+        if (n < p.n_seqs && row_tiles<ROWS>(s.qlen, group) > 4) {
+            const int at = atomicAdd(&longs, 1);
+            long_n[at] = n;
+            long_at[at] = mine;
+        }
+        __syncthreads();
+        for (int i = 0; i < longs; ++i) {
+            const Sequence ls = load_sequence(p, long_n[i]);
+            const int mts = row_tiles<ROWS>(ls.qlen, group);
+            for (int k = tid; k < mts * p.pool.hkv; k += kPlanThreads) {
+                const int mt = k % mts;
+                plan.items[long_at[i] + k] = make_int4(long_n[i], k / mts, mt, make_item<ROWS, kTile>(p, ls, group, mt).tiles);
+            }
+        }
+        __syncthreads();
+    }
+    long long mine = 0;
+    for (long long i = tid; i < items; i += kPlanThreads) mine += plan.items[i].w + kItemCost;
+    block_scan(mine, total, part);
+    const long long per = max((total + plan.ctas - 1) / plan.ctas, 1LL);
+    if (tid == 0) plan.per[0] = per;
+    long long before = 0;
+    for (long long i0 = 0; i0 < items; i0 += kPlanThreads) {
+        const long long i = i0 + tid;
+        const long long w = i < items ? plan.items[i].w + kItemCost : 0;
+        long long sum;
+        const long long at = before + block_scan(w, sum, part), unit = at - min(i, items) * kItemCost;
+        before += sum;
+        // a run that would begin inside an item's fixed cost begins at its first unit
+        for (long long c = (at + per - 1) / per; c < plan.ctas && c * per < at + w; ++c) {
+            const long long j = max(0LL, c * per - at - kItemCost);
+            plan.start[c] = {(int)i, (int)j, unit + j};
+        }
+    }
+    for (long long c = (total + per - 1) / per + tid; c <= plan.ctas; c += kPlanThreads) plan.start[c] = {0, 0, total - items * kItemCost};
+}
+
+// The run of one CTA, unit by unit; every role keeps its own.
+template <int ROWS>
+struct Walk {
+    const AttendProblem &p;
+    const TcPlan &plan;
+    int group, item, j, tiles, n, h, mt;
+    Sequence s;
+    Item it;
+    __device__ __forceinline__ Walk(const AttendProblem &p_, const TcPlan &plan_, int group_) : p(p_), plan(plan_), group(group_) {
+        const RunStart st = plan.start[blockIdx.x];
+        item = st.item;
+        load();
+        j = st.j;
+    }
+    __device__ __forceinline__ void load() {
+        const int4 d = plan.items[item];
+        n = d.x;
+        h = d.y;
+        mt = d.z;
+        tiles = d.w;
+        s = load_sequence(p, n);
+        it = make_item<ROWS, kTile>(p, s, group, mt);
+        j = 0;
+    }
+    __device__ __forceinline__ int token() const { return it.token(j, kTile); }
+    __device__ __forceinline__ bool last() const { return j == tiles - 1; }
+    // to the next unit (which the run must hold)
+    __device__ __forceinline__ void next() {
+        if (++j == tiles) {
+            ++item;
+            load();
+        }
+    }
+};
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __grid_constant__ AttendProblem p,
+                                                                     const __grid_constant__ TcPlan plan) {
+    using L = Tc<D>;
+    constexpr int NQ = L::NQ, SB = L::SB, ROWS = L::ROWS;
+    extern __shared__ uint8_t raw[];
+    TcSmem<D> &sm = *reinterpret_cast<TcSmem<D> *>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int group = p.hq / p.pool.hkv, cta = blockIdx.x;
+
+    if (warp == 0) tmem_alloc(&sm.tmem, 512);
+    if (tid == 32) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sm.k_full[i], kLoaderWarps);
+            mbar_init(&sm.v_full[i], kLoaderWarps);
+            mbar_init(&sm.k_empty[i], 1);
+            mbar_init(&sm.v_empty[i], 1);
+        }
+        for (int q = 0; q < NQ; ++q) {
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&sm.s_full[q][b], 1);
+                mbar_init(&sm.p_full[q][b], 4);
+            }
+            mbar_init(&sm.pv_done[q], 1);
+            mbar_init(&sm.q_full[q], 4);
+        }
+        for (int i = 0; i < kScaleSlots; ++i) {
+            mbar_init(&sm.sc_full[i], 1);
+            mbar_init(&sm.sc_empty[i], L::SOFTMAX_WARPS);
+        }
+        mbar_init(&sm.drain, 1);
+        sm.abort = 0;
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const long long per = plan.per[0];
+    const int units = (int)(plan.start[cta + 1].unit - plan.start[cta].unit);
+
+    // A bounded wait: when it runs out, or another thread's has, every role leaves its loop.
+    volatile int *abort = &sm.abort;
+    auto wait_one = [&](uint64_t *bar, int phase) -> bool {
+        if (mbar_try_wait(bar, (uint32_t)phase & 1)) return true;
+        const uint64_t t0 = global_timer_ns();
+        while (!mbar_try_wait(bar, (uint32_t)phase & 1)) {
+            if (*abort) return false;
+            if (global_timer_ns() - t0 > kWaitTimeoutNs) {
+                *abort = 1;
+                raise_error(p.err, kErrTimeout);
+                return false;
+            }
+        }
+        return true;
+    };
+    // ... by all lanes of a warp, with one answer: what follows may be warp-wide.
+    auto wait = [&](uint64_t *bar, int phase) -> bool { return __all_sync(0xffffffffu, wait_one(bar, phase)); };
+
+    if (warp < L::SOFTMAX_WARPS) {
+        set_max_registers_up<L::REGS_SOFTMAX>();
+        // ------------------------------------------------------------------------------------------ softmax
+        const int q = warp / 4, row = tid % 128;
+        const uint32_t quad = tmem + ((uint32_t)(warp & 3) << 21);      // lanes 32 (warp % 4) ..
+        const uint32_t o_at = quad + L::O + q * D, q_at = quad + L::Q + q * (D / 2), s_at = quad + L::S + q * SB * 64;
+        MergeMeta mm;
+        mm.last = -1;
+        if (units > 0) {
+            Walk<ROWS> w(p, plan, group);
+            bool ok = true;
+            for (int u = 0, seg = 0; ok && u < units; ++seg) {
+                // ---- a segment: the query row
+                const bool begun = w.j == 0;
+                const int seg_slot = u == 0 ? 0 : 1;
+                const long long grow = (long long)w.mt * ROWS + q * 128 + row;
+                const int i = (int)min(grow / group, (long long)w.s.qlen);
+                const bool valid = i < w.s.qlen;
+                const int pos = w.s.kvlen - w.s.qlen + i;
+                const size_t out_row = ((size_t)(w.s.q0 + (valid ? i : 0)) * p.hq + w.h * group + (int)(grow % group)) * D;
+                float rs;
+                {
+                    // 4 lanes to a row, 16 bytes each, 8 rows at a time: rows 16 half + 8 k + lane / 4 of the warp's 32
+                    rs = 0.f;
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        uint4 y[2][D / 32];
+                        float down[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const long long gr = (long long)w.mt * ROWS + q * 128 + 32 * (warp & 3) + 16 * half + 8 * k + lane / 4;
+                            const bool ok_row = gr / group < w.s.qlen;
+                            const uint4 *src = reinterpret_cast<const uint4 *>(
+                                p.q + ((size_t)(w.s.q0 + (ok_row ? (int)(gr / group) : 0)) * p.hq + w.h * group + (int)(gr % group)) * D) + lane % 4;
+#pragma unroll
+                            for (int c = 0; c < D / 32; ++c) y[k][c] = ok_row ? __ldg(src + 4 * c) : make_uint4(0, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            uint32_t big = 0;
+                            float up;
+#pragma unroll
+                            for (int c = 0; c < D / 32; ++c) big = max(big, amax_bits(y[k][c]));
+                            big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                            big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                            power_of_two_scale(big, down[k], up);
+                            if (p.sm_scale < 0.f) down[k] = -down[k];     // the row factor stays >= 0
+                            up = __shfl_sync(0xffffffffu, up, 4 * (lane % 8));
+                            if (lane / 8 == 2 * half + k) rs = up;
+                        }
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c) {
+                            uint32_t x[16];
+#pragma unroll
+                            for (int i2 = 0; i2 < 2; ++i2)
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const uint4 &z = y[k][2 * c + i2];
+                                    x[8 * i2 + 2 * k] = bf16x2_to_f16x2(z.x, down[k]);
+                                    x[8 * i2 + 2 * k + 1] = bf16x2_to_f16x2(z.y, down[k]);
+                                    x[8 * i2 + 4 + 2 * k] = bf16x2_to_f16x2(z.z, down[k]);
+                                    x[8 * i2 + 4 + 2 * k + 1] = bf16x2_to_f16x2(z.w, down[k]);
+                                }
+                            tmem_st_16x32(q_at + ((uint32_t)(16 * half) << 16) + 32 * c, x);
+                        }
+                    }
+                    rs *= fabsf(p.sm_scale) * 1.4426950408889634f;
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.q_full[q]);
+                }
+                float m = -INFINITY, l = 0.f;
+                bool ends;
+                for (bool first = true;; first = false) {
+                    // ---- one unit
+                    const int buf = u % SB;
+                    const uint32_t s_tm = s_at + buf * 64;
+                    const int tok0 = w.token();
+                    ends = w.last();
+                    if (!(ok = wait(&sm.s_full[q][buf], u / SB))) break;
+                    if (!(ok = wait(&sm.sc_full[u % kScaleSlots], u / kScaleSlots))) break;
+                    tc_fence_after();
+                    float s[64];
+                    tmem_ld32x2(s_tm, s_tm + 32, s, s + 32);
+                    float f[4], lv[4], rv[4];
+                    {
+                        const float *sc = sm.scale[u % kScaleSlots];
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            f[b] = rs * sc[b];
+                            lv[b] = sc[4 + b];
+                            rv[b] = sc[8 + b];
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.sc_empty[u % kScaleSlots]);
+                    if (!w.it.all_seen(tok0, tok0 + kTile, p.window, p.sinks)) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            s[c] = sees(pos, tok0 + c, p.window, p.sinks) ? fmaf(s[c], f[c / 16], lv[c / 16]) : -INFINITY;
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) f[b] = 1.f, lv[b] = 0.f;
+                    }
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        float x = s[16 * b];
+#pragma unroll
+                        for (int c = 1; c < 16; ++c) x = fmaxf(x, s[16 * b + c]);
+                        top = fmaxf(top, fmaf(x, f[b], lv[b]));
+                    }
+                    const bool grow_max = first ? true : top > m + 8.f;
+                    if (first) {
+                        m = top;
+                    } else if (__any_sync(0xffffffffu, grow_max)) {
+                        if (!(ok = wait(&sm.pv_done[q], u - 1))) break;
+                        tc_fence_after();
+                        const float to = grow_max ? top : m, c = m == to ? 1.f : exp2f(m - to);
+                        m = to;
+                        l *= c;
+#pragma unroll 1
+                        for (int k = 0; k < D / 32; ++k) {
+                            float o[32];
+                            tmem_ld32(o_at + 32 * k, o);
+                            uint32_t x[32];
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(o[e] * c);
+                            tmem_st32(o_at + 32 * k, x);
+                        }
+                        tmem_st_wait();
+                    }
+                    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const float off = lv[b] - base;
+                        float sum = 0.f;
+                        uint32_t x[8];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const float a = exp2_fast(fmaf(s[16 * b + 2 * c], f[b], off)), e = exp2_fast(fmaf(s[16 * b + 2 * c + 1], f[b], off));
+                            sum += a + e;
+                            const __half2 hh = __floats2half2_rn(a, e);
+                            x[c] = *reinterpret_cast<const uint32_t *>(&hh);
+                        }
+                        if (sum != 0.f) l = fmaf(sum, rv[b], l);   // a block that no row sees may have any scale
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) s[8 * b + c] = __uint_as_float(x[c]);
+                    }
+                    tmem_st32(s_tm, reinterpret_cast<const uint32_t *>(s));
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.p_full[q][buf]);
+                    ++u;
+                    if (ends || u == units) break;
+                    w.next();
+                }
+                if (!ok) break;
+                // ---- the segment's end
+                if (!(ok = wait(&sm.pv_done[q], u - 1))) break;
+                tc_fence_after();
+                const bool whole = begun && ends;
+                float *part = plan.parts + (size_t)(2 * cta + seg_slot) * (ROWS * D + 2 * ROWS) + (size_t)(q * 128 + row) * D;
+                const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+#pragma unroll 1
+                for (int k = 0; k < D / 32; ++k) {
+                    float o[32];
+                    tmem_ld32(o_at + 32 * k, o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] *= inv;
+                    if (valid && whole) {
+                        store_row<32>(p, out_row + 32 * k, o);
+                    } else if (valid) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4 *>(part + 32 * k + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    }
+                    __syncwarp();   // the next load is warp-wide
+                }
+                if (!whole) {
+                    float *ml = plan.parts + (size_t)(2 * cta + seg_slot) * (ROWS * D + 2 * ROWS) + ROWS * D;
+                    ml[q * 128 + row] = m;
+                    ml[ROWS + q * 128 + row] = l;
+                }
+                tc_fence_before();
+                if (begun && !ends) {
+                    const long long left = (long long)w.tiles - 1 - w.j;
+                    mm.first = cta;
+                    mm.slot = seg_slot;
+                    mm.last = cta + (int)((left + per - 1) / per);
+                    mm.n = w.n;
+                    mm.h = w.h;
+                    mm.mt = w.mt;
+                }
+                if (u < units) w.next();
+            }
+        }
+        if (tid == 0) plan.meta[cta] = mm;
+    } else if (warp < L::SOFTMAX_WARPS + kLoaderWarps) {
+        set_max_registers_down<L::REGS_LOADER>();
+        // ------------------------------------------------------------------------------------------ loaders
+        const int lw = warp - L::SOFTMAX_WARPS;                        // rows 8 lw .. 8 lw + 7 of a tile
+        // 4 lanes take the 64 codes of a column chunk of one row.  The 8 lanes that store together hold rows that
+        // differ in the two low bits, so that their pieces fall on different banks in both tiles' orders.
+        const int r = 8 * lw + ((lane >> 4) << 2) + ((((lane >> 2) & 1) * 3) ^ ((lane >> 3) & 1)), c16 = lane & 3;
+        const uint32_t v_lo = sw128_offset(r, 16 * c16), v_hi = sw128_offset(r, 16 * c16 + 8);
+        // K's columns stand in the order in which a query row's 32-element pieces enter TMEM: components 8 t + 0..3
+        // at 4 t, components 8 t + 4..7 at 16 + 4 t (t = 0..3)
+        const uint32_t k_lo = sw128_offset(r, 32 * (c16 >> 1) + 8 * (c16 & 1)), k_hi = sw128_offset(r, 32 * (c16 >> 1) + 16 + 8 * (c16 & 1));
+        if (units > 0) {
+            Walk<ROWS> w(p, plan, group);
+            uint4 kr[D / 64], vr[D / 64];
+            int page = -1, in_page = 0, head = 0;   // of this thread's row in the unit that `w` is at; -1: no such token
+            auto look_up = [&]() {
+                const int tok = w.token() + r;
+                head = w.h;
+                page = -1;
+                if (tok >= w.s.kvlen) return;
+                const int at = p.pool.page_of(tok);
+                in_page = tok - at * p.pool.page_size;
+                page = __ldg(p.pool.table + (size_t)w.n * p.pool.max_pages + at);
+                if ((unsigned)page >= (unsigned)p.pool.n_pages) page = -2;
+            };
+            auto row_offset = [&]() -> long long {                     // byte offset of that row, or -1
+                if (page == -2) raise_error(p.err, kErrInternal);
+                return page < 0 ? -1 : ((long long)(page * p.pool.hkv + head) * p.pool.page_size + in_page) * D + 16 * c16;
+            };
+            auto fetch = [&](const uint8_t *pages, long long off, uint4 (&x)[D / 64]) {
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    x[c] = off >= 0 ? __ldg(reinterpret_cast<const uint4 *>(pages + off + 64 * c)) : make_uint4(0, 0, 0, 0);
+            };
+            auto put = [&](uint8_t *tile, const uint4 (&x)[D / 64], uint32_t lo, uint32_t hi, bool keys) {
+                const uint32_t at = smem_u32(tile);
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    uint32_t y[8];
+                    codes_to_f16x2<FMT>(x[c].x, y[0], y[1]);
+                    codes_to_f16x2<FMT>(keys ? x[c].z : x[c].y, y[2], y[3]);
+                    codes_to_f16x2<FMT>(keys ? x[c].y : x[c].z, y[4], y[5]);
+                    codes_to_f16x2<FMT>(x[c].w, y[6], y[7]);
+                    const uint32_t a = at + c * (kTile * 128);
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a + lo), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a + hi), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7]) : "memory");
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            };
+            // codes are a unit ahead of their conversion, the table's entry another unit ahead
+            look_up();
+            long long off = row_offset();
+            fetch(p.k_pages, off, kr);
+            fetch(p.v_pages, off, vr);
+            if (units > 1) {
+                w.next();
+                look_up();
+            }
+            for (int u = 0; u < units; ++u) {
+                const int st = u % kStages, ph = u / kStages;
+                off = row_offset();
+                if (u + 2 < units) {
+                    w.next();
+                    look_up();
+                }
+                if (!wait(&sm.k_empty[st], ph + 1)) break;
+                put(sm.k[st], kr, k_lo, k_hi, true);
+                if (lane == 0) mbar_arrive(&sm.k_full[st]);
+                if (u + 1 < units) fetch(p.k_pages, off, kr);
+                if (!wait(&sm.v_empty[st], ph + 1)) break;
+                put(sm.v[st], vr, v_lo, v_hi, false);
+                if (lane == 0) mbar_arrive(&sm.v_full[st]);
+                if (u + 1 < units) fetch(p.v_pages, off, vr);
+            }
+        }
+    } else {
+        set_max_registers_down<L::REGS_OTHER>();
+        const int role = warp - L::SOFTMAX_WARPS - kLoaderWarps;
+        // ------------------------------------------------------------------------------------------ MMA
+        if (role == 0 && lane == 0 && units > 0) {
+            Walk<ROWS> w(p, plan, group);
+            constexpr uint32_t id_s = idesc_f16_f32(128, kTile, false, false), id_o = idesc_f16_f32(128, D, false, true);
+            auto scores = [&](int q, int u) {     // S = Q K^T of unit u
+                const uint64_t kd = smem_desc(smem_u32(sm.k[u % kStages]), 16, 1024, kLayoutSwizzle128B);
+                const uint32_t d = tmem + L::S + (q * SB + u % SB) * 64, a = tmem + L::Q + q * (D / 2);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) mma_tmem_a(d, a + 8 * k, kd + ((k >> 2) * (kTile * 128) >> 4) + 2 * (k & 3), id_s, k > 0);
+                mma_commit(&sm.s_full[q][u % SB]);
+            };
+            auto outputs = [&](int q, int u, bool first) {   // O += W V of unit u
+                const uint64_t vd = smem_desc(smem_u32(sm.v[u % kStages]), kTile * 128, 1024, kLayoutSwizzle128B);
+                const uint32_t a = tmem + L::S + (q * SB + u % SB) * 64;
+#pragma unroll
+                for (int k = 0; k < kTile / 16; ++k) mma_tmem_a(tmem + L::O + q * D, a + 8 * k, vd + 128 * k, id_o, !(first && k == 0));
+                mma_commit(&sm.pv_done[q]);
+            };
+            bool ok = true;
+            for (int u = 0, seg = 0; ok && u < units; ++seg) {
+                for (int q = 0; q < NQ && ok; ++q) ok = wait_one(&sm.q_full[q], seg);
+                if (ok) ok = wait_one(&sm.k_full[u % kStages], u / kStages);
+                if (!ok) break;
+                tc_fence_after();
+                for (int q = 0; q < NQ; ++q) scores(q, u);
+                mma_commit(&sm.k_empty[u % kStages]);
+                for (bool first = true;; first = false) {
+                    const bool ends = w.last() || u == units - 1;
+                    if (!ends) {
+                        if (!(ok = wait_one(&sm.k_full[(u + 1) % kStages], (u + 1) / kStages))) break;
+                        tc_fence_after();
+                        if (SB == 2) {
+                            for (int q = 0; q < NQ; ++q) scores(q, u + 1);
+                            mma_commit(&sm.k_empty[(u + 1) % kStages]);
+                        }
+                    }
+                    if (!(ok = wait_one(&sm.v_full[u % kStages], u / kStages))) break;
+                    for (int q = 0; q < NQ && ok; ++q) {
+                        if (!(ok = wait_one(&sm.p_full[q][u % SB], u / SB))) break;
+                        tc_fence_after();
+                        outputs(q, u, first);
+                        if (SB == 1 && !ends) scores(q, u + 1);
+                    }
+                    if (!ok) break;
+                    mma_commit(&sm.v_empty[u % kStages]);
+                    if (SB == 1 && !ends) mma_commit(&sm.k_empty[(u + 1) % kStages]);
+                    ++u;
+                    if (ends) break;
+                    w.next();
+                }
+                if (ok && u < units) w.next();
+            }
+            // every MMA has finished before the tensor memory is given back
+            mma_commit(&sm.drain);
+            if (!mbar_wait(&sm.drain, 0)) raise_error(p.err, kErrTimeout);
+        }
+        // ------------------------------------------------------------------------------------------ scales
+        if (role == 1 && units > 0) {
+            Walk<ROWS> w(p, plan, group);
+            // lanes 0..3 hold the unit's K scales, 4..7 its V scales: read a unit ahead, the table another one
+            const float *scales = lane < 4 ? p.k_scales : p.v_scales;
+            int page = -1, block = 0, head = 0;
+            auto look_up = [&]() {
+                const int tok = w.token() + (lane & 3) * kKvBlock;
+                head = w.h;
+                page = -1;
+                if (lane >= 8 || tok >= w.s.kvlen) return;
+                const int at = p.pool.page_of(tok);
+                block = (tok - at * p.pool.page_size) / kKvBlock;
+                page = __ldg(p.pool.table + (size_t)w.n * p.pool.max_pages + at);
+            };
+            auto fetch = [&]() {
+                return (unsigned)page < (unsigned)p.pool.n_pages
+                           ? __ldg(scales + ((size_t)page * p.pool.hkv + head) * (p.pool.page_size / kKvBlock) + block)
+                           : 0.f;
+            };
+            look_up();
+            float x = fetch();
+            if (units > 1) {
+                w.next();
+                look_up();
+            }
+            for (int u = 0; u < units; ++u) {
+                const int slot = u % kScaleSlots;
+                const float next = u + 1 < units ? fetch() : 0.f;
+                if (u + 2 < units) {
+                    w.next();
+                    look_up();
+                }
+                if (!wait(&sm.sc_empty[slot], u / kScaleSlots + 1)) break;
+                if (lane < 4) {
+                    sm.scale[slot][lane] = x;
+                } else if (lane < 8) {
+                    if (x == 0.f) x = kAmaxFloor;
+                    sm.scale[slot][lane] = log2f(x);
+                    sm.scale[slot][lane + 4] = 1.f / x;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.sc_full[slot]);
+                x = next;
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        tmem_relinquish();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the parts of the items that cross CTAs: a warp per row, lanes over the columns.
+template <int D>
+__global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendProblem p, const __grid_constant__ TcPlan plan) {
+    constexpr int ROWS = Tc<D>::ROWS, PER = D / 32;
+    const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + (threadIdx.x >> 5), group = p.hq / p.pool.hkv;
+    grid_dependency_wait();
+    const MergeMeta mm = plan.meta[blockIdx.x];
+    if (mm.last < 0) return;
+    const Sequence s = load_sequence(p, mm.n);
+    const long long grow = (long long)mm.mt * ROWS + row;
+    if (grow / group >= s.qlen) return;
+    const size_t stride = ROWS * D + 2 * ROWS;
+    const int count = mm.last - mm.first + 1;
+    auto part = [&](int k) { return plan.parts + (size_t)(2 * (mm.first + k) + (k == 0 ? mm.slot : 0)) * stride; };
+    float top = -INFINITY;
+    for (int k = 0; k < count; ++k) top = fmaxf(top, part(k)[ROWS * D + row]);
+    const float base = top == -INFINITY ? 0.f : top;
+    float l = 0.f, y[PER] = {};
+    for (int k = 0; k < count; ++k) {
+        const float w = exp2f(part(k)[ROWS * D + row] - base);
+        l = fmaf(w, part(k)[ROWS * D + ROWS + row], l);
+        const float *o = part(k) + row * D + lane * PER;
+#pragma unroll
+        for (int e = 0; e < PER; e += 2) {
+            const float2 x = *reinterpret_cast<const float2 *>(o + e);
+            y[e] = fmaf(w, x.x, y[e]);
+            y[e + 1] = fmaf(w, x.y, y[e + 1]);
+        }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) y[e] *= inv;
+    store_row<PER>(p, ((size_t)(s.q0 + (int)(grow / group)) * p.hq + mm.h * group + (int)(grow % group)) * D + lane * PER, y);
+}
+
+struct TcSizes {
+    long long items;
+    int ctas;
+    size_t start, per, list, parts, bytes;
+};
+
+// Workspace layout; `sms` bounds the CTAs (the size is asked for with the largest).
+TcSizes tc_sizes(int n_seqs, int total, int hq, int hkv, int d, int sms) {
+    TcSizes z;
+    const int rows = d == 256 ? 128 : 256;
+    z.items = hkv * (((long long)total * (hq / hkv) + rows - 1) / rows + n_seqs);
+    z.ctas = min(sms, kMaxTcCtas);
+    z.start = round256(kMaxTcCtas * sizeof(MergeMeta));
+    z.per = z.start + round256((kMaxTcCtas + 1) * sizeof(RunStart));
+    z.list = z.per + 256;
+    z.parts = z.list + round256((size_t)z.items * sizeof(int4));
+    z.bytes = z.parts + (size_t)2 * z.ctas * (rows * d + 2 * rows) * sizeof(float);
+    return z;
+}
+
+template <int D, int FMT>
+cudaError_t launch_tc(const AttendProblem &p) {
+    using L = Tc<D>;
+    const TcSizes z = tc_sizes(p.n_seqs, p.total, p.hq, p.pool.hkv, D, multiprocessor_count());
+    uint8_t *ws = static_cast<uint8_t *>(p.workspace);
+    TcPlan plan{};
+    plan.meta = reinterpret_cast<MergeMeta *>(ws);
+    plan.start = reinterpret_cast<RunStart *>(ws + z.start);
+    plan.per = reinterpret_cast<long long *>(ws + z.per);
+    plan.items = reinterpret_cast<int4 *>(ws + z.list);
+    plan.parts = reinterpret_cast<float *>(ws + z.parts);
+    plan.ctas = z.ctas;
+    constexpr size_t smem = sizeof(TcSmem<D>) + 1024;
+    static std::atomic<bool> ready[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= kMaxDevices || !ready[dev].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(attend_tc_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        if (dev < kMaxDevices) ready[dev].store(true, std::memory_order_relaxed);
+    }
+    attend_plan_kernel<L::ROWS><<<1, kPlanThreads, 0, p.stream>>>(p, plan);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_after(p.stream, dim3((unsigned)z.ctas), L::THREADS, smem, attend_tc_kernel<D, FMT>, p, plan)) != cudaSuccess) return e;
+    return launch_after(p.stream, dim3((unsigned)z.ctas, L::ROWS / 8), 256, 0, attend_join_kernel<D>, p, plan);
+}
+
+}  // namespace
+
+size_t attend_tc_workspace_bytes(int n_seqs, int total, int hq, int hkv, int d) {
+    return tc_sizes(n_seqs, total, hq, hkv, d, attend::kMaxTcCtas).bytes;
+}
+
+cudaError_t launch_attend_tc(const AttendProblem &p) {
+    const bool e4m3 = p.format == GDN_KV_E4M3;
+    switch (p.d) {
+        case 64: return e4m3 ? launch_tc<64, GDN_KV_E4M3>(p) : launch_tc<64, GDN_KV_INT8>(p);
+        case 128: return e4m3 ? launch_tc<128, GDN_KV_E4M3>(p) : launch_tc<128, GDN_KV_INT8>(p);
+        default: return e4m3 ? launch_tc<256, GDN_KV_E4M3>(p) : launch_tc<256, GDN_KV_INT8>(p);
+    }
+}
+
+}  // namespace gdn

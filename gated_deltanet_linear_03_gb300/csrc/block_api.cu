@@ -46,6 +46,8 @@ gdn_status check_pool(int hkv, int d, int max_pages, int n_pages, int page_size,
     return GDN_OK;
 }
 
+int page_shift(int page_size) { return (page_size & (page_size - 1)) == 0 ? __builtin_ctz((unsigned)page_size) : -1; }
+
 size_t pool_bytes(int hkv, int d, int n_pages, int page_size) { return (size_t)n_pages * hkv * page_size * d; }
 
 }  // namespace
@@ -110,7 +112,7 @@ gdn_status gdn_kv_append(int n_seqs, int total_tokens, int hq, int hkv, int d, i
     p.q_stride = q_stride; p.k_stride = k_stride; p.v_stride = v_stride;
     p.cos = cos; p.sin = sin; p.n_positions = rot > 0 ? n_positions : INT_MAX; p.interleaved = interleaved;
     p.cu = cu_seqlens; p.past = past_lens;
-    p.pool = {block_table, max_pages, n_pages, page_size, hkv};
+    p.pool = {block_table, max_pages, n_pages, page_size, hkv, page_shift(page_size)};
     p.format = format;
     p.k_pages = static_cast<uint8_t *>(k_pages); p.v_pages = static_cast<uint8_t *>(v_pages);
     p.k_scales = k_scales; p.v_scales = v_scales;
@@ -151,7 +153,7 @@ gdn_status gdn_kv_read(int n_seqs, int total_tokens, int hkv, int d, const int32
     gdn::ReadProblem p{};
     p.n_seqs = n_seqs; p.total = total_tokens; p.d = d;
     p.cu = cu_tokens;
-    p.pool = {block_table, max_pages, n_pages, page_size, hkv};
+    p.pool = {block_table, max_pages, n_pages, page_size, hkv, page_shift(page_size)};
     p.format = format;
     p.k_pages = static_cast<const uint8_t *>(k_pages); p.v_pages = static_cast<const uint8_t *>(v_pages);
     p.k_scales = k_scales; p.v_scales = v_scales;
@@ -216,7 +218,7 @@ gdn_status gdn_attend(int n_seqs, int total_tokens, int hq, int hkv, int d, cons
     gdn::AttendProblem p{};
     p.n_seqs = n_seqs; p.total = total_tokens; p.hq = hq; p.d = d;
     p.q = static_cast<const __nv_bfloat16 *>(q);
-    p.pool = {block_table, max_pages, n_pages, page_size, hkv};
+    p.pool = {block_table, max_pages, n_pages, page_size, hkv, page_shift(page_size)};
     p.format = format;
     p.k_pages = static_cast<const uint8_t *>(k_pages); p.v_pages = static_cast<const uint8_t *>(v_pages);
     p.k_scales = k_scales; p.v_scales = v_scales;

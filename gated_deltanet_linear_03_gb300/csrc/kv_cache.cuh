@@ -17,6 +17,8 @@ __host__ __device__ constexpr float kv_code_max() { return FMT == GDN_KV_INT8 ? 
 struct KvPool {
     const int32_t *table;   // [n_seqs, max_pages]
     int max_pages, n_pages, page_size, hkv;
+    int page_shift;         // log2 of page_size where that is a power of two, else -1
+    __device__ __forceinline__ int page_of(int token) const { return page_shift >= 0 ? token >> page_shift : token / page_size; }
 };
 
 // Four codes (one 32-bit word) to two fp16 pairs, exactly: (byte 0, byte 1) and (byte 2, byte 3).
