@@ -46,7 +46,7 @@ __device__ __forceinline__ void report_lengths(const AttendProblem &p, int cta) 
 
 template <int ROWS>
 __host__ __device__ __forceinline__ int row_tiles(int qlen, int group) {
-    return (int)(((long long)qlen * group + ROWS - 1) / ROWS);
+    return (qlen * group + ROWS - 1) / ROWS;   // rows of a call stay below 2^31 - 4096
 }
 
 // The tokens that ROWS consecutive query rows see together, in tiles: [0, near) of the sinks, then from `far` on.
@@ -67,7 +67,7 @@ __device__ __forceinline__ bool sees(int pos, int token, int window, int sinks) 
 template <int ROWS, int TILE>
 __device__ __forceinline__ Item make_item(const AttendProblem &p, const Sequence &s, int group, int mt) {
     Item it;
-    const int i0 = (int)((long long)mt * ROWS / group), i1 = (int)min((long long)s.qlen - 1, ((long long)mt * ROWS + ROWS - 1) / group);
+    const int i0 = mt * ROWS / group, i1 = min(s.qlen - 1, (mt * ROWS + ROWS - 1) / group);
     it.lo_pos = s.kvlen - s.qlen + i0;
     it.hi_pos = s.kvlen - s.qlen + i1;
     const int end = max(0, it.hi_pos + 1), end_tile = (end + TILE - 1) / TILE;
@@ -122,6 +122,19 @@ __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Two fp32 operations in one instruction: (a, b) = (a, b) * f + c, and (a, b) += (c, d).
+__device__ __forceinline__ void fma2(float &a, float &b, float f, float c) {
+    asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %2};\n mov.b64 z, {%3, %3};\n"
+        " fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
+        : "+f"(a), "+f"(b)
+        : "f"(f), "f"(c));
+}
+__device__ __forceinline__ void add2(float &a, float &b, float c, float d) {
+    asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+        : "+f"(a), "+f"(b)
+        : "f"(c), "f"(d));
 }
 
 __device__ __forceinline__ void lds128(uint32_t a, uint32_t (&w)[4]) {

@@ -39,14 +39,13 @@ struct Tc {
     static constexpr int ROWS = 128 * NQ;
     static constexpr int SB = NQ * (D + D / 2 + 128) <= 512 ? 2 : 1;   // score buffers of a tile
     static constexpr int O = 0, Q = NQ * D, S = NQ * (D + D / 2);      // TMEM columns
-    static constexpr int SOFTMAX_WARPS = 4 * NQ;
+    static constexpr int CS = 2 / NQ;                        // softmax threads a row, each on 64 / CS of a unit's tokens
+    static constexpr int SOFTMAX_WARPS = 8;
     static constexpr int WARPS = SOFTMAX_WARPS + kLoaderWarps + 4;     // the last four: MMA, scales, two idle
     static constexpr int THREADS = 32 * WARPS;
     // Registers a thread: at launch (the most that WARPS warps can have, a multiple of 8), then per role.  The roles'
-    // shares add up to what the CTA was launched with: 512 x 128 = 128 x 208 + 256 x 104 + 128 x 96 and
-    // 640 x 96 >= 256 x 152 + 256 x 56 + 128 x 56.
-    static constexpr int REGS_LAUNCH = NQ == 1 ? 128 : 96;
-    static constexpr int REGS_SOFTMAX = NQ == 1 ? 208 : 152, REGS_LOADER = NQ == 1 ? 104 : 56, REGS_OTHER = NQ == 1 ? 96 : 56;
+    // shares stay within what the CTA was launched with: 640 x 96 = 256 x 136 + 256 x 72 + 128 x 64.
+    static constexpr int REGS_LAUNCH = 96, REGS_SOFTMAX = 136, REGS_LOADER = 72, REGS_OTHER = 64;
     static_assert(32 * (SOFTMAX_WARPS * REGS_SOFTMAX + kLoaderWarps * REGS_LOADER + 4 * REGS_OTHER) <= THREADS * REGS_LAUNCH, "registers");
     static constexpr int TILE_BYTES = kTile * D * 2;
 };
@@ -59,6 +58,9 @@ struct __align__(1024) TcSmem {
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
     uint64_t s_full[Tc<D>::NQ][2], p_full[Tc<D>::NQ][2], pv_done[Tc<D>::NQ], q_full[Tc<D>::NQ];
     uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots], drain;
+    float row_scale[Tc<D>::ROWS];                  // the power of two taken out of each query row
+    float pair[2][Tc<D>::CS][128], pair_sum[Tc<D>::CS][128];   // maxima and sums that the two threads of a row tell each other
+    uint64_t pair_bar[4];
     uint32_t tmem;
     int abort;
 };
@@ -217,7 +219,7 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
     constexpr int NQ = L::NQ, SB = L::SB, ROWS = L::ROWS;
     extern __shared__ uint8_t raw[];
     TcSmem<D> &sm = *reinterpret_cast<TcSmem<D> *>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int group = p.hq / p.pool.hkv, cta = blockIdx.x;
 
     if (warp == 0) tmem_alloc(&sm.tmem, 512);
@@ -231,15 +233,16 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
         for (int q = 0; q < NQ; ++q) {
             for (int b = 0; b < 2; ++b) {
                 mbar_init(&sm.s_full[q][b], 1);
-                mbar_init(&sm.p_full[q][b], 4);
+                mbar_init(&sm.p_full[q][b], 4 * L::CS);
             }
             mbar_init(&sm.pv_done[q], 1);
-            mbar_init(&sm.q_full[q], 4);
+            mbar_init(&sm.q_full[q], 4 * L::CS);
         }
         for (int i = 0; i < kScaleSlots; ++i) {
             mbar_init(&sm.sc_full[i], 1);
             mbar_init(&sm.sc_empty[i], L::SOFTMAX_WARPS);
         }
+        for (int i = 0; i < 4; ++i) mbar_init(&sm.pair_bar[i], 2);
         mbar_init(&sm.drain, 1);
         sm.abort = 0;
         fence_mbar_init();
@@ -274,157 +277,176 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
     if (warp < L::SOFTMAX_WARPS) {
         set_max_registers_up<L::REGS_SOFTMAX>();
         // ------------------------------------------------------------------------------------------ softmax
-        const int q = warp / 4, row = tid % 128;
-        const uint32_t quad = tmem + ((uint32_t)(warp & 3) << 21);      // lanes 32 (warp % 4) ..
+        constexpr int CS = L::CS, NC = 64 / CS;                          // tokens of a thread's share of a unit
+        const int q = CS == 2 ? 0 : warp / 4, part_of = CS == 2 ? warp / 4 : 0, quadrant = warp & 3;
+        const int row = 32 * quadrant + lane;                            // of the 128-row tile
+        const uint32_t quad = tmem + ((uint32_t)quadrant << 21);         // its lanes
         const uint32_t o_at = quad + L::O + q * D, q_at = quad + L::Q + q * (D / 2), s_at = quad + L::S + q * SB * 64;
+        // The two warps that share rows meet at an mbarrier, so that this wait is bounded like the others.
+        int pair_phase = 0;
+        auto meet = [&]() -> bool {
+            __syncwarp();
+            if (CS == 1) return true;
+            if (lane == 0) mbar_arrive(&sm.pair_bar[quadrant]);
+            return wait(&sm.pair_bar[quadrant], pair_phase++);
+        };
         MergeMeta mm;
         mm.last = -1;
         if (units > 0) {
             Walk<ROWS> w(p, plan, group);
             bool ok = true;
-            for (int u = 0, seg = 0; ok && u < units; ++seg) {
-                // ---- a segment: the query row
+            int buf = 0, buf_phase = 0, slot = 0, slot_phase = 0;
+            for (int u = 0; ok && u < units;) {
+                // ---- a segment: the query rows
                 const bool begun = w.j == 0;
                 const int seg_slot = u == 0 ? 0 : 1;
-                const long long grow = (long long)w.mt * ROWS + q * 128 + row;
-                const int i = (int)min(grow / group, (long long)w.s.qlen);
+                const int grow = w.mt * ROWS + q * 128 + row, i = grow / group;
                 const bool valid = i < w.s.qlen;
                 const int pos = w.s.kvlen - w.s.qlen + i;
-                const size_t out_row = ((size_t)(w.s.q0 + (valid ? i : 0)) * p.hq + w.h * group + (int)(grow % group)) * D;
-                float rs;
-                {
-                    // 4 lanes to a row, 16 bytes each, 8 rows at a time: rows 16 half + 8 k + lane / 4 of the warp's 32
-                    rs = 0.f;
+                const size_t out_row = ((size_t)(w.s.q0 + (valid ? i : 0)) * p.hq + w.h * group + grow % group) * D;
+                // 4 lanes to a row, 16 bytes each, 8 rows at a time: rows 16 half + 8 k + lane / 4 of the warp's 32.  The
+                // first pass finds the rows' scales, the second (from L1) converts: fewer registers than holding them.
 #pragma unroll 1
-                    for (int half = 0; half < 2; ++half) {
-                        uint4 y[2][D / 32];
-                        float down[2];
+                for (int half = CS == 2 ? part_of : 0; half < (CS == 2 ? part_of + 1 : 2); ++half) {
+                    const uint4 *src[2];
+                    float down[2];
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const long long gr = (long long)w.mt * ROWS + q * 128 + 32 * (warp & 3) + 16 * half + 8 * k + lane / 4;
-                            const bool ok_row = gr / group < w.s.qlen;
-                            const uint4 *src = reinterpret_cast<const uint4 *>(
-                                p.q + ((size_t)(w.s.q0 + (ok_row ? (int)(gr / group) : 0)) * p.hq + w.h * group + (int)(gr % group)) * D) + lane % 4;
+                    for (int k = 0; k < 2; ++k) {
+                        const int r = 32 * quadrant + 16 * half + 8 * k + lane / 4, gr = w.mt * ROWS + q * 128 + r;
+                        const int i = gr / group;
+                        src[k] = i < w.s.qlen
+                                     ? reinterpret_cast<const uint4 *>(p.q + ((size_t)(w.s.q0 + i) * p.hq + w.h * group + gr % group) * D) + lane % 4
+                                     : nullptr;
+                        uint32_t big = 0;
 #pragma unroll
-                            for (int c = 0; c < D / 32; ++c) y[k][c] = ok_row ? __ldg(src + 4 * c) : make_uint4(0, 0, 0, 0);
-                        }
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            uint32_t big = 0;
-                            float up;
-#pragma unroll
-                            for (int c = 0; c < D / 32; ++c) big = max(big, amax_bits(y[k][c]));
-                            big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-                            big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-                            power_of_two_scale(big, down[k], up);
-                            if (p.sm_scale < 0.f) down[k] = -down[k];     // the row factor stays >= 0
-                            up = __shfl_sync(0xffffffffu, up, 4 * (lane % 8));
-                            if (lane / 8 == 2 * half + k) rs = up;
-                        }
-#pragma unroll
-                        for (int c = 0; c < D / 64; ++c) {
-                            uint32_t x[16];
-#pragma unroll
-                            for (int i2 = 0; i2 < 2; ++i2)
-#pragma unroll
-                                for (int k = 0; k < 2; ++k) {
-                                    const uint4 &z = y[k][2 * c + i2];
-                                    x[8 * i2 + 2 * k] = bf16x2_to_f16x2(z.x, down[k]);
-                                    x[8 * i2 + 2 * k + 1] = bf16x2_to_f16x2(z.y, down[k]);
-                                    x[8 * i2 + 4 + 2 * k] = bf16x2_to_f16x2(z.z, down[k]);
-                                    x[8 * i2 + 4 + 2 * k + 1] = bf16x2_to_f16x2(z.w, down[k]);
-                                }
-                            tmem_st_16x32(q_at + ((uint32_t)(16 * half) << 16) + 32 * c, x);
-                        }
+                        for (int c = 0; c < D / 32; ++c) big = max(big, amax_bits(src[k] ? __ldg(src[k] + 4 * c) : make_uint4(0, 0, 0, 0)));
+                        big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+                        big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+                        float up;
+                        power_of_two_scale(big, down[k], up);
+                        if (p.sm_scale < 0.f) down[k] = -down[k];     // the row factor stays >= 0
+                        if (lane % 4 == 0) sm.row_scale[q * 128 + r] = up;
                     }
-                    rs *= fabsf(p.sm_scale) * 1.4426950408889634f;
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.q_full[q]);
+#pragma unroll 2
+                    for (int c = 0; c < D / 64; ++c) {
+                        uint32_t x[16];
+#pragma unroll
+                        for (int i2 = 0; i2 < 2; ++i2)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const uint4 z = src[k] ? __ldg(src[k] + 4 * (2 * c + i2)) : make_uint4(0, 0, 0, 0);
+                                x[8 * i2 + 2 * k] = bf16x2_to_f16x2(z.x, down[k]);
+                                x[8 * i2 + 2 * k + 1] = bf16x2_to_f16x2(z.y, down[k]);
+                                x[8 * i2 + 4 + 2 * k] = bf16x2_to_f16x2(z.z, down[k]);
+                                x[8 * i2 + 4 + 2 * k + 1] = bf16x2_to_f16x2(z.w, down[k]);
+                            }
+                        tmem_st_16x32(q_at + ((uint32_t)(16 * half) << 16) + 32 * c, x);
+                    }
                 }
+                tmem_st_wait();
+                tc_fence_before();
+                if (!(ok = meet())) break;
+                if (lane == 0) mbar_arrive(&sm.q_full[q]);
+                const float rs = sm.row_scale[q * 128 + row] * fabsf(p.sm_scale) * 1.4426950408889634f;
                 float m = -INFINITY, l = 0.f;
                 bool ends;
                 for (bool first = true;; first = false) {
                     // ---- one unit
-                    const int buf = u % SB;
                     const uint32_t s_tm = s_at + buf * 64;
-                    const int tok0 = w.token();
+                    const int tok0 = w.token() + part_of * NC;
                     ends = w.last();
-                    if (!(ok = wait(&sm.s_full[q][buf], u / SB))) break;
-                    if (!(ok = wait(&sm.sc_full[u % kScaleSlots], u / kScaleSlots))) break;
+                    if (!(ok = wait(&sm.sc_full[slot], slot_phase))) break;
+                    if (!(ok = wait(&sm.s_full[q][buf], buf_phase))) break;
                     tc_fence_after();
-                    float s[64];
-                    tmem_ld32x2(s_tm, s_tm + 32, s, s + 32);
-                    float f[4], lv[4], rv[4];
-                    {
-                        const float *sc = sm.scale[u % kScaleSlots];
+                    const bool all_seen = w.it.all_seen(tok0, tok0 + NC, p.window, p.sinks);
+                    // 32 scores from `at` tokens into the share, with the factor and offset that make them x = s f + lv;
+                    // a score that the row does not see becomes -infinity
+                    float s[32], f[2], lv[2];
+                    auto load = [&](int at) {
+                        tmem_ld32(s_tm + part_of * NC + at, s);
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            f[b] = rs * sc[b];
-                            lv[b] = sc[4 + b];
-                            rv[b] = sc[8 + b];
+                        for (int b = 0; b < 2; ++b) {
+                            f[b] = rs * sm.scale[slot][part_of * (NC / 16) + at / 16 + b];
+                            lv[b] = sm.scale[slot][4 + part_of * (NC / 16) + at / 16 + b];
                         }
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.sc_empty[u % kScaleSlots]);
-                    if (!w.it.all_seen(tok0, tok0 + kTile, p.window, p.sinks)) {
+                        if (all_seen) return;
 #pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            s[c] = sees(pos, tok0 + c, p.window, p.sinks) ? fmaf(s[c], f[c / 16], lv[c / 16]) : -INFINITY;
+                        for (int c = 0; c < 32; ++c)
+                            s[c] = sees(pos, tok0 + at + c, p.window, p.sinks) ? fmaf(s[c], f[c / 16], lv[c / 16]) : -INFINITY;
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) f[b] = 1.f, lv[b] = 0.f;
-                    }
+                        for (int b = 0; b < 2; ++b) f[b] = 1.f, lv[b] = 0.f;
+                    };
                     float top = -INFINITY;
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        float x = s[16 * b];
+                    for (int at = 0; at < NC; at += 32) {
+                        load(at);
 #pragma unroll
-                        for (int c = 1; c < 16; ++c) x = fmaxf(x, s[16 * b + c]);
-                        top = fmaxf(top, fmaf(x, f[b], lv[b]));
-                    }
-                    const bool grow_max = first ? true : top > m + 8.f;
-                    if (first) {
-                        m = top;
-                    } else if (__any_sync(0xffffffffu, grow_max)) {
-                        if (!(ok = wait(&sm.pv_done[q], u - 1))) break;
-                        tc_fence_after();
-                        const float to = grow_max ? top : m, c = m == to ? 1.f : exp2f(m - to);
-                        m = to;
-                        l *= c;
-#pragma unroll 1
-                        for (int k = 0; k < D / 32; ++k) {
-                            float o[32];
-                            tmem_ld32(o_at + 32 * k, o);
-                            uint32_t x[32];
+                        for (int b = 0; b < 2; ++b) {
+                            float x[4];
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(o[e] * c);
-                            tmem_st32(o_at + 32 * k, x);
+                            for (int c = 0; c < 4; ++c) x[c] = fmaxf(fmaxf(s[16 * b + c], s[16 * b + 4 + c]), fmaxf(s[16 * b + 8 + c], s[16 * b + 12 + c]));
+                            top = fmaxf(top, fmaf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), f[b], lv[b]));
                         }
-                        tmem_st_wait();
+                    }
+                    if (CS == 2) {
+                        sm.pair[u & 1][part_of][row] = top;
+                        if (!(ok = meet())) break;   // both have read their scores too, so weights may overwrite them
+                        top = fmaxf(top, sm.pair[u & 1][CS - 1 - part_of][row]);
+                    }
+                    if (__any_sync(0xffffffffu, first || top > m + 8.f)) {
+                        if (first) {
+                            m = top;
+                        } else {
+                            if (!(ok = wait(&sm.pv_done[q], u - 1))) break;
+                            tc_fence_after();
+                            const float to = top > m + 8.f ? top : m, c = m == to ? 1.f : exp2f(m - to);
+                            m = to;
+                            l *= c;
+#pragma unroll 1
+                            for (int k = part_of; k < D / 32; k += CS) {
+                                float o[32];
+                                tmem_ld32(o_at + 32 * k, o);
+                                uint32_t x[32];
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(o[e] * c);
+                                tmem_st32(o_at + 32 * k, x);
+                            }
+                            tmem_st_wait();
+                        }
                     }
                     const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const float off = lv[b] - base;
-                        float sum = 0.f;
-                        uint32_t x[8];
+                    for (int at = 0; at < NC; at += 32) {
+                        if (NC > 32) load(at);   // two shares of 32 do not both stay in registers
+                        uint32_t x[16];
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            const float a = exp2_fast(fmaf(s[16 * b + 2 * c], f[b], off)), e = exp2_fast(fmaf(s[16 * b + 2 * c + 1], f[b], off));
-                            sum += a + e;
-                            const __half2 hh = __floats2half2_rn(a, e);
-                            x[c] = *reinterpret_cast<const uint32_t *>(&hh);
+                        for (int b = 0; b < 2; ++b) {
+                            const float off = lv[b] - base;
+                            float sum[2] = {0.f, 0.f};
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                float e0 = s[16 * b + 2 * c], e1 = s[16 * b + 2 * c + 1];
+                                fma2(e0, e1, f[b], off);
+                                e0 = exp2_fast(e0);
+                                e1 = exp2_fast(e1);
+                                add2(sum[0], sum[1], e0, e1);
+                                const __half2 hh = __floats2half2_rn(e0, e1);
+                                x[8 * b + c] = *reinterpret_cast<const uint32_t *>(&hh);
+                            }
+                            sum[0] += sum[1];
+                            // a block that no row sees may have any scale
+                            if (sum[0] != 0.f) l = fmaf(sum[0], sm.scale[slot][8 + part_of * (NC / 16) + at / 16 + b], l);
                         }
-                        if (sum != 0.f) l = fmaf(sum, rv[b], l);   // a block that no row sees may have any scale
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) s[8 * b + c] = __uint_as_float(x[c]);
+                        tmem_st16(s_tm + part_of * 16 + at / 2, x);   // columns below the ones still to be read
                     }
-                    tmem_st32(s_tm, reinterpret_cast<const uint32_t *>(s));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.sc_empty[slot]);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.p_full[q][buf]);
+                    if (++buf == SB) buf = 0, buf_phase ^= 1;
+                    if (++slot == kScaleSlots) slot = 0, slot_phase ^= 1;
                     ++u;
                     if (ends || u == units) break;
                     w.next();
@@ -433,11 +455,16 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                 // ---- the segment's end
                 if (!(ok = wait(&sm.pv_done[q], u - 1))) break;
                 tc_fence_after();
+                if (CS == 2) {
+                    sm.pair_sum[part_of][row] = l;
+                    if (!(ok = meet())) break;
+                    l += sm.pair_sum[CS - 1 - part_of][row];
+                }
                 const bool whole = begun && ends;
                 float *part = plan.parts + (size_t)(2 * cta + seg_slot) * (ROWS * D + 2 * ROWS) + (size_t)(q * 128 + row) * D;
                 const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
 #pragma unroll 1
-                for (int k = 0; k < D / 32; ++k) {
+                for (int k = part_of; k < D / 32; k += CS) {
                     float o[32];
                     tmem_ld32(o_at + 32 * k, o);
 #pragma unroll
@@ -450,7 +477,7 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                     }
                     __syncwarp();   // the next load is warp-wide
                 }
-                if (!whole) {
+                if (!whole && part_of == 0) {
                     float *ml = plan.parts + (size_t)(2 * cta + seg_slot) * (ROWS * D + 2 * ROWS) + ROWS * D;
                     ml[q * 128 + row] = m;
                     ml[ROWS + q * 128 + row] = l;
@@ -549,56 +576,72 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
         set_max_registers_down<L::REGS_OTHER>();
         const int role = warp - L::SOFTMAX_WARPS - kLoaderWarps;
         // ------------------------------------------------------------------------------------------ MMA
-        if (role == 0 && lane == 0 && units > 0) {
-            Walk<ROWS> w(p, plan, group);
+        if (role == 0 && units > 0 && elect_one()) {
+            // Only the ends of the items matter here: units left of this one, the next one's read ahead.
+            int item = plan.start[cta].item, left = plan.items[item].w - plan.start[cta].j, next_left = 0;
+            if (left < units) next_left = plan.items[item + 1].w;
             constexpr uint32_t id_s = idesc_f16_f32(128, kTile, false, false), id_o = idesc_f16_f32(128, D, false, true);
-            auto scores = [&](int q, int u) {     // S = Q K^T of unit u
-                const uint64_t kd = smem_desc(smem_u32(sm.k[u % kStages]), 16, 1024, kLayoutSwizzle128B);
-                const uint32_t d = tmem + L::S + (q * SB + u % SB) * 64, a = tmem + L::Q + q * (D / 2);
+            const uint64_t kd0 = smem_desc(smem_u32(sm.k[0]), 16, 1024, kLayoutSwizzle128B);
+            const uint64_t vd0 = smem_desc(smem_u32(sm.v[0]), kTile * 128, 1024, kLayoutSwizzle128B);
+            constexpr uint32_t kStep = L::TILE_BYTES >> 4;
+            auto scores = [&](int q, int stage, int buf) {     // S = Q K^T
+                const uint64_t kd = kd0 + stage * kStep;
+                const uint32_t d = tmem + L::S + (q * SB + buf) * 64, a = tmem + L::Q + q * (D / 2);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) mma_tmem_a(d, a + 8 * k, kd + ((k >> 2) * (kTile * 128) >> 4) + 2 * (k & 3), id_s, k > 0);
-                mma_commit(&sm.s_full[q][u % SB]);
+                mma_commit(&sm.s_full[q][buf]);
             };
-            auto outputs = [&](int q, int u, bool first) {   // O += W V of unit u
-                const uint64_t vd = smem_desc(smem_u32(sm.v[u % kStages]), kTile * 128, 1024, kLayoutSwizzle128B);
-                const uint32_t a = tmem + L::S + (q * SB + u % SB) * 64;
+            auto outputs = [&](int q, int stage, int buf, bool first) {   // O += W V
+                const uint64_t vd = vd0 + stage * kStep;
+                const uint32_t a = tmem + L::S + (q * SB + buf) * 64;
 #pragma unroll
                 for (int k = 0; k < kTile / 16; ++k) mma_tmem_a(tmem + L::O + q * D, a + 8 * k, vd + 128 * k, id_o, !(first && k == 0));
                 mma_commit(&sm.pv_done[q]);
             };
-            bool ok = true;
-            for (int u = 0, seg = 0; ok && u < units; ++seg) {
-                for (int q = 0; q < NQ && ok; ++q) ok = wait_one(&sm.q_full[q], seg);
-                if (ok) ok = wait_one(&sm.k_full[u % kStages], u / kStages);
-                if (!ok) break;
-                tc_fence_after();
-                for (int q = 0; q < NQ; ++q) scores(q, u);
-                mma_commit(&sm.k_empty[u % kStages]);
-                for (bool first = true;; first = false) {
-                    const bool ends = w.last() || u == units - 1;
-                    if (!ends) {
-                        if (!(ok = wait_one(&sm.k_full[(u + 1) % kStages], (u + 1) / kStages))) break;
-                        tc_fence_after();
-                        if (SB == 2) {
-                            for (int q = 0; q < NQ; ++q) scores(q, u + 1);
-                            mma_commit(&sm.k_empty[(u + 1) % kStages]);
-                        }
-                    }
-                    if (!(ok = wait_one(&sm.v_full[u % kStages], u / kStages))) break;
-                    for (int q = 0; q < NQ && ok; ++q) {
-                        if (!(ok = wait_one(&sm.p_full[q][u % SB], u / SB))) break;
-                        tc_fence_after();
-                        outputs(q, u, first);
-                        if (SB == 1 && !ends) scores(q, u + 1);
-                    }
-                    if (!ok) break;
-                    mma_commit(&sm.v_empty[u % kStages]);
-                    if (SB == 1 && !ends) mma_commit(&sm.k_empty[(u + 1) % kStages]);
-                    ++u;
-                    if (ends) break;
-                    w.next();
+            int st = 0, ph = 0, buf = 0, buf_phase = 0, seg = 0;   // of unit u
+            bool first = true;
+            for (int u = 0; u < units; ++u) {
+                if (first) {
+                    bool ok = true;
+                    for (int q = 0; q < NQ; ++q) ok = ok && wait_one(&sm.q_full[q], seg);
+                    if (!ok || !wait_one(&sm.k_full[st], ph)) break;
+                    tc_fence_after();
+                    for (int q = 0; q < NQ; ++q) scores(q, st, buf);
+                    mma_commit(&sm.k_empty[st]);
                 }
-                if (ok && u < units) w.next();
+                const bool ends = left == 1 || u == units - 1;
+                const int nst = st + 1 == kStages ? 0 : st + 1, nph = nst == 0 ? ph ^ 1 : ph;
+                const int nbuf = SB == 2 ? buf ^ 1 : 0, nbuf_phase = nbuf == 0 ? buf_phase ^ 1 : buf_phase;
+                if (!ends) {
+                    if (!wait_one(&sm.k_full[nst], nph)) break;
+                    tc_fence_after();
+                    if (SB == 2) {
+                        for (int q = 0; q < NQ; ++q) scores(q, nst, nbuf);
+                        mma_commit(&sm.k_empty[nst]);
+                    }
+                }
+                if (!wait_one(&sm.v_full[st], ph)) break;
+                bool ok = true;
+                for (int q = 0; q < NQ; ++q) {
+                    if (!(ok = wait_one(&sm.p_full[q][buf], buf_phase))) break;
+                    tc_fence_after();
+                    outputs(q, st, buf, first);
+                    if (SB == 1 && !ends) scores(q, nst, nbuf);
+                }
+                if (!ok) break;
+                mma_commit(&sm.v_empty[st]);
+                if (SB == 1 && !ends) mma_commit(&sm.k_empty[nst]);
+                st = nst;
+                ph = nph;
+                buf = nbuf;
+                buf_phase = nbuf_phase;
+                first = ends;
+                if (--left == 0) {
+                    ++seg;
+                    ++item;
+                    left = next_left;
+                    if (u + 1 + left < units) next_left = plan.items[item + 1].w;
+                }
             }
             // every MMA has finished before the tensor memory is given back
             mma_commit(&sm.drain);
@@ -667,7 +710,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     const MergeMeta mm = plan.meta[blockIdx.x];
     if (mm.last < 0) return;
     const Sequence s = load_sequence(p, mm.n);
-    const long long grow = (long long)mm.mt * ROWS + row;
+    const int grow = mm.mt * ROWS + row;
     if (grow / group >= s.qlen) return;
     const size_t stride = ROWS * D + 2 * ROWS;
     const int count = mm.last - mm.first + 1;
@@ -690,7 +733,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
     for (int e = 0; e < PER; ++e) y[e] *= inv;
-    store_row<PER>(p, ((size_t)(s.q0 + (int)(grow / group)) * p.hq + mm.h * group + (int)(grow % group)) * D + lane * PER, y);
+    store_row<PER>(p, ((size_t)(s.q0 + grow / group) * p.hq + mm.h * group + grow % group) * D + lane * PER, y);
 }
 
 struct TcSizes {

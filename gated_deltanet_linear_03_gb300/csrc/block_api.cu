@@ -171,6 +171,7 @@ static gdn_status check_attend_shape(int n_seqs, int total_tokens, int hq, int h
     if (n_seqs == 0 && total_tokens > 0) return GDN_ERR_INVALID_ARG;
     if (hq % hkv != 0 || (total_tokens > 0 && max_q_len == 0)) return GDN_ERR_INVALID_ARG;
     if (d != 64 && d != 128 && d != 256) return GDN_ERR_UNSUPPORTED;
+    if ((double)total_tokens * hq >= 2147483648.0 - 4096) return GDN_ERR_UNSUPPORTED;   // the kernels count query rows in 32 bits
     return GDN_OK;
 }
 
