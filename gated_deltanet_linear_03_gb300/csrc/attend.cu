@@ -12,7 +12,8 @@
 // the device, so a captured graph follows them.  A CTA writes finished items to `out`; of an item that crosses
 // CTAs each writes (O, M, l) to the workspace and attend_merge_kernel joins them.
 //
-// A unit in a CTA of 4 warps: cp.async brings K and V rows (codes) through a ring of shared-memory stages; warp w
+// A CTA has a producer warp and four compute warps.  The producer looks pages up a unit ahead and brings K and V
+// rows (codes) and block scales through a ring of shared-memory stages with cp.async.  Of a unit, compute warp w
 // forms the 16 x 16 scores of tokens 16 w .. 16 w + 15 (one scale block) with mma.m16n8k16 on codes turned to
 // fp16 exactly; the warps exchange row maxima and weights through shared memory; warp w then accumulates columns
 // [w D/4, (w + 1) D/4) of O over all 64 tokens.  Splitting O by columns keeps it at D/8 registers a thread.
@@ -26,7 +27,8 @@ using namespace attend;
 
 constexpr int kRows = 16;        // query rows of an item
 constexpr int kTile = 64;        // tokens of a unit
-constexpr int kThreads = 128;
+constexpr int kCompute = 128;    // threads of the compute warps
+constexpr int kThreads = kCompute + 32;
 
 template <int D>
 __host__ __device__ constexpr int stages() { return D == 256 ? 3 : D == 128 ? 4 : 6; }
@@ -40,6 +42,8 @@ struct __align__(128) Smem {
     __half p[kRows * kTile];               // weights, 16-byte pieces swizzled by row
     float scale[stages<D>()][8];           // K scales of the unit's four blocks, then V scales
     float red[4][kRows];                   // row maxima (then sums) of the four warps
+    uint64_t full[stages<D>()], empty[stages<D>()];
+    int abort;
     long long scan[4];
     int start_seq;
     long long start_off;
@@ -61,9 +65,13 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int by
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// Arrive on `bar` once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sm100::smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// The compute warps' barrier.  None of them leaves the unit loop early (a wait that runs out only sets a flag).
+__device__ __forceinline__ void sync_compute() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kCompute) : "memory"); }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -117,8 +125,16 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D>()) attend_split_kerne
     sm100::grid_launch_dependents();
 
     // ---- this CTA's units: a scan over the sequences' costs
-    const int chunk = (p.n_seqs + kThreads - 1) / kThreads;
-    const int s_lo = min(tid * chunk, p.n_seqs), s_hi = min(s_lo + chunk, p.n_seqs);
+    if (tid == kCompute) {
+        for (int i = 0; i < S; ++i) {
+            sm100::mbar_init(&sm.full[i], 32);
+            sm100::mbar_init(&sm.empty[i], 4);
+        }
+        sm.abort = 0;
+        sm100::fence_mbar_init();
+    }
+    const int chunk = (p.n_seqs + kCompute - 1) / kCompute;
+    const int s_lo = tid < kCompute ? min(tid * chunk, p.n_seqs) : p.n_seqs, s_hi = min(s_lo + chunk, p.n_seqs);
     long long mine = 0;
     for (int n = s_lo; n < s_hi; ++n) mine += sequence_cost<kRows, kTile>(p, load_sequence(p, n), group);
     long long upto = mine;
@@ -127,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D>()) attend_split_kerne
         const long long y = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += y;
     }
-    if (lane == 31) sm.scan[warp] = upto;
+    if (lane == 31 && warp < 4) sm.scan[warp] = upto;
     __syncthreads();
     long long total = 0;
 #pragma unroll
@@ -170,7 +186,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D>()) attend_split_kerne
         }
         cc.j = (int)off;
     }
-    Cursor lc = cc;   // the unit being loaded
     auto advance = [&](Cursor &c) {
         if (++c.j < c.it.tiles) return;
         c.j = 0;
@@ -186,45 +201,70 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D>()) attend_split_kerne
         }
         c.it = make_item<kRows, kTile>(p, c.s, group, c.mt);
     };
-
-    // ---- loads of one unit into a stage
-    auto issue = [&](int stage) {
-        constexpr int UPR = D / 16, RPP = kThreads / UPR;   // pieces a row, rows a pass of the CTA
-        const int tok0 = lc.it.token(lc.j, kTile);
-        int row = -1;                                       // pool row of the lane's block's first token
-        const int bt = tok0 + (lane & 3) * kKvBlock;
-        if (bt < lc.s.kvlen) {
-            const int page = p.pool.table[(size_t)lc.n * p.pool.max_pages + bt / p.pool.page_size];
-            if (page >= 0 && page < p.pool.n_pages)
-                row = (page * p.pool.hkv + lc.h) * p.pool.page_size + bt % p.pool.page_size;
-            else if (tid < 4)
-                raise_error(p.err, kErrInternal);
-        }
-        if (tid < 8) {
-            const float *sc = tid < 4 ? p.k_scales : p.v_scales;
-            cp_async4(sm100::smem_u32(&sm.scale[stage][tid]), row >= 0 ? sc + row / kKvBlock : sc, row >= 0 ? 4 : 0);
-        }
-        const int u = tid % UPR, r0 = tid / UPR;
-        const uint32_t ks = sm100::smem_u32(sm.k[stage]), vs = sm100::smem_u32(sm.v[stage]);
-#pragma unroll
-        for (int i = 0; i < kTile / RPP; ++i) {
-            const int r = r0 + i * RPP;
-            const int base = __shfl_sync(0xffffffffu, row, r / kKvBlock);
-            const bool ok = base >= 0 && tok0 + r < lc.s.kvlen;
-            const size_t off = ok ? (size_t)(base + r % kKvBlock) * D + u * 16 : 0;
-            cp_async16(ks + piece<D>(r, u), p.k_pages + off, ok ? 16 : 0);
-            cp_async16(vs + piece<D>(r, u), p.v_pages + off, ok ? 16 : 0);
+    // A bounded wait; when it runs out the error is recorded and every later wait returns at once.
+    volatile int *abort = &sm.abort;
+    auto wait = [&](uint64_t *bar, int phase) {
+        if (sm100::mbar_try_wait(bar, (uint32_t)phase & 1)) return;
+        const uint64_t t0 = sm100::global_timer_ns();
+        while (!sm100::mbar_try_wait(bar, (uint32_t)phase & 1)) {
+            if (*abort) return;
+            if (sm100::global_timer_ns() - t0 > sm100::kWaitTimeoutNs) {
+                *abort = 1;
+                raise_error(p.err, kErrTimeout);
+                return;
+            }
         }
     };
-
     const int units = (int)(stop - start);
+
+    if (warp == 4) {
+        // ---- the producer: lane b (mod 4) holds the pool row where block b of a unit begins, -1 for none
+        auto look_up = [&]() -> int {
+            const int tok = cc.it.token(cc.j, kTile) + (lane & 3) * kKvBlock;
+            if (tok >= cc.s.kvlen) return -1;
+            const int at = p.pool.page_of(tok), page = __ldg(p.pool.table + (size_t)cc.n * p.pool.max_pages + at);
+            if ((unsigned)page < (unsigned)p.pool.n_pages) return (page * p.pool.hkv + cc.h) * p.pool.page_size + tok - at * p.pool.page_size;
+            raise_error(p.err, kErrInternal);
+            return -1;
+        };
+        constexpr int UPR = D / 16, RPI = 32 / UPR;      // pieces a row, rows a warp-wide copy
+        const int u = lane % UPR, r0 = lane / UPR;
+        int row = look_up(), kept = cc.s.kvlen - cc.it.token(cc.j, kTile);   // tokens of the unit that exist
+        int stage = 0, phase = 1;
+        for (int unit = 0; unit < units; ++unit) {
+            int next_row = -1, next_kept = 0;
+            if (unit + 1 < units) {
+                advance(cc);
+                next_row = look_up();
+                next_kept = cc.s.kvlen - cc.it.token(cc.j, kTile);
+            }
+            wait(&sm.empty[stage], phase);
+            if (*abort) break;
+            if (lane < 8) {
+                const float *sc = lane < 4 ? p.k_scales : p.v_scales;
+                cp_async4(sm100::smem_u32(&sm.scale[stage][lane]), row >= 0 ? sc + row / kKvBlock : sc, row >= 0 ? 4 : 0);
+            }
+            const uint32_t ks = sm100::smem_u32(sm.k[stage]), vs = sm100::smem_u32(sm.v[stage]);
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i) {
-        if (i < units) {
-            issue(i);
-            advance(lc);
+            for (int b = 0; b < kTile / kKvBlock; ++b) {
+                const int base = __shfl_sync(0xffffffffu, row, b);
+                const size_t off = base >= 0 ? (size_t)base * D + r0 * D + u * 16 : 0;
+#pragma unroll
+                for (int i = 0; i < kKvBlock / RPI; ++i) {
+                    const int r = b * kKvBlock + i * RPI + r0;
+                    const int bytes = base >= 0 && r < kept ? 16 : 0;        // rows that do not exist become zeros
+                    const size_t at = bytes ? off + i * RPI * D : 0;
+                    cp_async16(ks + piece<D>(r, u), p.k_pages + at, bytes);
+                    cp_async16(vs + piece<D>(r, u), p.v_pages + at, bytes);
+                }
+            }
+            cp_async_arrive(&sm.full[stage]);
+            if (++stage == S) stage = 0, phase ^= 1;
+            row = next_row;
+            kept = next_kept;
         }
-        cp_async_commit();
+        cp_async_wait_all();
+        return;
     }
 
     uint32_t qf[KI][4][4];      // queries in fp16: rows g and g + 8, component order as the codes are read
@@ -234,8 +274,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D>()) attend_split_kerne
     bool begun = false;         // the segment starts its item
     int seg_unit = 0;           // first unit of the segment
 
+    int stage = 0, phase = 0;
     for (int unit = 0; unit < units; ++unit) {
-        const int stage = unit % S;
         if (unit == 0 || cc.j == 0) {   // a new item: queries to registers
             begun = cc.j == 0;
             seg_unit = unit;
@@ -278,13 +318,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D>()) attend_split_kerne
                 for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
         }
 
-        cp_async_wait<S - 2>();
-        __syncthreads();
-        if (unit + S - 1 < units) {
-            issue((unit + S - 1) % S);
-            advance(lc);
-        }
-        cp_async_commit();
+        wait(&sm.full[stage], phase);
+        __syncwarp();
 
         // ---- scores of this warp's 16 tokens
         const int tok0 = cc.it.token(cc.j, kTile) + warp * kKvBlock;
@@ -326,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D>()) attend_split_kerne
             big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
             if (t == 0) sm.red[warp][g + 8 * r] = big;
         }
-        __syncthreads();
+        sync_compute();
         // ---- weights
         float corr[2];
 #pragma unroll
@@ -353,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D>()) attend_split_kerne
             acc[i][0] *= corr[0]; acc[i][1] *= corr[0];
             acc[i][2] *= corr[1]; acc[i][3] *= corr[1];
         }
-        __syncthreads();
+        sync_compute();
         // ---- outputs: this warp's columns over all 64 tokens
         const uint32_t vbase = sm100::smem_u32(sm.v[stage]), pbase = sm100::smem_u32(sm.p);
 #pragma unroll
@@ -372,6 +407,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D>()) attend_split_kerne
 #pragma unroll
             for (int i = 0; i < NT; ++i) mma_f16(acc[i], a, b0[i], b1[i]);
         }
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(&sm.empty[stage]);
+        if (++stage == S) stage = 0, phase ^= 1;
 
         // ---- the segment's end: finish the item, or hand its part to the merge
         const bool ends = cc.j == cc.it.tiles - 1;
@@ -382,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D>()) attend_split_kerne
                 l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
                 if (t == 0) sm.red[warp][g + 8 * r] = l[r];   // every warp has read the maxima
             }
-            __syncthreads();
+            sync_compute();
             const bool whole = begun && ends;
             const int slot = 2 * cta + (seg_unit == 0 ? 0 : 1);
             float *part = plan.parts + (size_t)slot * (kRows * D + 2 * kRows);
@@ -423,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D>()) attend_split_kerne
                 mm.mt = cc.mt;
                 plan.meta[plan.meta_by_item ? (cc.n * p.pool.hkv + cc.h) * plan.mt_max + cc.mt : cta] = mm;
             }
-            __syncthreads();   // red is free again
+            sync_compute();   // red is free again
         }
         advance(cc);
     }
@@ -431,11 +469,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D>()) attend_split_kerne
 
 constexpr int kMergeThreads = 256;
 
-// Joins the parts of one item's row: o = sum_i 2^{M_i - M} O_i / sum_i 2^{M_i - M} l_i.
+// Joins the parts of one item's row, 64 columns a CTA: o = sum_i 2^{M_i - M} O_i / sum_i 2^{M_i - M} l_i.  16 lanes
+// hold the columns and 16 groups of them share the parts, so that all of an item's parts are asked for at once.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const __grid_constant__ AttendProblem p,
                                                                      const __grid_constant__ SplitPlan plan) {
-    constexpr int LANES = D / 4, GROUPS = kMergeThreads / LANES;
+    constexpr int LANES = 16, GROUPS = kMergeThreads / LANES;
     __shared__ float weight[kMaxSplitCtas];
     __shared__ float red[2][kMergeThreads / 32];
     __shared__ float4 sum[GROUPS][LANES];
@@ -454,6 +493,13 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const __gri
     const size_t stride = ROWS * D + 2 * ROWS;
     const int count = mm.last - mm.first + 1;
     auto part = [&](int k) { return plan.parts + (size_t)(2 * (mm.first + k) + (k == 0 ? mm.slot : 0)) * stride; };
+
+    const int col = blockIdx.z * 64 + 4 * (tid % LANES), grp = tid / LANES;
+    constexpr int HELD = 8;   // parts of a thread that are asked for before the weights are known
+    float4 held[HELD];
+#pragma unroll
+    for (int k = 0; k < HELD; ++k)
+        if (grp + k * GROUPS < count) held[k] = *reinterpret_cast<const float4 *>(part(grp + k * GROUPS) + row * D + col);
 
     float big = -INFINITY;
     for (int k = tid; k < count; k += kMergeThreads) {
@@ -482,24 +528,23 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const __gri
 #pragma unroll
     for (int w = 0; w < kMergeThreads / 32; ++w) l += red[1][w];
 
-    const int at = tid % LANES, grp = tid / LANES;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = grp; k < count; k += GROUPS) {
-        const float4 o = *reinterpret_cast<const float4 *>(part(k) + row * D + 4 * at);
-        const float w = weight[k];
+    auto add = [&](const float4 &o, float w) {
         a.x += w * o.x; a.y += w * o.y; a.z += w * o.z; a.w += w * o.w;
-    }
-    sum[grp][at] = a;
+    };
+#pragma unroll
+    for (int k = 0; k < HELD; ++k)
+        if (grp + k * GROUPS < count) add(held[k], weight[grp + k * GROUPS]);
+    for (int k = grp + HELD * GROUPS; k < count; k += GROUPS)
+        add(*reinterpret_cast<const float4 *>(part(k) + row * D + col), weight[k]);
+    sum[grp][tid % LANES] = a;
     __syncthreads();
     if (grp != 0) return;
 #pragma unroll
-    for (int k = 1; k < GROUPS; ++k) {
-        const float4 o = sum[k][at];
-        a.x += o.x; a.y += o.y; a.z += o.z; a.w += o.w;
-    }
+    for (int k = 1; k < GROUPS; ++k) add(sum[k][tid], 1.f);
     const float f = l == 0.f ? 0.f : 1.f / l;
     const float y[4] = {a.x * f, a.y * f, a.z * f, a.w * f};
-    store_row<4>(p, ((size_t)(s.q0 + i) * p.hq + mm.h * group + grow % group) * D + 4 * at, y);
+    store_row<4>(p, ((size_t)(s.q0 + i) * p.hq + mm.h * group + grow % group) * D + col, y);
 }
 
 long long unit_bound(int n_seqs, int hq, int hkv, int max_q_len, int max_kv_len) {
@@ -534,7 +579,7 @@ cudaError_t launch_split(const AttendProblem &p) {
     attend_split_kernel<D, FMT><<<ctas, kThreads, sizeof(Smem<D>), p.stream>>>(p, plan);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (ctas == 1 || bound == items) return cudaSuccess;   // no item crosses CTAs
-    return launch_after(p.stream, dim3((unsigned)(plan.meta_by_item ? items : ctas), kRows), kMergeThreads, 0,
+    return launch_after(p.stream, dim3((unsigned)(plan.meta_by_item ? items : ctas), (unsigned)min(kRows, p.max_q_len * group), D / 64), kMergeThreads, 0,
                         attend_merge_kernel<D, kRows>, p, plan);
 }
 

@@ -2,9 +2,10 @@
 //
 //     y = x rsqrt(mean(x^2) + eps) w_post,   y *= act(gate),   r' = r + s y,   h = r' rsqrt(mean(r'^2) + eps) w_pre
 //
-// One CTA holds one row in registers (pieces of 8 elements, C of them a thread), so x, gate and residual are
-// read once and r' and h written once; the two sums of squares are CTA reductions in fp32.  Every load of the
-// row and of the weights is issued before the first reduction.  Bound by memory.
+// A CTA carries rows one after another, one at a time in registers (pieces of 8 elements, C of them a thread), so x,
+// gate and residual are read once and r' and h written once; the two sums of squares are CTA reductions in fp32.  The
+// next row's pieces are asked for before this row's sums are formed, and the weights stay in registers: with a row a
+// CTA the weights came from L1 for every row, more bytes than the row itself.  Bound by memory.
 #include "kv_cache.cuh"
 
 namespace gdn {
@@ -41,71 +42,122 @@ __device__ __forceinline__ float cta_sum(float v, float *part) {
     return v;
 }
 
+// The pieces of one row as they lie in memory.
 template <int C, bool RES32>
-__global__ void __launch_bounds__(512) block_norm_kernel(const __grid_constant__ BlockNormProblem p) {
-    __shared__ float part[2][16];
-    const int pieces = p.dim / 8, nt = blockDim.x;
-    const size_t base = (size_t)blockIdx.x * p.dim;
-    float y[C][8], r[C][8], g[C][8];
-    float ss = 0.f;
+struct RowPieces {
+    uint4 x[C], gate[C], res[C][RES32 ? 2 : 1];
+    __device__ __forceinline__ void load(const BlockNormProblem &p, int row, int pieces) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-        const int c = threadIdx.x + i * nt;
-        if (c < pieces) {
-            const size_t at = base + 8 * (size_t)c;
-            unpack8(*reinterpret_cast<const uint4 *>(p.x + at), y[i]);
-            if (p.gate) unpack8(*reinterpret_cast<const uint4 *>(p.gate + at), g[i]);
-            if (RES32) load8f(static_cast<const float *>(p.residual) + at, r[i]);
-            else unpack8(*reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.residual) + at), r[i]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[i][e] = r[i][e] = g[i][e] = 0.f;
+        for (int i = 0; i < C; ++i) {
+            const int c = threadIdx.x + i * blockDim.x;
+            const size_t at = (size_t)row * p.dim + 8 * (size_t)c;
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            const bool ok = c < pieces;
+            x[i] = ok ? *reinterpret_cast<const uint4 *>(p.x + at) : zero;
+            gate[i] = ok && p.gate ? *reinterpret_cast<const uint4 *>(p.gate + at) : zero;
+            const uint4 *r = RES32 ? reinterpret_cast<const uint4 *>(static_cast<const float *>(p.residual) + at)
+                                   : reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.residual) + at);
+            res[i][0] = ok ? r[0] : zero;
+            if constexpr (RES32) res[i][1] = ok ? r[1] : zero;
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(y[i][e], y[i][e], ss);
     }
+};
+
+// STAY: the next row and the weights are held in registers.  A row of more than 8192 needs them for itself, and is one
+// of few: its CTA loads it when it comes to it, and the weights where they are used.
+template <int C, bool RES32, bool STAY>
+__global__ void __launch_bounds__(STAY ? 512 : 1024, C == 1 ? 2 : 1) block_norm_kernel(const __grid_constant__ BlockNormProblem p) {
+    __shared__ float part[2][2][32];   // by sum, and by turn: a row's last reader may still be at the other turn's
+    int turn = 0;
+    const int pieces = p.dim / 8, nt = blockDim.x;
     const float inv_dim = 1.f / p.dim;
-    float f = 1.f;
-    if (p.post_w) f = rsqrtf(cta_sum(ss, part[0]) * inv_dim + p.eps);
-    ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
+    RowPieces<C, RES32> next;
+    int row = blockIdx.x;
+    if (STAY) next.load(p, row, pieces);
+    // what y is multiplied by, the norm's weight and the scale, for this thread's piece i; and the weight of h
+    auto load_post = [&](int i, float (&w)[8]) {
         const int c = threadIdx.x + i * nt;
-        if (c >= pieces) continue;
-        float w[8], s[8];
+        float s[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] = 1.f, s[e] = p.scale;
-        if (p.post_w) load8f(p.post_w + 8 * c, w);
-        if (p.scale_w) load8f(p.scale_w + 8 * c, s);
+        if (c < pieces && p.post_w) load8f(p.post_w + 8 * c, w);
+        if (c < pieces && p.scale_w) load8f(p.scale_w + 8 * c, s);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float v = y[i][e] * f * w[e];
-            if (p.gate) {
-                const float sig = 1.f / (1.f + __expf(-g[i][e]));
-                v *= p.silu ? g[i][e] * sig : sig;
-            }
-            r[i][e] = fmaf(s[e], v, r[i][e]);
-            ss = fmaf(r[i][e], r[i][e], ss);
-        }
-        const size_t at = base + 8 * (size_t)c;
-        if (RES32) {
-            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.residual_out) + at);
-            o[0] = make_float4(r[i][0], r[i][1], r[i][2], r[i][3]);
-            o[1] = make_float4(r[i][4], r[i][5], r[i][6], r[i][7]);
-        } else {
-            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.residual_out) + at) = pack8(r[i]);
+        for (int e = 0; e < 8; ++e) w[e] *= s[e];
+    };
+    auto load_pre = [&](int i, float (&w)[8]) {
+        const int c = threadIdx.x + i * nt;
+        if (c < pieces) load8f(p.pre_w + 8 * c, w);
+    };
+    float post[C][8], pre[C][8];
+    if (STAY) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            load_post(i, post[i]);
+            load_pre(i, pre[i]);
         }
     }
-    f = rsqrtf(cta_sum(ss, part[1]) * inv_dim + p.eps);
+    for (; row < p.rows; row += gridDim.x, turn ^= 1) {
+        if (!STAY) next.load(p, row, pieces);
+        const RowPieces<C, RES32> cur = next;
+        if (STAY && row + (int)gridDim.x < p.rows) next.load(p, row + gridDim.x, pieces);
+        float y[C][8], r[C][8];
+        float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-        const int c = threadIdx.x + i * nt;
-        if (c >= pieces) continue;
-        float w[8];
-        load8f(p.pre_w + 8 * c, w);
+        for (int i = 0; i < C; ++i) {
+            unpack8(cur.x[i], y[i]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] *= r[i][e] * f;
-        *reinterpret_cast<uint4 *>(p.out + base + 8 * (size_t)c) = pack8(w);
+            for (int e = 0; e < 8; ++e) ss = fmaf(y[i][e], y[i][e], ss);
+        }
+        float f = 1.f;
+        if (p.post_w) f = rsqrtf(cta_sum(ss, part[0][turn]) * inv_dim + p.eps);
+        ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            if constexpr (RES32) {
+                const uint4 a = cur.res[i][0], b = cur.res[i][1];
+                const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) r[i][e] = __uint_as_float(w[e]);
+            } else {
+                unpack8(cur.res[i][0], r[i]);
+            }
+            float g[8];
+            unpack8(cur.gate[i], g);
+            if (!STAY) load_post(i, post[i]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float v = y[i][e] * f * post[i][e];
+                if (p.gate) {
+                    const float sig = __fdividef(1.f, 1.f + __expf(-g[e]));
+                    v *= p.silu ? g[e] * sig : sig;
+                }
+                r[i][e] += v;
+                ss = fmaf(r[i][e], r[i][e], ss);
+            }
+            const int c = threadIdx.x + i * nt;
+            if (c < pieces) {
+                const size_t at = (size_t)row * p.dim + 8 * (size_t)c;
+                if (RES32) {
+                    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.residual_out) + at);
+                    o[0] = make_float4(r[i][0], r[i][1], r[i][2], r[i][3]);
+                    o[1] = make_float4(r[i][4], r[i][5], r[i][6], r[i][7]);
+                } else {
+                    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.residual_out) + at) = pack8(r[i]);
+                }
+            }
+        }
+        f = rsqrtf(cta_sum(ss, part[1][turn]) * inv_dim + p.eps);
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int c = threadIdx.x + i * nt;
+            if (c >= pieces) continue;
+            if (!STAY) load_pre(i, pre[i]);
+            float h[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[e] = r[i][e] * f * pre[i][e];
+            *reinterpret_cast<uint4 *>(p.out + (size_t)row * p.dim + 8 * (size_t)c) = pack8(h);
+        }
     }
 }
 
@@ -113,13 +165,18 @@ __global__ void __launch_bounds__(512) block_norm_kernel(const __grid_constant__
 
 cudaError_t launch_block_norm(const BlockNormProblem &p) {
     const int pieces = p.dim / 8;
-    // two pieces a thread (enough loads in flight with 8 or more CTAs an SM), four where that would pass 512 threads
-    const int c = pieces <= 32 ? 1 : pieces <= 1024 ? 2 : 4;
+    // One piece a thread up to 512 of them, so that many rows' loads are in flight with few registers; then two.
+    const int c = pieces <= 512 ? 1 : 2;
     const int threads = ((pieces + c - 1) / c + 31) / 32 * 32;
     using Fn = void (*)(const BlockNormProblem);
-    const Fn fn = p.residual_f32 ? (c == 1 ? block_norm_kernel<1, true> : c == 2 ? block_norm_kernel<2, true> : block_norm_kernel<4, true>)
-                                 : (c == 1 ? block_norm_kernel<1, false> : c == 2 ? block_norm_kernel<2, false> : block_norm_kernel<4, false>);
-    fn<<<(unsigned)p.rows, (unsigned)threads, 0, p.stream>>>(p);
+    const bool f32 = p.residual_f32;
+    const Fn fn = c == 1 ? (f32 ? block_norm_kernel<1, true, true> : block_norm_kernel<1, false, true>)
+                  : threads <= 512 ? (f32 ? block_norm_kernel<2, true, true> : block_norm_kernel<2, false, true>)
+                                   : (f32 ? block_norm_kernel<2, true, false> : block_norm_kernel<2, false, false>);
+    // CTAs that stay: what fits on the SMs at once, the same number of rows each as far as that goes
+    const int fit = multiprocessor_count() * max(1, min(24, (c == 1 ? 1024 : 512) / threads));
+    const int rounds = (p.rows + fit - 1) / fit, ctas = (p.rows + rounds - 1) / rounds;
+    fn<<<(unsigned)ctas, (unsigned)threads, 0, p.stream>>>(p);
     return cudaGetLastError();
 }
 

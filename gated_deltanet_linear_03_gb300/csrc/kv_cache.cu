@@ -88,54 +88,84 @@ __device__ __forceinline__ uint2 quantise8(const uint4 &u, float inv) {
     return make_uint2(values_to_codes<FMT>(x[0], x[1], x[2], x[3]), values_to_codes<FMT>(x[4], x[5], x[6], x[7]));
 }
 
-// Query CTAs: each thread rotates one pair of pieces (or one interleaved piece, or copies one past rot).  Both
-// pieces of a pair are read before either is written, so q_out may be q.
-__device__ __forceinline__ void rotate_queries(const AppendProblem &p, long first, int threads) {
-    const int pieces = p.d / 8;
-    const bool in_place = p.q_out == p.q;
-    const int turned = p.interleaved ? p.rot / 8 : p.rot / 16;      // units that rotate
-    const int units = turned + (in_place ? 0 : pieces - p.rot / 8);
-    if (units == 0) return;
-    const long all = (long)p.total * p.hq * units;
-    for (long i = first; i < all; i += threads) {
-        const int u = (int)(i % units);
-        const long row = i / units;
-        const int t = (int)(row / p.hq), h = (int)(row % p.hq);
-        const __nv_bfloat16 *src = p.q + t * p.q_stride + (long)h * p.d;
-        __nv_bfloat16 *dst = p.q_out + row * p.d;
-        if (u >= turned) {
-            const int c = p.rot / 8 + u - turned;
-            *reinterpret_cast<uint4 *>(dst + 8 * c) = *reinterpret_cast<const uint4 *>(src + 8 * c);
-            continue;
-        }
-        const int n = sequence_of(p.cu, p.n_seqs, t);
-        const int pos = p.past[n] + t - p.cu[n];
-        if (pos < 0 || pos >= p.n_positions) {
-            raise_error(p.err, kErrInternal);
-            continue;
-        }
+// Query warps.  A warp takes one token and up to kHeadPasses passes over its heads (a pass is 256 / D heads, a piece of 8
+// elements a lane): position, cosines and sines are found once, and all of the warp's loads are in flight together.
+// The other piece of a pair comes from its lane, so every piece is read before any is written: q_out may be q.
+constexpr int kHeadPasses = 8;
+
+template <int D>
+__host__ __device__ inline int head_parts(int hq) { return (hq * (D / 8) + 32 * kHeadPasses - 1) / (32 * kHeadPasses); }
+
+template <int D>
+__device__ __forceinline__ void rotate_queries(const AppendProblem &p, int warp, int lane) {
+    constexpr int LPR = D / 8, HEADS = 32 / LPR;
+    const int parts = head_parts<D>(p.hq), t = warp / parts, h0 = (warp % parts) * kHeadPasses * HEADS + lane / LPR;
+    if (t >= p.total) return;
+    const int c = lane % LPR;
+    const bool turned = 8 * c < p.rot, first = 16 * c < p.rot;
+    const bool moves = turned || p.q_out != p.q;     // in place, the pieces past rot stay where they are
+    const __nv_bfloat16 *src = p.q + t * p.q_stride + (long)h0 * D + 8 * c;
+    __nv_bfloat16 *dst = p.q_out + ((long)t * p.hq + h0) * D + 8 * c;
+    uint4 x[kHeadPasses];
+#pragma unroll
+    for (int i = 0; i < kHeadPasses; ++i)
+        x[i] = moves && h0 + i * HEADS < p.hq ? *reinterpret_cast<const uint4 *>(src + i * HEADS * D) : make_uint4(0, 0, 0, 0);
+    const int n = sequence_of(p.cu, p.n_seqs, t);
+    const int pos = p.past[n] + t - p.cu[n];
+    const bool ok = p.rot == 0 || (pos >= 0 && pos < p.n_positions);
+    if (!ok) {
+        if (lane == 0) raise_error(p.err, kErrInternal);
+        return;
+    }
+    float cc[8], ss[8];
+    const int other = first ? lane + p.rot / 16 : lane - p.rot / 16;
+    if (turned) {
         const float *cos = p.cos + (size_t)pos * (p.rot / 2), *sin = p.sin + (size_t)pos * (p.rot / 2);
         if (p.interleaved) {
-            float x[8];
-            unpack8(*reinterpret_cast<const uint4 *>(src + 8 * u), x);
-            rotate_pairs(x, cos + 4 * u, sin + 4 * u);
-            *reinterpret_cast<uint4 *>(dst + 8 * u) = pack8(x);
+            const float4 a = __ldg(reinterpret_cast<const float4 *>(cos + 4 * c)), b = __ldg(reinterpret_cast<const float4 *>(sin + 4 * c));
+            cc[0] = a.x; cc[1] = a.y; cc[2] = a.z; cc[3] = a.w;
+            ss[0] = b.x; ss[1] = b.y; ss[2] = b.z; ss[3] = b.w;
         } else {
-            const int v = u + p.rot / 16;
-            float a[8], b[8], cc[8], ss[8];
-            unpack8(*reinterpret_cast<const uint4 *>(src + 8 * u), a);
-            unpack8(*reinterpret_cast<const uint4 *>(src + 8 * v), b);
-            load8(cos + 8 * u, cc);
-            load8(sin + 8 * u, ss);
+            const int at = 8 * (first ? c : c - p.rot / 16);
+            load8(cos + at, cc);
+            load8(sin + at, ss);
+            if (first) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float x = a[e] * cc[e] - b[e] * ss[e];
-                b[e] = b[e] * cc[e] + a[e] * ss[e];
-                a[e] = x;
+                for (int e = 0; e < 8; ++e) ss[e] = -ss[e];     // a cos - b sin in one half, b cos + a sin in the other
             }
-            *reinterpret_cast<uint4 *>(dst + 8 * u) = pack8(a);
-            *reinterpret_cast<uint4 *>(dst + 8 * v) = pack8(b);
         }
+    }
+#pragma unroll
+    for (int i = 0; i < kHeadPasses; ++i) {
+        if (h0 - lane / LPR + i * HEADS >= p.hq) break;          // the same for the whole warp
+        if (p.rot > 0 && p.interleaved) {
+            if (turned) {
+                float y[8];
+                unpack8(x[i], y);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float a = y[2 * e], b = y[2 * e + 1];
+                    y[2 * e] = a * cc[e] - b * ss[e];
+                    y[2 * e + 1] = b * cc[e] + a * ss[e];
+                }
+                x[i] = pack8(y);
+            }
+        } else if (p.rot > 0) {
+            uint4 z;
+            z.x = __shfl_sync(0xffffffffu, x[i].x, other);
+            z.y = __shfl_sync(0xffffffffu, x[i].y, other);
+            z.z = __shfl_sync(0xffffffffu, x[i].z, other);
+            z.w = __shfl_sync(0xffffffffu, x[i].w, other);
+            if (turned) {
+                float y[8], o[8];
+                unpack8(x[i], y);
+                unpack8(z, o);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = y[e] * cc[e] + o[e] * ss[e];
+                x[i] = pack8(y);
+            }
+        }
+        if (moves && h0 + i * HEADS < p.hq) *reinterpret_cast<uint4 *>(dst + i * HEADS * D) = x[i];
     }
 }
 
@@ -149,7 +179,7 @@ __global__ void __launch_bounds__(D) kv_append_kernel(const __grid_constant__ Ap
     __shared__ uint32_t part[2][D / 32];
     const long kv_ctas = block_slots(p.n_seqs, p.total) * p.pool.hkv;
     if (blockIdx.x >= kv_ctas) {
-        rotate_queries(p, ((long)blockIdx.x - kv_ctas) * D + threadIdx.x, (int)(gridDim.x - kv_ctas) * D);
+        rotate_queries<D>(p, (int)(blockIdx.x - kv_ctas) * (D / 32) + threadIdx.x / 32, threadIdx.x % 32);
         return;
     }
     const int slot = blockIdx.x / p.pool.hkv, h = blockIdx.x % p.pool.hkv;
@@ -301,10 +331,10 @@ cudaError_t launch_kv_append(const AppendProblem &p) {
     const long kv_ctas = block_slots(p.n_seqs, p.total) * p.pool.hkv;
     long q_ctas = 0;
     if (p.q) {
-        const long units = (p.interleaved ? p.rot / 8 : p.rot / 16) + (p.q_out == p.q ? 0 : p.d / 8 - p.rot / 8);
-        q_ctas = ((long)p.total * p.hq * units + 2 * p.d - 1) / (2 * p.d);   // two units a thread
+        const int parts = p.d == 64 ? head_parts<64>(p.hq) : p.d == 128 ? head_parts<128>(p.hq) : head_parts<256>(p.hq);
+        q_ctas = ((long)p.total * parts + p.d / 32 - 1) / (p.d / 32);
     }
-    if (kv_ctas + q_ctas > 2147483647L) return cudaErrorInvalidValue;
+    if (kv_ctas + q_ctas > 2147483647L / 8) return cudaErrorInvalidValue;
     using Fn = void (*)(const AppendProblem);
     const bool e4m3 = p.format == GDN_KV_E4M3;
     const Fn fn = p.d == 64 ? (e4m3 ? kv_append_kernel<64, GDN_KV_E4M3> : kv_append_kernel<64, GDN_KV_INT8>)
