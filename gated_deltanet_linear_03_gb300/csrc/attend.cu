@@ -6,17 +6,18 @@
 // codes, are at most 1 for a running maximum M of x (so they fit fp16 whatever the scales are), and
 // sum_j e^{s_j} = 2^M sum_b (1 / V_b) sum_{j in b} w_j.
 //
-// Work.  A unit is 64 tokens of one item, an item is (sequence, key/value head, 16 query rows: the group's heads
-// of consecutive tokens).  All units of the call form one line; CTA c of G takes units [c per, (c + 1) per), so
+// Work.  A unit is 64 tokens of one item, an item is (sequence, key/value head, 8 NR query rows: the group's heads
+// of consecutive tokens; NR = 1 where no sequence has more than 8 rows, else 2).  All units of the call form one line; CTA c of G takes units [c per, (c + 1) per), so
 // ragged batches balance by themselves and one long sequence spreads over the whole GPU.  Lengths are read on
 // the device, so a captured graph follows them.  A CTA writes finished items to `out`; of an item that crosses
 // CTAs each writes (O, M, l) to the workspace and attend_merge_kernel joins them.
 //
 // A CTA has a producer warp and four compute warps.  The producer looks pages up a unit ahead and brings K and V
 // rows (codes) and block scales through a ring of shared-memory stages with cp.async.  Of a unit, compute warp w
-// forms the 16 x 16 scores of tokens 16 w .. 16 w + 15 (one scale block) with mma.m16n8k16 on codes turned to
-// fp16 exactly; the warps exchange row maxima and weights through shared memory; warp w then accumulates columns
-// [w D/4, (w + 1) D/4) of O over all 64 tokens.  Splitting O by columns keeps it at D/8 registers a thread.
+// forms the scores of tokens 16 w .. 16 w + 15 (one scale block) with mma.m16n8k16 on codes turned to fp16 exactly,
+// as S^T = K Q^T: the 16 tokens are the instruction's rows and 8 query rows its columns, so that a group of 8 heads
+// fills it.  The warps exchange maxima and weights through shared memory; warp w then accumulates columns
+// [w D/4, (w + 1) D/4) of O^T = V^T W^T over all 64 tokens, D/16 registers a thread and 8 rows.
 // Bound by memory: the codes are read once for all heads of a group.
 #include "attend.cuh"
 
@@ -25,28 +26,30 @@ namespace {
 
 using namespace attend;
 
-constexpr int kRows = 16;        // query rows of an item
 constexpr int kTile = 64;        // tokens of a unit
 constexpr int kCompute = 128;    // threads of the compute warps
 constexpr int kThreads = kCompute + 32;
 
-template <int D>
-__host__ __device__ constexpr int stages() { return D == 256 ? 3 : D == 128 ? 4 : 6; }
-template <int D>
-__host__ __device__ constexpr int ctas_per_sm() { return D == 256 ? 2 : D == 128 ? 3 : 4; }
+// Stages and CTAs of an SM: about 190 KB of codes in flight, as many CTAs as the registers allow (their chains of
+// short steps hide one another).
+template <int D, int NR>
+__host__ __device__ constexpr int ctas_per_sm() { return D == 256 ? (NR == 1 ? 3 : 2) : D == 128 ? (NR == 1 ? 4 : 3) : (NR == 1 ? 6 : 4); }
+template <int D, int NR>
+__host__ __device__ constexpr int stages() { return 196608 / (ctas_per_sm<D, NR>() * 2 * kTile * D); }
 
-template <int D>
+template <int D, int NR>
 struct __align__(128) Smem {
-    uint8_t k[stages<D>()][kTile * D];
-    uint8_t v[stages<D>()][kTile * D];
+    static constexpr int S = stages<D, NR>(), kRows = 8 * NR;
+    uint8_t k[S][kTile * D];
+    uint8_t v[S][kTile * D];
     __half p[kRows * kTile];               // weights, 16-byte pieces swizzled by row
-    float scale[stages<D>()][8];           // K scales of the unit's four blocks, then V scales
+    float scale[S][8];                     // K scales of the unit's four blocks, then V scales
     float red[4][kRows];                   // row maxima (then sums) of the four warps
-    uint64_t full[stages<D>()], empty[stages<D>()];
+    uint64_t full[S], empty[S];
     int abort;
-    long long scan[4];
+    int scan[4];
     int start_seq;
-    long long start_off;
+    int start_off;
 };
 
 // Byte offset of 16-byte piece u of row r in a stage.  The piece index is permuted by the row so that the two
@@ -114,12 +117,12 @@ struct Cursor {
     Item it;
 };
 
-template <int D, int FMT>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm<D>()) attend_split_kernel(const __grid_constant__ AttendProblem p,
-                                                                                  const __grid_constant__ SplitPlan plan) {
-    constexpr int S = stages<D>(), KI = D / 64, NT = D / 32;
+template <int D, int FMT, int NR>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NR>()) attend_split_kernel(const __grid_constant__ AttendProblem p,
+                                                                                      const __grid_constant__ SplitPlan plan) {
+    constexpr int S = stages<D, NR>(), KI = D / 64, NT = D / 32, kRows = 8 * NR;
     extern __shared__ __align__(128) uint8_t raw[];
-    Smem<D> &sm = *reinterpret_cast<Smem<D> *>(raw);
+    Smem<D, NR> &sm = *reinterpret_cast<Smem<D, NR> *>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int group = p.hq / p.pool.hkv, cta = blockIdx.x;
     sm100::grid_launch_dependents();
@@ -135,31 +138,31 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D>()) attend_split_kerne
     }
     const int chunk = (p.n_seqs + kCompute - 1) / kCompute;
     const int s_lo = tid < kCompute ? min(tid * chunk, p.n_seqs) : p.n_seqs, s_hi = min(s_lo + chunk, p.n_seqs);
-    long long mine = 0;
+    int mine = 0;                                     // the host has checked that all units fit 31 bits
     for (int n = s_lo; n < s_hi; ++n) mine += sequence_cost<kRows, kTile>(p, load_sequence(p, n), group);
-    long long upto = mine;
+    int upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += y;
     }
     if (lane == 31 && warp < 4) sm.scan[warp] = upto;
     __syncthreads();
-    long long total = 0;
+    int total = 0;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
         if (w < warp) upto += sm.scan[w];
         total += sm.scan[w];
     }
-    const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)plan.min_units);
-    const long long start = cta * per, stop = min(total, start + per);
+    const int per = max((int)(((unsigned)total + gridDim.x - 1) / gridDim.x), plan.min_units);
+    const int start = (int)min((long long)cta * per, (long long)total), stop = min(total - start, per) + start;
     if (tid == 0 && !plan.meta_by_item) plan.meta[cta].last = -1;
     if (tid == 0) report_lengths(p, cta);
     if (start >= stop) return;
     if (start >= upto - mine && start < upto) {
-        long long off = start - (upto - mine);
+        int off = start - (upto - mine);
         for (int n = s_lo; n < s_hi; ++n) {
-            const long long c = sequence_cost<kRows, kTile>(p, load_sequence(p, n), group);
+            const int c = sequence_cost<kRows, kTile>(p, load_sequence(p, n), group);
             if (off < c) {
                 sm.start_seq = n;
                 sm.start_off = off;
@@ -175,16 +178,16 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D>()) attend_split_kerne
     cc.s = load_sequence(p, cc.n);
     {
         const int mts = row_tiles<kRows>(cc.s.qlen, group);
-        long long off = sm.start_off;
-        const long long head_cost = sequence_cost<kRows, kTile>(p, cc.s, group) / p.pool.hkv;
-        cc.h = (int)(off / head_cost);
+        int off = sm.start_off;
+        const int head_cost = sequence_cost<kRows, kTile>(p, cc.s, group) / p.pool.hkv;
+        cc.h = off / head_cost;
         off -= cc.h * head_cost;
         for (cc.mt = 0; cc.mt < mts; ++cc.mt) {
             cc.it = make_item<kRows, kTile>(p, cc.s, group, cc.mt);
             if (off < cc.it.tiles) break;
             off -= cc.it.tiles;
         }
-        cc.j = (int)off;
+        cc.j = off;
     }
     auto advance = [&](Cursor &c) {
         if (++c.j < c.it.tiles) return;
@@ -215,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D>()) attend_split_kerne
             }
         }
     };
-    const int units = (int)(stop - start);
+    const int units = stop - start;
 
     if (warp == 4) {
         // ---- the producer: lane b (mod 4) holds the pool row where block b of a unit begins, -1 for none
@@ -267,10 +270,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D>()) attend_split_kerne
         return;
     }
 
-    uint32_t qf[KI][4][4];      // queries in fp16: rows g and g + 8, component order as the codes are read
-    float acc[NT][4];           // O: rows g, g + 8 of this warp's columns
-    float m[2], l[2], rs[2];    // running maximum, this thread's part of the sum, row scale (log2 units per product)
-    int pos[2];
+    uint32_t qf[NR][KI][4][2];  // queries in fp16: row 8 r + g, component order as the codes are read
+    float acc[NR][NT / 2][4];   // O^T: this warp's columns NT g .. NT g + NT - 1 of rows 8 r + 2 t and + 1
+    float m[NR][2], l[NR][2];   // those rows' running maximum, and this thread's part of their sum
+    float rs[NR][2];            // and their scale, log2 units per product
+    int pos[NR][2];
     bool begun = false;         // the segment starts its item
     int seg_unit = 0;           // first unit of the segment
 
@@ -279,14 +283,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D>()) attend_split_kerne
         if (unit == 0 || cc.j == 0) {   // a new item: queries to registers
             begun = cc.j == 0;
             seg_unit = unit;
-            const int first_row = cc.mt * kRows;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int row = first_row + g + 8 * r, i = row / group;
+            for (int r = 0; r < NR; ++r) {
+                const int row = cc.mt * kRows + 8 * r + g, i = row / group;
                 const bool ok = i < cc.s.qlen;
-                pos[r] = cc.s.kvlen - cc.s.qlen + i;
-                m[r] = -INFINITY;
-                l[r] = 0.f;
                 const __nv_bfloat16 *src = p.q + ((size_t)(cc.s.q0 + (ok ? i : 0)) * p.hq + cc.h * group + row % group) * D + 16 * t;
                 uint4 w[KI][2];
                 uint32_t big = 0;
@@ -301,111 +301,131 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D>()) attend_split_kerne
                 big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
                 float down, up;
                 power_of_two_scale(big, down, up);
-                rs[r] = p.sm_scale * 1.4426950408889634f * up;
 #pragma unroll
                 for (int k = 0; k < KI; ++k)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const uint32_t x[4] = {w[k][e].x, w[k][e].y, w[k][e].z, w[k][e].w};
 #pragma unroll
-                        for (int f = 0; f < 4; ++f)
-                            qf[k][2 * e + f / 2][(f & 1) * 2 + r] = bf16x2_to_f16x2(x[f], down);
+                        for (int f = 0; f < 4; ++f) qf[r][k][2 * e + f / 2][f & 1] = bf16x2_to_f16x2(x[f], down);
                     }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    // row 8 r + 2 t + c is loaded by the lanes of g = 2 t + c
+                    rs[r][c] = p.sm_scale * 1.4426950408889634f * __shfl_sync(0xffffffffu, up, 4 * (2 * t + c));
+                    pos[r][c] = cc.s.kvlen - cc.s.qlen + (cc.mt * kRows + 8 * r + 2 * t + c) / group;
+                    m[r][c] = -INFINITY;
+                    l[r][c] = 0.f;
+                }
+#pragma unroll
+                for (int i2 = 0; i2 < NT / 2; ++i2)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[r][i2][e] = 0.f;
             }
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
         }
 
         wait(&sm.full[stage], phase);
         __syncwarp();
 
-        // ---- scores of this warp's 16 tokens
+        // ---- scores of this warp's 16 tokens: rows g and g + 8 of the block against every query row
         const int tok0 = cc.it.token(cc.j, kTile) + warp * kKvBlock;
-        float sc[2][2][4] = {};
+        float sc[NR][2][4] = {};
         const uint32_t kbase = sm100::smem_u32(sm.k[stage]);
 #pragma unroll
-        for (int k = 0; k < KI; ++k)
+        for (int k = 0; k < KI; ++k) {
+            uint32_t w0[4], w1[4];
+            lds128(kbase + piece<D>(warp * kKvBlock + g, 4 * k + t), w0);
+            lds128(kbase + piece<D>(warp * kKvBlock + 8 + g, 4 * k + t), w1);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                uint32_t w[4];
-                lds128(kbase + piece<D>(warp * kKvBlock + 8 * j + g, 4 * k + t), w);
+            for (int e = 0; e < 4; ++e) {
+                uint32_t a[4];
+                codes_to_f16x2<FMT>(w0[e], a[0], a[2]);
+                codes_to_f16x2<FMT>(w1[e], a[1], a[3]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    uint32_t b0, b1;
-                    codes_to_f16x2<FMT>(w[e], b0, b1);
-                    mma_f16(sc[j][e & 1], qf[k][e], b0, b1);
-                }
+                for (int r = 0; r < NR; ++r) mma_f16(sc[r][e & 1], a, qf[r][k][e][0], qf[r][k][e][1]);
             }
+        }
         const float kscale = sm.scale[stage][warp];
         float vscale = sm.scale[stage][4 + warp];
         if (vscale == 0.f) vscale = kAmaxFloor;
         const float lv = log2f(vscale), rv = 1.f / vscale;
         const bool all_seen = cc.it.all_seen(tok0, tok0 + kKvBlock, p.window, p.sinks);
-        float x[2][2][2];   // [row][n-tile][column]
+        float x[NR][2][2];   // [8 rows][token g, g + 8][row 2 t, 2 t + 1]
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const float f = rs[r] * kscale;
-            float big = -INFINITY;
+        for (int r = 0; r < NR; ++r)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int c = 0; c < 2; ++c) {
+                const float f = rs[r][c] * kscale;
+                float big = -INFINITY;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float y = fmaf(sc[j][0][2 * r + e] + sc[j][1][2 * r + e], f, lv);
-                    if (!all_seen && !sees(pos[r], tok0 + 8 * j + 2 * t + e, p.window, p.sinks)) y = -INFINITY;
-                    x[r][j][e] = y;
+                for (int j = 0; j < 2; ++j) {
+                    float y = fmaf(sc[r][0][2 * j + c] + sc[r][1][2 * j + c], f, lv);
+                    if (!all_seen && !sees(pos[r][c], tok0 + 8 * j + g, p.window, p.sinks)) y = -INFINITY;
+                    x[r][j][c] = y;
                     big = fmaxf(big, y);
                 }
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-            if (t == 0) sm.red[warp][g + 8 * r] = big;
-        }
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 4));
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 8));
+                big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 16));
+                if (g == 0) sm.red[warp][8 * r + 2 * t + c] = big;
+            }
         sync_compute();
         // ---- weights
-        float corr[2];
+        const uint32_t pbase = sm100::smem_u32(sm.p);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = g + 8 * r;
-            const float big = fmaxf(fmaxf(fmaxf(sm.red[0][row], sm.red[1][row]), fmaxf(sm.red[2][row], sm.red[3][row])), m[r]);
-            const float safe = big == -INFINITY ? 0.f : big;
-            corr[r] = exp2f(m[r] - safe);
-            m[r] = big;
-            float sum = 0.f;
+        for (int r = 0; r < NR; ++r) {
+            float e[2][2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float a = exp2f(x[r][j][0] - safe), b = exp2f(x[r][j][1] - safe);
-                sum += a + b;
-                // fp16 weights: at most 1, 2^-11 relative error each, far below the bf16 rounding of the output
-                const __half2 h = __floats2half2_rn(a, b);
-                const int u = (2 * warp + j) ^ (row & 7);
-                *reinterpret_cast<__half2 *>(reinterpret_cast<uint8_t *>(sm.p) + row * 128 + u * 16 + 4 * t) = h;
+            for (int c = 0; c < 2; ++c) {
+                const int row = 8 * r + 2 * t + c;
+                const float big = fmaxf(fmaxf(fmaxf(sm.red[0][row], sm.red[1][row]), fmaxf(sm.red[2][row], sm.red[3][row])), m[r][c]);
+                const float safe = big == -INFINITY ? 0.f : big;
+                const float corr = exp2f(m[r][c] - safe);
+                m[r][c] = big;
+                e[0][c] = exp2_fast(x[r][0][c] - safe);
+                e[1][c] = exp2_fast(x[r][1][c] - safe);
+                const float sum = e[0][c] + e[1][c];
+                l[r][c] = l[r][c] * corr + (sum == 0.f ? 0.f : sum * rv);   // a block that the row does not see may have any scale
+#pragma unroll
+                for (int i = 0; i < NT / 2; ++i) {
+                    acc[r][i][c] *= corr;
+                    acc[r][i][2 + c] *= corr;
+                }
             }
-            l[r] = l[r] * corr[r] + (sum == 0.f ? 0.f : sum * rv);   // a block that the row does not see may have any scale
-        }
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            acc[i][0] *= corr[0]; acc[i][1] *= corr[0];
-            acc[i][2] *= corr[1]; acc[i][3] *= corr[1];
+            // fp16 weights: at most 1, 2^-11 relative error each, far below the bf16 rounding of the output.  They are
+            // stored transposed, as 64 tokens of each row.
+            const __half2 h0 = __floats2half2_rn(e[0][0], e[0][1]), h1 = __floats2half2_rn(e[1][0], e[1][1]);
+            const int row = 8 * r + (lane & 7), u = (2 * warp + ((lane >> 3) & 1)) ^ (lane & 7);
+            asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1, %2};" ::"r"(pbase + row * 128 + u * 16),
+                         "r"(*reinterpret_cast<const uint32_t *>(&h0)), "r"(*reinterpret_cast<const uint32_t *>(&h1))
+                         : "memory");
         }
         sync_compute();
         // ---- outputs: this warp's columns over all 64 tokens
-        const uint32_t vbase = sm100::smem_u32(sm.v[stage]), pbase = sm100::smem_u32(sm.p);
+        const uint32_t vbase = sm100::smem_u32(sm.v[stage]);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            uint32_t a[4];
-            {
-                const int row = lane & 15, u = (2 * b + (lane >> 4)) ^ (row & 7);
+        for (int half = 0; half < 2; ++half) {
+            uint32_t wt[NR][4];     // weights of 32 tokens: the two registers of two k-steps
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                const int row = 8 * r + (lane & 7), u = (4 * half + (lane >> 3)) ^ (lane & 7);
                 asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3])
+                             : "=r"(wt[r][0]), "=r"(wt[r][1]), "=r"(wt[r][2]), "=r"(wt[r][3])
                              : "r"(pbase + row * 128 + u * 16)
                              : "memory");
             }
-            uint32_t b0[NT], b1[NT];
-            value_columns<D, FMT>(vbase, b * 16 + 2 * t, warp, g, b0);
-            value_columns<D, FMT>(vbase, b * 16 + 2 * t + 8, warp, g, b1);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) mma_f16(acc[i], a, b0[i], b1[i]);
+            for (int b = 0; b < 2; ++b) {
+                uint32_t v0[NT], v1[NT];
+                value_columns<D, FMT>(vbase, (2 * half + b) * 16 + 2 * t, warp, g, v0);
+                value_columns<D, FMT>(vbase, (2 * half + b) * 16 + 2 * t + 8, warp, g, v1);
+#pragma unroll
+                for (int i = 0; i < NT / 2; ++i) {
+                    const uint32_t a[4] = {v0[2 * i], v0[2 * i + 1], v1[2 * i], v1[2 * i + 1]};
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) mma_f16(acc[r][i], a, wt[r][2 * b], wt[r][2 * b + 1]);
+                }
+            }
         }
         __syncwarp();
         if (lane == 0) sm100::mbar_arrive(&sm.empty[stage]);
@@ -415,47 +435,52 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D>()) attend_split_kerne
         const bool ends = cc.j == cc.it.tiles - 1;
         if (ends || unit == units - 1) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-                if (t == 0) sm.red[warp][g + 8 * r] = l[r];   // every warp has read the maxima
-            }
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    l[r][c] += __shfl_xor_sync(0xffffffffu, l[r][c], 4);
+                    l[r][c] += __shfl_xor_sync(0xffffffffu, l[r][c], 8);
+                    l[r][c] += __shfl_xor_sync(0xffffffffu, l[r][c], 16);
+                    if (g == 0) sm.red[warp][8 * r + 2 * t + c] = l[r][c];   // every warp has read the maxima
+                }
             sync_compute();
             const bool whole = begun && ends;
             const int slot = 2 * cta + (seg_unit == 0 ? 0 : 1);
             float *part = plan.parts + (size_t)slot * (kRows * D + 2 * kRows);
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int row = g + 8 * r, grow = cc.mt * kRows + row, i = grow / group;
-                const float sum = (sm.red[0][row] + sm.red[1][row]) + (sm.red[2][row] + sm.red[3][row]);
-                if (i >= cc.s.qlen) continue;
-                const int col = warp * (D / 4) + 2 * NT * t;
-                float y[2 * NT];
-                const float f = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+            for (int r = 0; r < NR; ++r)
 #pragma unroll
-                for (int k = 0; k < NT; ++k) {
-                    y[k] = acc[k][2 * r] * f;
-                    y[NT + k] = acc[k][2 * r + 1] * f;
-                }
-                if (whole) {
-                    store_row<2 * NT>(p, ((size_t)(cc.s.q0 + i) * p.hq + cc.h * group + grow % group) * D + col, y);
-                } else {
-                    float *o = part + row * D + col;
+                for (int c = 0; c < 2; ++c) {
+                    const int row = 8 * r + 2 * t + c, grow = cc.mt * kRows + row, i = grow / group;
+                    const float sum = (sm.red[0][row] + sm.red[1][row]) + (sm.red[2][row] + sm.red[3][row]);
+                    if (i >= cc.s.qlen) continue;
+                    const int col = warp * (D / 4) + NT * g;
+                    float y[NT];
+                    const float f = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
 #pragma unroll
-                    for (int k = 0; k < 2 * NT; k += 4) *reinterpret_cast<float4 *>(o + k) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
-                    if (warp == 0 && t == 0) {
-                        part[kRows * D + row] = m[r];
-                        part[kRows * D + kRows + row] = sum;
+                    for (int k = 0; k < NT / 2; ++k) {
+                        y[2 * k] = acc[r][k][c] * f;
+                        y[2 * k + 1] = acc[r][k][2 + c] * f;
+                    }
+                    if (whole) {
+                        store_row<NT>(p, ((size_t)(cc.s.q0 + i) * p.hq + cc.h * group + grow % group) * D + col, y);
+                    } else {
+                        float *o = part + row * D + col;
+#pragma unroll
+                        for (int k = 0; k < NT; k += 2) *reinterpret_cast<float2 *>(o + k) = make_float2(y[k], y[k + 1]);
+                        if (warp == 0 && g == 0) {
+                            part[kRows * D + row] = m[r][c];
+                            part[kRows * D + kRows + row] = sum;
+                        }
                     }
                 }
-            }
             if (begun && tid == 0 && (plan.meta_by_item || !ends)) {
                 // units left of the item after this CTA decide how many CTAs carry it
-                const long long left = (long long)cc.it.tiles - 1 - cc.j;
+                const int left = cc.it.tiles - 1 - cc.j;
                 MergeMeta mm;
                 mm.first = cta;
                 mm.slot = seg_unit == 0 ? 0 : 1;
-                mm.last = ends ? -1 : cta + (int)((left + per - 1) / per);
+                mm.last = ends ? -1 : cta + (left - 1) / per + 1;
                 mm.n = cc.n;
                 mm.h = cc.h;
                 mm.mt = cc.mt;
@@ -547,22 +572,26 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const __gri
     store_row<4>(p, ((size_t)(s.q0 + i) * p.hq + mm.h * group + grow % group) * D + col, y);
 }
 
+// Query rows of an item: the group's heads of one token where they are at most 8 and alone, else 16.
+int item_rows(int group, int max_q_len) { return (long long)group * max_q_len <= 8 ? 8 : 16; }
+
 long long unit_bound(int n_seqs, int hq, int hkv, int max_q_len, int max_kv_len) {
-    const long long mts = row_tiles<kRows>(max_q_len, hq / hkv);
+    const int group = hq / hkv, rows = item_rows(group, max_q_len);
+    const long long mts = ((long long)max_q_len * group + rows - 1) / rows;
     const long long tiles = max_kv_len > 0 ? (max_kv_len + kTile - 1) / kTile : 1;
     return n_seqs * (long long)hkv * mts * tiles;
 }
 
-template <int D, int FMT>
+template <int D, int FMT, int NR>
 cudaError_t launch_split(const AttendProblem &p) {
     const int group = p.hq / p.pool.hkv;
     const long long bound = unit_bound(p.n_seqs, p.hq, p.pool.hkv, p.max_q_len, p.max_kv_len);
-    const long long fit = (long long)multiprocessor_count() * ctas_per_sm<D>();
-    const int ctas = (int)min(bound, min(fit, (long long)kMaxSplitCtas));
+    const long long fit = (long long)multiprocessor_count() * ctas_per_sm<D, NR>();
     SplitPlan plan{};
-    plan.mt_max = row_tiles<kRows>(p.max_q_len, group);
+    plan.mt_max = row_tiles<8 * NR>(p.max_q_len, group);
     plan.min_units = 1;
     const long long items = (long long)p.n_seqs * p.pool.hkv * plan.mt_max;
+    const int ctas = (int)min((bound + plan.min_units - 1) / plan.min_units, min(fit, (long long)kMaxSplitCtas));
     plan.meta_by_item = items <= ctas;
     plan.meta = static_cast<MergeMeta *>(p.workspace);
     plan.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(p.workspace) + kMetaBytes);
@@ -572,15 +601,20 @@ cudaError_t launch_split(const AttendProblem &p) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= kMaxDevices || !ready[dev].load(std::memory_order_relaxed)) {
-        e = cudaFuncSetAttribute(attend_split_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem<D>));
+        e = cudaFuncSetAttribute(attend_split_kernel<D, FMT, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem<D, NR>));
         if (e != cudaSuccess) return e;
         if (dev < kMaxDevices) ready[dev].store(true, std::memory_order_relaxed);
     }
-    attend_split_kernel<D, FMT><<<ctas, kThreads, sizeof(Smem<D>), p.stream>>>(p, plan);
+    attend_split_kernel<D, FMT, NR><<<ctas, kThreads, sizeof(Smem<D, NR>), p.stream>>>(p, plan);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (ctas == 1 || bound == items) return cudaSuccess;   // no item crosses CTAs
-    return launch_after(p.stream, dim3((unsigned)(plan.meta_by_item ? items : ctas), (unsigned)min(kRows, p.max_q_len * group), D / 64), kMergeThreads, 0,
-                        attend_merge_kernel<D, kRows>, p, plan);
+    return launch_after(p.stream, dim3((unsigned)(plan.meta_by_item ? items : ctas), (unsigned)min(8 * NR, p.max_q_len * group), D / 64),
+                        kMergeThreads, 0, attend_merge_kernel<D, 8 * NR>, p, plan);
+}
+
+template <int D, int FMT>
+cudaError_t launch_split(const AttendProblem &p) {
+    return item_rows(p.hq / p.pool.hkv, p.max_q_len) == 8 ? launch_split<D, FMT, 1>(p) : launch_split<D, FMT, 2>(p);
 }
 
 // The tensor-core kernel (attend_tc.cu) for more query rows than four of this kernel's items.
@@ -591,8 +625,13 @@ bool use_tensor_kernel(int group, int max_q_len) { return (long long)group * max
 size_t attend_workspace_bytes(int n_seqs, int total, int hq, int hkv, int d, int max_q_len, int max_kv_len) {
     if (n_seqs == 0 || total == 0) return 0;
     if (use_tensor_kernel(hq / hkv, max_q_len)) return attend_tc_workspace_bytes(n_seqs, total, hq, hkv, d);
+    const int rows = item_rows(hq / hkv, max_q_len);
     const long long slots = 2 * min(unit_bound(n_seqs, hq, hkv, max_q_len, max_kv_len), (long long)kMaxSplitCtas);
-    return kMetaBytes + (size_t)slots * (kRows * d + 2 * kRows) * sizeof(float);
+    return kMetaBytes + (size_t)slots * (rows * d + 2 * rows) * sizeof(float);
+}
+
+bool attend_supported(int n_seqs, int hq, int hkv, int max_q_len, int max_kv_len) {
+    return use_tensor_kernel(hq / hkv, max_q_len) || unit_bound(n_seqs, hq, hkv, max_q_len, max_kv_len) < 2147483647LL;
 }
 
 cudaError_t launch_attend(const AttendProblem &p) {

@@ -86,8 +86,8 @@ __device__ __forceinline__ Item make_item(const AttendProblem &p, const Sequence
 
 // Units of all heads of a sequence.
 template <int ROWS, int TILE>
-__device__ __forceinline__ long long sequence_cost(const AttendProblem &p, const Sequence &s, int group) {
-    long long c = 0;
+__device__ __forceinline__ int sequence_cost(const AttendProblem &p, const Sequence &s, int group) {
+    int c = 0;
     const int mts = row_tiles<ROWS>(s.qlen, group);
     for (int mt = 0; mt < mts; ++mt) c += make_item<ROWS, TILE>(p, s, group, mt).tiles;
     return c * p.pool.hkv;
@@ -147,11 +147,15 @@ __device__ __forceinline__ void store_row(const AttendProblem &p, size_t at, con
     if (p.out_f32) {
         float *o = static_cast<float *>(p.out) + at;
 #pragma unroll
-        for (int i = 0; i < N; i += 4) *reinterpret_cast<float4 *>(o + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+        for (int i = 0; i < N; i += 4) {
+            if constexpr (N == 2) *reinterpret_cast<float2 *>(o) = make_float2(y[0], y[1]);
+            else *reinterpret_cast<float4 *>(o + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+        }
         return;
     }
     __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + at;
     uint32_t w[N / 2];
+    static_assert(N == 2 || N % 4 == 0, "pieces of 4, 8 or 16 bytes");
 #pragma unroll
     for (int i = 0; i < N / 2; ++i) {
         const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
@@ -160,8 +164,10 @@ __device__ __forceinline__ void store_row(const AttendProblem &p, size_t at, con
     if constexpr (N >= 8) {
 #pragma unroll
         for (int i = 0; i < N / 8; ++i) reinterpret_cast<uint4 *>(o)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    } else {
+    } else if constexpr (N == 4) {
         *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
+    } else {
+        *reinterpret_cast<uint32_t *>(o) = w[0];
     }
 }
 

@@ -170,9 +170,11 @@ gdn_status gdn_kv_read(int n_seqs, int total_tokens, int hkv, int d, const int32
 static gdn_status check_attend_shape(int n_seqs, int total_tokens, int hq, int hkv, int d, int max_q_len, int max_kv_len) {
     if (n_seqs < 0 || total_tokens < 0 || hq <= 0 || hkv <= 0 || d <= 0 || max_q_len < 0 || max_kv_len < 0) return GDN_ERR_INVALID_ARG;
     if (n_seqs == 0 && total_tokens > 0) return GDN_ERR_INVALID_ARG;
+    if (total_tokens < max_q_len) max_q_len = total_tokens;
     if (hq % hkv != 0 || (total_tokens > 0 && max_q_len == 0)) return GDN_ERR_INVALID_ARG;
     if (d != 64 && d != 128 && d != 256) return GDN_ERR_UNSUPPORTED;
     if ((double)total_tokens * hq >= 2147483648.0 - 4096) return GDN_ERR_UNSUPPORTED;   // the kernels count query rows in 32 bits
+    if (!gdn::attend_supported(n_seqs, hq, hkv, max_q_len, max_kv_len)) return GDN_ERR_UNSUPPORTED;         // and units of work
     return GDN_OK;
 }
 
@@ -182,6 +184,7 @@ size_t gdn_attend_workspace_size(int n_seqs, int total_tokens, int hq, int hkv, 
                                  gdn_status *status) {
     const gdn_status st = check_attend_shape(n_seqs, total_tokens, hq, hkv, d, max_q_len, max_kv_len);
     if (status) *status = st;
+    if (max_q_len > total_tokens) max_q_len = total_tokens;
     return st == GDN_OK ? gdn::attend_workspace_bytes(n_seqs, total_tokens, hq, hkv, d, max_q_len, max_kv_len) : 0;
 }
 
