@@ -12,13 +12,15 @@
 // the device, so a captured graph follows them.  A CTA writes finished items to `out`; of an item that crosses
 // CTAs each writes (O, M, l) to the workspace and attend_merge_kernel joins them.
 //
-// A CTA has a producer warp and four compute warps.  The producer looks pages up a unit ahead and brings K and V
-// rows (codes) and block scales through a ring of shared-memory stages with cp.async.  Of a unit, compute warp w
+// A CTA has a producer warp and four compute warps.  The producer looks pages up and reads block scales a unit ahead
+// and brings the blocks' codes through a ring of shared-memory stages by TMA, a box of 16 rows for each block.  Of a unit, compute warp w
 // forms the scores of tokens 16 w .. 16 w + 15 (one scale block) with mma.m16n8k16 on codes turned to fp16 exactly,
 // as S^T = K Q^T: the 16 tokens are the instruction's rows and 8 query rows its columns, so that a group of 8 heads
 // fills it.  The warps exchange maxima and weights through shared memory; warp w then accumulates columns
 // [w D/4, (w + 1) D/4) of O^T = V^T W^T over all 64 tokens, D/16 registers a thread and 8 rows.
 // Bound by memory: the codes are read once for all heads of a group.
+#include <cudaTypedefs.h>
+
 #include "attend.cuh"
 
 namespace gdn {
@@ -38,7 +40,7 @@ template <int D, int NR>
 __host__ __device__ constexpr int stages() { return 196608 / (ctas_per_sm<D, NR>() * 2 * kTile * D); }
 
 template <int D, int NR>
-struct __align__(128) Smem {
+struct __align__(1024) Smem {
     static constexpr int S = stages<D, NR>(), kRows = 8 * NR;
     uint8_t k[S][kTile * D];
     uint8_t v[S][kTile * D];
@@ -52,27 +54,19 @@ struct __align__(128) Smem {
     int start_off;
 };
 
-// Byte offset of 16-byte piece u of row r in a stage.  The piece index is permuted by the row so that the two
-// access patterns (scores: 8 lanes read 4 pieces of 2 neighbouring rows; outputs: 16 lanes read 2 pieces of 4
-// even, or 4 odd, rows) touch each bank once.
+// Byte offset of 16-byte piece u of row r in a stage, as TMA's swizzle places it: boxes of 16 rows and 128 bytes, one
+// after another for each block, pieces exchanged by the row's low bits (at d = 64 boxes of 64-byte rows, by row pairs).
 template <int D>
 __device__ __forceinline__ uint32_t piece(int r, int u) {
-    if (D == 64) return (uint32_t)((r >> 1) * 128 + ((((r & 1) << 2) | (u ^ ((r >> 1) & 3))) << 4));
-    const int f = (((r >> 1) & 3) << 1) ^ ((r & 1) << 2);
-    return (uint32_t)(r * D + ((u ^ f) << 4));
+    if (D == 64) return (uint32_t)(r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
+    return (uint32_t)(((r >> 4) * (D / 128) + (u >> 3)) * 2048 + (r & 15) * 128 + (((u & 7) ^ (r & 7)) << 4));
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-// Arrive on `bar` once this thread's copies so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sm100::smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// The row of an 8-row group that takes place k in the matrix instructions.  Rows of neighbouring places differ in bit
+// 2 and the even (odd) places hold one row of each pair, so that with the swizzle above the lanes that read together
+// (scores: 4 pieces of places 2 a, 2 a + 1; outputs: 2 pieces of the four even, or odd, places) touch each bank once.
+__device__ __forceinline__ int row_at(int k) { return (0x37156240 >> (4 * k)) & 7; }
+
 // The compute warps' barrier.  None of them leaves the unit loop early (a wait that runs out only sets a flag).
 __device__ __forceinline__ void sync_compute() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kCompute) : "memory"); }
 
@@ -82,12 +76,12 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Fragments of V for one 8-token half of a k-step: rows r and r + 1 of the stage, the columns 8 (or 4, 2)
-// * g .. of warp w's quarter.  b[i] = (code at row r, code at row r + 1) of column i as an fp16 pair.
+// Fragments of V for one 8-token half of a k-step: rows r and s of the stage, the columns 8 (or 4, 2) * g .. of warp
+// w's quarter.  b[i] = (code at row r, code at row s) of column i as an fp16 pair.
 template <int D, int FMT>
-__device__ __forceinline__ void value_columns(uint32_t base, int r, int w, int g, uint32_t (&b)[D / 32]) {
+__device__ __forceinline__ void value_columns(uint32_t base, int r, int s, int w, int g, uint32_t (&b)[D / 32]) {
     const int col = w * (D / 4) + g * (D / 32);   // first column byte
-    const uint32_t a0 = base + piece<D>(r, col >> 4) + (col & 15), a1 = base + piece<D>(r + 1, col >> 4) + (col & 15);
+    const uint32_t a0 = base + piece<D>(r, col >> 4) + (col & 15), a1 = base + piece<D>(s, col >> 4) + (col & 15);
     if constexpr (D == 64) {
         uint16_t x, y;
         asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(a0) : "memory");
@@ -119,10 +113,12 @@ struct Cursor {
 
 template <int D, int FMT, int NR>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NR>()) attend_split_kernel(const __grid_constant__ AttendProblem p,
-                                                                                      const __grid_constant__ SplitPlan plan) {
+                                                                                      const __grid_constant__ SplitPlan plan,
+                                                                                      const __grid_constant__ CUtensorMap k_map,
+                                                                                      const __grid_constant__ CUtensorMap v_map) {
     constexpr int S = stages<D, NR>(), KI = D / 64, NT = D / 32, kRows = 8 * NR;
-    extern __shared__ __align__(128) uint8_t raw[];
-    Smem<D, NR> &sm = *reinterpret_cast<Smem<D, NR> *>(raw);
+    extern __shared__ uint8_t raw[];
+    Smem<D, NR> &sm = *reinterpret_cast<Smem<D, NR> *>(raw + ((1024u - (sm100::smem_u32(raw) & 1023u)) & 1023u));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int group = p.hq / p.pool.hkv, cta = blockIdx.x;
     sm100::grid_launch_dependents();
@@ -130,11 +126,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NR>()) attend_split_k
     // ---- this CTA's units: a scan over the sequences' costs
     if (tid == kCompute) {
         for (int i = 0; i < S; ++i) {
-            sm100::mbar_init(&sm.full[i], 32);
+            sm100::mbar_init(&sm.full[i], 1);
             sm100::mbar_init(&sm.empty[i], 4);
         }
         sm.abort = 0;
         sm100::fence_mbar_init();
+        sm100::tma_prefetch_desc(&k_map);
+        sm100::tma_prefetch_desc(&v_map);
     }
     const int chunk = (p.n_seqs + kCompute - 1) / kCompute;
     const int s_lo = tid < kCompute ? min(tid * chunk, p.n_seqs) : p.n_seqs, s_hi = min(s_lo + chunk, p.n_seqs);
@@ -221,52 +219,47 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NR>()) attend_split_k
     const int units = stop - start;
 
     if (warp == 4) {
-        // ---- the producer: lane b (mod 4) holds the pool row where block b of a unit begins, -1 for none
+        // ---- the producer: of lanes 0..7, lane b holds K's block b of a unit and lane 4 + b V's: the pool row where it
+        // begins, -1 where there is none
         auto look_up = [&]() -> int {
             const int tok = cc.it.token(cc.j, kTile) + (lane & 3) * kKvBlock;
-            if (tok >= cc.s.kvlen) return -1;
+            if (lane >= 8 || tok >= cc.s.kvlen) return -1;
             const int at = p.pool.page_of(tok), page = __ldg(p.pool.table + (size_t)cc.n * p.pool.max_pages + at);
             if ((unsigned)page < (unsigned)p.pool.n_pages) return (page * p.pool.hkv + cc.h) * p.pool.page_size + tok - at * p.pool.page_size;
             raise_error(p.err, kErrInternal);
             return -1;
         };
-        constexpr int UPR = D / 16, RPI = 32 / UPR;      // pieces a row, rows a warp-wide copy
-        const int u = lane % UPR, r0 = lane / UPR;
-        int row = look_up(), kept = cc.s.kvlen - cc.it.token(cc.j, kTile);   // tokens of the unit that exist
-        int stage = 0, phase = 1;
+        auto scale_of = [&](int row) -> float { return row >= 0 ? __ldg((lane < 4 ? p.k_scales : p.v_scales) + row / kKvBlock) : 0.f; };
+        const CUtensorMap *map = lane < 4 ? &k_map : &v_map;
+        int row = look_up(), stage = 0, phase = 1, issued = 0;
         for (int unit = 0; unit < units; ++unit) {
-            int next_row = -1, next_kept = 0;
+            const float scale = scale_of(row);
+            int next = -1;
             if (unit + 1 < units) {
                 advance(cc);
-                next_row = look_up();
-                next_kept = cc.s.kvlen - cc.it.token(cc.j, kTile);
+                next = look_up();
             }
             wait(&sm.empty[stage], phase);
+            __syncwarp();
             if (*abort) break;
             if (lane < 8) {
-                const float *sc = lane < 4 ? p.k_scales : p.v_scales;
-                cp_async4(sm100::smem_u32(&sm.scale[stage][lane]), row >= 0 ? sc + row / kKvBlock : sc, row >= 0 ? 4 : 0);
-            }
-            const uint32_t ks = sm100::smem_u32(sm.k[stage]), vs = sm100::smem_u32(sm.v[stage]);
+                // a block that does not exist is loaded from the pool's first rows: no score of it is seen, and its
+                // V rows are cleared before they are used
+                uint8_t *dst = (lane < 4 ? sm.k[stage] : sm.v[stage]) + (lane & 3) * (kKvBlock * D);
 #pragma unroll
-            for (int b = 0; b < kTile / kKvBlock; ++b) {
-                const int base = __shfl_sync(0xffffffffu, row, b);
-                const size_t off = base >= 0 ? (size_t)base * D + r0 * D + u * 16 : 0;
-#pragma unroll
-                for (int i = 0; i < kKvBlock / RPI; ++i) {
-                    const int r = b * kKvBlock + i * RPI + r0;
-                    const int bytes = base >= 0 && r < kept ? 16 : 0;        // rows that do not exist become zeros
-                    const size_t at = bytes ? off + i * RPI * D : 0;
-                    cp_async16(ks + piece<D>(r, u), p.k_pages + at, bytes);
-                    cp_async16(vs + piece<D>(r, u), p.v_pages + at, bytes);
-                }
+                for (int x = 0; x < D; x += 128) sm100::tma_load_2d(dst + x * kKvBlock, map, &sm.full[stage], x, max(row, 0));
+                sm.scale[stage][lane] = scale;
             }
-            cp_async_arrive(&sm.full[stage]);
+            __syncwarp();
+            if (lane == 0) sm100::mbar_arrive_expect_tx(&sm.full[stage], 2 * kTile * D);
             if (++stage == S) stage = 0, phase ^= 1;
-            row = next_row;
-            kept = next_kept;
+            row = next;
+            ++issued;
         }
-        cp_async_wait_all();
+        // every copy is waited for by the compute warps; where they have given up, here
+        if (*abort)
+            for (int k = max(0, issued - S); k < issued; ++k)
+                if (!sm100::mbar_wait(&sm.full[k % S], (uint32_t)(k / S) & 1)) raise_error(p.err, kErrTimeout);
         return;
     }
 
@@ -327,15 +320,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NR>()) attend_split_k
         wait(&sm.full[stage], phase);
         __syncwarp();
 
-        // ---- scores of this warp's 16 tokens: rows g and g + 8 of the block against every query row
+        // ---- scores of this warp's 16 tokens: places g and g + 8 of the block against every query row
         const int tok0 = cc.it.token(cc.j, kTile) + warp * kKvBlock;
         float sc[NR][2][4] = {};
         const uint32_t kbase = sm100::smem_u32(sm.k[stage]);
 #pragma unroll
         for (int k = 0; k < KI; ++k) {
             uint32_t w0[4], w1[4];
-            lds128(kbase + piece<D>(warp * kKvBlock + g, 4 * k + t), w0);
-            lds128(kbase + piece<D>(warp * kKvBlock + 8 + g, 4 * k + t), w1);
+            lds128(kbase + piece<D>(warp * kKvBlock + row_at(g), 4 * k + t), w0);
+            lds128(kbase + piece<D>(warp * kKvBlock + 8 + row_at(g), 4 * k + t), w1);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 uint32_t a[4];
@@ -360,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NR>()) attend_split_k
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     float y = fmaf(sc[r][0][2 * j + c] + sc[r][1][2 * j + c], f, lv);
-                    if (!all_seen && !sees(pos[r][c], tok0 + 8 * j + g, p.window, p.sinks)) y = -INFINITY;
+                    if (!all_seen && !sees(pos[r][c], tok0 + 8 * j + row_at(g), p.window, p.sinks)) y = -INFINITY;
                     x[r][j][c] = y;
                     big = fmaxf(big, y);
                 }
@@ -369,6 +362,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NR>()) attend_split_k
                 big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 16));
                 if (g == 0) sm.red[warp][8 * r + 2 * t + c] = big;
             }
+        // V rows past the sequence's end, whatever they hold, are cleared: their weights are 0, and 0 times a code is not
+        // 0 for a code that is NaN.  (Keys there only make scores that the mask replaces.)
+        const bool tail = tok0 + kKvBlock > cc.s.kvlen;
+        if (tail) {
+            for (int i = lane; i < kKvBlock * (D / 16); i += 32)
+                if (tok0 + i / (D / 16) >= cc.s.kvlen)
+                    *reinterpret_cast<uint4 *>(sm.v[stage] + piece<D>(warp * kKvBlock + i / (D / 16), i % (D / 16))) = make_uint4(0, 0, 0, 0);
+            sm100::fence_proxy_async_smem();   // before the stage is filled by TMA again
+        }
         sync_compute();
         // ---- weights
         const uint32_t pbase = sm100::smem_u32(sm.p);
@@ -417,8 +419,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NR>()) attend_split_k
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 uint32_t v0[NT], v1[NT];
-                value_columns<D, FMT>(vbase, (2 * half + b) * 16 + 2 * t, warp, g, v0);
-                value_columns<D, FMT>(vbase, (2 * half + b) * 16 + 2 * t + 8, warp, g, v1);
+                const int r0 = (2 * half + b) * 16 + row_at(2 * t), r1 = (2 * half + b) * 16 + row_at(2 * t + 1);
+                value_columns<D, FMT>(vbase, r0, r1, warp, g, v0);
+                value_columns<D, FMT>(vbase, r0 + 8, r1 + 8, warp, g, v1);
 #pragma unroll
                 for (int i = 0; i < NT / 2; ++i) {
                     const uint32_t a[4] = {v0[2 * i], v0[2 * i + 1], v1[2 * i], v1[2 * i + 1]};
@@ -506,10 +509,8 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const __gri
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.y;
     const int group = p.hq / p.pool.hkv;
     sm100::grid_dependency_wait();
-    if (plan.meta_by_item) {   // items that no CTA visited have no entry
-        const int per_seq = p.pool.hkv * plan.mt_max, n = blockIdx.x / per_seq;
-        if (blockIdx.x % plan.mt_max >= row_tiles<ROWS>(load_sequence(p, n).qlen, group)) return;
-    }
+    // items that no CTA visited have no entry
+    if (blockIdx.x % plan.mt_max >= row_tiles<ROWS>(load_sequence(p, blockIdx.x / (p.pool.hkv * plan.mt_max)).qlen, group)) return;
     const MergeMeta mm = plan.meta[blockIdx.x];
     if (mm.last < 0) return;
     const Sequence s = load_sequence(p, mm.n);
@@ -572,6 +573,29 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const __gri
     store_row<4>(p, ((size_t)(s.q0 + i) * p.hq + mm.h * group + grow % group) * D + col, y);
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+        cudaDriverEntryPointQueryResult q;
+        void *f = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+        return nullptr;
+    }();
+    return fn;
+}
+
+// The pool as rows of d bytes, read in boxes of one block (and at most 128 bytes of its rows).
+bool pool_map(CUtensorMap *m, const uint8_t *pages, const KvPool &pool, int d) {
+    const auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)pool.n_pages * pool.hkv * pool.page_size}, strides[1] = {(cuuint64_t)d};
+    const cuuint32_t box[2] = {(cuuint32_t)min(d, 128), kKvBlock}, es[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(pages), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              d == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Query rows of an item: the group's heads of one token where they are at most 8 and alone, else 16.
 int item_rows(int group, int max_q_len) { return (long long)group * max_q_len <= 8 ? 8 : 16; }
 
@@ -596,20 +620,28 @@ cudaError_t launch_split(const AttendProblem &p) {
     plan.meta = static_cast<MergeMeta *>(p.workspace);
     plan.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(p.workspace) + kMetaBytes);
 
+    constexpr size_t smem = sizeof(Smem<D, NR>) + 1024;
     static std::atomic<bool> ready[kMaxDevices];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= kMaxDevices || !ready[dev].load(std::memory_order_relaxed)) {
-        e = cudaFuncSetAttribute(attend_split_kernel<D, FMT, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem<D, NR>));
+        e = cudaFuncSetAttribute(attend_split_kernel<D, FMT, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         if (dev < kMaxDevices) ready[dev].store(true, std::memory_order_relaxed);
     }
-    attend_split_kernel<D, FMT, NR><<<ctas, kThreads, sizeof(Smem<D, NR>), p.stream>>>(p, plan);
+    CUtensorMap k_map, v_map;
+    if (!pool_map(&k_map, p.k_pages, p.pool, D) || !pool_map(&v_map, p.v_pages, p.pool, D)) return cudaErrorInvalidValue;
+    attend_split_kernel<D, FMT, NR><<<ctas, kThreads, smem, p.stream>>>(p, plan, k_map, v_map);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (ctas == 1 || bound == items) return cudaSuccess;   // no item crosses CTAs
-    return launch_after(p.stream, dim3((unsigned)(plan.meta_by_item ? items : ctas), (unsigned)min(8 * NR, p.max_q_len * group), D / 64),
-                        kMergeThreads, 0, attend_merge_kernel<D, 8 * NR>, p, plan);
+    // Few items in many parts (by item): CTAs for pieces of their rows.  Many items in a few parts each: one CTA does
+    // all of an item's rows.
+    if (plan.meta_by_item)
+        return launch_after(p.stream, dim3((unsigned)items, (unsigned)min(8 * NR, p.max_q_len * group), D / 64), kMergeThreads, 0,
+                            attend_merge_kernel<D, 8 * NR>, p, plan);
+    return launch_after(p.stream, dim3((unsigned)ctas, NR), 256, 0, attend_join_kernel<D, 8 * NR>, p,
+                        static_cast<const MergeMeta *>(plan.meta), static_cast<const float *>(plan.parts));
 }
 
 template <int D, int FMT>

@@ -188,5 +188,43 @@ cudaError_t launch_after(cudaStream_t stream, dim3 grid, int threads, size_t sme
     return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
+// Joins the parts of the items that cross CTAs, meta by first CTA: a warp per row, lanes over the columns.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendProblem p, const MergeMeta *meta, const float *parts) {
+    constexpr int PER = D / 32;
+    const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + (threadIdx.x >> 5), group = p.hq / p.pool.hkv;
+    sm100::grid_dependency_wait();
+    const MergeMeta mm = meta[blockIdx.x];
+    if (mm.last < 0) return;
+    const Sequence s = load_sequence(p, mm.n);
+    const int grow = mm.mt * ROWS + row;
+    if (grow / group >= s.qlen) return;
+    const size_t stride = ROWS * D + 2 * ROWS;
+    const int count = mm.last - mm.first + 1;
+    auto part = [&](int k) { return parts + (size_t)(2 * (mm.first + k) + (k == 0 ? mm.slot : 0)) * stride; };
+    float top = -INFINITY;
+    for (int k = lane; k < count; k += 32) top = fmaxf(top, part(k)[ROWS * D + row]);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float base = top == -INFINITY ? 0.f : top;
+    float l = 0.f, y[PER] = {};
+#pragma unroll 4
+    for (int k = 0; k < count; ++k) {
+        const float w = exp2f(part(k)[ROWS * D + row] - base);
+        l = fmaf(w, part(k)[ROWS * D + ROWS + row], l);
+        const float *o = part(k) + row * D + lane * PER;
+#pragma unroll
+        for (int e = 0; e < PER; e += 2) {
+            const float2 x = *reinterpret_cast<const float2 *>(o + e);
+            y[e] = fmaf(w, x.x, y[e]);
+            y[e + 1] = fmaf(w, x.y, y[e + 1]);
+        }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) y[e] *= inv;
+    store_row<PER>(p, ((size_t)(s.q0 + grow / group) * p.hq + mm.h * group + grow % group) * D + lane * PER, y);
+}
+
 }  // namespace attend
 }  // namespace gdn

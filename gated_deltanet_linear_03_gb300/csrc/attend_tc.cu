@@ -701,41 +701,6 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
     }
 }
 
-// Joins the parts of the items that cross CTAs: a warp per row, lanes over the columns.
-template <int D>
-__global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendProblem p, const __grid_constant__ TcPlan plan) {
-    constexpr int ROWS = Tc<D>::ROWS, PER = D / 32;
-    const int lane = threadIdx.x & 31, row = blockIdx.y * 8 + (threadIdx.x >> 5), group = p.hq / p.pool.hkv;
-    grid_dependency_wait();
-    const MergeMeta mm = plan.meta[blockIdx.x];
-    if (mm.last < 0) return;
-    const Sequence s = load_sequence(p, mm.n);
-    const int grow = mm.mt * ROWS + row;
-    if (grow / group >= s.qlen) return;
-    const size_t stride = ROWS * D + 2 * ROWS;
-    const int count = mm.last - mm.first + 1;
-    auto part = [&](int k) { return plan.parts + (size_t)(2 * (mm.first + k) + (k == 0 ? mm.slot : 0)) * stride; };
-    float top = -INFINITY;
-    for (int k = 0; k < count; ++k) top = fmaxf(top, part(k)[ROWS * D + row]);
-    const float base = top == -INFINITY ? 0.f : top;
-    float l = 0.f, y[PER] = {};
-    for (int k = 0; k < count; ++k) {
-        const float w = exp2f(part(k)[ROWS * D + row] - base);
-        l = fmaf(w, part(k)[ROWS * D + ROWS + row], l);
-        const float *o = part(k) + row * D + lane * PER;
-#pragma unroll
-        for (int e = 0; e < PER; e += 2) {
-            const float2 x = *reinterpret_cast<const float2 *>(o + e);
-            y[e] = fmaf(w, x.x, y[e]);
-            y[e + 1] = fmaf(w, x.y, y[e + 1]);
-        }
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) y[e] *= inv;
-    store_row<PER>(p, ((size_t)(s.q0 + grow / group) * p.hq + mm.h * group + grow % group) * D + lane * PER, y);
-}
-
 struct TcSizes {
     long long items;
     int ctas;
@@ -781,7 +746,8 @@ cudaError_t launch_tc(const AttendProblem &p) {
     attend_plan_kernel<L::ROWS><<<1, kPlanThreads, 0, p.stream>>>(p, plan);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if ((e = launch_after(p.stream, dim3((unsigned)z.ctas), L::THREADS, smem, attend_tc_kernel<D, FMT>, p, plan)) != cudaSuccess) return e;
-    return launch_after(p.stream, dim3((unsigned)z.ctas, L::ROWS / 8), 256, 0, attend_join_kernel<D>, p, plan);
+    return launch_after(p.stream, dim3((unsigned)z.ctas, L::ROWS / 8), 256, 0, attend_join_kernel<D, L::ROWS>, p,
+                        static_cast<const MergeMeta *>(plan.meta), static_cast<const float *>(plan.parts));
 }
 
 }  // namespace

@@ -342,3 +342,23 @@ def test_refusals(attn):
         call(workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
     with pytest.raises(GdnError):
         call(out=q)                                       # overlaps an input
+
+
+@pytest.mark.parametrize("m", [1, 40, 130])
+def test_garbage_past_the_end_is_not_read(attn, m):
+    """NaN codes in the rows after a sequence's last token, NaN scales after its last block, NaN pages around it."""
+    lens = [m + 45]
+    cache = ref.make_cache(lens, 2, 128, 32, F8, 14)
+    clean = ref.Cache(*[x.clone() for x in (cache.table, *cache.args)])
+    used = cache.table[0, :-(-lens[0] // 32)].tolist()
+    for pages, scales in ((cache.k_pages, cache.k_scales), (cache.v_pages, cache.v_scales)):
+        raw = pages.view(torch.uint8)
+        for page in range(pages.shape[0]):
+            if page not in used:
+                raw[page] = 0x7F
+                scales[page] = math.nan
+        raw[used[-1], :, lens[0] % 32:] = 0xFF
+        scales[used[-1], :, -(-(lens[0] % 32) // 16):] = math.nan
+    q = torch.randn(m, 4, 128, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    out, cu = run(attn, q, cache, [m], lens)
+    check(out, *ref.attend(q, clean, cu, lens))
