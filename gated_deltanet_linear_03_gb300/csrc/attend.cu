@@ -616,7 +616,9 @@ cudaError_t launch_split(const AttendProblem &p) {
     plan.min_units = 1;
     const long long items = (long long)p.n_seqs * p.pool.hkv * plan.mt_max;
     const int ctas = (int)min((bound + plan.min_units - 1) / plan.min_units, min(fit, (long long)kMaxSplitCtas));
-    plan.meta_by_item = items <= ctas;
+    // Few items in many parts: the merge goes by item, with a CTA for each piece of its rows.  Otherwise by the CTAs that
+    // items cross, one CTA for all of an item's rows (64 sequences of 8 heads: 17 us by item, 5 us so).
+    plan.meta_by_item = 4 * items <= ctas;
     plan.meta = static_cast<MergeMeta *>(p.workspace);
     plan.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(p.workspace) + kMetaBytes);
 
@@ -635,8 +637,6 @@ cudaError_t launch_split(const AttendProblem &p) {
     attend_split_kernel<D, FMT, NR><<<ctas, kThreads, smem, p.stream>>>(p, plan, k_map, v_map);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if (ctas == 1 || bound == items) return cudaSuccess;   // no item crosses CTAs
-    // Few items in many parts (by item): CTAs for pieces of their rows.  Many items in a few parts each: one CTA does
-    // all of an item's rows.
     if (plan.meta_by_item)
         return launch_after(p.stream, dim3((unsigned)items, (unsigned)min(8 * NR, p.max_q_len * group), D / 64), kMergeThreads, 0,
                             attend_merge_kernel<D, 8 * NR>, p, plan);

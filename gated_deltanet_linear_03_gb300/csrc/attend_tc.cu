@@ -109,72 +109,62 @@ __device__ __forceinline__ T block_scan(T v, T &sum, T *part) {
     return before + x - v;
 }
 
-// One CTA lists the items (sequence-major, heads inside, row tiles inside) and finds where every run begins.
+// One CTA lists the items (sequence-major, heads inside, row tiles inside) and finds where every run begins.  Each thread
+// takes consecutive items, so one scan over the threads gives all positions; the sequences' first items are scanned
+// before, a batch of sequences at a time.
 template <int ROWS>
 __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_constant__ AttendProblem p,
                                                                    const __grid_constant__ TcPlan plan) {
-    __shared__ long long part[kPlanThreads / 32];
+    __shared__ int part[kPlanThreads / 32];
+    __shared__ long long part_cost[kPlanThreads / 32];
+    __shared__ int first[kPlanThreads + 1];       // first item of each sequence of the batch
+    __shared__ Sequence seqs[kPlanThreads];
     const int tid = threadIdx.x, group = p.hq / p.pool.hkv;
     grid_launch_dependents();
-    for (int n = tid; n < p.n_seqs; n += kPlanThreads)
-        if (__ldg(p.cu + n + 1) - __ldg(p.cu + n) > p.max_q_len || __ldg(p.kv_lens + n) > p.max_kv_len || __ldg(p.kv_lens + n) < 0 ||
-            __ldg(p.cu + n + 1) > p.total || __ldg(p.cu + n) < 0 || __ldg(p.cu + n + 1) < __ldg(p.cu + n))
-            raise_error(p.err, kErrInternal);
-    // the items, written by the threads that hold their sequences
-    long long items = 0, total = 0;
+    int items = 0;
     for (int n0 = 0; n0 < p.n_seqs; n0 += kPlanThreads) {
-        const int n = n0 + tid;
+        const int n = n0 + tid, batch = min(kPlanThreads, p.n_seqs - n0);
         Sequence s{};
-        if (n < p.n_seqs) s = load_sequence(p, n);
-        long long mine = (long long)row_tiles<ROWS>(s.qlen, group) * p.pool.hkv, sum;
-        mine = block_scan(mine, sum, part) + items;
-        items += sum;
-        // long sequences are written by the whole CTA below, one after another
         if (n < p.n_seqs) {
-            const int mts = row_tiles<ROWS>(s.qlen, group);
-            if (mts <= 4)
-                for (int h = 0; h < p.pool.hkv; ++h)
-                    for (int mt = 0; mt < mts; ++mt) plan.items[mine + h * mts + mt] = make_int4(n, h, mt, make_item<ROWS, kTile>(p, s, group, mt).tiles);
+            s = load_sequence(p, n);
+            const int a = __ldg(p.cu + n), b = __ldg(p.cu + n + 1), c = __ldg(p.kv_lens + n);
+            if (b - a > p.max_q_len || c > p.max_kv_len || c < 0 || b > p.total || a < 0 || b < a) raise_error(p.err, kErrInternal);
         }
-        __shared__ int long_n[kPlanThreads], longs;
-        __shared__ long long long_at[kPlanThreads];
-        if (tid == 0) longs = 0;
+        seqs[tid] = s;
+        int sum;
+        first[tid] = block_scan(row_tiles<ROWS>(s.qlen, group) * p.pool.hkv, sum, part);
+        if (tid == 0) first[batch] = sum;
         __syncthreads();
-        if (n < p.n_seqs && row_tiles<ROWS>(s.qlen, group) > 4) {
-            const int at = atomicAdd(&longs, 1);
-            long_n[at] = n;
-            long_at[at] = mine;
-        }
-        __syncthreads();
-        for (int i = 0; i < longs; ++i) {
-            const Sequence ls = load_sequence(p, long_n[i]);
-            const int mts = row_tiles<ROWS>(ls.qlen, group);
-            for (int k = tid; k < mts * p.pool.hkv; k += kPlanThreads) {
-                const int mt = k % mts;
-                plan.items[long_at[i] + k] = make_int4(long_n[i], k / mts, mt, make_item<ROWS, kTile>(p, ls, group, mt).tiles);
+        for (int k = tid; k < sum; k += kPlanThreads) {
+            int lo = 0;
+            for (int hi = batch; hi - lo > 1;) {
+                const int mid = (lo + hi) >> 1;
+                if (first[mid] <= k) lo = mid;
+                else hi = mid;
             }
+            const int mts = row_tiles<ROWS>(seqs[lo].qlen, group), h = (k - first[lo]) / mts, mt = k - first[lo] - h * mts;
+            plan.items[items + k] = make_int4(n0 + lo, h, mt, make_item<ROWS, kTile>(p, seqs[lo], group, mt).tiles);
         }
+        items += sum;
         __syncthreads();
     }
-    long long mine = 0;
-    for (long long i = tid; i < items; i += kPlanThreads) mine += plan.items[i].w + kItemCost;
-    block_scan(mine, total, part);
+    const int each = (items + kPlanThreads - 1) / kPlanThreads, i0 = min(tid * each, items), i1 = min(i0 + each, items);
+    long long mine = 0, total;
+    for (int i = i0; i < i1; ++i) mine += plan.items[i].w + kItemCost;
+    long long at = block_scan(mine, total, part_cost);
     const long long per = max((total + plan.ctas - 1) / plan.ctas, 1LL);
     if (tid == 0) plan.per[0] = per;
-    long long before = 0;
-    for (long long i0 = 0; i0 < items; i0 += kPlanThreads) {
-        const long long i = i0 + tid;
-        const long long w = i < items ? plan.items[i].w + kItemCost : 0;
-        long long sum;
-        const long long at = before + block_scan(w, sum, part), unit = at - min(i, items) * kItemCost;
-        before += sum;
+    long long c = (at + per - 1) / per;           // the first run that begins at or after this thread's items
+    for (int i = i0; i < i1; ++i) {
+        const int w = plan.items[i].w + kItemCost;
         // a run that would begin inside an item's fixed cost begins at its first unit
-        for (long long c = (at + per - 1) / per; c < plan.ctas && c * per < at + w; ++c) {
-            const long long j = max(0LL, c * per - at - kItemCost);
-            plan.start[c] = {(int)i, (int)j, unit + j};
+        for (; c < plan.ctas && c * per < at + w; ++c) {
+            const int j = max(0, (int)(c * per - at) - kItemCost);
+            plan.start[c] = {i, j, at - (long long)i * kItemCost + j};
         }
+        at += w;
     }
-    for (long long c = (total + per - 1) / per + tid; c <= plan.ctas; c += kPlanThreads) plan.start[c] = {0, 0, total - items * kItemCost};
+    for (long long r = (total + per - 1) / per + tid; r <= plan.ctas; r += kPlanThreads) plan.start[r] = {0, 0, total - (long long)items * kItemCost};
 }
 
 // The run of one CTA, unit by unit; every role keeps its own.
