@@ -10,8 +10,8 @@
 //   softmax (4 NQ)  thread = row.  Load the query rows, scale each exactly by a power of two, and put them into TMEM
 //                   as the fp16 A operand of the score products; per unit read 64 scores, keep maximum and sum in
 //                   registers, write the fp16 weights over the scores in TMEM as the A operand of the output
-//                   products; rescale O in TMEM only when the row's maximum has grown by more than 2^8 (weights
-//                   then stay at most 2^8: fp16 holds them, and few units pay the pass over O); store the outputs.
+//                   products; rescale O in TMEM only when a weight would pass 2^15, the most that fp16 holds, so that
+//                   few units pay a second pass or one over O; store the outputs.
 //   loaders (8)     codes from global memory to registers (a unit ahead), turned to fp16 exactly, into 128B-swizzled
 //                   shared-memory tiles: the same layout serves K (K-major B) and V (MN-major B).
 //   MMA (1)         S = Q K^T of the next unit before O += W V of this one, so the tensor pipe works while the
@@ -59,7 +59,9 @@ struct __align__(1024) TcSmem {
     uint64_t s_full[Tc<D>::NQ][2], p_full[Tc<D>::NQ][2], pv_done[Tc<D>::NQ], q_full[Tc<D>::NQ];
     uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots], drain;
     float row_scale[Tc<D>::ROWS];                  // the power of two taken out of each query row
-    float pair[2][Tc<D>::CS][128], pair_sum[Tc<D>::CS][128];   // maxima and sums that the two threads of a row tell each other
+    // what the two warps of a row tell each other: maxima, sums, and whether a weight would be too large
+    float pair[Tc<D>::CS][128], pair_sum[Tc<D>::CS][128];
+    int over[2][Tc<D>::CS][4];
     uint64_t pair_bar[4];
     uint32_t tmem;
     int abort;
@@ -274,12 +276,11 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
         const uint32_t o_at = quad + L::O + q * D, q_at = quad + L::Q + q * (D / 2), s_at = quad + L::S + q * SB * 64;
         // The two warps that share rows meet at an mbarrier, so that this wait is bounded like the others.
         int pair_phase = 0;
-        auto meet = [&]() -> bool {
+        auto come = [&]() {
             __syncwarp();
-            if (CS == 1) return true;
-            if (lane == 0) mbar_arrive(&sm.pair_bar[quadrant]);
-            return wait(&sm.pair_bar[quadrant], pair_phase++);
+            if (CS == 2 && lane == 0) mbar_arrive(&sm.pair_bar[quadrant]);
         };
+        auto meet = [&]() -> bool { return CS == 1 || wait(&sm.pair_bar[quadrant], pair_phase++); };   // after come()
         MergeMeta mm;
         mm.last = -1;
         if (units > 0) {
@@ -335,6 +336,7 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                 }
                 tmem_st_wait();
                 tc_fence_before();
+                come();
                 if (!(ok = meet())) break;
                 if (lane == 0) mbar_arrive(&sm.q_full[q]);
                 const float rs = sm.row_scale[q * 128 + row] * fabsf(p.sm_scale) * 1.4426950408889634f;
@@ -349,86 +351,111 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                     if (!(ok = wait(&sm.s_full[q][buf], buf_phase))) break;
                     tc_fence_after();
                     const bool all_seen = w.it.all_seen(tok0, tok0 + NC, p.window, p.sinks);
-                    // 32 scores from `at` tokens into the share, with the factor and offset that make them x = s f + lv;
-                    // a score that the row does not see becomes -infinity
-                    float s[32], f[2], lv[2];
-                    auto load = [&](int at) {
-                        tmem_ld32(s_tm + part_of * NC + at, s);
+                    float f[NC / 16], lv[NC / 16];
+                    // In the common pass the weights are formed at once with the maximum that the rows have, while the unit's
+                    // own maxima are found: only where one is above it by more than 2^15 (or the row saw nothing so far) the maximum is
+                    // raised, O scaled, and the pass done again.  Raised maxima then leave weights of at most 1, and they
+                    // never pass 2^15, which fp16 holds.
+                    bool raise = first;
+                    for (;;) {
+                        float s[NC];
+                        if constexpr (CS == 2) tmem_ld32(s_tm + part_of * 32, s);
+                        else tmem_ld32x2(s_tm, s_tm + 32, s, s + 32);
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            f[b] = rs * sm.scale[slot][part_of * (NC / 16) + at / 16 + b];
-                            lv[b] = sm.scale[slot][4 + part_of * (NC / 16) + at / 16 + b];
+                        for (int b = 0; b < NC / 16; ++b) {
+                            f[b] = rs * sm.scale[slot][part_of * (NC / 16) + b];
+                            lv[b] = sm.scale[slot][4 + part_of * (NC / 16) + b];
                         }
-                        if (all_seen) return;
+                        if (!all_seen) {
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            s[c] = sees(pos, tok0 + at + c, p.window, p.sinks) ? fmaf(s[c], f[c / 16], lv[c / 16]) : -INFINITY;
+                            for (int c = 0; c < NC; ++c)
+                                s[c] = sees(pos, tok0 + c, p.window, p.sinks) ? fmaf(s[c], f[c / 16], lv[c / 16]) : -INFINITY;
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) f[b] = 1.f, lv[b] = 0.f;
-                    };
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int at = 0; at < NC; at += 32) {
-                        load(at);
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            float x[4];
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) x[c] = fmaxf(fmaxf(s[16 * b + c], s[16 * b + 4 + c]), fmaxf(s[16 * b + 8 + c], s[16 * b + 12 + c]));
-                            top = fmaxf(top, fmaf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), f[b], lv[b]));
+                            for (int b = 0; b < NC / 16; ++b) f[b] = 1.f, lv[b] = 0.f;
                         }
-                    }
-                    if (CS == 2) {
-                        sm.pair[u & 1][part_of][row] = top;
-                        if (!(ok = meet())) break;   // both have read their scores too, so weights may overwrite them
-                        top = fmaxf(top, sm.pair[u & 1][CS - 1 - part_of][row]);
-                    }
-                    if (__any_sync(0xffffffffu, first || top > m + 8.f)) {
-                        if (first) {
-                            m = top;
-                        } else {
-                            if (!(ok = wait(&sm.pv_done[q], u - 1))) break;
-                            tc_fence_after();
-                            const float to = top > m + 8.f ? top : m, c = m == to ? 1.f : exp2f(m - to);
-                            m = to;
-                            l *= c;
-#pragma unroll 1
-                            for (int k = part_of; k < D / 32; k += CS) {
-                                float o[32];
-                                tmem_ld32(o_at + 32 * k, o);
-                                uint32_t x[32];
+                        const bool raised = raise;
+                        if (raise) {
+                            float top = -INFINITY;
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(o[e] * c);
-                                tmem_st32(o_at + 32 * k, x);
+                            for (int b = 0; b < NC / 16; ++b) {
+                                float x[4];
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) x[c] = fmaxf(fmaxf(s[16 * b + c], s[16 * b + 4 + c]), fmaxf(s[16 * b + 8 + c], s[16 * b + 12 + c]));
+                                top = fmaxf(top, fmaf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), f[b], lv[b]));
                             }
-                            tmem_st_wait();
+                            if (CS == 2) {
+                                sm.pair[part_of][row] = top;
+                                come();
+                                if (!(ok = meet())) break;
+                                top = fmaxf(top, sm.pair[CS - 1 - part_of][row]);
+                            }
+                            if (first) {
+                                m = top;
+                            } else {
+                                if (!(ok = wait(&sm.pv_done[q], u - 1))) break;
+                                tc_fence_after();
+                                const float to = fmaxf(m, top), c = m == to ? 1.f : exp2f(m - to);
+                                m = to;
+                                l *= c;
+#pragma unroll 1
+                                for (int k = part_of; k < D / 32; k += CS) {
+                                    float o[32];
+                                    tmem_ld32(o_at + 32 * k, o);
+                                    uint32_t x[32];
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(o[e] * c);
+                                    tmem_st32(o_at + 32 * k, x);
+                                }
+                                tmem_st_wait();
+                            }
                         }
-                    }
-                    const float base = m == -INFINITY ? 0.f : m;
+                        const float base = m == -INFINITY ? 0.f : m;
+                        float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int at = 0; at < NC; at += 32) {
-                        if (NC > 32) load(at);   // two shares of 32 do not both stay in registers
-                        uint32_t x[16];
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) {
+                        for (int b = 0; b < NC / 16; ++b) {
                             const float off = lv[b] - base;
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                fma2(s[16 * b + 2 * c], s[16 * b + 2 * c + 1], f[b], off);
+                                top[c & 1] = fmaxf(top[c & 1], fmaxf(s[16 * b + 2 * c], s[16 * b + 2 * c + 1]));
+                            }
+                        }
+                        bool over = !raised && __any_sync(0xffffffffu, fmaxf(top[0], top[1]) > (m == -INFINITY ? m : 15.f));
+                        if (CS == 2 && !raised) {
+                            if (lane == 0) sm.over[pair_phase & 1][part_of][quadrant] = over;
+                            come();
+                        }
+                        uint32_t x[NC / 2];
+                        float add = 0.f;
+#pragma unroll
+                        for (int b = 0; b < NC / 16; ++b) {
                             float sum[2] = {0.f, 0.f};
 #pragma unroll
                             for (int c = 0; c < 8; ++c) {
-                                float e0 = s[16 * b + 2 * c], e1 = s[16 * b + 2 * c + 1];
-                                fma2(e0, e1, f[b], off);
-                                e0 = exp2_fast(e0);
-                                e1 = exp2_fast(e1);
+                                const float e0 = exp2_fast(s[16 * b + 2 * c]), e1 = exp2_fast(s[16 * b + 2 * c + 1]);
                                 add2(sum[0], sum[1], e0, e1);
                                 const __half2 hh = __floats2half2_rn(e0, e1);
                                 x[8 * b + c] = *reinterpret_cast<const uint32_t *>(&hh);
                             }
                             sum[0] += sum[1];
                             // a block that no row sees may have any scale
-                            if (sum[0] != 0.f) l = fmaf(sum[0], sm.scale[slot][8 + part_of * (NC / 16) + at / 16 + b], l);
+                            if (sum[0] != 0.f) add = fmaf(sum[0], sm.scale[slot][8 + part_of * (NC / 16) + b], add);
                         }
-                        tmem_st16(s_tm + part_of * 16 + at / 2, x);   // columns below the ones still to be read
+                        if (CS == 2 && !raised) {
+                            const int turn = pair_phase & 1;
+                            if (!(ok = meet())) break;   // both have read their scores too, so weights may overwrite them
+                            over |= sm.over[turn][CS - 1 - part_of][quadrant];
+                        }
+                        if (over) {
+                            raise = true;
+                            continue;
+                        }
+                        l += add;
+                        if constexpr (CS == 2) tmem_st16(s_tm + part_of * 16, x);
+                        else tmem_st32(s_tm, x);
+                        break;
                     }
+                    if (!ok) break;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.sc_empty[slot]);
                     tmem_st_wait();
@@ -447,6 +474,7 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                 tc_fence_after();
                 if (CS == 2) {
                     sm.pair_sum[part_of][row] = l;
+                    come();
                     if (!(ok = meet())) break;
                     l += sm.pair_sum[CS - 1 - part_of][row];
                 }
