@@ -205,16 +205,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NR>()) attend_split_k
     // A bounded wait; when it runs out the error is recorded and every later wait returns at once.
     volatile int *abort = &sm.abort;
     auto wait = [&](uint64_t *bar, int phase) {
-        if (sm100::mbar_try_wait(bar, (uint32_t)phase & 1)) return;
-        const uint64_t t0 = sm100::global_timer_ns();
-        while (!sm100::mbar_try_wait(bar, (uint32_t)phase & 1)) {
-            if (*abort) return;
-            if (sm100::global_timer_ns() - t0 > sm100::kWaitTimeoutNs) {
-                *abort = 1;
-                raise_error(p.err, kErrTimeout);
-                return;
-            }
-        }
+        bool late = false;
+        sm100::mbar_poll(bar, (uint32_t)phase & 1, abort, &late);
+        if (late) raise_error(p.err, kErrTimeout);
     };
     const int units = stop - start;
 

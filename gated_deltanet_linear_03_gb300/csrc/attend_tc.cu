@@ -7,18 +7,17 @@
 // that crosses CTAs is joined by attend_join_kernel.
 //
 // Warps of a CTA, each following the same run of units through mbarriers:
-//   softmax (4 NQ)  thread = row.  Load the query rows, scale each exactly by a power of two, and put them into TMEM
-//                   as the fp16 A operand of the score products; per unit read 64 scores, keep maximum and sum in
-//                   registers, write the fp16 weights over the scores in TMEM as the A operand of the output
-//                   products; rescale O in TMEM only when a weight would pass 2^15, the most that fp16 holds, so that
-//                   few units pay a second pass or one over O; store the outputs.
-//   loaders (8)     codes from global memory to registers (a unit ahead), turned to fp16 exactly, into 128B-swizzled
-//                   shared-memory tiles: the same layout serves K (K-major B) and V (MN-major B).
-//   MMA (1)         S = Q K^T of the next unit before O += W V of this one, so the tensor pipe works while the
-//                   softmax does.
-//   scales (1)      the unit's four block scales, their logarithms and reciprocals.
+//   softmax (8 NQ)  a warp has 16 rows, 4 lanes to a row.  It brings their queries, scaled exactly by a power of two, into
+//                   TMEM as the fp16 A operand of the score products; per unit it reads the rows' 64 scores, forms the
+//                   weights in one pass with the rows' present reference M and writes them as fp16 over the scores, where
+//                   they are the A operand of the output products.  Only where a score is above M by more than 15 (2^15
+//                   is the most that fp16 holds) M is raised, O scaled in TMEM, and the pass done again.  So the
+//                   common pass needs no exchange beyond the warp, and no reduction over a row until the item's end.
+//   loaders         codes from global memory to registers, turned to fp16 exactly, into 128B-swizzled shared-memory tiles:
+//                   the same layout serves K (K-major B) and V (MN-major B).  And the block scales.
+//   MMA (2)         one issues S = Q K^T, as far ahead as there are score buffers, one O += W V.
 // Queries and weights as TMEM operands leave shared memory to K and V: per unit 2 x 64 x D x 2 bytes written by the
-// loaders and read once by the MMAs.
+// loaders and read NQ times by the MMAs.
 // Bound by the tensor pipe (4 D FLOP a row and token).
 #include "attend.cuh"
 
@@ -30,39 +29,37 @@ using namespace sm100;
 
 constexpr int kTile = 64;
 constexpr int kStages = 3;
-constexpr int kScaleSlots = 4;
-constexpr int kLoaderWarps = 8;
+constexpr int kScaleSlots = 32;    // of block scales, a unit each
 
 template <int D>
 struct Tc {
-    static constexpr int NQ = D == 256 ? 1 : 2;              // 128-row tiles of a CTA
+    static constexpr int NQ = D == 256 ? 1 : 2;              // 128-row tiles of a CTA, which share its K and V
     static constexpr int ROWS = 128 * NQ;
     static constexpr int SB = NQ * (D + D / 2 + 128) <= 512 ? 2 : 1;   // score buffers of a tile
-    static constexpr int O = 0, Q = NQ * D, S = NQ * (D + D / 2);      // TMEM columns
-    static constexpr int CS = 2 / NQ;                        // softmax threads a row, each on 64 / CS of a unit's tokens
-    static constexpr int SOFTMAX_WARPS = 8;
-    static constexpr int WARPS = SOFTMAX_WARPS + kLoaderWarps + 4;     // the last four: MMA, scales, two idle
-    static constexpr int THREADS = 32 * WARPS;
-    // Registers a thread: at launch (the most that WARPS warps can have, a multiple of 8), then per role.  The roles'
-    // shares stay within what the CTA was launched with: 640 x 96 = 256 x 136 + 256 x 72 + 128 x 64.
-    static constexpr int REGS_LAUNCH = 96, REGS_SOFTMAX = 136, REGS_LOADER = 72, REGS_OTHER = 64;
-    static_assert(32 * (SOFTMAX_WARPS * REGS_SOFTMAX + kLoaderWarps * REGS_LOADER + 4 * REGS_OTHER) <= THREADS * REGS_LAUNCH, "registers");
-    static constexpr int TILE_BYTES = kTile * D * 2;
+    static constexpr int O = 0, Q = NQ * D, S = NQ * (D + D / 2);      // TMEM columns: O fp32, Q two fp16 a column, S of 64
+    static constexpr int LU = 256 / D;                       // units of a load tile: 16 KB of K codes and 16 KB of V codes
+    static constexpr int LG = D == 256 ? 2 : 1;              // groups of 8 loader warps, which take the tiles in turn
+    // A loader is at most kStages + LG tiles ahead of the score product, and that SB units ahead of the softmax.
+    static_assert(LU * (kStages + LG) + SB < kScaleSlots, "scale slots");
+    static constexpr int SOFTMAX_WARPS = 8 * NQ, LOADER_WARPS = 8 * LG;
+    static constexpr int WARPS = SOFTMAX_WARPS + LOADER_WARPS + 4;     // the last four: MMA, MMA, two idle
+    static constexpr int THREADS = 32 * WARPS;               // 896
+    // Registers a thread: at launch (the most that 28 warps can have, a multiple of 8), then per role.  The roles' shares
+    // stay within what the CTA was launched with: 896 x 72 = 256 x 104 + 512 x 64 + 128 x 40 >= 512 x 80 + 256 x 64 + 128 x 40.
+    static constexpr int REGS_LAUNCH = 72, REGS_SOFTMAX = NQ == 1 ? 104 : 80, REGS_LOADER = 64, REGS_OTHER = 40;
+    static_assert(32 * (SOFTMAX_WARPS * REGS_SOFTMAX + LOADER_WARPS * REGS_LOADER + 4 * REGS_OTHER) <= THREADS * REGS_LAUNCH, "registers");
+    static constexpr int TILE_ROWS = kTile * LU, TILE_BYTES = TILE_ROWS * D * 2, CHUNK = TILE_ROWS * 128;   // CHUNK: 64 columns
 };
 
 template <int D>
 struct __align__(1024) TcSmem {
+    static constexpr int NQ = Tc<D>::NQ;
     uint8_t k[kStages][Tc<D>::TILE_BYTES];
     uint8_t v[kStages][Tc<D>::TILE_BYTES];
     float scale[kScaleSlots][12];        // K scales, log2 of V scales, reciprocals of V scales
+    float row_m[Tc<D>::ROWS], row_l[Tc<D>::ROWS];   // at an item's end
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-    uint64_t s_full[Tc<D>::NQ][2], p_full[Tc<D>::NQ][2], pv_done[Tc<D>::NQ], q_full[Tc<D>::NQ];
-    uint64_t sc_full[kScaleSlots], sc_empty[kScaleSlots], drain;
-    float row_scale[Tc<D>::ROWS];                  // the power of two taken out of each query row
-    // what the two warps of a row tell each other: maxima, sums, and whether a weight would be too large
-    float pair[Tc<D>::CS][128], pair_sum[Tc<D>::CS][128];
-    int over[2][Tc<D>::CS][4];
-    uint64_t pair_bar[4];
+    uint64_t s_full[NQ][2], s_free[NQ][2], p_full[NQ][2], pv_done[NQ], q_full[NQ], drain[2];
     uint32_t tmem;
     int abort;
 };
@@ -115,8 +112,7 @@ __device__ __forceinline__ T block_scan(T v, T &sum, T *part) {
 // takes consecutive items, so one scan over the threads gives all positions; the sequences' first items are scanned
 // before, a batch of sequences at a time.
 template <int ROWS>
-__global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_constant__ AttendProblem p,
-                                                                   const __grid_constant__ TcPlan plan) {
+__global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_constant__ AttendProblem p, const __grid_constant__ TcPlan plan) {
     __shared__ int part[kPlanThreads / 32];
     __shared__ long long part_cost[kPlanThreads / 32];
     __shared__ int first[kPlanThreads + 1];       // first item of each sequence of the batch
@@ -169,7 +165,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
     for (long long r = (total + per - 1) / per + tid; r <= plan.ctas; r += kPlanThreads) plan.start[r] = {0, 0, total - (long long)items * kItemCost};
 }
 
-// The run of one CTA, unit by unit; every role keeps its own.
+// Where a role stands in its CTA's run; every role keeps its own.
 template <int ROWS>
 struct Walk {
     const AttendProblem &p;
@@ -194,13 +190,13 @@ struct Walk {
         j = 0;
     }
     __device__ __forceinline__ int token() const { return it.token(j, kTile); }
-    __device__ __forceinline__ bool last() const { return j == tiles - 1; }
-    // to the next unit (which the run must hold)
+    // to the next unit, or item (which the run must hold)
     __device__ __forceinline__ void next() {
-        if (++j == tiles) {
-            ++item;
-            load();
-        }
+        if (++j == tiles) next_item();
+    }
+    __device__ __forceinline__ void next_item() {
+        ++item;
+        load();
     }
 };
 
@@ -217,25 +213,22 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
     if (warp == 0) tmem_alloc(&sm.tmem, 512);
     if (tid == 32) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sm.k_full[i], kLoaderWarps);
-            mbar_init(&sm.v_full[i], kLoaderWarps);
+            mbar_init(&sm.k_full[i], 8);
+            mbar_init(&sm.v_full[i], 8);
             mbar_init(&sm.k_empty[i], 1);
             mbar_init(&sm.v_empty[i], 1);
         }
         for (int q = 0; q < NQ; ++q) {
-            for (int b = 0; b < 2; ++b) {
-                mbar_init(&sm.s_full[q][b], 1);
-                mbar_init(&sm.p_full[q][b], 4 * L::CS);
+            for (int b = 0; b < SB; ++b) {
+                mbar_init(&sm.s_full[q][b], 2);
+                mbar_init(&sm.s_free[q][b], 1);
+                mbar_init(&sm.p_full[q][b], 8);
             }
             mbar_init(&sm.pv_done[q], 1);
-            mbar_init(&sm.q_full[q], 4 * L::CS);
+            mbar_init(&sm.q_full[q], 8);
         }
-        for (int i = 0; i < kScaleSlots; ++i) {
-            mbar_init(&sm.sc_full[i], 1);
-            mbar_init(&sm.sc_empty[i], L::SOFTMAX_WARPS);
-        }
-        for (int i = 0; i < 4; ++i) mbar_init(&sm.pair_bar[i], 2);
-        mbar_init(&sm.drain, 1);
+        mbar_init(&sm.drain[0], 1);
+        mbar_init(&sm.drain[1], 1);
         sm.abort = 0;
         fence_mbar_init();
     }
@@ -248,65 +241,51 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
     const long long per = plan.per[0];
     const int units = (int)(plan.start[cta + 1].unit - plan.start[cta].unit);
 
-    // A bounded wait: when it runs out, or another thread's has, every role leaves its loop.
+    // Waits are bounded.  One that runs out records the error and sets a flag with which every later wait returns at once;
+    // no warp leaves its loop, so no named barrier is left waiting.
     volatile int *abort = &sm.abort;
-    auto wait_one = [&](uint64_t *bar, int phase) -> bool {
-        if (mbar_try_wait(bar, (uint32_t)phase & 1)) return true;
-        const uint64_t t0 = global_timer_ns();
-        while (!mbar_try_wait(bar, (uint32_t)phase & 1)) {
-            if (*abort) return false;
-            if (global_timer_ns() - t0 > kWaitTimeoutNs) {
-                *abort = 1;
-                raise_error(p.err, kErrTimeout);
-                return false;
-            }
-        }
-        return true;
+    auto poll = [&](uint64_t *bar, int phase) {
+        bool late = false;
+        mbar_poll(bar, (uint32_t)phase & 1, abort, &late);
+        if (late) raise_error(p.err, kErrTimeout);
     };
-    // ... by all lanes of a warp, with one answer: what follows may be warp-wide.
-    auto wait = [&](uint64_t *bar, int phase) -> bool { return __all_sync(0xffffffffu, wait_one(bar, phase)); };
+    auto arrive = [&](uint64_t *bar) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
 
     if (warp < L::SOFTMAX_WARPS) {
-        set_max_registers_up<L::REGS_SOFTMAX>();
+        set_max_registers<L::REGS_SOFTMAX, L::REGS_LAUNCH>();
         // ------------------------------------------------------------------------------------------ softmax
-        constexpr int CS = L::CS, NC = 64 / CS;                          // tokens of a thread's share of a unit
-        const int q = CS == 2 ? 0 : warp / 4, part_of = CS == 2 ? warp / 4 : 0, quadrant = warp & 3;
-        const int row = 32 * quadrant + lane;                            // of the 128-row tile
-        const uint32_t quad = tmem + ((uint32_t)quadrant << 21);         // its lanes
-        const uint32_t o_at = quad + L::O + q * D, q_at = quad + L::Q + q * (D / 2), s_at = quad + L::S + q * SB * 64;
-        // The two warps that share rows meet at an mbarrier, so that this wait is bounded like the others.
-        int pair_phase = 0;
-        auto come = [&]() {
+        const int q = NQ == 2 ? warp / 8 : 0, quadrant = warp & 3, half = (warp >> 2) & 1, g = lane >> 2, t = lane & 3;
+        const int row0 = 128 * q + 32 * quadrant + 16 * half + g;        // this lane's rows: row0 and row0 + 8
+        const uint32_t quad = tmem + ((uint32_t)quadrant << 21), part16 = quad + ((uint32_t)(16 * half) << 16);   // lanes
+        const uint32_t o_cols = L::O + q * D, q_at = part16 + L::Q + q * (D / 2), s_at = part16 + L::S + q * SB * 64;
+        auto wait = [&](uint64_t *bar, int phase) {
+            poll(bar, phase);
             __syncwarp();
-            if (CS == 2 && lane == 0) mbar_arrive(&sm.pair_bar[quadrant]);
         };
-        auto meet = [&]() -> bool { return CS == 1 || wait(&sm.pair_bar[quadrant], pair_phase++); };   // after come()
         MergeMeta mm;
         mm.last = -1;
         if (units > 0) {
             Walk<ROWS> w(p, plan, group);
-            bool ok = true;
-            int buf = 0, buf_phase = 0, slot = 0, slot_phase = 0;
-            for (int u = 0; ok && u < units;) {
-                // ---- a segment: the query rows
+            int buf = 0, phase = 0;
+            for (int u = 0, seg = 0; u < units; ++seg) {
+                // ---- a segment, units of one item: its queries, 4 lanes to a row, 16 bytes each.  The first pass finds the
+                // rows' scales, the second (from L1) converts.
                 const bool begun = w.j == 0;
-                const int seg_slot = u == 0 ? 0 : 1;
-                const int grow = w.mt * ROWS + q * 128 + row, i = grow / group;
-                const bool valid = i < w.s.qlen;
-                const int pos = w.s.kvlen - w.s.qlen + i;
-                const size_t out_row = ((size_t)(w.s.q0 + (valid ? i : 0)) * p.hq + w.h * group + grow % group) * D;
-                // 4 lanes to a row, 16 bytes each, 8 rows at a time: rows 16 half + 8 k + lane / 4 of the warp's 32.  The
-                // first pass finds the rows' scales, the second (from L1) converts: fewer registers than holding them.
-#pragma unroll 1
-                for (int half = CS == 2 ? part_of : 0; half < (CS == 2 ? part_of + 1 : 2); ++half) {
+                const int seg_slot = u == 0 ? 0 : 1, u_end = min(units, u + w.tiles - w.j);
+                float rs[2];
+                int pos[2];
+                {
                     const uint4 *src[2];
                     float down[2];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const int r = 32 * quadrant + 16 * half + 8 * k + lane / 4, gr = w.mt * ROWS + q * 128 + r;
-                        const int i = gr / group;
+                        const int gr = w.mt * ROWS + row0 + 8 * k, i = gr / group;
+                        pos[k] = w.s.kvlen - w.s.qlen + i;
                         src[k] = i < w.s.qlen
-                                     ? reinterpret_cast<const uint4 *>(p.q + ((size_t)(w.s.q0 + i) * p.hq + w.h * group + gr % group) * D) + lane % 4
+                                     ? reinterpret_cast<const uint4 *>(p.q + ((size_t)(w.s.q0 + i) * p.hq + w.h * group + gr % group) * D) + t
                                      : nullptr;
                         uint32_t big = 0;
 #pragma unroll
@@ -316,7 +295,7 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                         float up;
                         power_of_two_scale(big, down[k], up);
                         if (p.sm_scale < 0.f) down[k] = -down[k];     // the row factor stays >= 0
-                        if (lane % 4 == 0) sm.row_scale[q * 128 + r] = up;
+                        rs[k] = up * fabsf(p.sm_scale) * 1.4426950408889634f;
                     }
 #pragma unroll 2
                     for (int c = 0; c < D / 64; ++c) {
@@ -331,178 +310,161 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                                 x[8 * i2 + 4 + 2 * k] = bf16x2_to_f16x2(z.z, down[k]);
                                 x[8 * i2 + 4 + 2 * k + 1] = bf16x2_to_f16x2(z.w, down[k]);
                             }
-                        tmem_st_16x32(q_at + ((uint32_t)(16 * half) << 16) + 32 * c, x);
+                        tmem_st_16x32(q_at + 32 * c, x);
                     }
+                    tmem_st_wait();
                 }
-                tmem_st_wait();
                 tc_fence_before();
-                come();
-                if (!(ok = meet())) break;
-                if (lane == 0) mbar_arrive(&sm.q_full[q]);
-                const float rs = sm.row_scale[q * 128 + row] * fabsf(p.sm_scale) * 1.4426950408889634f;
-                float m = -INFINITY, l = 0.f;
-                bool ends;
-                for (bool first = true;; first = false) {
+                arrive(&sm.q_full[q]);              // also: this warp has read its part of the item before
+                float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+                bool raise = true;                  // the item's first unit sets M
+                for (; u < u_end; ++u, ++w.j) {
                     // ---- one unit
                     const uint32_t s_tm = s_at + buf * 64;
-                    const int tok0 = w.token() + part_of * NC;
-                    ends = w.last();
-                    if (!(ok = wait(&sm.sc_full[slot], slot_phase))) break;
-                    if (!(ok = wait(&sm.s_full[q][buf], buf_phase))) break;
+                    const int tok0 = w.token();
+                    const bool all_seen = w.it.all_seen(tok0, tok0 + kTile, p.window, p.sinks);
+                    const float *scale = sm.scale[u % kScaleSlots];
+                    wait(&sm.s_full[q][buf], phase);
                     tc_fence_after();
-                    const bool all_seen = w.it.all_seen(tok0, tok0 + NC, p.window, p.sinks);
-                    float f[NC / 16], lv[NC / 16];
-                    // In the common pass the weights are formed at once with the maximum that the rows have, while the unit's
-                    // own maxima are found: only where one is above it by more than 2^15 (or the row saw nothing so far) the maximum is
-                    // raised, O scaled, and the pass done again.  Raised maxima then leave weights of at most 1, and they
-                    // never pass 2^15, which fp16 holds.
-                    bool raise = first;
+                    const bool first = raise;
                     for (;;) {
-                        float s[NC];
-                        if constexpr (CS == 2) tmem_ld32(s_tm + part_of * 32, s);
-                        else tmem_ld32x2(s_tm, s_tm + 32, s, s + 32);
-#pragma unroll
-                        for (int b = 0; b < NC / 16; ++b) {
-                            f[b] = rs * sm.scale[slot][part_of * (NC / 16) + b];
-                            lv[b] = sm.scale[slot][4 + part_of * (NC / 16) + b];
-                        }
+                        // scores of row k at tokens 8 i + 2 t, + 1: s[4 i + 2 k], + 1
+                        float s[32];
+                        tmem_ld_16x64(s_tm, s);
+                        float4 ks = *reinterpret_cast<const float4 *>(scale), lv = *reinterpret_cast<const float4 *>(scale + 4);
+                        float ksc[4] = {ks.x, ks.y, ks.z, ks.w}, lvs[4] = {lv.x, lv.y, lv.z, lv.w};
+                        float f0 = rs[0], f1 = rs[1];
                         if (!all_seen) {
 #pragma unroll
-                            for (int c = 0; c < NC; ++c)
-                                s[c] = sees(pos, tok0 + c, p.window, p.sinks) ? fmaf(s[c], f[c / 16], lv[c / 16]) : -INFINITY;
+                            for (int i = 0; i < 8; ++i)
 #pragma unroll
-                            for (int b = 0; b < NC / 16; ++b) f[b] = 1.f, lv[b] = 0.f;
+                                for (int e = 0; e < 4; ++e)
+                                    s[4 * i + e] = sees(pos[e / 2], tok0 + 8 * i + 2 * t + (e & 1), p.window, p.sinks)
+                                                       ? fmaf(s[4 * i + e], rs[e / 2] * ksc[i / 2], lvs[i / 2]) : -INFINITY;
+                            f0 = f1 = 1.f;
+#pragma unroll
+                            for (int b = 0; b < 4; ++b) ksc[b] = 1.f, lvs[b] = 0.f;
                         }
-                        const bool raised = raise;
                         if (raise) {
-                            float top = -INFINITY;
+                            float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                            for (int b = 0; b < NC / 16; ++b) {
-                                float x[4];
+                            for (int b = 0; b < 4; ++b)
 #pragma unroll
-                                for (int c = 0; c < 4; ++c) x[c] = fmaxf(fmaxf(s[16 * b + c], s[16 * b + 4 + c]), fmaxf(s[16 * b + 8 + c], s[16 * b + 12 + c]));
-                                top = fmaxf(top, fmaf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), f[b], lv[b]));
+                                for (int k = 0; k < 2; ++k) {
+                                    const float *x = s + 8 * b + 2 * k;
+                                    top[k] = fmaxf(top[k], fmaf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[4], x[5])), (k ? f1 : f0) * ksc[b], lvs[b]));
+                                }
+                            float c[2];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 1));
+                                top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 2));
+                                const float to = fmaxf(m[k], top[k]);
+                                c[k] = m[k] == to ? 1.f : exp2f(m[k] - to);
+                                m[k] = to;
+                                l[k] *= c[k];
                             }
-                            if (CS == 2) {
-                                sm.pair[part_of][row] = top;
-                                come();
-                                if (!(ok = meet())) break;
-                                top = fmaxf(top, sm.pair[CS - 1 - part_of][row]);
-                            }
-                            if (first) {
-                                m = top;
-                            } else {
-                                if (!(ok = wait(&sm.pv_done[q], u - 1))) break;
+                            if (!first) {
+                                wait(&sm.pv_done[q], u - 1);
                                 tc_fence_after();
-                                const float to = fmaxf(m, top), c = m == to ? 1.f : exp2f(m - to);
-                                m = to;
-                                l *= c;
 #pragma unroll 1
-                                for (int k = part_of; k < D / 32; k += CS) {
-                                    float o[32];
-                                    tmem_ld32(o_at + 32 * k, o);
-                                    uint32_t x[32];
+                                for (int k = 0; k < D / 32; ++k) {
+                                    float o[16];
+                                    tmem_ld_16x32(part16 + o_cols + 32 * k, o);
+                                    uint32_t x[16];
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(o[e] * c);
-                                    tmem_st32(o_at + 32 * k, x);
+                                    for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(o[e] * c[(e >> 1) & 1]);
+                                    tmem_st_16x32(part16 + o_cols + 32 * k, x);
                                 }
                                 tmem_st_wait();
                             }
                         }
-                        const float base = m == -INFINITY ? 0.f : m;
+                        const float base0 = m[0] == -INFINITY ? 0.f : m[0], base1 = m[1] == -INFINITY ? 0.f : m[1];
                         float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                        for (int b = 0; b < NC / 16; ++b) {
-                            const float off = lv[b] - base;
+                        for (int b = 0; b < 4; ++b)
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                fma2(s[16 * b + 2 * c], s[16 * b + 2 * c + 1], f[b], off);
-                                top[c & 1] = fmaxf(top[c & 1], fmaxf(s[16 * b + 2 * c], s[16 * b + 2 * c + 1]));
+                            for (int k = 0; k < 2; ++k) {
+                                float *x = s + 8 * b + 2 * k;
+                                const float f = (k ? f1 : f0) * ksc[b], off = lvs[b] - (k ? base1 : base0);
+                                fma2(x[0], x[1], f, off);
+                                fma2(x[4], x[5], f, off);
+                                top[k] = fmaxf(top[k], fmaxf(fmaxf(x[0], x[1]), fmaxf(x[4], x[5])));
                             }
-                        }
-                        bool over = !raised && __any_sync(0xffffffffu, fmaxf(top[0], top[1]) > (m == -INFINITY ? m : 15.f));
-                        if (CS == 2 && !raised) {
-                            if (lane == 0) sm.over[pair_phase & 1][part_of][quadrant] = over;
-                            come();
-                        }
-                        uint32_t x[NC / 2];
-                        float add = 0.f;
-#pragma unroll
-                        for (int b = 0; b < NC / 16; ++b) {
-                            float sum[2] = {0.f, 0.f};
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                const float e0 = exp2_fast(s[16 * b + 2 * c]), e1 = exp2_fast(s[16 * b + 2 * c + 1]);
-                                add2(sum[0], sum[1], e0, e1);
-                                const __half2 hh = __floats2half2_rn(e0, e1);
-                                x[8 * b + c] = *reinterpret_cast<const uint32_t *>(&hh);
-                            }
-                            sum[0] += sum[1];
-                            // a block that no row sees may have any scale
-                            if (sum[0] != 0.f) add = fmaf(sum[0], sm.scale[slot][8 + part_of * (NC / 16) + b], add);
-                        }
-                        if (CS == 2 && !raised) {
-                            const int turn = pair_phase & 1;
-                            if (!(ok = meet())) break;   // both have read their scores too, so weights may overwrite them
-                            over |= sm.over[turn][CS - 1 - part_of][quadrant];
-                        }
-                        if (over) {
+                        if (!raise && __any_sync(0xffffffffu, top[0] > (m[0] == -INFINITY ? m[0] : 15.f) || top[1] > (m[1] == -INFINITY ? m[1] : 15.f))) {
                             raise = true;
                             continue;
                         }
-                        l += add;
-                        if constexpr (CS == 2) tmem_st16(s_tm + part_of * 16, x);
-                        else tmem_st32(s_tm, x);
+                        raise = false;
+                        const float4 rvv = *reinterpret_cast<const float4 *>(scale + 8);
+                        const float rv[4] = {rvv.x, rvv.y, rvv.z, rvv.w};
+                        uint32_t x[16];      // of 8 tokens i: row 0, row 1
+#pragma unroll
+                        for (int b = 0; b < 4; ++b)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                float sum[2] = {0.f, 0.f};
+#pragma unroll
+                                for (int i = 0; i < 2; ++i) {
+                                    const float e0 = exp2_fast(s[8 * b + 4 * i + 2 * k]), e1 = exp2_fast(s[8 * b + 4 * i + 2 * k + 1]);
+                                    add2(sum[0], sum[1], e0, e1);
+                                    const __half2 hh = __floats2half2_rn(e0, e1);
+                                    x[2 * (2 * b + i) + k] = *reinterpret_cast<const uint32_t *>(&hh);
+                                }
+                                sum[0] += sum[1];
+                                // a block that the row does not see may have any scale
+                                if (sum[0] != 0.f) l[k] = fmaf(sum[0], rv[b], l[k]);
+                            }
+                        tmem_st_16x32b(s_tm, x);
                         break;
                     }
-                    if (!ok) break;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.sc_empty[slot]);
                     tmem_st_wait();
                     tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.p_full[q][buf]);
-                    if (++buf == SB) buf = 0, buf_phase ^= 1;
-                    if (++slot == kScaleSlots) slot = 0, slot_phase ^= 1;
-                    ++u;
-                    if (ends || u == units) break;
-                    w.next();
+                    arrive(&sm.p_full[q][buf]);
+                    if (++buf == SB) buf = 0, phase ^= 1;
                 }
-                if (!ok) break;
-                // ---- the segment's end
-                if (!(ok = wait(&sm.pv_done[q], u - 1))) break;
+                // ---- the segment's end: sums over the rows' lanes, then thread = row and every second 32 columns of O
+                const bool whole = begun && w.j == w.tiles;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
+                    l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
+                    if (t == 0) {
+                        sm.row_m[row0 + 8 * k] = m[k];
+                        sm.row_l[row0 + 8 * k] = l[k];
+                    }
+                }
+                named_barrier(1 + 4 * q + quadrant, 64);       // the quadrant's two warps
+                wait(&sm.pv_done[q], u_end - 1);
                 tc_fence_after();
-                if (CS == 2) {
-                    sm.pair_sum[part_of][row] = l;
-                    come();
-                    if (!(ok = meet())) break;
-                    l += sm.pair_sum[CS - 1 - part_of][row];
-                }
-                const bool whole = begun && ends;
-                float *part = plan.parts + (size_t)(2 * cta + seg_slot) * (ROWS * D + 2 * ROWS) + (size_t)(q * 128 + row) * D;
-                const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+                const int row = 128 * q + 32 * quadrant + lane, grow = w.mt * ROWS + row, i = grow / group;
+                const bool valid = i < w.s.qlen;
+                const float sum = sm.row_l[row], inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+                const size_t out_row = ((size_t)(w.s.q0 + (valid ? i : 0)) * p.hq + w.h * group + grow % group) * D;
+                float *part = plan.parts + (size_t)(2 * cta + seg_slot) * (ROWS * D + 2 * ROWS);
 #pragma unroll 1
-                for (int k = part_of; k < D / 32; k += CS) {
+                for (int k = half; k < D / 32; k += 2) {
                     float o[32];
-                    tmem_ld32(o_at + 32 * k, o);
+                    tmem_ld32(quad + o_cols + 32 * k, o);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] *= inv;
                     if (valid && whole) {
                         store_row<32>(p, out_row + 32 * k, o);
                     } else if (valid) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4 *>(part + 32 * k + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4 *>(part + (size_t)row * D + 32 * k + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                     }
                     __syncwarp();   // the next load is warp-wide
                 }
-                if (!whole && part_of == 0) {
-                    float *ml = plan.parts + (size_t)(2 * cta + seg_slot) * (ROWS * D + 2 * ROWS) + ROWS * D;
-                    ml[q * 128 + row] = m;
-                    ml[ROWS + q * 128 + row] = l;
+                if (!whole && half == 0) {
+                    part[ROWS * D + row] = sm.row_m[row];
+                    part[ROWS * D + ROWS + row] = sum;
                 }
                 tc_fence_before();
-                if (begun && !ends) {
-                    const long long left = (long long)w.tiles - 1 - w.j;
+                named_barrier(1 + 4 * q + quadrant, 64);       // row_m and row_l are free again
+                if (begun && !whole) {
+                    const long long left = (long long)w.tiles - w.j;
                     mm.first = cta;
                     mm.slot = seg_slot;
                     mm.last = cta + (int)((left + per - 1) / per);
@@ -510,14 +472,17 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                     mm.h = w.h;
                     mm.mt = w.mt;
                 }
-                if (u < units) w.next();
+                if (u < units) w.next_item();
             }
         }
         if (tid == 0) plan.meta[cta] = mm;
-    } else if (warp < L::SOFTMAX_WARPS + kLoaderWarps) {
-        set_max_registers_down<L::REGS_LOADER>();
+    } else if (warp < L::SOFTMAX_WARPS + L::LOADER_WARPS) {
+        set_max_registers<L::REGS_LOADER, L::REGS_LAUNCH>();
         // ------------------------------------------------------------------------------------------ loaders
-        const int lw = warp - L::SOFTMAX_WARPS;                        // rows 8 lw .. 8 lw + 7 of a tile
+        // At d = 256 two groups of 8 warps take the load tiles in turn, so that two tiles' codes are on their way at a time:
+        // their latency is longer than one tile's products.  (Two tiles in one group's registers were not faster.)
+        constexpr int LU = L::LU, CH = D / 64;
+        const int lg = (warp - L::SOFTMAX_WARPS) / 8, lw = (warp - L::SOFTMAX_WARPS) % 8;   // rows 8 lw .. 8 lw + 7 of every unit
         // 4 lanes take the 64 codes of a column chunk of one row.  The 8 lanes that store together hold rows that
         // differ in the two low bits, so that their pieces fall on different banks in both tiles' orders.
         const int r = 8 * lw + ((lane >> 4) << 2) + ((((lane >> 2) & 1) * 3) ^ ((lane >> 3) & 1)), c16 = lane & 3;
@@ -525,136 +490,169 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
         // K's columns stand in the order in which a query row's 32-element pieces enter TMEM: components 8 t + 0..3
         // at 4 t, components 8 t + 4..7 at 16 + 4 t (t = 0..3)
         const uint32_t k_lo = sw128_offset(r, 32 * (c16 >> 1) + 8 * (c16 & 1)), k_hi = sw128_offset(r, 32 * (c16 >> 1) + 16 + 8 * (c16 & 1));
+        // lanes 0 and 1 of the even warps, which stand in their block's first row, bring its K and its V scale
+        const bool scaler = (lw & 1) == 0 && lane < 2;
+        auto wait = [&](uint64_t *bar, int phase) {
+            if (lw == 0) poll(bar, phase);
+            named_barrier(1 + 4 * NQ + lg, 256);
+        };
         if (units > 0) {
             Walk<ROWS> w(p, plan, group);
-            uint4 kr[D / 64], vr[D / 64];
-            int page = -1, in_page = 0, head = 0;   // of this thread's row in the unit that `w` is at; -1: no such token
+            // where the next tile begins: unit u; it holds `held` units, of one item
+            int u = 0, held = min(min(LU, w.tiles - w.j), units);
+            auto skip = [&]() {
+                u += held;
+                if (u >= units) return;
+                w.j += held;
+                if (w.j == w.tiles) w.next_item();
+                held = min(min(LU, w.tiles - w.j), units - u);
+            };
+            int page[LU], in_page[LU], head = 0;   // of this thread's rows in the tile that `w` is at; -1: no such token
             auto look_up = [&]() {
-                const int tok = w.token() + r;
                 head = w.h;
-                page = -1;
-                if (tok >= w.s.kvlen) return;
-                const int at = p.pool.page_of(tok);
-                in_page = tok - at * p.pool.page_size;
-                page = __ldg(p.pool.table + (size_t)w.n * p.pool.max_pages + at);
-                if ((unsigned)page >= (unsigned)p.pool.n_pages) page = -2;
-            };
-            auto row_offset = [&]() -> long long {                     // byte offset of that row, or -1
-                if (page == -2) raise_error(p.err, kErrInternal);
-                return page < 0 ? -1 : ((long long)(page * p.pool.hkv + head) * p.pool.page_size + in_page) * D + 16 * c16;
-            };
-            auto fetch = [&](const uint8_t *pages, long long off, uint4 (&x)[D / 64]) {
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                    x[c] = off >= 0 ? __ldg(reinterpret_cast<const uint4 *>(pages + off + 64 * c)) : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < LU; ++i) {
+                    page[i] = -1;
+                    const int tok = i < held ? w.it.token(w.j + i, kTile) + r : 0;
+                    if (i >= held || tok >= w.s.kvlen) continue;
+                    const int at = p.pool.page_of(tok);
+                    in_page[i] = tok - at * p.pool.page_size;
+                    page[i] = __ldg(p.pool.table + (size_t)w.n * p.pool.max_pages + at);
+                    if ((unsigned)page[i] >= (unsigned)p.pool.n_pages) page[i] = -2;
+                }
             };
-            auto put = [&](uint8_t *tile, const uint4 (&x)[D / 64], uint32_t lo, uint32_t hi, bool keys) {
+            auto fetch = [&](const uint8_t *pages, const int (&row)[LU], uint4 (&x)[LU * CH]) {
+#pragma unroll
+                for (int i = 0; i < LU; ++i)
+#pragma unroll
+                    for (int c = 0; c < CH; ++c)
+                        x[i * CH + c] = row[i] >= 0 ? __ldg(reinterpret_cast<const uint4 *>(pages + (size_t)row[i] * D + 16 * c16 + 64 * c))
+                                                    : make_uint4(0, 0, 0, 0);
+            };
+            auto put = [&](uint8_t *tile, const uint4 (&x)[LU * CH], uint32_t lo, uint32_t hi, bool keys) {
                 const uint32_t at = smem_u32(tile);
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    uint32_t y[8];
-                    codes_to_f16x2<FMT>(x[c].x, y[0], y[1]);
-                    codes_to_f16x2<FMT>(keys ? x[c].z : x[c].y, y[2], y[3]);
-                    codes_to_f16x2<FMT>(keys ? x[c].y : x[c].z, y[4], y[5]);
-                    codes_to_f16x2<FMT>(x[c].w, y[6], y[7]);
-                    const uint32_t a = at + c * (kTile * 128);
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a + lo), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
-                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a + hi), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7]) : "memory");
-                }
+                for (int i = 0; i < LU; ++i)
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) {
+                        const uint4 z = x[i * CH + c];
+                        uint32_t y[8];
+                        codes_to_f16x2<FMT>(z.x, y[0], y[1]);
+                        codes_to_f16x2<FMT>(keys ? z.z : z.y, y[2], y[3]);
+                        codes_to_f16x2<FMT>(keys ? z.y : z.z, y[4], y[5]);
+                        codes_to_f16x2<FMT>(z.w, y[6], y[7]);
+                        const uint32_t a = at + c * L::CHUNK + i * (kTile * 128);
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a + lo), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a + hi), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7]) : "memory");
+                    }
                 fence_proxy_async_smem();
-                __syncwarp();
             };
-            // codes are a unit ahead of their conversion, the table's entry another unit ahead
-            look_up();
-            long long off = row_offset();
-            fetch(p.k_pages, off, kr);
-            fetch(p.v_pages, off, vr);
-            if (units > 1) {
-                w.next();
-                look_up();
+            int tile = 0;                          // of this group: lg, lg + 2, ...
+            if (lg == 1) {
+                skip();
+                tile = 1;
             }
-            for (int u = 0; u < units; ++u) {
-                const int st = u % kStages, ph = u / kStages;
-                off = row_offset();
-                if (u + 2 < units) {
-                    w.next();
-                    look_up();
+            look_up();
+            while (u < units) {
+                // this tile's codes and scales are asked for, then the table's entries of the group's next one
+                const int u_now = u, held_now = held, st = tile % kStages, ph = tile / kStages + 1;
+                int row[LU];
+                uint4 kr[LU * CH], vr[LU * CH];
+                float scale[LU];
+#pragma unroll
+                for (int i = 0; i < LU; ++i) {
+                    if (page[i] == -2) raise_error(p.err, kErrInternal);
+                    row[i] = page[i] < 0 ? -1 : (page[i] * p.pool.hkv + head) * p.pool.page_size + in_page[i];
+                    scale[i] = scaler && row[i] >= 0 ? __ldg((lane == 0 ? p.k_scales : p.v_scales) + row[i] / kKvBlock) : 0.f;
                 }
-                if (!wait(&sm.k_empty[st], ph + 1)) break;
+                fetch(p.k_pages, row, kr);
+                fetch(p.v_pages, row, vr);
+#pragma unroll
+                for (int i = 0; i < L::LG; ++i)
+                    if (u < units) skip();
+                if (u < units) look_up();
+                tile += L::LG;
+                wait(&sm.k_empty[st], ph);
+                if (scaler) {
+#pragma unroll
+                    for (int i = 0; i < LU; ++i) {
+                        if (i >= held_now) break;
+                        float *slot = sm.scale[(u_now + i) % kScaleSlots] + lw / 2;
+                        if (lane == 0) {
+                            slot[0] = scale[i];
+                        } else {
+                            const float x = scale[i] == 0.f ? kAmaxFloor : scale[i];
+                            slot[4] = log2f(x);
+                            slot[8] = 1.f / x;
+                        }
+                    }
+                }
                 put(sm.k[st], kr, k_lo, k_hi, true);
-                if (lane == 0) mbar_arrive(&sm.k_full[st]);
-                if (u + 1 < units) fetch(p.k_pages, off, kr);
-                if (!wait(&sm.v_empty[st], ph + 1)) break;
+                arrive(&sm.k_full[st]);
+                wait(&sm.v_empty[st], ph);
                 put(sm.v[st], vr, v_lo, v_hi, false);
-                if (lane == 0) mbar_arrive(&sm.v_full[st]);
-                if (u + 1 < units) fetch(p.v_pages, off, vr);
+                arrive(&sm.v_full[st]);
             }
         }
     } else {
-        set_max_registers_down<L::REGS_OTHER>();
-        const int role = warp - L::SOFTMAX_WARPS - kLoaderWarps;
+        set_max_registers<L::REGS_OTHER, L::REGS_LAUNCH>();
+        const int role = warp - L::SOFTMAX_WARPS - L::LOADER_WARPS;
         // ------------------------------------------------------------------------------------------ MMA
-        if (role == 0 && units > 0 && elect_one()) {
-            // Only the ends of the items matter here: units left of this one, the next one's read ahead.
+        // Two warps, each with one thread that issues: the issue of an MMA blocks while the few before it run, so one
+        // thread for both products leaves the tensor pipe idle during each of its waits.  Of the items only their ends
+        // matter here: units left of this one, the next one's read ahead.
+        if (role < 2 && units > 0 && elect_one()) {
             int item = plan.start[cta].item, left = plan.items[item].w - plan.start[cta].j, next_left = 0;
             if (left < units) next_left = plan.items[item + 1].w;
-            constexpr uint32_t id_s = idesc_f16_f32(128, kTile, false, false), id_o = idesc_f16_f32(128, D, false, true);
-            const uint64_t kd0 = smem_desc(smem_u32(sm.k[0]), 16, 1024, kLayoutSwizzle128B);
-            const uint64_t vd0 = smem_desc(smem_u32(sm.v[0]), kTile * 128, 1024, kLayoutSwizzle128B);
-            constexpr uint32_t kStep = L::TILE_BYTES >> 4;
-            auto scores = [&](int q, int stage, int buf) {     // S = Q K^T
-                const uint64_t kd = kd0 + stage * kStep;
-                const uint32_t d = tmem + L::S + (q * SB + buf) * 64, a = tmem + L::Q + q * (D / 2);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) mma_tmem_a(d, a + 8 * k, kd + ((k >> 2) * (kTile * 128) >> 4) + 2 * (k & 3), id_s, k > 0);
-                mma_commit(&sm.s_full[q][buf]);
-            };
-            auto outputs = [&](int q, int stage, int buf, bool first) {   // O += W V
-                const uint64_t vd = vd0 + stage * kStep;
-                const uint32_t a = tmem + L::S + (q * SB + buf) * 64;
-#pragma unroll
-                for (int k = 0; k < kTile / 16; ++k) mma_tmem_a(tmem + L::O + q * D, a + 8 * k, vd + 128 * k, id_o, !(first && k == 0));
-                mma_commit(&sm.pv_done[q]);
-            };
-            int st = 0, ph = 0, buf = 0, buf_phase = 0, seg = 0;   // of unit u
+            int st = 0, ph = 0, sub = 0, buf = 0, buf_phase = 0, seg = 0;   // of unit u: its load tile's stage, its place there
             bool first = true;
             for (int u = 0; u < units; ++u) {
-                if (first) {
-                    bool ok = true;
-                    for (int q = 0; q < NQ; ++q) ok = ok && wait_one(&sm.q_full[q], seg);
-                    if (!ok || !wait_one(&sm.k_full[st], ph)) break;
-                    tc_fence_after();
-                    for (int q = 0; q < NQ; ++q) scores(q, st, buf);
-                    mma_commit(&sm.k_empty[st]);
-                }
-                const bool ends = left == 1 || u == units - 1;
-                const int nst = st + 1 == kStages ? 0 : st + 1, nph = nst == 0 ? ph ^ 1 : ph;
-                const int nbuf = SB == 2 ? buf ^ 1 : 0, nbuf_phase = nbuf == 0 ? buf_phase ^ 1 : buf_phase;
-                if (!ends) {
-                    if (!wait_one(&sm.k_full[nst], nph)) break;
-                    tc_fence_after();
-                    if (SB == 2) {
-                        for (int q = 0; q < NQ; ++q) scores(q, nst, nbuf);
-                        mma_commit(&sm.k_empty[nst]);
+                const bool ends = left == 1, tile_ends = ends || sub == L::LU - 1 || u == units - 1;
+                if (role == 0) {
+                    // S = Q K^T.  A buffer is free once the output product has read the weights that took its place.
+                    if (sub == 0) poll(&sm.k_full[st], ph);
+                    constexpr uint32_t id = idesc_f16_f32(128, kTile, false, false);
+                    const uint64_t kd = smem_desc(smem_u32(sm.k[0]), 16, 1024, kLayoutSwizzle128B) +
+                                        ((st * L::TILE_BYTES + sub * (kTile * 128)) >> 4);
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) {
+                        if (first) poll(&sm.q_full[q], seg);
+                        poll(&sm.s_free[q][buf], buf_phase ^ 1);
+                        tc_fence_after();
+                        const uint32_t d = tmem + L::S + (q * SB + buf) * 64, a = tmem + L::Q + q * (D / 2);
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) mma_tmem_a(d, a + 8 * k, kd + ((k >> 2) * L::CHUNK >> 4) + 2 * (k & 3), id, k > 0);
+                        mma_commit(&sm.s_full[q][buf]);
+                        mbar_arrive(&sm.s_full[q][buf]);   // the block scales, which this thread has waited for, are visible too
                     }
+                    if (tile_ends) mma_commit(&sm.k_empty[st]);
+                } else {
+                    // O += W V, from 0 at an item's first unit in this run
+                    if (sub == 0) poll(&sm.v_full[st], ph);
+                    constexpr uint32_t id = idesc_f16_f32(128, D, false, true);
+                    const uint64_t vd = smem_desc(smem_u32(sm.v[0]), L::CHUNK, 1024, kLayoutSwizzle128B) +
+                                        ((st * L::TILE_BYTES + sub * (kTile * 128)) >> 4);
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) {
+                        poll(&sm.p_full[q][buf], buf_phase);
+                        tc_fence_after();
+                        const uint32_t a = tmem + L::S + (q * SB + buf) * 64;
+#pragma unroll
+                        for (int k = 0; k < kTile / 16; ++k) mma_tmem_a(tmem + L::O + q * D, a + 8 * k, vd + 128 * k, id, !(first && k == 0));
+                        mma_commit(&sm.s_free[q][buf]);
+                        mma_commit(&sm.pv_done[q]);
+                    }
+                    if (tile_ends) mma_commit(&sm.v_empty[st]);
                 }
-                if (!wait_one(&sm.v_full[st], ph)) break;
-                bool ok = true;
-                for (int q = 0; q < NQ; ++q) {
-                    if (!(ok = wait_one(&sm.p_full[q][buf], buf_phase))) break;
-                    tc_fence_after();
-                    outputs(q, st, buf, first);
-                    if (SB == 1 && !ends) scores(q, nst, nbuf);
+                ++sub;
+                if (tile_ends) {
+                    sub = 0;
+                    if (++st == kStages) st = 0, ph ^= 1;
                 }
-                if (!ok) break;
-                mma_commit(&sm.v_empty[st]);
-                if (SB == 1 && !ends) mma_commit(&sm.k_empty[nst]);
-                st = nst;
-                ph = nph;
-                buf = nbuf;
-                buf_phase = nbuf_phase;
+                if (++buf == SB) buf = 0, buf_phase ^= 1;
                 first = ends;
-                if (--left == 0) {
+                --left;
+                if (ends) {
                     ++seg;
                     ++item;
                     left = next_left;
@@ -662,54 +660,8 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                 }
             }
             // every MMA has finished before the tensor memory is given back
-            mma_commit(&sm.drain);
-            if (!mbar_wait(&sm.drain, 0)) raise_error(p.err, kErrTimeout);
-        }
-        // ------------------------------------------------------------------------------------------ scales
-        if (role == 1 && units > 0) {
-            Walk<ROWS> w(p, plan, group);
-            // lanes 0..3 hold the unit's K scales, 4..7 its V scales: read a unit ahead, the table another one
-            const float *scales = lane < 4 ? p.k_scales : p.v_scales;
-            int page = -1, block = 0, head = 0;
-            auto look_up = [&]() {
-                const int tok = w.token() + (lane & 3) * kKvBlock;
-                head = w.h;
-                page = -1;
-                if (lane >= 8 || tok >= w.s.kvlen) return;
-                const int at = p.pool.page_of(tok);
-                block = (tok - at * p.pool.page_size) / kKvBlock;
-                page = __ldg(p.pool.table + (size_t)w.n * p.pool.max_pages + at);
-            };
-            auto fetch = [&]() {
-                return (unsigned)page < (unsigned)p.pool.n_pages
-                           ? __ldg(scales + ((size_t)page * p.pool.hkv + head) * (p.pool.page_size / kKvBlock) + block)
-                           : 0.f;
-            };
-            look_up();
-            float x = fetch();
-            if (units > 1) {
-                w.next();
-                look_up();
-            }
-            for (int u = 0; u < units; ++u) {
-                const int slot = u % kScaleSlots;
-                const float next = u + 1 < units ? fetch() : 0.f;
-                if (u + 2 < units) {
-                    w.next();
-                    look_up();
-                }
-                if (!wait(&sm.sc_empty[slot], u / kScaleSlots + 1)) break;
-                if (lane < 4) {
-                    sm.scale[slot][lane] = x;
-                } else if (lane < 8) {
-                    if (x == 0.f) x = kAmaxFloor;
-                    sm.scale[slot][lane] = log2f(x);
-                    sm.scale[slot][lane + 4] = 1.f / x;
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.sc_full[slot]);
-                x = next;
-            }
+            mma_commit(&sm.drain[role]);
+            if (!mbar_wait(&sm.drain[role], 0)) raise_error(p.err, kErrTimeout);
         }
     }
     __syncthreads();
@@ -728,7 +680,7 @@ struct TcSizes {
 // Workspace layout; `sms` bounds the CTAs (the size is asked for with the largest).
 TcSizes tc_sizes(int n_seqs, int total, int hq, int hkv, int d, int sms) {
     TcSizes z;
-    const int rows = d == 256 ? 128 : 256;
+    const int rows = d == 256 ? Tc<256>::ROWS : Tc<128>::ROWS;
     z.items = hkv * (((long long)total * (hq / hkv) + rows - 1) / rows + n_seqs);
     z.ctas = min(sms, kMaxTcCtas);
     z.start = round256(kMaxTcCtas * sizeof(MergeMeta));
@@ -741,7 +693,6 @@ TcSizes tc_sizes(int n_seqs, int total, int hq, int hkv, int d, int sms) {
 
 template <int D, int FMT>
 cudaError_t launch_tc(const AttendProblem &p) {
-    using L = Tc<D>;
     const TcSizes z = tc_sizes(p.n_seqs, p.total, p.hq, p.pool.hkv, D, multiprocessor_count());
     uint8_t *ws = static_cast<uint8_t *>(p.workspace);
     TcPlan plan{};
@@ -761,9 +712,10 @@ cudaError_t launch_tc(const AttendProblem &p) {
         if (e != cudaSuccess) return e;
         if (dev < kMaxDevices) ready[dev].store(true, std::memory_order_relaxed);
     }
+    using L = Tc<D>;
     attend_plan_kernel<L::ROWS><<<1, kPlanThreads, 0, p.stream>>>(p, plan);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = launch_after(p.stream, dim3((unsigned)z.ctas), L::THREADS, smem, attend_tc_kernel<D, FMT>, p, plan)) != cudaSuccess) return e;
+    if ((e = launch_after(p.stream, dim3((unsigned)z.ctas), Tc<D>::THREADS, smem, attend_tc_kernel<D, FMT>, p, plan)) != cudaSuccess) return e;
     return launch_after(p.stream, dim3((unsigned)z.ctas, L::ROWS / 8), 256, 0, attend_join_kernel<D, L::ROWS>, p,
                         static_cast<const MergeMeta *>(plan.meta), static_cast<const float *>(plan.parts));
 }
