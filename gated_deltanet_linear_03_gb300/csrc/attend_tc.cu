@@ -59,7 +59,7 @@ struct __align__(1024) TcSmem {
     float scale[kScaleSlots][12];        // K scales, log2 of V scales, reciprocals of V scales
     float row_m[Tc<D>::ROWS], row_l[Tc<D>::ROWS];   // at an item's end
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-    uint64_t s_full[NQ][2], s_free[NQ][2], p_full[NQ][2], pv_done[NQ], q_full[NQ], drain[2];
+    uint64_t s_full[NQ][2], s_free[NQ][2], p_full[NQ][2], q_full[NQ], drain[2];
     uint32_t tmem;
     int abort;
 };
@@ -165,6 +165,11 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
     for (long long r = (total + per - 1) / per + tid; r <= plan.ctas; r += kPlanThreads) plan.start[r] = {0, 0, total - (long long)items * kItemCost};
 }
 
+template <bool V>
+struct Flag {
+    static constexpr bool value = V;
+};
+
 // Where a role stands in its CTA's run; every role keeps its own.
 template <int ROWS>
 struct Walk {
@@ -224,7 +229,6 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                 mbar_init(&sm.s_free[q][b], 1);
                 mbar_init(&sm.p_full[q][b], 8);
             }
-            mbar_init(&sm.pv_done[q], 1);
             mbar_init(&sm.q_full[q], 8);
         }
         mbar_init(&sm.drain[0], 1);
@@ -318,11 +322,12 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                 arrive(&sm.q_full[q]);              // also: this warp has read its part of the item before
                 float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
                 bool raise = true;                  // the item's first unit sets M
+                // units before this one are seen by every row as a whole
+                const int seen_to = p.window == 0 ? (w.it.lo_pos + 1) / kTile : 0;
                 for (; u < u_end; ++u, ++w.j) {
                     // ---- one unit
                     const uint32_t s_tm = s_at + buf * 64;
-                    const int tok0 = w.token();
-                    const bool all_seen = w.it.all_seen(tok0, tok0 + kTile, p.window, p.sinks);
+                    const bool all_seen = w.j < seen_to || (p.window != 0 && w.it.all_seen(w.token(), w.token() + kTile, p.window, p.sinks));
                     const float *scale = sm.scale[u % kScaleSlots];
                     wait(&sm.s_full[q][buf], phase);
                     tc_fence_after();
@@ -331,30 +336,27 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                         // scores of row k at tokens 8 i + 2 t, + 1: s[4 i + 2 k], + 1
                         float s[32];
                         tmem_ld_16x64(s_tm, s);
-                        float4 ks = *reinterpret_cast<const float4 *>(scale), lv = *reinterpret_cast<const float4 *>(scale + 4);
-                        float ksc[4] = {ks.x, ks.y, ks.z, ks.w}, lvs[4] = {lv.x, lv.y, lv.z, lv.w};
-                        float f0 = rs[0], f1 = rs[1];
+                        const float4 ks = *reinterpret_cast<const float4 *>(scale), lv = *reinterpret_cast<const float4 *>(scale + 4);
+                        const float ksc[4] = {ks.x, ks.y, ks.z, ks.w}, lvs[4] = {lv.x, lv.y, lv.z, lv.w};
                         if (!all_seen) {
+                            // a score that the row does not see becomes -infinity
+                            const int tok0 = w.token();
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
-                                    s[4 * i + e] = sees(pos[e / 2], tok0 + 8 * i + 2 * t + (e & 1), p.window, p.sinks)
-                                                       ? fmaf(s[4 * i + e], rs[e / 2] * ksc[i / 2], lvs[i / 2]) : -INFINITY;
-                            f0 = f1 = 1.f;
-#pragma unroll
-                            for (int b = 0; b < 4; ++b) ksc[b] = 1.f, lvs[b] = 0.f;
+                                    if (!sees(pos[e / 2], tok0 + 8 * i + 2 * t + (e & 1), p.window, p.sinks)) s[4 * i + e] = -INFINITY;
                         }
                         if (raise) {
-                            float top[2] = {-INFINITY, -INFINITY};
+                            float top[2] = {-INFINITY, -INFINITY}, c[2];
 #pragma unroll
                             for (int b = 0; b < 4; ++b)
 #pragma unroll
                                 for (int k = 0; k < 2; ++k) {
                                     const float *x = s + 8 * b + 2 * k;
-                                    top[k] = fmaxf(top[k], fmaf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[4], x[5])), (k ? f1 : f0) * ksc[b], lvs[b]));
+                                    const float y = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[4], x[5]));
+                                    top[k] = fmaxf(top[k], y == -INFINITY ? y : fmaf(y, rs[k] * ksc[b], lvs[b]));
                                 }
-                            float c[2];
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
                                 top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 1));
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                                 l[k] *= c[k];
                             }
                             if (!first) {
-                                wait(&sm.pv_done[q], u - 1);
+                                wait(&sm.s_free[q][(u - 1) % SB], (u - 1) / SB);     // the output product of the unit before
                                 tc_fence_after();
 #pragma unroll 1
                                 for (int k = 0; k < D / 32; ++k) {
@@ -379,42 +381,59 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                                 tmem_st_wait();
                             }
                         }
-                        const float base0 = m[0] == -INFINITY ? 0.f : m[0], base1 = m[1] == -INFINITY ? 0.f : m[1];
-                        float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                        for (int b = 0; b < 4; ++b)
+                        uint32_t x[16];      // of 8 tokens i: row 0, row 1
+                        float sum[2][4];     // of row k's four blocks
+                        auto weigh = [&](auto masked) {
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
-                                float *x = s + 8 * b + 2 * k;
-                                const float f = (k ? f1 : f0) * ksc[b], off = lvs[b] - (k ? base1 : base0);
-                                fma2(x[0], x[1], f, off);
-                                fma2(x[4], x[5], f, off);
-                                top[k] = fmaxf(top[k], fmaxf(fmaxf(x[0], x[1]), fmaxf(x[4], x[5])));
+                                const float base = m[k] == -INFINITY ? 0.f : m[k];
+#pragma unroll
+                                for (int b = 0; b < 4; ++b) {
+                                    const float f = rs[k] * ksc[b], off = lvs[b] - base;
+                                    float part[2];
+#pragma unroll
+                                    for (int i = 0; i < 2; ++i) {
+                                        const float s0 = s[8 * b + 4 * i + 2 * k], s1 = s[8 * b + 4 * i + 2 * k + 1];
+                                        float e0 = s0, e1 = s1;
+                                        fma2(e0, e1, f, off);
+                                        e0 = exp2_fast(e0);
+                                        e1 = exp2_fast(e1);
+                                        if (masked.value) {     // whatever the block's scales are
+                                            if (s0 == -INFINITY) e0 = 0.f;
+                                            if (s1 == -INFINITY) e1 = 0.f;
+                                        }
+                                        if (i == 0) part[0] = e0, part[1] = e1;
+                                        else add2(part[0], part[1], e0, e1);
+                                        const __half2 hh = __floats2half2_rn(e0, e1);
+                                        x[2 * (2 * b + i) + k] = *reinterpret_cast<const uint32_t *>(&hh);
+                                    }
+                                    sum[k][b] = part[0] + part[1];
+                                }
                             }
-                        if (!raise && __any_sync(0xffffffffu, top[0] > (m[0] == -INFINITY ? m[0] : 15.f) || top[1] > (m[1] == -INFINITY ? m[1] : 15.f))) {
+                        };
+                        if (all_seen) weigh(Flag<false>());
+                        else weigh(Flag<true>());
+                        const float4 rvv = *reinterpret_cast<const float4 *>(scale + 8);
+                        float add[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) add[k] = (sum[k][0] + sum[k][1]) + (sum[k][2] + sum[k][3]);
+                        // a weight above 2^15 makes its sum so too; a row that saw nothing so far takes its M from any weight
+                        if (!raise && __any_sync(0xffffffffu, add[0] > (m[0] == -INFINITY ? 0.f : 32768.f) || add[1] > (m[1] == -INFINITY ? 0.f : 32768.f))) {
                             raise = true;
                             continue;
                         }
                         raise = false;
-                        const float4 rvv = *reinterpret_cast<const float4 *>(scale + 8);
-                        const float rv[4] = {rvv.x, rvv.y, rvv.z, rvv.w};
-                        uint32_t x[16];      // of 8 tokens i: row 0, row 1
 #pragma unroll
-                        for (int b = 0; b < 4; ++b)
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                float sum[2] = {0.f, 0.f};
-#pragma unroll
-                                for (int i = 0; i < 2; ++i) {
-                                    const float e0 = exp2_fast(s[8 * b + 4 * i + 2 * k]), e1 = exp2_fast(s[8 * b + 4 * i + 2 * k + 1]);
-                                    add2(sum[0], sum[1], e0, e1);
-                                    const __half2 hh = __floats2half2_rn(e0, e1);
-                                    x[2 * (2 * b + i) + k] = *reinterpret_cast<const uint32_t *>(&hh);
-                                }
-                                sum[0] += sum[1];
-                                // a block that the row does not see may have any scale
-                                if (sum[0] != 0.f) l[k] = fmaf(sum[0], rv[b], l[k]);
+                        for (int k = 0; k < 2; ++k) {
+                            if (all_seen) {
+                                l[k] += sum[k][0] * rvv.x + sum[k][1] * rvv.y + sum[k][2] * rvv.z + sum[k][3] * rvv.w;
+                            } else {
+                                if (sum[k][0] != 0.f) l[k] = fmaf(sum[k][0], rvv.x, l[k]);
+                                if (sum[k][1] != 0.f) l[k] = fmaf(sum[k][1], rvv.y, l[k]);
+                                if (sum[k][2] != 0.f) l[k] = fmaf(sum[k][2], rvv.z, l[k]);
+                                if (sum[k][3] != 0.f) l[k] = fmaf(sum[k][3], rvv.w, l[k]);
                             }
+                        }
                         tmem_st_16x32b(s_tm, x);
                         break;
                     }
@@ -435,7 +454,9 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                     }
                 }
                 named_barrier(1 + 4 * q + quadrant, 64);       // the quadrant's two warps
-                wait(&sm.pv_done[q], u_end - 1);
+                // The last output product (a barrier for all units in turn would not do here: it may be two phases behind, which
+                // looks like one ahead)
+                wait(&sm.s_free[q][(u_end - 1) % SB], (u_end - 1) / SB);
                 tc_fence_after();
                 const int row = 128 * q + 32 * quadrant + lane, grow = w.mt * ROWS + row, i = grow / group;
                 const bool valid = i < w.s.qlen;
@@ -526,8 +547,7 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                 for (int i = 0; i < LU; ++i)
 #pragma unroll
                     for (int c = 0; c < CH; ++c)
-                        x[i * CH + c] = row[i] >= 0 ? __ldg(reinterpret_cast<const uint4 *>(pages + (size_t)row[i] * D + 16 * c16 + 64 * c))
-                                                    : make_uint4(0, 0, 0, 0);
+                        x[i * CH + c] = __ldg(reinterpret_cast<const uint4 *>(pages + (size_t)max(row[i], 0) * D + 16 * c16 + 64 * c));
             };
             auto put = [&](uint8_t *tile, const uint4 (&x)[LU * CH], uint32_t lo, uint32_t hi, bool keys) {
                 const uint32_t at = smem_u32(tile);
@@ -557,12 +577,14 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                 // this tile's codes and scales are asked for, then the table's entries of the group's next one
                 const int u_now = u, held_now = held, st = tile % kStages, ph = tile / kStages + 1;
                 int row[LU];
+                bool missing = false;
                 uint4 kr[LU * CH], vr[LU * CH];
                 float scale[LU];
 #pragma unroll
                 for (int i = 0; i < LU; ++i) {
                     if (page[i] == -2) raise_error(p.err, kErrInternal);
                     row[i] = page[i] < 0 ? -1 : (page[i] * p.pool.hkv + head) * p.pool.page_size + in_page[i];
+                    missing |= row[i] < 0;
                     scale[i] = scaler && row[i] >= 0 ? __ldg((lane == 0 ? p.k_scales : p.v_scales) + row[i] / kKvBlock) : 0.f;
                 }
                 fetch(p.k_pages, row, kr);
@@ -586,6 +608,11 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                             slot[8] = 1.f / x;
                         }
                     }
+                }
+                if (__any_sync(0xffffffffu, missing)) {       // rows that do not exist become zeros
+#pragma unroll
+                    for (int i = 0; i < LU * CH; ++i)
+                        if (row[i / CH] < 0) kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
                 }
                 put(sm.k[st], kr, k_lo, k_hi, true);
                 arrive(&sm.k_full[st]);
@@ -640,7 +667,6 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
 #pragma unroll
                         for (int k = 0; k < kTile / 16; ++k) mma_tmem_a(tmem + L::O + q * D, a + 8 * k, vd + 128 * k, id, !(first && k == 0));
                         mma_commit(&sm.s_free[q][buf]);
-                        mma_commit(&sm.pv_done[q]);
                     }
                     if (tile_ends) mma_commit(&sm.v_empty[st]);
                 }

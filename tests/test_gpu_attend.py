@@ -362,3 +362,17 @@ def test_garbage_past_the_end_is_not_read(attn, m):
     q = torch.randn(m, 4, 128, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
     out, cu = run(attn, q, cache, [m], lens)
     check(out, *ref.attend(q, clean, cu, lens))
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(256, 6, 3), (128, 8, 2), (64, 8, 1)])
+def test_repeated_calls_agree(attn, d, hq, hkv):
+    """Short runs (a unit or two a CTA) many times over: nothing is read before the product that writes it has finished."""
+    cache = ref.make_cache([700], hkv, d, 48, I8, 30)
+    q = torch.randn(300, hq, d, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    first = None
+    for _ in range(40):
+        out, cu = run(attn, q, cache, [300], [700], window=200, sinks=100)
+        if first is None:
+            first = out
+            check(out, *ref.attend(q, cache, cu, [700], 200, 100))
+        assert torch.equal(out, first)
