@@ -10,6 +10,8 @@ call only enqueues work on the current stream of the tensors' device (or ``strea
 """
 from __future__ import annotations
 
+import ctypes
+import functools
 import math
 from typing import Optional, Tuple
 
@@ -21,74 +23,83 @@ KV_BLOCK = 16                                             # tokens that share a 
 FORMAT = {torch.int8: 0, torch.float8_e4m3fn: 1}
 
 
-def _contiguous(name: str, t: torch.Tensor, dtype, ndim: int, device) -> int:
-    """Check a tensor and return its address."""
-    if t.dtype is not dtype or t.dim() != ndim or t.device != device or not t.is_contiguous():
-        _refuse(name, t, dtype, ndim, device)
-    return t.data_ptr()
+# These calls are made for every layer of every generated token, where the host's time counts as much as the GPU's, so the
+# checks are written for the case that nothing is wrong; `_refuse` finds out what was.
+def _contiguous(name: str, t: torch.Tensor, dtype, ndim: int, index: int) -> int:
+    """The address of a contiguous tensor of this type on CUDA device ``index``."""
+    if t.dtype is dtype and t.get_device() == index and t.dim() == ndim and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(name, t, dtype, ndim, index)
 
 
-def _refuse(name, t, dtype, ndim, device):
+def _refuse(name, t, dtype, ndim, index):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on cuda:{index}")
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     raise ValueError(f"{name} must be a contiguous {ndim}-d tensor")
 
 
-def _device(t: torch.Tensor, name: str) -> torch.device:
+def _device(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
-    return t.device
+    return index
 
 
-def _launch(fn, name, device, stream, *args):
+def _launch(fn, name, index, stream, *args):
     """Call ``fn(*args, stream)`` with the tensors' device current."""
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(device.index)
-    else:
-        handle = stream.cuda_stream
-    if torch._C._cuda_getDevice() == device.index:
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    if _current_device() == index:
         st = fn(*args, handle)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             st = fn(*args, handle)
     if st != GDN_OK:
         raise GdnError(st, name)
 
 
-def _token_rows(name: str, t: torch.Tensor, heads: int, d: int, device) -> Tuple[int, int]:
+def _raw_stream(index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
+def _token_rows(name: str, t: torch.Tensor, heads: int, d: int, index: int) -> Tuple[int, int]:
     """Address and token stride of a bf16 [T, heads, d] tensor whose head vectors are contiguous."""
-    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.device != device:
-        _refuse(name, t, torch.bfloat16, 3, device)
-    if t.shape[1] != heads or t.shape[2] != d:
-        raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {tuple(t.shape)}")
-    stride = t.stride()
+    if t.dtype is not torch.bfloat16 or t.get_device() != index or t.dim() != 3:
+        _refuse(name, t, torch.bfloat16, 3, index)
+    shape, stride = t.shape, t.stride()
+    if shape[1] != heads or shape[2] != d:
+        raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {tuple(shape)}")
     if stride[2] != 1 or (heads > 1 and stride[1] != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), max(stride[0], heads * d) if t.shape[0] <= 1 else stride[0]
+    return t.data_ptr(), stride[0] if shape[0] > 1 else max(stride[0], heads * d)
 
 
-def _pool(k_pages, v_pages, k_scales, v_scales, block_table, device):
+def _pool(k_pages, v_pages, k_scales, v_scales, block_table, index):
     """Checked (addresses, (table address, max_pages, n_pages, page_size, format), hkv, d) of a cache."""
-    if k_pages.dtype not in FORMAT:
-        raise ValueError(f"k_pages must be int8 or float8_e4m3fn, got {k_pages.dtype}")
-    kp = _contiguous("k_pages", k_pages, k_pages.dtype, 4, device)
-    vp = _contiguous("v_pages", v_pages, k_pages.dtype, 4, device)
-    ks = _contiguous("k_scales", k_scales, torch.float32, 3, device)
-    vs = _contiguous("v_scales", v_scales, torch.float32, 3, device)
-    table = _contiguous("block_table", block_table, torch.int32, 2, device)
-    n_pages, hkv, page, d = k_pages.shape
-    if v_pages.shape != k_pages.shape:
+    dtype = k_pages.dtype
+    fmt = FORMAT.get(dtype)
+    if fmt is None:
+        raise ValueError(f"k_pages must be int8 or float8_e4m3fn, got {dtype}")
+    addresses = (_contiguous("k_pages", k_pages, dtype, 4, index), _contiguous("v_pages", v_pages, dtype, 4, index),
+                 _contiguous("k_scales", k_scales, torch.float32, 3, index),
+                 _contiguous("v_scales", v_scales, torch.float32, 3, index))
+    table = _contiguous("block_table", block_table, torch.int32, 2, index)
+    shape = k_pages.shape
+    n_pages, hkv, page, d = shape
+    if v_pages.shape != shape:
         raise ValueError("v_pages must have the shape of k_pages")
-    want = (n_pages, hkv, page // KV_BLOCK)
-    if k_scales.shape != want or v_scales.shape != want:
-        raise ValueError(f"k_scales and v_scales must be {want}")
-    return (kp, vp, ks, vs), (table, block_table.shape[1], n_pages, page, FORMAT[k_pages.dtype]), hkv, d
+    if k_scales.shape != (n_pages, hkv, page // KV_BLOCK) or v_scales.shape != k_scales.shape:
+        raise ValueError(f"k_scales and v_scales must be {(n_pages, hkv, page // KV_BLOCK)}")
+    return addresses, (table, block_table.shape[1], n_pages, page, fmt), hkv, d
 
 
 def alloc_cache(n_pages: int, hkv: int, page_size: int, d: int, n_slots: int, dtype=torch.int8, device="cuda"):
@@ -153,7 +164,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cos: Optional[torch.Tensor], sin
         if q.shape[0] != T:
             raise ValueError("q and k must have the same tokens")
         if q_out is None:
-            q_out = torch.empty(T, hq, d, dtype=torch.bfloat16, device=dev)
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         qo = _contiguous("q_out", q_out, torch.bfloat16, 3, dev)
         if q_out.shape != q.shape:
             raise ValueError("q_out must have the shape of q")
@@ -180,17 +191,17 @@ def kv_read(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Tensor
     n = cu_tokens.shape[0] - 1
     if block_table.shape[0] != n:
         raise ValueError("cu_tokens and block_table must describe the same sequences")
-    k = torch.empty(total_tokens, hkv, d, dtype=out_dtype, device=dev)
-    v = torch.empty(total_tokens, hkv, d, dtype=out_dtype, device=dev)
+    k = torch.empty(total_tokens, hkv, d, dtype=out_dtype, device=k_pages.device)
+    v = torch.empty_like(k)
     _launch(lib.gdn_kv_read, "gdn_kv_read", dev, stream, n, total_tokens, hkv, d, cu, *pool, *pages, k.data_ptr(),
             v.data_ptr(), DTYPE[out_dtype])
     return k, v
 
 
+@functools.lru_cache(maxsize=4096)
 def attend_workspace_size(n_seqs: int, total_tokens: int, hq: int, hkv: int, d: int, max_q_len: int,
                           max_kv_len: int) -> int:
     """Bytes of workspace that :func:`attend` needs for this problem (``gdn_attend_workspace_size``)."""
-    import ctypes
     st = ctypes.c_int(0)
     need = load_library().gdn_attend_workspace_size(n_seqs, total_tokens, hq, hkv, d, max_q_len, max_kv_len, st)
     if st.value != GDN_OK:
@@ -220,15 +231,15 @@ def attend(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scal
     if cu_seqlens.shape[0] != n + 1 or block_table.shape[0] != n:
         raise ValueError("cu_seqlens, kv_lens and block_table must describe the same sequences")
     if out is None:
-        out = torch.empty(T, hq, d, dtype=out_dtype, device=dev)
+        out = torch.empty_like(q, dtype=out_dtype)
     op = _contiguous("out", out, out.dtype, 3, dev)
     if out.shape != q.shape or out.dtype not in DTYPE:
         raise ValueError("out must have the shape of q, in bf16 or fp32")
     max_q_len = min(max_q_len, T)
     if workspace is None:
         need = attend_workspace_size(n, T, hq, hkv, d, max_q_len, max_kv_len)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the other tensors' device")
     table, max_pages, n_pages, page, fmt = pool
     _launch(lib.gdn_attend, "gdn_attend", dev, stream, n, T, hq, hkv, d, qp, *pages, table, max_pages, n_pages, page,

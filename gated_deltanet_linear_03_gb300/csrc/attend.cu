@@ -214,23 +214,39 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NR>()) attend_split_k
     if (warp == 4) {
         // ---- the producer: of lanes 0..7, lane b holds K's block b of a unit and lane 4 + b V's: the pool row where it
         // begins, -1 where there is none
-        auto look_up = [&]() -> int {
+        bool exists;
+        int entry, in_page, head;
+        auto look_up = [&]() {      // asks for the table's entry, which is looked at when the unit's turn comes
             const int tok = cc.it.token(cc.j, kTile) + (lane & 3) * kKvBlock;
-            if (lane >= 8 || tok >= cc.s.kvlen) return -1;
-            const int at = p.pool.page_of(tok), page = __ldg(p.pool.table + (size_t)cc.n * p.pool.max_pages + at);
-            if ((unsigned)page < (unsigned)p.pool.n_pages) return (page * p.pool.hkv + cc.h) * p.pool.page_size + tok - at * p.pool.page_size;
+            exists = lane < 8 && tok < cc.s.kvlen;
+            if (!exists) return;
+            const int at = p.pool.page_of(tok);
+            entry = __ldg(p.pool.table + (size_t)cc.n * p.pool.max_pages + at);
+            in_page = tok - at * p.pool.page_size;
+            head = cc.h;
+        };
+        auto pool_row = [&]() -> int {
+            if (!exists) return -1;
+            if ((unsigned)entry < (unsigned)p.pool.n_pages) return (entry * p.pool.hkv + head) * p.pool.page_size + in_page;
             raise_error(p.err, kErrInternal);
             return -1;
         };
         auto scale_of = [&](int row) -> float { return row >= 0 ? __ldg((lane < 4 ? p.k_scales : p.v_scales) + row / kKvBlock) : 0.f; };
         const CUtensorMap *map = lane < 4 ? &k_map : &v_map;
-        int row = look_up(), stage = 0, phase = 1, issued = 0;
+        look_up();
+        int row = pool_row(), stage = 0, phase = 1, issued = 0;
+        float scale = scale_of(row);
+        if (units > 1) {
+            advance(cc);
+            look_up();
+        }
         for (int unit = 0; unit < units; ++unit) {
-            const float scale = scale_of(row);
-            int next = -1;
-            if (unit + 1 < units) {
+            // the next unit's rows and scales, and the table's entries of the one after it
+            const int next_row = unit + 1 < units ? pool_row() : -1;
+            const float next_scale = scale_of(next_row);
+            if (unit + 2 < units) {
                 advance(cc);
-                next = look_up();
+                look_up();
             }
             wait(&sm.empty[stage], phase);
             __syncwarp();
@@ -246,7 +262,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NR>()) attend_split_k
             __syncwarp();
             if (lane == 0) sm100::mbar_arrive_expect_tx(&sm.full[stage], 2 * kTile * D);
             if (++stage == S) stage = 0, phase ^= 1;
-            row = next;
+            row = next_row;
+            scale = next_scale;
             ++issued;
         }
         // every copy is waited for by the compute warps; where they have given up, here

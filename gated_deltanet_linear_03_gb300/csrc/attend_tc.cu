@@ -528,18 +528,19 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                 if (w.j == w.tiles) w.next_item();
                 held = min(min(LU, w.tiles - w.j), units - u);
             };
-            int page[LU], in_page[LU], head = 0;   // of this thread's rows in the tile that `w` is at; -1: no such token
+            bool held_row[LU];                     // whether this thread's rows in the tile that `w` is at exist,
+            int entry[LU], in_page[LU], head = 0;   // and their table entries and places in the pages
             auto look_up = [&]() {
                 head = w.h;
 #pragma unroll
                 for (int i = 0; i < LU; ++i) {
-                    page[i] = -1;
+                    held_row[i] = false;
                     const int tok = i < held ? w.it.token(w.j + i, kTile) + r : 0;
                     if (i >= held || tok >= w.s.kvlen) continue;
                     const int at = p.pool.page_of(tok);
                     in_page[i] = tok - at * p.pool.page_size;
-                    page[i] = __ldg(p.pool.table + (size_t)w.n * p.pool.max_pages + at);
-                    if ((unsigned)page[i] >= (unsigned)p.pool.n_pages) page[i] = -2;
+                    held_row[i] = true;                    // its entry is looked at when the tile's turn comes
+                    entry[i] = __ldg(p.pool.table + (size_t)w.n * p.pool.max_pages + at);
                 }
             };
             auto fetch = [&](const uint8_t *pages, const int (&row)[LU], uint4 (&x)[LU * CH]) {
@@ -582,8 +583,11 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                 float scale[LU];
 #pragma unroll
                 for (int i = 0; i < LU; ++i) {
-                    if (page[i] == -2) raise_error(p.err, kErrInternal);
-                    row[i] = page[i] < 0 ? -1 : (page[i] * p.pool.hkv + head) * p.pool.page_size + in_page[i];
+                    row[i] = -1;
+                    if (held_row[i]) {
+                        if ((unsigned)entry[i] < (unsigned)p.pool.n_pages) row[i] = (entry[i] * p.pool.hkv + head) * p.pool.page_size + in_page[i];
+                        else raise_error(p.err, kErrInternal);
+                    }
                     missing |= row[i] < 0;
                     scale[i] = scaler && row[i] >= 0 ? __ldg((lane == 0 ? p.k_scales : p.v_scales) + row[i] / kKvBlock) : 0.f;
                 }

@@ -102,8 +102,8 @@ gdn_status gdn_kv_append(int n_seqs, int total_tokens, int hq, int hkv, int d, i
     if (!disjoint(outs, ins)) return GDN_ERR_INVALID_ARG;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const void *anchors[] = {k, k_pages, open_out, q_out};
-    for (const void *a : anchors)
-        if ((st = gdn::on_current_device(a, cs)) != GDN_OK) return st;
+    st = gdn::on_current_device(anchors, sizeof(anchors) / sizeof(anchors[0]), cs);
+    if (st != GDN_OK) return st;
 
     gdn::AppendProblem p{};
     p.n_seqs = n_seqs; p.total = total_tokens; p.hq = hq; p.d = d; p.rot = rot;
@@ -148,8 +148,8 @@ gdn_status gdn_kv_read(int n_seqs, int total_tokens, int hkv, int d, const int32
     if (!disjoint(outs, ins)) return GDN_ERR_INVALID_ARG;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const void *anchors[] = {k_pages, k_out, v_out};
-    for (const void *a : anchors)
-        if ((st = gdn::on_current_device(a, cs)) != GDN_OK) return st;
+    st = gdn::on_current_device(anchors, sizeof(anchors) / sizeof(anchors[0]), cs);
+    if (st != GDN_OK) return st;
 
     gdn::ReadProblem p{};
     p.n_seqs = n_seqs; p.total = total_tokens; p.d = d;
@@ -217,8 +217,8 @@ gdn_status gdn_attend(int n_seqs, int total_tokens, int hq, int hkv, int d, cons
     if (!disjoint(outs, ins)) return GDN_ERR_INVALID_ARG;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const void *anchors[] = {q, k_pages, out, workspace};
-    for (const void *a : anchors)
-        if ((st = gdn::on_current_device(a, cs)) != GDN_OK) return st;
+    st = gdn::on_current_device(anchors, sizeof(anchors) / sizeof(anchors[0]), cs);
+    if (st != GDN_OK) return st;
 
     gdn::AttendProblem p{};
     p.n_seqs = n_seqs; p.total = total_tokens; p.hq = hq; p.d = d;
@@ -260,9 +260,8 @@ gdn_status gdn_block_norm(int rows, int dim, const void *x, const void *gate, in
     if (!disjoint(outs, ins)) return GDN_ERR_INVALID_ARG;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     const void *anchors[] = {x, residual_out, out};
-    gdn_status st;
-    for (const void *a : anchors)
-        if ((st = gdn::on_current_device(a, cs)) != GDN_OK) return st;
+    gdn_status st = gdn::on_current_device(anchors, sizeof(anchors) / sizeof(anchors[0]), cs);
+    if (st != GDN_OK) return st;
 
     gdn::BlockNormProblem p{};
     p.rows = rows; p.dim = dim;

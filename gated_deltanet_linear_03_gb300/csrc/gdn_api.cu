@@ -133,7 +133,30 @@ __global__ void selftest_wait_kernel(uint64_t limit_ns, unsigned int *err) {
 // The host helpers that the other entry-point files share.
 namespace gdn {
 unsigned int *error_word() { return device_error_ptr(); }
-gdn_status on_current_device(const void *p, cudaStream_t stream) { return check_on_current_device(p, stream); }
+// check_on_current_device of several pointers, asking for the stream's capture and the current device once.
+gdn_status on_current_device(const void *const *pointers, int n, cudaStream_t stream) {
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    int dev = -1;
+    if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess) {
+        cudaGetLastError();
+        return GDN_ERR_CUDA;
+    }
+    if (cs != cudaStreamCaptureStatusNone) return GDN_OK;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return GDN_ERR_CUDA;
+    }
+    for (int i = 0; i < n; ++i) {
+        cudaPointerAttributes a{};
+        if (!pointers[i]) continue;
+        if (cudaPointerGetAttributes(&a, pointers[i]) != cudaSuccess) {
+            cudaGetLastError();
+            return GDN_ERR_INVALID_ARG;
+        }
+        if ((a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged) || a.device != dev) return GDN_ERR_INVALID_ARG;
+    }
+    return GDN_OK;
+}
 int multiprocessor_count() { return sm_count(); }
 }  // namespace gdn
 

@@ -124,9 +124,9 @@ size_t chunked_workspace_bytes(int n_seqs, const int32_t *cu_host, int hv, int d
 int plan_state_pass(int n_seqs, const int32_t *cu_host, int hv, int sms, int *first_seq, int capacity);
 
 // Host helpers of the entry points (gdn_api.cu): the current device's error word (null if it cannot be found),
-// the check that a pointer is memory of the current device, and the device's multiprocessors.
+// the check that pointers are memory of the current device, and the device's multiprocessors.
 unsigned int *error_word();
-gdn_status on_current_device(const void *p, cudaStream_t stream);
+gdn_status on_current_device(const void *const *pointers, int n, cudaStream_t stream);
 int multiprocessor_count();
 
 }  // namespace gdn

@@ -34,32 +34,27 @@ def block_norm(x: torch.Tensor, residual: torch.Tensor, pre_weight: torch.Tensor
     if nd < 1:
         raise ValueError("x must have a last dimension to normalise over")
     dim = shape[-1]
-    xp = _contiguous("x", x, torch.bfloat16, nd, dev)
-    if residual.dtype not in DTYPE:
-        raise ValueError(f"residual must be bf16 or fp32, got {residual.dtype}")
-    rp = _contiguous("residual", residual, residual.dtype, nd, dev)
-    pre = _contiguous("pre_weight", pre_weight, torch.float32, 1, dev)
-    gp = _contiguous("gate", gate, torch.bfloat16, nd, dev) if gate is not None else 0
-    post = _contiguous("post_weight", post_weight, torch.float32, 1, dev) if post_weight is not None else 0
-    sw, number = 0, 1.0
-    if isinstance(scale, torch.Tensor):
-        sw = _contiguous("scale", scale, torch.float32, 1, dev)
-    else:
-        number = float(scale)
-    for name, t in (("pre_weight", pre_weight), ("post_weight", post_weight), ("scale", scale if sw else None)):
-        if t is not None and t.shape[0] != dim:
-            raise ValueError(f"{name} must have {dim} entries")
-    if gate_act not in GATE_ACT:
-        raise ValueError(f"gate_act must be one of {sorted(GATE_ACT)}")
+    res = residual.dtype
+    if res not in DTYPE:
+        raise ValueError(f"residual must be bf16 or fp32, got {res}")
     if residual_out is None:
         residual_out = torch.empty_like(residual)
     if out is None:
         out = torch.empty_like(x)
-    ro = _contiguous("residual_out", residual_out, residual.dtype, nd, dev)
-    op = _contiguous("out", out, torch.bfloat16, nd, dev)
     if residual.shape != shape or residual_out.shape != shape or out.shape != shape or (gate is not None and gate.shape != shape):
         raise ValueError("x, gate, residual and the outputs must have one shape")
-    rows = x.numel() // dim if dim else 0
-    _launch(lib.gdn_block_norm, "gdn_block_norm", dev, stream, rows, dim, xp, gp, GATE_ACT[gate_act], rp,
-            DTYPE[residual.dtype], post, pre, sw, number, float(eps), ro, op)
+    scaled = isinstance(scale, torch.Tensor)
+    if pre_weight.shape[0] != dim or (post_weight is not None and post_weight.shape[0] != dim) or (scaled and scale.shape[0] != dim):
+        raise ValueError(f"pre_weight, post_weight and a scale per channel must have {dim} entries")
+    act = GATE_ACT.get(gate_act)
+    if act is None:
+        raise ValueError(f"gate_act must be one of {sorted(GATE_ACT)}")
+    bf16, f32 = torch.bfloat16, torch.float32
+    _launch(lib.gdn_block_norm, "gdn_block_norm", dev, stream, x.numel() // dim if dim else 0, dim,
+            _contiguous("x", x, bf16, nd, dev), 0 if gate is None else _contiguous("gate", gate, bf16, nd, dev), act,
+            _contiguous("residual", residual, res, nd, dev), DTYPE[res],
+            0 if post_weight is None else _contiguous("post_weight", post_weight, f32, 1, dev),
+            _contiguous("pre_weight", pre_weight, f32, 1, dev), _contiguous("scale", scale, f32, 1, dev) if scaled else 0,
+            1.0 if scaled else scale, eps, _contiguous("residual_out", residual_out, res, nd, dev),
+            _contiguous("out", out, bf16, nd, dev))
     return residual_out, out
