@@ -202,13 +202,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NR>()) attend_split_k
         }
         c.it = make_item<kRows, kTile>(p, c.s, group, c.mt);
     };
-    // A bounded wait; when it runs out the error is recorded and every later wait returns at once.
+    // A bounded wait; when it runs out a flag is set with which every later wait returns at once and which becomes the
+    // call's error at the end.
     volatile int *abort = &sm.abort;
-    auto wait = [&](uint64_t *bar, int phase) {
-        bool late = false;
-        sm100::mbar_poll(bar, (uint32_t)phase & 1, abort, &late);
-        if (late) raise_error(p.err, kErrTimeout);
-    };
+    auto wait = [&](uint64_t *bar, int phase) { sm100::mbar_poll(bar, (uint32_t)phase & 1, abort); };
     const int units = stop - start;
 
     if (warp == 4) {
@@ -267,9 +264,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NR>()) attend_split_k
             ++issued;
         }
         // every copy is waited for by the compute warps; where they have given up, here
-        if (*abort)
-            for (int k = max(0, issued - S); k < issued; ++k)
-                if (!sm100::mbar_wait(&sm.full[k % S], (uint32_t)(k / S) & 1)) raise_error(p.err, kErrTimeout);
+        if (*abort) {
+            for (int k = max(0, issued - S); k < issued; ++k) sm100::mbar_wait(&sm.full[k % S], (uint32_t)(k / S) & 1);
+            raise_error(p.err, kErrTimeout);
+        }
         return;
     }
 
@@ -503,6 +501,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NR>()) attend_split_k
         }
         advance(cc);
     }
+    if (tid == 0 && *abort) raise_error(p.err, kErrTimeout);
 }
 
 constexpr int kMergeThreads = 256;

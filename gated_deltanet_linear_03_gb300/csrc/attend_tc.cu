@@ -29,24 +29,27 @@ using namespace sm100;
 
 constexpr int kTile = 64;
 constexpr int kStages = 3;
-constexpr int kScaleSlots = 32;    // of block scales, a unit each
+constexpr int kSlots = 32, kSlotGroup = 8;   // what the look-up warp leaves of a unit: a ring of slots, filled eight at a time
 
 template <int D>
 struct Tc {
     static constexpr int NQ = D == 256 ? 1 : 2;              // 128-row tiles of a CTA, which share its K and V
     static constexpr int ROWS = 128 * NQ;
-    static constexpr int SB = NQ * (D + D / 2 + 128) <= 512 ? 2 : 1;   // score buffers of a tile
-    static constexpr int O = 0, Q = NQ * D, S = NQ * (D + D / 2);      // TMEM columns: O fp32, Q two fp16 a column, S of 64
+    // TMEM columns: O fp32, Q two fp16 a column, then rings of score buffers (64) and of weight buffers (32, two fp16 a
+    // column).  Scores leave their buffer as soon as they are in registers, so the next score product runs beside the
+    // arithmetic even where one buffer is all that fits.
+    static constexpr int O = 0, Q = NQ * D, S = NQ * (D + D / 2);
+    static constexpr int PR = D == 64 ? 4 : 2, SR = (512 - S - 32 * PR) / 64, P = S + 64 * SR;
+    static_assert(SR >= 1 && P + 32 * PR <= 512 && PR % NQ == 0, "tensor memory");
     static constexpr int LU = 256 / D;                       // units of a load tile: 16 KB of K codes and 16 KB of V codes
     static constexpr int LG = D == 256 ? 2 : 1;              // groups of 8 loader warps, which take the tiles in turn
-    // A loader is at most kStages + LG tiles ahead of the score product, and that SB units ahead of the softmax.
-    static_assert(LU * (kStages + LG) + SB < kScaleSlots, "scale slots");
+    static_assert(kSlotGroup % LU == 0 && 2 * kSlotGroup >= LU * (LG + 1), "a tile's units lie in one group of slots");
     static constexpr int SOFTMAX_WARPS = 8 * NQ, LOADER_WARPS = 8 * LG;
-    static constexpr int WARPS = SOFTMAX_WARPS + LOADER_WARPS + 4;     // the last four: MMA, MMA, two idle
+    static constexpr int WARPS = SOFTMAX_WARPS + LOADER_WARPS + 4;     // the last four: MMA, MMA, look-up, idle
     static constexpr int THREADS = 32 * WARPS;               // 896
     // Registers a thread: at launch (the most that 28 warps can have, a multiple of 8), then per role.  The roles' shares
-    // stay within what the CTA was launched with: 896 x 72 = 256 x 104 + 512 x 64 + 128 x 40 >= 512 x 80 + 256 x 64 + 128 x 40.
-    static constexpr int REGS_LAUNCH = 72, REGS_SOFTMAX = NQ == 1 ? 104 : 80, REGS_LOADER = 64, REGS_OTHER = 40;
+    // stay within what the CTA was launched with: 896 x 72 = 256 x 104 + 512 x 56 + 128 x 72 = 512 x 88 + 256 x 56 + 128 x 40.
+    static constexpr int REGS_LAUNCH = 72, REGS_SOFTMAX = NQ == 1 ? 104 : 88, REGS_LOADER = 56, REGS_OTHER = NQ == 1 ? 72 : 40;
     static_assert(32 * (SOFTMAX_WARPS * REGS_SOFTMAX + LOADER_WARPS * REGS_LOADER + 4 * REGS_OTHER) <= THREADS * REGS_LAUNCH, "registers");
     static constexpr int TILE_ROWS = kTile * LU, TILE_BYTES = TILE_ROWS * D * 2, CHUNK = TILE_ROWS * 128;   // CHUNK: 64 columns
 };
@@ -56,10 +59,12 @@ struct __align__(1024) TcSmem {
     static constexpr int NQ = Tc<D>::NQ;
     uint8_t k[kStages][Tc<D>::TILE_BYTES];
     uint8_t v[kStages][Tc<D>::TILE_BYTES];
-    float scale[kScaleSlots][12];        // K scales, log2 of V scales, reciprocals of V scales
+    float scale[kSlots][12];             // of a unit's 4 blocks: K scales, log2 of V scales, reciprocals of V scales
+    int2 block[kSlots][4];               // and their first rows in the pool (-1: none), and how many tokens they hold
     float row_m[Tc<D>::ROWS], row_l[Tc<D>::ROWS];   // at an item's end
+    uint64_t slots_full[kSlots / kSlotGroup], slots_free[kSlots / kSlotGroup];
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-    uint64_t s_full[NQ][2], s_free[NQ][2], p_full[NQ][2], q_full[NQ], drain[2];
+    uint64_t s_full[NQ][2], s_read[Tc<D>::SR], p_full[Tc<D>::PR], p_free[Tc<D>::PR], q_full[NQ], drain[2];
     uint32_t tmem;
     int abort;
 };
@@ -70,12 +75,18 @@ struct RunStart {
     long long unit;
 };
 
+// An item as its units' roles see it, worked out once: (sequence, key/value head, row tile) and its units, the sequence,
+// and the tokens that its rows see (an Item's fields).
+struct __align__(16) TcItem {
+    int n, h, mt, tiles, q0, qlen, kvlen, lo_pos, hi_pos, near_tiles, far_tile, unused;
+};
+
 // Workspace of a call: the merge entries, the runs' starts, the item list, the parts.
 struct TcPlan {
     MergeMeta *meta;       // [ctas]
     RunStart *start;       // [ctas + 1]
     long long *per;        // cost of a run
-    int4 *items;           // (sequence, head, row tile, units)
+    TcItem *items;
     float *parts;
     int ctas;
 };
@@ -141,20 +152,22 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
                 else hi = mid;
             }
             const int mts = row_tiles<ROWS>(seqs[lo].qlen, group), h = (k - first[lo]) / mts, mt = k - first[lo] - h * mts;
-            plan.items[items + k] = make_int4(n0 + lo, h, mt, make_item<ROWS, kTile>(p, seqs[lo], group, mt).tiles);
+            const Sequence q = seqs[lo];
+            const Item it = make_item<ROWS, kTile>(p, q, group, mt);
+            plan.items[items + k] = {n0 + lo, h, mt, it.tiles, q.q0, q.qlen, q.kvlen, it.lo_pos, it.hi_pos, it.near_tiles, it.far_tile, 0};
         }
         items += sum;
         __syncthreads();
     }
     const int each = (items + kPlanThreads - 1) / kPlanThreads, i0 = min(tid * each, items), i1 = min(i0 + each, items);
     long long mine = 0, total;
-    for (int i = i0; i < i1; ++i) mine += plan.items[i].w + kItemCost;
+    for (int i = i0; i < i1; ++i) mine += plan.items[i].tiles + kItemCost;
     long long at = block_scan(mine, total, part_cost);
     const long long per = max((total + plan.ctas - 1) / plan.ctas, 1LL);
     if (tid == 0) plan.per[0] = per;
     long long c = (at + per - 1) / per;           // the first run that begins at or after this thread's items
     for (int i = i0; i < i1; ++i) {
-        const int w = plan.items[i].w + kItemCost;
+        const int w = plan.items[i].tiles + kItemCost;
         // a run that would begin inside an item's fixed cost begins at its first unit
         for (; c < plan.ctas && c * per < at + w; ++c) {
             const int j = max(0, (int)(c * per - at) - kItemCost);
@@ -165,43 +178,52 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
     for (long long r = (total + per - 1) / per + tid; r <= plan.ctas; r += kPlanThreads) plan.start[r] = {0, 0, total - (long long)items * kItemCost};
 }
 
+// A word with its n lowest bits set (none below 0, all above 63).
+__device__ __forceinline__ unsigned long long low_bits(int n) { return n <= 0 ? 0ull : n > 63 ? ~0ull : (1ull << n) - 1; }
+
 template <bool V>
 struct Flag {
     static constexpr bool value = V;
 };
 
+template <int AT>
+__device__ __forceinline__ void store_shared(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0 + %5], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w), "n"(AT) : "memory");
+}
+
+// A loader thread's codes of a tile as fp16, from piece N (16 codes) on: the first and the last 8 of K's order, or of V's.
+template <int D, int FMT, bool KEYS, int N = 0>
+__device__ __forceinline__ void put_codes(uint32_t lo, uint32_t hi, const uint4 (&x)[Tc<D>::LU * D / 64]) {
+    constexpr int CH = D / 64, at = N % CH * Tc<D>::CHUNK + N / CH * (kTile * 128);
+    const uint4 z = x[N];
+    uint32_t y[8];
+    codes_to_f16x2<FMT>(z.x, y[0], y[1]);
+    codes_to_f16x2<FMT>(KEYS ? z.z : z.y, y[2], y[3]);
+    codes_to_f16x2<FMT>(KEYS ? z.y : z.z, y[4], y[5]);
+    codes_to_f16x2<FMT>(z.w, y[6], y[7]);
+    store_shared<at>(lo, y[0], y[1], y[2], y[3]);
+    store_shared<at>(hi, y[4], y[5], y[6], y[7]);
+    if constexpr (N + 1 < Tc<D>::LU * CH) put_codes<D, FMT, KEYS, N + 1>(lo, hi, x);
+}
+
+// The first token of an item's unit j.
+__device__ __forceinline__ int first_token(const TcItem &it, int j) { return (j < it.near_tiles ? j : it.far_tile + j - it.near_tiles) * kTile; }
+
 // Where a role stands in its CTA's run; every role keeps its own.
-template <int ROWS>
 struct Walk {
-    const AttendProblem &p;
     const TcPlan &plan;
-    int group, item, j, tiles, n, h, mt;
-    Sequence s;
-    Item it;
-    __device__ __forceinline__ Walk(const AttendProblem &p_, const TcPlan &plan_, int group_) : p(p_), plan(plan_), group(group_) {
+    int item, j;
+    TcItem it;
+    __device__ __forceinline__ explicit Walk(const TcPlan &plan_) : plan(plan_) {
         const RunStart st = plan.start[blockIdx.x];
         item = st.item;
-        load();
+        it = plan.items[item];
         j = st.j;
     }
-    __device__ __forceinline__ void load() {
-        const int4 d = plan.items[item];
-        n = d.x;
-        h = d.y;
-        mt = d.z;
-        tiles = d.w;
-        s = load_sequence(p, n);
-        it = make_item<ROWS, kTile>(p, s, group, mt);
-        j = 0;
-    }
-    __device__ __forceinline__ int token() const { return it.token(j, kTile); }
-    // to the next unit, or item (which the run must hold)
-    __device__ __forceinline__ void next() {
-        if (++j == tiles) next_item();
-    }
+    // to the next item (which the run must hold)
     __device__ __forceinline__ void next_item() {
-        ++item;
-        load();
+        it = plan.items[++item];
+        j = 0;
     }
 };
 
@@ -209,7 +231,7 @@ template <int D, int FMT>
 __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __grid_constant__ AttendProblem p,
                                                                      const __grid_constant__ TcPlan plan) {
     using L = Tc<D>;
-    constexpr int NQ = L::NQ, SB = L::SB, ROWS = L::ROWS;
+    constexpr int NQ = L::NQ, SR = L::SR, PR = L::PR, ROWS = L::ROWS;
     extern __shared__ uint8_t raw[];
     TcSmem<D> &sm = *reinterpret_cast<TcSmem<D> *>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -224,12 +246,18 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
             mbar_init(&sm.v_empty[i], 1);
         }
         for (int q = 0; q < NQ; ++q) {
-            for (int b = 0; b < SB; ++b) {
-                mbar_init(&sm.s_full[q][b], 2);
-                mbar_init(&sm.s_free[q][b], 1);
-                mbar_init(&sm.p_full[q][b], 8);
-            }
+            mbar_init(&sm.s_full[q][0], 2);
+            mbar_init(&sm.s_full[q][1], 2);
             mbar_init(&sm.q_full[q], 8);
+        }
+        for (int b = 0; b < SR; ++b) mbar_init(&sm.s_read[b], 8);
+        for (int b = 0; b < PR; ++b) {
+            mbar_init(&sm.p_full[b], 8);
+            mbar_init(&sm.p_free[b], 1);
+        }
+        for (int i = 0; i < kSlots / kSlotGroup; ++i) {
+            mbar_init(&sm.slots_full[i], 1);
+            mbar_init(&sm.slots_free[i], 1);
         }
         mbar_init(&sm.drain[0], 1);
         mbar_init(&sm.drain[1], 1);
@@ -245,14 +273,9 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
     const long long per = plan.per[0];
     const int units = (int)(plan.start[cta + 1].unit - plan.start[cta].unit);
 
-    // Waits are bounded.  One that runs out records the error and sets a flag with which every later wait returns at once;
-    // no warp leaves its loop, so no named barrier is left waiting.
-    volatile int *abort = &sm.abort;
-    auto poll = [&](uint64_t *bar, int phase) {
-        bool late = false;
-        mbar_poll(bar, (uint32_t)phase & 1, abort, &late);
-        if (late) raise_error(p.err, kErrTimeout);
-    };
+    // Waits are bounded.  One that runs out sets a flag with which every later wait returns at once and which becomes the
+    // call's error at the end; no warp leaves its loop, so no named barrier is left waiting.
+    auto poll = [&](uint64_t *bar, int phase) { mbar_poll(bar, (uint32_t)phase & 1, &sm.abort); };
     auto arrive = [&](uint64_t *bar) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
@@ -264,7 +287,7 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
         const int q = NQ == 2 ? warp / 8 : 0, quadrant = warp & 3, half = (warp >> 2) & 1, g = lane >> 2, t = lane & 3;
         const int row0 = 128 * q + 32 * quadrant + 16 * half + g;        // this lane's rows: row0 and row0 + 8
         const uint32_t quad = tmem + ((uint32_t)quadrant << 21), part16 = quad + ((uint32_t)(16 * half) << 16);   // lanes
-        const uint32_t o_cols = L::O + q * D, q_at = part16 + L::Q + q * (D / 2), s_at = part16 + L::S + q * SB * 64;
+        const uint32_t o_cols = L::O + q * D, q_at = part16 + L::Q + q * (D / 2);
         auto wait = [&](uint64_t *bar, int phase) {
             poll(bar, phase);
             __syncwarp();
@@ -272,13 +295,14 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
         MergeMeta mm;
         mm.last = -1;
         if (units > 0) {
-            Walk<ROWS> w(p, plan, group);
-            int buf = 0, phase = 0;
+            Walk w(plan);
+            // the product number (unit u, tile q) in both rings: number % SR, number % PR
+            auto number = [&](int u) { return u * NQ + q; };
             for (int u = 0, seg = 0; u < units; ++seg) {
                 // ---- a segment, units of one item: its queries, 4 lanes to a row, 16 bytes each.  The first pass finds the
                 // rows' scales, the second (from L1) converts.
                 const bool begun = w.j == 0;
-                const int seg_slot = u == 0 ? 0 : 1, u_end = min(units, u + w.tiles - w.j);
+                const int seg_slot = u == 0 ? 0 : 1, u_end = min(units, u + w.it.tiles - w.j);
                 float rs[2];
                 int pos[2];
                 {
@@ -286,10 +310,10 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                     float down[2];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const int gr = w.mt * ROWS + row0 + 8 * k, i = gr / group;
-                        pos[k] = w.s.kvlen - w.s.qlen + i;
-                        src[k] = i < w.s.qlen
-                                     ? reinterpret_cast<const uint4 *>(p.q + ((size_t)(w.s.q0 + i) * p.hq + w.h * group + gr % group) * D) + t
+                        const int gr = w.it.mt * ROWS + row0 + 8 * k, i = gr / group;
+                        pos[k] = w.it.kvlen - w.it.qlen + i;
+                        src[k] = i < w.it.qlen
+                                     ? reinterpret_cast<const uint4 *>(p.q + ((size_t)(w.it.q0 + i) * p.hq + w.it.h * group + gr % group) * D) + t
                                      : nullptr;
                         uint32_t big = 0;
 #pragma unroll
@@ -322,31 +346,38 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                 arrive(&sm.q_full[q]);              // also: this warp has read its part of the item before
                 float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
                 bool raise = true;                  // the item's first unit sets M
-                // units before this one are seen by every row as a whole
-                const int seen_to = p.window == 0 ? (w.it.lo_pos + 1) / kTile : 0;
+                const int seen_to = w.it.lo_pos + 2 - kTile;     // units that begin before are in no row's future
                 for (; u < u_end; ++u, ++w.j) {
                     // ---- one unit
-                    const uint32_t s_tm = s_at + buf * 64;
-                    const bool all_seen = w.j < seen_to || (p.window != 0 && w.it.all_seen(w.token(), w.token() + kTile, p.window, p.sinks));
-                    const float *scale = sm.scale[u % kScaleSlots];
-                    wait(&sm.s_full[q][buf], phase);
+                    const int n = number(u), sb = n % SR, pb = n % PR;
+                    const int tok0 = first_token(w.it, w.j);
+                    const bool all_seen = tok0 < seen_to && (p.window == 0 || tok0 > w.it.hi_pos - p.window || tok0 + kTile <= p.sinks);
+                    const float *scale = sm.scale[u % kSlots];
+                    wait(&sm.s_full[q][u & 1], u >> 1);
                     tc_fence_after();
-                    const bool first = raise;
-                    for (;;) {
-                        // scores of row k at tokens 8 i + 2 t, + 1: s[4 i + 2 k], + 1
-                        float s[32];
-                        tmem_ld_16x64(s_tm, s);
-                        const float4 ks = *reinterpret_cast<const float4 *>(scale), lv = *reinterpret_cast<const float4 *>(scale + 4);
-                        const float ksc[4] = {ks.x, ks.y, ks.z, ks.w}, lvs[4] = {lv.x, lv.y, lv.z, lv.w};
-                        if (!all_seen) {
-                            // a score that the row does not see becomes -infinity
-                            const int tok0 = w.token();
+                    // scores of row k at tokens 8 i + 2 t, + 1: s[4 i + 2 k], + 1
+                    float s[32];
+                    tmem_ld_16x64(part16 + L::S + 64 * sb, s);
+                    tc_fence_before();
+                    arrive(&sm.s_read[sb]);
+                    const float4 ks = *reinterpret_cast<const float4 *>(scale), lv = *reinterpret_cast<const float4 *>(scale + 4);
+                    const float ksc[4] = {ks.x, ks.y, ks.z, ks.w}, lvs[4] = {lv.x, lv.y, lv.z, lv.w};
+                    if (!all_seen) {
+                        // a score that the row does not see becomes -infinity
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            unsigned long long seen = low_bits(pos[k] - tok0 + 1);
+                            if (p.window != 0) seen &= ~low_bits(pos[k] - min(p.window, max(pos[k], 0) + 1) - tok0 + 1) | low_bits(p.sinks - tok0);
+                            seen >>= 2 * t;
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
 #pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (!sees(pos[e / 2], tok0 + 8 * i + 2 * t + (e & 1), p.window, p.sinks)) s[4 * i + e] = -INFINITY;
+                                for (int e = 0; e < 2; ++e)
+                                    if (!(seen >> (8 * i + e) & 1)) s[4 * i + 2 * k + e] = -INFINITY;
                         }
+                    }
+                    const bool first = raise;
+                    for (;;) {
                         if (raise) {
                             float top[2] = {-INFINITY, -INFINITY}, c[2];
 #pragma unroll
@@ -367,7 +398,7 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                                 l[k] *= c[k];
                             }
                             if (!first) {
-                                wait(&sm.s_free[q][(u - 1) % SB], (u - 1) / SB);     // the output product of the unit before
+                                wait(&sm.p_free[number(u - 1) % PR], number(u - 1) / PR);     // the output product of the unit before
                                 tc_fence_after();
 #pragma unroll 1
                                 for (int k = 0; k < D / 32; ++k) {
@@ -434,16 +465,19 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                                 if (sum[k][3] != 0.f) l[k] = fmaf(sum[k][3], rvv.w, l[k]);
                             }
                         }
-                        tmem_st_16x32b(s_tm, x);
+                        if (n >= PR) {       // the output product that read this buffer before
+                            wait(&sm.p_free[pb], n / PR - 1);
+                            tc_fence_after();
+                        }
+                        tmem_st_16x32b(part16 + L::P + 32 * pb, x);
                         break;
                     }
                     tmem_st_wait();
                     tc_fence_before();
-                    arrive(&sm.p_full[q][buf]);
-                    if (++buf == SB) buf = 0, phase ^= 1;
+                    arrive(&sm.p_full[pb]);
                 }
                 // ---- the segment's end: sums over the rows' lanes, then thread = row and every second 32 columns of O
-                const bool whole = begun && w.j == w.tiles;
+                const bool whole = begun && w.j == w.it.tiles;
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
@@ -456,12 +490,12 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                 named_barrier(1 + 4 * q + quadrant, 64);       // the quadrant's two warps
                 // The last output product (a barrier for all units in turn would not do here: it may be two phases behind, which
                 // looks like one ahead)
-                wait(&sm.s_free[q][(u_end - 1) % SB], (u_end - 1) / SB);
+                wait(&sm.p_free[number(u_end - 1) % PR], number(u_end - 1) / PR);
                 tc_fence_after();
-                const int row = 128 * q + 32 * quadrant + lane, grow = w.mt * ROWS + row, i = grow / group;
-                const bool valid = i < w.s.qlen;
+                const int row = 128 * q + 32 * quadrant + lane, grow = w.it.mt * ROWS + row, i = grow / group;
+                const bool valid = i < w.it.qlen;
                 const float sum = sm.row_l[row], inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-                const size_t out_row = ((size_t)(w.s.q0 + (valid ? i : 0)) * p.hq + w.h * group + grow % group) * D;
+                const size_t out_row = ((size_t)(w.it.q0 + (valid ? i : 0)) * p.hq + w.it.h * group + grow % group) * D;
                 float *part = plan.parts + (size_t)(2 * cta + seg_slot) * (ROWS * D + 2 * ROWS);
 #pragma unroll 1
                 for (int k = half; k < D / 32; k += 2) {
@@ -485,13 +519,13 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                 tc_fence_before();
                 named_barrier(1 + 4 * q + quadrant, 64);       // row_m and row_l are free again
                 if (begun && !whole) {
-                    const long long left = (long long)w.tiles - w.j;
+                    const long long left = (long long)w.it.tiles - w.j;
                     mm.first = cta;
                     mm.slot = seg_slot;
                     mm.last = cta + (int)((left + per - 1) / per);
-                    mm.n = w.n;
-                    mm.h = w.h;
-                    mm.mt = w.mt;
+                    mm.n = w.it.n;
+                    mm.h = w.it.h;
+                    mm.mt = w.it.mt;
                 }
                 if (u < units) w.next_item();
             }
@@ -511,119 +545,41 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
         // K's columns stand in the order in which a query row's 32-element pieces enter TMEM: components 8 t + 0..3
         // at 4 t, components 8 t + 4..7 at 16 + 4 t (t = 0..3)
         const uint32_t k_lo = sw128_offset(r, 32 * (c16 >> 1) + 8 * (c16 & 1)), k_hi = sw128_offset(r, 32 * (c16 >> 1) + 16 + 8 * (c16 & 1));
-        // lanes 0 and 1 of the even warps, which stand in their block's first row, bring its K and its V scale
-        const bool scaler = (lw & 1) == 0 && lane < 2;
         auto wait = [&](uint64_t *bar, int phase) {
             if (lw == 0) poll(bar, phase);
             named_barrier(1 + 4 * NQ + lg, 256);
         };
-        if (units > 0) {
-            Walk<ROWS> w(p, plan, group);
-            // where the next tile begins: unit u; it holds `held` units, of one item
-            int u = 0, held = min(min(LU, w.tiles - w.j), units);
-            auto skip = [&]() {
-                u += held;
-                if (u >= units) return;
-                w.j += held;
-                if (w.j == w.tiles) w.next_item();
-                held = min(min(LU, w.tiles - w.j), units - u);
-            };
-            bool held_row[LU];                     // whether this thread's rows in the tile that `w` is at exist,
-            int entry[LU], in_page[LU], head = 0;   // and their table entries and places in the pages
-            auto look_up = [&]() {
-                head = w.h;
+        const int in_block = r % kKvBlock;
+        for (int tile = lg; tile * LU < units; tile += L::LG) {
+            // the tile's codes are asked for; they are on their way while its place is waited for
+            const int u = tile * LU, st = tile % kStages, ph = tile / kStages + 1;
+            if (u % kSlotGroup < LU * L::LG) wait(&sm.slots_full[u / kSlotGroup % (kSlots / kSlotGroup)], u / kSlots);
+            bool there[LU], missing = false;
+            uint4 kr[LU * CH], vr[LU * CH];
 #pragma unroll
-                for (int i = 0; i < LU; ++i) {
-                    held_row[i] = false;
-                    const int tok = i < held ? w.it.token(w.j + i, kTile) + r : 0;
-                    if (i >= held || tok >= w.s.kvlen) continue;
-                    const int at = p.pool.page_of(tok);
-                    in_page[i] = tok - at * p.pool.page_size;
-                    held_row[i] = true;                    // its entry is looked at when the tile's turn comes
-                    entry[i] = __ldg(p.pool.table + (size_t)w.n * p.pool.max_pages + at);
-                }
-            };
-            auto fetch = [&](const uint8_t *pages, const int (&row)[LU], uint4 (&x)[LU * CH]) {
+            for (int i = 0; i < LU; ++i) {
+                const int2 block = sm.block[(u + i) % kSlots][lw / 2];
+                there[i] = in_block < block.y && u + i < units;
+                missing |= !there[i];
+                const size_t at = (size_t)(there[i] ? block.x + in_block : 0) * D + 16 * c16;
 #pragma unroll
-                for (int i = 0; i < LU; ++i)
+                for (int c = 0; c < CH; ++c) kr[i * CH + c] = __ldg(reinterpret_cast<const uint4 *>(p.k_pages + at + 64 * c));
 #pragma unroll
-                    for (int c = 0; c < CH; ++c)
-                        x[i * CH + c] = __ldg(reinterpret_cast<const uint4 *>(pages + (size_t)max(row[i], 0) * D + 16 * c16 + 64 * c));
-            };
-            auto put = [&](uint8_t *tile, const uint4 (&x)[LU * CH], uint32_t lo, uint32_t hi, bool keys) {
-                const uint32_t at = smem_u32(tile);
-#pragma unroll
-                for (int i = 0; i < LU; ++i)
-#pragma unroll
-                    for (int c = 0; c < CH; ++c) {
-                        const uint4 z = x[i * CH + c];
-                        uint32_t y[8];
-                        codes_to_f16x2<FMT>(z.x, y[0], y[1]);
-                        codes_to_f16x2<FMT>(keys ? z.z : z.y, y[2], y[3]);
-                        codes_to_f16x2<FMT>(keys ? z.y : z.z, y[4], y[5]);
-                        codes_to_f16x2<FMT>(z.w, y[6], y[7]);
-                        const uint32_t a = at + c * L::CHUNK + i * (kTile * 128);
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a + lo), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a + hi), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7]) : "memory");
-                    }
-                fence_proxy_async_smem();
-            };
-            int tile = 0;                          // of this group: lg, lg + 2, ...
-            if (lg == 1) {
-                skip();
-                tile = 1;
+                for (int c = 0; c < CH; ++c) vr[i * CH + c] = __ldg(reinterpret_cast<const uint4 *>(p.v_pages + at + 64 * c));
             }
-            look_up();
-            while (u < units) {
-                // this tile's codes and scales are asked for, then the table's entries of the group's next one
-                const int u_now = u, held_now = held, st = tile % kStages, ph = tile / kStages + 1;
-                int row[LU];
-                bool missing = false;
-                uint4 kr[LU * CH], vr[LU * CH];
-                float scale[LU];
+            wait(&sm.k_empty[st], ph);
+            if (__any_sync(0xffffffffu, missing)) {       // rows that do not exist become zeros
 #pragma unroll
-                for (int i = 0; i < LU; ++i) {
-                    row[i] = -1;
-                    if (held_row[i]) {
-                        if ((unsigned)entry[i] < (unsigned)p.pool.n_pages) row[i] = (entry[i] * p.pool.hkv + head) * p.pool.page_size + in_page[i];
-                        else raise_error(p.err, kErrInternal);
-                    }
-                    missing |= row[i] < 0;
-                    scale[i] = scaler && row[i] >= 0 ? __ldg((lane == 0 ? p.k_scales : p.v_scales) + row[i] / kKvBlock) : 0.f;
-                }
-                fetch(p.k_pages, row, kr);
-                fetch(p.v_pages, row, vr);
-#pragma unroll
-                for (int i = 0; i < L::LG; ++i)
-                    if (u < units) skip();
-                if (u < units) look_up();
-                tile += L::LG;
-                wait(&sm.k_empty[st], ph);
-                if (scaler) {
-#pragma unroll
-                    for (int i = 0; i < LU; ++i) {
-                        if (i >= held_now) break;
-                        float *slot = sm.scale[(u_now + i) % kScaleSlots] + lw / 2;
-                        if (lane == 0) {
-                            slot[0] = scale[i];
-                        } else {
-                            const float x = scale[i] == 0.f ? kAmaxFloor : scale[i];
-                            slot[4] = log2f(x);
-                            slot[8] = 1.f / x;
-                        }
-                    }
-                }
-                if (__any_sync(0xffffffffu, missing)) {       // rows that do not exist become zeros
-#pragma unroll
-                    for (int i = 0; i < LU * CH; ++i)
-                        if (row[i / CH] < 0) kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
-                }
-                put(sm.k[st], kr, k_lo, k_hi, true);
-                arrive(&sm.k_full[st]);
-                wait(&sm.v_empty[st], ph);
-                put(sm.v[st], vr, v_lo, v_hi, false);
-                arrive(&sm.v_full[st]);
+                for (int i = 0; i < LU * CH; ++i)
+                    if (!there[i / CH]) kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
             }
+            put_codes<D, FMT, true>(smem_u32(sm.k[st]) + k_lo, smem_u32(sm.k[st]) + k_hi, kr);
+            fence_proxy_async_smem();
+            arrive(&sm.k_full[st]);
+            wait(&sm.v_empty[st], ph);
+            put_codes<D, FMT, false>(smem_u32(sm.v[st]) + v_lo, smem_u32(sm.v[st]) + v_hi, vr);
+            fence_proxy_async_smem();
+            arrive(&sm.v_full[st]);
         }
     } else {
         set_max_registers<L::REGS_OTHER, L::REGS_LAUNCH>();
@@ -633,14 +589,15 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
         // thread for both products leaves the tensor pipe idle during each of its waits.  Of the items only their ends
         // matter here: units left of this one, the next one's read ahead.
         if (role < 2 && units > 0 && elect_one()) {
-            int item = plan.start[cta].item, left = plan.items[item].w - plan.start[cta].j, next_left = 0;
-            if (left < units) next_left = plan.items[item + 1].w;
-            int st = 0, ph = 0, sub = 0, buf = 0, buf_phase = 0, seg = 0;   // of unit u: its load tile's stage, its place there
+            int item = plan.start[cta].item, left = plan.items[item].tiles - plan.start[cta].j, next_left = 0;
+            if (left < units) next_left = plan.items[item + 1].tiles;
+            int st = 0, ph = 0, sub = 0, seg = 0;   // of unit u: its load tile's stage, its place there
+            int ring = 0, ring_phase = 0;           // of the next product: its buffer in its ring
             bool first = true;
             for (int u = 0; u < units; ++u) {
-                const bool ends = left == 1, tile_ends = ends || sub == L::LU - 1 || u == units - 1;
+                const bool ends = left == 1, tile_ends = sub == L::LU - 1 || u == units - 1;
                 if (role == 0) {
-                    // S = Q K^T.  A buffer is free once the output product has read the weights that took its place.
+                    // S = Q K^T.  A buffer is free once the softmax warps have its scores in registers.
                     if (sub == 0) poll(&sm.k_full[st], ph);
                     constexpr uint32_t id = idesc_f16_f32(128, kTile, false, false);
                     const uint64_t kd = smem_desc(smem_u32(sm.k[0]), 16, 1024, kLayoutSwizzle128B) +
@@ -648,13 +605,14 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
 #pragma unroll
                     for (int q = 0; q < NQ; ++q) {
                         if (first) poll(&sm.q_full[q], seg);
-                        poll(&sm.s_free[q][buf], buf_phase ^ 1);
+                        poll(&sm.s_read[ring], ring_phase ^ 1);
                         tc_fence_after();
-                        const uint32_t d = tmem + L::S + (q * SB + buf) * 64, a = tmem + L::Q + q * (D / 2);
+                        const uint32_t d = tmem + L::S + 64 * ring, a = tmem + L::Q + q * (D / 2);
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k) mma_tmem_a(d, a + 8 * k, kd + ((k >> 2) * L::CHUNK >> 4) + 2 * (k & 3), id, k > 0);
-                        mma_commit(&sm.s_full[q][buf]);
-                        mbar_arrive(&sm.s_full[q][buf]);   // the block scales, which this thread has waited for, are visible too
+                        mma_commit(&sm.s_full[q][u & 1]);
+                        mbar_arrive(&sm.s_full[q][u & 1]);   // the block scales, which this thread has waited for, are visible too
+                        if (++ring == SR) ring = 0, ring_phase ^= 1;
                     }
                     if (tile_ends) mma_commit(&sm.k_empty[st]);
                 } else {
@@ -665,36 +623,79 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                                         ((st * L::TILE_BYTES + sub * (kTile * 128)) >> 4);
 #pragma unroll
                     for (int q = 0; q < NQ; ++q) {
-                        poll(&sm.p_full[q][buf], buf_phase);
+                        poll(&sm.p_full[ring], ring_phase);
                         tc_fence_after();
-                        const uint32_t a = tmem + L::S + (q * SB + buf) * 64;
+                        const uint32_t a = tmem + L::P + 32 * ring;
 #pragma unroll
                         for (int k = 0; k < kTile / 16; ++k) mma_tmem_a(tmem + L::O + q * D, a + 8 * k, vd + 128 * k, id, !(first && k == 0));
-                        mma_commit(&sm.s_free[q][buf]);
+                        mma_commit(&sm.p_free[ring]);
+                        if (++ring == PR) ring = 0, ring_phase ^= 1;
                     }
                     if (tile_ends) mma_commit(&sm.v_empty[st]);
+                    // the softmax warps have read the slots of all units up to this one
+                    if (u % kSlotGroup == kSlotGroup - 1) mbar_arrive(&sm.slots_free[u / kSlotGroup % (kSlots / kSlotGroup)]);
                 }
                 ++sub;
                 if (tile_ends) {
                     sub = 0;
                     if (++st == kStages) st = 0, ph ^= 1;
                 }
-                if (++buf == SB) buf = 0, buf_phase ^= 1;
                 first = ends;
                 --left;
                 if (ends) {
                     ++seg;
                     ++item;
                     left = next_left;
-                    if (u + 1 + left < units) next_left = plan.items[item + 1].w;
+                    if (u + 1 + left < units) next_left = plan.items[item + 1].tiles;
                 }
             }
             // every MMA has finished before the tensor memory is given back
             mma_commit(&sm.drain[role]);
-            if (!mbar_wait(&sm.drain[role], 0)) raise_error(p.err, kErrTimeout);
+            poll(&sm.drain[role], 0);
+        } else if (role == 2 && units > 0) {
+            // -------------------------------------------------------------------------------------- look-up
+            // Eight units at a time, a lane to a block of 16 tokens: its place in the pool and its scales.
+            const int b = lane & 3;
+            const RunStart start = plan.start[cta];
+            int item = start.item, j = start.j;
+            TcItem it = plan.items[item];
+            bool bad = false;                       // an entry outside the pool
+            j += lane >> 2;
+            for (int g = 0; g * kSlotGroup < units; ++g, j += kSlotGroup) {
+                const int u = g * kSlotGroup + (lane >> 2);
+                int2 block = make_int2(-1, 0);
+                float ks = 0.f, vs = 0.f;
+                if (u < units) {
+                    while (j >= it.tiles) {
+                        j -= it.tiles;
+                        it = plan.items[++item];
+                    }
+                    const int tok = first_token(it, j) + kKvBlock * b;
+                    if (tok < it.kvlen) {
+                        const int at = p.pool.page_of(tok), entry = __ldg(p.pool.table + (size_t)it.n * p.pool.max_pages + at);
+                        if ((unsigned)entry < (unsigned)p.pool.n_pages) {
+                            block = make_int2((entry * p.pool.hkv + it.h) * p.pool.page_size + tok - at * p.pool.page_size, min(it.kvlen - tok, kKvBlock));
+                            ks = __ldg(p.k_scales + block.x / kKvBlock);
+                            vs = __ldg(p.v_scales + block.x / kKvBlock);
+                        } else {
+                            bad = true;
+                        }
+                    }
+                }
+                if (vs == 0.f) vs = kAmaxFloor;
+                if (u >= kSlots) poll(&sm.slots_free[g % (kSlots / kSlotGroup)], g / (kSlots / kSlotGroup) - 1);
+                float *scale = sm.scale[u % kSlots] + b;
+                scale[0] = ks;
+                scale[4] = log2f(vs);
+                scale[8] = 1.f / vs;
+                sm.block[u % kSlots][b] = block;
+                arrive(&sm.slots_full[g % (kSlots / kSlotGroup)]);
+            }
+            if (bad) raise_error(p.err, kErrInternal);
         }
     }
     __syncthreads();
+    if (tid == 0 && sm.abort) raise_error(p.err, kErrTimeout);
     if (warp == 0) {
         tmem_relinquish();
         tmem_dealloc(tmem, 512);
@@ -716,7 +717,7 @@ TcSizes tc_sizes(int n_seqs, int total, int hq, int hkv, int d, int sms) {
     z.start = round256(kMaxTcCtas * sizeof(MergeMeta));
     z.per = z.start + round256((kMaxTcCtas + 1) * sizeof(RunStart));
     z.list = z.per + 256;
-    z.parts = z.list + round256((size_t)z.items * sizeof(int4));
+    z.parts = z.list + round256((size_t)z.items * sizeof(TcItem));
     z.bytes = z.parts + (size_t)2 * z.ctas * (rows * d + 2 * rows) * sizeof(float);
     return z;
 }
@@ -729,7 +730,7 @@ cudaError_t launch_tc(const AttendProblem &p) {
     plan.meta = reinterpret_cast<MergeMeta *>(ws);
     plan.start = reinterpret_cast<RunStart *>(ws + z.start);
     plan.per = reinterpret_cast<long long *>(ws + z.per);
-    plan.items = reinterpret_cast<int4 *>(ws + z.list);
+    plan.items = reinterpret_cast<TcItem *>(ws + z.list);
     plan.parts = reinterpret_cast<float *>(ws + z.parts);
     plan.ctas = z.ctas;
     constexpr size_t smem = sizeof(TcSmem<D>) + 1024;

@@ -75,21 +75,19 @@ __device__ __forceinline__ bool mbar_spin(uint64_t *bar, uint32_t parity) {
         if (global_timer_ns() - t0 > kWaitTimeoutNs) return false;
     }
 }
-// A bounded wait whose clock is looked at once in 256 polls.  False once kWaitTimeoutNs have passed, with *abort and
-// *timed_out set, or when another thread has set *abort.
-__device__ __forceinline__ bool mbar_poll(uint64_t *bar, uint32_t parity, volatile int *abort, bool *timed_out) {
+// A bounded wait of few instructions, whose clock is looked at only after some thousand polls.  Returns at the phase's end, or
+// with *abort set once kWaitTimeoutNs have passed, or when another thread has set *abort.
+__device__ __forceinline__ void mbar_poll(uint64_t *bar, uint32_t parity, volatile int *abort) {
     uint64_t t0 = 0;
-    for (;;) {
-        for (int i = 0; i < 256; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-        if (*abort) return false;
+    int n = 0;
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        if (++n < 4096) continue;
         const uint64_t now = global_timer_ns();
-        if (t0 == 0) {
-            t0 = now;
-        } else if (now - t0 > kWaitTimeoutNs) {
+        if (t0 == 0) t0 = now;
+        if (*abort || now - t0 > kWaitTimeoutNs) {
             *abort = 1;
-            *timed_out = true;
-            return false;
+            return;
         }
     }
 }
