@@ -354,14 +354,14 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                     const bool all_seen = tok0 < seen_to && (p.window == 0 || tok0 > w.it.hi_pos - p.window || tok0 + kTile <= p.sinks);
                     const float *scale = sm.scale[u % kSlots];
                     wait(&sm.s_full[q][u & 1], u >> 1);
+                    const float4 ks = *reinterpret_cast<const float4 *>(scale), lv = *reinterpret_cast<const float4 *>(scale + 4);
+                    const float ksc[4] = {ks.x, ks.y, ks.z, ks.w}, lvs[4] = {lv.x, lv.y, lv.z, lv.w};
                     tc_fence_after();
                     // scores of row k at tokens 8 i + 2 t, + 1: s[4 i + 2 k], + 1
                     float s[32];
                     tmem_ld_16x64(part16 + L::S + 64 * sb, s);
                     tc_fence_before();
                     arrive(&sm.s_read[sb]);
-                    const float4 ks = *reinterpret_cast<const float4 *>(scale), lv = *reinterpret_cast<const float4 *>(scale + 4);
-                    const float ksc[4] = {ks.x, ks.y, ks.z, ks.w}, lvs[4] = {lv.x, lv.y, lv.z, lv.w};
                     if (!all_seen) {
                         // a score that the row does not see becomes -infinity
 #pragma unroll
@@ -546,8 +546,8 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
         // at 4 t, components 8 t + 4..7 at 16 + 4 t (t = 0..3)
         const uint32_t k_lo = sw128_offset(r, 32 * (c16 >> 1) + 8 * (c16 & 1)), k_hi = sw128_offset(r, 32 * (c16 >> 1) + 16 + 8 * (c16 & 1));
         auto wait = [&](uint64_t *bar, int phase) {
-            if (lw == 0) poll(bar, phase);
-            named_barrier(1 + 4 * NQ + lg, 256);
+            poll(bar, phase);
+            __syncwarp();
         };
         const int in_block = r % kKvBlock;
         for (int tile = lg; tile * LU < units; tile += L::LG) {
