@@ -67,6 +67,15 @@ def _raw_stream(index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index)
 
 
+def _empty(stream, shape, dtype, device) -> torch.Tensor:
+    """Memory for what a call writes, from the pool of the stream that it runs on: memory of another stream could still be
+    in use there, or be given away there while the call runs."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _current_device() -> int:
     return torch._C._cuda_getDevice()
 
@@ -164,7 +173,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cos: Optional[torch.Tensor], sin
         if q.shape[0] != T:
             raise ValueError("q and k must have the same tokens")
         if q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            q_out = _empty(stream, q.shape, q.dtype, q.device)
         qo = _contiguous("q_out", q_out, torch.bfloat16, 3, dev)
         if q_out.shape != q.shape:
             raise ValueError("q_out must have the shape of q")
@@ -191,8 +200,9 @@ def kv_read(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Tensor
     n = cu_tokens.shape[0] - 1
     if block_table.shape[0] != n:
         raise ValueError("cu_tokens and block_table must describe the same sequences")
-    k = torch.empty(total_tokens, hkv, d, dtype=out_dtype, device=k_pages.device)
-    v = torch.empty_like(k)
+    if out_dtype not in DTYPE:
+        raise ValueError("out_dtype must be bf16 or fp32")
+    k, v = (_empty(stream, (total_tokens, hkv, d), out_dtype, k_pages.device) for _ in range(2))
     _launch(lib.gdn_kv_read, "gdn_kv_read", dev, stream, n, total_tokens, hkv, d, cu, *pool, *pages, k.data_ptr(),
             v.data_ptr(), DTYPE[out_dtype])
     return k, v
@@ -231,14 +241,14 @@ def attend(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scal
     if cu_seqlens.shape[0] != n + 1 or block_table.shape[0] != n:
         raise ValueError("cu_seqlens, kv_lens and block_table must describe the same sequences")
     if out is None:
-        out = torch.empty_like(q, dtype=out_dtype)
+        out = _empty(stream, q.shape, out_dtype, q.device)
     op = _contiguous("out", out, out.dtype, 3, dev)
     if out.shape != q.shape or out.dtype not in DTYPE:
         raise ValueError("out must have the shape of q, in bf16 or fp32")
     max_q_len = min(max_q_len, T)
     if workspace is None:
         need = attend_workspace_size(n, T, hq, hkv, d, max_q_len, max_kv_len)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _empty(stream, need, torch.uint8, q.device)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the other tensors' device")
     table, max_pages, n_pages, page, fmt = pool

@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NR>()) attend_split_k
         if (w < warp) upto += sm.scan[w];
         total += sm.scan[w];
     }
-    const int per = max((int)(((unsigned)total + gridDim.x - 1) / gridDim.x), plan.min_units);
+    const int per = max((int)(((unsigned)total + gridDim.x - 1) / gridDim.x), 1);
     const int start = (int)min((long long)cta * per, (long long)total), stop = min(total - start, per) + start;
     if (tid == 0 && !plan.meta_by_item) plan.meta[cta].last = -1;
     if (tid == 0) report_lengths(p, cta);
@@ -622,9 +622,8 @@ cudaError_t launch_split(const AttendProblem &p) {
     const long long fit = (long long)multiprocessor_count() * ctas_per_sm<D, NR>();
     SplitPlan plan{};
     plan.mt_max = row_tiles<8 * NR>(p.max_q_len, group);
-    plan.min_units = 1;
     const long long items = (long long)p.n_seqs * p.pool.hkv * plan.mt_max;
-    const int ctas = (int)min((bound + plan.min_units - 1) / plan.min_units, min(fit, (long long)kMaxSplitCtas));
+    const int ctas = (int)min(bound, min(fit, (long long)kMaxSplitCtas));
     // Few items in many parts: the merge goes by item, with a CTA for each piece of its rows.  Otherwise by the CTAs that
     // items cross, one CTA for all of an item's rows (64 sequences of 8 heads: 17 us by item, 5 us so).
     plan.meta_by_item = 4 * items <= ctas;

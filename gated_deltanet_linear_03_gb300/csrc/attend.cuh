@@ -20,7 +20,7 @@ constexpr size_t kMetaBytes = (kMaxSplitCtas * sizeof(MergeMeta) + 255) / 256 * 
 struct SplitPlan {
     MergeMeta *meta;      // by item where the items are at most the CTAs, else by first CTA
     float *parts;         // two slots a CTA: its first segment, and one that starts later in its range
-    int meta_by_item, mt_max, min_units;
+    int meta_by_item, mt_max;
 };
 
 // A sequence as the kernels see it: first query row, queries, cached tokens (cut to the call's bounds).

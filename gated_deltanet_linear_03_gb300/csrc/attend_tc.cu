@@ -89,6 +89,7 @@ struct TcPlan {
     TcItem *items;
     float *parts;
     int ctas;
+    int max_items;         // that the list has room for: all that sequences in order within `total` rows can have
 };
 
 __host__ __device__ inline size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -144,6 +145,8 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
         first[tid] = block_scan(row_tiles<ROWS>(s.qlen, group) * p.pool.hkv, sum, part);
         if (tid == 0) first[batch] = sum;
         __syncthreads();
+        if (tid == 0 && sum > plan.max_items - items) raise_error(p.err, kErrInternal);
+        sum = min(sum, plan.max_items - items);
         for (int k = tid; k < sum; k += kPlanThreads) {
             int lo = 0;
             for (int hi = batch; hi - lo > 1;) {
@@ -733,6 +736,7 @@ cudaError_t launch_tc(const AttendProblem &p) {
     plan.items = reinterpret_cast<TcItem *>(ws + z.list);
     plan.parts = reinterpret_cast<float *>(ws + z.parts);
     plan.ctas = z.ctas;
+    plan.max_items = (int)min(z.items, 2147483647LL);
     constexpr size_t smem = sizeof(TcSmem<D>) + 1024;
     static std::atomic<bool> ready[kMaxDevices];
     int dev = 0;

@@ -9,7 +9,7 @@ from typing import Optional, Tuple, Union
 
 import torch
 
-from .attn import _contiguous, _device, _launch
+from .attn import _contiguous, _device, _empty, _launch
 from .gdn import DTYPE, load_library
 
 GATE_ACT = {"sigmoid": 0, "silu": 1}
@@ -38,9 +38,9 @@ def block_norm(x: torch.Tensor, residual: torch.Tensor, pre_weight: torch.Tensor
     if res not in DTYPE:
         raise ValueError(f"residual must be bf16 or fp32, got {res}")
     if residual_out is None:
-        residual_out = torch.empty_like(residual)
+        residual_out = _empty(stream, residual.shape, res, residual.device)
     if out is None:
-        out = torch.empty_like(x)
+        out = _empty(stream, x.shape, x.dtype, x.device)
     if residual.shape != shape or residual_out.shape != shape or out.shape != shape or (gate is not None and gate.shape != shape):
         raise ValueError("x, gate, residual and the outputs must have one shape")
     scaled = isinstance(scale, torch.Tensor)
