@@ -605,14 +605,15 @@ bool pool_map(CUtensorMap *m, const uint8_t *pages, const KvPool &pool, int d) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Query rows of an item: the group's heads of one token where they are at most 8 and alone, else 16.
+// Query rows of an item: 8 where no sequence has more (a head group's single tokens), else 16, of which half would idle there
+// (8 rows: 2 heads x 32768 tokens of d = 256 16.5 us as 8, 21 us as 16; 16 x 8 heads x 8192 tokens of d = 128 62 / 79 us).
 int item_rows(int group, int max_q_len) { return (long long)group * max_q_len <= 8 ? 8 : 16; }
 
 long long unit_bound(int n_seqs, int hq, int hkv, int max_q_len, int max_kv_len) {
     const int group = hq / hkv, rows = item_rows(group, max_q_len);
     const long long mts = ((long long)max_q_len * group + rows - 1) / rows;
     const long long tiles = max_kv_len > 0 ? (max_kv_len + kTile - 1) / kTile : 1;
-    return n_seqs * (long long)hkv * mts * tiles;
+    return (long long)min((double)n_seqs * hkv * mts * tiles, 4e18);   // far above what is accepted, and no overflow
 }
 
 template <int D, int FMT, int NR>
@@ -657,25 +658,35 @@ cudaError_t launch_split(const AttendProblem &p) {
     return item_rows(p.hq / p.pool.hkv, p.max_q_len) == 8 ? launch_split<D, FMT, 1>(p) : launch_split<D, FMT, 2>(p);
 }
 
-// The tensor-core kernel (attend_tc.cu) for more query rows than four of this kernel's items.
-bool use_tensor_kernel(int group, int max_q_len) { return (long long)group * max_q_len > 64; }
+// The tensor-core kernel (attend_tc.cu) reads the cache once for 128 (d = 256) or 256 query rows, this one for 16, but it
+// has a planning launch, a longer pipeline to fill and larger parts to join.  By query rows of a key/value head and, where few, by
+// this kernel's units of work.  Measured, us here / there:
+//   d = 256: 2 heads x 2048 tokens   64 rows 13 / 30   256 rows 28 / 35     16 x 2 heads x 8192   16 rows 57 / 56   32 rows 95 / 57
+//            2 heads x 32768 tokens  64 rows 45 / 54    96 rows 62 / 58
+//   d = 128: 8 heads x 2048 tokens   64 rows 20 / 23   128 rows 28 / 25     16 x 8 heads x 8192   32 rows 144 / 189 64 rows 272 / 191
+//            8 heads x 32768 tokens  48 rows 62 / 63    64 rows 79 / 64
+bool use_tensor_kernel(int n_seqs, int hq, int hkv, int d, int max_q_len, int max_kv_len) {
+    const long long rows = (long long)(hq / hkv) * max_q_len, units = unit_bound(n_seqs, hq, hkv, max_q_len, max_kv_len);
+    if (d == 256) return rows > 256 || (rows > 16 && units >= 6000);
+    return rows > 64 || (rows > 48 && units >= 12000);
+}
 
 }  // namespace
 
 size_t attend_workspace_bytes(int n_seqs, int total, int hq, int hkv, int d, int max_q_len, int max_kv_len) {
     if (n_seqs == 0 || total == 0) return 0;
-    if (use_tensor_kernel(hq / hkv, max_q_len)) return attend_tc_workspace_bytes(n_seqs, total, hq, hkv, d);
+    if (use_tensor_kernel(n_seqs, hq, hkv, d, max_q_len, max_kv_len)) return attend_tc_workspace_bytes(n_seqs, total, hq, hkv, d);
     const int rows = item_rows(hq / hkv, max_q_len);
     const long long slots = 2 * min(unit_bound(n_seqs, hq, hkv, max_q_len, max_kv_len), (long long)kMaxSplitCtas);
     return kMetaBytes + (size_t)slots * (rows * d + 2 * rows) * sizeof(float);
 }
 
-bool attend_supported(int n_seqs, int hq, int hkv, int max_q_len, int max_kv_len) {
-    return use_tensor_kernel(hq / hkv, max_q_len) || unit_bound(n_seqs, hq, hkv, max_q_len, max_kv_len) < 2147483647LL;
+bool attend_supported(int n_seqs, int hq, int hkv, int d, int max_q_len, int max_kv_len) {
+    return use_tensor_kernel(n_seqs, hq, hkv, d, max_q_len, max_kv_len) || unit_bound(n_seqs, hq, hkv, max_q_len, max_kv_len) < 2147483647LL;
 }
 
 cudaError_t launch_attend(const AttendProblem &p) {
-    if (use_tensor_kernel(p.hq / p.pool.hkv, p.max_q_len)) return launch_attend_tc(p);
+    if (use_tensor_kernel(p.n_seqs, p.hq, p.pool.hkv, p.d, p.max_q_len, p.max_kv_len)) return launch_attend_tc(p);
     const bool e4m3 = p.format == GDN_KV_E4M3;
     switch (p.d) {
         case 64: return e4m3 ? launch_split<64, GDN_KV_E4M3>(p) : launch_split<64, GDN_KV_INT8>(p);

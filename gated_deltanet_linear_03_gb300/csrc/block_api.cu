@@ -174,7 +174,7 @@ static gdn_status check_attend_shape(int n_seqs, int total_tokens, int hq, int h
     if (hq % hkv != 0 || (total_tokens > 0 && max_q_len == 0)) return GDN_ERR_INVALID_ARG;
     if (d != 64 && d != 128 && d != 256) return GDN_ERR_UNSUPPORTED;
     if ((double)total_tokens * hq >= 2147483648.0 - 4096) return GDN_ERR_UNSUPPORTED;   // the kernels count query rows in 32 bits
-    if (!gdn::attend_supported(n_seqs, hq, hkv, max_q_len, max_kv_len)) return GDN_ERR_UNSUPPORTED;         // and units of work
+    if (!gdn::attend_supported(n_seqs, hq, hkv, d, max_q_len, max_kv_len)) return GDN_ERR_UNSUPPORTED;         // and units of work
     return GDN_OK;
 }
 

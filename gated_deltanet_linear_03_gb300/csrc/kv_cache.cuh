@@ -128,7 +128,7 @@ struct AttendProblem {
 };
 cudaError_t launch_attend(const AttendProblem &p);
 size_t attend_workspace_bytes(int n_seqs, int total, int hq, int hkv, int d, int max_q_len, int max_kv_len);
-bool attend_supported(int n_seqs, int hq, int hkv, int max_q_len, int max_kv_len);
+bool attend_supported(int n_seqs, int hq, int hkv, int d, int max_q_len, int max_kv_len);
 // the tensor-core kernel, for many query rows
 cudaError_t launch_attend_tc(const AttendProblem &p);
 size_t attend_tc_workspace_bytes(int n_seqs, int total, int hq, int hkv, int d);
