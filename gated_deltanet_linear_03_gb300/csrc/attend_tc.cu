@@ -61,7 +61,6 @@ struct __align__(1024) TcSmem {
     uint8_t v[kStages][Tc<D>::TILE_BYTES];
     float scale[kSlots][12];             // of a unit's 4 blocks: K scales, log2 of V scales, reciprocals of V scales
     int2 block[kSlots][4];               // and their first rows in the pool (-1: none), and how many tokens they hold
-    float row_m[Tc<D>::ROWS], row_l[Tc<D>::ROWS];   // at an item's end
     uint64_t slots_full[kSlots / kSlotGroup], slots_free[kSlots / kSlotGroup];
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
     uint64_t s_full[NQ][2], s_read[Tc<D>::SR], p_full[Tc<D>::PR], p_free[Tc<D>::PR], q_full[NQ], drain[2];
@@ -209,26 +208,21 @@ __device__ __forceinline__ void put_codes(uint32_t lo, uint32_t hi, const uint4 
     if constexpr (N + 1 < Tc<D>::LU * CH) put_codes<D, FMT, KEYS, N + 1>(lo, hi, x);
 }
 
-// The first token of an item's unit j.
-__device__ __forceinline__ int first_token(const TcItem &it, int j) { return (j < it.near_tiles ? j : it.far_tile + j - it.near_tiles) * kTile; }
+// 4 x 4 words of 4 neighbouring lanes, lane t's word i becoming lane i's word t.
+__device__ __forceinline__ void transpose4(uint32_t (&y)[4], int t) {
+#pragma unroll
+    for (int s = 1; s <= 2; s <<= 1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & s) continue;
+            const uint32_t r = __shfl_xor_sync(0xffffffffu, t & s ? y[i] : y[i + s], s);
+            if (t & s) y[i] = r;
+            else y[i + s] = r;
+        }
+}
 
-// Where a role stands in its CTA's run; every role keeps its own.
-struct Walk {
-    const TcPlan &plan;
-    int item, j;
-    TcItem it;
-    __device__ __forceinline__ explicit Walk(const TcPlan &plan_) : plan(plan_) {
-        const RunStart st = plan.start[blockIdx.x];
-        item = st.item;
-        it = plan.items[item];
-        j = st.j;
-    }
-    // to the next item (which the run must hold)
-    __device__ __forceinline__ void next_item() {
-        it = plan.items[++item];
-        j = 0;
-    }
-};
+// The first token of unit j of an item with these fields.
+__device__ __forceinline__ int first_token(int near_tiles, int far_tile, int j) { return (j < near_tiles ? j : far_tile + j - near_tiles) * kTile; }
 
 template <int D, int FMT>
 __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __grid_constant__ AttendProblem p,
@@ -295,32 +289,47 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
             poll(bar, phase);
             __syncwarp();
         };
-        MergeMeta mm;
-        mm.last = -1;
+        if (tid == 0) plan.meta[cta].last = -1;
         if (units > 0) {
-            Walk w(plan);
+            int item = plan.start[cta].item, j = plan.start[cta].j;      // the item, and its unit that is next
             // the product number (unit u, tile q) in both rings: number % SR, number % PR
             auto number = [&](int u) { return u * NQ + q; };
+            // An item's queries, 4 lanes to a row, 16 bytes each.  Their lines are brought into L2 while the item before writes
+            // its outputs; then the first pass finds the rows' scales, the second (from L1) converts.
+            const uint4 *src[2] = {nullptr, nullptr};
+            auto piece = [&](int k, int c) { return src[k] ? __ldg(src[k] + 4 * c) : make_uint4(0, 0, 0, 0); };
+            auto ask = [&](const TcItem &it) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int gr = it.mt * ROWS + row0 + 8 * k, i = gr / group;
+                    src[k] = i < it.qlen
+                                 ? reinterpret_cast<const uint4 *>(p.q + ((size_t)(it.q0 + i) * p.hq + it.h * group + gr % group) * D) + t
+                                 : nullptr;
+                    if (src[k] && t < D / 64) prefetch_l2(src[k] + 7 * t);      // its lines, a lane each
+                }
+            };
+            ask(plan.items[item]);
             for (int u = 0, seg = 0; u < units; ++seg) {
-                // ---- a segment, units of one item: its queries, 4 lanes to a row, 16 bytes each.  The first pass finds the
-                // rows' scales, the second (from L1) converts.
-                const bool begun = w.j == 0;
-                const int seg_slot = u == 0 ? 0 : 1, u_end = min(units, u + w.it.tiles - w.j);
+                // ---- a segment: units of one item
+                // (few of the item's fields stay in registers over its units; at its end they are read again)
+                const int u_first = u, j_first = j;
+                int u_end, seen_to, hi_pos, near_tiles, far_tile;
                 float rs[2];
                 int pos[2];
                 {
-                    const uint4 *src[2];
+                    const TcItem it = plan.items[item];
+                    u_end = min(units, u + it.tiles - j);
+                    seen_to = it.lo_pos + 2 - kTile;                 // units that begin before are in no row's future
+                    hi_pos = it.hi_pos;
+                    near_tiles = it.near_tiles;
+                    far_tile = it.far_tile;
                     float down[2];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const int gr = w.it.mt * ROWS + row0 + 8 * k, i = gr / group;
-                        pos[k] = w.it.kvlen - w.it.qlen + i;
-                        src[k] = i < w.it.qlen
-                                     ? reinterpret_cast<const uint4 *>(p.q + ((size_t)(w.it.q0 + i) * p.hq + w.it.h * group + gr % group) * D) + t
-                                     : nullptr;
+                        pos[k] = it.kvlen - it.qlen + (it.mt * ROWS + row0 + 8 * k) / group;
                         uint32_t big = 0;
 #pragma unroll
-                        for (int c = 0; c < D / 32; ++c) big = max(big, amax_bits(src[k] ? __ldg(src[k] + 4 * c) : make_uint4(0, 0, 0, 0)));
+                        for (int c = 0; c < D / 32; ++c) big = max(big, amax_bits(piece(k, c)));
                         big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
                         big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
                         float up;
@@ -335,7 +344,7 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                         for (int i2 = 0; i2 < 2; ++i2)
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
-                                const uint4 z = src[k] ? __ldg(src[k] + 4 * (2 * c + i2)) : make_uint4(0, 0, 0, 0);
+                                const uint4 z = piece(k, 2 * c + i2);
                                 x[8 * i2 + 2 * k] = bf16x2_to_f16x2(z.x, down[k]);
                                 x[8 * i2 + 2 * k + 1] = bf16x2_to_f16x2(z.y, down[k]);
                                 x[8 * i2 + 4 + 2 * k] = bf16x2_to_f16x2(z.z, down[k]);
@@ -345,16 +354,16 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                     }
                     tmem_st_wait();
                 }
+                if (u_end < units) prefetch_l1(plan.items + item + 1);
                 tc_fence_before();
                 arrive(&sm.q_full[q]);              // also: this warp has read its part of the item before
                 float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
                 bool raise = true;                  // the item's first unit sets M
-                const int seen_to = w.it.lo_pos + 2 - kTile;     // units that begin before are in no row's future
-                for (; u < u_end; ++u, ++w.j) {
+                for (; u < u_end; ++u, ++j) {
                     // ---- one unit
                     const int n = number(u), sb = n % SR, pb = n % PR;
-                    const int tok0 = first_token(w.it, w.j);
-                    const bool all_seen = tok0 < seen_to && (p.window == 0 || tok0 > w.it.hi_pos - p.window || tok0 + kTile <= p.sinks);
+                    const int tok0 = first_token(near_tiles, far_tile, j);
+                    const bool all_seen = tok0 < seen_to && (p.window == 0 || tok0 > hi_pos - p.window || tok0 + kTile <= p.sinks);
                     const float *scale = sm.scale[u % kSlots];
                     wait(&sm.s_full[q][u & 1], u >> 1);
                     const float4 ks = *reinterpret_cast<const float4 *>(scale), lv = *reinterpret_cast<const float4 *>(scale + 4);
@@ -479,61 +488,81 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                     tc_fence_before();
                     arrive(&sm.p_full[pb]);
                 }
-                // ---- the segment's end: sums over the rows' lanes, then thread = row and every second 32 columns of O
-                const bool whole = begun && w.j == w.it.tiles;
+                // ---- the segment's end.  The next item's queries are on their way while this one's outputs are written.
+                int out_row[2];                     // token and head, -1: none
+                bool whole;
+                {
+                    const TcItem it = plan.items[item];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int grow = it.mt * ROWS + row0 + 8 * k, i = grow / group;
+                        out_row[k] = i < it.qlen ? (it.q0 + i) * p.hq + it.h * group + grow % group : -1;
+                    }
+                    whole = j_first == 0 && j == it.tiles;
+                    if (tid == 0 && j_first == 0 && !whole)
+                        plan.meta[cta] = {cta, u_first == 0 ? 0 : 1, cta + (int)(((long long)it.tiles - j + per - 1) / per), it.n, it.h, it.mt};
+                }
+                const bool more = u < units;
+                if (more) {
+                    ++item;
+                    j = 0;
+                    ask(plan.items[item]);
+                }
+                float inv[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
                     l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
-                    if (t == 0) {
-                        sm.row_m[row0 + 8 * k] = m[k];
-                        sm.row_l[row0 + 8 * k] = l[k];
-                    }
+                    inv[k] = whole ? (l[k] == 0.f ? 0.f : 1.f / l[k]) : 1.f;
                 }
-                named_barrier(1 + 4 * q + quadrant, 64);       // the quadrant's two warps
                 // The last output product (a barrier for all units in turn would not do here: it may be two phases behind, which
                 // looks like one ahead)
                 wait(&sm.p_free[number(u_end - 1) % PR], number(u_end - 1) / PR);
                 tc_fence_after();
-                const int row = 128 * q + 32 * quadrant + lane, grow = w.it.mt * ROWS + row, i = grow / group;
-                const bool valid = i < w.it.qlen;
-                const float sum = sm.row_l[row], inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
-                const size_t out_row = ((size_t)(w.it.q0 + (valid ? i : 0)) * p.hq + w.it.h * group + grow % group) * D;
-                float *part = plan.parts + (size_t)(2 * cta + seg_slot) * (ROWS * D + 2 * ROWS);
+                float *part = plan.parts + (size_t)(2 * cta + (u_first == 0 ? 0 : 1)) * (ROWS * D + 2 * ROWS);
 #pragma unroll 1
-                for (int k = half; k < D / 32; k += 2) {
-                    float o[32];
-                    tmem_ld32(quad + o_cols + 32 * k, o);
+                for (int c = 0; c < D; c += 32) {
+                    float o[16];            // columns c + 8 i + 2 t, + 1 of row k: o[4 i + 2 k], + 1
+                    tmem_ld_16x32(part16 + o_cols + c, o);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] *= inv;
-                    if (valid && whole) {
-                        store_row<32>(p, out_row + 32 * k, o);
-                    } else if (valid) {
+                    for (int e = 0; e < 16; ++e) o[e] *= inv[(e >> 1) & 1];
+                    // the 4 lanes of a row exchange, so that each holds 4 (8) neighbouring columns and 16 bytes leave at a time
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4 *>(part + (size_t)row * D + 32 * k + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    for (int k = 0; k < 2; ++k) {
+                        if (whole && !p.out_f32) {
+                            uint32_t y[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const __nv_bfloat162 b = __floats2bfloat162_rn(o[4 * i + 2 * k], o[4 * i + 2 * k + 1]);
+                                y[i] = *reinterpret_cast<const uint32_t *>(&b);
+                            }
+                            transpose4(y, t);
+                            if (out_row[k] >= 0)
+                                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + (size_t)out_row[k] * D + c + 8 * t) = make_uint4(y[0], y[1], y[2], y[3]);
+                            continue;
+                        }
+                        float *to = whole ? static_cast<float *>(p.out) + (size_t)max(out_row[k], 0) * D : part + (size_t)(row0 + 8 * k) * D;
+#pragma unroll
+                        for (int i = 0; i < 4; i += 2) {
+                            const float *a = o + 4 * i + 2 * k, *b = a + 4;
+                            const bool odd = t & 1;
+                            const float r0 = __shfl_xor_sync(0xffffffffu, odd ? a[0] : b[0], 1), r1 = __shfl_xor_sync(0xffffffffu, odd ? a[1] : b[1], 1);
+                            const float4 y = odd ? make_float4(r0, r1, b[0], b[1]) : make_float4(a[0], a[1], r0, r1);
+                            if (out_row[k] >= 0) *reinterpret_cast<float4 *>(to + c + 8 * (i + (t & 1)) + 4 * (t >> 1)) = y;
+                        }
                     }
                     __syncwarp();   // the next load is warp-wide
                 }
-                if (!whole && half == 0) {
-                    part[ROWS * D + row] = sm.row_m[row];
-                    part[ROWS * D + ROWS + row] = sum;
+                if (!whole && t == 0) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        part[ROWS * D + row0 + 8 * k] = m[k];
+                        part[ROWS * D + ROWS + row0 + 8 * k] = l[k];
+                    }
                 }
                 tc_fence_before();
-                named_barrier(1 + 4 * q + quadrant, 64);       // row_m and row_l are free again
-                if (begun && !whole) {
-                    const long long left = (long long)w.it.tiles - w.j;
-                    mm.first = cta;
-                    mm.slot = seg_slot;
-                    mm.last = cta + (int)((left + per - 1) / per);
-                    mm.n = w.it.n;
-                    mm.h = w.it.h;
-                    mm.mt = w.it.mt;
-                }
-                if (u < units) w.next_item();
             }
         }
-        if (tid == 0) plan.meta[cta] = mm;
     } else if (warp < L::SOFTMAX_WARPS + L::LOADER_WARPS) {
         set_max_registers<L::REGS_LOADER, L::REGS_LAUNCH>();
         // ------------------------------------------------------------------------------------------ loaders
@@ -673,7 +702,7 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                         j -= it.tiles;
                         it = plan.items[++item];
                     }
-                    const int tok = first_token(it, j) + kKvBlock * b;
+                    const int tok = first_token(it.near_tiles, it.far_tile, j) + kKvBlock * b;
                     if (tok < it.kvlen) {
                         const int at = p.pool.page_of(tok), entry = __ldg(p.pool.table + (size_t)it.n * p.pool.max_pages + at);
                         if ((unsigned)entry < (unsigned)p.pool.n_pages) {
