@@ -295,9 +295,11 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
             // the product number (unit u, tile q) in both rings: number % SR, number % PR
             auto number = [&](int u) { return u * NQ + q; };
             // An item's queries, 4 lanes to a row, 16 bytes each.  Their lines are brought into L2 while the item before writes
-            // its outputs; then the first pass finds the rows' scales, the second (from L1) converts.
+            // its outputs.  Up to d = 128 a lane holds its pieces over both passes, which find the rows' scales and convert; at
+            // d = 256 that many registers spill (8192-token prompt 592 us against 560), and the second pass reads L1.
+            constexpr bool kHold = D <= 128;
+            constexpr int HELD = kHold ? D / 32 : 1;
             const uint4 *src[2] = {nullptr, nullptr};
-            auto piece = [&](int k, int c) { return src[k] ? __ldg(src[k] + 4 * c) : make_uint4(0, 0, 0, 0); };
             auto ask = [&](const TcItem &it) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
@@ -324,12 +326,19 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                     near_tiles = it.near_tiles;
                     far_tile = it.far_tile;
                     float down[2];
+                    uint4 raw[2][HELD];
+                    auto piece = [&](int k, int c) { return src[k] ? __ldg(src[k] + 4 * c) : make_uint4(0, 0, 0, 0); };
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int c = 0; c < HELD; ++c)
+                            if (kHold) raw[k][c] = piece(k, c);
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         pos[k] = it.kvlen - it.qlen + (it.mt * ROWS + row0 + 8 * k) / group;
                         uint32_t big = 0;
 #pragma unroll
-                        for (int c = 0; c < D / 32; ++c) big = max(big, amax_bits(piece(k, c)));
+                        for (int c = 0; c < D / 32; ++c) big = max(big, amax_bits(kHold ? raw[k][c % HELD] : piece(k, c)));
                         big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
                         big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
                         float up;
@@ -337,14 +346,14 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                         if (p.sm_scale < 0.f) down[k] = -down[k];     // the row factor stays >= 0
                         rs[k] = up * fabsf(p.sm_scale) * 1.4426950408889634f;
                     }
-#pragma unroll 2
+#pragma unroll kHold ? D / 64 : 2
                     for (int c = 0; c < D / 64; ++c) {
                         uint32_t x[16];
 #pragma unroll
                         for (int i2 = 0; i2 < 2; ++i2)
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
-                                const uint4 z = piece(k, 2 * c + i2);
+                                const uint4 z = kHold ? raw[k][(2 * c + i2) % HELD] : piece(k, 2 * c + i2);
                                 x[8 * i2 + 2 * k] = bf16x2_to_f16x2(z.x, down[k]);
                                 x[8 * i2 + 2 * k + 1] = bf16x2_to_f16x2(z.y, down[k]);
                                 x[8 * i2 + 4 + 2 * k] = bf16x2_to_f16x2(z.z, down[k]);
@@ -491,8 +500,11 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                 // ---- the segment's end.  The next item's queries are on their way while this one's outputs are written.
                 int out_row[2];                     // token and head, -1: none
                 bool whole;
+                const bool more = u < units;
+                TcItem next;
                 {
                     const TcItem it = plan.items[item];
+                    if (more) next = plan.items[item + 1];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const int grow = it.mt * ROWS + row0 + 8 * k, i = grow / group;
@@ -502,11 +514,10 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                     if (tid == 0 && j_first == 0 && !whole)
                         plan.meta[cta] = {cta, u_first == 0 ? 0 : 1, cta + (int)(((long long)it.tiles - j + per - 1) / per), it.n, it.h, it.mt};
                 }
-                const bool more = u < units;
                 if (more) {
                     ++item;
                     j = 0;
-                    ask(plan.items[item]);
+                    ask(next);
                 }
                 float inv[2];
 #pragma unroll
