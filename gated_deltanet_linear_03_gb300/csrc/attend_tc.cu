@@ -35,12 +35,9 @@ template <int D>
 struct Tc {
     static constexpr int NQ = D == 256 ? 1 : 2;              // 128-row tiles of a CTA, which share its K and V
     static constexpr int ROWS = 128 * NQ;
-    // TMEM columns: O fp32, Q two fp16 a column, then rings of score buffers (64) and of weight buffers (32, two fp16 a
-    // column).  Scores leave their buffer as soon as they are in registers, so the next score product runs beside the
-    // arithmetic even where one buffer is all that fits.
-    static constexpr int O = 0, Q = NQ * D, S = NQ * (D + D / 2);
-    static constexpr int PR = D == 64 ? 4 : 2, SR = (512 - S - 32 * PR) / 64, P = S + 64 * SR;
-    static_assert(SR >= 1 && P + 32 * PR <= 512 && PR % NQ == 0, "tensor memory");
+    // TMEM columns: O fp32, Q two fp16 a column, then SB buffers a tile of 64 scores, over which the weights are written.
+    static constexpr int O = 0, Q = NQ * D, S = NQ * (D + D / 2), SB = S + NQ * 128 <= 512 ? 2 : 1;
+    static_assert(S + NQ * SB * 64 <= 512, "tensor memory");
     static constexpr int LU = 256 / D;                       // units of a load tile: 16 KB of K codes and 16 KB of V codes
     static constexpr int LG = D == 256 ? 2 : 1;              // groups of 8 loader warps, which take the tiles in turn
     static_assert(kSlotGroup % LU == 0 && 2 * kSlotGroup >= LU * (LG + 1), "a tile's units lie in one group of slots");
@@ -63,7 +60,7 @@ struct __align__(1024) TcSmem {
     int2 block[kSlots][4];               // and their first rows in the pool (-1: none), and how many tokens they hold
     uint64_t slots_full[kSlots / kSlotGroup], slots_free[kSlots / kSlotGroup];
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-    uint64_t s_full[NQ][2], s_read[Tc<D>::SR], p_full[Tc<D>::PR], p_free[Tc<D>::PR], q_full[NQ], drain[2];
+    uint64_t s_full[NQ * Tc<D>::SB], p_full[NQ * Tc<D>::SB], p_free[NQ * Tc<D>::SB], q_full[NQ], drain[2];
     uint32_t tmem;
     int abort;
 };
@@ -228,7 +225,7 @@ template <int D, int FMT>
 __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __grid_constant__ AttendProblem p,
                                                                      const __grid_constant__ TcPlan plan) {
     using L = Tc<D>;
-    constexpr int NQ = L::NQ, SR = L::SR, PR = L::PR, ROWS = L::ROWS;
+    constexpr int NQ = L::NQ, SB = L::SB, ROWS = L::ROWS;
     extern __shared__ uint8_t raw[];
     TcSmem<D> &sm = *reinterpret_cast<TcSmem<D> *>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -242,13 +239,9 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
             mbar_init(&sm.k_empty[i], 1);
             mbar_init(&sm.v_empty[i], 1);
         }
-        for (int q = 0; q < NQ; ++q) {
-            mbar_init(&sm.s_full[q][0], 2);
-            mbar_init(&sm.s_full[q][1], 2);
-            mbar_init(&sm.q_full[q], 8);
-        }
-        for (int b = 0; b < SR; ++b) mbar_init(&sm.s_read[b], 8);
-        for (int b = 0; b < PR; ++b) {
+        for (int q = 0; q < NQ; ++q) mbar_init(&sm.q_full[q], 8);
+        for (int b = 0; b < NQ * SB; ++b) {
+            mbar_init(&sm.s_full[b], 2);
             mbar_init(&sm.p_full[b], 8);
             mbar_init(&sm.p_free[b], 1);
         }
@@ -292,8 +285,9 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
         if (tid == 0) plan.meta[cta].last = -1;
         if (units > 0) {
             int item = plan.start[cta].item, j = plan.start[cta].j;      // the item, and its unit that is next
-            // the product number (unit u, tile q) in both rings: number % SR, number % PR
-            auto number = [&](int u) { return u * NQ + q; };
+            // unit u's score buffer, and which use of it that is
+            auto buffer = [&](int u) { return q * SB + u % SB; };
+            auto use = [&](int u) { return u / SB; };
             // An item's queries, 4 lanes to a row, 16 bytes each.  Their lines are brought into L2 while the item before writes
             // its outputs.  Up to d = 128 a lane holds its pieces over both passes, which find the rows' scales and convert; at
             // d = 256 that many registers spill (8192-token prompt 592 us against 560), and the second pass reads L1.
@@ -370,19 +364,18 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                 bool raise = true;                  // the item's first unit sets M
                 for (; u < u_end; ++u, ++j) {
                     // ---- one unit
-                    const int n = number(u), sb = n % SR, pb = n % PR;
+                    const int buf = buffer(u);
+                    const uint32_t s_tm = part16 + L::S + 64 * buf;
                     const int tok0 = first_token(near_tiles, far_tile, j);
                     const bool all_seen = tok0 < seen_to && (p.window == 0 || tok0 > hi_pos - p.window || tok0 + kTile <= p.sinks);
                     const float *scale = sm.scale[u % kSlots];
-                    wait(&sm.s_full[q][u & 1], u >> 1);
+                    wait(&sm.s_full[buf], use(u));
                     const float4 ks = *reinterpret_cast<const float4 *>(scale), lv = *reinterpret_cast<const float4 *>(scale + 4);
                     const float ksc[4] = {ks.x, ks.y, ks.z, ks.w}, lvs[4] = {lv.x, lv.y, lv.z, lv.w};
                     tc_fence_after();
                     // scores of row k at tokens 8 i + 2 t, + 1: s[4 i + 2 k], + 1
                     float s[32];
-                    tmem_ld_16x64(part16 + L::S + 64 * sb, s);
-                    tc_fence_before();
-                    arrive(&sm.s_read[sb]);
+                    tmem_ld_16x64(s_tm, s);
                     if (!all_seen) {
                         // a score that the row does not see becomes -infinity
 #pragma unroll
@@ -419,7 +412,7 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                                 l[k] *= c[k];
                             }
                             if (!first) {
-                                wait(&sm.p_free[number(u - 1) % PR], number(u - 1) / PR);     // the output product of the unit before
+                                wait(&sm.p_free[buffer(u - 1)], use(u - 1));     // the output product of the unit before
                                 tc_fence_after();
 #pragma unroll 1
                                 for (int k = 0; k < D / 32; ++k) {
@@ -486,16 +479,12 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                                 if (sum[k][3] != 0.f) l[k] = fmaf(sum[k][3], rvv.w, l[k]);
                             }
                         }
-                        if (n >= PR) {       // the output product that read this buffer before
-                            wait(&sm.p_free[pb], n / PR - 1);
-                            tc_fence_after();
-                        }
-                        tmem_st_16x32b(part16 + L::P + 32 * pb, x);
+                        tmem_st_16x32b(s_tm, x);
                         break;
                     }
                     tmem_st_wait();
                     tc_fence_before();
-                    arrive(&sm.p_full[pb]);
+                    arrive(&sm.p_full[buf]);
                 }
                 // ---- the segment's end.  The next item's queries are on their way while this one's outputs are written.
                 int out_row[2];                     // token and head, -1: none
@@ -528,7 +517,7 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                 }
                 // The last output product (a barrier for all units in turn would not do here: it may be two phases behind, which
                 // looks like one ahead)
-                wait(&sm.p_free[number(u_end - 1) % PR], number(u_end - 1) / PR);
+                wait(&sm.p_free[buffer(u_end - 1)], use(u_end - 1));
                 tc_fence_after();
                 float *part = plan.parts + (size_t)(2 * cta + (u_first == 0 ? 0 : 1)) * (ROWS * D + 2 * ROWS);
 #pragma unroll 1
@@ -635,12 +624,12 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
             int item = plan.start[cta].item, left = plan.items[item].tiles - plan.start[cta].j, next_left = 0;
             if (left < units) next_left = plan.items[item + 1].tiles;
             int st = 0, ph = 0, sub = 0, seg = 0;   // of unit u: its load tile's stage, its place there
-            int ring = 0, ring_phase = 0;           // of the next product: its buffer in its ring
+            int buf = 0, buf_phase = 0;             // its score buffer
             bool first = true;
             for (int u = 0; u < units; ++u) {
                 const bool ends = left == 1, tile_ends = sub == L::LU - 1 || u == units - 1;
                 if (role == 0) {
-                    // S = Q K^T.  A buffer is free once the softmax warps have its scores in registers.
+                    // S = Q K^T.  A buffer is free once the output product has read the weights that took its place.
                     if (sub == 0) poll(&sm.k_full[st], ph);
                     constexpr uint32_t id = idesc_f16_f32(128, kTile, false, false);
                     const uint64_t kd = smem_desc(smem_u32(sm.k[0]), 16, 1024, kLayoutSwizzle128B) +
@@ -648,14 +637,13 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
 #pragma unroll
                     for (int q = 0; q < NQ; ++q) {
                         if (first) poll(&sm.q_full[q], seg);
-                        poll(&sm.s_read[ring], ring_phase ^ 1);
+                        poll(&sm.p_free[q * SB + buf], buf_phase ^ 1);
                         tc_fence_after();
-                        const uint32_t d = tmem + L::S + 64 * ring, a = tmem + L::Q + q * (D / 2);
+                        const uint32_t d = tmem + L::S + 64 * (q * SB + buf), a = tmem + L::Q + q * (D / 2);
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k) mma_tmem_a(d, a + 8 * k, kd + ((k >> 2) * L::CHUNK >> 4) + 2 * (k & 3), id, k > 0);
-                        mma_commit(&sm.s_full[q][u & 1]);
-                        mbar_arrive(&sm.s_full[q][u & 1]);   // the block scales, which this thread has waited for, are visible too
-                        if (++ring == SR) ring = 0, ring_phase ^= 1;
+                        mma_commit(&sm.s_full[q * SB + buf]);
+                        mbar_arrive(&sm.s_full[q * SB + buf]);   // the block scales, which this thread has waited for, are visible too
                     }
                     if (tile_ends) mma_commit(&sm.k_empty[st]);
                 } else {
@@ -666,13 +654,12 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                                         ((st * L::TILE_BYTES + sub * (kTile * 128)) >> 4);
 #pragma unroll
                     for (int q = 0; q < NQ; ++q) {
-                        poll(&sm.p_full[ring], ring_phase);
+                        poll(&sm.p_full[q * SB + buf], buf_phase);
                         tc_fence_after();
-                        const uint32_t a = tmem + L::P + 32 * ring;
+                        const uint32_t a = tmem + L::S + 64 * (q * SB + buf);
 #pragma unroll
                         for (int k = 0; k < kTile / 16; ++k) mma_tmem_a(tmem + L::O + q * D, a + 8 * k, vd + 128 * k, id, !(first && k == 0));
-                        mma_commit(&sm.p_free[ring]);
-                        if (++ring == PR) ring = 0, ring_phase ^= 1;
+                        mma_commit(&sm.p_free[q * SB + buf]);
                     }
                     if (tile_ends) mma_commit(&sm.v_empty[st]);
                     // the softmax warps have read the slots of all units up to this one
@@ -683,6 +670,7 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                     sub = 0;
                     if (++st == kStages) st = 0, ph ^= 1;
                 }
+                if (++buf == SB) buf = 0, buf_phase ^= 1;
                 first = ends;
                 --left;
                 if (ends) {
