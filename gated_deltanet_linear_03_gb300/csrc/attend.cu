@@ -659,26 +659,38 @@ cudaError_t launch_split(const AttendProblem &p) {
 }
 
 // The tensor-core kernel (attend_tc.cu) reads the cache once for 128 (d = 256) or 256 query rows, this one for 16, but it
-// has a planning launch, a longer pipeline to fill and larger parts to join.  By query rows of a key/value head and, where few, by
-// this kernel's units of work.  Measured, us here / there:
-//   d = 256: 2 heads x 2048 tokens   64 rows 13 / 30   256 rows 28 / 35     16 x 2 heads x 8192   16 rows 57 / 56   32 rows 95 / 57
-//            2 heads x 32768 tokens  64 rows 45 / 54    96 rows 62 / 58
-//   d = 128: 8 heads x 2048 tokens   64 rows 20 / 23   128 rows 28 / 25     16 x 8 heads x 8192   32 rows 144 / 189 64 rows 272 / 191
-//            8 heads x 32768 tokens  48 rows 62 / 63    64 rows 79 / 64
-bool use_tensor_kernel(int n_seqs, int hq, int hkv, int d, int max_q_len, int max_kv_len) {
-    const long long rows = (long long)(hq / hkv) * max_q_len, units = unit_bound(n_seqs, hq, hkv, max_q_len, max_kv_len);
-    if (d == 256) return rows > 256 || (rows > 16 && units >= 6000);
-    return rows > 64 || (rows > 48 && units >= 12000);
+// has a planning launch, a longer pipeline to fill and larger parts to join.  By query rows of a key/value head and, where these
+// are few, by this kernel's units of work.  Measured, us here / there (sequences x heads x tokens):
+//   d = 256:  1 x 2 x 2048   128 rows 19 / 28   256 rows 28 / 31       1 x 2 x 8192  128 rows 32 / 40  256 rows 52 / 34
+//             1 x 2 x 32768   48 rows 39 / 46    64 rows 46 / 48       4 x 2 x 8192   32 rows 34 / 31   64 rows 53 / 34
+//   d = 128:  1 x 8 x 2048    64 rows 20 / 21   128 rows 28 / 22       4 x 8 x 8192   32 rows 51 / 58   64 rows 77 / 58
+//             1 x 8 x 32768   32 rows 46 / 60    48 rows 63 / 61      16 x 8 x 8192   32 rows 144 / 180 48 rows 209 / 181
+//   d = 64:   1 x 1 x 2048   128 rows 11 / 20   256 rows 15 / 22       4 x 1 x 8192   64 rows 17 / 22  128 rows 25 / 23
+//             1 x 1 x 32768  128 rows 24 / 37   256 rows 39 / 39      16 x 1 x 8192   32 rows 24 / 28   48 rows 33 / 28
+// `tokens` bounds what a row sees.
+bool use_tensor_kernel(int n_seqs, int hq, int hkv, int d, int max_q_len, int tokens) {
+    const long long rows = (long long)(hq / hkv) * max_q_len, units = unit_bound(n_seqs, hq, hkv, max_q_len, tokens);
+    if (d == 256) return rows > 256 || (rows > 16 && units >= 4000);
+    if (d == 128) return rows > 64 || (rows > 32 && units >= 4000);
+    return rows > 256 || (rows > 32 && units >= 6000);
+}
+
+bool use_tensor_kernel(const AttendProblem &p) {
+    const long long tokens = p.window == 0 ? p.max_kv_len : min((long long)p.max_kv_len, (long long)p.window + p.sinks + p.max_q_len);
+    return use_tensor_kernel(p.n_seqs, p.hq, p.pool.hkv, p.d, p.max_q_len, (int)tokens);
 }
 
 }  // namespace
 
 size_t attend_workspace_bytes(int n_seqs, int total, int hq, int hkv, int d, int max_q_len, int max_kv_len) {
     if (n_seqs == 0 || total == 0) return 0;
-    if (use_tensor_kernel(n_seqs, hq, hkv, d, max_q_len, max_kv_len)) return attend_tc_workspace_bytes(n_seqs, total, hq, hkv, d);
+    // whichever kernels a call of these bounds may take: with a window it may be the one for fewer tokens
+    size_t need = 0;
+    if (use_tensor_kernel(n_seqs, hq, hkv, d, max_q_len, max_kv_len)) need = attend_tc_workspace_bytes(n_seqs, total, hq, hkv, d);
+    if (use_tensor_kernel(n_seqs, hq, hkv, d, max_q_len, 1)) return need;
     const int rows = item_rows(hq / hkv, max_q_len);
     const long long slots = 2 * min(unit_bound(n_seqs, hq, hkv, max_q_len, max_kv_len), (long long)kMaxSplitCtas);
-    return kMetaBytes + (size_t)slots * (rows * d + 2 * rows) * sizeof(float);
+    return max(need, kMetaBytes + (size_t)slots * (rows * d + 2 * rows) * sizeof(float));
 }
 
 bool attend_supported(int n_seqs, int hq, int hkv, int d, int max_q_len, int max_kv_len) {
@@ -686,7 +698,7 @@ bool attend_supported(int n_seqs, int hq, int hkv, int d, int max_q_len, int max
 }
 
 cudaError_t launch_attend(const AttendProblem &p) {
-    if (use_tensor_kernel(p.n_seqs, p.hq, p.pool.hkv, p.d, p.max_q_len, p.max_kv_len)) return launch_attend_tc(p);
+    if (use_tensor_kernel(p)) return launch_attend_tc(p);
     const bool e4m3 = p.format == GDN_KV_E4M3;
     switch (p.d) {
         case 64: return e4m3 ? launch_split<64, GDN_KV_E4M3>(p) : launch_split<64, GDN_KV_INT8>(p);

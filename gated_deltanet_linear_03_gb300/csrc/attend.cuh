@@ -208,18 +208,26 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     for (int o = 16; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float base = top == -INFINITY ? 0.f : top;
     float l = 0.f, y[PER] = {};
-#pragma unroll 4
-    for (int k = 0; k < count; ++k) {
-        const float w = exp2f(part(k)[ROWS * D + row] - base);
-        l = fmaf(w, part(k)[ROWS * D + ROWS + row], l);
-        const float *o = part(k) + row * D + lane * PER;
+    for (int k0 = 0; k0 < count; k0 += 32) {
+        // a lane to a part for the weights, then the parts one after another, eight asked for at a time
+        const bool mine = k0 + lane < count;
+        const float w = mine ? exp2f(part(k0 + lane)[ROWS * D + row] - base) : 0.f;
+        if (mine) l = fmaf(w, part(k0 + lane)[ROWS * D + ROWS + row], l);
+        const int many = min(32, count - k0);
+#pragma unroll 8
+        for (int k = 0; k < many; ++k) {
+            const float wk = __shfl_sync(0xffffffffu, w, k);
+            const float *o = part(k0 + k) + row * D + lane * PER;
 #pragma unroll
-        for (int e = 0; e < PER; e += 2) {
-            const float2 x = *reinterpret_cast<const float2 *>(o + e);
-            y[e] = fmaf(w, x.x, y[e]);
-            y[e + 1] = fmaf(w, x.y, y[e + 1]);
+            for (int e = 0; e < PER; e += 2) {
+                const float2 x = *reinterpret_cast<const float2 *>(o + e);
+                y[e] = fmaf(wk, x.x, y[e]);
+                y[e + 1] = fmaf(wk, x.y, y[e + 1]);
+            }
         }
     }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
     for (int e = 0; e < PER; ++e) y[e] *= inv;

@@ -91,8 +91,10 @@ struct TcPlan {
 __host__ __device__ inline size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 constexpr int kPlanThreads = 1024;
-// What an item costs beside its units, in units: its queries' way into TMEM, the pipeline's fill, its outputs.
-constexpr int kItemCost = 4;
+// What an item costs beside its units, in units: its queries' way into TMEM, the pipeline's fill, its outputs.  (8192-token
+// prompt of d = 256 544 us with 4, 468 with 7, 475 with 10; ragged prompts of d = 128 262 us with 3, 254 with 4, 265 with 6.)
+template <int D>
+__host__ __device__ constexpr int item_cost() { return D == 256 ? 7 : 4; }
 
 // Exclusive prefix of v over the CTA, and the sum.
 template <typename T>
@@ -119,7 +121,7 @@ __device__ __forceinline__ T block_scan(T v, T &sum, T *part) {
 // One CTA lists the items (sequence-major, heads inside, row tiles inside) and finds where every run begins.  Each thread
 // takes consecutive items, so one scan over the threads gives all positions; the sequences' first items are scanned
 // before, a batch of sequences at a time.
-template <int ROWS>
+template <int ROWS, int ITEM_COST>
 __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_constant__ AttendProblem p, const __grid_constant__ TcPlan plan) {
     __shared__ int part[kPlanThreads / 32];
     __shared__ long long part_cost[kPlanThreads / 32];
@@ -160,21 +162,21 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
     }
     const int each = (items + kPlanThreads - 1) / kPlanThreads, i0 = min(tid * each, items), i1 = min(i0 + each, items);
     long long mine = 0, total;
-    for (int i = i0; i < i1; ++i) mine += plan.items[i].tiles + kItemCost;
+    for (int i = i0; i < i1; ++i) mine += plan.items[i].tiles + ITEM_COST;
     long long at = block_scan(mine, total, part_cost);
     const long long per = max((total + plan.ctas - 1) / plan.ctas, 1LL);
     if (tid == 0) plan.per[0] = per;
     long long c = (at + per - 1) / per;           // the first run that begins at or after this thread's items
     for (int i = i0; i < i1; ++i) {
-        const int w = plan.items[i].tiles + kItemCost;
+        const int w = plan.items[i].tiles + ITEM_COST;
         // a run that would begin inside an item's fixed cost begins at its first unit
         for (; c < plan.ctas && c * per < at + w; ++c) {
-            const int j = max(0, (int)(c * per - at) - kItemCost);
-            plan.start[c] = {i, j, at - (long long)i * kItemCost + j};
+            const int j = max(0, (int)(c * per - at) - ITEM_COST);
+            plan.start[c] = {i, j, at - (long long)i * ITEM_COST + j};
         }
         at += w;
     }
-    for (long long r = (total + per - 1) / per + tid; r <= plan.ctas; r += kPlanThreads) plan.start[r] = {0, 0, total - (long long)items * kItemCost};
+    for (long long r = (total + per - 1) / per + tid; r <= plan.ctas; r += kPlanThreads) plan.start[r] = {0, 0, total - (long long)items * ITEM_COST};
 }
 
 // A word with its n lowest bits set (none below 0, all above 63).
@@ -776,7 +778,7 @@ cudaError_t launch_tc(const AttendProblem &p) {
         if (dev < kMaxDevices) ready[dev].store(true, std::memory_order_relaxed);
     }
     using L = Tc<D>;
-    attend_plan_kernel<L::ROWS><<<1, kPlanThreads, 0, p.stream>>>(p, plan);
+    attend_plan_kernel<L::ROWS, item_cost<D>()><<<1, kPlanThreads, 0, p.stream>>>(p, plan);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     if ((e = launch_after(p.stream, dim3((unsigned)z.ctas), Tc<D>::THREADS, smem, attend_tc_kernel<D, FMT>, p, plan)) != cudaSuccess) return e;
     return launch_after(p.stream, dim3((unsigned)z.ctas, L::ROWS / 8), 256, 0, attend_join_kernel<D, L::ROWS>, p,
