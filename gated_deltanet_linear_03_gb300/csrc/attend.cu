@@ -7,8 +7,8 @@
 // sum_j e^{s_j} = 2^M sum_b (1 / V_b) sum_{j in b} w_j.
 //
 // Work.  A unit is 64 tokens of one item, an item is (sequence, key/value head, 8 NR query rows: the group's heads
-// of consecutive tokens; NR = 1 where no sequence has more than 8 rows, else 2).  All units of the call form one line; CTA c of G takes units [c per, (c + 1) per), so
-// ragged batches balance by themselves and one long sequence spreads over the whole GPU.  Lengths are read on
+// of consecutive tokens; NR = 1 where no sequence has more than 8 rows, else 2).  All units of the call form one line;
+// CTA c of G takes units [c per, (c + 1) per), so ragged batches balance by themselves and one long sequence spreads over the whole GPU.  Lengths are read on
 // the device, so a captured graph follows them.  A CTA writes finished items to `out`; of an item that crosses
 // CTAs each writes (O, M, l) to the workspace and attend_merge_kernel joins them.
 //
@@ -18,7 +18,11 @@
 // as S^T = K Q^T: the 16 tokens are the instruction's rows and 8 query rows its columns, so that a group of 8 heads
 // fills it.  The warps exchange maxima and weights through shared memory; warp w then accumulates columns
 // [w D/4, (w + 1) D/4) of O^T = V^T W^T over all 64 tokens, D/16 registers a thread and 8 rows.
-// Bound by memory: the codes are read once for all heads of a group.
+// Bound by memory: the codes are read once for all heads of a group.  128 K tokens of 2 heads of d = 256, 134 MB: 30 us, and
+// 5 for the merge, 0.57 of a copy's rate together; 64 sequences of 256 to 8192 tokens
+// and 8 heads of d = 128, 300 MB: 62 us, 0.72.  The kernel's own
+// DRAM rate is 0.58 to 0.66 of the peak, issue slots 44 to 55 % busy: what is missing is the start (lengths, table, first codes:
+// three latencies one after another, some 3 us) and the end (parts, merge).
 #include <cudaTypedefs.h>
 
 #include "attend.cuh"
@@ -626,8 +630,9 @@ cudaError_t launch_split(const AttendProblem &p) {
     const long long items = (long long)p.n_seqs * p.pool.hkv * plan.mt_max;
     const int ctas = (int)min(bound, min(fit, (long long)kMaxSplitCtas));
     // Few items in many parts: the merge goes by item, with a CTA for each piece of its rows.  Otherwise by the CTAs that
-    // items cross, one CTA for all of an item's rows (64 sequences of 8 heads: 17 us by item, 5 us so).
-    plan.meta_by_item = 4 * items <= ctas;
+    // items cross, one CTA for 8 rows.  Measured for 16 heads over 2 of d = 256, us by item / by CTA: 2 items 35 / 88 (128 K
+    // tokens), 9.5 / 24 (4 K), 16 items 23 / 29, 32 items 35 / 37, 96 items 54 / 45, 200 items 68 / 46 (456 CTAs).
+    plan.meta_by_item = 8 * items <= ctas;
     plan.meta = static_cast<MergeMeta *>(p.workspace);
     plan.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(p.workspace) + kMetaBytes);
 

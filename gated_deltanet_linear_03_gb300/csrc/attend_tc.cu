@@ -6,19 +6,31 @@
 // attend_plan_kernel lists the items and cuts their units into equal runs, one per CTA (one CTA per SM); an item
 // that crosses CTAs is joined by attend_join_kernel.
 //
-// Warps of a CTA, each following the same run of units through mbarriers:
+// Warps of a CTA, each following the same run of units through mbarriers (28 warps, 896 threads):
 //   softmax (8 NQ)  a warp has 16 rows, 4 lanes to a row.  It brings their queries, scaled exactly by a power of two, into
 //                   TMEM as the fp16 A operand of the score products; per unit it reads the rows' 64 scores, forms the
 //                   weights in one pass with the rows' present reference M and writes them as fp16 over the scores, where
 //                   they are the A operand of the output products.  Only where a score is above M by more than 15 (2^15
 //                   is the most that fp16 holds) M is raised, O scaled in TMEM, and the pass done again.  So the
 //                   common pass needs no exchange beyond the warp, and no reduction over a row until the item's end.
-//   loaders         codes from global memory to registers, turned to fp16 exactly, into 128B-swizzled shared-memory tiles:
-//                   the same layout serves K (K-major B) and V (MN-major B).  And the block scales.
+//                   At an item's end it writes its rows' outputs, or their part for the join.
+//   look-up (1)     table entries, rows in the pool and block scales of eight units at a time, a lane to a block of 16 tokens.
+//   loaders (8, 16) codes from global memory to registers, turned to fp16 exactly, into 128B-swizzled shared-memory tiles:
+//                   the same layout serves K (K-major B) and V (MN-major B).
 //   MMA (2)         one issues S = Q K^T, as far ahead as there are score buffers, one O += W V.
 // Queries and weights as TMEM operands leave shared memory to K and V: per unit 2 x 64 x D x 2 bytes written by the
 // loaders and read NQ times by the MMAs.
-// Bound by the tensor pipe (4 D FLOP a row and token).
+//
+// Floor: the tensor pipe, 4 D FLOP a row and token (1024 cycles a unit at d = 256).  Measured at d = 256, 16 heads over 2:
+// 8192-token prompt 467 us, 0.63 of a library product's rate; 509 tokens behind 16384 127 us, 0.56; d = 128, 32 over 8:
+// 8192 tokens 330 us, 0.44; ragged prompts of 100 to 5000 tokens 256 us, 0.36.  A unit takes about 1900 cycles at d = 256 and
+// 2650 for the two tiles of d = 128: what bounds it is the way of a unit's scores from product to product (commit, TMEM to
+// registers, weights, back, commit) with two score buffers a tile, or one at d = 128, which is all that TMEM holds; the softmax
+// and loader warps issue in 53 % of the cycles and share them with that way, and at d = 256 the tiles' writes and the products'
+// reads together take most of shared memory's bandwidth.  An item's ends (queries in, pipeline full, outputs out) cost some
+// 7 units' time at d = 256, 4 at d = 128, which short prompts pay most often.
+// Tried and slower: weights in buffers of their own, so that the next score product may start when the scores are in
+// registers; two sets of softmax warps on alternate units; one warp that issues both products in a fixed order.
 #include "attend.cuh"
 
 namespace gdn {
@@ -33,7 +45,9 @@ constexpr int kSlots = 32, kSlotGroup = 8;   // what the look-up warp leaves of 
 
 template <int D>
 struct Tc {
-    static constexpr int NQ = D == 256 ? 1 : 2;              // 128-row tiles of a CTA, which share its K and V
+    // 128-row tiles of a CTA, which share its K and V.  At d = 256 TMEM holds one; below, two are faster than one: 8192-token
+    // prompt of d = 128 331 us against 371, of d = 64 217 against 315.
+    static constexpr int NQ = D == 256 ? 1 : 2;
     static constexpr int ROWS = 128 * NQ;
     // TMEM columns: O fp32, Q two fp16 a column, then SB buffers a tile of 64 scores, over which the weights are written.
     static constexpr int O = 0, Q = NQ * D, S = NQ * (D + D / 2), SB = S + NQ * 128 <= 512 ? 2 : 1;
@@ -568,8 +582,9 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
     } else if (warp < L::SOFTMAX_WARPS + L::LOADER_WARPS) {
         set_max_registers<L::REGS_LOADER, L::REGS_LAUNCH>();
         // ------------------------------------------------------------------------------------------ loaders
-        // At d = 256 two groups of 8 warps take the load tiles in turn, so that two tiles' codes are on their way at a time:
-        // their latency is longer than one tile's products.  (Two tiles in one group's registers were not faster.)
+        // At d = 256 two groups of 8 warps take the load tiles in turn, so that two tiles' codes are on their way at a time: their
+        // latency is longer than one tile's products (509 tokens behind 16384 128 us against 132 with one group, 8192-token
+        // prompt 469 / 487).  With two tiles of rows the softmax warps take the registers.
         constexpr int LU = L::LU, CH = D / 64;
         const int lg = (warp - L::SOFTMAX_WARPS) / 8, lw = (warp - L::SOFTMAX_WARPS) % 8;   // rows 8 lw .. 8 lw + 7 of every unit
         // 4 lanes take the 64 codes of a column chunk of one row.  The 8 lanes that store together hold rows that

@@ -5,7 +5,8 @@
 // A CTA carries rows one after another, one at a time in registers (pieces of 8 elements, C of them a thread), so x,
 // gate and residual are read once and r' and h written once; the two sums of squares are CTA reductions in fp32.  The
 // next row's pieces are asked for before this row's sums are formed, and the weights stay in registers: with a row a
-// CTA the weights came from L1 for every row, more bytes than the row itself.  Bound by memory.
+// CTA the weights came from L1 for every row, more bytes than the row itself.  Bound by memory: 16383 rows of 2048 with
+// gate and fp32 residual, 470 MB, in 77 us = 6.1 TB/s, 0.90 of a copy's rate; one row takes 2.6 us, a launch and its latencies.
 #include "kv_cache.cuh"
 
 namespace gdn {
@@ -63,8 +64,9 @@ struct RowPieces {
     }
 };
 
-// STAY: the next row and the weights are held in registers.  A row of more than 8192 needs them for itself, and is one
-// of few: its CTA loads it when it comes to it, and the weights where they are used.
+// STAY: the next row and the weights are held in registers (4000 x 8192: 70 us against 105 without, fp32 residual; 55 / 98,
+// bf16).  A row of more than 8192 needs the registers for itself, and is one of few: its CTA loads it when it comes to it,
+// and the weights where they are used.
 template <int C, bool RES32, bool STAY>
 __global__ void __launch_bounds__(STAY ? 512 : 1024, C == 1 ? 2 : 1) block_norm_kernel(const __grid_constant__ BlockNormProblem p) {
     __shared__ float part[2][2][32];   // by sum, and by turn: a row's last reader may still be at the other turn's
@@ -165,8 +167,10 @@ __global__ void __launch_bounds__(STAY ? 512 : 1024, C == 1 ? 2 : 1) block_norm_
 
 cudaError_t launch_block_norm(const BlockNormProblem &p) {
     const int pieces = p.dim / 8;
-    // One piece a thread up to 512 of them, so that many rows' loads are in flight with few registers; then two.
-    const int c = pieces <= 512 ? 1 : 2;
+    // One piece a thread up to 512 of them, then two.  Many short rows with an fp32 residual, whose piece is two loads, are
+    // faster with two as well: 16383 x 2048 77 us against 81, 32000 x 1024 75 / 79; but 8000 x 4096 73 / 71, one row 3.1 / 2.8,
+    // and with a bf16 residual 52.5 / 52.1.
+    const int c = pieces > 512 || (p.residual_f32 && pieces <= 256 && p.rows >= 4096) ? 2 : 1;
     const int threads = ((pieces + c - 1) / c + 31) / 32 * 32;
     using Fn = void (*)(const BlockNormProblem);
     const bool f32 = p.residual_f32;
