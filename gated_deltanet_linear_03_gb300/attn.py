@@ -53,18 +53,14 @@ def _device(t: torch.Tensor, name: str) -> int:
 
 def _launch(fn, name, index, stream, *args):
     """Call ``fn(*args, stream)`` with the tensors' device current."""
-    handle = _raw_stream(index) if stream is None else stream.cuda_stream
-    if _current_device() == index:
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
         st = fn(*args, handle)
     else:
         with torch.cuda.device(index):
             st = fn(*args, handle)
     if st != GDN_OK:
         raise GdnError(st, name)
-
-
-def _raw_stream(index: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _empty(stream, shape, dtype, device) -> torch.Tensor:
@@ -74,10 +70,6 @@ def _empty(stream, shape, dtype, device) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _current_device() -> int:
-    return torch._C._cuda_getDevice()
 
 
 def _token_rows(name: str, t: torch.Tensor, heads: int, d: int, index: int) -> Tuple[int, int]:
@@ -106,9 +98,10 @@ def _pool(k_pages, v_pages, k_scales, v_scales, block_table, index):
     n_pages, hkv, page, d = shape
     if v_pages.shape != shape:
         raise ValueError("v_pages must have the shape of k_pages")
-    if k_scales.shape != (n_pages, hkv, page // KV_BLOCK) or v_scales.shape != k_scales.shape:
+    scales = k_scales.shape
+    if scales != (n_pages, hkv, page // KV_BLOCK) or v_scales.shape != scales:
         raise ValueError(f"k_scales and v_scales must be {(n_pages, hkv, page // KV_BLOCK)}")
-    return addresses, (table, block_table.shape[1], n_pages, page, fmt), hkv, d
+    return addresses, (table, block_table.size(1), n_pages, page, fmt), hkv, d
 
 
 def alloc_cache(n_pages: int, hkv: int, page_size: int, d: int, n_slots: int, dtype=torch.int8, device="cuda"):
@@ -134,15 +127,15 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cos: Optional[torch.Tensor], sin
     lib = load_library()
     dev = _device(k, "k")
     pages, pool, hkv, d = _pool(k_pages, v_pages, k_scales, v_scales, block_table, dev)
-    T = k.shape[0]
+    T = k.size(0)
     kp, k_stride = _token_rows("k", k, hkv, d, dev)
     vp, v_stride = _token_rows("v", v, hkv, d, dev)
-    if v.shape[0] != T:
+    if v.size(0) != T:
         raise ValueError("k and v must have the same tokens")
     cu = _contiguous("cu_seqlens", cu_seqlens, torch.int32, 1, dev)
     past = _contiguous("past_lens", past_lens, torch.int32, 1, dev)
-    n = past_lens.shape[0]
-    if cu_seqlens.shape[0] != n + 1 or block_table.shape[0] != n:
+    n = past_lens.size(0)
+    if cu_seqlens.size(0) != n + 1 or block_table.size(0) != n:
         raise ValueError("cu_seqlens, past_lens and block_table must describe the same sequences")
     rot = positions = cp = sp = 0
     if (cos is None) != (sin is None):
@@ -150,40 +143,46 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cos: Optional[torch.Tensor], sin
     if cos is not None:
         cp = _contiguous("cos", cos, torch.float32, 2, dev)
         sp = _contiguous("sin", sin, torch.float32, 2, dev)
-        if cos.shape != sin.shape:
+        positions, half = cos.shape
+        if sin.shape != (positions, half):
             raise ValueError("cos and sin must have the same shape")
-        positions, rot = cos.shape[0], 2 * cos.shape[1]
-    op = _contiguous("open_in", open_in, torch.bfloat16, 5, dev)
-    if open_in.shape[1:] != (2, hkv, KV_BLOCK, d):
+        rot = 2 * half
+    oo = op = _contiguous("open_in", open_in, torch.bfloat16, 5, dev)
+    n_slots = open_in.size(0)
+    opened = (n_slots, 2, hkv, KV_BLOCK, d)
+    if open_in.shape != opened:
         raise ValueError(f"open_in must be [slots, 2, {hkv}, {KV_BLOCK}, {d}]")
     if open_out is None:
         open_out = open_in
-    oo = _contiguous("open_out", open_out, torch.bfloat16, 5, dev)
-    if open_out.shape != open_in.shape:
-        raise ValueError("open_out must have the shape of open_in")
+    else:
+        oo = _contiguous("open_out", open_out, torch.bfloat16, 5, dev)
+        if open_out.shape != opened:
+            raise ValueError("open_out must have the shape of open_in")
     sl = 0
     if slots is not None:
         sl = _contiguous("slots", slots, torch.int32, 1, dev)
-        if slots.shape[0] != n:
+        if slots.size(0) != n:
             raise ValueError("slots must name one slot for each sequence")
     hq = qp = q_stride = qo = 0
     if q is not None:
-        hq = q.shape[1] if q.dim() == 3 else 0
+        hq = q.size(1) if q.dim() == 3 else 0
         qp, q_stride = _token_rows("q", q, hq, d, dev)
-        if q.shape[0] != T:
+        if q.size(0) != T:
             raise ValueError("q and k must have the same tokens")
         if q_out is None:
-            q_out = _empty(stream, q.shape, q.dtype, q.device)
-        qo = _contiguous("q_out", q_out, torch.bfloat16, 3, dev)
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have the shape of q")
+            q_out = _empty(stream, (T, hq, d), torch.bfloat16, q.device)
+            qo = q_out.data_ptr()
+        else:
+            qo = _contiguous("q_out", q_out, torch.bfloat16, 3, dev)
+            if q_out.shape != (T, hq, d):
+                raise ValueError("q_out must have the shape of q")
         if T == 0:
             qp = qo = 0
     elif q_out is not None:
         raise ValueError("q_out without q")
     _launch(lib.gdn_kv_append, "gdn_kv_append", dev, stream, n, T, hq, hkv, d, rot, qp, q_stride, kp, k_stride, vp,
             v_stride, cp, sp, positions, int(bool(interleaved)), cu, past, *pool, *pages, op, oo, sl,
-            open_in.shape[0], qo)
+            n_slots, qo)
     return q_out, open_out
 
 
@@ -197,14 +196,16 @@ def kv_read(k_pages: torch.Tensor, v_pages: torch.Tensor, k_scales: torch.Tensor
     dev = _device(k_pages, "k_pages")
     pages, pool, hkv, d = _pool(k_pages, v_pages, k_scales, v_scales, block_table, dev)
     cu = _contiguous("cu_tokens", cu_tokens, torch.int32, 1, dev)
-    n = cu_tokens.shape[0] - 1
-    if block_table.shape[0] != n:
+    n = cu_tokens.size(0) - 1
+    if block_table.size(0) != n:
         raise ValueError("cu_tokens and block_table must describe the same sequences")
-    if out_dtype not in DTYPE:
+    out_code = DTYPE.get(out_dtype)
+    if out_code is None:
         raise ValueError("out_dtype must be bf16 or fp32")
-    k, v = (_empty(stream, (total_tokens, hkv, d), out_dtype, k_pages.device) for _ in range(2))
+    shape, device = (total_tokens, hkv, d), k_pages.device
+    k, v = _empty(stream, shape, out_dtype, device), _empty(stream, shape, out_dtype, device)
     _launch(lib.gdn_kv_read, "gdn_kv_read", dev, stream, n, total_tokens, hkv, d, cu, *pool, *pages, k.data_ptr(),
-            v.data_ptr(), DTYPE[out_dtype])
+            v.data_ptr(), out_code)
     return k, v
 
 
@@ -232,27 +233,35 @@ def attend(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scal
     dev = _device(q, "q")
     pages, pool, hkv, d = _pool(k_pages, v_pages, k_scales, v_scales, block_table, dev)
     qp = _contiguous("q", q, torch.bfloat16, 3, dev)
-    T, hq = q.shape[0], q.shape[1]
-    if q.shape[2] != d:
-        raise ValueError(f"q must be [tokens, heads, {d}], got {tuple(q.shape)}")
+    shape = q.shape
+    T, hq, width = shape
+    if width != d:
+        raise ValueError(f"q must be [tokens, heads, {d}], got {tuple(shape)}")
     cu = _contiguous("cu_seqlens", cu_seqlens, torch.int32, 1, dev)
     lens = _contiguous("kv_lens", kv_lens, torch.int32, 1, dev)
-    n = kv_lens.shape[0]
-    if cu_seqlens.shape[0] != n + 1 or block_table.shape[0] != n:
+    n = kv_lens.size(0)
+    if cu_seqlens.size(0) != n + 1 or block_table.size(0) != n:
         raise ValueError("cu_seqlens, kv_lens and block_table must describe the same sequences")
-    if out is None:
-        out = _empty(stream, q.shape, out_dtype, q.device)
-    op = _contiguous("out", out, out.dtype, 3, dev)
-    if out.shape != q.shape or out.dtype not in DTYPE:
+    if out is not None:
+        out_dtype = out.dtype
+        op = _contiguous("out", out, out_dtype, 3, dev)
+    out_code = DTYPE.get(out_dtype)
+    if out_code is None or (out is not None and out.shape != shape):
         raise ValueError("out must have the shape of q, in bf16 or fp32")
-    max_q_len = min(max_q_len, T)
+    if out is None:
+        out = _empty(stream, shape, out_dtype, q.device)
+        op = out.data_ptr()
+    if max_q_len > T:
+        max_q_len = T
     if workspace is None:
-        need = attend_workspace_size(n, T, hq, hkv, d, max_q_len, max_kv_len)
-        workspace = _empty(stream, need, torch.uint8, q.device)
+        ws_bytes = attend_workspace_size(n, T, hq, hkv, d, max_q_len, max_kv_len)
+        workspace = _empty(stream, ws_bytes, torch.uint8, q.device)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the other tensors' device")
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
     table, max_pages, n_pages, page, fmt = pool
     _launch(lib.gdn_attend, "gdn_attend", dev, stream, n, T, hq, hkv, d, qp, *pages, table, max_pages, n_pages, page,
             fmt, cu, lens, max_q_len, max_kv_len, 1.0 / math.sqrt(d) if sm_scale is None else sm_scale, window, sinks,
-            op, DTYPE[out.dtype], workspace.data_ptr(), workspace.numel() * workspace.element_size())
+            op, out_code, workspace.data_ptr(), ws_bytes)
     return out

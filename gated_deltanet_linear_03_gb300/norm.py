@@ -34,27 +34,34 @@ def block_norm(x: torch.Tensor, residual: torch.Tensor, pre_weight: torch.Tensor
     if nd < 1:
         raise ValueError("x must have a last dimension to normalise over")
     dim = shape[-1]
+    bf16, f32 = torch.bfloat16, torch.float32
     res = residual.dtype
-    if res not in DTYPE:
+    res_code = DTYPE.get(res)
+    if res_code is None:
         raise ValueError(f"residual must be bf16 or fp32, got {res}")
-    if residual_out is None:
-        residual_out = _empty(stream, residual.shape, res, residual.device)
-    if out is None:
-        out = _empty(stream, x.shape, x.dtype, x.device)
-    if residual.shape != shape or residual_out.shape != shape or out.shape != shape or (gate is not None and gate.shape != shape):
+    if residual.shape != shape or (gate is not None and gate.shape != shape) or \
+            (residual_out is not None and residual_out.shape != shape) or (out is not None and out.shape != shape):
         raise ValueError("x, gate, residual and the outputs must have one shape")
     scaled = isinstance(scale, torch.Tensor)
-    if pre_weight.shape[0] != dim or (post_weight is not None and post_weight.shape[0] != dim) or (scaled and scale.shape[0] != dim):
+    if pre_weight.size(0) != dim or (post_weight is not None and post_weight.size(0) != dim) or (scaled and scale.size(0) != dim):
         raise ValueError(f"pre_weight, post_weight and a scale per channel must have {dim} entries")
     act = GATE_ACT.get(gate_act)
     if act is None:
         raise ValueError(f"gate_act must be one of {sorted(GATE_ACT)}")
-    bf16, f32 = torch.bfloat16, torch.float32
-    _launch(lib.gdn_block_norm, "gdn_block_norm", dev, stream, x.numel() // dim if dim else 0, dim,
-            _contiguous("x", x, bf16, nd, dev), 0 if gate is None else _contiguous("gate", gate, bf16, nd, dev), act,
-            _contiguous("residual", residual, res, nd, dev), DTYPE[res],
+    xp, rp = _contiguous("x", x, bf16, nd, dev), _contiguous("residual", residual, res, nd, dev)
+    if residual_out is None:
+        residual_out = _empty(stream, shape, res, x.device)
+        rop = residual_out.data_ptr()
+    else:
+        rop = _contiguous("residual_out", residual_out, res, nd, dev)
+    if out is None:
+        out = _empty(stream, shape, bf16, x.device)
+        op = out.data_ptr()
+    else:
+        op = _contiguous("out", out, bf16, nd, dev)
+    _launch(lib.gdn_block_norm, "gdn_block_norm", dev, stream, x.numel() // dim if dim else 0, dim, xp,
+            0 if gate is None else _contiguous("gate", gate, bf16, nd, dev), act, rp, res_code,
             0 if post_weight is None else _contiguous("post_weight", post_weight, f32, 1, dev),
             _contiguous("pre_weight", pre_weight, f32, 1, dev), _contiguous("scale", scale, f32, 1, dev) if scaled else 0,
-            1.0 if scaled else scale, eps, _contiguous("residual_out", residual_out, res, nd, dev),
-            _contiguous("out", out, bf16, nd, dev))
+            1.0 if scaled else scale, eps, rop, op)
     return residual_out, out
