@@ -19,10 +19,10 @@
 // fills it.  The warps exchange maxima and weights through shared memory; warp w then accumulates columns
 // [w D/4, (w + 1) D/4) of O^T = V^T W^T over all 64 tokens, D/16 registers a thread and 8 rows.
 // Bound by memory: the codes are read once for all heads of a group.  128 K tokens of 2 heads of d = 256, 134 MB: 30 us, and
-// 5 for the merge, 0.57 of a copy's rate together; 64 sequences of 256 to 8192 tokens
+// 4 for the merge, 0.59 of a copy's rate together; 64 sequences of 256 to 8192 tokens
 // and 8 heads of d = 128, 300 MB: 62 us, 0.72.  The kernel's own
 // DRAM rate is 0.58 to 0.66 of the peak, issue slots 44 to 55 % busy: what is missing is the start (lengths, table, first codes:
-// three latencies one after another, some 3 us) and the end (parts, merge).
+// three latencies one after another, some 4 us) and the end (CTAs that finish between 22 and 26 us, parts, merge).
 #include <cudaTypedefs.h>
 
 #include "attend.cuh"
@@ -129,6 +129,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NR>()) attend_split_k
 
     // ---- this CTA's units: a scan over the sequences' costs
     if (tid == kCompute) {
+        sm100::tma_prefetch_desc(&k_map);
+        sm100::tma_prefetch_desc(&v_map);
         for (int i = 0; i < S; ++i) {
             sm100::mbar_init(&sm.full[i], 1);
             sm100::mbar_init(&sm.empty[i], 4);
@@ -242,13 +244,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NR>()) attend_split_k
             look_up();
         }
         for (int unit = 0; unit < units; ++unit) {
-            // the next unit's rows and scales, and the table's entries of the one after it
-            const int next_row = unit + 1 < units ? pool_row() : -1;
-            const float next_scale = scale_of(next_row);
-            if (unit + 2 < units) {
-                advance(cc);
-                look_up();
-            }
             wait(&sm.empty[stage], phase);
             __syncwarp();
             if (*abort) break;
@@ -258,8 +253,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NR>()) attend_split_k
                 uint8_t *dst = (lane < 4 ? sm.k[stage] : sm.v[stage]) + (lane & 3) * (kKvBlock * D);
 #pragma unroll
                 for (int x = 0; x < D; x += 128) sm100::tma_load_2d(dst + x * kKvBlock, map, &sm.full[stage], x, max(row, 0));
-                sm.scale[stage][lane] = scale;
             }
+            // the next unit's rows and scales, and the table's entries of the one after it, while this one's codes come
+            const int next_row = unit + 1 < units ? pool_row() : -1;
+            const float next_scale = scale_of(next_row);
+            if (unit + 2 < units) {
+                advance(cc);
+                look_up();
+            }
+            if (lane < 8) sm.scale[stage][lane] = scale;
             __syncwarp();
             if (lane == 0) sm100::mbar_arrive_expect_tx(&sm.full[stage], 2 * kTile * D);
             if (++stage == S) stage = 0, phase ^= 1;
@@ -516,17 +518,17 @@ template <int D, int ROWS>
 __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const __grid_constant__ AttendProblem p,
                                                                      const __grid_constant__ SplitPlan plan) {
     constexpr int LANES = 16, GROUPS = kMergeThreads / LANES;
-    __shared__ float weight[kMaxSplitCtas];
+    __shared__ float weight[kMaxSplitCtas], part_l[kMaxSplitCtas];
     __shared__ float red[2][kMergeThreads / 32];
     __shared__ float4 sum[GROUPS][LANES];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.y;
     const int group = p.hq / p.pool.hkv;
+    // (an item's sequence is read before the split kernel has ended; items that no CTA visited have no entry)
+    const Sequence s = load_sequence(p, blockIdx.x / (p.pool.hkv * plan.mt_max));
+    if ((int)(blockIdx.x % plan.mt_max) >= row_tiles<ROWS>(s.qlen, group)) return;
     sm100::grid_dependency_wait();
-    // items that no CTA visited have no entry
-    if (blockIdx.x % plan.mt_max >= row_tiles<ROWS>(load_sequence(p, blockIdx.x / (p.pool.hkv * plan.mt_max)).qlen, group)) return;
     const MergeMeta mm = plan.meta[blockIdx.x];
     if (mm.last < 0) return;
-    const Sequence s = load_sequence(p, mm.n);
     const int grow = mm.mt * ROWS + row, i = grow / group;
     if (i >= s.qlen) return;
     const size_t stride = ROWS * D + 2 * ROWS;
@@ -542,8 +544,9 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const __gri
 
     float big = -INFINITY;
     for (int k = tid; k < count; k += kMergeThreads) {
-        const float x = part(k)[ROWS * D + row];
+        const float x = part(k)[ROWS * D + row], y = part(k)[ROWS * D + ROWS + row];
         weight[k] = x;
+        part_l[k] = y;
         big = fmaxf(big, x);
     }
 #pragma unroll
@@ -557,7 +560,7 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const __gri
     for (int k = tid; k < count; k += kMergeThreads) {
         const float w = exp2f(weight[k] - safe);
         weight[k] = w;
-        l += w * part(k)[ROWS * D + ROWS + row];
+        l += w * part_l[k];
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -629,10 +632,10 @@ cudaError_t launch_split(const AttendProblem &p) {
     plan.mt_max = row_tiles<8 * NR>(p.max_q_len, group);
     const long long items = (long long)p.n_seqs * p.pool.hkv * plan.mt_max;
     const int ctas = (int)min(bound, min(fit, (long long)kMaxSplitCtas));
-    // Few items in many parts: the merge goes by item, with a CTA for each piece of its rows.  Otherwise by the CTAs that
-    // items cross, one CTA for 8 rows.  Measured for 16 heads over 2 of d = 256, us by item / by CTA: 2 items 35 / 88 (128 K
-    // tokens), 9.5 / 24 (4 K), 16 items 23 / 29, 32 items 35 / 37, 96 items 54 / 45, 200 items 68 / 46 (456 CTAs).
-    plan.meta_by_item = 8 * items <= ctas;
+    // Few items: the merge goes by item, with a CTA for each piece of its rows.  Otherwise by the CTAs that items cross, one CTA
+    // for 8 rows.  Measured for 16 heads over 2 of d = 256, us by item / by CTA: 2 items of 5 units 8.8 / 10.1, of 64 units 9.5 / 24,
+    // of 2048 35 / 88, 16 items of 128 units 23 / 29, 32 items 35 / 37, 96 items of 64 54 / 45, 200 items of 32 68 / 46.
+    plan.meta_by_item = items <= 48;
     plan.meta = static_cast<MergeMeta *>(p.workspace);
     plan.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(p.workspace) + kMetaBytes);
 
