@@ -40,7 +40,6 @@ using namespace attend;
 using namespace sm100;
 
 constexpr int kTile = 64;
-constexpr int kStages = 3;
 constexpr int kSlots = 32, kSlotGroup = 8;   // what the look-up warp leaves of a unit: a ring of slots, filled eight at a time
 
 template <int D>
@@ -49,31 +48,38 @@ struct Tc {
     // prompt of d = 128 331 us against 371, of d = 64 217 against 315.
     static constexpr int NQ = D == 256 ? 1 : 2;
     static constexpr int ROWS = 128 * NQ;
+    // Queries in shared memory instead of TMEM at d = 128: a score product then takes 1.5 times as long, but there is room for a
+    // second score buffer a tile (8192-token prompt 276 us against 315, ragged prompts 226 / 249; at d = 256, four buffers instead
+    // of two, 493 / 441; at d = 64, as many as without, 177 / 173 for ragged prompts).
+    static constexpr bool QS = D == 128;
     // TMEM columns: O fp32, Q two fp16 a column, then SB buffers a tile of 64 scores, over which the weights are written.
-    static constexpr int O = 0, Q = NQ * D, S = NQ * (D + D / 2), SB = S + NQ * 128 <= 512 ? 2 : 1;
-    static_assert(S + NQ * SB * 64 <= 512, "tensor memory");
-    static constexpr int LU = 256 / D;                       // units of a load tile: 16 KB of K codes and 16 KB of V codes
+    static constexpr int O = 0, Q = NQ * D, S = NQ * (QS ? D : D + D / 2), SB = (512 - S) / (64 * NQ);
+    static_assert(SB >= 1 && S + NQ * SB * 64 <= 512, "tensor memory");
+    // Stages of K and V tiles in shared memory.  What they leave is L1 cache, through which queries and codes come: at d = 256
+    // three stages leave next to none (8192-token prompt 468 us with three, 441 with two; of d = 128 276 / 272).
+    static constexpr int STAGES = 2;
     static constexpr int LG = D == 256 ? 2 : 1;              // groups of 8 loader warps, which take the tiles in turn
-    static_assert(kSlotGroup % LU == 0 && 2 * kSlotGroup >= LU * (LG + 1), "a tile's units lie in one group of slots");
     static constexpr int SOFTMAX_WARPS = 8 * NQ, LOADER_WARPS = 8 * LG;
     static constexpr int WARPS = SOFTMAX_WARPS + LOADER_WARPS + 4;     // the last four: MMA, MMA, look-up, idle
     static constexpr int THREADS = 32 * WARPS;               // 896
     // Registers a thread: at launch (the most that 28 warps can have, a multiple of 8), then per role.  The roles' shares
-    // stay within what the CTA was launched with: 896 x 72 = 256 x 104 + 512 x 56 + 128 x 72 = 512 x 88 + 256 x 56 + 128 x 40.
-    static constexpr int REGS_LAUNCH = 72, REGS_SOFTMAX = NQ == 1 ? 104 : 88, REGS_LOADER = 56, REGS_OTHER = NQ == 1 ? 72 : 40;
+    // stay within what the CTA was launched with: 896 x 72 = 256 x 104 + 512 x 56 + 128 x 72 = 512 x 88 + 256 x 48 + 128 x 56.
+    static constexpr int REGS_LAUNCH = 72, REGS_SOFTMAX = NQ == 1 ? 104 : 88, REGS_LOADER = NQ == 1 ? 56 : 48, REGS_OTHER = NQ == 1 ? 72 : 56;
     static_assert(32 * (SOFTMAX_WARPS * REGS_SOFTMAX + LOADER_WARPS * REGS_LOADER + 4 * REGS_OTHER) <= THREADS * REGS_LAUNCH, "registers");
-    static constexpr int TILE_ROWS = kTile * LU, TILE_BYTES = TILE_ROWS * D * 2, CHUNK = TILE_ROWS * 128;   // CHUNK: 64 columns
+    static constexpr int TILE_BYTES = kTile * D * 2, CHUNK = kTile * 128;   // CHUNK: 64 columns
+    static constexpr int Q_BYTES = QS ? 128 * D * 2 : 0, Q_CHUNK = 128 * 128;   // of a tile's queries
 };
 
 template <int D>
 struct __align__(1024) TcSmem {
-    static constexpr int NQ = Tc<D>::NQ;
-    uint8_t k[kStages][Tc<D>::TILE_BYTES];
-    uint8_t v[kStages][Tc<D>::TILE_BYTES];
+    static constexpr int NQ = Tc<D>::NQ, STAGES = Tc<D>::STAGES;
+    uint8_t k[STAGES][Tc<D>::TILE_BYTES];
+    uint8_t v[STAGES][Tc<D>::TILE_BYTES];
+    uint8_t q[NQ * Tc<D>::Q_BYTES + 1024 * !Tc<D>::QS];   // (never empty)
     float scale[kSlots][12];             // of a unit's 4 blocks: K scales, log2 of V scales, reciprocals of V scales
     int2 block[kSlots][4];               // and their first rows in the pool (-1: none), and how many tokens they hold
     uint64_t slots_full[kSlots / kSlotGroup], slots_free[kSlots / kSlotGroup];
-    uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+    uint64_t k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES];
     uint64_t s_full[NQ * Tc<D>::SB], p_full[NQ * Tc<D>::SB], p_free[NQ * Tc<D>::SB], q_full[NQ], drain[2];
     uint32_t tmem;
     int abort;
@@ -206,19 +212,18 @@ __device__ __forceinline__ void store_shared(uint32_t a, uint32_t x, uint32_t y,
     asm volatile("st.shared.v4.b32 [%0 + %5], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w), "n"(AT) : "memory");
 }
 
-// A loader thread's codes of a tile as fp16, from piece N (16 codes) on: the first and the last 8 of K's order, or of V's.
+// A loader thread's codes of a unit's tile as fp16, from piece N (16 codes) on: the first and the last 8 of K's order, or of V's.
 template <int D, int FMT, bool KEYS, int N = 0>
-__device__ __forceinline__ void put_codes(uint32_t lo, uint32_t hi, const uint4 (&x)[Tc<D>::LU * D / 64]) {
-    constexpr int CH = D / 64, at = N % CH * Tc<D>::CHUNK + N / CH * (kTile * 128);
+__device__ __forceinline__ void put_codes(uint32_t lo, uint32_t hi, const uint4 (&x)[D / 64]) {
     const uint4 z = x[N];
     uint32_t y[8];
     codes_to_f16x2<FMT>(z.x, y[0], y[1]);
     codes_to_f16x2<FMT>(KEYS ? z.z : z.y, y[2], y[3]);
     codes_to_f16x2<FMT>(KEYS ? z.y : z.z, y[4], y[5]);
     codes_to_f16x2<FMT>(z.w, y[6], y[7]);
-    store_shared<at>(lo, y[0], y[1], y[2], y[3]);
-    store_shared<at>(hi, y[4], y[5], y[6], y[7]);
-    if constexpr (N + 1 < Tc<D>::LU * CH) put_codes<D, FMT, KEYS, N + 1>(lo, hi, x);
+    store_shared<N * Tc<D>::CHUNK>(lo, y[0], y[1], y[2], y[3]);
+    store_shared<N * Tc<D>::CHUNK>(hi, y[4], y[5], y[6], y[7]);
+    if constexpr (N + 1 < D / 64) put_codes<D, FMT, KEYS, N + 1>(lo, hi, x);
 }
 
 // 4 x 4 words of 4 neighbouring lanes, lane t's word i becoming lane i's word t.
@@ -241,7 +246,7 @@ template <int D, int FMT>
 __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __grid_constant__ AttendProblem p,
                                                                      const __grid_constant__ TcPlan plan) {
     using L = Tc<D>;
-    constexpr int NQ = L::NQ, SB = L::SB, ROWS = L::ROWS;
+    constexpr int NQ = L::NQ, SB = L::SB, STAGES = L::STAGES, ROWS = L::ROWS;
     extern __shared__ uint8_t raw[];
     TcSmem<D> &sm = *reinterpret_cast<TcSmem<D> *>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -249,7 +254,7 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
 
     if (warp == 0) tmem_alloc(&sm.tmem, 512);
     if (tid == 32) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < STAGES; ++i) {
             mbar_init(&sm.k_full[i], 8);
             mbar_init(&sm.v_full[i], 8);
             mbar_init(&sm.k_empty[i], 1);
@@ -294,6 +299,7 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
         const int row0 = 128 * q + 32 * quadrant + 16 * half + g;        // this lane's rows: row0 and row0 + 8
         const uint32_t quad = tmem + ((uint32_t)quadrant << 21), part16 = quad + ((uint32_t)(16 * half) << 16);   // lanes
         const uint32_t o_cols = L::O + q * D, q_at = part16 + L::Q + q * (D / 2);
+        const uint32_t q_tile = smem_u32(sm.q) + q * L::Q_BYTES;
         auto wait = [&](uint64_t *bar, int phase) {
             poll(bar, phase);
             __syncwarp();
@@ -369,9 +375,21 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                                 x[8 * i2 + 4 + 2 * k] = bf16x2_to_f16x2(z.z, down[k]);
                                 x[8 * i2 + 4 + 2 * k + 1] = bf16x2_to_f16x2(z.w, down[k]);
                             }
-                        tmem_st_16x32(q_at + 32 * c, x);
+                        if (L::QS) {
+                            // a row's 64 columns c, in their own order: pieces 4 i2 + t of 8
+#pragma unroll
+                            for (int i2 = 0; i2 < 2; ++i2)
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const uint32_t at = q_tile + c * L::Q_CHUNK + sw128_offset((row0 & 127) + 8 * k, 32 * i2 + 8 * t);
+                                    store_shared<0>(at, x[8 * i2 + 2 * k], x[8 * i2 + 2 * k + 1], x[8 * i2 + 4 + 2 * k], x[8 * i2 + 4 + 2 * k + 1]);
+                                }
+                        } else {
+                            tmem_st_16x32(q_at + 32 * c, x);
+                        }
                     }
-                    tmem_st_wait();
+                    if (L::QS) fence_proxy_async_smem();
+                    else tmem_st_wait();
                 }
                 if (u_end < units) prefetch_l1(plan.items + item + 1);
                 tc_fence_before();
@@ -582,47 +600,43 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
     } else if (warp < L::SOFTMAX_WARPS + L::LOADER_WARPS) {
         set_max_registers<L::REGS_LOADER, L::REGS_LAUNCH>();
         // ------------------------------------------------------------------------------------------ loaders
-        // At d = 256 two groups of 8 warps take the load tiles in turn, so that two tiles' codes are on their way at a time: their
-        // latency is longer than one tile's products (509 tokens behind 16384 128 us against 132 with one group, 8192-token
-        // prompt 469 / 487).  With two tiles of rows the softmax warps take the registers.
-        constexpr int LU = L::LU, CH = D / 64;
+        // At d = 256 two groups of 8 warps take the units in turn, so that two units' codes are on their way at a time: their
+        // latency is longer than one unit's products (8192-token prompt 457 us against 546 with one group).  With two tiles of
+        // rows the softmax warps take the registers.  The codes go through L1 (read past it: 457 against 440), because each
+        // request takes half of a row's lines.
+        constexpr int CH = D / 64;
         const int lg = (warp - L::SOFTMAX_WARPS) / 8, lw = (warp - L::SOFTMAX_WARPS) % 8;   // rows 8 lw .. 8 lw + 7 of every unit
         // 4 lanes take the 64 codes of a column chunk of one row.  The 8 lanes that store together hold rows that
         // differ in the two low bits, so that their pieces fall on different banks in both tiles' orders.
         const int r = 8 * lw + ((lane >> 4) << 2) + ((((lane >> 2) & 1) * 3) ^ ((lane >> 3) & 1)), c16 = lane & 3;
         const uint32_t v_lo = sw128_offset(r, 16 * c16), v_hi = sw128_offset(r, 16 * c16 + 8);
         // K's columns stand in the order in which a query row's 32-element pieces enter TMEM: components 8 t + 0..3
-        // at 4 t, components 8 t + 4..7 at 16 + 4 t (t = 0..3)
-        const uint32_t k_lo = sw128_offset(r, 32 * (c16 >> 1) + 8 * (c16 & 1)), k_hi = sw128_offset(r, 32 * (c16 >> 1) + 16 + 8 * (c16 & 1));
+        // at 4 t, components 8 t + 4..7 at 16 + 4 t (t = 0..3); with queries in shared memory, in their own
+        const uint32_t k_lo = L::QS ? v_lo : sw128_offset(r, 32 * (c16 >> 1) + 8 * (c16 & 1)),
+                       k_hi = L::QS ? v_hi : sw128_offset(r, 32 * (c16 >> 1) + 16 + 8 * (c16 & 1));
         auto wait = [&](uint64_t *bar, int phase) {
             poll(bar, phase);
             __syncwarp();
         };
         const int in_block = r % kKvBlock;
-        for (int tile = lg; tile * LU < units; tile += L::LG) {
-            // the tile's codes are asked for; they are on their way while its place is waited for
-            const int u = tile * LU, st = tile % kStages, ph = tile / kStages + 1;
-            if (u % kSlotGroup < LU * L::LG) wait(&sm.slots_full[u / kSlotGroup % (kSlots / kSlotGroup)], u / kSlots);
-            bool there[LU], missing = false;
-            uint4 kr[LU * CH], vr[LU * CH];
+        for (int u = lg; u < units; u += L::LG) {
+            // the unit's codes are asked for; they are on their way while its place is waited for
+            const int st = u % STAGES, ph = u / STAGES + 1;
+            if (u % kSlotGroup < L::LG) wait(&sm.slots_full[u / kSlotGroup % (kSlots / kSlotGroup)], u / kSlots);
+            const int2 block = sm.block[u % kSlots][lw / 2];
+            const bool there = in_block < block.y;
+            const size_t at = (size_t)(there ? block.x + in_block : 0) * D + 16 * c16;
+            uint4 kr[CH], vr[CH];
 #pragma unroll
-            for (int i = 0; i < LU; ++i) {
-                const int2 block = sm.block[(u + i) % kSlots][lw / 2];
-                there[i] = in_block < block.y && u + i < units;
-                missing |= !there[i];
-                const size_t at = (size_t)(there[i] ? block.x + in_block : 0) * D + 16 * c16;
+            for (int c = 0; c < CH; ++c) kr[c] = __ldg(reinterpret_cast<const uint4 *>(p.k_pages + at + 64 * c));
 #pragma unroll
-                for (int c = 0; c < CH; ++c) kr[i * CH + c] = __ldg(reinterpret_cast<const uint4 *>(p.k_pages + at + 64 * c));
-#pragma unroll
-                for (int c = 0; c < CH; ++c) vr[i * CH + c] = __ldg(reinterpret_cast<const uint4 *>(p.v_pages + at + 64 * c));
-            }
+            for (int c = 0; c < CH; ++c) vr[c] = __ldg(reinterpret_cast<const uint4 *>(p.v_pages + at + 64 * c));
             wait(&sm.k_empty[st], ph);
-            if (__any_sync(0xffffffffu, missing)) {       // rows that do not exist become zeros
+            if (!there) {       // rows that do not exist become zeros
 #pragma unroll
-                for (int i = 0; i < LU * CH; ++i)
-                    if (!there[i / CH]) kr[i] = vr[i] = make_uint4(0, 0, 0, 0);
+                for (int c = 0; c < CH; ++c) kr[c] = vr[c] = make_uint4(0, 0, 0, 0);
             }
-            put_codes<D, FMT, true>(smem_u32(sm.k[st]) + k_lo, smem_u32(sm.k[st]) + k_hi, kr);
+            put_codes<D, FMT, !L::QS>(smem_u32(sm.k[st]) + k_lo, smem_u32(sm.k[st]) + k_hi, kr);
             fence_proxy_async_smem();
             arrive(&sm.k_full[st]);
             wait(&sm.v_empty[st], ph);
@@ -640,35 +654,40 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
         if (role < 2 && units > 0 && elect_one()) {
             int item = plan.start[cta].item, left = plan.items[item].tiles - plan.start[cta].j, next_left = 0;
             if (left < units) next_left = plan.items[item + 1].tiles;
-            int st = 0, ph = 0, sub = 0, seg = 0;   // of unit u: its load tile's stage, its place there
+            int st = 0, ph = 0, seg = 0;            // of unit u: its tiles' stage
             int buf = 0, buf_phase = 0;             // its score buffer
             bool first = true;
             for (int u = 0; u < units; ++u) {
-                const bool ends = left == 1, tile_ends = sub == L::LU - 1 || u == units - 1;
+                const bool ends = left == 1;
                 if (role == 0) {
                     // S = Q K^T.  A buffer is free once the output product has read the weights that took its place.
-                    if (sub == 0) poll(&sm.k_full[st], ph);
+                    poll(&sm.k_full[st], ph);
                     constexpr uint32_t id = idesc_f16_f32(128, kTile, false, false);
                     const uint64_t kd = smem_desc(smem_u32(sm.k[0]), 16, 1024, kLayoutSwizzle128B) +
-                                        ((st * L::TILE_BYTES + sub * (kTile * 128)) >> 4);
+                                        (st * L::TILE_BYTES >> 4);
 #pragma unroll
                     for (int q = 0; q < NQ; ++q) {
                         if (first) poll(&sm.q_full[q], seg);
                         poll(&sm.p_free[q * SB + buf], buf_phase ^ 1);
                         tc_fence_after();
                         const uint32_t d = tmem + L::S + 64 * (q * SB + buf), a = tmem + L::Q + q * (D / 2);
+                        const uint64_t qd = smem_desc(smem_u32(sm.q) + q * L::Q_BYTES, 16, 1024, kLayoutSwizzle128B);
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k) mma_tmem_a(d, a + 8 * k, kd + ((k >> 2) * L::CHUNK >> 4) + 2 * (k & 3), id, k > 0);
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint64_t kk = kd + ((k >> 2) * L::CHUNK >> 4) + 2 * (k & 3);
+                            if (L::QS) mma_f16(d, qd + ((k >> 2) * L::Q_CHUNK >> 4) + 2 * (k & 3), kk, id, k > 0);
+                            else mma_tmem_a(d, a + 8 * k, kk, id, k > 0);
+                        }
                         mma_commit(&sm.s_full[q * SB + buf]);
                         mbar_arrive(&sm.s_full[q * SB + buf]);   // the block scales, which this thread has waited for, are visible too
                     }
-                    if (tile_ends) mma_commit(&sm.k_empty[st]);
+                    mma_commit(&sm.k_empty[st]);
                 } else {
                     // O += W V, from 0 at an item's first unit in this run
-                    if (sub == 0) poll(&sm.v_full[st], ph);
+                    poll(&sm.v_full[st], ph);
                     constexpr uint32_t id = idesc_f16_f32(128, D, false, true);
                     const uint64_t vd = smem_desc(smem_u32(sm.v[0]), L::CHUNK, 1024, kLayoutSwizzle128B) +
-                                        ((st * L::TILE_BYTES + sub * (kTile * 128)) >> 4);
+                                        (st * L::TILE_BYTES >> 4);
 #pragma unroll
                     for (int q = 0; q < NQ; ++q) {
                         poll(&sm.p_full[q * SB + buf], buf_phase);
@@ -678,15 +697,11 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                         for (int k = 0; k < kTile / 16; ++k) mma_tmem_a(tmem + L::O + q * D, a + 8 * k, vd + 128 * k, id, !(first && k == 0));
                         mma_commit(&sm.p_free[q * SB + buf]);
                     }
-                    if (tile_ends) mma_commit(&sm.v_empty[st]);
+                    mma_commit(&sm.v_empty[st]);
                     // the softmax warps have read the slots of all units up to this one
                     if (u % kSlotGroup == kSlotGroup - 1) mbar_arrive(&sm.slots_free[u / kSlotGroup % (kSlots / kSlotGroup)]);
                 }
-                ++sub;
-                if (tile_ends) {
-                    sub = 0;
-                    if (++st == kStages) st = 0, ph ^= 1;
-                }
+                if (++st == STAGES) st = 0, ph ^= 1;
                 if (++buf == SB) buf = 0, buf_phase ^= 1;
                 first = ends;
                 --left;
