@@ -8,7 +8,7 @@
 //
 // Warps of a CTA, each following the same run of units through mbarriers (28 warps, 896 threads):
 //   softmax (8 NQ)  a warp has 16 rows, 4 lanes to a row.  It brings their queries, scaled exactly by a power of two, into
-//                   TMEM as the fp16 A operand of the score products; per unit it reads the rows' 64 scores, forms the
+//                   TMEM (d = 128: shared memory) as the fp16 A operand of the score products; per unit it reads the rows' 64 scores, forms the
 //                   weights in one pass with the rows' present reference M and writes them as fp16 over the scores, where
 //                   they are the A operand of the output products.  Only where a score is above M by more than 15 (2^15
 //                   is the most that fp16 holds) M is raised, O scaled in TMEM, and the pass done again.  So the
@@ -22,13 +22,12 @@
 // loaders and read NQ times by the MMAs.
 //
 // Floor: the tensor pipe, 4 D FLOP a row and token (1024 cycles a unit at d = 256).  Measured at d = 256, 16 heads over 2:
-// 8192-token prompt 467 us, 0.63 of a library product's rate; 509 tokens behind 16384 127 us, 0.56; d = 128, 32 over 8:
-// 8192 tokens 330 us, 0.44; ragged prompts of 100 to 5000 tokens 256 us, 0.36.  A unit takes about 1900 cycles at d = 256 and
-// 2650 for the two tiles of d = 128: what bounds it is the way of a unit's scores from product to product (commit, TMEM to
-// registers, weights, back, commit) with two score buffers a tile, or one at d = 128, which is all that TMEM holds; the softmax
-// and loader warps issue in 53 % of the cycles and share them with that way, and at d = 256 the tiles' writes and the products'
-// reads together take most of shared memory's bandwidth.  An item's ends (queries in, pipeline full, outputs out) cost some
-// 7 units' time at d = 256, 4 at d = 128, which short prompts pay most often.
+// 8192-token prompt 441 us, 0.66 of a library product's rate; 509 tokens behind 16384 119 us, 0.60; d = 128: 8192 tokens of
+// 16 heads over 2 252 us, 0.58, ragged prompts of 100 to 5000 tokens of 32 over 8 207 us, 0.45.  What bounds a unit is the way
+// of its scores from product to product (commit, TMEM to registers, weights, back, commit) with two score buffers a tile, which is
+// all that TMEM holds; the softmax and loader warps issue in more than half of the cycles and share them with that way, and the
+// tiles' writes and the products' reads together take most of shared memory's bandwidth.  An item's ends (queries in, pipeline
+// full, outputs out) cost some 7 units' time, which short prompts pay most often.
 // Tried and slower: weights in buffers of their own, so that the next score product may start when the scores are in
 // registers; two sets of softmax warps on alternate units; one warp that issues both products in a fixed order.
 #include "attend.cuh"
@@ -44,8 +43,8 @@ constexpr int kSlots = 32, kSlotGroup = 8;   // what the look-up warp leaves of 
 
 template <int D>
 struct Tc {
-    // 128-row tiles of a CTA, which share its K and V.  At d = 256 TMEM holds one; below, two are faster than one: 8192-token
-    // prompt of d = 128 331 us against 371, of d = 64 217 against 315.
+    // 128-row tiles of a CTA, which share its K and V.  At d = 256 TMEM holds one; below, two are faster than one: ragged prompts
+    // of d = 128 207 us against 285, of d = 64 172 against 251.
     static constexpr int NQ = D == 256 ? 1 : 2;
     static constexpr int ROWS = 128 * NQ;
     // Queries in shared memory instead of TMEM at d = 128: a score product then takes 1.5 times as long, but there is room for a
@@ -111,10 +110,11 @@ struct TcPlan {
 __host__ __device__ inline size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 constexpr int kPlanThreads = 1024;
-// What an item costs beside its units, in units: its queries' way into TMEM, the pipeline's fill, its outputs.  (8192-token
-// prompt of d = 256 544 us with 4, 468 with 7, 475 with 10; ragged prompts of d = 128 262 us with 3, 254 with 4, 265 with 6.)
+// What an item costs beside its units, in units: its queries' way in, the pipeline's fill, its outputs.  (8192-token prompt of
+// d = 256 491 us with 5, 441 with 7, 442 with 8; ragged prompts of d = 128 227 us with 4, 207 with 6, 211 with 8, of d = 64 174
+// with 4, 172 with 5, 176 with 7.)
 template <int D>
-__host__ __device__ constexpr int item_cost() { return D == 256 ? 7 : 4; }
+__host__ __device__ constexpr int item_cost() { return D == 256 ? 7 : D == 128 ? 6 : 5; }
 
 // Exclusive prefix of v over the CTA, and the sum.
 template <typename T>
