@@ -619,12 +619,14 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
             __syncwarp();
         };
         const int in_block = r % kKvBlock;
+        const unsigned pool_rows = (unsigned)(p.pool.n_pages * p.pool.hkv * p.pool.page_size);
         for (int u = lg; u < units; u += L::LG) {
             // the unit's codes are asked for; they are on their way while its place is waited for
             const int st = u % STAGES, ph = u / STAGES + 1;
             if (u % kSlotGroup < L::LG) wait(&sm.slots_full[u / kSlotGroup % (kSlots / kSlotGroup)], u / kSlots);
             const int2 block = sm.block[u % kSlots][lw / 2];
-            const bool there = in_block < block.y;
+            // (a slot that the look-up gave up on holds anything: rows outside the pool are not read either)
+            const bool there = in_block < block.y && (unsigned)(block.x + in_block) < pool_rows;
             const size_t at = (size_t)(there ? block.x + in_block : 0) * D + 16 * c16;
             uint4 kr[CH], vr[CH];
 #pragma unroll
