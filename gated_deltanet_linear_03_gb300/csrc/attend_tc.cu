@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
     const int units = (int)(plan.start[cta + 1].unit - plan.start[cta].unit);
 
     // Waits are bounded.  One that runs out sets a flag with which every later wait returns at once and which becomes the
-    // call's error at the end; no warp leaves its loop, so no named barrier is left waiting.
+    // call's error at the end; no warp leaves its loop.
     auto poll = [&](uint64_t *bar, int phase) { mbar_poll(bar, (uint32_t)phase & 1, &sm.abort); };
     auto arrive = [&](uint64_t *bar) {
         __syncwarp();

@@ -189,11 +189,6 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// Barrier `id` (1..15) among `threads` threads of the CTA, whole warps.
-__device__ __forceinline__ void named_barrier(int id, int threads) {
-    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-
 // ------------------------------------------------------------------ fences
 __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -314,18 +309,6 @@ __device__ __forceinline__ void tmem_ldx2(uint32_t ta, uint32_t tb, float (&a)[N
     }
 }
 
-// 32 lanes x 32 consecutive 32-bit columns, followed by the wait, in one statement (as tmem_ld16).
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-        "tcgen05.wait::ld.sync.aligned;\n"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
 // 16 lanes x 32 columns as four 8-column groups: of group i a thread holds columns 8 i + 2 (lane % 4), + 1 of rows
 // lane / 4 (v[4 i], v[4 i + 1]) and lane / 4 + 8 (v[4 i + 2], v[4 i + 3]).
 __device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const uint32_t *v) {

@@ -71,3 +71,23 @@ def test_stream_argument(attn):
     check(outs[0][0], *ref.attend(q, cache, [0, m], lens))
     for o in outs[1:]:
         assert all(torch.equal(a, b) for a, b in zip(o, outs[0]))
+
+
+@pytest.mark.parametrize("window", [0, 20])
+def test_more_sequences_than_a_planning_pass(attn, window):
+    """1100 short prompts: the items are listed 1024 sequences at a time, and most runs hold several items."""
+    lens = [33 + n % 29 for n in range(1100)]
+    new = [33 if n % 7 else 0 for n in range(1100)]
+    cache = ref.make_cache(lens, 1, 64, 32, I8, 6)
+    q = torch.randn(sum(new), 8, 64, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    out, cu = run(attn, q, cache, new, lens, window=window)
+    check(out, *ref.attend(q, cache, cu, lens, window))
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(64, 4, 1), (128, 4, 2), (256, 4, 1)])
+def test_negative_scale_of_prompts(attn, d, hq, hkv):
+    lens = [400]
+    cache = ref.make_cache(lens, hkv, d, 16, F8, 7)
+    q = torch.randn(150, hq, d, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    out, cu = run(attn, q, cache, [150], lens, sm_scale=-0.07)
+    check(out, *ref.attend(q, cache, cu, lens, sm_scale=-0.07))
