@@ -9,7 +9,7 @@
 // rows are read once, the maximum is a CTA reduction, and codes leave as 8-byte pieces of full lines.  The
 // queries' rotation, most of the bytes with grouped heads, runs in the same launch on further CTAs.
 // Bound by memory: T (hq + 2 hkv) d 2-byte reads, T hq d 2-byte and 2 T hkv d 1-byte writes.  16384 tokens of 16 heads over
-// 2 of d = 256: 72 us, 0.76 of a copy's rate; one token takes 5.4 us, a launch and three dependent latencies.
+// 2 of d = 256, read back as well: 68 us, 0.81 of a copy's rate; one token takes 5.4 us, a launch and three dependent latencies.
 #include "kv_cache.cuh"
 
 namespace gdn {
@@ -92,7 +92,7 @@ __device__ __forceinline__ uint2 quantise8(const uint4 &u, float inv) {
 // Query warps.  A warp takes one token and up to kHeadPasses passes over its heads (a pass is 256 / D heads, a piece of 8
 // elements a lane): position, cosines and sines are found once, and all of the warp's loads are in flight together.
 // The other piece of a pair comes from its lane, so every piece is read before any is written: q_out may be q.
-constexpr int kHeadPasses = 8;
+constexpr int kHeadPasses = 4;
 
 template <int D>
 __host__ __device__ inline int head_parts(int hq) { return (hq * (D / 8) + 32 * kHeadPasses - 1) / (32 * kHeadPasses); }
@@ -174,8 +174,10 @@ __device__ __forceinline__ void rotate_queries(const AppendProblem &p, int warp,
 // ceil((past % 16 + new) / 16) <= floor(new / 16) + 2 of them without a scan over the sequences.
 __host__ __device__ inline long block_slots(int n_seqs, int total) { return total / kKvBlock + 2L * n_seqs; }
 
+// 1280 threads an SM: with four passes a query warp fits their 51 registers.  16384 tokens, us for (passes, threads): (4, 1280) 70,
+// (4, 768) 79, (4, 1536) 73, (8, 768) 73, (8, 1024) 72, (8, 1280) 81, (2, 2048) 82, (16, 768) 82.
 template <int D, int FMT>
-__global__ void __launch_bounds__(D) kv_append_kernel(const __grid_constant__ AppendProblem p) {
+__global__ void __launch_bounds__(D, 1280 / D) kv_append_kernel(const __grid_constant__ AppendProblem p) {
     constexpr int PIECES = D / 8, ROWS = D / PIECES;   // 8 rows per pass of the CTA, two passes
     __shared__ uint32_t part[2][D / 32];
     const long kv_ctas = block_slots(p.n_seqs, p.total) * p.pool.hkv;
