@@ -282,21 +282,23 @@ __global__ void __launch_bounds__(D, 1280 / D) kv_append_kernel(const __grid_con
 // One thread reads 16 codes of K and of V (one 16-byte load each) and writes 16 values of each.
 template <int FMT, bool F32>
 __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ ReadProblem p) {
-    const int units = p.d / 16;
+    const int units = p.d / 16, shift = 31 - __clz(units);            // d is a power of two
     const long i = (long)blockIdx.x * 256 + threadIdx.x;
     if (i >= (long)p.total * p.pool.hkv * units) return;
-    const int u = (int)(i % units);
-    const long row = i / units;                       // (token, head)
-    const int t = (int)(row / p.pool.hkv), h = (int)(row % p.pool.hkv);
+    const int u = (int)i & (units - 1);
+    const long row = i >> shift;                      // (token, head)
+    const int t = row >> 32 == 0 ? (int)((unsigned)row / (unsigned)p.pool.hkv) : (int)(row / p.pool.hkv), h = (int)(row - (long)t * p.pool.hkv);
     const int n = sequence_of(p.cu, p.n_seqs, t);
     const int at = t - p.cu[n];
-    int page = -1;
-    if (at >= 0 && at < (long)p.pool.max_pages * p.pool.page_size)
-        page = p.pool.table[(size_t)n * p.pool.max_pages + at / p.pool.page_size];
+    int page = -1, in_page = 0;
+    if (at >= 0 && at < (long)p.pool.max_pages * p.pool.page_size) {
+        const int nth = p.pool.page_of(at);
+        in_page = at - nth * p.pool.page_size;
+        page = p.pool.table[(size_t)n * p.pool.max_pages + nth];
+    }
     const bool ok = page >= 0 && page < p.pool.n_pages;
     if (!ok) raise_error(p.err, kErrInternal);
     const size_t head = (size_t)(ok ? page : 0) * p.pool.hkv + h;
-    const int in_page = at % p.pool.page_size;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         uint4 codes = make_uint4(0, 0, 0, 0);
