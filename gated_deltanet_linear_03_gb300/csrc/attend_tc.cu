@@ -199,6 +199,10 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
     for (long long r = (total + per - 1) / per + tid; r <= plan.ctas; r += kPlanThreads) plan.start[r] = {0, 0, total - (long long)items * ITEM_COST};
 }
 
+// M of a row that has seen no token yet: so low that the weight of any token against it is infinite, however small its score.
+// (Under a window a row may see its first token in a later unit than its item's first row.)
+constexpr float kNoReference = -3.4028235e38f;
+
 // A word with its n lowest bits set (none below 0, all above 63).
 __device__ __forceinline__ unsigned long long low_bits(int n) { return n <= 0 ? 0ull : n > 63 ? ~0ull : (1ull << n) - 1; }
 
@@ -394,7 +398,7 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                 if (u_end < units) prefetch_l1(plan.items + item + 1);
                 tc_fence_before();
                 arrive(&sm.q_full[q]);              // also: this warp has read its part of the item before
-                float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+                float m[2] = {kNoReference, kNoReference}, l[2] = {0.f, 0.f};
                 bool raise = true;                  // the item's first unit sets M
                 for (; u < u_end; ++u, ++j) {
                     // ---- one unit
@@ -465,10 +469,9 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                         auto weigh = [&](auto masked) {
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
-                                const float base = m[k] == -INFINITY ? 0.f : m[k];
 #pragma unroll
                                 for (int b = 0; b < 4; ++b) {
-                                    const float f = rs[k] * ksc[b], off = lvs[b] - base;
+                                    const float f = rs[k] * ksc[b], off = lvs[b] - m[k];
                                     float part[2];
 #pragma unroll
                                     for (int i = 0; i < 2; ++i) {
@@ -496,8 +499,8 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                         float add[2];
 #pragma unroll
                         for (int k = 0; k < 2; ++k) add[k] = (sum[k][0] + sum[k][1]) + (sum[k][2] + sum[k][3]);
-                        // a weight above 2^15 makes its sum so too; a row that saw nothing so far takes its M from any weight
-                        if (!raise && __any_sync(0xffffffffu, add[0] > (m[0] == -INFINITY ? 0.f : 32768.f) || add[1] > (m[1] == -INFINITY ? 0.f : 32768.f))) {
+                        // a weight above 2^15 makes its sum so too, and so does any token that a row without M sees
+                        if (!raise && __any_sync(0xffffffffu, add[0] > 32768.f || add[1] > 32768.f)) {
                             raise = true;
                             continue;
                         }
