@@ -237,6 +237,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NR>()) attend_split_k
         };
         auto scale_of = [&](int row) -> float { return row >= 0 ? __ldg((lane < 4 ? p.k_scales : p.v_scales) + row / kKvBlock) : 0.f; };
         const CUtensorMap *map = lane < 4 ? &k_map : &v_map;
+        const int no_row = p.pool.n_pages * p.pool.hkv * p.pool.page_size;      // past the pool's last: the load fills zeros in
         look_up();
         int row = pool_row(), stage = 0, phase = 1, issued = 0;
         float scale = scale_of(row);
@@ -249,11 +250,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NR>()) attend_split_k
             __syncwarp();
             if (*abort) break;
             if (lane < 8) {
-                // a block that does not exist is loaded from the pool's first rows: no score of it is seen, and its
-                // V rows are cleared before they are used
                 uint8_t *dst = (lane < 4 ? sm.k[stage] : sm.v[stage]) + (lane & 3) * (kKvBlock * D);
 #pragma unroll
-                for (int x = 0; x < D; x += 128) sm100::tma_load_2d(dst + x * kKvBlock, map, &sm.full[stage], x, max(row, 0));
+                for (int x = 0; x < D; x += 128) sm100::tma_load_2d(dst + x * kKvBlock, map, &sm.full[stage], x, row >= 0 ? row : no_row);
             }
             // the next unit's rows and scales, and the table's entries of the one after it, while this one's codes come
             const int next_row = unit + 1 < units ? pool_row() : -1;
@@ -377,9 +376,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NR>()) attend_split_k
                 big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 16));
                 if (g == 0) sm.red[warp][8 * r + 2 * t + c] = big;
             }
-        // V rows past the sequence's end, whatever they hold, are cleared: their weights are 0, and 0 times a code is not
-        // 0 for a code that is NaN.  (Keys there only make scores that the mask replaces.)
-        const bool tail = tok0 + kKvBlock > cc.s.kvlen;
+        // V rows of the last block that lie past the sequence's end, whatever they hold, are cleared: their weights are 0, and 0
+        // times a code is not 0 for a code that is NaN.  (Keys there only make scores that the mask replaces.)
+        const bool tail = tok0 < cc.s.kvlen && tok0 + kKvBlock > cc.s.kvlen;
         if (tail) {
             for (int i = lane; i < kKvBlock * (D / 16); i += 32)
                 if (tok0 + i / (D / 16) >= cc.s.kvlen)

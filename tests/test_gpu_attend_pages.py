@@ -1,0 +1,49 @@
+"""gdn_attend and table entries: what a page outside the pool reads as, for both kernels and both formats."""
+import math
+
+import pytest
+import torch
+
+import attn_helpers as ref
+from test_gpu_attend import F8, I8, check, run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def attn():
+    from gated_deltanet_linear_03_gb300 import attn as a
+    return a
+
+
+@pytest.mark.parametrize("dtype", [I8, F8])
+@pytest.mark.parametrize("d,m", [(64, 1), (128, 1), (256, 1), (64, 40), (64, 270), (128, 70), (256, 140)])
+def test_pages_outside_the_pool_read_as_zeros(attn, d, m, dtype):
+    """Whatever the pool holds, its first rows included: here codes 0x7F (NaN in 8-bit floats) and NaN scales."""
+    from gated_deltanet_linear_03_gb300 import gdn
+    assert gdn.device_error() == 0
+    page, lens = 16, [m + 150]
+    cache = ref.make_cache(lens, 2, d, page, dtype, 7)
+    n_pages = cache.k_pages.shape[0]
+    used = set(cache.table[0, :-(-lens[0] // page)].tolist())
+    zero, spoilt = [p for p in range(n_pages) if p not in used][:2]
+    for pages, scales in ((cache.k_pages, cache.k_scales), (cache.v_pages, cache.v_scales)):
+        raw = pages.view(torch.uint8)
+        raw[zero], scales[zero] = 0, 2.0 ** -60 / ref.QMAX[dtype]
+        raw[spoilt], scales[spoilt] = 0x7F, math.nan
+    # the spoilt page is moved to the front of the pool, where a row that does not exist might be looked for
+    order = list(range(n_pages))
+    order[0], order[spoilt] = order[spoilt], order[0]
+    back = torch.tensor([order.index(p) for p in range(n_pages)], dtype=torch.int32)
+    moved = ref.Cache(back[cache.table.long()], *[x.view(torch.uint8)[order].view(x.dtype) if x.element_size() == 1 else x[order]
+                                                  for x in cache.args])
+    zero = int(back[zero])
+    q = torch.randn(m, 4, d, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    gone = (1, 4, 5)                                        # pages of the middle; every query sees them
+    for bad in (-1, n_pages, 2 ** 31 - 1, -2 ** 31):
+        a, b = moved.table.clone(), moved.table.clone()
+        a[0, list(gone)], b[0, list(gone)] = bad, zero
+        out, cu = run(attn, q, ref.Cache(a, *moved.args), [m], lens)
+        assert gdn.device_error() == 6
+        check(out, *ref.attend(q, ref.Cache(b, *moved.args), cu, lens))
+
