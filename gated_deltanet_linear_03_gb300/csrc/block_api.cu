@@ -111,7 +111,10 @@ gdn_status gdn_kv_append(int n_seqs, int total_tokens, int hq, int hkv, int d, i
     p.k = static_cast<const __nv_bfloat16 *>(k);
     p.v = static_cast<const __nv_bfloat16 *>(v);
     p.q_stride = q_stride; p.k_stride = k_stride; p.v_stride = v_stride;
-    p.cos = cos; p.sin = sin; p.n_positions = rot > 0 ? n_positions : INT_MAX; p.interleaved = interleaved;
+    p.cos = cos; p.sin = sin; p.interleaved = interleaved;
+    const long long held = (long long)max_pages * page_size;
+    p.max_len = (int)(held < INT_MAX ? held : INT_MAX);
+    if (rot > 0 && n_positions < p.max_len) p.max_len = n_positions;
     p.cu = cu_seqlens; p.past = past_lens;
     p.pool = {block_table, max_pages, n_pages, page_size, hkv, page_shift(page_size)};
     p.format = format;

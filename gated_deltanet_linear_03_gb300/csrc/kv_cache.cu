@@ -89,6 +89,12 @@ __device__ __forceinline__ uint2 quantise8(const uint4 &u, float inv) {
     return make_uint2(values_to_codes<FMT>(x[0], x[1], x[2], x[3]), values_to_codes<FMT>(x[4], x[5], x[6], x[7]));
 }
 
+// Does the call take a sequence of `len` new tokens?  Its positions have cosines and sines and a place in the table, and its
+// slot exists; otherwise all of it is left out.
+__device__ __forceinline__ bool taken(const AppendProblem &p, int past, int len, int slot) {
+    return past >= 0 && past <= p.max_len - len && (unsigned)slot < (unsigned)p.n_slots;
+}
+
 // Query warps.  A warp takes one token and up to kHeadPasses passes over its heads (a pass is 256 / D heads, a piece of 8
 // elements a lane): position, cosines and sines are found once, and all of the warp's loads are in flight together.
 // The other piece of a pair comes from its lane, so every piece is read before any is written: q_out may be q.
@@ -107,17 +113,18 @@ __device__ __forceinline__ void rotate_queries(const AppendProblem &p, int warp,
     const bool moves = turned || p.q_out != p.q;     // in place, the pieces past rot stay where they are
     const __nv_bfloat16 *src = p.q + t * p.q_stride + (long)h0 * D + 8 * c;
     __nv_bfloat16 *dst = p.q_out + ((long)t * p.hq + h0) * D + 8 * c;
+    const int n = sequence_of(p.cu, p.n_seqs, t);
+    const int c0 = max(p.cu[n], 0), c1 = min(p.cu[n + 1], p.total), past = p.past[n];
+    if (t < c0 || t >= c1) return;                  // no sequence's
+    if (!taken(p, past, c1 - c0, p.slots ? p.slots[n] : n)) {
+        if (lane == 0) raise_error(p.err, kErrInternal);
+        return;
+    }
+    const int pos = past + t - c0;
     uint4 x[kHeadPasses];
 #pragma unroll
     for (int i = 0; i < kHeadPasses; ++i)
         x[i] = moves && h0 + i * HEADS < p.hq ? *reinterpret_cast<const uint4 *>(src + i * HEADS * D) : make_uint4(0, 0, 0, 0);
-    const int n = sequence_of(p.cu, p.n_seqs, t);
-    const int pos = p.past[n] + t - p.cu[n];
-    const bool ok = p.rot == 0 || (pos >= 0 && pos < p.n_positions);
-    if (!ok) {
-        if (lane == 0) raise_error(p.err, kErrInternal);
-        return;
-    }
     float cc[8], ss[8];
     const int other = first ? lane + p.rot / 16 : lane - p.rot / 16;
     if (turned) {
@@ -193,18 +200,15 @@ __global__ void __launch_bounds__(D, 1280 / D) kv_append_kernel(const __grid_con
         if (p.cu[mid] / kKvBlock + 2 * mid <= slot) n = mid;
         else hi = mid;
     }
-    const int c0 = min(max(p.cu[n], 0), p.total), c1 = min(max(p.cu[n + 1], c0), p.total), len = c1 - c0;
-    const int past = p.past[n];
-    const int end = past <= 0x7fffffff - len ? past + len : -1;
+    const int c0 = min(max(p.cu[n], 0), p.total), len = min(max(p.cu[n + 1], c0), p.total) - c0;
+    const int past = p.past[n], os = p.slots ? p.slots[n] : n;
     const int local = slot - (p.cu[n] / kKvBlock + 2 * n);
     if (len == 0 && past >= 0 && past % kKvBlock == 0) return;
-    const int os = p.slots ? p.slots[n] : n;
-    const int first = past / kKvBlock, last = (end - 1) / kKvBlock;
-    if (past < 0 || end < 0 || (p.rot > 0 && end > p.n_positions) || (long)end > (long)p.pool.max_pages * p.pool.page_size ||
-        os < 0 || os >= p.n_slots) {
+    if (!taken(p, past, len, os)) {
         if (threadIdx.x == 0) raise_error(p.err, kErrInternal);
         return;
     }
+    const int end = past + len, first = past / kKvBlock, last = (end - 1) / kKvBlock;
     if (local > last - first) return;
     // The first block reads open_in, the last writes open_out, which may be the same memory: when they are
     // different blocks, one CTA does both, in that order.

@@ -79,7 +79,7 @@ struct AppendProblem {
     const __nv_bfloat16 *q, *k, *v;
     long long q_stride, k_stride, v_stride;
     const float *cos, *sin;
-    int n_positions, interleaved;
+    int max_len, interleaved;       // longest sequence that the cos and sin tables and the block table hold
     const int32_t *cu, *past;
     KvPool pool;
     int format;

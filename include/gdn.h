@@ -422,8 +422,9 @@ typedef enum {
  * with zeros in the places of tokens still to come.  An unfinished block is quantised again from its bf16
  * tokens as it grows, so the cache does not depend on how a prompt was divided into calls.  A block with an
  * infinity or NaN gets that as its scale and codes 0: it reads as NaN, its neighbours are unharmed.
- * A token whose position is negative, or outside the cos/sin tables or the block table, records
- * GDN_ERR_INTERNAL and its sequence is left out.
+ * A sequence with a position that is negative, or outside the cos/sin tables or the block table, or with a slot
+ * outside [0, n_slots), records GDN_ERR_INTERNAL and is left out: nothing of it is stored, and its rows of q_out
+ * and open_out are untouched, as are the q_out rows of tokens that no sequence holds.
  */
 GDN_API gdn_status gdn_kv_append(int n_seqs, int total_tokens, int hq, int hkv, int d, int rot,
                                  const void *q, long long q_stride, const void *k, long long k_stride,
