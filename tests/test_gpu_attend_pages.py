@@ -47,3 +47,35 @@ def test_pages_outside_the_pool_read_as_zeros(attn, d, m, dtype):
         assert gdn.device_error() == 6
         check(out, *ref.attend(q, ref.Cache(b, *moved.args), cu, lens))
 
+
+
+@pytest.mark.parametrize("kv", [64, 5000])
+def test_replays_without_queries(attn, kv):
+    """A captured call of a few items, replayed while its sequences come and go: without any query it writes nothing, and the
+    kernel after it may change the lengths."""
+    lens = [kv, kv - 7]
+    cache = ref.make_cache(lens, 2, 128, 32, I8, 3)
+    c = cache.on("cuda")
+    q = torch.randn(2, 8, 128, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    qd, cu, length = q.cuda(), torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda"), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    none, both = torch.zeros_like(cu), cu.clone()
+    out = torch.empty(2, 8, 128, device="cuda")
+    ws = torch.empty(attn.attend_workspace_size(2, 2, 8, 2, 128, 1, kv), dtype=torch.uint8, device="cuda")
+    kw = dict(max_q_len=1, max_kv_len=kv, out=out, workspace=ws)
+    attn.attend(qd, *c.args, c.table, cu, length, **kw)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        attn.attend(qd, *c.args, c.table, cu, length, **kw)
+    want, tol = ref.attend(q, cache, [0, 1, 2], lens)
+    for _ in range(20):
+        cu.copy_(none)
+        out.fill_(5.0)
+        graph.replay()
+        cu.copy_(both)
+        torch.cuda.synchronize()
+        assert (out == 5).all()
+        graph.replay()
+        cu.copy_(none)
+        torch.cuda.synchronize()
+        check(out, want, tol)
