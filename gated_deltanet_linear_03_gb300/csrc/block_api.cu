@@ -248,6 +248,7 @@ gdn_status gdn_block_norm(int rows, int dim, const void *x, const void *gate, in
                           const float *scale_weight, float scale, float eps, void *residual_out, void *out, void *stream) {
     if (rows < 0 || dim <= 0) return GDN_ERR_INVALID_ARG;
     if (dim % 8 != 0 || dim > 16384) return GDN_ERR_UNSUPPORTED;
+    if (rows > INT_MAX - 65536) return GDN_ERR_UNSUPPORTED;                             // a CTA's next row is counted in 32 bits
     if (residual_dtype != GDN_DTYPE_BF16 && residual_dtype != GDN_DTYPE_F32) return GDN_ERR_UNSUPPORTED;
     if (gate_act != GDN_GATE_SIGMOID && gate_act != GDN_GATE_SILU) return GDN_ERR_UNSUPPORTED;
     if (!isfinite(scale) || !isfinite(eps) || eps < 0.f) return GDN_ERR_INVALID_ARG;

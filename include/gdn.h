@@ -486,7 +486,7 @@ GDN_API gdn_status gdn_attend(int n_seqs, int total_tokens, int hq, int hkv, int
  *     h  = r' / sqrt(mean(r'^2) + eps) * pre_weight
  * in fp32; r' and h are rounded once, h from the unrounded r'.
  *
- *   rows, dim               dim a multiple of 8, 8 .. 16384
+ *   rows, dim               rows 0 .. 2^31 - 65537; dim a multiple of 8, 8 .. 16384
  *   x, gate                 bf16 [rows, dim]; gate may be NULL
  *   gate_act                GDN_GATE_SIGMOID (act(g) = 1 / (1 + e^-g)) or GDN_GATE_SILU (g / (1 + e^-g))
  *   residual, residual_out  [rows, dim], dtype residual_dtype; residual_out may be residual (in place)
