@@ -176,6 +176,7 @@ static gdn_status check_attend_shape(int n_seqs, int total_tokens, int hq, int h
     if (total_tokens < max_q_len) max_q_len = total_tokens;
     if (hq % hkv != 0 || (total_tokens > 0 && max_q_len == 0)) return GDN_ERR_INVALID_ARG;
     if (d != 64 && d != 128 && d != 256) return GDN_ERR_UNSUPPORTED;
+    if (max_kv_len > INT_MAX - 4096) return GDN_ERR_UNSUPPORTED;                        // a tile's tokens are counted in 32 bits
     if ((double)total_tokens * hq >= 2147483648.0 - 4096) return GDN_ERR_UNSUPPORTED;   // the kernels count query rows in 32 bits
     if (!gdn::attend_supported(n_seqs, hq, hkv, d, max_q_len, max_kv_len)) return GDN_ERR_UNSUPPORTED;         // and units of work
     return GDN_OK;

@@ -456,7 +456,7 @@ GDN_API gdn_status gdn_kv_read(int n_seqs, int total_tokens, int hkv, int d, con
  *   kv_lens        int32 [n_seqs] on the device: tokens of each sequence in the cache.  Its m queries stand at
  *                  positions kv_lens[n] - m .. kv_lens[n] - 1
  *   max_q_len,     upper bounds of the device values, known on the host: they choose the kernel and size the
- *   max_kv_len     workspace.  A sequence beyond a bound records GDN_ERR_INTERNAL and is cut to it.  A CUDA
+ *   max_kv_len     workspace (max_kv_len at most 2^31 - 4097, and what the table holds).  A sequence beyond a bound records GDN_ERR_INTERNAL and is cut to it.  A CUDA
  *                  graph may be captured with generous bounds and replayed as the lengths grow.
  *   sm_scale       multiplies the products q.k (finite; usually 1/sqrt(d))
  *   window, sinks  a query at position p sees token j when j <= p and (window == 0, or j > p - window, or
