@@ -72,7 +72,7 @@ gdn_status gdn_kv_append(int n_seqs, int total_tokens, int hq, int hkv, int d, i
     if (k_stride < kv_row || v_stride < kv_row || (q && q_stride < q_row)) return GDN_ERR_INVALID_ARG;
     if (k_stride % 8 || v_stride % 8 || (q && q_stride % 8)) return GDN_ERR_ALIGNMENT;
     if (n_seqs == 0 && total_tokens > 0) return GDN_ERR_INVALID_ARG;
-    if ((double)total_tokens * hq * (d / 8) >= 2147483648.0 * 32 * 8) return GDN_ERR_UNSUPPORTED;   // query warps are counted in 32 bits
+    if (!gdn::append_supported(n_seqs, total_tokens, hq, hkv, d)) return GDN_ERR_UNSUPPORTED;
     if (n_seqs == 0) return GDN_OK;
     if (!slots && n_slots < n_seqs) return GDN_ERR_INVALID_ARG;
     if (!cu_seqlens || !past_lens || !block_table || !k_pages || !v_pages || !k_scales || !v_scales || !open_in || !open_out)

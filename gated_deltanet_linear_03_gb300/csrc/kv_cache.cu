@@ -336,14 +336,19 @@ __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ Re
 
 }  // namespace
 
+namespace {
+long append_query_ctas(int total, int hq, int d) {
+    const int parts = d == 64 ? head_parts<64>(hq) : d == 128 ? head_parts<128>(hq) : head_parts<256>(hq);
+    return ((long)total * parts + d / 32 - 1) / (d / 32);
+}
+}  // namespace
+
+bool append_supported(int n_seqs, int total, int hq, int hkv, int d) {
+    return (double)hq * d < 2147483648.0 && (double)block_slots(n_seqs, total) * hkv + append_query_ctas(total, hq, d) <= 2147483647 / 8;
+}
+
 cudaError_t launch_kv_append(const AppendProblem &p) {
-    const long kv_ctas = block_slots(p.n_seqs, p.total) * p.pool.hkv;
-    long q_ctas = 0;
-    if (p.q) {
-        const int parts = p.d == 64 ? head_parts<64>(p.hq) : p.d == 128 ? head_parts<128>(p.hq) : head_parts<256>(p.hq);
-        q_ctas = ((long)p.total * parts + p.d / 32 - 1) / (p.d / 32);
-    }
-    if (kv_ctas + q_ctas > 2147483647L / 8) return cudaErrorInvalidValue;
+    const long kv_ctas = block_slots(p.n_seqs, p.total) * p.pool.hkv, q_ctas = p.q ? append_query_ctas(p.total, p.hq, p.d) : 0;
     using Fn = void (*)(const AppendProblem);
     const bool e4m3 = p.format == GDN_KV_E4M3;
     const Fn fn = p.d == 64 ? (e4m3 ? kv_append_kernel<64, GDN_KV_E4M3> : kv_append_kernel<64, GDN_KV_INT8>)

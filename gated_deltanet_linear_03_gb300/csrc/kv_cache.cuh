@@ -94,6 +94,7 @@ struct AppendProblem {
     cudaStream_t stream;
 };
 cudaError_t launch_kv_append(const AppendProblem &p);
+bool append_supported(int n_seqs, int total, int hq, int hkv, int d);   // the kernel counts its CTAs and query warps in 32 bits
 
 struct ReadProblem {
     int n_seqs, total, d;

@@ -1,7 +1,7 @@
 """Host-only checks of sizes whose sums would leave 32 bits in the cache, attention and block-norm kernels: they are refused."""
 import pytest
 
-from test_block_abi import UNSUPPORTED, attend, lib, norm, workspace  # noqa: F401
+from test_block_abi import UNSUPPORTED, append, at, attend, lib, norm, workspace  # noqa: F401
 
 TOP = 2 ** 31 - 1
 
@@ -22,3 +22,10 @@ def test_attend_lengths(lib, kv):  # noqa: F811
 
 def test_attend_lengths_below(lib):  # noqa: F811
     assert workspace(lib, mk=TOP - 4096)[1] == 0
+
+
+@pytest.mark.parametrize("kw", [dict(n=2 ** 27, slots=at(15)), dict(T=2 ** 30, hkv=8, ks=1024, vs=1024, hq=8, qs=1024),
+                                dict(T=2 ** 20, hkv=2, hq=2 ** 18, qs=2 ** 25)])
+def test_append_work(lib, kw):  # noqa: F811
+    """Blocks and query warps are counted in 32 bits; too many are a size that is not supported, not a failed launch."""
+    assert append(lib, **kw) == UNSUPPORTED
