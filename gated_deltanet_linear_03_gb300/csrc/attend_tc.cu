@@ -117,19 +117,18 @@ template <int D>
 __host__ __device__ constexpr int item_cost() { return D == 256 ? 7 : D == 128 ? 6 : 5; }
 
 // Exclusive prefix of v over the CTA, and the sum.
-template <typename T>
-__device__ __forceinline__ T block_scan(T v, T &sum, T *part) {
+__device__ __forceinline__ long long block_scan(long long v, long long &sum, long long *part) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    T x = v;
+    long long x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const T y = __shfl_up_sync(0xffffffffu, x, o);
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
     __syncthreads();
     if (lane == 31) part[warp] = x;
     __syncthreads();
-    T before = 0;
+    long long before = 0;
     sum = 0;
     for (int w = 0; w < (int)blockDim.x / 32; ++w) {
         if (w < warp) before += part[w];
@@ -143,8 +142,7 @@ __device__ __forceinline__ T block_scan(T v, T &sum, T *part) {
 // before, a batch of sequences at a time.
 template <int ROWS, int ITEM_COST>
 __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_constant__ AttendProblem p, const __grid_constant__ TcPlan plan) {
-    __shared__ int part[kPlanThreads / 32];
-    __shared__ long long part_cost[kPlanThreads / 32];
+    __shared__ long long part[kPlanThreads / 32];
     __shared__ int first[kPlanThreads + 1];       // first item of each sequence of the batch
     __shared__ Sequence seqs[kPlanThreads];
     const int tid = threadIdx.x, group = p.hq / p.pool.hkv;
@@ -159,12 +157,14 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
             if (b - a > p.max_q_len || c > p.max_kv_len || c < 0 || b > p.total || a < 0 || b < a) raise_error(p.err, kErrInternal);
         }
         seqs[tid] = s;
-        int sum;
-        first[tid] = block_scan(row_tiles<ROWS>(s.qlen, group) * p.pool.hkv, sum, part);
+        // (in 64 bits: sequences out of order may hold the call's rows many times over; what is too many is cut, and recorded)
+        const long long room = plan.max_items - items;
+        long long all;
+        first[tid] = (int)min(block_scan((long long)row_tiles<ROWS>(s.qlen, group) * p.pool.hkv, all, part), room);
+        const int sum = (int)min(all, room);
         if (tid == 0) first[batch] = sum;
         __syncthreads();
-        if (tid == 0 && sum > plan.max_items - items) raise_error(p.err, kErrInternal);
-        sum = min(sum, plan.max_items - items);
+        if (tid == 0 && all > room) raise_error(p.err, kErrInternal);
         for (int k = tid; k < sum; k += kPlanThreads) {
             int lo = 0;
             for (int hi = batch; hi - lo > 1;) {
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kPlanThreads) attend_plan_kernel(const __grid_
     const int each = (items + kPlanThreads - 1) / kPlanThreads, i0 = min(tid * each, items), i1 = min(i0 + each, items);
     long long mine = 0, total;
     for (int i = i0; i < i1; ++i) mine += plan.items[i].tiles + ITEM_COST;
-    long long at = block_scan(mine, total, part_cost);
+    long long at = block_scan(mine, total, part);
     const long long per = max((total + plan.ctas - 1) / plan.ctas, 1LL);
     if (tid == 0) plan.per[0] = per;
     long long c = (at + per - 1) / per;           // the first run that begins at or after this thread's items
