@@ -51,6 +51,12 @@ def _device(t: torch.Tensor, name: str) -> int:
     return index
 
 
+def _int32(x: int) -> int:
+    """``x`` for a C int: a value beyond its range becomes the range's end, or -1, which the library judges as it would ``x``
+    (ctypes alone would pass its low 32 bits)."""
+    return x if -1 <= x <= 0x7fffffff else 0x7fffffff if x > 0 else -1
+
+
 def _launch(fn, name, index, stream, *args):
     """Call ``fn(*args, stream)`` with the tensors' device current."""
     handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
@@ -214,7 +220,8 @@ def attend_workspace_size(n_seqs: int, total_tokens: int, hq: int, hkv: int, d: 
                           max_kv_len: int) -> int:
     """Bytes of workspace that :func:`attend` needs for this problem (``gdn_attend_workspace_size``)."""
     st = ctypes.c_int(0)
-    need = load_library().gdn_attend_workspace_size(n_seqs, total_tokens, hq, hkv, d, max_q_len, max_kv_len, st)
+    sizes = map(_int32, (n_seqs, total_tokens, hq, hkv, d, max_q_len, max_kv_len))
+    need = load_library().gdn_attend_workspace_size(*sizes, st)
     if st.value != GDN_OK:
         raise GdnError(st.value, "gdn_attend_workspace_size")
     return int(need)
@@ -262,6 +269,6 @@ def attend(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scal
         ws_bytes = workspace.numel() * workspace.element_size()
     table, max_pages, n_pages, page, fmt = pool
     _launch(lib.gdn_attend, "gdn_attend", dev, stream, n, T, hq, hkv, d, qp, *pages, table, max_pages, n_pages, page,
-            fmt, cu, lens, max_q_len, max_kv_len, 1.0 / math.sqrt(d) if sm_scale is None else sm_scale, window, sinks,
-            op, out_code, workspace.data_ptr(), ws_bytes)
+            fmt, cu, lens, _int32(max_q_len), _int32(max_kv_len), 1.0 / math.sqrt(d) if sm_scale is None else sm_scale,
+            _int32(window), _int32(sinks), op, out_code, workspace.data_ptr(), ws_bytes)
     return out

@@ -9,7 +9,7 @@ from typing import Optional, Tuple, Union
 
 import torch
 
-from .attn import _contiguous, _device, _empty, _launch
+from .attn import _contiguous, _device, _empty, _int32, _launch
 from .gdn import DTYPE, load_library
 
 GATE_ACT = {"sigmoid": 0, "silu": 1}
@@ -59,7 +59,7 @@ def block_norm(x: torch.Tensor, residual: torch.Tensor, pre_weight: torch.Tensor
         op = out.data_ptr()
     else:
         op = _contiguous("out", out, bf16, nd, dev)
-    _launch(lib.gdn_block_norm, "gdn_block_norm", dev, stream, x.numel() // dim if dim else 0, dim, xp,
+    _launch(lib.gdn_block_norm, "gdn_block_norm", dev, stream, _int32(x.numel() // dim) if dim else 0, dim, xp,
             0 if gate is None else _contiguous("gate", gate, bf16, nd, dev), act, rp, res_code,
             0 if post_weight is None else _contiguous("post_weight", post_weight, f32, 1, dev),
             _contiguous("pre_weight", pre_weight, f32, 1, dev), _contiguous("scale", scale, f32, 1, dev) if scaled else 0,

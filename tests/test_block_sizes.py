@@ -29,3 +29,10 @@ def test_attend_lengths_below(lib):  # noqa: F811
 def test_append_work(lib, kw):  # noqa: F811
     """Blocks and query warps are counted in 32 bits; too many are a size that is not supported, not a failed launch."""
     assert append(lib, **kw) == UNSUPPORTED
+
+
+def test_python_integers():
+    """Values that do not fit a C int keep their meaning: nothing wraps round."""
+    from gated_deltanet_linear_03_gb300.attn import _int32
+    assert [_int32(x) for x in (0, 7, TOP, TOP + 1, 2 ** 32, 2 ** 32 + 5, -1, -2, -2 ** 31, -2 ** 32, -2 ** 40)] == \
+        [0, 7, TOP, TOP, TOP, TOP, -1, -1, -1, -1, -1]
