@@ -87,7 +87,7 @@ def _token_rows(name: str, t: torch.Tensor, heads: int, d: int, index: int) -> T
         raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {tuple(shape)}")
     if stride[2] != 1 or (heads > 1 and stride[1] != d):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), stride[0] if shape[0] > 1 else max(stride[0], heads * d)
+    return t.data_ptr(), stride[0] if shape[0] > 1 else heads * d       # (a single token's stride says nothing)
 
 
 def _pool(k_pages, v_pages, k_scales, v_scales, block_table, index):

@@ -80,3 +80,22 @@ def test_tokens_of_no_sequence(attn):
     pos = torch.cat([torch.arange(20), torch.arange(13)])
     check_rotated(out[:33], q[:33].cpu(), pos, run)
     assert (out[33:] == 9).all()
+
+
+@pytest.mark.parametrize("pad", [0, 4, 64])
+def test_one_token_of_a_wider_row(attn, pad):
+    """A single token's q, k and v as slices of one row: no other token stands a stride away, so any stride is right, also for
+    a query that is rotated in place."""
+    hq, hkv, d = 6, 2, 128
+    whole = Run(attn, [9], hq, hkv, d, 32, 16, I8, seed=3)
+    part = Run(attn, [9], hq, hkv, d, 32, 16, I8, seed=3)
+    q, k, v = whole.inputs([1])
+    width = (hq + 2 * hkv) * d + pad
+    fused = torch.zeros(2 * width, dtype=torch.bfloat16, device="cuda")
+    fused[:width - pad] = torch.cat([x.flatten() for x in (q, k, v)]).cuda()
+    qs, ks, vs = (fused.as_strided((1, h, d), (width, d, 1), at * d) for h, at in ((hq, 0), (hkv, hq), (hkv, hq + hkv)))
+    want, _ = whole.append([1], q, k, v)
+    got, _ = part.append([1], qs, ks, vs, q_out=qs)
+    assert got is qs and torch.equal(got, want)
+    for x, y in zip(whole.pool, part.pool):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
