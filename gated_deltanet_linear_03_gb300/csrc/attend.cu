@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NR>()) attend_split_k
         int entry, in_page, head;
         auto look_up = [&]() {      // asks for the table's entry, which is looked at when the unit's turn comes
             const int tok = cc.it.token(cc.j, kTile) + (lane & 3) * kKvBlock;
-            exists = lane < 8 && tok < cc.s.kvlen;
+            exists = lane < 8 && tok < cc.s.kvlen && in_sight(cc.it.lo_pos, cc.it.hi_pos, tok, tok + kKvBlock, p.window, p.sinks);
             if (!exists) return;
             const int at = p.pool.page_of(tok);
             entry = __ldg(p.pool.table + (size_t)cc.n * p.pool.max_pages + at);

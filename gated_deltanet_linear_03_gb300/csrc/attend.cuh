@@ -64,6 +64,12 @@ __device__ __forceinline__ bool sees(int pos, int token, int window, int sinks) 
     return token <= pos && (window == 0 || token > pos - window || token < sinks);
 }
 
+// Does any of the rows at lo_pos .. hi_pos see any of tokens [a, b)?  A block of the cache that none sees is not looked up: the
+// pages that a window has left may belong to somebody else.
+__device__ __forceinline__ bool in_sight(int lo_pos, int hi_pos, int a, int b, int window, int sinks) {
+    return a <= hi_pos && (window == 0 || b - 1 > lo_pos - window || a < sinks);
+}
+
 template <int ROWS, int TILE>
 __device__ __forceinline__ Item make_item(const AttendProblem &p, const Sequence &s, int group, int mt) {
     Item it;

@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(Tc<D>::THREADS, 1) attend_tc_kernel(const __gr
                         it = plan.items[++item];
                     }
                     const int tok = first_token(it.near_tiles, it.far_tile, j) + kKvBlock * b;
-                    if (tok < it.kvlen) {
+                    if (tok < it.kvlen && in_sight(it.lo_pos, it.hi_pos, tok, tok + kKvBlock, p.window, p.sinks)) {
                         const int at = p.pool.page_of(tok), entry = __ldg(p.pool.table + (size_t)it.n * p.pool.max_pages + at);
                         if ((unsigned)entry < (unsigned)p.pool.n_pages) {
                             block = make_int2((entry * p.pool.hkv + it.h) * p.pool.page_size + tok - at * p.pool.page_size, min(it.kvlen - tok, kKvBlock));

@@ -461,7 +461,8 @@ GDN_API gdn_status gdn_kv_read(int n_seqs, int total_tokens, int hkv, int d, con
  *   sm_scale       multiplies the products q.k (finite; usually 1/sqrt(d))
  *   window, sinks  a query at position p sees token j when j <= p and (window == 0, or j > p - window, or
  *                  j < sinks): a sliding window of `window` tokens, its own included, whose first `sinks`
- *                  tokens stay visible.  A query that sees nothing gets zeros.
+ *                  tokens stay visible.  A query that sees nothing gets zeros.  A page none of whose tokens is seen
+ *                  by any query is not read, nor is its table entry: it may have been given away.
  *   out            [T, hq, d], dtype out_dtype
  *   workspace      at least gdn_attend_workspace_size() bytes, 256-byte aligned; contents do not matter
  *

@@ -79,3 +79,32 @@ def test_replays_without_queries(attn, kv):
         cu.copy_(none)
         torch.cuda.synchronize()
         check(out, want, tol)
+
+
+@pytest.mark.parametrize("d,hq,hkv,page", [(64, 4, 2, 16), (128, 8, 1, 48), (256, 4, 2, 32)])
+@pytest.mark.parametrize("m", [1, 5, 200])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (40, 0), (40, 5), (129, 20)])
+def test_pages_that_the_window_has_left(attn, window, sinks, m, d, hq, hkv, page):
+    """Pages that no query sees any more are given away: their entries are outside the pool, or the pages hold anything.  That
+    is no error and changes nothing, although tiles that are read begin inside or before them."""
+    from gated_deltanet_linear_03_gb300 import gdn
+    assert gdn.device_error() == 0
+    lens = [m + 700, m + 333]
+    new = [m, m]
+    cache = ref.make_cache(lens, hkv, d, page, F8, 9)
+    clean = ref.Cache(*[x.clone() for x in (cache.table, *cache.args)])
+    gone = []
+    for n, length in enumerate(lens):
+        for j in range(-(-length // page)):
+            if j * page >= sinks and (j + 1) * page - 1 <= length - m - window:
+                gone.append(int(cache.table[n, j]))
+                cache.table[n, j] = -1
+    assert len(gone) > 5
+    for pages, scales in ((cache.k_pages, cache.k_scales), (cache.v_pages, cache.v_scales)):
+        pages.view(torch.uint8)[gone] = 0x7F
+        scales[gone] = math.nan
+    q = torch.randn(2 * m, hq, d, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16)
+    for table in (cache.table, clean.table):
+        out, cu = run(attn, q, ref.Cache(table, *cache.args), new, lens, window=window, sinks=sinks)
+        assert gdn.device_error() == 0
+        check(out, *ref.attend(q, clean, cu, lens, window, sinks))
