@@ -99,15 +99,6 @@ __device__ __forceinline__ int sequence_cost(const AttendProblem &p, const Seque
     return c * p.pool.hkv;
 }
 
-// Largest magnitude of 8 bf16 values as the bits of a float (NaN above infinity above every finite number).
-__device__ __forceinline__ uint32_t amax_bits(const uint4 &u) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, max((w[i] << 16) & 0x7fff0000u, w[i] & 0x7fff0000u));
-    return m;
-}
-
 // Powers of two, down * up = 1, that bring a row with this largest magnitude below 2: bf16 components then turn
 // to fp16 exactly, except ones below 2^-14 of the largest, which keep an error below 2^-24 of it.  A row of zeros, or
 // one with an infinity or NaN, is left as it is.

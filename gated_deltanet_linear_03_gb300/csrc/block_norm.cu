@@ -12,24 +12,6 @@
 namespace gdn {
 namespace {
 
-__device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
-    x[0] = bf16_lo(u.x); x[1] = bf16_hi(u.x); x[2] = bf16_lo(u.y); x[3] = bf16_hi(u.y);
-    x[4] = bf16_lo(u.z); x[5] = bf16_hi(u.z); x[6] = bf16_lo(u.w); x[7] = bf16_hi(u.w);
-}
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&b);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void load8f(const float *p, float (&x)[8]) {
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *(reinterpret_cast<const float4 *>(p) + 1);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-
 // Sum over the CTA; `part` is one float per warp, a different one for each of the two sums.
 __device__ __forceinline__ float cta_sum(float v, float *part) {
 #pragma unroll
@@ -82,14 +64,14 @@ __global__ void __launch_bounds__(STAY ? 512 : 1024, C == 1 ? 2 : 1) block_norm_
         float s[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] = 1.f, s[e] = p.scale;
-        if (c < pieces && p.post_w) load8f(p.post_w + 8 * c, w);
-        if (c < pieces && p.scale_w) load8f(p.scale_w + 8 * c, s);
+        if (c < pieces && p.post_w) load8(p.post_w + 8 * c, w);
+        if (c < pieces && p.scale_w) load8(p.scale_w + 8 * c, s);
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] *= s[e];
     };
     auto load_pre = [&](int i, float (&w)[8]) {
         const int c = threadIdx.x + i * nt;
-        if (c < pieces) load8f(p.pre_w + 8 * c, w);
+        if (c < pieces) load8(p.pre_w + 8 * c, w);
     };
     float post[C][8], pre[C][8];
     if (STAY) {

@@ -15,35 +15,14 @@
 namespace gdn {
 namespace {
 
-__device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
-    x[0] = bf16_lo(u.x); x[1] = bf16_hi(u.x); x[2] = bf16_lo(u.y); x[3] = bf16_hi(u.y);
-    x[4] = bf16_lo(u.z); x[5] = bf16_hi(u.z); x[6] = bf16_lo(u.w); x[7] = bf16_hi(u.w);
-}
-
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&p);
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
-}
-
-// 8 consecutive table entries.
-__device__ __forceinline__ void load8(const float *__restrict__ p, float (&x)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-
-// Interleaved pairs inside one piece of 8 elements: cos and sin of its four pairs.
-__device__ __forceinline__ void rotate_pairs(float (&x)[8], const float *__restrict__ cos, const float *__restrict__ sin) {
-    const float4 c = __ldg(reinterpret_cast<const float4 *>(cos)), s = __ldg(reinterpret_cast<const float4 *>(sin));
-    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+// Interleaved pairs inside one piece of 8 elements, by cos and sin of its four pairs (the first of c and s).
+template <int N>
+__device__ __forceinline__ void rotate_pairs(float (&x)[8], const float (&c)[N], const float (&s)[N]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float a = x[2 * i], b = x[2 * i + 1];
-        x[2 * i] = a * cc[i] - b * ss[i];
-        x[2 * i + 1] = b * cc[i] + a * ss[i];
+        x[2 * i] = a * c[i] - b * s[i];
+        x[2 * i + 1] = b * c[i] + a * s[i];
     }
 }
 
@@ -55,7 +34,10 @@ __device__ __forceinline__ uint4 rotated_piece(const __nv_bfloat16 *__restrict__
     float x[8];
     unpack8(raw, x);
     if (interleaved) {
-        rotate_pairs(x, cos + 4 * c, sin + 4 * c);
+        float cc[4], ss[4];
+        load4(cos + 4 * c, cc);
+        load4(sin + 4 * c, ss);
+        rotate_pairs(x, cc, ss);
     } else {
         const bool first = 16 * c < rot;                     // the a-half of the pairs
         const int other = first ? c + rot / 16 : c - rot / 16;
@@ -68,16 +50,6 @@ __device__ __forceinline__ uint4 rotated_piece(const __nv_bfloat16 *__restrict__
         for (int i = 0; i < 8; ++i) x[i] = first ? x[i] * cc[i] - y[i] * ss[i] : x[i] * cc[i] + y[i] * ss[i];
     }
     return pack8(x);
-}
-
-// Largest magnitude of 8 bf16 values as the bits of a float: ordered like the magnitudes, with infinity above
-// every finite number and NaN above infinity.
-__device__ __forceinline__ uint32_t amax_bits(const uint4 &u) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) m = max(m, max((w[i] << 16) & 0x7fff0000u, w[i] & 0x7fff0000u));
-    return m;
 }
 
 template <int FMT>
@@ -130,9 +102,8 @@ __device__ __forceinline__ void rotate_queries(const AppendProblem &p, int warp,
     if (turned) {
         const float *cos = p.cos + (size_t)pos * (p.rot / 2), *sin = p.sin + (size_t)pos * (p.rot / 2);
         if (p.interleaved) {
-            const float4 a = __ldg(reinterpret_cast<const float4 *>(cos + 4 * c)), b = __ldg(reinterpret_cast<const float4 *>(sin + 4 * c));
-            cc[0] = a.x; cc[1] = a.y; cc[2] = a.z; cc[3] = a.w;
-            ss[0] = b.x; ss[1] = b.y; ss[2] = b.z; ss[3] = b.w;
+            load4(cos + 4 * c, cc);
+            load4(sin + 4 * c, ss);
         } else {
             const int at = 8 * (first ? c : c - p.rot / 16);
             load8(cos + at, cc);
@@ -150,12 +121,7 @@ __device__ __forceinline__ void rotate_queries(const AppendProblem &p, int warp,
             if (turned) {
                 float y[8];
                 unpack8(x[i], y);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float a = y[2 * e], b = y[2 * e + 1];
-                    y[2 * e] = a * cc[e] - b * ss[e];
-                    y[2 * e + 1] = b * cc[e] + a * ss[e];
-                }
+                rotate_pairs(y, cc, ss);
                 x[i] = pack8(y);
             }
         } else if (p.rot > 0) {

@@ -63,6 +63,40 @@ __device__ __forceinline__ uint32_t values_to_codes(float a, float b, float c, f
     return w;
 }
 
+// 8 bf16 values (16 bytes) to 32 bits and back, rounded once.
+__device__ __forceinline__ void unpack8(const uint4 &u, float (&x)[8]) {
+    x[0] = bf16_lo(u.x); x[1] = bf16_hi(u.x); x[2] = bf16_lo(u.y); x[3] = bf16_hi(u.y);
+    x[4] = bf16_lo(u.z); x[5] = bf16_hi(u.z); x[6] = bf16_lo(u.w); x[7] = bf16_hi(u.w);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+    return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+}
+
+// 4 or 8 consecutive entries of a table that the call does not write.
+template <int N>
+__device__ __forceinline__ void load4(const float *p, float (&x)[N]) {
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+}
+__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
+    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+
+// Largest magnitude of 8 bf16 values as the bits of a float: ordered like the magnitudes, with infinity above
+// every finite number and NaN above infinity.
+__device__ __forceinline__ uint32_t amax_bits(const uint4 &u) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, max((w[i] << 16) & 0x7fff0000u, w[i] & 0x7fff0000u));
+    return m;
+}
+
 // The sequence that holds row t of n packed ones: the last i with cu[i] <= t (t < cu[n]).
 __device__ __forceinline__ int sequence_of(const int32_t *__restrict__ cu, int n, int t) {
     int lo = 0, hi = n;
