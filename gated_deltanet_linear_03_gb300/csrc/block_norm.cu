@@ -149,10 +149,12 @@ __global__ void __launch_bounds__(STAY ? 512 : 1024, C == 1 ? 2 : 1) block_norm_
 
 cudaError_t launch_block_norm(const BlockNormProblem &p) {
     const int pieces = p.dim / 8;
-    // One piece a thread up to 512 of them, then two.  Many short rows with an fp32 residual, whose piece is two loads, are
-    // faster with two as well: 16383 x 2048 77 us against 81, 32000 x 1024 75 / 79; but 8000 x 4096 73 / 71, one row 3.1 / 2.8,
-    // and with a bf16 residual 52.5 / 52.1.
-    const int c = pieces > 512 || (p.residual_f32 && pieces <= 256 && p.rows >= 4096) ? 2 : 1;
+    // One piece a thread up to 512 of them, then two.  Many short rows with an fp32 residual, whose piece is two loads, mostly
+    // gain from two as well (us with two / with one): 16383 x 2048 77 / 80, 4096 x 2048 19.9 / 20.4, 60000 x 1536 208 / 220,
+    // 32000 x 1024 75 / 79, 16384 x 512 20.3 / 20.5, 16384 x 264 13.4 / 16.0; less so 16384 x 640 26.7 / 24.7 and 4096 x 768
+    // 10.1 / 9.0.  Not where one warp holds the row with one (16384 x 256 12.9 / 11.4), at 8000 x 4096 73 / 71, for one row
+    // (of 2048 3.1 / 2.9), nor with a bf16 residual (16383 x 2048 52.5 / 52.1).
+    const int c = pieces > 512 || (p.residual_f32 && pieces > 32 && pieces <= 256 && p.rows >= 4096) ? 2 : 1;
     const int threads = ((pieces + c - 1) / c + 31) / 32 * 32;
     using Fn = void (*)(const BlockNormProblem);
     const bool f32 = p.residual_f32;
