@@ -408,8 +408,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm<D, NR>()) attend_split_k
                     acc[r][i][2 + c] *= corr;
                 }
             }
-            // fp16 weights: at most 1, 2^-11 relative error each, far below the bf16 rounding of the output.  They are
-            // stored transposed, as 64 tokens of each row.
+            // fp16 weights: at most 1, with an error of 2^-11 of themselves or 2^-25, whichever is larger, far below the bf16
+            // rounding of the output.  They are stored transposed, as 64 tokens of each row.
             const __half2 h0 = __floats2half2_rn(e[0][0], e[0][1]), h1 = __floats2half2_rn(e[1][0], e[1][1]);
             const int row = 8 * r + (lane & 7), u = (2 * warp + ((lane >> 3) & 1)) ^ (lane & 7);
             asm volatile("stmatrix.sync.aligned.m8n8.x2.trans.shared.b16 [%0], {%1, %2};" ::"r"(pbase + row * 128 + u * 16),
@@ -639,7 +639,9 @@ cudaError_t launch_split(const AttendProblem &p) {
     const int ctas = (int)min(bound, min(fit, (long long)kMaxSplitCtas));
     // Few items: the merge goes by item, with a CTA for each piece of its rows.  Otherwise by the CTAs that items cross, one CTA
     // for 8 rows.  Measured for 16 heads over 2 of d = 256, us by item / by CTA: 2 items of 5 units 8.8 / 10.1, of 64 units 9.5 / 24,
-    // of 2048 35 / 88, 16 items of 128 units 23 / 29, 32 items 35 / 37, 96 items of 64 54 / 45, 200 items of 32 68 / 46.
+    // of 2048 35 / 88, 16 items of 128 units 23 / 29, 32 items 35 / 37, 48 of 64 31.6 / 30.5, 64 of 64 38.5 / 35.5, 96 of 64 54 / 45,
+    // 200 items of 32 68 / 46; of d = 128, 32 items of 64 units 14.6 / 16.5, 48 19.1 / 20.8, 64 21.1 / 22.5, 96 28.7 / 28.9, 192 46.6 /
+    // 43.6; of d = 64, 48 items of 64 units 16.5 / 18.2, 64 20.6 / 22.5, 96 26.4 / 25.8: at 48 no head size loses more than 4 %.
     plan.meta_by_item = items <= 48;
     plan.meta = static_cast<MergeMeta *>(p.workspace);
     plan.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(p.workspace) + kMetaBytes);

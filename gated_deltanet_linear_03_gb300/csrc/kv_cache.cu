@@ -9,7 +9,9 @@
 // rows are read once, the maximum is a CTA reduction, and codes leave as 8-byte pieces of full lines.  The
 // queries' rotation, most of the bytes with grouped heads, runs in the same launch on further CTAs.
 // Bound by memory: T (hq + 2 hkv) d 2-byte reads, T hq d 2-byte and 2 T hkv d 1-byte writes.  16384 tokens of 16 heads over
-// 2 of d = 256, read back as well: 68 us, 0.81 of a copy's rate; one token takes 5.4 us, a launch and three dependent latencies.
+// 2 of d = 256 56 us, 0.85 of a copy's rate (of 32 heads over 8 of d = 128 72 us, 0.77); one token 3.1 us, a launch and three
+// dependent latencies, 61 sequences' tokens 4.6 us, where the search for a token's sequence adds six.
+// Read: codes and scales in, values out, one pass.  16384 tokens of 2 heads of d = 256 12.7 us, 0.58 of a copy's rate.
 #include "kv_cache.cuh"
 
 namespace gdn {
@@ -147,8 +149,11 @@ __device__ __forceinline__ void rotate_queries(const AppendProblem &p, int warp,
 // ceil((past % 16 + new) / 16) <= floor(new / 16) + 2 of them without a scan over the sequences.
 __host__ __device__ inline long block_slots(int n_seqs, int total) { return total / kKvBlock + 2L * n_seqs; }
 
-// 1280 threads an SM: with four passes a query warp fits their 51 registers.  16384 tokens, us for (passes, threads): (4, 1280) 70,
-// (4, 768) 79, (4, 1536) 73, (8, 768) 73, (8, 1024) 72, (8, 1280) 81, (2, 2048) 82, (16, 768) 82.
+// 1280 threads an SM, 48 registers each.  16384 tokens with the read-back, us for (passes, threads):
+//   16 heads over 2 of d = 256   (4, 1280) 68.5, (4, 768) 78, (4, 1536) 71.7, (8, 768) 72.3, (8, 1024) 70.0, (8, 1280) 80, (2, 1280) 75
+//   32 heads over 8 of d = 128   (4, 1280) 93.8, (4, 768) 99, (4, 1536) 95.2, (8, 768) 96.4, (8, 1024) 94.9, (8, 1280) 103, (2, 1280) 101
+//   16 heads over 4 of d = 64    (4, 1280) 27.2, (4, 768) 29, (4, 1536) 29.6, (8, 768) 29.0, (8, 1024) 28.6, (8, 1280) 34, (2, 1280) 29
+// and within 4 % of one another for single tokens of 61 sequences, but (2, 2048) 7 % slower.
 template <int D, int FMT>
 __global__ void __launch_bounds__(D, 1280 / D) kv_append_kernel(const __grid_constant__ AppendProblem p) {
     constexpr int PIECES = D / 8, ROWS = D / PIECES;   // 8 rows per pass of the CTA, two passes

@@ -389,7 +389,9 @@ GDN_API gdn_status gdn_prefill_host(int n_seqs, int total_tokens, int hk, int hv
  */
 typedef enum {
     GDN_KV_INT8 = 0,   /* two's complement, codes -127 .. 127 */
-    GDN_KV_E4M3 = 1    /* 8-bit floats: 4 exponent bits, 3 mantissa bits, largest 448 */
+    GDN_KV_E4M3 = 1    /* 8-bit floats: 4 exponent bits, 3 mantissa bits, largest 448.  Codes 0x7f and 0xff (NaN) are
+                          not used: what is not finite stands in its block's scale.  In a block that any query
+                          of a call sees they may spoil queries that do not see their token. */
 } gdn_kv_format;
 
 #define GDN_KV_BLOCK 16
@@ -466,8 +468,10 @@ GDN_API gdn_status gdn_kv_read(int n_seqs, int total_tokens, int hkv, int d, con
  *   out            [T, hq, d], dtype out_dtype
  *   workspace      at least gdn_attend_workspace_size() bytes, 256-byte aligned; contents do not matter
  *
- * Products and sums are accumulated in fp32, codes enter them exactly; queries are rounded to fp16 after an
- * exact scaling by a power of two per row, softmax weights to fp16.
+ * Products and sums are accumulated in fp32, codes enter them exactly.  Two roundings are coarser, with fp32 outputs
+ * too: queries are rounded to fp16 after an exact scaling by a power of two per row (components below 2^-14 of the
+ * row's largest lose bits), and softmax weights to fp16 (an error of 2^-11 of the weight, or of 2^-25 of the row's
+ * largest where that is more).
  */
 GDN_API size_t gdn_attend_workspace_size(int n_seqs, int total_tokens, int hq, int hkv, int d, int max_q_len,
                                          int max_kv_len, gdn_status *status);
