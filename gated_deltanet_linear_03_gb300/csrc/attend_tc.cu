@@ -22,8 +22,9 @@
 // loaders and read NQ times by the MMAs.
 //
 // Floor: the tensor pipe, 4 D FLOP a row and token (1024 cycles a unit at d = 256).  Measured at d = 256, 16 heads over 2:
-// 8192-token prompt 441 us, 0.66 of a library product's rate; 509 tokens behind 16384 119 us, 0.60; d = 128: 8192 tokens of
-// 16 heads over 2 252 us, 0.58, ragged prompts of 100 to 5000 tokens of 32 over 8 207 us, 0.45.  What bounds a unit is the way
+// 8192-token prompt 439 us, 0.66 of a library product's rate; 509 tokens behind 16384 119 us, 0.60; d = 128: 8192 tokens of
+// 16 heads over 2 254 us, 0.57, ragged prompts of 100 to 5000 tokens of 32 over 8 207 us, 0.44; of d = 64 171 us, 0.27 (its
+// exponentials are as many as at d = 128, its products half).  What bounds a unit is the way
 // of its scores from product to product (commit, TMEM to registers, weights, back, commit) with two score buffers a tile, which is
 // all that TMEM holds; the softmax and loader warps issue in more than half of the cycles and share them with that way, and the
 // tiles' writes and the products' reads together take most of shared memory's bandwidth.  An item's ends (queries in, pipeline
