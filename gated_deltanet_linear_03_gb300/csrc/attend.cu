@@ -19,7 +19,7 @@
 // fills it.  The warps exchange maxima and weights through shared memory; warp w then accumulates columns
 // [w D/4, (w + 1) D/4) of O^T = V^T W^T over all 64 tokens, D/16 registers a thread and 8 rows.
 // Bound by memory: the codes are read once for all heads of a group.  128 K tokens of 2 heads of d = 256, 134 MB: 30 us, and
-// 4 for the merge, 0.59 of a copy's rate together; 64 sequences of 256 to 8192 tokens
+// 4 for the merge, 0.58 of a copy's rate together; 64 sequences of 256 to 8192 tokens
 // and 8 heads of d = 128, 300 MB: 63 us, 0.70.  The kernel's own
 // DRAM rate is 0.58 to 0.65 of the peak, issue slots 44 to 57 % busy: what is missing is the start (lengths, table, first codes:
 // three latencies one after another, some 4 us) and the end (CTAs that finish between 22 and 26 us, parts, merge).
