@@ -6,14 +6,15 @@ batch decode step, behind the C ABI in include/gdn.h.
     out = gdn.decode_step(state, q, k, v, log_alpha, beta)
 
 and what the layers around it need: an 8-bit paged key/value cache with attention
-over it (``attn``), and the norms between blocks (``norm``).
+over it (``attn``), the norms between blocks (``norm``), the short convolution and the
+selective state space scan (``ssm``), and projections by weights of 4 bits (``linear``).
 
 The binding (``gdn``) is imported lazily so that ``synth`` (input generators)
 can be used without loading the CUDA library.
 """
 import importlib
 
-__all__ = ["attn", "gdn", "norm", "synth"]
+__all__ = ["attn", "gdn", "linear", "norm", "ssm", "synth"]
 
 
 def __getattr__(name):

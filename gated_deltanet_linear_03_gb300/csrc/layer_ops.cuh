@@ -1,0 +1,75 @@
+// What the kernels around the recurrence share: the sequences' conventions (include/gdn.h) and the problems that the
+// entry points pass to the launchers.
+#pragma once
+
+#include "kv_cache.cuh"
+
+namespace gdn {
+
+// Sequences of one call, and the states that they carry.
+struct Sequences {
+    int n, total;
+    const int32_t *cu;          // null: one token each
+    const int32_t *slots;       // null: slot n
+    int n_slots;
+    unsigned int *err;
+    __device__ __forceinline__ int of(int t) const { return cu ? sequence_of(cu, n, t) : t; }
+    __device__ __forceinline__ int begin(int i) const { return cu ? min(max(cu[i], 0), total) : i; }
+    __device__ __forceinline__ int end(int i) const { return cu ? min(max(cu[i + 1], 0), total) : i + 1; }
+    // the slot of sequence i, or -1 where there is none
+    __device__ __forceinline__ int slot(int i) const {
+        const int s = slots ? slots[i] : i;
+        return (unsigned)s < (unsigned)n_slots ? s : -1;
+    }
+};
+
+struct ConvProblem {
+    Sequences seqs;
+    int channels, width;
+    const __nv_bfloat16 *x;
+    long long x_stride;
+    const float *weight, *bias;
+    int silu;
+    const __nv_bfloat16 *state_in;
+    __nv_bfloat16 *state_out;
+    __nv_bfloat16 *out;
+    cudaStream_t stream;
+};
+cudaError_t launch_short_conv(const ConvProblem &p);
+
+struct ScanProblem {
+    Sequences seqs;
+    int channels, n_state, groups, max_len;
+    const __nv_bfloat16 *x, *dt, *z, *b, *c;
+    long long x_stride, dt_stride, z_stride, b_stride, c_stride;
+    const float *a, *skip, *dt_bias;
+    int softplus;
+    const float *state_in;
+    float *state_out;
+    void *out;
+    int out_f32;
+    void *workspace;
+    cudaStream_t stream;
+};
+cudaError_t launch_ssm_scan(const ScanProblem &p);
+size_t ssm_scan_workspace_bytes(int n_seqs, int total, int channels, int n_state, int groups, int max_len);
+
+// A matrix in 4 bits.
+struct Q4Matrix {
+    const uint8_t *codes;
+    const __nv_bfloat16 *scales, *offsets;
+};
+
+struct Q4Problem {
+    int rows, n_out, k, group;
+    const __nv_bfloat16 *x;
+    long long x_stride;
+    Q4Matrix w, up;             // up: of the gated form only
+    int gated, gelu;
+    void *out;
+    int out_f32;
+    cudaStream_t stream;
+};
+cudaError_t launch_q4(const Q4Problem &p);
+
+}  // namespace gdn

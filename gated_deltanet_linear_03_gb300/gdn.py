@@ -26,7 +26,8 @@ EXPORTS = ("gdn_prefill", "gdn_prefill_chunked_phase", "gdn_prefill_workspace_si
            "gdn_device_error", "gdn_status_string", "gdn_version", "gdn_prefill_noalloc", "gdn_prefill_algo",
            "gdn_prefill_host", "gdn_prefill_host_staging_size", "gdn_selftest_bounded_wait",
            "gdn_prefill_pass_plan", "gdn_kv_append", "gdn_kv_read", "gdn_attend", "gdn_attend_workspace_size",
-           "gdn_block_norm")
+           "gdn_block_norm", "gdn_short_conv", "gdn_ssm_scan", "gdn_ssm_scan_workspace_size", "gdn_q4_linear",
+           "gdn_q4_gated")
 NOALLOC_SCRATCH_BYTES = 97 * 1024 * 1024
 PHASE = {"prep": 1, "pass": 2}
 
@@ -98,6 +99,16 @@ def bind(path: str) -> ctypes.CDLL:
     lib.gdn_attend.restype = I
     lib.gdn_block_norm.argtypes = [I, I, P, P, I, P, I, P, P, P, F, F, P, P, P]
     lib.gdn_block_norm.restype = I
+    lib.gdn_short_conv.argtypes = [I, I, I, I, P, L, P, P, I, P, P, P, P, I, P, P]
+    lib.gdn_short_conv.restype = I
+    lib.gdn_ssm_scan_workspace_size.argtypes = [I, I, I, I, I, I, ctypes.POINTER(I)]
+    lib.gdn_ssm_scan_workspace_size.restype = Z
+    lib.gdn_ssm_scan.argtypes = [I, I, I, I, I, P, L, P, L, P, P, L, P, L, P, P, L, P, I, P, I, P, P, P, I, P, I, P, Z, P]
+    lib.gdn_ssm_scan.restype = I
+    lib.gdn_q4_linear.argtypes = [I, I, I, I, P, L, P, P, P, P, I, P]
+    lib.gdn_q4_linear.restype = I
+    lib.gdn_q4_gated.argtypes = [I, I, I, I, P, L, P, P, P, P, P, P, I, P, I, P]
+    lib.gdn_q4_gated.restype = I
     return lib
 
 

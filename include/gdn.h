@@ -509,6 +509,117 @@ GDN_API gdn_status gdn_block_norm(int rows, int dim, const void *x, const void *
                                   const float *pre_weight, const float *scale_weight, float scale, float eps,
                                   void *residual_out, void *out, void *stream);
 
+/*
+ * What a token meets besides the recurrence, attention and the norms: the short convolution in front of a linear
+ * recurrence, the selective state space scan (the other recurrent layer that hybrid models interleave with
+ * attention), and projections by weights of 4 bits (the checkpoint of "Optimizing on-device inference for Apple
+ * Silicon" is of this kind: groups of 64 inputs share a bf16 scale and offset).
+ *
+ * Conventions of the calls on sequences (gdn_short_conv, gdn_ssm_scan):
+ *   cu_seqlens          int32 [n_seqs + 1] on the device, not decreasing: sequence n's tokens are [cu[n], cu[n + 1]);
+ *                       outputs of tokens that no sequence holds are left as they were.  NULL: every sequence has
+ *                       one token, and total_tokens is n_seqs.
+ *   state_in, state_out [n_slots, ...]: what each sequence carries from call to call; sequence n uses slot slots[n]
+ *                       (int32 [n_seqs] on the device, all different), or slot n when slots is NULL.  state_in NULL:
+ *                       all sequences begin.  state_out NULL: nothing is kept.  state_out may be state_in (any other
+ *                       overlap is an error).  A sequence without tokens keeps its state.  A slot outside
+ *                       [0, n_slots) records GDN_ERR_INTERNAL and its sequence is left out: none of its outputs is
+ *                       written.
+ */
+
+/*
+ * gdn_short_conv: causal convolution of each channel with a few taps, and its activation.
+ *     y[t, c] = act(bias[c] + sum_j weight[c, j] x[t - (width - 1) + j, c]),  j = 0 .. width - 1
+ * where rows before a sequence's first token come from its state: its last width - 1 inputs, oldest first.  A prompt
+ * may be fed in pieces: the results are those of one call.
+ *
+ *   channels, width    channels a multiple of 8; width 2, 3 or 4
+ *   x                  bf16 [T, channels], tokens x_stride elements apart (a multiple of 8, at least channels)
+ *   weight, bias       fp32 [channels, width] and [channels]; bias may be NULL
+ *   act                GDN_CONV_NONE or GDN_CONV_SILU (y / (1 + e^-y))
+ *   state_in/out       bf16 [n_slots, width - 1, channels]
+ *   out                bf16 [T, channels], contiguous; overlaps no input.  Sums are formed in fp32 and rounded once.
+ */
+typedef enum {
+    GDN_CONV_NONE = 0,
+    GDN_CONV_SILU = 1
+} gdn_conv_act;
+
+GDN_API gdn_status gdn_short_conv(int n_seqs, int total_tokens, int channels, int width, const void *x,
+                                  long long x_stride, const float *weight, const float *bias, int act,
+                                  const int32_t *cu_seqlens, const void *state_in, void *state_out,
+                                  const int32_t *slots, int n_slots, void *out, void *stream);
+
+/*
+ * gdn_ssm_scan: the selective state space scan.  Per channel c, with n_state numbers h and step width D,
+ *     D = dt[t, c] + dt_bias[c],  D = log(1 + e^D) when dt_softplus
+ *     h[n] = exp(D a[c, n]) h[n] + D x[t, c] B[t, n]
+ *     y[t, c] = (sum_n h[n] C[t, n] + skip[c] x[t, c]) * z / (1 + e^-z)      (the last factor with a gate z[t, c])
+ * channel c reads row c / (channels / groups) of B and C.
+ *
+ *   channels, n_state, groups   channels a multiple of 8 * groups; n_state 16, 32, 64 or 128
+ *   x, dt, z           bf16 [T, channels], tokens x_stride, dt_stride, z_stride elements apart (multiples of 8, at
+ *                      least channels); z may be NULL
+ *   b, c               bf16 [T, groups, n_state], tokens b_stride, c_stride elements apart (multiples of 8, at least
+ *                      groups * n_state)
+ *   a                  fp32 [channels, n_state], usually negative
+ *   dt_bias, skip      fp32 [channels], may be NULL
+ *   dt_softplus        1 or 0
+ *   state_in/out       fp32 [n_slots, channels, n_state]
+ *   max_len            the longest sequence's tokens as far as the host knows (0: not known).  Together with the
+ *                      other sizes it chooses between a scan in one piece and one in pieces that are joined; the
+ *                      results differ by roundings only, whatever it says.
+ *   out                [T, channels], dtype out_dtype
+ *   workspace          at least gdn_ssm_scan_workspace_size() bytes for the same sizes, 256-byte aligned; contents do
+ *                      not matter
+ *
+ * States, step widths, decays and sums are fp32; out is rounded once.
+ */
+GDN_API size_t gdn_ssm_scan_workspace_size(int n_seqs, int total_tokens, int channels, int n_state, int groups,
+                                           int max_len, gdn_status *status);
+
+GDN_API gdn_status gdn_ssm_scan(int n_seqs, int total_tokens, int channels, int n_state, int groups,
+                                const void *x, long long x_stride, const void *dt, long long dt_stride,
+                                const float *a, const void *b, long long b_stride, const void *c, long long c_stride,
+                                const float *skip, const void *z, long long z_stride, const float *dt_bias,
+                                int dt_softplus, const int32_t *cu_seqlens, int max_len, const float *state_in,
+                                float *state_out, const int32_t *slots, int n_slots, void *out, int out_dtype,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * gdn_q4_linear: y = x W^T for a matrix W [n_out, k] held in 4 bits.
+ *     W[n, i] = scales[n, i / group] * code[n, i] + offsets[n, i / group]      (code - 8 times scale without offsets)
+ *
+ *   rows, n_out, k     k a multiple of group, at most 65536; rows and n_out as they come
+ *   group              64 or 128
+ *   x                  bf16 [rows, k], rows x_stride elements apart (a multiple of 8, at least k)
+ *   codes              [n_out, k / 2] bytes, inputs 2i and 2i + 1 in the low and the high half of byte i, 0 .. 15
+ *   scales, offsets    bf16 [n_out, k / group]; offsets may be NULL
+ *   out                [rows, n_out], dtype out_dtype
+ *
+ * Codes enter the products exactly; products and sums are fp32, scaled group by group; out is rounded once.  A row of x
+ * with an infinity or NaN gives outputs that are not finite.
+ */
+GDN_API gdn_status gdn_q4_linear(int rows, int n_out, int k, int group, const void *x, long long x_stride,
+                                 const void *codes, const void *scales, const void *offsets, void *out, int out_dtype,
+                                 void *stream);
+
+/*
+ * gdn_q4_gated: the first half of a gated feed-forward block, y = act(x Wg^T) * (x Wu^T), both matrices [n_out, k] in
+ * the layout of gdn_q4_linear (offsets of both or of neither).  Both products, the activation and their product are
+ * one kernel; everything up to the one rounding of out (bf16 or fp32 [rows, n_out]) is fp32.
+ *   act                GDN_FFN_SILU (u / (1 + e^-u)) or GDN_FFN_GELU (u/2 (1 + tanh(sqrt(2/pi) (u + 0.044715 u^3))))
+ */
+typedef enum {
+    GDN_FFN_SILU = 0,
+    GDN_FFN_GELU = 1
+} gdn_ffn_act;
+
+GDN_API gdn_status gdn_q4_gated(int rows, int n_out, int k, int group, const void *x, long long x_stride,
+                                const void *gate_codes, const void *gate_scales, const void *gate_offsets,
+                                const void *up_codes, const void *up_scales, const void *up_offsets, int act,
+                                void *out, int out_dtype, void *stream);
+
 /* Static, human-readable name of a status code. */
 GDN_API const char *gdn_status_string(gdn_status status);
 
