@@ -86,179 +86,405 @@ __global__ void __launch_bounds__(kScanThreads) step_kernel(const __grid_constan
 }
 
 // ---------------------------------------------------------------------------------------------- prompts
+// Pairs of fp32 numbers in one 64-bit register: a product or fused product-sum of both is one instruction.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float x, float y) {
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void halves(Pair p, float &x, float &y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p)); }
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+struct alignas(16) Pair2 { Pair x, y; };
+
+constexpr int kTile = 32;                   // tokens of one turn
+constexpr int kPromptThreads = 256;         // 4 warps that scan, 4 that prepare the next tile and finish the last one
+constexpr int kMaxPiece = 2048;             // tokens of a piece of a scan in pieces
+
 template <int N_, int S_>
 struct Shape {
-    static constexpr int N = N_, S = S_, LANES = N / S, CH = kScanThreads / LANES, CHUNKS = CH / 8;
-    static constexpr int TT = kScanThreads / CHUNKS < 32 ? kScanThreads / CHUNKS : 32;   // tokens of a tile
-    static constexpr int PARTS = LANES < 4 ? LANES : 4;             // partial sums of y that go through shared memory
-    static constexpr int Y_PIECE = 8 * PARTS + 4;                   // floats of 8 channels' partial sums, and 4 against bank conflicts
+    static constexpr int N = N_, S = S_, LANES = N / S, V = 32 / LANES, CH = 4 * V;     // V: channels of a warp
     struct Tile {
-        float2 du[TT][CH];             // step width (times log2 e) and step width times x
-        float b[TT][N], c[TT][N];
-        float y[TT * CHUNKS][Y_PIECE];
+        float4 du[kTile][CH];               // step width D (times log2 e) twice, and D x twice
+        float b[kTile][N], c[kTile][N];
+        float y[4 * kTile][36];             // by token and warp: the lanes' parts of y; 4 floats of padding against bank conflicts
     };
 };
 
-// What a thread reads of one tile: one token's 8 channels, and its share of the vectors.
+// V bf16 values, as they lie in memory.
+template <int V> struct Bits { using T = uint4; };
+template <> struct Bits<4> { using T = uint2; };
+template <> struct Bits<2> { using T = uint32_t; };
+template <int V>
+__device__ __forceinline__ void unpack(const typename Bits<V>::T &u, float (&x)[V]) {
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(&u);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+        x[2 * i] = bf16_lo(w[i]);
+        x[2 * i + 1] = bf16_hi(w[i]);
+    }
+}
+
+// What a preparing thread reads of one tile: V channels of one token, and its share of the vectors.
 template <class SH>
 struct Raw {
-    static constexpr int VECTORS = (2 * SH::TT * SH::N / 8 + kScanThreads - 1) / kScanThreads;
-    uint4 x, dt, z, bc[VECTORS];
-    __device__ __forceinline__ void load(const ScanProblem &p, int t0, int t1, int c0, int c1, int group, bool with_y) {
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        const int t = t0 + threadIdx.x / SH::CHUNKS, c = c0 + 8 * (threadIdx.x % SH::CHUNKS);
-        const bool ok = threadIdx.x < SH::TT * SH::CHUNKS && t < t1 && c < c1;
-        x = ok ? *reinterpret_cast<const uint4 *>(p.x + t * p.x_stride + c) : zero;
-        dt = ok ? *reinterpret_cast<const uint4 *>(p.dt + t * p.dt_stride + c) : zero;
-        z = ok && with_y && p.z ? *reinterpret_cast<const uint4 *>(p.z + t * p.z_stride + c) : zero;
+    using T = typename Bits<SH::V>::T;
+    static constexpr int PIECES = kTile * SH::N / 8, VECTORS = 2 * PIECES / 128;
+    T x, dt, z;
+    uint4 bc[VECTORS];
+    template <bool WITH_Y>
+    __device__ __forceinline__ void load(const ScanProblem &p, int id, int t0, int t1, int c, bool live, int group) {
+        const int t = t0 + id / 4;
+        const bool ok = live && t < t1;
+        x = dt = z = T{};
+        if (ok) {
+            x = *reinterpret_cast<const T *>(p.x + t * p.x_stride + c);
+            dt = *reinterpret_cast<const T *>(p.dt + t * p.dt_stride + c);
+            if (WITH_Y && p.z) z = *reinterpret_cast<const T *>(p.z + t * p.z_stride + c);
+        }
 #pragma unroll
         for (int i = 0; i < VECTORS; ++i) {
-            const int k = threadIdx.x + i * kScanThreads, which = k / (SH::TT * SH::N / 8), at = k % (SH::TT * SH::N / 8);
+            const int k = id + i * 128, which = k / PIECES, at = k % PIECES;
             const int tb = t0 + at / (SH::N / 8), e = group * SH::N + at % (SH::N / 8) * 8;
-            bc[i] = zero;
-            if (which < 2 && tb < t1) bc[i] = *reinterpret_cast<const uint4 *>(which ? p.c + tb * p.c_stride + e : p.b + tb * p.b_stride + e);
+            bc[i] = make_uint4(0, 0, 0, 0);
+            if (tb < t1 && (WITH_Y || which == 0))
+                bc[i] = *reinterpret_cast<const uint4 *>(which ? p.c + tb * p.c_stride + e : p.b + tb * p.b_stride + e);
         }
     }
 };
 
-__device__ __forceinline__ float channel_value(const float *p, int c, int channels) { return p && c < channels ? __ldg(p + c) : 0.f; }
+// All of the CTA's warps meet here, those that scan and those that prepare, from different places.
+__device__ __forceinline__ void turn() { asm volatile("barrier.sync 1, %0;" ::"n"(kPromptThreads) : "memory"); }
 
-// Tokens [t0, t1) of one sequence for the CTA's channels, from c0 and below c1; h is this lane's part of its channel's state.
+// Tokens [t0, t1) of one sequence for the CTA's channels c0 .. and below c1.  h: a scanning lane's part of its channel's
+// state; *width_sum: the sum of its step widths (times log2 e).
 template <class SH, bool WITH_Y>
-__device__ __forceinline__ void scan_tokens(const ScanProblem &p, typename SH::Tile &s, int t0, int t1, int c0, int c1, int group,
-                                            const float (&a)[SH::S], float (&h)[SH::S], float *width_sum) {
-    constexpr int S = SH::S, TT = SH::TT, N = SH::N;
-    const int chan = threadIdx.x / SH::LANES, part = threadIdx.x % SH::LANES;
-    const int mt = threadIdx.x / SH::CHUNKS, mc = threadIdx.x % SH::CHUNKS;
-    const bool mine = threadIdx.x < TT * SH::CHUNKS;
-    Raw<SH> raw;
-    raw.load(p, t0, t1, c0, c1, group, WITH_Y);
-    float total = 0.f;
-    for (int at = t0; at < t1; at += TT) {
-        const Raw<SH> cur = raw;
-        if (mine) {
-            float x[8], d[8];
-            unpack8(cur.x, x);
-            unpack8(cur.dt, d);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = c0 + 8 * mc + e;
-                const float w = at + mt < t1 ? step_width(d[e] + channel_value(p.dt_bias, c, c1), p.softplus) : 0.f;
-                s.du[mt][8 * mc + e] = make_float2(w * kLog2e, w * x[e]);      // (a row beyond the end changes nothing)
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < Raw<SH>::VECTORS; ++i) {
-            const int k = threadIdx.x + i * kScanThreads, which = k / (TT * N / 8), v = k % (TT * N / 8);
-            if (which >= 2) continue;
-            float f[8];
-            unpack8(cur.bc[i], f);
-            float4 *to = reinterpret_cast<float4 *>((which ? s.c[0] : s.b[0]) + 8 * v);
-            to[0] = make_float4(f[0], f[1], f[2], f[3]);
-            to[1] = make_float4(f[4], f[5], f[6], f[7]);
-        }
-        __syncthreads();
-        if (at + TT < t1) raw.load(p, at + TT, t1, c0, c1, group, WITH_Y);
+__device__ __forceinline__ void scan_tokens(const ScanProblem &p, typename SH::Tile *tiles, int t0, int t1, int c0, int c1, int group,
+                                            const Pair (&a)[SH::S / 2], Pair (&h)[SH::S / 2], float *width_sum) {
+    constexpr int S = SH::S, N = SH::N, V = SH::V, LANES = SH::LANES;
+    const int n = (t1 - t0 + kTile - 1) / kTile;
+    if (n <= 0) return;
+    if (threadIdx.x < 128) {
+        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, part = lane % LANES, chan = warp * V + lane / LANES;
+        float total = 0.f;
+        turn();
+        for (int i = 0; i < n; ++i) {
+            typename SH::Tile &s = tiles[i & 1];
+            const float4 *du = &s.du[0][chan];
+            const float *b = &s.b[0][S * part], *c = &s.c[0][S * part];
+            float *y = &s.y[warp][lane];
 #pragma unroll 8
-        for (int t = 0; t < TT; ++t) {
-            const float2 du = s.du[t][chan];
-            float b[S], c[S];
-            load_state(&s.b[t][S * part], b);
-            if (WITH_Y) load_state(&s.c[t][S * part], c);
-            else total += du.x;
-            float y = 0.f;
+            for (int t = 0; t < kTile; ++t) {
+                const Pair2 w = *reinterpret_cast<const Pair2 *>(du + t * SH::CH);
+                Pair sum = 0;
 #pragma unroll
-            for (int i = 0; i < S; ++i) {
-                h[i] = fmaf(ex2(du.x * a[i]), h[i], du.y * b[i]);
-                if (WITH_Y) y = fmaf(h[i], c[i], y);
-            }
-            if (WITH_Y) {
+                for (int k = 0; k < S / 4; ++k) {
+                    const Pair2 bb = *reinterpret_cast<const Pair2 *>(b + t * N + 4 * k);
+                    Pair2 cc{};
+                    if (WITH_Y) cc = *reinterpret_cast<const Pair2 *>(c + t * N + 4 * k);
 #pragma unroll
-                for (int o = SH::LANES / 2; o >= SH::PARTS; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-                if (part < SH::PARTS) s.y[t * SH::CHUNKS + chan / 8][chan % 8 * SH::PARTS + part] = y;
+                    for (int m = 0; m < 2; ++m) {
+                        float e0, e1;
+                        halves(mul2(w.x, a[2 * k + m]), e0, e1);
+                        h[2 * k + m] = fma2(pair(ex2(e0), ex2(e1)), h[2 * k + m], mul2(w.y, m ? bb.y : bb.x));
+                        if (WITH_Y) sum = k + m ? fma2(h[2 * k + m], m ? cc.y : cc.x, sum) : mul2(h[0], cc.x);
+                    }
+                }
+                if (WITH_Y) {
+                    float lo, hi;
+                    halves(sum, lo, hi);
+                    y[t * 4 * 36] = lo + hi;
+                } else {
+                    float lo, hi;
+                    halves(w.x, lo, hi);
+                    total += lo;
+                }
             }
+            turn();
         }
-        __syncthreads();
-        if (WITH_Y && mine && at + mt < t1 && c0 + 8 * mc < c1) {
-            float x[8], z[8], y[8];
-            unpack8(cur.x, x);
-            unpack8(cur.z, z);
-            const float *from = s.y[threadIdx.x];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                y[e] = 0.f;
-#pragma unroll
-                for (int q = 0; q < SH::PARTS; ++q) y[e] += from[e * SH::PARTS + q];
-                y[e] = fmaf(channel_value(p.skip, c0 + 8 * mc + e, c1), x[e], y[e]);
-                if (p.z) y[e] *= silu(z[e]);
-            }
-            const size_t to = (size_t)(at + mt) * p.channels + c0 + 8 * mc;
-            if (p.out_f32) {
-                float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + to);
-                o[0] = make_float4(y[0], y[1], y[2], y[3]);
-                o[1] = make_float4(y[4], y[5], y[6], y[7]);
-            } else {
-                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + to) = pack8(y);
-            }
-        }
-    }
-    if (!WITH_Y) *width_sum = total;
-}
-
-// One CTA carries a whole sequence for its channels.
-template <class SH>
-__global__ void __launch_bounds__(kScanThreads) scan_kernel(const __grid_constant__ ScanProblem p, int ctas_per_group) {
-    extern __shared__ __align__(16) unsigned char smem[];
-    typename SH::Tile &s = *reinterpret_cast<typename SH::Tile *>(smem);
-    const int per_group = p.channels / p.groups, ctas = ctas_per_group * p.groups;
-    const int n = blockIdx.x / ctas, group = blockIdx.x % ctas / ctas_per_group;
-    const int c0 = group * per_group + blockIdx.x % ctas_per_group * SH::CH;
-    const int slot = p.seqs.slot(n);
-    if (slot < 0) {
-        if (threadIdx.x == 0) raise_error(p.seqs.err, kErrInternal);
+        if (!WITH_Y) *width_sum = total;
         return;
     }
-    const int c1 = (group + 1) * per_group, c = c0 + threadIdx.x / SH::LANES, part = threadIdx.x % SH::LANES;
+    const int id = threadIdx.x - 128, c = c0 + V * (id % 4);
     const bool live = c < c1;
-    const size_t at = ((size_t)slot * p.channels + c) * SH::N + SH::S * part;
-    float h[SH::S], a[SH::S];
+    float bias[V], skip[V];
 #pragma unroll
-    for (int i = 0; i < SH::S; ++i) h[i] = a[i] = 0.f;
-    if (live) {
-        if (p.state_in) load_state(p.state_in + at, h);
-        load_state(p.a + (size_t)c * SH::N + SH::S * part, a);
+    for (int e = 0; e < V; ++e) {
+        bias[e] = live && p.dt_bias ? __ldg(p.dt_bias + c + e) : 0.f;
+        skip[e] = live && WITH_Y && p.skip ? __ldg(p.skip + c + e) : 0.f;
     }
-    float unused;
-    scan_tokens<SH, true>(p, s, p.seqs.begin(n), p.seqs.end(n), c0, c1, group, a, h, &unused);
-    if (live && p.state_out) store_state(p.state_out + at, h);
+    Raw<SH> raw;
+    typename Raw<SH>::T x1{}, z1{}, x0{}, z0{};            // of the tile that is scanned, and of the one before it
+    auto prepare = [&](int i) {
+        typename SH::Tile &s = tiles[i & 1];
+        float x[V], d[V];
+        unpack<V>(raw.x, x);
+        unpack<V>(raw.dt, d);
+        const bool inside = t0 + i * kTile + id / 4 < t1;
+        float4 *to = &s.du[id / 4][V * (id % 4)];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float w = inside ? step_width(d[e] + bias[e], p.softplus) : 0.f;        // (a row beyond the end changes nothing)
+            to[e] = make_float4(w * kLog2e, w * kLog2e, w * x[e], w * x[e]);
+        }
+#pragma unroll
+        for (int k = 0; k < Raw<SH>::VECTORS; ++k) {
+            const int at = id + k * 128, which = at / Raw<SH>::PIECES, v = at % Raw<SH>::PIECES;
+            float f[8];
+            unpack8(raw.bc[k], f);
+            float4 *bc = reinterpret_cast<float4 *>((which ? s.c[0] : s.b[0]) + 8 * v);
+            bc[0] = make_float4(f[0], f[1], f[2], f[3]);
+            bc[1] = make_float4(f[4], f[5], f[6], f[7]);
+        }
+        x0 = x1, z0 = z1, x1 = raw.x, z1 = raw.z;
+        if (i + 1 < n) raw.template load<WITH_Y>(p, id, t0 + (i + 1) * kTile, t1, c, live, group);
+    };
+    auto finish = [&](int i, const typename Raw<SH>::T &xr, const typename Raw<SH>::T &zr) {
+        const int t = t0 + i * kTile + id / 4;
+        if (!WITH_Y || !live || t >= t1) return;
+        float x[V], z[V], y[V];
+        unpack<V>(xr, x);
+        unpack<V>(zr, z);
+        const float *from = tiles[i & 1].y[id];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            float q[LANES];
+#pragma unroll
+            for (int k = 0; k < LANES / 4; ++k) {
+                const float4 f = *reinterpret_cast<const float4 *>(from + e * LANES + 4 * k);
+                q[4 * k] = f.x; q[4 * k + 1] = f.y; q[4 * k + 2] = f.z; q[4 * k + 3] = f.w;
+            }
+#pragma unroll
+            for (int o = LANES / 2; o >= 1; o >>= 1)
+#pragma unroll
+                for (int k = 0; k < o; ++k) q[k] += q[k + o];
+            y[e] = fmaf(skip[e], x[e], q[0]);
+            if (p.z) y[e] *= silu(z[e]);
+        }
+        const size_t to = (size_t)t * p.channels + c;
+        if (p.out_f32) {
+            float2 *o = reinterpret_cast<float2 *>(static_cast<float *>(p.out) + to);
+#pragma unroll
+            for (int k = 0; k < V / 2; ++k) o[k] = make_float2(y[2 * k], y[2 * k + 1]);
+        } else {
+            typename Raw<SH>::T o;
+            uint32_t *w = reinterpret_cast<uint32_t *>(&o);
+#pragma unroll
+            for (int k = 0; k < V / 2; ++k) w[k] = pack2(y[2 * k], y[2 * k + 1]);
+            *reinterpret_cast<typename Raw<SH>::T *>(static_cast<__nv_bfloat16 *>(p.out) + to) = o;
+        }
+    };
+    raw.template load<WITH_Y>(p, id, t0, t1, c, live, group);
+    prepare(0);
+    turn();
+    for (int i = 0; i < n; ++i) {
+        // x1, z1 are tile i's; after prepare(i + 1) they are x0, z0
+        const auto xp = x0, zp = z0;
+        if (i + 1 < n) prepare(i + 1);
+        else x0 = x1, z0 = z1;
+        if (i > 0) finish(i - 1, xp, zp);
+        turn();
+    }
+    finish(n - 1, x0, z0);
 }
 
-template <int N, int S>
+// How a call's tokens are divided among CTAs.
+struct ScanPlan {
+    int piece;                  // tokens of a piece; 0: a CTA takes whole sequences
+    int pieces, empty;          // pieces, and further CTAs that look for sequences without tokens
+    int ctas_per_group;
+    float *ends, *widths, *begins;     // [pieces, channels, N], [pieces, channels], [pieces, channels, N]
+};
+constexpr int kEmptyPerCta = 64;
+
+enum Pass { kWhole, kEnds, kOutputs };
+
+template <class SH, int PASS>
+__global__ void __launch_bounds__(kPromptThreads, 2) scan_kernel(const __grid_constant__ ScanProblem p, const __grid_constant__ ScanPlan plan) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    typename SH::Tile *tiles = reinterpret_cast<typename SH::Tile *>(smem);
+    constexpr int N = SH::N, S = SH::S;
+    const int per_group = p.channels / p.groups, ctas = plan.ctas_per_group * p.groups;
+    const int unit = blockIdx.x / ctas, group = blockIdx.x % ctas / plan.ctas_per_group;
+    const int c0 = group * per_group + blockIdx.x % plan.ctas_per_group * SH::CH, c1 = (group + 1) * per_group;
+    // of a scanning lane: its channel and where its states lie in an array [.., channels, N]
+    const int c = c0 + threadIdx.x / SH::LANES, part = threadIdx.x % SH::LANES;
+    const bool live = threadIdx.x < 128 && c < c1;
+    const size_t at = (size_t)c * N + S * part, all = (size_t)p.channels * N;
+    Pair h[S / 2], a[S / 2];
+    auto load = [&](const float *from, Pair (&v)[S / 2]) {
+#pragma unroll
+        for (int k = 0; k < S / 4; ++k) {
+            const Pair2 q = from && live ? *reinterpret_cast<const Pair2 *>(from + at + 4 * k) : Pair2{0, 0};
+            v[2 * k] = q.x;
+            v[2 * k + 1] = q.y;
+        }
+    };
+    auto store = [&](float *to, const Pair (&v)[S / 2]) {
+        if (!live) return;
+#pragma unroll
+        for (int k = 0; k < S / 4; ++k) *reinterpret_cast<Pair2 *>(to + at + 4 * k) = Pair2{v[2 * k], v[2 * k + 1]};
+    };
+    auto state_in = [&](int slot) { return p.state_in ? p.state_in + slot * all : nullptr; };
+    load(p.a, a);
+    float width_sum;
+
+    if (PASS == kWhole) {
+        const int slot = p.seqs.slot(unit);
+        if (slot < 0) {
+            if (threadIdx.x == 0) raise_error(p.seqs.err, kErrInternal);
+            return;
+        }
+        load(state_in(slot), h);
+        scan_tokens<SH, true>(p, tiles, p.seqs.begin(unit), p.seqs.end(unit), c0, c1, group, a, h, &width_sum);
+        if (p.state_out) store(p.state_out + slot * all, h);
+        return;
+    }
+    const int t0 = unit * plan.piece, t1 = min(t0 + plan.piece, p.seqs.total);
+    if (PASS == kEnds) {
+        // the sequence that goes on behind this piece: what its state is at the piece's end, from its state at the piece's
+        // beginning if that is known (or else from zero), and the widths' sum, by which the rest decays until then
+        const int n = p.seqs.of(t1 - 1), b = p.seqs.begin(n), slot = p.seqs.slot(n);
+        if (p.seqs.end(n) <= t1 || b >= t1 || slot < 0) return;
+        load(b >= t0 ? state_in(slot) : nullptr, h);
+        if (b >= t0 && p.state_in) store(plan.begins + unit * all, h);       // (state_out may be state_in, and is written by others)
+        scan_tokens<SH, false>(p, tiles, max(b, t0), t1, c0, c1, group, a, h, &width_sum);
+        store(plan.ends + unit * all, h);
+        if (live && part == 0) plan.widths[(size_t)unit * p.channels + c] = width_sum;
+        return;
+    }
+    if (unit >= plan.pieces) {
+        const int first = (unit - plan.pieces) * kEmptyPerCta;
+        for (int n = first; n < min(first + kEmptyPerCta, p.seqs.n); ++n) {
+            if (p.seqs.end(n) > p.seqs.begin(n)) continue;
+            const int slot = p.seqs.slot(n);
+            if (slot < 0) {
+                if (threadIdx.x == 0) raise_error(p.seqs.err, kErrInternal);
+                continue;
+            }
+            load(state_in(slot), h);
+            store(p.state_out + slot * all, h);
+        }
+        return;
+    }
+    for (int t = t0, n = p.seqs.of(t0); t < t1 && n < p.seqs.n; ++n) {
+        const int b = p.seqs.begin(n), e = p.seqs.end(n), slot = p.seqs.slot(n);
+        if (e <= b || e <= t || b >= t1) {
+            if (b >= t1) break;
+            continue;
+        }
+        if (slot < 0) {
+            if (threadIdx.x == 0) raise_error(p.seqs.err, kErrInternal);
+            continue;
+        }
+        if (b >= t0) {
+            load(e > t1 && p.state_in ? plan.begins + unit * all : state_in(slot), h);
+        } else {
+#pragma unroll
+            for (int k = 0; k < S / 2; ++k) h[k] = 0;
+#pragma unroll 4
+            for (int j = b / plan.piece; j < unit; ++j) {
+                Pair end[S / 2];
+                load(plan.ends + j * all, end);
+                const float w = live ? plan.widths[(size_t)j * p.channels + c] : 0.f;
+#pragma unroll
+                for (int k = 0; k < S / 2; ++k) {
+                    float e0, e1;
+                    halves(mul2(pair(w, w), a[k]), e0, e1);
+                    h[k] = fma2(pair(ex2(e0), ex2(e1)), h[k], end[k]);
+                }
+            }
+        }
+        scan_tokens<SH, true>(p, tiles, max(b, t0), min(e, t1), c0, c1, group, a, h, &width_sum);
+        if (e <= t1 && p.state_out) store(p.state_out + slot * all, h);
+        t = e;
+    }
+}
+
+// S: states of a lane.
+template <int N> struct ShapeOf { using T = Shape<N, N == 128 ? 8 : 4>; };
+
+template <int N>
+ScanPlan plan_scan(int n_seqs, int total, int channels, int groups, int max_len) {
+    using SH = typename ShapeOf<N>::T;
+    ScanPlan s{};
+    s.ctas_per_group = (channels / groups + SH::CH - 1) / SH::CH;
+    const long ctas = (long)s.ctas_per_group * groups, at_once = 2L * multiprocessor_count();
+    const long longest = max_len > 0 && max_len < total ? max_len : total;
+    // Tokens that one CTA walks through, one after another: whole sequences, or pieces twice
+    const long whole = max(longest, (long)total * ctas / at_once);
+    const long halves = 2 * max(64L, (long)total * ctas / at_once);
+    if (whole <= halves * 5 / 4) return s;
+    const long pieces = max(1L, at_once / ctas);
+    long piece = ((total + pieces - 1) / pieces + kTile - 1) / kTile * kTile;
+    piece = min((long)kMaxPiece, max(64L, piece));
+    s.piece = (int)piece;
+    s.pieces = (int)((total + piece - 1) / piece);
+    return s;
+}
+
+template <int N>
 cudaError_t launch(const ScanProblem &p) {
+    using SH = typename ShapeOf<N>::T;
     if (!p.seqs.cu || p.max_len == 1) {
         constexpr int CH = kScanThreads / (N / 4);
         const long ctas = (long)((p.channels + CH - 1) / CH) * p.seqs.n;
         step_kernel<N><<<(unsigned)ctas, kScanThreads, 0, p.stream>>>(p);
         return cudaGetLastError();
     }
-    using SH = Shape<N, S>;
-    const int ctas_per_group = (p.channels / p.groups + SH::CH - 1) / SH::CH;
-    const cudaError_t e = cudaFuncSetAttribute(scan_kernel<SH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(typename SH::Tile));
-    if (e != cudaSuccess) return e;
-    scan_kernel<SH><<<(unsigned)((long)ctas_per_group * p.groups * p.seqs.n), kScanThreads, sizeof(typename SH::Tile), p.stream>>>(p, ctas_per_group);
-    return cudaGetLastError();
+    constexpr int smem = 2 * (int)sizeof(typename SH::Tile);
+    ScanPlan s = plan_scan<N>(p.seqs.n, p.seqs.total, p.channels, p.groups, p.max_len);
+    const long ctas = (long)s.ctas_per_group * p.groups;
+    using Fn = void (*)(const ScanProblem, const ScanPlan);
+    auto run = [&](Fn fn, long units) {
+        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        fn<<<(unsigned)(units * ctas), kPromptThreads, smem, p.stream>>>(p, s);
+        return cudaGetLastError();
+    };
+    if (s.piece == 0) return run(scan_kernel<SH, kWhole>, p.seqs.n);
+    const size_t states = (size_t)s.pieces * p.channels * N;
+    s.ends = static_cast<float *>(p.workspace);
+    s.begins = s.ends + states;
+    s.widths = s.begins + states;
+    if (p.state_out && p.state_out != p.state_in) s.empty = (p.seqs.n + kEmptyPerCta - 1) / kEmptyPerCta;
+    const cudaError_t e = run(scan_kernel<SH, kEnds>, s.pieces);
+    return e != cudaSuccess ? e : run(scan_kernel<SH, kOutputs>, s.pieces + s.empty);
+}
+
+template <int N>
+size_t workspace_bytes(int n_seqs, int total, int channels, int groups, int max_len) {
+    const ScanPlan s = plan_scan<N>(n_seqs, total, channels, groups, max_len);
+    return (size_t)s.pieces * channels * (2 * N + 1) * 4;
 }
 
 }  // namespace
 
-size_t ssm_scan_workspace_bytes(int, int, int, int, int, int) { return 0; }
+size_t ssm_scan_workspace_bytes(int n_seqs, int total, int channels, int n_state, int groups, int max_len) {
+    if (max_len == 1 || total == 0) return 0;
+    switch (n_state) {
+        case 16: return workspace_bytes<16>(n_seqs, total, channels, groups, max_len);
+        case 32: return workspace_bytes<32>(n_seqs, total, channels, groups, max_len);
+        case 64: return workspace_bytes<64>(n_seqs, total, channels, groups, max_len);
+        default: return workspace_bytes<128>(n_seqs, total, channels, groups, max_len);
+    }
+}
 
 cudaError_t launch_ssm_scan(const ScanProblem &p) {
     switch (p.n_state) {
-        case 16: return launch<16, 4>(p);
-        case 32: return launch<32, 4>(p);
-        case 64: return launch<64, 8>(p);
-        default: return launch<128, 16>(p);
+        case 16: return launch<16>(p);
+        case 32: return launch<32>(p);
+        case 64: return launch<64>(p);
+        default: return launch<128>(p);
     }
 }
 

@@ -61,35 +61,39 @@ def values(w: Q4) -> torch.Tensor:
     return ((q - 8) * s if w.offsets is None else q * s + w.offsets.float()[..., None]).flatten(1)
 
 
+# As in :mod:`attn`, the checks are written for the case that nothing is wrong.
 def _matrix(name: str, w: Q4, k: int, index: int):
     """(codes, scales, offsets addresses, n_out, group) of a matrix whose inputs are ``k``."""
     codes, scales, offsets = w
     cp = _contiguous(name + ".codes", codes, _U8, 2, index)
     sp = _contiguous(name + ".scales", scales, _BF16, 2, index)
     n_out, half = codes.shape
-    groups = scales.size(1)
-    if 2 * half != k or scales.size(0) != n_out or groups == 0 or k % groups:
+    rows, groups = shape = scales.shape
+    if 2 * half != k or rows != n_out or groups == 0 or k % groups:
         raise ValueError(f"{name} must have codes [n_out, {k // 2}] and scales [n_out, {k} / group], "
-                         f"got {tuple(codes.shape)} and {tuple(scales.shape)}")
+                         f"got {tuple(codes.shape)} and {tuple(shape)}")
     op = 0
     if offsets is not None:
         op = _contiguous(name + ".offsets", offsets, _BF16, 2, index)
-        if offsets.shape != scales.shape:
+        if offsets.shape != shape:
             raise ValueError(f"{name}.offsets must have the shape of its scales")
     return cp, sp, op, n_out, k // groups
 
 
-def _x_rows(x: torch.Tensor, index: int):
-    """(address, row stride, rows, k) of activations bf16 [..., k]: contiguous, or 2-d with contiguous rows."""
-    if x.dtype is not _BF16 or x.dim() < 1:
+def _rows(x: torch.Tensor, index: int):
+    """(row stride, rows, k) of activations bf16 [..., k]: contiguous, or 2-d with contiguous rows."""
+    shape = x.shape
+    if x.dtype is not _BF16 or not shape:
         _refuse("x", x, _BF16, 2, index)
-    k = x.size(-1)
-    rows = x.numel() // k if k else 0
-    if x.is_contiguous():
-        return x.data_ptr(), k, rows, k
-    if x.dim() != 2 or x.stride(1) != 1:
-        raise ValueError("x must be contiguous, or 2-d with contiguous rows")
-    return x.data_ptr(), x.stride(0) if rows > 1 else k, rows, k
+    k = shape[-1]
+    if len(shape) == 2:
+        if x.is_contiguous():
+            return k, shape[0], k
+        if x.stride(1) == 1:
+            return x.stride(0), shape[0], k
+    elif x.is_contiguous():
+        return k, x.numel() // k if k else 0, k
+    raise ValueError("x must be contiguous, or 2-d with contiguous rows")
 
 
 def _output(x, n_out, out, out_dtype, index, stream):
@@ -98,12 +102,12 @@ def _output(x, n_out, out, out_dtype, index, stream):
         code = DTYPE.get(out_dtype)
         if code is None:
             raise ValueError("out_dtype must be bf16 or fp32")
-        out = _empty(stream, shape, out_dtype, x.device)
-        return out, out.data_ptr(), code
+        return (x.new_empty(shape) if code == 0 and stream is None else _empty(stream, shape, out_dtype, x.device)), code
     code = DTYPE.get(out.dtype)
     if code is None or out.shape != shape:
         raise ValueError(f"out must be {shape}, in bf16 or fp32")
-    return out, _contiguous("out", out, out.dtype, len(shape), index), code
+    _contiguous("out", out, out.dtype, len(shape), index)
+    return out, code
 
 
 def q4_linear(x: torch.Tensor, w: Q4, *, out: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
@@ -111,10 +115,11 @@ def q4_linear(x: torch.Tensor, w: Q4, *, out: Optional[torch.Tensor] = None, out
     """Run ``gdn_q4_linear``: ``x`` (bf16 [..., k]) times the transpose of ``w``: [..., n_out] in bf16 or fp32."""
     lib = load_library()
     dev = _device(x, "x")
-    xp, stride, rows, k = _x_rows(x, dev)
+    stride, rows, k = _rows(x, dev)
     cp, sp, fp, n_out, group = _matrix("w", w, k, dev)
-    out, op, code = _output(x, n_out, out, out_dtype, dev, stream)
-    _launch(lib.gdn_q4_linear, "gdn_q4_linear", dev, stream, _int32(rows), n_out, k, group, xp, stride, cp, sp, fp, op, code)
+    out, code = _output(x, n_out, out, out_dtype, dev, stream)
+    _launch(lib.gdn_q4_linear, "gdn_q4_linear", dev, stream, _int32(rows), n_out, k, group, x.data_ptr(), stride, cp, sp, fp,
+            out.data_ptr(), code)
     return out
 
 
@@ -124,7 +129,7 @@ def q4_gated(x: torch.Tensor, gate: Q4, up: Q4, *, act: str = "silu", out: Optio
     in both or neither); ``act`` is "silu" or "gelu" (its tanh form)."""
     lib = load_library()
     dev = _device(x, "x")
-    xp, stride, rows, k = _x_rows(x, dev)
+    stride, rows, k = _rows(x, dev)
     gc, gs, go, n_out, group = _matrix("gate", gate, k, dev)
     uc, us, uo, n_up, up_group = _matrix("up", up, k, dev)
     if n_up != n_out or up_group != group or (go == 0) != (uo == 0):
@@ -132,7 +137,7 @@ def q4_gated(x: torch.Tensor, gate: Q4, up: Q4, *, act: str = "silu", out: Optio
     act_code = FFN_ACT.get(act)
     if act_code is None:
         raise ValueError(f"act must be one of {sorted(FFN_ACT)}")
-    out, op, code = _output(x, n_out, out, out_dtype, dev, stream)
-    _launch(lib.gdn_q4_gated, "gdn_q4_gated", dev, stream, _int32(rows), n_out, k, group, xp, stride, gc, gs, go, uc, us, uo,
-            act_code, op, code)
+    out, code = _output(x, n_out, out, out_dtype, dev, stream)
+    _launch(lib.gdn_q4_gated, "gdn_q4_gated", dev, stream, _int32(rows), n_out, k, group, x.data_ptr(), stride, gc, gs, go,
+            uc, us, uo, act_code, out.data_ptr(), code)
     return out

@@ -12,7 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
-from typing import Optional, Tuple
+from typing import Optional
 
 import torch
 
@@ -23,54 +23,61 @@ CONV_ACT = {"none": 0, "silu": 1}
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
-def _rows(name: str, t: torch.Tensor, tokens: int, width: int, index: int) -> Tuple[int, int]:
-    """Address and row stride of a bf16 [tokens, width] tensor whose rows are contiguous."""
+# As in :mod:`attn`, the checks are written for the case that nothing is wrong: few attribute look-ups, no calls where a
+# tensor is what it should be.
+def _rows(name: str, t: torch.Tensor, shape, index: int) -> int:
+    """The row stride of a bf16 [tokens, width] tensor whose rows are contiguous; ``shape`` is what it must be."""
     if t.dtype is not _BF16 or t.get_device() != index or t.dim() != 2:
         _refuse(name, t, _BF16, 2, index)
-    if t.shape != (tokens, width):
-        raise ValueError(f"{name} must be [{tokens}, {width}], got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return shape[1]                       # (a single row's stride says nothing)
     stride = t.stride()
-    if stride[1] != 1 and width > 1:
+    if stride[1] != 1:
         raise ValueError(f"{name}: rows must be contiguous")
-    return t.data_ptr(), stride[0] if tokens > 1 else width       # (a single row's stride says nothing)
+    return stride[0]
 
 
-def _sequences(cu_seqlens, tokens, state_in, state_out, slots, entry, dtype, index):
-    """(n_seqs, cu address, state addresses, slots address, n_slots) of a call."""
-    cu = sl = si = so = n_slots = 0
-    if cu_seqlens is None:
-        n = tokens
-    else:
-        cu = _contiguous("cu_seqlens", cu_seqlens, _I32, 1, index)
-        n = cu_seqlens.size(0) - 1
-    ndim = len(entry) + 1
+def _states(state_in, state_out, d0: int, d1: int, dtype, index: int):
+    """(addresses of both, slots) of states [slots, d0, d1]."""
+    si = so = n_slots = 0
     if state_in is not None:
-        si = _contiguous("state_in", state_in, dtype, ndim, index)
-        n_slots = state_in.size(0)
-        if state_in.shape[1:] != entry:
-            raise ValueError(f"state_in must be [slots, {', '.join(map(str, entry))}]")
+        si = _contiguous("state_in", state_in, dtype, 3, index)
+        n_slots, e0, e1 = state_in.shape
+        if e0 != d0 or e1 != d1:
+            raise ValueError(f"state_in must be [slots, {d0}, {d1}], got {tuple(state_in.shape)}")
+        if state_out is state_in:
+            return si, si, n_slots
     if state_out is not None:
-        so = si if state_out is state_in else _contiguous("state_out", state_out, dtype, ndim, index)
-        if state_out.shape[1:] != entry:
-            raise ValueError(f"state_out must be [slots, {', '.join(map(str, entry))}]")
-        if state_in is not None and state_out.size(0) != n_slots:
-            raise ValueError("state_in and state_out must have the same slots")
-        n_slots = state_out.size(0)
+        so = _contiguous("state_out", state_out, dtype, 3, index)
+        slots, e0, e1 = state_out.shape
+        if e0 != d0 or e1 != d1 or (si and slots != n_slots):
+            raise ValueError(f"state_out must be [slots, {d0}, {d1}] with as many slots as state_in, got {tuple(state_out.shape)}")
+        n_slots = slots
+    return si, so, n_slots
+
+
+def _packing(cu_seqlens, slots, tokens: int, index: int):
+    """(sequences, address of cu_seqlens, address of slots)."""
+    cu = sl = 0
+    n = tokens
+    if cu_seqlens is not None:
+        cu = _contiguous("cu_seqlens", cu_seqlens, _I32, 1, index)
+        n = cu_seqlens.shape[0] - 1
     if slots is not None:
         sl = _contiguous("slots", slots, _I32, 1, index)
-        if slots.size(0) != n:
+        if slots.shape[0] != n:
             raise ValueError("slots must name one slot for each sequence")
-    return n, cu, si, so, sl, n_slots
+    return n, cu, sl
 
 
-def _parameter(name: str, t: Optional[torch.Tensor], channels: int, index: int) -> int:
-    """The address of an optional fp32 [channels] tensor."""
-    if t is None:
-        return 0
-    p = _contiguous(name, t, _F32, 1, index)
-    if t.size(0) != channels:
-        raise ValueError(f"{name} must have {channels} entries")
-    return p
+def _parameter(name: str, t: torch.Tensor, channels: int, index: int) -> int:
+    """The address of an fp32 [channels] tensor."""
+    if t.dtype is _F32 and t.get_device() == index and t.is_contiguous() and t.shape == (channels,):
+        return t.data_ptr()
+    _refuse(name, t, _F32, 1, index) if t.dim() != 1 or t.shape[0] == channels else None
+    raise ValueError(f"{name} must have {channels} entries")
 
 
 def short_conv(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: Optional[torch.Tensor] = None, *,
@@ -86,28 +93,26 @@ def short_conv(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: Optional[torch
     those before the next call's; None for sequences that begin, or are not continued.  They may be the same tensor."""
     lib = load_library()
     dev = _device(x, "x")
-    if x.dim() != 2:
-        raise ValueError("x must be [tokens, channels]")
-    T, channels = x.shape
-    xp, stride = _rows("x", x, T, channels, dev)
+    shape = x.shape
+    stride = _rows("x", x, shape, dev)
+    T, channels = shape
     wp = _contiguous("weight", weight, _F32, 2, dev)
-    if weight.size(0) != channels:
+    rows, width = weight.shape
+    if rows != channels:
         raise ValueError(f"weight must be [{channels}, width]")
-    width = weight.size(1)
     code = CONV_ACT.get(act)
     if code is None:
         raise ValueError(f"act must be one of {sorted(CONV_ACT)}")
-    n, cu, si, so, sl, n_slots = _sequences(cu_seqlens, T, state_in, state_out, slots, (width - 1, channels), _BF16, dev)
-    bp = _parameter("bias", bias, channels, dev)
+    n, cu, sl = (T, 0, 0) if cu_seqlens is None and slots is None else _packing(cu_seqlens, slots, T, dev)
+    si, so, n_slots = _states(state_in, state_out, width - 1, channels, _BF16, dev)
+    bp = 0 if bias is None else _parameter("bias", bias, channels, dev)
     if out is None:
-        out = _empty(stream, (T, channels), _BF16, x.device)
-        op = out.data_ptr()
-    else:
-        op = _contiguous("out", out, _BF16, 2, dev)
-        if out.shape != (T, channels):
-            raise ValueError("out must have the shape of x")
-    _launch(lib.gdn_short_conv, "gdn_short_conv", dev, stream, n, T, channels, width, xp, stride, wp, bp, code, cu, si, so,
-            sl, n_slots, op)
+        out = x.new_empty((T, channels)) if stream is None else _empty(stream, shape, _BF16, x.device)
+    elif out.dtype is not _BF16 or out.get_device() != dev or not out.is_contiguous() or out.shape != shape:
+        _contiguous("out", out, _BF16, 2, dev)
+        raise ValueError("out must have the shape of x")
+    _launch(lib.gdn_short_conv, "gdn_short_conv", dev, stream, n, T, channels, width, x.data_ptr(), stride, wp, bp, code, cu, si,
+            so, sl, n_slots, out.data_ptr())
     return out
 
 
@@ -121,16 +126,18 @@ def scan_workspace_size(n_seqs: int, total_tokens: int, channels: int, n_state: 
     return int(need)
 
 
-def _vectors(name: str, t: torch.Tensor, shape, index: int) -> Tuple[int, int]:
-    """Address and token stride of a bf16 [tokens, groups, n_state] tensor whose tokens' rows are contiguous."""
+def _vectors(name: str, t: torch.Tensor, shape, index: int) -> int:
+    """The token stride of a bf16 [tokens, groups, n_state] tensor whose tokens' vectors are contiguous."""
     if t.dtype is not _BF16 or t.get_device() != index or t.dim() != 3:
         _refuse(name, t, _BF16, 3, index)
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return shape[1] * shape[2]
     stride = t.stride()
     if stride[2] != 1 or (shape[1] > 1 and stride[1] != shape[2]):
         raise ValueError(f"{name}: a token's vectors must be contiguous")
-    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1] * shape[2]
+    return stride[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
 def scan(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch.Tensor, c: torch.Tensor,
@@ -149,43 +156,50 @@ def scan(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch.Tensor, c:
     chooses the kernel, nothing else."""
     lib = load_library()
     dev = _device(x, "x")
-    if x.dim() != 2 or b.dim() != 3:
-        raise ValueError("x must be [tokens, channels] and b [tokens, groups, n_state]")
-    T, channels = x.shape
-    groups, n_state = b.size(1), b.size(2)
-    xp, x_stride = _rows("x", x, T, channels, dev)
-    dp, d_stride = _rows("dt", dt, T, channels, dev)
-    zp, z_stride = (0, 0) if z is None else _rows("z", z, T, channels, dev)
-    shape = (T, groups, n_state)
-    bp, b_stride = _vectors("b", b, shape, dev)
-    cp, c_stride = _vectors("c", c, shape, dev)
+    shape, vectors = x.shape, b.shape
+    x_stride = _rows("x", x, shape, dev)
+    d_stride = _rows("dt", dt, shape, dev)
+    b_stride = _vectors("b", b, vectors, dev)
+    c_stride = _vectors("c", c, vectors, dev)
+    T, channels = shape
+    tokens, groups, n_state = vectors
+    if tokens != T:
+        raise ValueError("x and b must have the same tokens")
+    zp = z_stride = 0
+    if z is not None:
+        z_stride = _rows("z", z, shape, dev)
+        zp = z.data_ptr()
     ap = _contiguous("a", a, _F32, 2, dev)
     if a.shape != (channels, n_state):
         raise ValueError(f"a must be [{channels}, {n_state}]")
-    n, cu, si, so, sl, n_slots = _sequences(cu_seqlens, T, state_in, state_out, slots, (channels, n_state), _F32, dev)
-    skip, bias = _parameter("d", d, channels, dev), _parameter("dt_bias", dt_bias, channels, dev)
-    if out is None:
-        if out_dtype not in DTYPE:
-            raise ValueError("out_dtype must be bf16 or fp32")
-        out = _empty(stream, (T, channels), out_dtype, x.device)
-        op = out.data_ptr()
-    else:
+    skip = 0 if d is None else _parameter("d", d, channels, dev)
+    bias = 0 if dt_bias is None else _parameter("dt_bias", dt_bias, channels, dev)
+    si, so, n_slots = _states(state_in, state_out, channels, n_state, _F32, dev)
+    if out is not None:
         out_dtype = out.dtype
-        op = _contiguous("out", out, out_dtype, 2, dev)
-        if out_dtype not in DTYPE or out.shape != (T, channels):
-            raise ValueError("out must have the shape of x, in bf16 or fp32")
-    max_len = 1 if cu_seqlens is None else min(_int32(max_len), T)
-    if workspace is None:
-        ws_bytes = 0 if max_len == 1 else scan_workspace_size(n, T, channels, n_state, groups, max_len)
-        wsp = 0
-        if ws_bytes:
-            workspace = _empty(stream, ws_bytes, torch.uint8, x.device)
-            wsp = workspace.data_ptr()
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the other tensors' device")
+        _contiguous("out", out, out_dtype, 2, dev)
+    out_code = DTYPE.get(out_dtype)
+    if out_code is None or (out is not None and out.shape != shape):
+        raise ValueError("out must have the shape of x, in bf16 or fp32")
+    if out is None:
+        out = x.new_empty((T, channels)) if stream is None and out_code == 0 else _empty(stream, shape, out_dtype, x.device)
+    wsp = ws_bytes = 0
+    if cu_seqlens is None:
+        n, cu, sl = (T, 0, 0) if slots is None else _packing(None, slots, T, dev)
+        max_len = 1
     else:
+        n, cu, sl = _packing(cu_seqlens, slots, T, dev)
+        max_len = min(_int32(max_len), T)
+        if workspace is None:
+            ws_bytes = scan_workspace_size(n, T, channels, n_state, groups, max_len)
+            if ws_bytes:
+                workspace = _empty(stream, ws_bytes, torch.uint8, x.device)
+                wsp = workspace.data_ptr()
+    if workspace is not None and not wsp:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the other tensors' device")
         ws_bytes, wsp = workspace.numel() * workspace.element_size(), workspace.data_ptr()
-    _launch(lib.gdn_ssm_scan, "gdn_ssm_scan", dev, stream, n, T, channels, n_state, groups, xp, x_stride, dp, d_stride, ap,
-            bp, b_stride, cp, c_stride, skip, zp, z_stride, bias, int(bool(dt_softplus)), cu, max_len, si, so, sl, n_slots, op,
-            DTYPE[out_dtype], wsp, ws_bytes)
+    _launch(lib.gdn_ssm_scan, "gdn_ssm_scan", dev, stream, n, T, channels, n_state, groups, x.data_ptr(), x_stride, dt.data_ptr(),
+            d_stride, ap, b.data_ptr(), b_stride, c.data_ptr(), c_stride, skip, zp, z_stride, bias, 1 if dt_softplus else 0, cu,
+            max_len, si, so, sl, n_slots, out.data_ptr(), out_code, wsp, ws_bytes)
     return out
