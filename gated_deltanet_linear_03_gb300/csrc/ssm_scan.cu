@@ -3,6 +3,7 @@
 //
 // A channel's states lie in the registers of N / S neighbouring lanes, S each, for as long as its sequence lasts.
 #include "layer_ops.cuh"
+#include "sm100.cuh"
 
 namespace gdn {
 namespace {
@@ -16,11 +17,30 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-__device__ __forceinline__ float step_width(float v, int softplus) {
-    return softplus ? fmaxf(v, 0.f) + log1pf(expf(-fabsf(v))) : v;
+__device__ __forceinline__ float reciprocal(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-__device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.f + __expf(-z)); }
+// log(1 + e^v) = max(v, 0) + log(1 + e), e = e^-|v|, without a branch and to a few units in the last place however small e is.
+// The exponential's argument is corrected for its rounding; log(1 + e) = 2 artanh(q) with q = e / (2 + e) <= 1/3, by its series.
+__device__ __forceinline__ float softplus(float v) {
+    const float m = -fabsf(v), t = m * kLog2e;
+    const float r = fmaf(m, 1.925963033500e-8f, fmaf(m, kLog2e, -t));       // what t lacks of m log2 e
+    float e = ex2(t);
+    e = fmaf(e, r * 0.69314718f, e);
+    const float q = e * reciprocal(2.f + e), q2 = q * q;
+    float s = fmaf(q2, 1.f / 13, 1.f / 11);
+    s = fmaf(q2, s, 1.f / 9);
+    s = fmaf(q2, s, 1.f / 7);
+    s = fmaf(q2, s, 1.f / 5);
+    s = fmaf(q2, s, 1.f / 3);
+    s = fmaf(q2, s, 1.f);
+    return fmaf(2.f * q, s, fmaxf(v, 0.f));
+}
+
+__device__ __forceinline__ float silu(float z) { return z * reciprocal(1.f + ex2(-kLog2e * z)); }
 
 template <int S>
 __device__ __forceinline__ void load_state(const float *p, float (&h)[S]) {
@@ -59,7 +79,7 @@ __global__ void __launch_bounds__(kScanThreads) step_kernel(const __grid_constan
     const int bc = c / (p.channels / p.groups) * N + 4 * part;
     for (int t = p.seqs.begin(n); t < p.seqs.end(n); ++t) {
         const float x = __bfloat162float(p.x[t * p.x_stride + c]);
-        const float d = step_width(__bfloat162float(p.dt[t * p.dt_stride + c]) + bias, p.softplus);
+        const float v = __bfloat162float(p.dt[t * p.dt_stride + c]) + bias, d = p.softplus ? softplus(v) : v;
         const float z = p.z ? __bfloat162float(p.z[t * p.z_stride + c]) : 0.f;
         const uint2 bw = *reinterpret_cast<const uint2 *>(p.b + t * p.b_stride + bc);
         const uint2 cw = *reinterpret_cast<const uint2 *>(p.c + t * p.c_stride + bc);
@@ -113,12 +133,32 @@ constexpr int kMaxPiece = 2048;             // tokens of a piece of a scan in pi
 template <int N_, int S_>
 struct Shape {
     static constexpr int N = N_, S = S_, LANES = N / S, V = 32 / LANES, CH = 4 * V;     // V: channels of a warp
+    // A tile's raw rows and vectors are asked for DEEP turns before it is prepared, to cover a read of memory; that of turn
+    // i + 1 + DEEP while tile i is scanned, so they need two places more.  (States of 128: two CTAs an SM leave room for less.)
+    static constexpr int DEEP = N == 128 ? 2 : 4, RING = DEEP + 2;
     struct Tile {
-        float4 du[kTile][CH];               // step width D (times log2 e) twice, and D x twice
-        float b[kTile][N], c[kTile][N];
+        float2 du[kTile][CH];               // step width D (times log2 e) and D x
         float y[4 * kTile][36];             // by token and warp: the lanes' parts of y; 4 floats of padding against bank conflicts
     };
+    struct Shared {
+        Tile tile[2];                       // prepared, and scanned
+        uint4 bc[RING][kTile][N / 4];      // by 4 states: B and C as they came, in bf16
+        __nv_bfloat16 x[RING][128][V], dt[RING][128][V], z[RING][128][V];      // by preparing thread
+    };
+    // Row id = 4 token + warp of V channels of du holds its pairs of channels in the order pair ^ key, so that 8 rows written at
+    // once meet few banks twice.
+    __device__ static __forceinline__ int key(int id) { return V == 8 ? (id >> 1) & 3 : V == 4 ? (id >> 2) & 1 : 0; }
 };
+
+// Copy BYTES (4, 8 or 16) to shared memory behind the thread's back, zeros where there is nothing to read.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *to, const void *from, bool there) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(sm100::smem_u32(to)), "l"(from), "n"(BYTES), "r"(there ? BYTES : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 
 // V bf16 values, as they lie in memory.
 template <int V> struct Bits { using T = uint4; };
@@ -134,79 +174,85 @@ __device__ __forceinline__ void unpack(const typename Bits<V>::T &u, float (&x)[
     }
 }
 
-// What a preparing thread reads of one tile: V channels of one token, and its share of the vectors.
-template <class SH>
-struct Raw {
-    using T = typename Bits<SH::V>::T;
-    static constexpr int PIECES = kTile * SH::N / 8, VECTORS = 2 * PIECES / 128;
-    T x, dt, z;
-    uint4 bc[VECTORS];
-    template <bool WITH_Y>
-    __device__ __forceinline__ void load(const ScanProblem &p, int id, int t0, int t1, int c, bool live, int group) {
-        const int t = t0 + id / 4;
-        const bool ok = live && t < t1;
-        x = dt = z = T{};
-        if (ok) {
-            x = *reinterpret_cast<const T *>(p.x + t * p.x_stride + c);
-            dt = *reinterpret_cast<const T *>(p.dt + t * p.dt_stride + c);
-            if (WITH_Y && p.z) z = *reinterpret_cast<const T *>(p.z + t * p.z_stride + c);
-        }
-#pragma unroll
-        for (int i = 0; i < VECTORS; ++i) {
-            const int k = id + i * 128, which = k / PIECES, at = k % PIECES;
-            const int tb = t0 + at / (SH::N / 8), e = group * SH::N + at % (SH::N / 8) * 8;
-            bc[i] = make_uint4(0, 0, 0, 0);
-            if (tb < t1 && (WITH_Y || which == 0))
-                bc[i] = *reinterpret_cast<const uint4 *>(which ? p.c + tb * p.c_stride + e : p.b + tb * p.b_stride + e);
-        }
-    }
-};
-
 // All of the CTA's warps meet here, those that scan and those that prepare, from different places.
 __device__ __forceinline__ void turn() { asm volatile("barrier.sync 1, %0;" ::"n"(kPromptThreads) : "memory"); }
 
 // Tokens [t0, t1) of one sequence for the CTA's channels c0 .. and below c1.  h: a scanning lane's part of its channel's
 // state; *width_sum: the sum of its step widths (times log2 e).
 template <class SH, bool WITH_Y>
-__device__ __forceinline__ void scan_tokens(const ScanProblem &p, typename SH::Tile *tiles, int t0, int t1, int c0, int c1, int group,
+__device__ __forceinline__ void scan_tokens(const ScanProblem &p, typename SH::Shared &sh, int t0, int t1, int c0, int c1, int group,
                                             const Pair (&a)[SH::S / 2], Pair (&h)[SH::S / 2], float *width_sum) {
     constexpr int S = SH::S, N = SH::N, V = SH::V, LANES = SH::LANES;
     const int n = (t1 - t0 + kTile - 1) / kTile;
     if (n <= 0) return;
     if (threadIdx.x < 128) {
-        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, part = lane % LANES, chan = warp * V + lane / LANES;
+        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, part = lane % LANES;
         float total = 0.f;
         turn();
+        // Steps go by batches: a batch's exponentials depend on nothing but its inputs, which are asked for a batch ahead
+        constexpr int BATCH = S == 4 ? 4 : 2;
+        struct Step { float2 w; uint4 bc[S / 4]; };
+        const int ch = lane / LANES;
         for (int i = 0; i < n; ++i) {
-            typename SH::Tile &s = tiles[i & 1];
-            const float4 *du = &s.du[0][chan];
-            const float *b = &s.b[0][S * part], *c = &s.c[0][S * part];
+            typename SH::Tile &s = sh.tile[i & 1];
+            const float2 *du = &s.du[0][warp * V];
+            const uint4 *bc = &sh.bc[i % SH::RING][0][S / 4 * part];
             float *y = &s.y[warp][lane];
-#pragma unroll 8
-            for (int t = 0; t < kTile; ++t) {
-                const Pair2 w = *reinterpret_cast<const Pair2 *>(du + t * SH::CH);
-                Pair sum = 0;
+            auto fetch = [&](int t, Step (&q)[BATCH]) {
 #pragma unroll
-                for (int k = 0; k < S / 4; ++k) {
-                    const Pair2 bb = *reinterpret_cast<const Pair2 *>(b + t * N + 4 * k);
-                    Pair2 cc{};
-                    if (WITH_Y) cc = *reinterpret_cast<const Pair2 *>(c + t * N + 4 * k);
+                for (int j = 0; j < BATCH; ++j) {
+                    q[j].w = du[(t + j) * SH::CH + (ch ^ 2 * SH::key(4 * (t + j) + warp))];
 #pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        float e0, e1;
-                        halves(mul2(w.x, a[2 * k + m]), e0, e1);
-                        h[2 * k + m] = fma2(pair(ex2(e0), ex2(e1)), h[2 * k + m], mul2(w.y, m ? bb.y : bb.x));
-                        if (WITH_Y) sum = k + m ? fma2(h[2 * k + m], m ? cc.y : cc.x, sum) : mul2(h[0], cc.x);
+                    for (int k = 0; k < S / 4; ++k) {
+                        const uint4 *from = bc + (t + j) * (N / 4) + k;
+                        if (WITH_Y) q[j].bc[k] = *from;
+                        else {
+                            const uint2 only = *reinterpret_cast<const uint2 *>(from);
+                            q[j].bc[k].x = only.x, q[j].bc[k].y = only.y;
+                        }
                     }
                 }
-                if (WITH_Y) {
-                    float lo, hi;
-                    halves(sum, lo, hi);
-                    y[t * 4 * 36] = lo + hi;
-                } else {
-                    float lo, hi;
-                    halves(w.x, lo, hi);
-                    total += lo;
+            };
+            Step next[BATCH];
+            fetch(0, next);
+#pragma unroll
+            for (int t = 0; t < kTile; t += BATCH) {
+                Step q[BATCH];
+#pragma unroll
+                for (int j = 0; j < BATCH; ++j) q[j] = next[j];
+                if (t + BATCH < kTile) fetch(t + BATCH, next);
+                Pair decay[BATCH][S / 2];
+#pragma unroll
+                for (int j = 0; j < BATCH; ++j) {
+                    const Pair w = pair(q[j].w.x, q[j].w.x);
+#pragma unroll
+                    for (int k = 0; k < S / 2; ++k) {
+                        float e0, e1;
+                        halves(mul2(w, a[k]), e0, e1);
+                        decay[j][k] = pair(ex2(e0), ex2(e1));
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < BATCH; ++j) {
+                    const Pair u = pair(q[j].w.y, q[j].w.y);
+                    Pair sum = 0;
+#pragma unroll
+                    for (int k = 0; k < S / 2; ++k) {
+                        const uint32_t b = k & 1 ? q[j].bc[k / 2].y : q[j].bc[k / 2].x;
+                        h[k] = fma2(decay[j][k], h[k], mul2(u, pair(bf16_lo(b), bf16_hi(b))));
+                        if (WITH_Y) {
+                            const uint32_t c = k & 1 ? q[j].bc[k / 2].w : q[j].bc[k / 2].z;
+                            const Pair cv = pair(bf16_lo(c), bf16_hi(c));
+                            sum = k ? fma2(h[k], cv, sum) : mul2(h[k], cv);
+                        }
+                    }
+                    if (WITH_Y) {
+                        float lo, hi;
+                        halves(sum, lo, hi);
+                        y[(t + j) * 4 * 36] = lo + hi;
+                    } else {
+                        total += q[j].w.x;
+                    }
                 }
             }
             turn();
@@ -222,39 +268,61 @@ __device__ __forceinline__ void scan_tokens(const ScanProblem &p, typename SH::T
         bias[e] = live && p.dt_bias ? __ldg(p.dt_bias + c + e) : 0.f;
         skip[e] = live && WITH_Y && p.skip ? __ldg(p.skip + c + e) : 0.f;
     }
-    Raw<SH> raw;
-    typename Raw<SH>::T x1{}, z1{}, x0{}, z0{};            // of the tile that is scanned, and of the one before it
+    using T = typename Bits<V>::T;
+    auto ask = [&](int i) {
+        if (i < n) {
+            const int t = t0 + i * kTile + id / 4, slot = i % SH::RING;
+            const bool there = live && t < t1;
+            copy_async<2 * V>(sh.x[slot][id], p.x + (there ? t * p.x_stride + c : 0), there);
+            copy_async<2 * V>(sh.dt[slot][id], p.dt + (there ? t * p.dt_stride + c : 0), there);
+            if (WITH_Y && p.z) copy_async<2 * V>(sh.z[slot][id], p.z + (there ? t * p.z_stride + c : 0), there);
+#pragma unroll
+            for (int k = 0; k < N / 16; ++k) {
+                const int at = id + k * 128, tv = t0 + i * kTile + at / (N / 4), e = group * N + at % (N / 4) * 4;
+                uint2 *to = reinterpret_cast<uint2 *>(&sh.bc[slot][0][at]);
+                copy_async<8>(to, p.b + (tv < t1 ? tv * p.b_stride + e : 0), tv < t1);
+                if (WITH_Y) copy_async<8>(to + 1, p.c + (tv < t1 ? tv * p.c_stride + e : 0), tv < t1);
+            }
+        }
+        copy_commit();                      // (a group for every turn, so that their number says which have arrived)
+    };
+    T x1{}, z1{}, x0{}, z0{};               // of the tile that is scanned, and of the one before it
     auto prepare = [&](int i) {
-        typename SH::Tile &s = tiles[i & 1];
+        typename SH::Tile &s = sh.tile[i & 1];
+        copy_wait<SH::DEEP - 1>();
+        const int slot = i % SH::RING;
+        const T xr = *reinterpret_cast<const T *>(sh.x[slot][id]), dr = *reinterpret_cast<const T *>(sh.dt[slot][id]);
+        x0 = x1, z0 = z1, x1 = xr;
+        if (WITH_Y && p.z) z1 = *reinterpret_cast<const T *>(sh.z[slot][id]);
         float x[V], d[V];
-        unpack<V>(raw.x, x);
-        unpack<V>(raw.dt, d);
+        unpack<V>(xr, x);
+        unpack<V>(dr, d);
         const bool inside = t0 + i * kTile + id / 4 < t1;
-        float4 *to = &s.du[id / 4][V * (id % 4)];
+        float4 *to = reinterpret_cast<float4 *>(&s.du[id / 4][V * (id % 4)]);
+        const int key = SH::key(id);
+#pragma unroll
+        for (int e = 0; e < V; ++e) d[e] += bias[e];
+        if (p.softplus) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) d[e] = softplus(d[e]);
+        }
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            const float w = inside ? step_width(d[e] + bias[e], p.softplus) : 0.f;        // (a row beyond the end changes nothing)
-            to[e] = make_float4(w * kLog2e, w * kLog2e, w * x[e], w * x[e]);
+            d[e] = inside ? d[e] : 0.f;                               // (a row beyond the end changes nothing)
+            x[e] *= d[e];
+            d[e] *= kLog2e;
         }
 #pragma unroll
-        for (int k = 0; k < Raw<SH>::VECTORS; ++k) {
-            const int at = id + k * 128, which = at / Raw<SH>::PIECES, v = at % Raw<SH>::PIECES;
-            float f[8];
-            unpack8(raw.bc[k], f);
-            float4 *bc = reinterpret_cast<float4 *>((which ? s.c[0] : s.b[0]) + 8 * v);
-            bc[0] = make_float4(f[0], f[1], f[2], f[3]);
-            bc[1] = make_float4(f[4], f[5], f[6], f[7]);
-        }
-        x0 = x1, z0 = z1, x1 = raw.x, z1 = raw.z;
-        if (i + 1 < n) raw.template load<WITH_Y>(p, id, t0 + (i + 1) * kTile, t1, c, live, group);
+        for (int e = 0; e < V / 2; ++e) to[e ^ key] = make_float4(d[2 * e], x[2 * e], d[2 * e + 1], x[2 * e + 1]);
+        ask(i + SH::DEEP);
     };
-    auto finish = [&](int i, const typename Raw<SH>::T &xr, const typename Raw<SH>::T &zr) {
+    auto finish = [&](int i, const T &xr, const T &zr) {
         const int t = t0 + i * kTile + id / 4;
         if (!WITH_Y || !live || t >= t1) return;
         float x[V], z[V], y[V];
         unpack<V>(xr, x);
         unpack<V>(zr, z);
-        const float *from = tiles[i & 1].y[id];
+        const float *from = sh.tile[i & 1].y[id];
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             float q[LANES];
@@ -268,7 +336,10 @@ __device__ __forceinline__ void scan_tokens(const ScanProblem &p, typename SH::T
 #pragma unroll
                 for (int k = 0; k < o; ++k) q[k] += q[k + o];
             y[e] = fmaf(skip[e], x[e], q[0]);
-            if (p.z) y[e] *= silu(z[e]);
+        }
+        if (p.z) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) y[e] *= silu(z[e]);
         }
         const size_t to = (size_t)t * p.channels + c;
         if (p.out_f32) {
@@ -276,19 +347,19 @@ __device__ __forceinline__ void scan_tokens(const ScanProblem &p, typename SH::T
 #pragma unroll
             for (int k = 0; k < V / 2; ++k) o[k] = make_float2(y[2 * k], y[2 * k + 1]);
         } else {
-            typename Raw<SH>::T o;
+            T o;
             uint32_t *w = reinterpret_cast<uint32_t *>(&o);
 #pragma unroll
             for (int k = 0; k < V / 2; ++k) w[k] = pack2(y[2 * k], y[2 * k + 1]);
-            *reinterpret_cast<typename Raw<SH>::T *>(static_cast<__nv_bfloat16 *>(p.out) + to) = o;
+            *reinterpret_cast<T *>(static_cast<__nv_bfloat16 *>(p.out) + to) = o;
         }
     };
-    raw.template load<WITH_Y>(p, id, t0, t1, c, live, group);
+    for (int i = 0; i < SH::DEEP; ++i) ask(i);
     prepare(0);
     turn();
     for (int i = 0; i < n; ++i) {
         // x1, z1 are tile i's; after prepare(i + 1) they are x0, z0
-        const auto xp = x0, zp = z0;
+        const T xp = x0, zp = z0;
         if (i + 1 < n) prepare(i + 1);
         else x0 = x1, z0 = z1;
         if (i > 0) finish(i - 1, xp, zp);
@@ -311,7 +382,7 @@ enum Pass { kWhole, kEnds, kOutputs };
 template <class SH, int PASS>
 __global__ void __launch_bounds__(kPromptThreads, 2) scan_kernel(const __grid_constant__ ScanProblem p, const __grid_constant__ ScanPlan plan) {
     extern __shared__ __align__(16) unsigned char smem[];
-    typename SH::Tile *tiles = reinterpret_cast<typename SH::Tile *>(smem);
+    typename SH::Shared &sh = *reinterpret_cast<typename SH::Shared *>(smem);
     constexpr int N = SH::N, S = SH::S;
     const int per_group = p.channels / p.groups, ctas = plan.ctas_per_group * p.groups;
     const int unit = blockIdx.x / ctas, group = blockIdx.x % ctas / plan.ctas_per_group;
@@ -345,7 +416,7 @@ __global__ void __launch_bounds__(kPromptThreads, 2) scan_kernel(const __grid_co
             return;
         }
         load(state_in(slot), h);
-        scan_tokens<SH, true>(p, tiles, p.seqs.begin(unit), p.seqs.end(unit), c0, c1, group, a, h, &width_sum);
+        scan_tokens<SH, true>(p, sh, p.seqs.begin(unit), p.seqs.end(unit), c0, c1, group, a, h, &width_sum);
         if (p.state_out) store(p.state_out + slot * all, h);
         return;
     }
@@ -357,7 +428,7 @@ __global__ void __launch_bounds__(kPromptThreads, 2) scan_kernel(const __grid_co
         if (p.seqs.end(n) <= t1 || b >= t1 || slot < 0) return;
         load(b >= t0 ? state_in(slot) : nullptr, h);
         if (b >= t0 && p.state_in) store(plan.begins + unit * all, h);       // (state_out may be state_in, and is written by others)
-        scan_tokens<SH, false>(p, tiles, max(b, t0), t1, c0, c1, group, a, h, &width_sum);
+        scan_tokens<SH, false>(p, sh, max(b, t0), t1, c0, c1, group, a, h, &width_sum);
         store(plan.ends + unit * all, h);
         if (live && part == 0) plan.widths[(size_t)unit * p.channels + c] = width_sum;
         return;
@@ -404,7 +475,7 @@ __global__ void __launch_bounds__(kPromptThreads, 2) scan_kernel(const __grid_co
                 }
             }
         }
-        scan_tokens<SH, true>(p, tiles, max(b, t0), min(e, t1), c0, c1, group, a, h, &width_sum);
+        scan_tokens<SH, true>(p, sh, max(b, t0), min(e, t1), c0, c1, group, a, h, &width_sum);
         if (e <= t1 && p.state_out) store(p.state_out + slot * all, h);
         t = e;
     }
@@ -441,7 +512,7 @@ cudaError_t launch(const ScanProblem &p) {
         step_kernel<N><<<(unsigned)ctas, kScanThreads, 0, p.stream>>>(p);
         return cudaGetLastError();
     }
-    constexpr int smem = 2 * (int)sizeof(typename SH::Tile);
+    constexpr int smem = (int)sizeof(typename SH::Shared);
     ScanPlan s = plan_scan<N>(p.seqs.n, p.seqs.total, p.channels, p.groups, p.max_len);
     const long ctas = (long)s.ctas_per_group * p.groups;
     using Fn = void (*)(const ScanProblem, const ScanPlan);
