@@ -52,12 +52,14 @@ gdn_status check_q4_shape(int rows, int n_out, int k, int group) {
     if (rows < 0 || n_out <= 0 || k <= 0) return GDN_ERR_INVALID_ARG;
     if (group != 64 && group != 128) return GDN_ERR_UNSUPPORTED;
     if (k % group != 0 || k > 65536) return GDN_ERR_UNSUPPORTED;
-    if (rows > INT_MAX - 65536 || n_out > INT_MAX - 65536) return GDN_ERR_UNSUPPORTED;    // tiles are counted in 32 bits
+    if (rows > INT_MAX - 65536 || n_out > INT_MAX - 65536) return GDN_ERR_UNSUPPORTED;
+    // CTAs are counted in 32 bits: 8 rows of x, 128 of weights and an eighth of the inputs each at the least
+    if (((double)rows / 8 + 1) * ((double)n_out / 128 + 1) * 8 >= 2147483648.0) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 
 gdn_status q4(int rows, int n_out, int k, int group, const void *x, long long x_stride, const gdn::Q4Matrix &w,
-              const gdn::Q4Matrix *up, int gelu, void *out, int out_dtype, void *stream) {
+              const gdn::Q4Matrix *up, int gelu, void *out, int out_dtype, void *workspace, size_t workspace_bytes, void *stream) {
     gdn_status st = check_q4_shape(rows, n_out, k, group);
     if (st != GDN_OK) return st;
     if (out_dtype != GDN_DTYPE_BF16 && out_dtype != GDN_DTYPE_F32) return GDN_ERR_UNSUPPORTED;
@@ -71,12 +73,15 @@ gdn_status q4(int rows, int n_out, int k, int group, const void *x, long long x_
     for (const void *p : ptrs)
         if (!aligned(p)) return GDN_ERR_ALIGNMENT;
     const size_t codes = (size_t)n_out * (k / 2), scales = (size_t)n_out * (k / group) * 2;
-    const Range outs[] = {{out, (size_t)rows * n_out * (out_dtype == GDN_DTYPE_F32 ? 4 : 2)}};
+    const size_t need = gdn::q4_workspace_bytes(rows, n_out, k, out_dtype == GDN_DTYPE_F32);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return GDN_ERR_ALIGNMENT;
+    const Range outs[] = {{out, (size_t)rows * n_out * (out_dtype == GDN_DTYPE_F32 ? 4 : 2)}, {workspace, need}};
     const Range ins[] = {{x, rows_bytes(rows, x_stride, k)}, {w.codes, codes}, {w.scales, scales}, {w.offsets, scales},
                          {v.codes, codes}, {v.scales, scales}, {v.offsets, scales}};
     if (!disjoint(outs, ins)) return GDN_ERR_INVALID_ARG;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-    const void *anchors[] = {x, w.codes, out};
+    const void *anchors[] = {x, w.codes, out, workspace};
     st = gdn::on_current_device(anchors, sizeof(anchors) / sizeof(anchors[0]), cs);
     if (st != GDN_OK) return st;
     gdn::Q4Problem p{};
@@ -85,6 +90,7 @@ gdn_status q4(int rows, int n_out, int k, int group, const void *x, long long x_
     p.x_stride = x_stride;
     p.w = w; p.up = v; p.gated = up != nullptr; p.gelu = gelu;
     p.out = out; p.out_f32 = out_dtype == GDN_DTYPE_F32;
+    p.workspace = workspace;
     p.stream = cs;
     return gdn::launch_q4(p) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
@@ -199,18 +205,28 @@ gdn_status gdn_ssm_scan(int n_seqs, int total_tokens, int channels, int n_state,
     return gdn::launch_ssm_scan(p) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
+size_t gdn_q4_workspace_size(int rows, int n_out, int k, int group, int out_dtype, gdn_status *status) {
+    gdn_status st = check_q4_shape(rows, n_out, k, group);
+    if (st == GDN_OK && out_dtype != GDN_DTYPE_BF16 && out_dtype != GDN_DTYPE_F32) st = GDN_ERR_UNSUPPORTED;
+    if (status) *status = st;
+    return st == GDN_OK ? gdn::q4_workspace_bytes(rows, n_out, k, out_dtype == GDN_DTYPE_F32) : 0;
+}
+
 gdn_status gdn_q4_linear(int rows, int n_out, int k, int group, const void *x, long long x_stride, const void *codes,
-                         const void *scales, const void *offsets, void *out, int out_dtype, void *stream) {
-    return q4(rows, n_out, k, group, x, x_stride, matrix(codes, scales, offsets), nullptr, 0, out, out_dtype, stream);
+                         const void *scales, const void *offsets, void *out, int out_dtype, void *workspace,
+                         size_t workspace_bytes, void *stream) {
+    return q4(rows, n_out, k, group, x, x_stride, matrix(codes, scales, offsets), nullptr, 0, out, out_dtype, workspace,
+              workspace_bytes, stream);
 }
 
 gdn_status gdn_q4_gated(int rows, int n_out, int k, int group, const void *x, long long x_stride, const void *gate_codes,
                         const void *gate_scales, const void *gate_offsets, const void *up_codes, const void *up_scales,
-                        const void *up_offsets, int act, void *out, int out_dtype, void *stream) {
+                        const void *up_offsets, int act, void *out, int out_dtype, void *workspace, size_t workspace_bytes,
+                        void *stream) {
     if (act != GDN_FFN_SILU && act != GDN_FFN_GELU) return GDN_ERR_UNSUPPORTED;
     const gdn::Q4Matrix up = matrix(up_codes, up_scales, up_offsets);
     return q4(rows, n_out, k, group, x, x_stride, matrix(gate_codes, gate_scales, gate_offsets), &up, act == GDN_FFN_GELU, out,
-              out_dtype, stream);
+              out_dtype, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

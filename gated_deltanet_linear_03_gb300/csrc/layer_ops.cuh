@@ -68,8 +68,19 @@ struct Q4Problem {
     int gated, gelu;
     void *out;
     int out_f32;
+    void *workspace;
     cudaStream_t stream;
 };
 cudaError_t launch_q4(const Q4Problem &p);
+size_t q4_workspace_bytes(int rows, int n_out, int k, int out_f32);
+// the kernel for many rows
+cudaError_t launch_q4_tc(const Q4Problem &p);
+size_t q4_tc_workspace_bytes(int rows, int k);
+
+// The activation of a gated feed-forward block.  gelu: 1 + tanh(v) = 2 / (1 + e^-2v), without the difference of nearly equal numbers.
+__device__ __forceinline__ float ffn_act(float u, int gelu) {
+    const float v = gelu ? 1.5957691216057308f * (u + 0.044715f * u * u * u) : u;
+    return u / (1.f + expf(-v));
+}
 
 }  // namespace gdn

@@ -42,13 +42,6 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
 
 __device__ __forceinline__ float bf16_value(__nv_bfloat16 v) { return __bfloat162float(v); }
 
-__device__ __forceinline__ float ffn_act(float u, int gelu) {
-    if (!gelu) return u / (1.f + expf(-u));
-    const float v = 0.7978845608028654f * (u + 0.044715f * u * u * u);
-    // 1 + tanh(v) = 2 / (1 + e^-2v), without the difference of nearly equal numbers
-    return u / (1.f + expf(-2.f * v));
-}
-
 struct Q4Launch {
     int slice;                // inputs of one CTA, a multiple of the group
     int cluster;              // CTAs that share the inputs
@@ -273,6 +266,14 @@ cudaError_t by_rows(const Q4Problem &p) {
 
 }  // namespace
 
-cudaError_t launch_q4(const Q4Problem &p) { return p.gated ? by_rows<true>(p) : by_rows<false>(p); }
+// Many rows and bf16 outputs: the kernel that multiplies on tcgen05, whose weights are rounded to fp16.
+static bool many_rows(int rows, int out_f32) { return rows > 16 && !out_f32; }
+
+size_t q4_workspace_bytes(int rows, int n_out, int k, int out_f32) { return many_rows(rows, out_f32) ? q4_tc_workspace_bytes(rows, k) : 0; }
+
+cudaError_t launch_q4(const Q4Problem &p) {
+    if (many_rows(p.rows, p.out_f32)) return launch_q4_tc(p);
+    return p.gated ? by_rows<true>(p) : by_rows<false>(p);
+}
 
 }  // namespace gdn

@@ -1,0 +1,455 @@
+// 4-bit products for many rows, on tcgen05: y[m, n] = sum_i W[n, i] x[m, i] with W = scale * code + offset.
+//
+// The weights are the product's first operand, 128 rows of W a CTA, and up to 256 rows of x its second: D[n, m] in TMEM.  Codes come by
+// TMA, 128 rows of 256 inputs a stage; 8 warps turn them into fp16 and write them into TMEM as the first operand's next 64 inputs,
+// a row a thread; x lies in shared memory.  So a weight is unpacked once for all rows of x of its CTA, and never goes through
+// shared memory as a number.
+//
+// Both operands are fp16, each row scaled by a power of two:
+//   x    the row's largest magnitude goes to [2^14, 2^15).  A bf16 number keeps all its bits down to 2^-32 of that.  A first kernel
+//        does this, and puts each 8 inputs in the order 0 4 1 5 2 6 3 7, in which a code word's pairs come out.
+//   W    by the row's largest 15 |scale| + |offset|, which goes to [2^-6, 2^-5); an element is rounded once, to fp16: by 2^-11 of itself
+//        and 2^-19 of the row's largest at most.  A code c in the low mantissa bits of a half is c 2^-24 (a subnormal, which the
+//        arithmetic takes as any other number), so one AND and one fused product-sum with (scale 2^24, offset) make two weights.
+// Sums are fp32; the powers of two are undone at the end.
+//
+// CTAs of a cluster share the inputs of one tile and join through distributed shared memory, in a fixed order.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "layer_ops.cuh"
+#include "sm100.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace sm100;
+
+constexpr int kRowsA = 128;               // weight rows of a CTA
+constexpr int kStep = 64;                 // inputs of a step of the product
+constexpr int kChunkIn = 256;             // inputs of a stage of codes
+constexpr int kSlots = 4;                 // steps of the first operand in TMEM, 32 columns each
+constexpr int kTcThreads = 352;           // 8 warps that unpack, one each for TMA of codes, TMA of x, and the product
+constexpr int kCodeBytes = kRowsA * kChunkIn / 2;
+constexpr int kXStages = 4;
+
+struct TcPlan {
+    int ntok, m_tiles, row_tiles, cluster;
+    int slice;                            // chunks of inputs of one CTA
+    int code_stages, tmem_cols;
+};
+
+struct TcBars {
+    uint64_t code_full[4], code_empty[4], x_full[kXStages], x_empty[kXStages], a_full[kSlots], a_empty[kSlots], done;
+    uint32_t tmem;
+    int abort;
+};
+
+// 32 lanes x 32 columns of 32 bits, a lane a thread, and the wait for them.
+__device__ __forceinline__ void tmem_st_row(uint32_t taddr, const uint32_t (&v)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,"
+                 "%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n tcgen05.wait::st.sync.aligned;\n" ::"r"(taddr),
+                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+                 "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+                 "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+                 "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t f16_twice(float v) {
+    const __half2 h = __float2half2_rn(v);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ float power_of_two(int e) { return __int_as_float((e + 127) << 23); }      // -126 .. 127
+
+// Scales and offsets of a row's groups of one chunk (4 of 64 inputs or 2 of 128), as they lie in memory.
+struct ChunkScales {
+    uint2 s, o;
+};
+
+template <bool OFFSETS>
+__device__ __forceinline__ ChunkScales chunk_scales(const Q4Matrix &w, size_t row, int groups, int first, int count, bool vector) {
+    ChunkScales c{};
+    const __nv_bfloat16 *s = w.scales + row * groups + first, *o = OFFSETS ? w.offsets + row * groups + first : nullptr;
+    if (vector) {                                        // the row's groups are a multiple of the chunk's
+        if (first >= groups) return c;
+        if (count == 4) {
+            c.s = *reinterpret_cast<const uint2 *>(s);
+            if (OFFSETS) c.o = *reinterpret_cast<const uint2 *>(o);
+        } else {
+            c.s.x = *reinterpret_cast<const uint32_t *>(s);
+            if (OFFSETS) c.o.x = *reinterpret_cast<const uint32_t *>(o);
+        }
+        return c;
+    }
+    uint32_t v[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < count && first + i < groups) {
+            v[i] = __bfloat16_as_ushort(s[i]);
+            if (OFFSETS) u[i] = __bfloat16_as_ushort(o[i]);
+        }
+    c.s = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
+    c.o = make_uint2(u[0] | u[1] << 16, u[2] | u[3] << 16);
+    return c;
+}
+
+__device__ __forceinline__ float nth_bf16(const uint2 &v, int i) {
+    const uint32_t w = i & 2 ? v.y : v.x;
+    return i & 1 ? bf16_hi(w) : bf16_lo(w);
+}
+
+template <bool GATED, bool OFFSETS>
+__global__ void __launch_bounds__(kTcThreads, 1)
+q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan l, const __grid_constant__ CUtensorMap code_map,
+             const __grid_constant__ CUtensorMap up_map, const __grid_constant__ CUtensorMap x_map, const int *__restrict__ x_exponents,
+             unsigned int *err) {
+    constexpr int MATS = GATED ? 2 : 1;
+    extern __shared__ unsigned char raw[];
+    __shared__ TcBars sm;
+    unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    unsigned char *codes = base, *xs = base + (size_t)l.code_stages * MATS * kCodeBytes;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int rank = l.cluster > 1 ? (int)cluster_ctarank() : 0, unit = blockIdx.x / l.cluster;
+    const int row0 = unit / l.m_tiles * kRowsA, m0 = unit % l.m_tiles * l.ntok;
+    const int chunk0 = rank * l.slice, k0 = chunk0 * kChunkIn;
+    const int steps = min(l.slice * (kChunkIn / kStep), (p.k - k0) / kStep), chunks = (steps + 3) / 4;       // at least one of each
+    const int x_bytes = l.ntok * 128;
+
+    if (warp == 0) tmem_alloc(&sm.tmem, l.tmem_cols);
+    if (tid == 32) {
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&sm.code_full[i], 1);
+            mbar_init(&sm.code_empty[i], 256);
+            mbar_init(&sm.x_full[i], 1);
+            mbar_init(&sm.x_empty[i], 1);
+            mbar_init(&sm.a_full[i], 128);
+            mbar_init(&sm.a_empty[i], 1);
+        }
+        mbar_init(&sm.done, 1);
+        sm.abort = 0;
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem, a_cols = tmem + MATS * l.ntok;
+    volatile int *abort = &sm.abort;
+
+    int exponent[MATS] = {};                    // of this thread's weight rows: W is scaled by 2^-exponent
+    if (warp == 8) {
+        if (lane == 0) {
+            for (int c = 0; c < chunks; ++c) {
+                const int s = c % l.code_stages;
+                if (c >= l.code_stages) mbar_poll(&sm.code_empty[s], (c / l.code_stages - 1) & 1, abort);
+                if (*abort) break;
+                mbar_arrive_expect_tx(&sm.code_full[s], MATS * kCodeBytes);
+                unsigned char *to = codes + (size_t)s * MATS * kCodeBytes;
+                tma_load_2d(to, &code_map, &sm.code_full[s], (k0 + c * kChunkIn) / 2, row0);
+                if (GATED) tma_load_2d(to + kCodeBytes, &up_map, &sm.code_full[s], (k0 + c * kChunkIn) / 2, row0);
+            }
+        }
+    } else if (warp == 9) {
+        if (lane == 0) {
+            grid_dependency_wait();             // the kernel before this one scales x
+            for (int t = 0; t < steps; ++t) {
+                const int s = t % kXStages;
+                if (t >= kXStages) mbar_poll(&sm.x_empty[s], (t / kXStages - 1) & 1, abort);
+                if (*abort) break;
+                mbar_arrive_expect_tx(&sm.x_full[s], x_bytes);
+                tma_load_2d(xs + (size_t)s * x_bytes, &x_map, &sm.x_full[s], 2 * (k0 + t * kStep), m0);     // (the map counts bytes)
+            }
+        }
+    } else if (warp == 10) {
+        if (lane == 0) {
+            const uint32_t id = idesc_f16_f32(kRowsA, l.ntok, false, false);
+            for (int t = 0; t < steps * MATS; ++t) {
+                const int k = t / MATS, which = t % MATS, slot = t % kSlots, s = k % kXStages;
+                if (which == 0) mbar_poll(&sm.x_full[s], (k / kXStages) & 1, abort);
+                mbar_poll(&sm.a_full[slot], (t / kSlots) & 1, abort);
+                if (*abort) break;
+                tc_fence_after();
+                const uint64_t xd = smem_desc(smem_u32(xs) + s * x_bytes, 16, 1024, kLayoutSwizzle128B);
+#pragma unroll
+                for (int i = 0; i < kStep / 16; ++i)
+                    mma_tmem_a(tmem + which * l.ntok, a_cols + 32 * slot + 8 * i, xd + 2 * i, id, k + i > 0);
+                mma_commit(&sm.a_empty[slot]);
+                if (which == MATS - 1) mma_commit(&sm.x_empty[s]);
+            }
+            mma_commit(&sm.done);
+        }
+    } else {
+        // Unpacking: warps 0 .. 3 and 4 .. 7 take turns, or each takes one of the two matrices
+        const int wg = warp / 4, r = tid & 127, count = kChunkIn / p.group, groups = p.k / p.group;
+        const bool vector = groups % count == 0;
+        const size_t row = min(row0 + r, p.n_out - 1);
+        const uint32_t lanes = (uint32_t)(warp % 4) << 21;        // this warp's lanes of TMEM
+#pragma unroll
+        for (int m = 0; m < MATS; ++m) {
+            const Q4Matrix &w = m ? p.up : p.w;
+            float top = 0.f;
+            const auto see = [&](float s, float o) { top = fmaxf(top, 15.f * fabsf(s) + fabsf(o)); };
+            if (groups % 8 == 0) {
+                for (int i = 0; i < groups; i += 8) {
+                    const uint4 s = *reinterpret_cast<const uint4 *>(w.scales + row * groups + i);
+                    uint4 o = make_uint4(0, 0, 0, 0);
+                    if (OFFSETS) o = *reinterpret_cast<const uint4 *>(w.offsets + row * groups + i);
+                    float fs[8], fo[8];
+                    unpack8(s, fs);
+                    unpack8(o, fo);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) see(fs[e], fo[e]);
+                }
+            } else {
+                for (int i = 0; i < groups; ++i)
+                    see(__bfloat162float(w.scales[row * groups + i]), OFFSETS ? __bfloat162float(w.offsets[row * groups + i]) : 0.f);
+            }
+            // 2^e <= top < 2^(e + 1) goes to [2^-6, 2^-5); nothing, or what is not finite, stays
+            const int e = (int)(__float_as_uint(top) >> 23) - 127;
+            exponent[m] = top > 0.f && e < 128 ? max(e, -120) + 6 : 0;
+        }
+        const int mine = GATED ? wg : 0, f = exponent[mine];
+        const Q4Matrix &w = mine ? p.up : p.w;
+        const float f0 = power_of_two(-f / 2), f1 = power_of_two(-f - -f / 2);
+        ChunkScales next = chunk_scales<OFFSETS>(w, row, groups, chunk0 * count, count, vector);
+        bool gone = false;
+        for (int c = 0; c < chunks; ++c) {
+            const ChunkScales cur = next;
+            if (c + 1 < chunks) next = chunk_scales<OFFSETS>(w, row, groups, (chunk0 + c + 1) * count, count, vector);
+            const int s = c % l.code_stages;
+            mbar_poll(&sm.code_full[s], (c / l.code_stages) & 1, abort);
+            const unsigned char *line = codes + (size_t)(s * MATS + mine) * kCodeBytes + r * 128;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = 4 * c + j;
+                if (k >= steps || (!GATED && (j & 1) != wg)) continue;
+                const int t = GATED ? 2 * k + wg : k, slot = t % kSlots;
+                const float sc = nth_bf16(cur.s, count == 4 ? j : j / 2) * f0 * f1;
+                const float of = OFFSETS ? nth_bf16(cur.o, count == 4 ? j : j / 2) * f0 * f1 : -8.f * sc;
+                const uint32_t s0 = f16_twice(sc * 16777216.f), s1 = f16_twice(sc * 1048576.f), o2 = f16_twice(of);
+                uint32_t v[32];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(line + (((2 * j + h) ^ (r & 7)) << 4));
+                    const uint32_t words[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t a = words[i], b = a >> 8;
+                        v[16 * h + 4 * i] = fma_f16x2(a & 0x000f000fu, s0, o2);
+                        v[16 * h + 4 * i + 1] = fma_f16x2(a & 0x00f000f0u, s1, o2);
+                        v[16 * h + 4 * i + 2] = fma_f16x2(b & 0x000f000fu, s0, o2);
+                        v[16 * h + 4 * i + 3] = fma_f16x2(b & 0x00f000f0u, s1, o2);
+                    }
+                }
+                if (t >= kSlots) {
+                    mbar_poll(&sm.a_empty[slot], (t / kSlots - 1) & 1, abort);
+                    tc_fence_after();
+                }
+                if (gone = __any_sync(0xffffffffu, *abort)) break;
+                tmem_st_row(a_cols + 32 * slot + lanes, v);
+                tc_fence_before();
+                mbar_arrive(&sm.a_full[slot]);
+            }
+            if (gone) break;
+            mbar_arrive(&sm.code_empty[s]);
+        }
+        mbar_poll(&sm.done, 0, abort);
+        tc_fence_after();
+    }
+
+    // Outputs.  Warps 0 .. 3 take the first half of the columns (rows of x), 4 .. 7 the second
+    __syncwarp();
+    const bool good = !__any_sync(0xffffffffu, *abort);
+    const int r = tid & 127, n = row0 + r, half = l.ntok / 2;
+    const uint32_t lanes = (uint32_t)(warp % 4) << 21;
+    const int m_end = min(l.ntok, p.rows - m0);
+    auto write = [&](int m, float y, float z, int ex) {
+        y = ldexpf(y, exponent[0] - ex);
+        if constexpr (GATED) y = ffn_act(y, p.gelu) * ldexpf(z, exponent[MATS - 1] - ex);
+        if (n < p.n_out) static_cast<__nv_bfloat16 *>(p.out)[(size_t)(m0 + m) * p.n_out + n] = __float2bfloat16_rn(y);
+    };
+    float *part = reinterpret_cast<float *>(base);            // [matrix][column][row]: the pipeline is done with this memory
+    if (warp < 8 && good) {
+        grid_dependency_wait();
+        for (int col = warp / 4 * half; col < (warp / 4 + 1) * half; col += 8) {
+            float y[8], z[8];
+            tmem_ld8x2(tmem + col + lanes, tmem + (MATS - 1) * l.ntok + col + lanes, y, z);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (l.cluster > 1) {
+                    part[(col + i) * kRowsA + r] = y[i];
+                    if (GATED) part[(l.ntok + col + i) * kRowsA + r] = z[i];
+                } else if (col + i < m_end) {
+                    write(col + i, y[i], z[i], x_exponents[m0 + col + i]);
+                }
+            }
+        }
+    }
+    if (l.cluster > 1) {
+        cluster_sync();
+        if (warp < 8 && good) {
+            for (int col = 2 * rank + warp / 4; col < m_end; col += 2 * l.cluster) {
+                float y = 0.f, z = 0.f;
+                for (int q = 0; q < l.cluster; ++q) {
+                    y += ld_dsmem_f32(part + col * kRowsA + r, q);
+                    if (GATED) z += ld_dsmem_f32(part + (l.ntok + col) * kRowsA + r, q);
+                }
+                write(col, y, z, x_exponents[m0 + col]);
+            }
+        }
+        cluster_sync();                            // a CTA's sums are read before it is gone
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0 && sm.abort) raise_error(err, kErrTimeout);
+    if (warp == 0) {
+        tmem_relinquish();
+        tmem_dealloc(tmem, l.tmem_cols);
+    }
+}
+
+// Rows of x in fp16, scaled by 2^exponent, each 8 inputs in the order 0 4 1 5 2 6 3 7.  A warp a row.
+__global__ void __launch_bounds__(128) scale_rows_kernel(const __grid_constant__ Q4Problem p, __half *__restrict__ out, int *__restrict__ exponents) {
+    grid_launch_dependents();
+    const int m = blockIdx.x * 4 + threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (m >= p.rows) return;
+    const uint4 *x = reinterpret_cast<const uint4 *>(p.x + (long long)m * p.x_stride);
+    uint32_t top = 0;
+    for (int i = lane; i < p.k / 8; i += 32) top = max(top, amax_bits(x[i]));
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // the largest goes to [2^14, 2^15); a row of zeros, or with what is not finite, stays as it is
+    const int e = (int)(top >> 23) - 127, s = top != 0 && e < 128 ? 14 - e : 0;
+    const float f0 = power_of_two(s / 2), f1 = power_of_two(s - s / 2);
+    if (lane == 0) exponents[m] = s;
+    uint4 *to = reinterpret_cast<uint4 *>(out + (size_t)m * p.k);
+    for (int i = lane; i < p.k / 8; i += 32) {
+        float f[8];
+        unpack8(x[i], f);
+        uint32_t h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const __half2 v = __floats2half2_rn(f[k] * f0 * f1, f[k + 4] * f0 * f1);
+            h[k] = *reinterpret_cast<const uint32_t *>(&v);
+        }
+        to[i] = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+        cudaDriverEntryPointQueryResult q;
+        void *f = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+        return nullptr;
+    }();
+    return fn;
+}
+
+// [rows, bytes of a row] read in boxes of 128 bytes of box_rows rows, 128-byte swizzled.
+bool byte_map(CUtensorMap *m, const void *at, uint64_t rows, uint64_t row_bytes, uint32_t box_rows) {
+    const auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {row_bytes, rows}, strides[1] = {row_bytes};
+    const cuuint32_t box[2] = {128, box_rows}, es[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(at), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int round_up(int a, int b) { return (a + b - 1) / b * b; }
+
+size_t tc_shared(const TcPlan &l, int mats) {
+    const size_t pipeline = (size_t)l.code_stages * mats * kCodeBytes + (size_t)kXStages * l.ntok * 128;
+    const size_t join = l.cluster > 1 ? (size_t)mats * l.ntok * kRowsA * 4 : 0;
+    return 1024 + max(pipeline, join);
+}
+
+// The division that should be done first: waves of CTAs times a CTA's steps, each as long as the product's or the unpacking's
+// part of it takes (cycles), and what a CTA takes besides.
+TcPlan plan_tc(int rows, int n_out, int k, bool gated) {
+    const int mats = gated ? 2 : 1, most = gated ? 192 : 256, sms = multiprocessor_count();
+    const int chunks = (k + kChunkIn - 1) / kChunkIn;
+    TcPlan best{};
+    double least = 1e300;
+    for (int tiles = (rows + most - 1) / most; tiles <= (rows + 15) / 16 && tiles <= 4 * ((rows + most - 1) / most); ++tiles) {
+        for (int cluster = 1; cluster <= 8 && cluster <= chunks; cluster *= 2) {
+            TcPlan l{};
+            l.ntok = round_up((rows + tiles - 1) / tiles, 16);
+            l.m_tiles = (rows + l.ntok - 1) / l.ntok;
+            l.row_tiles = (n_out + kRowsA - 1) / kRowsA;
+            l.cluster = cluster;
+            l.slice = (chunks + cluster - 1) / cluster;
+            if ((long)l.slice * (cluster - 1) >= chunks) continue;            // every CTA has inputs
+            l.code_stages = gated ? 3 : 4;
+            l.tmem_cols = 32;
+            while (l.tmem_cols < mats * l.ntok + 32 * kSlots) l.tmem_cols *= 2;
+            if (tc_shared(l, mats) > 226 * 1024) continue;
+            const double waves = ceil((double)l.row_tiles * l.m_tiles * cluster / sms);
+            const double time = waves * (l.slice * 4.0 * mats * max(l.ntok, 150) + 5000 + (cluster > 1 ? 1500 + 10.0 * l.ntok : 0));
+            if (time < least) least = time, best = l;
+        }
+    }
+    return best;
+}
+
+template <bool GATED, bool OFFSETS>
+cudaError_t launch_tc(const Q4Problem &p, const TcPlan &l, const CUtensorMap &codes, const CUtensorMap &up, const CUtensorMap &x,
+                      const int *exponents) {
+    const auto fn = q4_tc_kernel<GATED, OFFSETS>;
+    const size_t smem = tc_shared(l, GATED ? 2 : 1);
+    static std::atomic<bool> ready[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= kMaxDevices || !ready[dev].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - (int)sizeof(TcBars) - 64);
+        if (e != cudaSuccess) return e;
+        if (dev < kMaxDevices) ready[dev].store(true, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((long)l.row_tiles * l.m_tiles * l.cluster));
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = p.stream;
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = l.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = l.cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, fn, p, l, codes, up, x, exponents, error_word());
+}
+
+size_t exponent_bytes(int rows) { return ((size_t)rows * 4 + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t q4_tc_workspace_bytes(int rows, int k) { return exponent_bytes(rows) + (size_t)rows * k * 2; }
+
+cudaError_t launch_q4_tc(const Q4Problem &p) {
+    int *exponents = static_cast<int *>(p.workspace);
+    __half *x16 = reinterpret_cast<__half *>(static_cast<uint8_t *>(p.workspace) + exponent_bytes(p.rows));
+    const TcPlan l = plan_tc(p.rows, p.n_out, p.k, p.gated);
+    CUtensorMap codes, up, x;
+    if (!byte_map(&codes, p.w.codes, p.n_out, p.k / 2, kRowsA) || !byte_map(&x, x16, p.rows, (uint64_t)p.k * 2, l.ntok)) return cudaErrorInvalidValue;
+    if (!p.gated) up = codes;
+    else if (!byte_map(&up, p.up.codes, p.n_out, p.k / 2, kRowsA)) return cudaErrorInvalidValue;
+    scale_rows_kernel<<<(unsigned)((p.rows + 3) / 4), 128, 0, p.stream>>>(p, x16, exponents);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    if (p.gated) return p.w.offsets ? launch_tc<true, true>(p, l, codes, up, x, exponents) : launch_tc<true, false>(p, l, codes, up, x, exponents);
+    return p.w.offsets ? launch_tc<false, true>(p, l, codes, up, x, exponents) : launch_tc<false, false>(p, l, codes, up, x, exponents);
+}
+
+}  // namespace gdn

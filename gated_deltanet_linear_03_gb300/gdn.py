@@ -27,7 +27,7 @@ EXPORTS = ("gdn_prefill", "gdn_prefill_chunked_phase", "gdn_prefill_workspace_si
            "gdn_prefill_host", "gdn_prefill_host_staging_size", "gdn_selftest_bounded_wait",
            "gdn_prefill_pass_plan", "gdn_kv_append", "gdn_kv_read", "gdn_attend", "gdn_attend_workspace_size",
            "gdn_block_norm", "gdn_short_conv", "gdn_ssm_scan", "gdn_ssm_scan_workspace_size", "gdn_q4_linear",
-           "gdn_q4_gated")
+           "gdn_q4_gated", "gdn_q4_workspace_size")
 NOALLOC_SCRATCH_BYTES = 97 * 1024 * 1024
 PHASE = {"prep": 1, "pass": 2}
 
@@ -105,9 +105,11 @@ def bind(path: str) -> ctypes.CDLL:
     lib.gdn_ssm_scan_workspace_size.restype = Z
     lib.gdn_ssm_scan.argtypes = [I, I, I, I, I, P, L, P, L, P, P, L, P, L, P, P, L, P, I, P, I, P, P, P, I, P, I, P, Z, P]
     lib.gdn_ssm_scan.restype = I
-    lib.gdn_q4_linear.argtypes = [I, I, I, I, P, L, P, P, P, P, I, P]
+    lib.gdn_q4_linear.argtypes = [I, I, I, I, P, L, P, P, P, P, I, P, Z, P]
     lib.gdn_q4_linear.restype = I
-    lib.gdn_q4_gated.argtypes = [I, I, I, I, P, L, P, P, P, P, P, P, I, P, I, P]
+    lib.gdn_q4_gated.argtypes = [I, I, I, I, P, L, P, P, P, P, P, P, I, P, I, P, Z, P]
+    lib.gdn_q4_workspace_size.argtypes = [I, I, I, I, I, ctypes.POINTER(I)]
+    lib.gdn_q4_workspace_size.restype = Z
     lib.gdn_q4_gated.restype = I
     return lib
 

@@ -10,12 +10,14 @@ enqueues work on the current stream of the tensors' device (or ``stream``).
 """
 from __future__ import annotations
 
+import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import torch
 
 from .attn import _contiguous, _device, _empty, _int32, _launch, _refuse
-from .gdn import DTYPE, load_library
+from .gdn import DTYPE, GDN_OK, GdnError, load_library
 
 FFN_ACT = {"silu": 0, "gelu": 1}
 _BF16, _U8 = torch.bfloat16, torch.uint8
@@ -110,21 +112,45 @@ def _output(x, n_out, out, out_dtype, index, stream):
     return out, code
 
 
+@functools.lru_cache(maxsize=4096)
+def workspace_size(rows: int, n_out: int, k: int, group: int, out_dtype=torch.bfloat16) -> int:
+    """Bytes of workspace that :func:`q4_linear` and :func:`q4_gated` need for this problem (``gdn_q4_workspace_size``)."""
+    st = ctypes.c_int(0)
+    need = load_library().gdn_q4_workspace_size(_int32(rows), n_out, k, group, DTYPE[out_dtype], st)
+    if st.value != GDN_OK:
+        raise GdnError(st.value, "gdn_q4_workspace_size")
+    return int(need)
+
+
+def _workspace(workspace, rows, n_out, k, group, out, index, stream):
+    """(address, bytes, what keeps the memory alive): few rows need none."""
+    if workspace is not None:
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the other tensors' device")
+    else:
+        need = workspace_size(rows, n_out, k, group, out.dtype)
+        if need == 0:
+            return 0, 0, None
+        workspace = _empty(stream, need, _U8, out.device)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
 def q4_linear(x: torch.Tensor, w: Q4, *, out: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
-              stream=None) -> torch.Tensor:
+              workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Run ``gdn_q4_linear``: ``x`` (bf16 [..., k]) times the transpose of ``w``: [..., n_out] in bf16 or fp32."""
     lib = load_library()
     dev = _device(x, "x")
     stride, rows, k = _rows(x, dev)
     cp, sp, fp, n_out, group = _matrix("w", w, k, dev)
     out, code = _output(x, n_out, out, out_dtype, dev, stream)
+    wsp, ws_bytes, _keep = _workspace(workspace, rows, n_out, k, group, out, dev, stream)
     _launch(lib.gdn_q4_linear, "gdn_q4_linear", dev, stream, _int32(rows), n_out, k, group, x.data_ptr(), stride, cp, sp, fp,
-            out.data_ptr(), code)
+            out.data_ptr(), code, wsp, ws_bytes)
     return out
 
 
 def q4_gated(x: torch.Tensor, gate: Q4, up: Q4, *, act: str = "silu", out: Optional[torch.Tensor] = None,
-             out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+             out_dtype=torch.bfloat16, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Run ``gdn_q4_gated``: ``act(x gate^T) * (x up^T)`` for two matrices of one shape ([n_out, k], one group size, offsets
     in both or neither); ``act`` is "silu" or "gelu" (its tanh form)."""
     lib = load_library()
@@ -138,6 +164,7 @@ def q4_gated(x: torch.Tensor, gate: Q4, up: Q4, *, act: str = "silu", out: Optio
     if act_code is None:
         raise ValueError(f"act must be one of {sorted(FFN_ACT)}")
     out, code = _output(x, n_out, out, out_dtype, dev, stream)
+    wsp, ws_bytes, _keep = _workspace(workspace, rows, n_out, k, group, out, dev, stream)
     _launch(lib.gdn_q4_gated, "gdn_q4_gated", dev, stream, _int32(rows), n_out, k, group, x.data_ptr(), stride, gc, gs, go,
-            uc, us, uo, act_code, out.data_ptr(), code)
+            uc, us, uo, act_code, out.data_ptr(), code, wsp, ws_bytes)
     return out

@@ -597,17 +597,25 @@ GDN_API gdn_status gdn_ssm_scan(int n_seqs, int total_tokens, int channels, int 
  *   scales, offsets    bf16 [n_out, k / group]; offsets may be NULL
  *   out                [rows, n_out], dtype out_dtype
  *
- * Codes enter the products exactly; products and sums are fp32, scaled group by group; out is rounded once.  A row of x
- * with an infinity or NaN gives outputs that are not finite.
+ *   workspace          at least gdn_q4_workspace_size() bytes for the same sizes (0 for few rows, and for fp32 outputs),
+ *                      256-byte aligned; contents do not matter
+ *
+ * Products and sums are fp32; out is rounded once.  With fp32 outputs, or up to 16 rows, codes enter the products exactly
+ * and scales and offsets meet the sums group by group.  Otherwise the weights are rounded to fp16, by 2^-11 of
+ * themselves and 2^-19 of their row's largest 15 |scale| + |offset| at most, and a row of x loses what is below 2^-40 of its
+ * largest.  A row of x with an infinity or NaN gives outputs that are not finite, and no other row does.
  */
+GDN_API size_t gdn_q4_workspace_size(int rows, int n_out, int k, int group, int out_dtype, gdn_status *status);
+
 GDN_API gdn_status gdn_q4_linear(int rows, int n_out, int k, int group, const void *x, long long x_stride,
                                  const void *codes, const void *scales, const void *offsets, void *out, int out_dtype,
-                                 void *stream);
+                                 void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * gdn_q4_gated: the first half of a gated feed-forward block, y = act(x Wg^T) * (x Wu^T), both matrices [n_out, k] in
- * the layout of gdn_q4_linear (offsets of both or of neither).  Both products, the activation and their product are
- * one kernel; everything up to the one rounding of out (bf16 or fp32 [rows, n_out]) is fp32.
+ * the layout of gdn_q4_linear (offsets of both or of neither), with its roundings and its workspace.  Both products, the
+ * activation and their product are one kernel; everything behind the products up to the one rounding of out (bf16 or
+ * fp32 [rows, n_out]) is fp32.
  *   act                GDN_FFN_SILU (u / (1 + e^-u)) or GDN_FFN_GELU (u/2 (1 + tanh(sqrt(2/pi) (u + 0.044715 u^3))))
  */
 typedef enum {
@@ -618,7 +626,7 @@ typedef enum {
 GDN_API gdn_status gdn_q4_gated(int rows, int n_out, int k, int group, const void *x, long long x_stride,
                                 const void *gate_codes, const void *gate_scales, const void *gate_offsets,
                                 const void *up_codes, const void *up_scales, const void *up_offsets, int act,
-                                void *out, int out_dtype, void *stream);
+                                void *out, int out_dtype, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Static, human-readable name of a status code. */
 GDN_API const char *gdn_status_string(gdn_status status);

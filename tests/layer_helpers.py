@@ -88,23 +88,29 @@ def q4_values(w):
     return ((q - 8) * s if offsets is None else q * s + offsets.double()[..., None]).flatten(1)
 
 
-def q4_product(x, w):
+def q4_product(x, w, rounded=False):
     """(y, bound): products exact, their sums in 32 bits.  A group of 64 is summed by four matrix instructions, each an
     aligned sum that may cut what is below 2^-23 of its largest term, then scaled and added; the offset's part likewise:
-    (16 + 4 groups of 64) 2^-23 of the sum of the magnitudes that are added."""
+    (16 + 4 groups of 64) 2^-23 of the sum of the magnitudes that are added.  With weights rounded to fp16: 2^-11 of each, and
+    2^-19 of the row's largest 15 |scale| + |offset|, which holds for an input that falls below 2^-40 of its row's largest, too."""
     codes, scales, offsets = w
     n, half = codes.shape
     k, groups = 2 * half, scales.shape[1]
     q = torch.stack([codes % 16, codes // 16], dim=-1).view(n, k).double()
     s = scales.double().repeat_interleave(k // groups, dim=1).abs()
     o = 8 * s if offsets is None else offsets.double().repeat_interleave(k // groups, dim=1).abs()
-    y = x.double() @ q4_values(w).T
-    return y, (16 + 4 * (k // 64)) * 2.0 ** -23 * (x.double().abs() @ (q * s + o).T)
+    v, mag = q4_values(w), x.double().abs()
+    bound = (16 + 4 * (k // 64)) * 2.0 ** -23 * (mag @ (q * s + o).T)
+    if rounded:
+        top = (15 * s + (0 if offsets is None else o)).amax(dim=1)
+        bound = bound + 2.0 ** -11 * (mag @ v.abs().T) + 2.0 ** -19 * mag.sum(-1, keepdim=True) * top
+        bound = bound + 2.0 ** -40 * mag.amax(-1, keepdim=True) * v.abs().sum(-1)
+    return x.double() @ v.T, bound
 
 
-def gated(x, gate, up, act):
+def gated(x, gate, up, act, rounded=False):
     """(y, bound) of act(x gate) * (x up): slopes of both activations are below 1.13."""
-    (a, ea), (b, eb) = q4_product(x, gate), q4_product(x, up)
+    (a, ea), (b, eb) = q4_product(x, gate, rounded), q4_product(x, up, rounded)
     f = a * torch.sigmoid(a) if act == "silu" else 0.5 * a * (1 + torch.tanh(math.sqrt(2 / math.pi) * (a + 0.044715 * a ** 3)))
     y = f * b
     return y, 1.13 * ea * (b.abs() + eb) + f.abs() * eb + 2.0 ** -20 * y.abs() + 2.0 ** -20 * (a.abs() * b.abs()).clamp_max(1e-6)

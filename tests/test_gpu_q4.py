@@ -6,6 +6,7 @@ import layer_helpers as ref
 from layer_helpers import BF, F32
 
 pytestmark = pytest.mark.gpu
+FEW = 16                 # rows of x up to which codes enter the products exactly
 
 
 @pytest.fixture(scope="module")
@@ -34,17 +35,15 @@ def rows_of(rows, k, seed):
                                           (17, 129, 512), (33, 2047, 1024), (65, 200, 384), (130, 300, 2176)])
 def test_sizes(linear, rows, n_out, k, group, offsets):
     w, x = matrix(linear, n_out, k, group, offsets, seed=k), rows_of(rows, k, seed=rows)
-    y, e = ref.q4_product(x, w)
-    ref.check(linear.q4_linear(x, w, out_dtype=F32), y, e)
-    ref.check(linear.q4_linear(x, w), y, e)
+    ref.check(linear.q4_linear(x, w, out_dtype=F32), *ref.q4_product(x, w))
+    ref.check(linear.q4_linear(x, w), *ref.q4_product(x, w, rounded=rows > FEW))
 
 
 @pytest.mark.parametrize("rows", [1, 3, 8, 12, 16, 24, 32, 40, 64, 100, 509])
 @pytest.mark.parametrize("n_out,k", [(4100, 4096), (520, 192), (96, 8192)])
 def test_rows(linear, rows, n_out, k):
     w, x = matrix(linear, n_out, k, 64, True, seed=n_out), rows_of(rows, k, seed=rows)
-    y, e = ref.q4_product(x, w)
-    ref.check(linear.q4_linear(x, w), y, e)
+    ref.check(linear.q4_linear(x, w), *ref.q4_product(x, w, rounded=rows > FEW))
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
@@ -54,16 +53,15 @@ def test_rows(linear, rows, n_out, k):
 def test_gated(linear, rows, n_out, k, group, offsets, act):
     gate, up = (matrix(linear, n_out, k, group, offsets, seed=s) for s in (1, 2))
     x = rows_of(rows, k, seed=rows)
-    y, e = ref.gated(x, gate, up, act)
-    ref.check(linear.q4_gated(x, gate, up, act=act, out_dtype=F32), y, e)
-    ref.check(linear.q4_gated(x, gate, up, act=act), y, e)
+    ref.check(linear.q4_gated(x, gate, up, act=act, out_dtype=F32), *ref.gated(x, gate, up, act))
+    ref.check(linear.q4_gated(x, gate, up, act=act), *ref.gated(x, gate, up, act, rounded=rows > FEW))
 
 
 @pytest.mark.parametrize("rows,k", [(1, 16384), (40, 16384), (64, 12288), (3, 65536), (70, 65536)])
 def test_long_rows(linear, rows, k):
     w, x = matrix(linear, 40, k, 128, True, seed=1), rows_of(rows, k, seed=2)
-    y, e = ref.q4_product(x, w)
-    ref.check(linear.q4_linear(x, w, out_dtype=F32), y, e)
+    ref.check(linear.q4_linear(x, w, out_dtype=F32), *ref.q4_product(x, w))
+    ref.check(linear.q4_linear(x, w), *ref.q4_product(x, w, rounded=rows > FEW))
 
 
 def test_a_vocabulary(linear):
@@ -89,8 +87,7 @@ def test_beyond_32_bit_offsets(linear):
     x = rows_of(5000, 128, seed=6)
     out = linear.q4_linear(x, small)
     part = linear.Q4(small.codes[-300:], small.scales[-300:])
-    y, e = ref.q4_product(x[-70:], part)
-    ref.check(out[-70:, -300:], y, e)
+    ref.check(out[-70:, -300:], *ref.q4_product(x[-70:], part, rounded=True))
 
 
 def test_slices_shapes_and_outputs(linear):
@@ -125,8 +122,28 @@ def test_large_and_small_values(linear):
     """Activations up to 1e30 and down to 1e-30 in one call: every row keeps its own precision."""
     w, x = matrix(linear, 300, 512, 64, True, seed=11), rows_of(40, 512, seed=12).float()
     x = (x * 10.0 ** torch.linspace(-30, 30, 40, device="cuda")[:, None]).to(BF)
-    y, e = ref.q4_product(x, w)
-    ref.check(linear.q4_linear(x, w, out_dtype=F32), y, e)
+    ref.check(linear.q4_linear(x, w, out_dtype=F32), *ref.q4_product(x, w))
+    ref.check(linear.q4_linear(x, w), *ref.q4_product(x, w, rounded=True))
+
+
+@pytest.mark.parametrize("rows", [3, 50])
+def test_weights_of_very_different_sizes(linear, rows):
+    """Rows of weights up to 1e30 and down to 1e-30, and groups in a row a million times smaller than others."""
+    w, x = matrix(linear, 200, 1024, 64, True, seed=21), rows_of(rows, 1024, seed=22)
+    f = 10.0 ** torch.linspace(-30, 30, 200, device="cuda")[:, None] * 10.0 ** (-6 * torch.rand(200, 16, device="cuda"))
+    w = linear.Q4(w.codes, (w.scales * f).to(BF), (w.offsets * f).to(BF))
+    ref.check(linear.q4_linear(x, w, out_dtype=F32), *ref.q4_product(x, w))
+    ref.check(linear.q4_linear(x, w), *ref.q4_product(x, w, rounded=rows > FEW))
+
+
+def test_rows_of_zeros(linear):
+    w, x = matrix(linear, 200, 512, 64, True, seed=23), rows_of(40, 512, seed=24)
+    x[3] = 0
+    zero = linear.Q4(w.codes, w.scales.clone(), w.offsets.clone())
+    zero.scales[7], zero.offsets[7] = 0, 0
+    out = linear.q4_linear(x, zero)
+    assert (out[3] == 0).all() and (out[:, 7] == 0).all()
+    ref.check(out, *ref.q4_product(x, zero, rounded=True))
 
 
 @pytest.mark.parametrize("offsets", [True, False])

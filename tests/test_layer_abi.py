@@ -79,12 +79,13 @@ def test_scan_workspace_refuses(lib, kw, status):
 
 def q4(lib, gated, **kw):
     a = dict(rows=3, n=40, k=256, group=64, x=at(0), xs=256, codes=at(1), scales=at(2), offsets=at(3), codes2=at(4), scales2=at(5),
-             offsets2=at(6), act=0, out=at(7), odt=0)
+             offsets2=at(6), act=0, out=at(7), odt=0, ws=at(8), wsb=32 * MB)
     a.update(kw)
     first = (a["rows"], a["n"], a["k"], a["group"], P(a["x"]), a["xs"], P(a["codes"]), P(a["scales"]), P(a["offsets"]))
     if gated:
-        return lib.gdn_q4_gated(*first, P(a["codes2"]), P(a["scales2"]), P(a["offsets2"]), a["act"], P(a["out"]), a["odt"], None)
-    return lib.gdn_q4_linear(*first, P(a["out"]), a["odt"], None)
+        return lib.gdn_q4_gated(*first, P(a["codes2"]), P(a["scales2"]), P(a["offsets2"]), a["act"], P(a["out"]), a["odt"], P(a["ws"]),
+                                a["wsb"], None)
+    return lib.gdn_q4_linear(*first, P(a["out"]), a["odt"], P(a["ws"]), a["wsb"], None)
 
 
 @pytest.mark.parametrize("gated", [False, True])
@@ -94,10 +95,21 @@ def q4(lib, gated, **kw):
     (dict(rows=2 ** 31 - 1), UNSUPPORTED), (dict(n=2 ** 31 - 1), UNSUPPORTED), (dict(x=None), INVALID), (dict(codes=None), INVALID),
     (dict(scales=None), INVALID), (dict(out=None), INVALID), (dict(xs=248), INVALID), (dict(xs=260), ALIGNMENT),
     (dict(x=at(0) + 8), ALIGNMENT), (dict(codes=at(1) + 8), ALIGNMENT), (dict(scales=at(2) + 2), ALIGNMENT),
-    (dict(offsets=at(3) + 2), ALIGNMENT), (dict(out=at(7) + 2), ALIGNMENT), (dict(out=at(0)), INVALID), (dict(out=at(2) + 16), INVALID)])
+    (dict(offsets=at(3) + 2), ALIGNMENT), (dict(out=at(7) + 2), ALIGNMENT), (dict(out=at(0)), INVALID), (dict(out=at(2) + 16), INVALID),
+    (dict(rows=100, ws=None), WORKSPACE), (dict(rows=100, wsb=100 * 256 * 2), WORKSPACE), (dict(rows=100, ws=at(8) + 16), ALIGNMENT),
+    (dict(rows=100, ws=at(1)), INVALID)])
 def test_q4_refuses(lib, gated, kw, status):
     assert q4(lib, gated, **kw) == status
     assert q4(lib, gated, rows=0) == OK
+
+
+def test_q4_workspace(lib):
+    st = ctypes.c_int(-1)
+    size = lambda *a: (lib.gdn_q4_workspace_size(*a, st), st.value)  # noqa: E731
+    assert size(1, 40, 256, 64, 0) == (0, OK) and size(1000, 40, 256, 64, 1) == (0, OK)
+    assert size(100, 40, 256, 64, 0)[0] >= 100 * 256 * 2
+    for bad, status in (((-1, 40, 256, 64, 0), INVALID), ((1, 40, 250, 64, 0), UNSUPPORTED), ((1, 40, 256, 64, 2), UNSUPPORTED)):
+        assert size(*bad) == (0, status)
 
 
 @pytest.mark.parametrize("kw,status", [(dict(act=2), UNSUPPORTED), (dict(codes2=None), INVALID), (dict(scales2=None), INVALID),
