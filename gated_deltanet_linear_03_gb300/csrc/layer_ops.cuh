@@ -77,10 +77,18 @@ size_t q4_workspace_bytes(int rows, int n_out, int k, int out_f32);
 cudaError_t launch_q4_tc(const Q4Problem &p);
 size_t q4_tc_workspace_bytes(int rows, int k);
 
-// The activation of a gated feed-forward block.  gelu: 1 + tanh(v) = 2 / (1 + e^-2v), without the difference of nearly equal numbers.
-__device__ __forceinline__ float ffn_act(float u, int gelu) {
-    const float v = gelu ? 1.5957691216057308f * (u + 0.044715f * u * u * u) : u;
-    return u / (1.f + expf(-v));
+// The activation of a gated feed-forward block: u / (1 + e^-v), with v = u or, for gelu, 2 sqrt(2/pi) (u + 0.044715 u^3), as
+// 1 + tanh(w) = 2 / (1 + e^-2w) has no difference of nearly equal numbers.
+__device__ __forceinline__ float ffn_argument(float u, int gelu) {
+    return gelu ? 1.5957691216057308f * (u + 0.044715f * u * u * u) : u;
+}
+__device__ __forceinline__ float ffn_act(float u, int gelu) { return u / (1.f + expf(-ffn_argument(u, gelu))); }
+// The same to 2^-19 for |v| < 32, where it is rounded to bf16 next.
+__device__ __forceinline__ float ffn_act_fast(float u, int gelu) {
+    float e, q;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * ffn_argument(u, gelu)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.f + e));
+    return u * q;
 }
 
 }  // namespace gdn

@@ -26,23 +26,31 @@ namespace {
 using namespace sm100;
 
 constexpr int kRowsA = 128;               // weight rows of a CTA
-constexpr int kStep = 64;                 // inputs of a step of the product
+constexpr int kBlockIn = 64;              // inputs that a thread unpacks at once: 32 columns of TMEM
 constexpr int kChunkIn = 256;             // inputs of a stage of codes
-constexpr int kSlots = 4;                 // steps of the first operand in TMEM, 32 columns each
-constexpr int kTcThreads = 352;           // 8 warps that unpack, one each for TMA of codes, TMA of x, and the product
 constexpr int kCodeBytes = kRowsA * kChunkIn / 2;
-constexpr int kXStages = 4;
+constexpr int kTcThreads = 384;           // 8 warps that unpack, one each for TMA of codes and of x, one or two for the products
+constexpr int kMaxStages = 4;
+
+// A step is what one wait of the thread that issues the products is for.  Its instructions between two products, a few dozen in a
+// row, take longer than a product with few columns: with one matrix a step is two blocks, which the two halves of the unpacking warps
+// share; of two matrices each has its half of the warps, its own issuing warp, and steps of one block.
+template <bool GATED>
+struct Tc {
+    static constexpr int MATS = GATED ? 2 : 1, BLOCKS = GATED ? 1 : 2, STEP = BLOCKS * kBlockIn;
+};
 
 struct TcPlan {
     int ntok, m_tiles, row_tiles, cluster;
     int slice;                            // chunks of inputs of one CTA
-    int code_stages, tmem_cols;
+    int code_stages, x_stages, tmem_cols; // (columns: the sums, and two steps of each matrix, 128)
 };
 
 struct TcBars {
-    uint64_t code_full[4], code_empty[4], x_full[kXStages], x_empty[kXStages], a_full[kSlots], a_empty[kSlots], done;
+    uint64_t code_full[kMaxStages], code_empty[kMaxStages], x_full[kMaxStages], x_empty[kMaxStages], a_full[2][2], a_empty[2][2], done;
     uint32_t tmem;
     int abort;
+    float2 undo[256];                     // of each row of x: the two halves of 2^-exponent
 };
 
 // 32 lanes x 32 columns of 32 bits, a lane a thread, and the wait for them.
@@ -106,36 +114,95 @@ __device__ __forceinline__ float nth_bf16(const uint2 &v, int i) {
     return i & 1 ? bf16_hi(w) : bf16_lo(w);
 }
 
+// A wait of a whole warp in which one lane asks: 256 lanes that ask keep the shared-memory pipe from the threads that issue (a
+// poll that finds its phase complete then took those 230 cycles).
+__device__ __forceinline__ void warp_poll(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    if (threadIdx.x % 32 == 0) mbar_poll(bar, parity, abort);
+    __syncwarp();
+}
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) mbar_arrive(bar);
+}
+
+// The largest 15 |scale| + |offset| of a row.
+template <bool OFFSETS>
+__device__ __forceinline__ float largest(const Q4Matrix &w, size_t row, int groups) {
+    float top = 0.f;
+    const __nv_bfloat16 *s = w.scales + row * groups, *o = OFFSETS ? w.offsets + row * groups : nullptr;
+    if (groups % 8 != 0) {
+        for (int i = 0; i < groups; ++i)
+            top = fmaxf(top, 15.f * fabsf(__bfloat162float(s[i])) + (OFFSETS ? fabsf(__bfloat162float(o[i])) : 0.f));
+        return top;
+    }
+    for (int i = 0; i < groups; i += 32) {               // reads of four pieces are in flight together
+        uint4 vs[4], vo[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const bool there = i + 8 * q < groups;
+            vs[q] = vo[q] = make_uint4(0, 0, 0, 0);
+            if (there) vs[q] = *reinterpret_cast<const uint4 *>(s + i + 8 * q);
+            if (OFFSETS && there) vo[q] = *reinterpret_cast<const uint4 *>(o + i + 8 * q);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float fs[8], fo[8];
+            unpack8(vs[q], fs);
+            unpack8(vo[q], fo);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, 15.f * fabsf(fs[e]) + fabsf(fo[e]));
+        }
+    }
+    return top;
+}
+
 template <bool GATED, bool OFFSETS>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(kTcThreads, 2)
 q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan l, const __grid_constant__ CUtensorMap code_map,
              const __grid_constant__ CUtensorMap up_map, const __grid_constant__ CUtensorMap x_map, const int *__restrict__ x_exponents,
              unsigned int *err) {
-    constexpr int MATS = GATED ? 2 : 1;
+    using T = Tc<GATED>;
+    constexpr int MATS = T::MATS;
     extern __shared__ unsigned char raw[];
     __shared__ TcBars sm;
     unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     unsigned char *codes = base, *xs = base + (size_t)l.code_stages * MATS * kCodeBytes;
-    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int rank = l.cluster > 1 ? (int)cluster_ctarank() : 0, unit = blockIdx.x / l.cluster;
     const int row0 = unit / l.m_tiles * kRowsA, m0 = unit % l.m_tiles * l.ntok;
     const int chunk0 = rank * l.slice, k0 = chunk0 * kChunkIn;
-    const int steps = min(l.slice * (kChunkIn / kStep), (p.k - k0) / kStep), chunks = (steps + 3) / 4;       // at least one of each
-    const int x_bytes = l.ntok * 128;
+    const int blocks = min(l.slice * (kChunkIn / kBlockIn), (p.k - k0) / kBlockIn);                          // at least one
+    const int steps = (blocks + T::BLOCKS - 1) / T::BLOCKS, chunks = (blocks + 3) / 4;
+    const int x_block = l.ntok * 128;                   // bytes of a block of x
+    const int r = tid & 127, groups = p.k / p.group;
+    const size_t row = min(row0 + r, p.n_out - 1);
 
-    if (warp == 0) tmem_alloc(&sm.tmem, l.tmem_cols);
-    if (tid == 32) {
-        for (int i = 0; i < 4; ++i) {
+    if (warp == 8) tmem_alloc(&sm.tmem, l.tmem_cols);
+    if (warp == 9 && elect_one()) {
+        for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(&sm.code_full[i], 1);
-            mbar_init(&sm.code_empty[i], 256);
+            mbar_init(&sm.code_empty[i], 8);
             mbar_init(&sm.x_full[i], 1);
-            mbar_init(&sm.x_empty[i], 1);
-            mbar_init(&sm.a_full[i], 128);
-            mbar_init(&sm.a_empty[i], 1);
+            mbar_init(&sm.x_empty[i], MATS);
         }
-        mbar_init(&sm.done, 1);
+        for (int i = 0; i < 2; ++i)
+            for (int k = 0; k < 2; ++k) {
+                mbar_init(&sm.a_full[i][k], GATED ? 4 : 8);
+                mbar_init(&sm.a_empty[i][k], 1);
+            }
+        mbar_init(&sm.done, MATS);
         sm.abort = 0;
         fence_mbar_init();
+    }
+    int exponent[MATS] = {};                    // of this thread's weight rows: W is scaled by 2^-exponent
+    if (warp < 8) {
+#pragma unroll
+        for (int m = 0; m < MATS; ++m) {
+            // 2^e <= top < 2^(e + 1) goes to [2^-6, 2^-5); nothing, or what is not finite, stays
+            const float top = largest<OFFSETS>(m ? p.up : p.w, row, groups);
+            const int e = (int)(__float_as_uint(top) >> 23) - 127;
+            exponent[m] = top > 0.f && e < 128 ? max(e, -120) + 6 : 0;
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -143,141 +210,142 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
     const uint32_t tmem = sm.tmem, a_cols = tmem + MATS * l.ntok;
     volatile int *abort = &sm.abort;
 
-    int exponent[MATS] = {};                    // of this thread's weight rows: W is scaled by 2^-exponent
     if (warp == 8) {
-        if (lane == 0) {
+        if (elect_one()) {
+            int s = 0, phase = 1;               // (the first round finds every stage free)
             for (int c = 0; c < chunks; ++c) {
-                const int s = c % l.code_stages;
-                if (c >= l.code_stages) mbar_poll(&sm.code_empty[s], (c / l.code_stages - 1) & 1, abort);
+                mbar_poll(&sm.code_empty[s], phase, abort);
                 if (*abort) break;
                 mbar_arrive_expect_tx(&sm.code_full[s], MATS * kCodeBytes);
                 unsigned char *to = codes + (size_t)s * MATS * kCodeBytes;
                 tma_load_2d(to, &code_map, &sm.code_full[s], (k0 + c * kChunkIn) / 2, row0);
                 if (GATED) tma_load_2d(to + kCodeBytes, &up_map, &sm.code_full[s], (k0 + c * kChunkIn) / 2, row0);
+                if (++s == l.code_stages) s = 0, phase ^= 1;
             }
         }
     } else if (warp == 9) {
-        if (lane == 0) {
+        if (elect_one()) {
             grid_dependency_wait();             // the kernel before this one scales x
+            int s = 0, phase = 1;
             for (int t = 0; t < steps; ++t) {
-                const int s = t % kXStages;
-                if (t >= kXStages) mbar_poll(&sm.x_empty[s], (t / kXStages - 1) & 1, abort);
+                mbar_poll(&sm.x_empty[s], phase, abort);
                 if (*abort) break;
-                mbar_arrive_expect_tx(&sm.x_full[s], x_bytes);
-                tma_load_2d(xs + (size_t)s * x_bytes, &x_map, &sm.x_full[s], 2 * (k0 + t * kStep), m0);     // (the map counts bytes)
+                const int n = min(T::BLOCKS, blocks - t * T::BLOCKS);
+                mbar_arrive_expect_tx(&sm.x_full[s], n * x_block);
+                for (int i = 0; i < n; ++i)     // (the map counts bytes)
+                    tma_load_2d(xs + (size_t)(s * T::BLOCKS + i) * x_block, &x_map, &sm.x_full[s], 2 * (k0 + t * T::STEP + i * kBlockIn), m0);
+                if (++s == l.x_stages) s = 0, phase ^= 1;
             }
         }
-    } else if (warp == 10) {
-        if (lane == 0) {
-            const uint32_t id = idesc_f16_f32(kRowsA, l.ntok, false, false);
-            for (int t = 0; t < steps * MATS; ++t) {
-                const int k = t / MATS, which = t % MATS, slot = t % kSlots, s = k % kXStages;
-                if (which == 0) mbar_poll(&sm.x_full[s], (k / kXStages) & 1, abort);
-                mbar_poll(&sm.a_full[slot], (t / kSlots) & 1, abort);
+    } else if (warp >= 10) {
+        const int which = warp - 10;
+        if (which < MATS && elect_one()) {
+            const uint32_t id = idesc_f16_f32(kRowsA, l.ntok, false, false), d = tmem + which * l.ntok, a = a_cols + 64 * which;
+            const uint64_t first = smem_desc(smem_u32(xs), 16, 1024, kLayoutSwizzle128B);
+            int s = 0, phase = 0;
+            uint64_t xd = first;
+            for (int t = 0; t < steps; ++t) {
+                const int slot = t & 1;
+                mbar_poll(&sm.x_full[s], phase, abort);
+                mbar_poll(&sm.a_full[which][slot], (t >> 1) & 1, abort);
                 if (*abort) break;
                 tc_fence_after();
-                const uint64_t xd = smem_desc(smem_u32(xs) + s * x_bytes, 16, 1024, kLayoutSwizzle128B);
+                const uint32_t as = a + T::BLOCKS * 32 * slot;
+                if (t == 0) mma_tmem_a(d, as, xd, id, 0);
+                else mma_tmem_a(d, as, xd, id, 1);
 #pragma unroll
-                for (int i = 0; i < kStep / 16; ++i)
-                    mma_tmem_a(tmem + which * l.ntok, a_cols + 32 * slot + 8 * i, xd + 2 * i, id, k + i > 0);
-                mma_commit(&sm.a_empty[slot]);
-                if (which == MATS - 1) mma_commit(&sm.x_empty[s]);
+                for (int i = 1; i < 4; ++i) mma_tmem_a(d, as + 8 * i, xd + 2 * i, id, 1);
+                if (T::BLOCKS == 2 && 2 * t + 1 < blocks) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mma_tmem_a(d, as + 32 + 8 * i, xd + (x_block >> 4) + 2 * i, id, 1);
+                }
+                mma_commit(&sm.a_empty[which][slot]);
+                mma_commit(&sm.x_empty[s]);
+                xd += T::BLOCKS * (x_block >> 4);
+                if (++s == l.x_stages) s = 0, phase ^= 1, xd = first;
             }
             mma_commit(&sm.done);
         }
     } else {
-        // Unpacking: warps 0 .. 3 and 4 .. 7 take turns, or each takes one of the two matrices
-        const int wg = warp / 4, r = tid & 127, count = kChunkIn / p.group, groups = p.k / p.group;
+        // Unpacking: warps 0 .. 3 and 4 .. 7 take a step's two blocks, or each one of the two matrices
+        const int half = warp / 4, mine = GATED ? half : 0, f = exponent[mine];
+        const int count = kChunkIn / p.group;
         const bool vector = groups % count == 0;
-        const size_t row = min(row0 + r, p.n_out - 1);
-        const uint32_t lanes = (uint32_t)(warp % 4) << 21;        // this warp's lanes of TMEM
-#pragma unroll
-        for (int m = 0; m < MATS; ++m) {
-            const Q4Matrix &w = m ? p.up : p.w;
-            float top = 0.f;
-            const auto see = [&](float s, float o) { top = fmaxf(top, 15.f * fabsf(s) + fabsf(o)); };
-            if (groups % 8 == 0) {
-                for (int i = 0; i < groups; i += 8) {
-                    const uint4 s = *reinterpret_cast<const uint4 *>(w.scales + row * groups + i);
-                    uint4 o = make_uint4(0, 0, 0, 0);
-                    if (OFFSETS) o = *reinterpret_cast<const uint4 *>(w.offsets + row * groups + i);
-                    float fs[8], fo[8];
-                    unpack8(s, fs);
-                    unpack8(o, fo);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) see(fs[e], fo[e]);
-                }
-            } else {
-                for (int i = 0; i < groups; ++i)
-                    see(__bfloat162float(w.scales[row * groups + i]), OFFSETS ? __bfloat162float(w.offsets[row * groups + i]) : 0.f);
-            }
-            // 2^e <= top < 2^(e + 1) goes to [2^-6, 2^-5); nothing, or what is not finite, stays
-            const int e = (int)(__float_as_uint(top) >> 23) - 127;
-            exponent[m] = top > 0.f && e < 128 ? max(e, -120) + 6 : 0;
-        }
-        const int mine = GATED ? wg : 0, f = exponent[mine];
+        const uint32_t to = a_cols + ((uint32_t)(warp % 4) << 21) + (GATED ? 64 * half : 32 * half);        // this warp's lanes of TMEM
         const Q4Matrix &w = mine ? p.up : p.w;
         const float f0 = power_of_two(-f / 2), f1 = power_of_two(-f - -f / 2);
         ChunkScales next = chunk_scales<OFFSETS>(w, row, groups, chunk0 * count, count, vector);
         bool gone = false;
-        for (int c = 0; c < chunks; ++c) {
+        int s = 0, phase = 0;
+        for (int c = 0; c < chunks && !gone; ++c) {
             const ChunkScales cur = next;
             if (c + 1 < chunks) next = chunk_scales<OFFSETS>(w, row, groups, (chunk0 + c + 1) * count, count, vector);
-            const int s = c % l.code_stages;
-            mbar_poll(&sm.code_full[s], (c / l.code_stages) & 1, abort);
+            warp_poll(&sm.code_full[s], phase, abort);
             const unsigned char *line = codes + (size_t)(s * MATS + mine) * kCodeBytes + r * 128;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int k = 4 * c + j;
-                if (k >= steps || (!GATED && (j & 1) != wg)) continue;
-                const int t = GATED ? 2 * k + wg : k, slot = t % kSlots;
-                const float sc = nth_bf16(cur.s, count == 4 ? j : j / 2) * f0 * f1;
-                const float of = OFFSETS ? nth_bf16(cur.o, count == 4 ? j : j / 2) * f0 * f1 : -8.f * sc;
-                const uint32_t s0 = f16_twice(sc * 16777216.f), s1 = f16_twice(sc * 1048576.f), o2 = f16_twice(of);
+            for (int i = 0; i < 4 / T::BLOCKS; ++i) {
+                const int t = 4 / T::BLOCKS * c + i, j = T::BLOCKS * i + (GATED ? 0 : half), slot = i & 1;
+                if (t >= steps) break;
                 uint32_t v[32];
+                {
+                    const float sc = nth_bf16(cur.s, count == 4 ? j : j / 2) * f0 * f1;
+                    const float of = OFFSETS ? nth_bf16(cur.o, count == 4 ? j : j / 2) * f0 * f1 : -8.f * sc;
+                    const uint32_t s0 = f16_twice(sc * 16777216.f), s1 = f16_twice(sc * 1048576.f), o2 = f16_twice(of);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint4 q = *reinterpret_cast<const uint4 *>(line + (((2 * j + h) ^ (r & 7)) << 4));
-                    const uint32_t words[4] = {q.x, q.y, q.z, q.w};
+                    for (int h = 0; h < 2; ++h) {
+                        const uint4 q = *reinterpret_cast<const uint4 *>(line + (((2 * j + h) ^ (r & 7)) << 4));
+                        const uint32_t words[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t a = words[i], b = a >> 8;
-                        v[16 * h + 4 * i] = fma_f16x2(a & 0x000f000fu, s0, o2);
-                        v[16 * h + 4 * i + 1] = fma_f16x2(a & 0x00f000f0u, s1, o2);
-                        v[16 * h + 4 * i + 2] = fma_f16x2(b & 0x000f000fu, s0, o2);
-                        v[16 * h + 4 * i + 3] = fma_f16x2(b & 0x00f000f0u, s1, o2);
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t a = words[e], b = a >> 8;
+                            v[16 * h + 4 * e] = fma_f16x2(a & 0x000f000fu, s0, o2);
+                            v[16 * h + 4 * e + 1] = fma_f16x2(a & 0x00f000f0u, s1, o2);
+                            v[16 * h + 4 * e + 2] = fma_f16x2(b & 0x000f000fu, s0, o2);
+                            v[16 * h + 4 * e + 3] = fma_f16x2(b & 0x00f000f0u, s1, o2);
+                        }
                     }
                 }
-                if (t >= kSlots) {
-                    mbar_poll(&sm.a_empty[slot], (t / kSlots - 1) & 1, abort);
+                if (t >= 2) {
+                    warp_poll(&sm.a_empty[mine][slot], (t / 2 - 1) & 1, abort);
                     tc_fence_after();
                 }
                 if (gone = __any_sync(0xffffffffu, *abort)) break;
-                tmem_st_row(a_cols + 32 * slot + lanes, v);
+                tmem_st_row(to + T::BLOCKS * 32 * slot, v);     // (a block beyond the inputs is not multiplied)
                 tc_fence_before();
-                mbar_arrive(&sm.a_full[slot]);
+                warp_arrive(&sm.a_full[mine][slot]);
             }
-            if (gone) break;
-            mbar_arrive(&sm.code_empty[s]);
+            if (!gone) warp_arrive(&sm.code_empty[s]);
+            if (++s == l.code_stages) s = 0, phase ^= 1;
         }
-        mbar_poll(&sm.done, 0, abort);
+        grid_dependency_wait();
+        for (int m = tid; m < l.ntok; m += 256) {
+            const int e = m0 + m < p.rows ? -x_exponents[m0 + m] : 0;
+            sm.undo[m] = make_float2(power_of_two(e / 2), power_of_two(e - e / 2));
+        }
+        asm volatile("barrier.sync 1, 256;" ::: "memory");
+        warp_poll(&sm.done, 0, abort);
         tc_fence_after();
     }
 
     // Outputs.  Warps 0 .. 3 take the first half of the columns (rows of x), 4 .. 7 the second
     __syncwarp();
     const bool good = !__any_sync(0xffffffffu, *abort);
-    const int r = tid & 127, n = row0 + r, half = l.ntok / 2;
+    const int n = row0 + r, m_end = min(l.ntok, p.rows - m0);
     const uint32_t lanes = (uint32_t)(warp % 4) << 21;
-    const int m_end = min(l.ntok, p.rows - m0);
-    auto write = [&](int m, float y, float z, int ex) {
-        y = ldexpf(y, exponent[0] - ex);
-        if constexpr (GATED) y = ffn_act(y, p.gelu) * ldexpf(z, exponent[MATS - 1] - ex);
-        if (n < p.n_out) static_cast<__nv_bfloat16 *>(p.out)[(size_t)(m0 + m) * p.n_out + n] = __float2bfloat16_rn(y);
+    const float2 undo0 = make_float2(power_of_two(exponent[0] / 2), power_of_two(exponent[0] - exponent[0] / 2));
+    const int e1 = exponent[MATS - 1];
+    const float2 undo1 = make_float2(power_of_two(e1 / 2), power_of_two(e1 - e1 / 2));
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + (size_t)m0 * p.n_out + n;
+    auto write = [&](int m, float y, float z) {
+        // the halves of a power have its sign, so that nothing overflows in between that does not in the end
+        const float2 u = sm.undo[m];
+        y = y * (undo0.x * u.x) * (undo0.y * u.y);
+        if constexpr (GATED) y = ffn_act_fast(y, p.gelu) * (z * (undo1.x * u.x) * (undo1.y * u.y));
+        if (n < p.n_out) out[(size_t)m * p.n_out] = __float2bfloat16_rn(y);
     };
     float *part = reinterpret_cast<float *>(base);            // [matrix][column][row]: the pipeline is done with this memory
     if (warp < 8 && good) {
-        grid_dependency_wait();
+        const int half = l.ntok / 2;
         for (int col = warp / 4 * half; col < (warp / 4 + 1) * half; col += 8) {
             float y[8], z[8];
             tmem_ld8x2(tmem + col + lanes, tmem + (MATS - 1) * l.ntok + col + lanes, y, z);
@@ -287,7 +355,7 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
                     part[(col + i) * kRowsA + r] = y[i];
                     if (GATED) part[(l.ntok + col + i) * kRowsA + r] = z[i];
                 } else if (col + i < m_end) {
-                    write(col + i, y[i], z[i], x_exponents[m0 + col + i]);
+                    write(col + i, y[i], z[i]);
                 }
             }
         }
@@ -301,7 +369,7 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
                     y += ld_dsmem_f32(part + col * kRowsA + r, q);
                     if (GATED) z += ld_dsmem_f32(part + (l.ntok + col) * kRowsA + r, q);
                 }
-                write(col, y, z, x_exponents[m0 + col]);
+                write(col, y, z);
             }
         }
         cluster_sync();                            // a CTA's sums are read before it is gone
@@ -309,7 +377,7 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
     tc_fence_before();
     __syncthreads();
     if (tid == 0 && sm.abort) raise_error(err, kErrTimeout);
-    if (warp == 0) {
+    if (warp == 8) {
         tmem_relinquish();
         tmem_dealloc(tmem, l.tmem_cols);
     }
@@ -368,19 +436,21 @@ bool byte_map(CUtensorMap *m, const void *at, uint64_t rows, uint64_t row_bytes,
 int round_up(int a, int b) { return (a + b - 1) / b * b; }
 
 size_t tc_shared(const TcPlan &l, int mats) {
-    const size_t pipeline = (size_t)l.code_stages * mats * kCodeBytes + (size_t)kXStages * l.ntok * 128;
+    const size_t pipeline = (size_t)l.code_stages * mats * kCodeBytes + (size_t)l.x_stages * (mats == 2 ? 1 : 2) * l.ntok * 128;
     const size_t join = l.cluster > 1 ? (size_t)mats * l.ntok * kRowsA * 4 : 0;
     return 1024 + max(pipeline, join);
 }
 
-// The division that should be done first: waves of CTAs times a CTA's steps, each as long as the product's or the unpacking's
+constexpr size_t kTcShared = 227 * 1024 - sizeof(TcBars) - 64;
+
+// The division that should be done first: waves of CTAs times a CTA's blocks, each as long as the product's or the unpacking's
 // part of it takes (cycles), and what a CTA takes besides.
 TcPlan plan_tc(int rows, int n_out, int k, bool gated) {
     const int mats = gated ? 2 : 1, most = gated ? 192 : 256, sms = multiprocessor_count();
-    const int chunks = (k + kChunkIn - 1) / kChunkIn;
+    const int chunks = (k + kChunkIn - 1) / kChunkIn, fewest = (rows + most - 1) / most;
     TcPlan best{};
     double least = 1e300;
-    for (int tiles = (rows + most - 1) / most; tiles <= (rows + 15) / 16 && tiles <= 4 * ((rows + most - 1) / most); ++tiles) {
+    for (int tiles = fewest; tiles <= (rows + 15) / 16 && tiles <= fewest + 4; ++tiles) {
         for (int cluster = 1; cluster <= 8 && cluster <= chunks; cluster *= 2) {
             TcPlan l{};
             l.ntok = round_up((rows + tiles - 1) / tiles, 16);
@@ -390,11 +460,14 @@ TcPlan plan_tc(int rows, int n_out, int k, bool gated) {
             l.slice = (chunks + cluster - 1) / cluster;
             if ((long)l.slice * (cluster - 1) >= chunks) continue;            // every CTA has inputs
             l.code_stages = gated ? 3 : 4;
+            l.x_stages = kMaxStages;
+            const size_t room = mats * l.ntok + 128 <= 256 ? 112 * 1024 : kTcShared;      // two CTAs an SM where TMEM has room for them
+            while (l.x_stages > 2 && tc_shared(l, mats) > room) --l.x_stages;
             l.tmem_cols = 32;
-            while (l.tmem_cols < mats * l.ntok + 32 * kSlots) l.tmem_cols *= 2;
-            if (tc_shared(l, mats) > 226 * 1024) continue;
+            while (l.tmem_cols < mats * l.ntok + 128) l.tmem_cols *= 2;
+            if (tc_shared(l, mats) > kTcShared) continue;
             const double waves = ceil((double)l.row_tiles * l.m_tiles * cluster / sms);
-            const double time = waves * (l.slice * 4.0 * mats * max(l.ntok, 150) + 5000 + (cluster > 1 ? 1500 + 10.0 * l.ntok : 0));
+            const double time = waves * (l.slice * 4.0 * mats * max(2 * l.ntok + 44, 250) + 9000 + 30.0 * l.ntok * mats + (cluster > 1 ? 2000 : 0));
             if (time < least) least = time, best = l;
         }
     }
@@ -411,7 +484,7 @@ cudaError_t launch_tc(const Q4Problem &p, const TcPlan &l, const CUtensorMap &co
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= kMaxDevices || !ready[dev].load(std::memory_order_relaxed)) {
-        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - (int)sizeof(TcBars) - 64);
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcShared);
         if (e != cudaSuccess) return e;
         if (dev < kMaxDevices) ready[dev].store(true, std::memory_order_relaxed);
     }

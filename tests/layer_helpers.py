@@ -109,11 +109,12 @@ def q4_product(x, w, rounded=False):
 
 
 def gated(x, gate, up, act, rounded=False):
-    """(y, bound) of act(x gate) * (x up): slopes of both activations are below 1.13."""
+    """(y, bound) of act(x gate) * (x up): slopes of both activations are below 1.13; the exponential and the quotient are good to
+    2^-20, or to 2^-18 in the form for outputs in bf16 (its argument, below 64, is rounded: 64 log2 e 2^-24 log 2)."""
     (a, ea), (b, eb) = q4_product(x, gate, rounded), q4_product(x, up, rounded)
     f = a * torch.sigmoid(a) if act == "silu" else 0.5 * a * (1 + torch.tanh(math.sqrt(2 / math.pi) * (a + 0.044715 * a ** 3)))
     y = f * b
-    return y, 1.13 * ea * (b.abs() + eb) + f.abs() * eb + 2.0 ** -20 * y.abs() + 2.0 ** -20 * (a.abs() * b.abs()).clamp_max(1e-6)
+    return y, 1.13 * ea * (b.abs() + eb) + f.abs() * eb + 2.0 ** (-18 if rounded else -20) * y.abs() + 2.0 ** -20 * (a.abs() * b.abs()).clamp_max(1e-6)
 
 
 def check(got, want, bound):
