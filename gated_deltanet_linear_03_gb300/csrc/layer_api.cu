@@ -10,7 +10,7 @@ using namespace gdn::api;
 
 namespace {
 
-constexpr long long kMaxStride = 1ll << 40;       // row times stride stays in 64 bits
+constexpr long long kMaxStride = 1ll << 38;       // bytes between rows are counted in 40 bits, row times stride in 64
 
 // A bf16 row argument: its elements and their distance.
 gdn_status check_rows(const void *p, long long stride, long long row) {
@@ -53,8 +53,8 @@ gdn_status check_q4_shape(int rows, int n_out, int k, int group) {
     if (group != 64 && group != 128) return GDN_ERR_UNSUPPORTED;
     if (k % group != 0 || k > 65536) return GDN_ERR_UNSUPPORTED;
     if (rows > INT_MAX - 65536 || n_out > INT_MAX - 65536) return GDN_ERR_UNSUPPORTED;
-    // CTAs are counted in 32 bits: 8 rows of x, 128 of weights and an eighth of the inputs each at the least
-    if (((double)rows / 8 + 1) * ((double)n_out / 128 + 1) * 8 >= 2147483648.0) return GDN_ERR_UNSUPPORTED;
+    // CTAs and tiles are counted in 32 bits: 8 rows of x and 8 of weights each at the least
+    if (((double)rows / 8 + 1) * ((double)n_out / 8 + 1) >= 2147000000.0) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 

@@ -2,6 +2,8 @@
 // entry points pass to the launchers.
 #pragma once
 
+#include <cuda.h>
+
 #include "kv_cache.cuh"
 
 namespace gdn {
@@ -76,6 +78,45 @@ size_t q4_workspace_bytes(int rows, int n_out, int k, int out_f32);
 // the kernel for many rows
 cudaError_t launch_q4_tc(const Q4Problem &p);
 size_t q4_tc_workspace_bytes(int rows, int k);
+// [rows, bytes of a row, `pitch` bytes apart] read in boxes of 128 bytes of box_rows rows, 128-byte swizzled.
+bool byte_map(CUtensorMap *m, const void *at, uint64_t rows, uint64_t row_bytes, uint64_t pitch, uint32_t box_rows);
+
+// Scales and offsets of a row's groups of 256 inputs (4 of 64 inputs or 2 of 128), as they lie in memory.
+struct ChunkScales {
+    uint2 s, o;
+};
+
+template <bool OFFSETS>
+__device__ __forceinline__ ChunkScales chunk_scales(const Q4Matrix &w, size_t row, int groups, int first, int count, bool vector) {
+    ChunkScales c{};
+    const __nv_bfloat16 *s = w.scales + row * groups + first, *o = OFFSETS ? w.offsets + row * groups + first : nullptr;
+    if (vector) {                                        // the row's groups are a multiple of the chunk's
+        if (first >= groups) return c;
+        if (count == 4) {
+            c.s = *reinterpret_cast<const uint2 *>(s);
+            if (OFFSETS) c.o = *reinterpret_cast<const uint2 *>(o);
+        } else {
+            c.s.x = *reinterpret_cast<const uint32_t *>(s);
+            if (OFFSETS) c.o.x = *reinterpret_cast<const uint32_t *>(o);
+        }
+        return c;
+    }
+    uint32_t v[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < count && first + i < groups) {
+            v[i] = __bfloat16_as_ushort(s[i]);
+            if (OFFSETS) u[i] = __bfloat16_as_ushort(o[i]);
+        }
+    c.s = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
+    c.o = make_uint2(u[0] | u[1] << 16, u[2] | u[3] << 16);
+    return c;
+}
+
+__device__ __forceinline__ float nth_bf16(const uint2 &v, int i) {
+    const uint32_t w = i & 2 ? v.y : v.x;
+    return i & 1 ? bf16_hi(w) : bf16_lo(w);
+}
 
 // The activation of a gated feed-forward block: u / (1 + e^-v), with v = u or, for gelu, 2 sqrt(2/pi) (u + 0.044715 u^3), as
 // 1 + tanh(w) = 2 / (1 + e^-2w) has no difference of nearly equal numbers.

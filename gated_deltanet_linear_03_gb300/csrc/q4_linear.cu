@@ -1,29 +1,31 @@
 // gdn_q4_linear and gdn_q4_gated: products of activations with weights of 4 bits,
 //     y[m, n] = sum_G ( s[n, G] sum_{i in G} c[n, i] x[m, i]  +  o[n, G] sum_{i in G} x[m, i] ),
-// G over groups of 64 or 128 inputs; o = -8 s where the matrix has no offsets.
+// G over groups of 64 or 128 inputs; o = -8 s where the matrix has no offsets.  This is the kernel for few rows and for fp32
+// outputs; many rows go to q4_tc.cu.
 //
 // The inner sums go to the tensor cores (mma.sync, 16 weight rows by 8 rows of x by 16 inputs): a code is an integer below 16,
 // exact in bf16, so the products are exact and the sums fp32, and scale and offset meet them once a group instead of once a
-// weight.  Few rows are bound by reading the codes, where this takes the fewest instructions a weight; a matrix
-// instruction of the tcgen05 kind would have to be fed from shared memory or TMEM, by the same registers.
+// weight.  With outputs in bf16 the codes enter as 128 + c, which saves the subtraction and is taken back with the offset
+// (2^-16 of the sums' terms); with fp32 outputs as c.
 //
-// A fragment's order of inputs is free as long as both operands keep it.  Lane (g, t) of a warp reads the 16 codes
-// 16 t .. 16 t + 15 of a block of 64 inputs for weight rows g and g + 8: 8 bytes each, whole 32-byte sectors of a row, as they
-// lie in memory.  A code word's pairs (i, i + 4) come out of one AND/OR each, and x lies in shared memory with each 8 inputs in
-// the order 0 4 1 5 2 6 3 7, so a lane's x is 32 consecutive bytes.
+// Codes and x come by TMA, stages of 16 w weight rows (w = 1, 2, 4 or 8) and all rows of x by 256 inputs, which one thread asks for
+// several stages ahead, across tiles: what reads memory is never waiting for what computes.  Eight warps compute, w along the rows by
+// 8 / w along the inputs; a ninth asks; a tenth sums x over blocks of 64 inputs.  Partial sums meet in shared memory in a fixed order.
 //
-// The 8 warps of a CTA are WN along the rows (16 each) by 8 / WN along the inputs; CTAs of a cluster share the inputs further, and
-// each CTA keeps its slice of x in shared memory for all the tiles of rows that it comes to.  Partial sums meet in shared
-// memory, across a cluster through distributed shared memory: the order of the sum is fixed.
+// A fragment's order of inputs is free as long as both operands keep it: lane (g, t) takes inputs 16 t .. 16 t + 15 of a block of 64,
+// for weight rows g and g + 8 (of two matrices, rows g of each) and for row g of x: 8 bytes of codes and 32 bytes of x in a row.
 #include "layer_ops.cuh"
 #include "sm100.cuh"
 
 namespace gdn {
+
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kBlock = 64;            // inputs of one step of a warp
-constexpr int kAhead = 4;             // blocks whose codes are asked for at once
+using namespace sm100;
+
+constexpr int kWarps = 8, kThreads = 32 * (kWarps + 2);
+constexpr int kChunkIn = 256;
+constexpr int kMaxStages = 6;
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -31,237 +33,279 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Codes i and i + 4 (i = SHIFT / 4) of a word as a bf16 pair: under the exponent of 128 a code is 128 + c exactly.
-template <int SHIFT>
-__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
-    const uint32_t biased = ((w >> SHIFT) & 0x000f000fu) | 0x43004300u;
-    uint32_t r;
-    asm("sub.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(biased), "r"(0x43004300u));
-    return r;
+// The eight codes of a word as four bf16 pairs of neighbours.  Under the exponent of 128 a code is 128 + c exactly.
+template <bool EXACT>
+__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&v)[4]) {
+    const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
+    const uint32_t lo = __byte_perm(even, odd, 0x5140), hi = __byte_perm(even, odd, 0x7362);
+    v[0] = __byte_perm(lo, 0x43434343u, 0x4140);
+    v[1] = __byte_perm(lo, 0x43434343u, 0x4342);
+    v[2] = __byte_perm(hi, 0x43434343u, 0x4140);
+    v[3] = __byte_perm(hi, 0x43434343u, 0x4342);
+    if (EXACT) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm("sub.bf16x2 %0, %1, %2;" : "=r"(v[i]) : "r"(v[i]), "r"(0x43004300u));
+    }
 }
 
-__device__ __forceinline__ float bf16_value(__nv_bfloat16 v) { return __bfloat162float(v); }
-
-struct Q4Launch {
-    int slice;                // inputs of one CTA, a multiple of the group
-    int cluster;              // CTAs that share the inputs
-    int row_tiles, m_blocks;
+struct FewPlan {
+    int w, m_blocks, row_tiles, stages;
+    int codes_bytes;                      // of a stage
 };
 
-// What a warp reads for kAhead blocks: codes of two rows, their scales and offsets.
-template <bool OFFSETS>
-struct Piece {
-    uint2 code[kAhead][2];
-    __nv_bfloat16 scale[kAhead][2], offset[OFFSETS ? kAhead : 1][2];
+struct FewBars {
+    uint64_t full[kMaxStages], summed[kMaxStages], empty[kMaxStages], joined[2];
+    int abort;
 };
 
-template <int NT, int WN, bool GATED, bool OFFSETS>
-__global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) q4_kernel(const __grid_constant__ Q4Problem p, const Q4Launch l) {
-    constexpr int WK = kWarps / WN, COLS = 8 * NT, ROWS = 16 * WN, OUT_ROWS = GATED ? ROWS / 2 : ROWS;
-    extern __shared__ __align__(16) unsigned char smem[];
-    const int rank = l.cluster > 1 ? (int)sm100::cluster_ctarank() : 0;
-    const int k0 = rank * l.slice, slice = min(l.slice, p.k - k0), blocks = slice / kBlock;     // (the last slice may be shorter)
-    const int x_row = l.slice * 2 + 16;                      // bytes; the 16 keep lanes of different rows on different banks
-    float *sums = reinterpret_cast<float *>(smem);           // [slice / 64][COLS]
-    unsigned char *xs = smem + (size_t)(l.slice / kBlock) * COLS * 4;
-    float *part = reinterpret_cast<float *>(xs + (size_t)COLS * x_row);     // [WK][ROWS][COLS]
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-    const int wn = warp / WK, wk = warp % WK;
-    const int work = blockIdx.x / l.cluster, workers = gridDim.x / l.cluster;
-    const int m0 = (work % l.m_blocks) * COLS, m_rows = min(COLS, p.rows - m0);
+template <int NT, bool GATED, bool OFFSETS, bool EXACT>
+__global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
+q4_few_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ FewPlan l, const __grid_constant__ CUtensorMap code_map,
+              const __grid_constant__ CUtensorMap up_map, const __grid_constant__ CUtensorMap x_map, unsigned int *err) {
+    constexpr int COLS = 8 * NT, X_BOX = COLS * 128, X_BYTES = 4 * X_BOX;
+    extern __shared__ unsigned char raw[];
+    __shared__ FewBars sm;
+    unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    const int stage_bytes = l.codes_bytes + X_BYTES;
+    float *sums = reinterpret_cast<float *>(base + (size_t)l.stages * stage_bytes);      // [stage][4][COLS]
+    float *part = sums + l.stages * 4 * COLS;                                            // [2][8 / w][COLS][16 w + 4]
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+    const int w = l.w, kw = kWarps / w, rows = 16 * w, out_rows = GATED ? rows / 2 : rows;
+    const int chunks = (p.k + kChunkIn - 1) / kChunkIn, units = l.row_tiles * l.m_blocks;
+    volatile int *abort = &sm.abort;
 
-    // this CTA's slice of x, and its sums over blocks of 64: 8 lanes a block
-    {
-        const int pieces = slice / 8;
-        for (int i = threadIdx.x; i < COLS * pieces; i += kThreads) {     // pieces is a multiple of 8: 8 lanes stay together
-            const int m = i / pieces, c = i % pieces;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (m < m_rows) v = *reinterpret_cast<const uint4 *>(p.x + (long long)(m0 + m) * p.x_stride + k0 + 8 * c);
-            float f[8];
-            unpack8(v, f);
-            float s = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
-            const unsigned live = __activemask();
-#pragma unroll
-            for (int o = 4; o >= 1; o >>= 1) s += __shfl_xor_sync(live, s, o);
-            if (c % 8 == 0) sums[(c / 8) * COLS + m] = s;
-            uint4 q;
-            q.x = __byte_perm(v.x, v.z, 0x5410);        // 0 4
-            q.y = __byte_perm(v.x, v.z, 0x7632);        // 1 5
-            q.z = __byte_perm(v.y, v.w, 0x5410);        // 2 6
-            q.w = __byte_perm(v.y, v.w, 0x7632);        // 3 7
-            *reinterpret_cast<uint4 *>(xs + (size_t)m * x_row + 16 * c) = q;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < l.stages; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.summed[i], 1);
+            mbar_init(&sm.empty[i], kWarps + 1);
         }
+        mbar_init(&sm.joined[0], kWarps);
+        mbar_init(&sm.joined[1], kWarps);
+        sm.abort = 0;
+        fence_mbar_init();
     }
     __syncthreads();
 
-    const int per = (blocks + WK - 1) / WK, b_lo = min(wk * per, blocks), b_hi = min(b_lo + per, blocks);
-    const int groups = p.k / p.group, shift = p.group == 128 ? 1 : 0;
-    const unsigned char *x_lane = xs + (size_t)g * x_row + 32 * t;
-    const int step = workers / l.m_blocks;
-    for (int tile = work / l.m_blocks; tile < l.row_tiles; tile += step) {
-        // this lane's two weight rows (a row beyond the matrix repeats its last one, and is not written)
-        const int n0 = tile * OUT_ROWS + wn * (GATED ? 8 : 16) + g;
-        const int r0 = min(n0, p.n_out - 1), r1 = GATED ? r0 : min(n0 + 8, p.n_out - 1);
+    int s = 0, phase = 0;
+    const auto advance = [&] { if (++s == l.stages) s = 0, phase ^= 1; };
+    if (warp == kWarps) {
+        if (elect_one()) {
+            for (int u = blockIdx.x; u < units && !*abort; u += gridDim.x) {
+                const int n0 = u / l.m_blocks * out_rows, m0 = u % l.m_blocks * COLS;
+                for (int c = 0; c < chunks; ++c) {
+                    mbar_poll(&sm.empty[s], phase ^ 1, abort);
+                    if (*abort) break;
+                    unsigned char *to = base + (size_t)s * stage_bytes;
+                    mbar_arrive_expect_tx(&sm.full[s], stage_bytes);
+                    tma_load_2d(to, &code_map, &sm.full[s], c * (kChunkIn / 2), n0);
+                    if (GATED) tma_load_2d(to + l.codes_bytes / 2, &up_map, &sm.full[s], c * (kChunkIn / 2), n0);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        tma_load_2d(to + l.codes_bytes + j * X_BOX, &x_map, &sm.full[s], 2 * (c * kChunkIn + 64 * j), m0);    // (the map counts bytes)
+                    advance();
+                }
+            }
+        }
+    } else if (warp == kWarps + 1) {
+        // sums of x over blocks of 64 inputs: a lane a block of a row, the four blocks at different banks
+        const int j = lane % 4;
+        bool gone = false;
+        for (int u = blockIdx.x; u < units && !gone; u += gridDim.x)
+            for (int c = 0; c < chunks; ++c) {
+                mbar_poll(&sm.full[s], phase, abort);
+                if (gone = __any_sync(0xffffffffu, *abort)) break;
+                const unsigned char *x = base + (size_t)s * stage_bytes + l.codes_bytes + j * X_BOX;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const int m = lane / 4 + 8 * i;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        float f[8];
+                        unpack8(*reinterpret_cast<const uint4 *>(x + m * 128 + ((((q + 2 * j) & 7) ^ (m & 7)) << 4)), f);
+                        sum += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+                    }
+                    sums[(s * 4 + j) * COLS + m] = sum;
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&sm.summed[s]);
+                    mbar_arrive(&sm.empty[s]);
+                }
+                advance();
+            }
+    } else {
+        const int g = lane / 4, t = lane % 4, rg = warp % w, ks = warp / w;
+        const int groups = p.k / p.group, count = kChunkIn / p.group;
+        const bool vector = groups % count == 0;
         const Q4Matrix &second = GATED ? p.up : p.w;
-        const uint8_t *code0 = p.w.codes + (size_t)r0 * (p.k / 2) + k0 / 2 + 8 * t;
-        const uint8_t *code1 = second.codes + (size_t)r1 * (p.k / 2) + k0 / 2 + 8 * t;
-        const size_t at0 = (size_t)r0 * groups + (k0 / kBlock >> shift), at1 = (size_t)r1 * groups + (k0 / kBlock >> shift);
-        float acc[NT][4];
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-
-        auto load = [&](Piece<OFFSETS> &q, int b) {
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const int at = min(b + i, b_hi - 1);
-                q.code[i][0] = __ldg(reinterpret_cast<const uint2 *>(code0 + (size_t)at * 32));
-                q.code[i][1] = __ldg(reinterpret_cast<const uint2 *>(code1 + (size_t)at * 32));
-                q.scale[i][0] = p.w.scales[at0 + (at >> shift)];
-                q.scale[i][1] = second.scales[at1 + (at >> shift)];
-                if constexpr (OFFSETS) {
-                    q.offset[i][0] = p.w.offsets[at0 + (at >> shift)];
-                    q.offset[i][1] = second.offsets[at1 + (at >> shift)];
-                }
+        // where this lane's codes are in a stage: rows g and g + 8 of its 16, or row g of its 8 of either matrix
+        const int line0 = (GATED ? 8 * rg + g : 16 * rg + g) * 128, line1 = GATED ? l.codes_bytes / 2 + line0 : line0 + 8 * 128;
+        const int stride = rows + 4;
+        size_t r0 = 0, r1 = 0;
+        ChunkScales next0, next1;
+        const auto ask = [&](int u, int c) {      // the scales of unit u's chunk c (a row beyond the matrix repeats its last one)
+            if (c == 0) {
+                const int n = u / l.m_blocks * out_rows + (GATED ? 8 : 16) * rg + g;
+                r0 = min(n, p.n_out - 1);
+                r1 = GATED ? r0 : min(n + 8, p.n_out - 1);
             }
+            next0 = chunk_scales<OFFSETS>(p.w, r0, groups, c * count, count, vector);
+            next1 = chunk_scales<OFFSETS>(second, r1, groups, c * count, count, vector);
         };
-        Piece<OFFSETS> next;
-        if (b_lo < b_hi) load(next, b_lo);
-        for (int b = b_lo; b < b_hi; b += kAhead) {
-            const Piece<OFFSETS> cur = next;
-            if (b + kAhead < b_hi) load(next, b + kAhead);
+        int buffer = 0, joins = 0;
+        bool gone = false;
+        if ((int)blockIdx.x < units) ask(blockIdx.x, 0);
+        for (int u = blockIdx.x; u < units && !gone; u += gridDim.x) {
+            float acc[NT][4];
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                if (b + i >= b_hi) break;
-                uint32_t a[4][4];
+            for (int i = 0; i < NT; ++i)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t w0 = h ? cur.code[i][0].y : cur.code[i][0].x, w1 = h ? cur.code[i][1].y : cur.code[i][1].x;
-                    a[2 * h][0] = code_pair<0>(w0);
-                    a[2 * h][1] = code_pair<0>(w1);
-                    a[2 * h][2] = code_pair<4>(w0);
-                    a[2 * h][3] = code_pair<4>(w1);
-                    a[2 * h + 1][0] = code_pair<8>(w0);
-                    a[2 * h + 1][1] = code_pair<8>(w1);
-                    a[2 * h + 1][2] = code_pair<12>(w0);
-                    a[2 * h + 1][3] = code_pair<12>(w1);
+                for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+            for (int c = 0; c < chunks; ++c) {
+                const ChunkScales cur0 = next0, cur1 = next1;
+                if (c + 1 < chunks) ask(u, c + 1);
+                else if (u + (int)gridDim.x < units) ask(u + gridDim.x, 0);
+                mbar_poll(&sm.full[s], phase, abort);
+                mbar_poll(&sm.summed[s], phase, abort);
+                if (gone = __any_sync(0xffffffffu, *abort)) break;
+                const unsigned char *stage = base + (size_t)s * stage_bytes;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (((4 * c + j) & (kw - 1)) != ks) continue;
+                    const int at = (((2 * j + t / 2) ^ g) << 4) + 8 * (t & 1);
+                    const uint2 q0 = *reinterpret_cast<const uint2 *>(stage + line0 + at), q1 = *reinterpret_cast<const uint2 *>(stage + line1 + at);
+                    uint32_t v0[4], v1[4], a[4][4];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        code_pairs<EXACT>(h ? q0.y : q0.x, v0);
+                        code_pairs<EXACT>(h ? q1.y : q1.x, v1);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            a[2 * h + i][0] = v0[2 * i];
+                            a[2 * h + i][1] = v1[2 * i];
+                            a[2 * h + i][2] = v0[2 * i + 1];
+                            a[2 * h + i][3] = v1[2 * i + 1];
+                        }
+                    }
+                    const int which = count == 4 ? j : j / 2;
+                    const float s0 = nth_bf16(cur0.s, which), s1 = nth_bf16(cur1.s, which);
+                    constexpr float BIAS = EXACT ? 0.f : 128.f;
+                    const float o0 = OFFSETS ? fmaf(-BIAS, s0, nth_bf16(cur0.o, which)) : -(BIAS + 8.f) * s0;
+                    const float o1 = OFFSETS ? fmaf(-BIAS, s1, nth_bf16(cur1.o, which)) : -(BIAS + 8.f) * s1;
+                    const unsigned char *x = stage + l.codes_bytes + j * X_BOX + g * 128;
+                    const float *xsum = sums + (s * 4 + j) * COLS + 2 * t;
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        const uint4 b0 = *reinterpret_cast<const uint4 *>(x + i * 1024 + (((2 * t) ^ g) << 4));
+                        const uint4 b1 = *reinterpret_cast<const uint4 *>(x + i * 1024 + (((2 * t + 1) ^ g) << 4));
+                        float d[4] = {0.f, 0.f, 0.f, 0.f};
+                        mma_16816(d, a[0], b0.x, b0.y);
+                        mma_16816(d, a[1], b0.z, b0.w);
+                        mma_16816(d, a[2], b1.x, b1.y);
+                        mma_16816(d, a[3], b1.z, b1.w);
+                        const float2 xs = *reinterpret_cast<const float2 *>(xsum + 8 * i);
+                        acc[i][0] = fmaf(s0, d[0], fmaf(o0, xs.x, acc[i][0]));
+                        acc[i][1] = fmaf(s0, d[1], fmaf(o0, xs.y, acc[i][1]));
+                        acc[i][2] = fmaf(s1, d[2], fmaf(o1, xs.x, acc[i][2]));
+                        acc[i][3] = fmaf(s1, d[3], fmaf(o1, xs.y, acc[i][3]));
+                    }
                 }
-                const float s0 = bf16_value(cur.scale[i][0]), s1 = bf16_value(cur.scale[i][1]);
-                const float o0 = OFFSETS ? bf16_value(cur.offset[OFFSETS ? i : 0][0]) : -8.f * s0;
-                const float o1 = OFFSETS ? bf16_value(cur.offset[OFFSETS ? i : 0][1]) : -8.f * s1;
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const uint4 *xb = reinterpret_cast<const uint4 *>(x_lane + (size_t)(8 * j) * x_row + (size_t)(b + i) * 128);
-                    const uint4 u = xb[0], v = xb[1];
-                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma_16816(d, a[0], u.x, u.y);
-                    mma_16816(d, a[1], u.z, u.w);
-                    mma_16816(d, a[2], v.x, v.y);
-                    mma_16816(d, a[3], v.z, v.w);
-                    const float2 xsum = *reinterpret_cast<const float2 *>(sums + (b + i) * COLS + 8 * j + 2 * t);
-                    acc[j][0] = fmaf(s0, d[0], fmaf(o0, xsum.x, acc[j][0]));
-                    acc[j][1] = fmaf(s0, d[1], fmaf(o0, xsum.y, acc[j][1]));
-                    acc[j][2] = fmaf(s1, d[2], fmaf(o1, xsum.x, acc[j][2]));
-                    acc[j][3] = fmaf(s1, d[3], fmaf(o1, xsum.y, acc[j][3]));
-                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.empty[s]);
+                advance();
             }
-        }
-        // partial sums of [WK][rows][columns], joined in the same order every time
-        float *mine = part + ((size_t)wk * ROWS + wn * 16) * COLS;
+            if (gone) break;
+            // The warps' sums meet.  Two buffers in turn: whoever writes one again has waited for all of the other, whose writers had
+            // read this one
+            float *mine = part + (size_t)buffer * kw * COLS * stride;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            *reinterpret_cast<float2 *>(mine + g * COLS + 8 * j + 2 * t) = make_float2(acc[j][0], acc[j][1]);
-            *reinterpret_cast<float2 *>(mine + (g + 8) * COLS + 8 * j + 2 * t) = make_float2(acc[j][2], acc[j][3]);
-        }
-        if (l.cluster > 1) sm100::cluster_sync();
-        else __syncthreads();
-        const int elements = OUT_ROWS * m_rows, share = (elements + l.cluster - 1) / l.cluster;
-        for (int i = rank * share + threadIdx.x; i < min((rank + 1) * share, elements); i += kThreads) {
-            const int r = i % OUT_ROWS, m = i / OUT_ROWS;            // neighbours write neighbouring outputs
-            const int row = GATED ? r / 8 * 16 + r % 8 : r;
-            float y = 0.f, z = 0.f;
-            for (int q = 0; q < l.cluster; ++q)
+            for (int i = 0; i < NT; ++i)
 #pragma unroll
-                for (int w = 0; w < WK; ++w) {
-                    const float *from = part + ((size_t)w * ROWS + row) * COLS + m;
-                    y += l.cluster > 1 ? sm100::ld_dsmem_f32(from, q) : *from;
-                    if constexpr (GATED) z += l.cluster > 1 ? sm100::ld_dsmem_f32(from + 8 * COLS, q) : from[8 * COLS];
+                for (int e = 0; e < 4; ++e)
+                    mine[(ks * COLS + 8 * i + 2 * t + (e & 1)) * stride + 16 * rg + g + (e & 2) * 4] = acc[i][e];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.joined[buffer]);
+            mbar_poll(&sm.joined[buffer], joins >> 1 & 1, abort);
+            if (gone = __any_sync(0xffffffffu, *abort)) break;
+            ++joins;
+            const int n0 = u / l.m_blocks * out_rows, m0 = u % l.m_blocks * COLS, m_rows = min(COLS, p.rows - m0);
+            for (int i = threadIdx.x; i < out_rows * m_rows; i += 32 * kWarps) {
+                const int r = i & (out_rows - 1), m = i / out_rows, n = n0 + r;        // neighbours write neighbouring outputs
+                const int from = GATED ? r / 8 * 16 + r % 8 : r;
+                float y = 0.f, z = 0.f;
+                for (int k = 0; k < kw; ++k) {
+                    y += mine[(k * COLS + m) * stride + from];
+                    if (GATED) z += mine[(k * COLS + m) * stride + from + 8];
                 }
-            if constexpr (GATED) y = ffn_act(y, p.gelu) * z;
-            const int n = tile * OUT_ROWS + r;
-            if (n >= p.n_out) continue;
-            const size_t at = (size_t)(m0 + m) * p.n_out + n;
-            if (p.out_f32) static_cast<float *>(p.out)[at] = y;
-            else static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(y);
+                if (GATED) y = ffn_act(y, p.gelu) * z;
+                if (n >= p.n_out) continue;
+                const size_t to = (size_t)(m0 + m) * p.n_out + n;
+                if (p.out_f32) static_cast<float *>(p.out)[to] = y;
+                else static_cast<__nv_bfloat16 *>(p.out)[to] = __float2bfloat16_rn(y);
+            }
+            buffer ^= 1;
         }
-        if (l.cluster > 1) sm100::cluster_sync();      // the sums are read before they are overwritten, or their CTA is gone
-        else __syncthreads();
     }
+    __syncthreads();
+    if (threadIdx.x == 0 && sm.abort) raise_error(err, kErrTimeout);
 }
 
-constexpr int kMaxCluster = 8;
-constexpr size_t kMaxShared = 220 * 1024;
-
-// Inputs of a CTA are a multiple of 128: of either group, and whole lines of a weight row.
-int units_of(int k) { return (k + 127) / 128; }
-
-template <int NT, int WN>
-size_t shared_bytes(int k, int cluster) {
-    constexpr int COLS = 8 * NT;
-    const size_t slice = (size_t)(units_of(k) + cluster - 1) / cluster * 128;
-    return slice / kBlock * COLS * 4 + COLS * (slice * 2 + 16) + (size_t)(kWarps / WN) * 16 * WN * COLS * 4;
+size_t few_shared(int cols, const FewPlan &l) {
+    const size_t stage = l.codes_bytes + (size_t)cols * 512;
+    return 1024 + l.stages * (stage + 16 * cols) + (size_t)2 * (kWarps / l.w) * cols * (16 * l.w + 4) * 4;
 }
 
-template <int NT, int WN, bool GATED>
+template <int NT, bool GATED>
 cudaError_t launch(const Q4Problem &p) {
-    constexpr int COLS = 8 * NT, ROWS = 16 * WN, OUT_ROWS = GATED ? ROWS / 2 : ROWS;
-    Q4Launch l;
-    l.row_tiles = (p.n_out + OUT_ROWS - 1) / OUT_ROWS;
-    l.m_blocks = (p.rows + COLS - 1) / COLS;
+    constexpr int COLS = 8 * NT, FIT = NT <= 2 ? 2 : 1;
     const int sms = multiprocessor_count();
-    // CTAs of a cluster: enough that x fits into shared memory, and that there is a CTA for every SM
-    const int units = units_of(p.k);
-    l.cluster = 1;
-    while (l.cluster < kMaxCluster && (shared_bytes<NT, WN>(p.k, l.cluster) > 100 * 1024 || (long)l.row_tiles * l.m_blocks * l.cluster < sms) &&
-           units >= 4 * l.cluster) l.cluster *= 2;
-    while ((units + l.cluster - 1) / l.cluster * (l.cluster - 1) >= units) l.cluster /= 2;     // every CTA has inputs
-    l.slice = (units + l.cluster - 1) / l.cluster * 128;
-    const size_t smem = shared_bytes<NT, WN>(p.k, l.cluster);
-    using Fn = void (*)(const Q4Problem, const Q4Launch);
-    const Fn fn = p.w.offsets ? (Fn)q4_kernel<NT, WN, GATED, true> : (Fn)q4_kernel<NT, WN, GATED, false>;
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    FewPlan l{};
+    l.m_blocks = (p.rows + COLS - 1) / COLS;
+    // rows of a tile: as few rounds as possible of tiles that cost their rows and a little
+    double least = 1e300;
+    for (int w = 8; w >= 1; w /= 2) {
+        const long tiles = (p.n_out + (GATED ? 8 : 16) * w - 1) / ((GATED ? 8 : 16) * w);
+        const double cost = ceil((double)tiles * l.m_blocks / (sms * FIT)) * (w + 0.7);
+        if (cost < least) least = cost, l.w = w, l.row_tiles = (int)tiles;
+    }
+    l.codes_bytes = 16 * l.w * 128;
+    constexpr size_t kShared = (FIT == 2 ? 112 : 226) * 1024 - sizeof(FewBars);
+    l.stages = kMaxStages;
+    while (l.stages > 2 && few_shared(COLS, l) > kShared) --l.stages;
+    const int box_rows = (GATED ? 8 : 16) * l.w;
+    CUtensorMap codes, up, x;
+    if (!byte_map(&codes, p.w.codes, p.n_out, p.k / 2, p.k / 2, box_rows) || !byte_map(&x, p.x, p.rows, 2 * (uint64_t)p.k, 2 * p.x_stride, COLS))
+        return cudaErrorInvalidValue;
+    if (!GATED) up = codes;
+    else if (!byte_map(&up, p.up.codes, p.n_out, p.k / 2, p.k / 2, box_rows)) return cudaErrorInvalidValue;
+
+    using Fn = void (*)(const Q4Problem, const FewPlan, const CUtensorMap, const CUtensorMap, const CUtensorMap, unsigned int *);
+    static const Fn fns[2][2] = {{q4_few_kernel<NT, GATED, false, false>, q4_few_kernel<NT, GATED, false, true>},
+                                 {q4_few_kernel<NT, GATED, true, false>, q4_few_kernel<NT, GATED, true, true>}};
+    const int offsets = p.w.offsets != nullptr, exact = p.out_f32;
+    static std::atomic<bool> ready[kMaxDevices][2][2];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const int fit = smem <= 100 * 1024 && NT <= 2 ? 2 : 1;
-    // clusters that stay: as many as fit, the same number of tiles each as far as that goes
-    long workers = (long)sms * fit / l.cluster / l.m_blocks;
-    if (workers < 1) workers = 1;
-    const long rounds = (l.row_tiles + workers - 1) / workers;
-    workers = (l.row_tiles + rounds - 1) / rounds;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(workers * l.m_blocks * l.cluster));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = p.stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = l.cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = l.cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, fn, p, l);
+    if (dev >= kMaxDevices || !ready[dev][offsets][exact].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(fns[offsets][exact], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kShared);
+        if (e != cudaSuccess) return e;
+        if (dev < kMaxDevices) ready[dev][offsets][exact].store(true, std::memory_order_relaxed);
+    }
+    const long units = (long)l.row_tiles * l.m_blocks;
+    fns[offsets][exact]<<<(unsigned)min(units, (long)sms * FIT), kThreads, few_shared(COLS, l), p.stream>>>(p, l, codes, up, x, error_word());
+    return cudaGetLastError();
 }
 
-// A CTA takes 8, 16, 32 or 64 rows of x, as many as there are and as its shared memory holds of them.
-template <int NT, int WN>
-bool fits(const Q4Problem &p) { return shared_bytes<NT, WN>(p.k, kMaxCluster) <= kMaxShared; }
-
+// A CTA takes 8, 16, 32 or 64 rows of x.
 template <bool GATED>
 cudaError_t by_rows(const Q4Problem &p) {
-    if (p.rows > 32 && fits<8, 8>(p)) return launch<8, 8, GATED>(p);
-    if (p.rows > 16 && fits<4, 4>(p)) return launch<4, 4, GATED>(p);
-    if (p.rows > 8 && fits<2, 2>(p)) return launch<2, 2, GATED>(p);
-    return launch<1, 1, GATED>(p);
+    if (p.rows > 32) return launch<8, GATED>(p);
+    if (p.rows > 16) return launch<4, GATED>(p);
+    if (p.rows > 8) return launch<2, GATED>(p);
+    return launch<1, GATED>(p);
 }
 
 }  // namespace

@@ -77,43 +77,6 @@ __device__ __forceinline__ uint32_t f16_twice(float v) {
 
 __device__ __forceinline__ float power_of_two(int e) { return __int_as_float((e + 127) << 23); }      // -126 .. 127
 
-// Scales and offsets of a row's groups of one chunk (4 of 64 inputs or 2 of 128), as they lie in memory.
-struct ChunkScales {
-    uint2 s, o;
-};
-
-template <bool OFFSETS>
-__device__ __forceinline__ ChunkScales chunk_scales(const Q4Matrix &w, size_t row, int groups, int first, int count, bool vector) {
-    ChunkScales c{};
-    const __nv_bfloat16 *s = w.scales + row * groups + first, *o = OFFSETS ? w.offsets + row * groups + first : nullptr;
-    if (vector) {                                        // the row's groups are a multiple of the chunk's
-        if (first >= groups) return c;
-        if (count == 4) {
-            c.s = *reinterpret_cast<const uint2 *>(s);
-            if (OFFSETS) c.o = *reinterpret_cast<const uint2 *>(o);
-        } else {
-            c.s.x = *reinterpret_cast<const uint32_t *>(s);
-            if (OFFSETS) c.o.x = *reinterpret_cast<const uint32_t *>(o);
-        }
-        return c;
-    }
-    uint32_t v[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (i < count && first + i < groups) {
-            v[i] = __bfloat16_as_ushort(s[i]);
-            if (OFFSETS) u[i] = __bfloat16_as_ushort(o[i]);
-        }
-    c.s = make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
-    c.o = make_uint2(u[0] | u[1] << 16, u[2] | u[3] << 16);
-    return c;
-}
-
-__device__ __forceinline__ float nth_bf16(const uint2 &v, int i) {
-    const uint32_t w = i & 2 ? v.y : v.x;
-    return i & 1 ? bf16_hi(w) : bf16_lo(w);
-}
-
 // A wait of a whole warp in which one lane asks: 256 lanes that ask keep the shared-memory pipe from the threads that issue (a
 // poll that finds its phase complete then took those 230 cycles).
 __device__ __forceinline__ void warp_poll(uint64_t *bar, uint32_t parity, volatile int *abort) {
@@ -411,28 +374,6 @@ __global__ void __launch_bounds__(128) scale_rows_kernel(const __grid_constant__
     }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
-        cudaDriverEntryPointQueryResult q;
-        void *f = nullptr;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-        return nullptr;
-    }();
-    return fn;
-}
-
-// [rows, bytes of a row] read in boxes of 128 bytes of box_rows rows, 128-byte swizzled.
-bool byte_map(CUtensorMap *m, const void *at, uint64_t rows, uint64_t row_bytes, uint32_t box_rows) {
-    const auto fn = encode_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[2] = {row_bytes, rows}, strides[1] = {row_bytes};
-    const cuuint32_t box[2] = {128, box_rows}, es[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(at), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 int round_up(int a, int b) { return (a + b - 1) / b * b; }
 
 size_t tc_shared(const TcPlan &l, int mats) {
@@ -508,6 +449,27 @@ size_t exponent_bytes(int rows) { return ((size_t)rows * 4 + 255) / 256 * 256; }
 
 }  // namespace
 
+static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+        cudaDriverEntryPointQueryResult q;
+        void *f = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+        return nullptr;
+    }();
+    return fn;
+}
+
+bool byte_map(CUtensorMap *m, const void *at, uint64_t rows, uint64_t row_bytes, uint64_t pitch, uint32_t box_rows) {
+    const auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {row_bytes, rows}, strides[1] = {pitch};
+    const cuuint32_t box[2] = {128, box_rows}, es[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(at), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 size_t q4_tc_workspace_bytes(int rows, int k) { return exponent_bytes(rows) + (size_t)rows * k * 2; }
 
 cudaError_t launch_q4_tc(const Q4Problem &p) {
@@ -515,9 +477,9 @@ cudaError_t launch_q4_tc(const Q4Problem &p) {
     __half *x16 = reinterpret_cast<__half *>(static_cast<uint8_t *>(p.workspace) + exponent_bytes(p.rows));
     const TcPlan l = plan_tc(p.rows, p.n_out, p.k, p.gated);
     CUtensorMap codes, up, x;
-    if (!byte_map(&codes, p.w.codes, p.n_out, p.k / 2, kRowsA) || !byte_map(&x, x16, p.rows, (uint64_t)p.k * 2, l.ntok)) return cudaErrorInvalidValue;
+    if (!byte_map(&codes, p.w.codes, p.n_out, p.k / 2, p.k / 2, kRowsA) || !byte_map(&x, x16, p.rows, (uint64_t)p.k * 2, (uint64_t)p.k * 2, l.ntok)) return cudaErrorInvalidValue;
     if (!p.gated) up = codes;
-    else if (!byte_map(&up, p.up.codes, p.n_out, p.k / 2, kRowsA)) return cudaErrorInvalidValue;
+    else if (!byte_map(&up, p.up.codes, p.n_out, p.k / 2, p.k / 2, kRowsA)) return cudaErrorInvalidValue;
     scale_rows_kernel<<<(unsigned)((p.rows + 3) / 4), 128, 0, p.stream>>>(p, x16, exponents);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;

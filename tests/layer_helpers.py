@@ -88,11 +88,12 @@ def q4_values(w):
     return ((q - 8) * s if offsets is None else q * s + offsets.double()[..., None]).flatten(1)
 
 
-def q4_product(x, w, rounded=False):
+def q4_product(x, w, rounded=None):
     """(y, bound): products exact, their sums in 32 bits.  A group of 64 is summed by four matrix instructions, each an
     aligned sum that may cut what is below 2^-23 of its largest term, then scaled and added; the offset's part likewise:
-    (16 + 4 groups of 64) 2^-23 of the sum of the magnitudes that are added.  With weights rounded to fp16: 2^-11 of each, and
-    2^-19 of the row's largest 15 |scale| + |offset|, which holds for an input that falls below 2^-40 of its row's largest, too."""
+    (16 + 4 groups of 64) 2^-23 of the sum of the magnitudes that are added, among which, rounded=False (few rows and bf16
+    outputs), are the 128 that every code carries along.  rounded=True (many), weights rounded to fp16: 2^-11 of each, and 2^-19
+    of the row's largest 15 |scale| + |offset|; inputs below 2^-40 of their row's largest may be lost."""
     codes, scales, offsets = w
     n, half = codes.shape
     k, groups = 2 * half, scales.shape[1]
@@ -100,7 +101,8 @@ def q4_product(x, w, rounded=False):
     s = scales.double().repeat_interleave(k // groups, dim=1).abs()
     o = 8 * s if offsets is None else offsets.double().repeat_interleave(k // groups, dim=1).abs()
     v, mag = q4_values(w), x.double().abs()
-    bound = (16 + 4 * (k // 64)) * 2.0 ** -23 * (mag @ (q * s + o).T)
+    carried = 0 if rounded is None else 128 * s
+    bound = (16 + 4 * (k // 64)) * 2.0 ** -23 * (mag @ (q * s + o + 2 * carried).T)
     if rounded:
         top = (15 * s + (0 if offsets is None else o)).amax(dim=1)
         bound = bound + 2.0 ** -11 * (mag @ v.abs().T) + 2.0 ** -19 * mag.sum(-1, keepdim=True) * top
@@ -108,13 +110,13 @@ def q4_product(x, w, rounded=False):
     return x.double() @ v.T, bound
 
 
-def gated(x, gate, up, act, rounded=False):
+def gated(x, gate, up, act, rounded=None):
     """(y, bound) of act(x gate) * (x up): slopes of both activations are below 1.13; the exponential and the quotient are good to
     2^-20, or to 2^-18 in the form for outputs in bf16 (its argument, below 64, is rounded: 64 log2 e 2^-24 log 2)."""
     (a, ea), (b, eb) = q4_product(x, gate, rounded), q4_product(x, up, rounded)
     f = a * torch.sigmoid(a) if act == "silu" else 0.5 * a * (1 + torch.tanh(math.sqrt(2 / math.pi) * (a + 0.044715 * a ** 3)))
     y = f * b
-    return y, 1.13 * ea * (b.abs() + eb) + f.abs() * eb + 2.0 ** (-18 if rounded else -20) * y.abs() + 2.0 ** -20 * (a.abs() * b.abs()).clamp_max(1e-6)
+    return y, 1.13 * ea * (b.abs() + eb) + f.abs() * eb + 2.0 ** (-20 if rounded is None else -18) * y.abs() + 2.0 ** -20 * (a.abs() * b.abs()).clamp_max(1e-6)
 
 
 def check(got, want, bound):
