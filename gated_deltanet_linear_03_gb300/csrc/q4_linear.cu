@@ -1,7 +1,7 @@
 // gdn_q4_linear and gdn_q4_gated: products of activations with weights of 4 bits,
 //     y[m, n] = sum_G ( s[n, G] sum_{i in G} c[n, i] x[m, i]  +  o[n, G] sum_{i in G} x[m, i] ),
-// G over groups of 64 or 128 inputs; o = -8 s where the matrix has no offsets.  This is the kernel for few rows and for fp32
-// outputs; many rows go to q4_tc.cu.
+// G over groups of 64 or 128 inputs; o = -8 s where the matrix has no offsets.  This is the kernel for a few rows and for fp32
+// outputs; one or two rows go to q4_vec.cu, many to q4_tc.cu.
 //
 // The inner sums go to the tensor cores (mma.sync, 16 weight rows by 8 rows of x by 16 inputs): a code is an integer below 16,
 // exact in bf16, so the products are exact and the sums fp32, and scale and offset meet them once a group instead of once a
@@ -316,6 +316,7 @@ static bool many_rows(int rows, int out_f32) { return rows > 16 && !out_f32; }
 size_t q4_workspace_bytes(int rows, int n_out, int k, int out_f32) { return many_rows(rows, out_f32) ? q4_tc_workspace_bytes(rows, k) : 0; }
 
 cudaError_t launch_q4(const Q4Problem &p) {
+    if (q4_vec_takes(p.rows, p.k)) return launch_q4_vec(p);
     if (many_rows(p.rows, p.out_f32)) return launch_q4_tc(p);
     return p.gated ? by_rows<true>(p) : by_rows<false>(p);
 }

@@ -461,13 +461,18 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-bool byte_map(CUtensorMap *m, const void *at, uint64_t rows, uint64_t row_bytes, uint64_t pitch, uint32_t box_rows) {
+bool box_map(CUtensorMap *m, const void *at, uint64_t rows, uint64_t row_bytes, uint64_t pitch, uint32_t box_bytes, uint32_t box_rows,
+             bool swizzled) {
     const auto fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[2] = {row_bytes, rows}, strides[1] = {pitch};
-    const cuuint32_t box[2] = {128, box_rows}, es[2] = {1, 1};
+    const cuuint32_t box[2] = {box_bytes, box_rows}, es[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(at), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              swizzled ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool byte_map(CUtensorMap *m, const void *at, uint64_t rows, uint64_t row_bytes, uint64_t pitch, uint32_t box_rows) {
+    return box_map(m, at, rows, row_bytes, pitch, 128, box_rows, true);
 }
 
 size_t q4_tc_workspace_bytes(int rows, int k) { return exponent_bytes(rows) + (size_t)rows * k * 2; }
