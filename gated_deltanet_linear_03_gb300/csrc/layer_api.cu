@@ -111,8 +111,8 @@ gdn_status gdn_short_conv(int n_seqs, int total_tokens, int channels, int width,
     if (act != GDN_CONV_NONE && act != GDN_CONV_SILU) return GDN_ERR_UNSUPPORTED;
     gdn_status st = check_sequences(n_seqs, total_tokens, cu_seqlens, state_in, state_out, slots, n_slots);
     if (st != GDN_OK) return st;
-    // CTAs are counted in 32 bits: a token and 1024 channels each at most
-    if (((double)n_seqs + total_tokens + 64) * ((channels + 1023) / 1024) >= 2147483648.0) return GDN_ERR_UNSUPPORTED;
+    // CTAs are counted in 32 bits: a token and 512 channels each at the least
+    if (((double)n_seqs + total_tokens + 64) * (channels / 512 + 1) >= 2147483648.0) return GDN_ERR_UNSUPPORTED;
     if (n_seqs == 0) return GDN_OK;
     if (!weight || (total_tokens > 0 && (!x || !out))) return GDN_ERR_INVALID_ARG;
     st = check_rows(x, x_stride, channels);

@@ -8,6 +8,45 @@
 
 namespace gdn {
 
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float reciprocal(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float silu(float z) { return z * reciprocal(1.f + ex2(-kLog2e * z)); }
+
+// Pairs of fp32 numbers in one 64-bit register: a product or fused product-sum of both is one instruction.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float x, float y) {
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void halves(Pair p, float &x, float &y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p)); }
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 // Sequences of one call, and the states that they carry.
 struct Sequences {
     int n, total;
@@ -132,10 +171,7 @@ __device__ __forceinline__ float ffn_argument(float u, int gelu) {
 __device__ __forceinline__ float ffn_act(float u, int gelu) { return u / (1.f + expf(-ffn_argument(u, gelu))); }
 // The same to 2^-19 for |v| < 32, where it is rounded to bf16 next.
 __device__ __forceinline__ float ffn_act_fast(float u, int gelu) {
-    float e, q;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * ffn_argument(u, gelu)));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.f + e));
-    return u * q;
+    return u * reciprocal(1.f + ex2(-kLog2e * ffn_argument(u, gelu)));
 }
 
 }  // namespace gdn

@@ -46,7 +46,7 @@ __device__ __forceinline__ float power_of_two(int e) { return __int_as_float((e 
 // What a warp reads of its rows at one slice comes by TMA into its own ring, kDeep slices ahead: no registers wait for memory, and a
 // row's place in a stage is a constant.  Scales come the same way where the rows of scales can be a tensor's (a multiple of
 // 16 bytes), else through registers, a slice ahead.
-constexpr int kDeep = 5;
+constexpr int kDeep = 3;
 template <int MATS>
 struct Stage {                             // each box begins on a 128-byte boundary
     uint2 code[kRows][32];                 // by lane
@@ -76,6 +76,38 @@ q4_vec_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ VecMa
     const int slice0 = ks * kSlices, slices = min(kSlices, (p.k + kSlice - 1) / kSlice - slice0);
     const int step = gridDim.x * together, turns = (p.n_out + OUT - 1) / OUT;
 
+    constexpr int MATS = GATED ? 2 : 1;
+    Stage<MATS> *ring = reinterpret_cast<Stage<MATS> *>(raw) + warp * kDeep;
+    volatile int *abort = &gave_up;
+    int turn = blockIdx.x * together + warp / kw, buffer = 0;
+    // every warp of a CTA goes through the same number of turns: its last ones may be beyond the matrix
+    const int rounds = (turns + step - 1) / step, total = rounds * max(slices, 0);
+    if (lane == 0) {
+        for (int i = 0; i < kDeep; ++i) mbar_init(&full[warp][i], 1);
+        if (warp == 0) gave_up = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    // the next slice to ask for
+    int ask_turn = turn, ask_slice = 0, asked = 0;
+    auto ask = [&](int place) {
+        if (asked++ < total && elect_one()) {
+            Stage<MATS> &to = ring[place];
+            const int col = (slice0 + ask_slice) * kSlice, row = ask_turn * OUT, group = (col / 64 >> shift) & ~7;
+            uint64_t *bar = &full[warp][place];
+            mbar_arrive_expect_tx(bar, kRows * (kSlice / 2 + (SCALE_TMA ? OFFSETS ? 32 : 16 : 0)));
+#pragma unroll
+            for (int m = 0; m < MATS; ++m) {                      // (the maps count bytes)
+                tma_load_2d(to.code[m * OUT], &maps.codes[m], bar, col / 2, row);
+                if (SCALE_TMA) {
+                    tma_load_2d(to.scale[m], &maps.scales[m], bar, 2 * group, row);
+                    if (OFFSETS) tma_load_2d(to.offset[m], &maps.offsets[m], bar, 2 * group, row);
+                }
+            }
+        }
+        if (++ask_slice == slices) ask_slice = 0, ask_turn += step;
+    };
+    for (int i = 0; i < kDeep; ++i) ask(i);
     // x at this lane's inputs as halves in the order of the codes' pairs, and its sum over the lane's group, both scaled
     uint32_t x[M][kSlices][8];
     float xsum[M][kSlices];
@@ -129,38 +161,6 @@ q4_vec_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ VecMa
         }
     }
 
-    constexpr int MATS = GATED ? 2 : 1;
-    Stage<MATS> *ring = reinterpret_cast<Stage<MATS> *>(raw) + warp * kDeep;
-    volatile int *abort = &gave_up;
-    int turn = blockIdx.x * together + warp / kw, buffer = 0;
-    // every warp of a CTA goes through the same number of turns: its last ones may be beyond the matrix
-    const int rounds = (turns + step - 1) / step, total = rounds * max(slices, 0);
-    if (lane == 0) {
-        for (int i = 0; i < kDeep; ++i) mbar_init(&full[warp][i], 1);
-        if (warp == 0) gave_up = 0;
-        fence_mbar_init();
-    }
-    __syncthreads();
-    // the next slice to ask for
-    int ask_turn = turn, ask_slice = 0, asked = 0;
-    auto ask = [&](int place) {
-        if (asked++ < total && elect_one()) {
-            Stage<MATS> &to = ring[place];
-            const int col = (slice0 + ask_slice) * kSlice, row = ask_turn * OUT, group = (col / 64 >> shift) & ~7;
-            uint64_t *bar = &full[warp][place];
-            mbar_arrive_expect_tx(bar, kRows * (kSlice / 2 + (SCALE_TMA ? OFFSETS ? 32 : 16 : 0)));
-#pragma unroll
-            for (int m = 0; m < MATS; ++m) {                      // (the maps count bytes)
-                tma_load_2d(to.code[m * OUT], &maps.codes[m], bar, col / 2, row);
-                if (SCALE_TMA) {
-                    tma_load_2d(to.scale[m], &maps.scales[m], bar, 2 * group, row);
-                    if (OFFSETS) tma_load_2d(to.offset[m], &maps.offsets[m], bar, 2 * group, row);
-                }
-            }
-        }
-        if (++ask_slice == slices) ask_slice = 0, ask_turn += step;
-    };
-    for (int i = 0; i < kDeep; ++i) ask(i);
     const auto scales_of = [&](Scales &q, int at_turn, int i) {
         const int group = min((slice0 + i) * kSlice + 16 * lane, p.k - 16) / 64 >> shift;          // (inputs beyond the last meet zeros of x)
 #pragma unroll

@@ -9,20 +9,6 @@ namespace gdn {
 namespace {
 
 constexpr int kScanThreads = 128;
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ float reciprocal(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // log(1 + e^v) = max(v, 0) + log(1 + e), e = e^-|v|, without a branch and to a few units in the last place however small e is.
 // The exponential's argument is corrected for its rounding; log(1 + e) = 2 artanh(q) with q = e / (2 + e) <= 1/3, by its series.
 __device__ __forceinline__ float softplus(float v) {
@@ -39,8 +25,6 @@ __device__ __forceinline__ float softplus(float v) {
     s = fmaf(q2, s, 1.f);
     return fmaf(2.f * q, s, fmaxf(v, 0.f));
 }
-
-__device__ __forceinline__ float silu(float z) { return z * reciprocal(1.f + ex2(-kLog2e * z)); }
 
 template <int S>
 __device__ __forceinline__ void load_state(const float *p, float (&h)[S]) {
@@ -106,24 +90,6 @@ __global__ void __launch_bounds__(kScanThreads) step_kernel(const __grid_constan
 }
 
 // ---------------------------------------------------------------------------------------------- prompts
-// Pairs of fp32 numbers in one 64-bit register: a product or fused product-sum of both is one instruction.
-using Pair = unsigned long long;
-__device__ __forceinline__ Pair pair(float x, float y) {
-    Pair r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ void halves(Pair p, float &x, float &y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p)); }
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-    Pair r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-    Pair r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 struct alignas(16) Pair2 { Pair x, y; };
 
 constexpr int kTile = 32;                   // tokens of one turn
