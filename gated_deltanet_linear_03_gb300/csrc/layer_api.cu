@@ -43,8 +43,8 @@ gdn_status check_scan_shape(int n_seqs, int total_tokens, int channels, int n_st
     if (n_seqs == 0 && total_tokens > 0) return GDN_ERR_INVALID_ARG;
     if (n_state != 16 && n_state != 32 && n_state != 64 && n_state != 128) return GDN_ERR_UNSUPPORTED;
     if (channels % 8 != 0 || channels % groups != 0 || channels / groups % 8 != 0) return GDN_ERR_UNSUPPORTED;
-    // CTAs are counted in 32 bits
-    if (((double)n_seqs + total_tokens) * (channels / 8) >= 2147483648.0) return GDN_ERR_UNSUPPORTED;
+    // warps, of 4 channels each at the least, are counted in 32 bits
+    if (((double)n_seqs + total_tokens + 64) * (channels / 4 + groups) >= 2147000000.0) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 

@@ -10,20 +10,24 @@ namespace {
 
 constexpr int kScanThreads = 128;
 // log(1 + e^v) = max(v, 0) + log(1 + e), e = e^-|v|, without a branch and to a few units in the last place however small e is.
-// The exponential's argument is corrected for its rounding; log(1 + e) = 2 artanh(q) with q = e / (2 + e) <= 1/3, by its series.
-__device__ __forceinline__ float softplus(float v) {
-    const float m = -fabsf(v), t = m * kLog2e;
-    const float r = fmaf(m, 1.925963033500e-8f, fmaf(m, kLog2e, -t));       // what t lacks of m log2 e
-    float e = ex2(t);
-    e = fmaf(e, r * 0.69314718f, e);
-    const float q = e * reciprocal(2.f + e), q2 = q * q;
-    float s = fmaf(q2, 1.f / 13, 1.f / 11);
-    s = fmaf(q2, s, 1.f / 9);
-    s = fmaf(q2, s, 1.f / 7);
-    s = fmaf(q2, s, 1.f / 5);
-    s = fmaf(q2, s, 1.f / 3);
-    s = fmaf(q2, s, 1.f);
-    return fmaf(2.f * q, s, fmaxf(v, 0.f));
+// The exponential's argument is corrected for its rounding; log(1 + e) = 2 artanh(q) with q = e / (2 + e) <= 1/3, by a
+// polynomial for artanh(q) / q in q^2 on [0, 1/9] whose largest relative error is least (Remez's exchange, 4e-9).
+__device__ __forceinline__ Pair softplus(Pair v) {
+    const auto both = [](float x) { return pair(x, x); };
+    float v0, v1, t0, t1;
+    halves(v, v0, v1);
+    const Pair m = pair(-fabsf(v0), -fabsf(v1)), t = mul2(m, both(kLog2e));
+    const Pair r = fma2(m, both(1.925963033500e-8f), fma2(m, both(kLog2e), t ^ 0x8000000080000000ull));       // what t lacks of m log2 e
+    halves(t, t0, t1);
+    Pair e = pair(ex2(t0), ex2(t1));
+    e = fma2(e, mul2(r, both(0.69314718f)), e);
+    halves(add2(e, both(2.f)), t0, t1);
+    const Pair q = mul2(e, pair(reciprocal(t0), reciprocal(t1))), q2 = mul2(q, q);
+    Pair s = fma2(q2, both(0.14089168f), both(0.13980301f));
+    s = fma2(q2, s, both(0.20012455f));
+    s = fma2(q2, s, both(0.33333157f));
+    s = fma2(q2, s, both(1.f));
+    return fma2(add2(q, q), s, pair(fmaxf(v0, 0.f), fmaxf(v1, 0.f)));
 }
 
 template <int S>
@@ -41,79 +45,109 @@ __device__ __forceinline__ void store_state(float *p, const float (&h)[S]) {
 }
 
 // ---------------------------------------------------------------------------------------------- single tokens
-// A thread takes 4 states of one channel of one sequence, and reads what it needs of a token itself.  Right for any number of
+// A thread takes 4 states each of two channels of one sequence, and reads what it needs of a token itself.  Right for any number of
 // tokens, meant for one.
 template <int N>
 __global__ void __launch_bounds__(kScanThreads) step_kernel(const __grid_constant__ ScanProblem p) {
     constexpr int LANES = N / 4, CH = kScanThreads / LANES;
-    const int ctas = (p.channels + CH - 1) / CH;
-    const int n = blockIdx.x / ctas, ch = blockIdx.x % ctas * CH + threadIdx.x / LANES, part = threadIdx.x % LANES;
+    const int ctas = (p.channels + 2 * CH - 1) / (2 * CH);
+    const int n = blockIdx.x / ctas, part = threadIdx.x % LANES, ch0 = blockIdx.x % ctas * 2 * CH + threadIdx.x / LANES;
     const int slot = p.seqs.slot(n);
     if (slot < 0) {
         if (threadIdx.x == 0) raise_error(p.seqs.err, kErrInternal);
         return;
     }
-    const bool live = ch < p.channels;       // the shuffles want whole warps
-    const int c = live ? ch : p.channels - 1;
-    const size_t at = ((size_t)slot * p.channels + c) * N + 4 * part;
-    float h[4] = {0.f, 0.f, 0.f, 0.f}, a[4];
-    if (p.state_in) load_state(p.state_in + at, h);
-    load4(p.a + (size_t)c * N + 4 * part, a);
-    const float bias = p.dt_bias ? p.dt_bias[c] : 0.f, skip = p.skip ? p.skip[c] : 0.f;
-    const int bc = c / (p.channels / p.groups) * N + 4 * part;
+    const int per_group = p.channels / p.groups;
+    bool live[2];
+    int c[2], bc[2];
+    size_t at[2];
+    float h[2][4], a[2][4], bias[2], skip[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        live[m] = ch0 + m * CH < p.channels;             // the shuffles want whole warps
+        c[m] = live[m] ? ch0 + m * CH : p.channels - 1;
+        at[m] = ((size_t)slot * p.channels + c[m]) * N + 4 * part;
+        bc[m] = c[m] / per_group * N + 4 * part;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[m][i] = 0.f;
+        if (p.state_in) load_state(p.state_in + at[m], h[m]);
+        load4(p.a + (size_t)c[m] * N + 4 * part, a[m]);
+        bias[m] = p.dt_bias ? __ldg(p.dt_bias + c[m]) : 0.f;
+        skip[m] = p.skip ? __ldg(p.skip + c[m]) : 0.f;
+    }
     for (int t = p.seqs.begin(n); t < p.seqs.end(n); ++t) {
-        const float x = __bfloat162float(p.x[t * p.x_stride + c]);
-        const float v = __bfloat162float(p.dt[t * p.dt_stride + c]) + bias, d = p.softplus ? softplus(v) : v;
-        const float z = p.z ? __bfloat162float(p.z[t * p.z_stride + c]) : 0.f;
-        const uint2 bw = *reinterpret_cast<const uint2 *>(p.b + t * p.b_stride + bc);
-        const uint2 cw = *reinterpret_cast<const uint2 *>(p.c + t * p.c_stride + bc);
-        const float b[4] = {bf16_lo(bw.x), bf16_hi(bw.x), bf16_lo(bw.y), bf16_hi(bw.y)};
-        const float cc[4] = {bf16_lo(cw.x), bf16_hi(cw.x), bf16_lo(cw.y), bf16_hi(cw.y)};
-        const float u = d * x, dl = d * kLog2e;
-        float y = 0.f;
+        float x[2], z[2] = {0.f, 0.f}, d[2];
+        uint2 bw[2], cw[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            h[i] = fmaf(ex2(dl * a[i]), h[i], u * b[i]);
-            y = fmaf(h[i], cc[i], y);
+        for (int m = 0; m < 2; ++m) {
+            x[m] = __bfloat162float(p.x[t * p.x_stride + c[m]]);
+            d[m] = __bfloat162float(p.dt[t * p.dt_stride + c[m]]) + bias[m];
+            if (p.z) z[m] = __bfloat162float(p.z[t * p.z_stride + c[m]]);
+            bw[m] = *reinterpret_cast<const uint2 *>(p.b + t * p.b_stride + bc[m]);
+            cw[m] = *reinterpret_cast<const uint2 *>(p.c + t * p.c_stride + bc[m]);
         }
+        if (p.softplus) halves(softplus(pair(d[0], d[1])), d[0], d[1]);
 #pragma unroll
-        for (int o = LANES / 2; o >= 1; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-        if (live && part == 0) {
-            y = fmaf(skip, x, y);
-            if (p.z) y *= silu(z);
-            const size_t to = (size_t)t * p.channels + c;
-            if (p.out_f32) static_cast<float *>(p.out)[to] = y;
-            else static_cast<__nv_bfloat16 *>(p.out)[to] = __float2bfloat16_rn(y);
+        for (int m = 0; m < 2; ++m) {
+            const float b[4] = {bf16_lo(bw[m].x), bf16_hi(bw[m].x), bf16_lo(bw[m].y), bf16_hi(bw[m].y)};
+            const float cc[4] = {bf16_lo(cw[m].x), bf16_hi(cw[m].x), bf16_lo(cw[m].y), bf16_hi(cw[m].y)};
+            const float u = d[m] * x[m], dl = d[m] * kLog2e;
+            float y = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                h[m][i] = fmaf(ex2(dl * a[m][i]), h[m][i], u * b[i]);
+                y = fmaf(h[m][i], cc[i], y);
+            }
+#pragma unroll
+            for (int o = LANES / 2; o >= 1; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+            if (live[m] && part == 0) {
+                y = fmaf(skip[m], x[m], y);
+                if (p.z) y *= silu(z[m]);
+                const size_t to = (size_t)t * p.channels + c[m];
+                if (p.out_f32) static_cast<float *>(p.out)[to] = y;
+                else static_cast<__nv_bfloat16 *>(p.out)[to] = __float2bfloat16_rn(y);
+            }
         }
     }
-    if (live && p.state_out) store_state(p.state_out + at, h);
+    if (!p.state_out) return;
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+        if (live[m]) store_state(p.state_out + at[m], h[m]);
 }
 
 // ---------------------------------------------------------------------------------------------- prompts
 struct alignas(16) Pair2 { Pair x, y; };
 
-constexpr int kTile = 32;                   // tokens of one turn
-constexpr int kPromptThreads = 256;         // 4 warps that scan, 4 that prepare the next tile and finish the last one
+constexpr int kPromptWarps = 4, kPromptThreads = 32 * kPromptWarps;      // of a CTA; each goes its own way
+constexpr int kPromptCtas = 3;              // CTAs an SM
 constexpr int kMaxPiece = 2048;             // tokens of a piece of a scan in pieces
+constexpr int kTile = 8;                    // tokens of a turn
+constexpr int kStores = 8;
 
-template <int N_, int S_>
+template <int N_>
 struct Shape {
-    static constexpr int N = N_, S = S_, LANES = N / S, V = 32 / LANES, CH = 4 * V;     // V: channels of a warp
-    // A tile's raw rows and vectors are asked for DEEP turns before it is prepared, to cover a read of memory; that of turn
-    // i + 1 + DEEP while tile i is scanned, so they need two places more.  (States of 128: two CTAs an SM leave room for less.)
-    static constexpr int DEEP = N == 128 ? 2 : 4, RING = DEEP + 2;
-    struct Tile {
-        float2 du[kTile][CH];               // step width D (times log2 e) and D x
-        float y[4 * kTile][36];             // by token and warp: the lanes' parts of y; 4 floats of padding against bank conflicts
+    static constexpr int N = N_;
+    // A lane scans 8 states of 2 neighbouring channels
+    static constexpr int LANES = N / 8, V = 64 / LANES;               // lanes of a channel pair; channels of a warp
+    // and prepares VH channels of one token (states of 128: half of the lanes do)
+    static constexpr int VH = V >= 8 ? V / 4 : 2, CHUNKS = V / VH;
+    // A tile's raw rows and vectors are asked for DEEP turns ahead, to cover a read of memory
+    static constexpr int DEEP = N == 128 ? 2 : 3, RING = DEEP + 1;
+    static constexpr int VECTORS = kTile * N / 8 < 32 ? 1 : kTile * N / 8 / 32;      // pieces of 8 entries of B that a lane copies
+    // B and C are widened to 32 bits once, or where they are used: a warp of few channels has too few uses for the former
+    static constexpr bool WIDE = N == 16;
+    struct Shared {                         // of a warp
+        float4 du[kTile][V / 2];            // of two channels: step width D (times log2 e) and D x
+        float4 y[kTile][16];                // by lane: its part of y, for two channels
+        float b[WIDE ? kTile : 1][N], c[WIDE ? kTile : 1][N];
+        uint4 braw[RING][kTile * N / 8], craw[RING][kTile * N / 8];           // as they came, in bf16
+        __nv_bfloat16 x[RING][32][VH], dt[RING][32][VH], z[RING][32][VH];      // by preparing lane
     };
-    struct Shared {
-        Tile tile[2];                       // prepared, and scanned
-        uint4 bc[RING][kTile][N / 4];      // by 4 states: B and C as they came, in bf16
-        __nv_bfloat16 x[RING][128][V], dt[RING][128][V], z[RING][128][V];      // by preparing thread
-    };
-    // Row id = 4 token + warp of V channels of du holds its pairs of channels in the order pair ^ key, so that 8 rows written at
-    // once meet few banks twice.
-    __device__ static __forceinline__ int key(int id) { return V == 8 ? (id >> 1) & 3 : V == 4 ? (id >> 2) & 1 : 0; }
+    // Of the 16-byte entries of du and y a preparing lane (token t, chunk c) has DU and Y next to one another; they are in the
+    // order entry ^ key, key = key of the chunk ^ key of the token, so that what 8 lanes touch at once lies in different banks.
+    static constexpr int DU = VH / 2, Y = 16 / CHUNKS;
+    __host__ __device__ static constexpr int du_key(int t, int chunk) { return DU == 4 ? 2 * (t & 1) ^ chunk >> 1 : DU == 2 ? t & 1 : 0; }
+    __host__ __device__ static constexpr int y_key(int t, int chunk) { return Y == 4 ? 2 * (t & 1) ^ chunk >> 1 : 2 * (t & 3) ^ chunk; }
 };
 
 // Copy BYTES (4, 8 or 16) to shared memory behind the thread's back, zeros where there is nothing to read.
@@ -131,258 +165,279 @@ template <int V> struct Bits { using T = uint4; };
 template <> struct Bits<4> { using T = uint2; };
 template <> struct Bits<2> { using T = uint32_t; };
 template <int V>
-__device__ __forceinline__ void unpack(const typename Bits<V>::T &u, float (&x)[V]) {
+__device__ __forceinline__ void unpack(const typename Bits<V>::T &u, Pair (&x)[V / 2]) {
     const uint32_t *w = reinterpret_cast<const uint32_t *>(&u);
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-        x[2 * i] = bf16_lo(w[i]);
-        x[2 * i + 1] = bf16_hi(w[i]);
-    }
+    for (int i = 0; i < V / 2; ++i) x[i] = pair(bf16_lo(w[i]), bf16_hi(w[i]));
 }
 
-// All of the CTA's warps meet here, those that scan and those that prepare, from different places.
-__device__ __forceinline__ void turn() { asm volatile("barrier.sync 1, %0;" ::"n"(kPromptThreads) : "memory"); }
-
-// Tokens [t0, t1) of one sequence for the CTA's channels c0 .. and below c1.  h: a scanning lane's part of its channel's
-// state; *width_sum: the sum of its step widths (times log2 e).
+// Tokens [t0, t1) of one sequence for the warp's channels c0 .. and below c1.  h: a lane's part of its channels' states;
+// width_sum: the sums of their step widths (times log2 e).
 template <class SH, bool WITH_Y>
 __device__ __forceinline__ void scan_tokens(const ScanProblem &p, typename SH::Shared &sh, int t0, int t1, int c0, int c1, int group,
-                                            const Pair (&a)[SH::S / 2], Pair (&h)[SH::S / 2], float *width_sum) {
-    constexpr int S = SH::S, N = SH::N, V = SH::V, LANES = SH::LANES;
-    const int n = (t1 - t0 + kTile - 1) / kTile;
-    if (n <= 0) return;
-    if (threadIdx.x < 128) {
-        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, part = lane % LANES;
-        float total = 0.f;
-        turn();
-        // Steps go by batches: a batch's exponentials depend on nothing but its inputs, which are asked for a batch ahead
-        constexpr int BATCH = S == 4 ? 4 : 2;
-        struct Step { float2 w; uint4 bc[S / 4]; };
-        const int ch = lane / LANES;
-        for (int i = 0; i < n; ++i) {
-            typename SH::Tile &s = sh.tile[i & 1];
-            const float2 *du = &s.du[0][warp * V];
-            const uint4 *bc = &sh.bc[i % SH::RING][0][S / 4 * part];
-            float *y = &s.y[warp][lane];
-            auto fetch = [&](int t, Step (&q)[BATCH]) {
+                                            const Pair (&a)[2][4], Pair (&h)[2][4], float (&width_sum)[2]) {
+    constexpr int N = SH::N, LANES = SH::LANES, VH = SH::VH, CHUNKS = SH::CHUNKS;
+    using T = typename Bits<VH>::T;
+    const int n = (t1 - t0 + kTile - 1) / kTile, lane = threadIdx.x % 32;
+    width_sum[0] = width_sum[1] = 0.f;
+    // as a preparing lane: one token's VH channels
+    const int my_t = lane / CHUNKS, chunk = lane % CHUNKS, c = c0 + VH * chunk;
+    const bool live = my_t < kTile && c < c1;
+    Pair bias[VH / 2], skip[VH / 2];
 #pragma unroll
-                for (int j = 0; j < BATCH; ++j) {
-                    q[j].w = du[(t + j) * SH::CH + (ch ^ 2 * SH::key(4 * (t + j) + warp))];
-#pragma unroll
-                    for (int k = 0; k < S / 4; ++k) {
-                        const uint4 *from = bc + (t + j) * (N / 4) + k;
-                        if (WITH_Y) q[j].bc[k] = *from;
-                        else {
-                            const uint2 only = *reinterpret_cast<const uint2 *>(from);
-                            q[j].bc[k].x = only.x, q[j].bc[k].y = only.y;
-                        }
-                    }
-                }
-            };
-            Step next[BATCH];
-            fetch(0, next);
-#pragma unroll
-            for (int t = 0; t < kTile; t += BATCH) {
-                Step q[BATCH];
-#pragma unroll
-                for (int j = 0; j < BATCH; ++j) q[j] = next[j];
-                if (t + BATCH < kTile) fetch(t + BATCH, next);
-                Pair decay[BATCH][S / 2];
-#pragma unroll
-                for (int j = 0; j < BATCH; ++j) {
-                    const Pair w = pair(q[j].w.x, q[j].w.x);
-#pragma unroll
-                    for (int k = 0; k < S / 2; ++k) {
-                        float e0, e1;
-                        halves(mul2(w, a[k]), e0, e1);
-                        decay[j][k] = pair(ex2(e0), ex2(e1));
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < BATCH; ++j) {
-                    const Pair u = pair(q[j].w.y, q[j].w.y);
-                    Pair sum = 0;
-#pragma unroll
-                    for (int k = 0; k < S / 2; ++k) {
-                        const uint32_t b = k & 1 ? q[j].bc[k / 2].y : q[j].bc[k / 2].x;
-                        h[k] = fma2(decay[j][k], h[k], mul2(u, pair(bf16_lo(b), bf16_hi(b))));
-                        if (WITH_Y) {
-                            const uint32_t c = k & 1 ? q[j].bc[k / 2].w : q[j].bc[k / 2].z;
-                            const Pair cv = pair(bf16_lo(c), bf16_hi(c));
-                            sum = k ? fma2(h[k], cv, sum) : mul2(h[k], cv);
-                        }
-                    }
-                    if (WITH_Y) {
-                        float lo, hi;
-                        halves(sum, lo, hi);
-                        y[(t + j) * 4 * 36] = lo + hi;
-                    } else {
-                        total += q[j].w.x;
-                    }
-                }
-            }
-            turn();
-        }
-        if (!WITH_Y) *width_sum = total;
-        return;
+    for (int e = 0; e < VH / 2; ++e) {
+        const float2 zero = make_float2(0.f, 0.f);
+        const float2 b = live && p.dt_bias ? __ldg(reinterpret_cast<const float2 *>(p.dt_bias + c) + e) : zero;
+        const float2 k = live && WITH_Y && p.skip ? __ldg(reinterpret_cast<const float2 *>(p.skip + c) + e) : zero;
+        bias[e] = pair(b.x, b.y);
+        skip[e] = pair(k.x, k.y);
     }
-    const int id = threadIdx.x - 128, c = c0 + V * (id % 4);
-    const bool live = c < c1;
-    float bias[V], skip[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-        bias[e] = live && p.dt_bias ? __ldg(p.dt_bias + c + e) : 0.f;
-        skip[e] = live && WITH_Y && p.skip ? __ldg(p.skip + c + e) : 0.f;
-    }
-    using T = typename Bits<V>::T;
+    // what this lane asks for next
+    const bool copies = 32 <= kTile * N / 8 || lane < kTile * N / 8;
+    const int vec_t = lane / (N / 8);
+    long long at_x = (long long)(t0 + my_t) * p.x_stride + c, at_dt = (long long)(t0 + my_t) * p.dt_stride + c;
+    long long at_z = (long long)(t0 + my_t) * p.z_stride + c;
+    long long at_b = (long long)(t0 + vec_t) * p.b_stride + group * N + lane % (N / 8) * 8;
+    long long at_c = (long long)(t0 + vec_t) * p.c_stride + group * N + lane % (N / 8) * 8;
     auto ask = [&](int i) {
         if (i < n) {
-            const int t = t0 + i * kTile + id / 4, slot = i % SH::RING;
-            const bool there = live && t < t1;
-            copy_async<2 * V>(sh.x[slot][id], p.x + (there ? t * p.x_stride + c : 0), there);
-            copy_async<2 * V>(sh.dt[slot][id], p.dt + (there ? t * p.dt_stride + c : 0), there);
-            if (WITH_Y && p.z) copy_async<2 * V>(sh.z[slot][id], p.z + (there ? t * p.z_stride + c : 0), there);
+            const int left = t1 - (t0 + i * kTile), slot = i % SH::RING;
+            const bool there = live && my_t < left;
+            copy_async<2 * VH>(sh.x[slot][lane], p.x + (there ? at_x : 0), there);
+            copy_async<2 * VH>(sh.dt[slot][lane], p.dt + (there ? at_dt : 0), there);
+            if (WITH_Y && p.z) copy_async<2 * VH>(sh.z[slot][lane], p.z + (there ? at_z : 0), there);
+            if (copies) {
 #pragma unroll
-            for (int k = 0; k < N / 16; ++k) {
-                const int at = id + k * 128, tv = t0 + i * kTile + at / (N / 4), e = group * N + at % (N / 4) * 4;
-                uint2 *to = reinterpret_cast<uint2 *>(&sh.bc[slot][0][at]);
-                copy_async<8>(to, p.b + (tv < t1 ? tv * p.b_stride + e : 0), tv < t1);
-                if (WITH_Y) copy_async<8>(to + 1, p.c + (tv < t1 ? tv * p.c_stride + e : 0), tv < t1);
+                for (int k = 0; k < SH::VECTORS; ++k) {
+                    const int row = k * 32 / (N / 8);
+                    const bool held = vec_t + row < left;
+                    copy_async<16>(&sh.braw[slot][lane + 32 * k], p.b + (held ? at_b + row * p.b_stride : 0), held);
+                    if (WITH_Y) copy_async<16>(&sh.craw[slot][lane + 32 * k], p.c + (held ? at_c + row * p.c_stride : 0), held);
+                }
             }
+            at_x += kTile * p.x_stride;
+            at_dt += kTile * p.dt_stride;
+            at_b += kTile * p.b_stride;
+            if (WITH_Y) at_z += kTile * p.z_stride, at_c += kTile * p.c_stride;
         }
         copy_commit();                      // (a group for every turn, so that their number says which have arrived)
     };
-    T x1{}, z1{}, x0{}, z0{};               // of the tile that is scanned, and of the one before it
-    auto prepare = [&](int i) {
-        typename SH::Tile &s = sh.tile[i & 1];
-        copy_wait<SH::DEEP - 1>();
+    // as a scanning lane: where its channels' entry of du is, and its half of an entry of y
+    const int entry = lane / LANES, part = lane % LANES, du_chunk = entry / SH::DU, y_chunk = lane / 2 / SH::Y;
+    for (int i = 0; i < SH::DEEP; ++i) ask(i);
+    for (int i = 0; i < n; ++i) {
         const int slot = i % SH::RING;
-        const T xr = *reinterpret_cast<const T *>(sh.x[slot][id]), dr = *reinterpret_cast<const T *>(sh.dt[slot][id]);
-        x0 = x1, z0 = z1, x1 = xr;
-        if (WITH_Y && p.z) z1 = *reinterpret_cast<const T *>(sh.z[slot][id]);
-        float x[V], d[V];
-        unpack<V>(xr, x);
-        unpack<V>(dr, d);
-        const bool inside = t0 + i * kTile + id / 4 < t1;
-        float4 *to = reinterpret_cast<float4 *>(&s.du[id / 4][V * (id % 4)]);
-        const int key = SH::key(id);
-#pragma unroll
-        for (int e = 0; e < V; ++e) d[e] += bias[e];
-        if (p.softplus) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) d[e] = softplus(d[e]);
-        }
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            d[e] = inside ? d[e] : 0.f;                               // (a row beyond the end changes nothing)
-            x[e] *= d[e];
-            d[e] *= kLog2e;
-        }
-#pragma unroll
-        for (int e = 0; e < V / 2; ++e) to[e ^ key] = make_float4(d[2 * e], x[2 * e], d[2 * e + 1], x[2 * e + 1]);
+        copy_wait<SH::DEEP - 1>();
+        __syncwarp();                       // the tile has arrived for all lanes, and all are done with the one before
         ask(i + SH::DEEP);
-    };
-    auto finish = [&](int i, const T &xr, const T &zr) {
-        const int t = t0 + i * kTile + id / 4;
-        if (!WITH_Y || !live || t >= t1) return;
-        float x[V], z[V], y[V];
-        unpack<V>(xr, x);
-        unpack<V>(zr, z);
-        const float *from = sh.tile[i & 1].y[id];
+        const T xr = *reinterpret_cast<const T *>(sh.x[slot][lane]);
+        if (SH::WIDE && copies) {
+            const auto widen = [&](const uint4 *from, float *to) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            float q[LANES];
+                for (int k = 0; k < SH::VECTORS; ++k) {
+                    float f[8];
+                    unpack8(from[lane + 32 * k], f);
+                    float4 *o = reinterpret_cast<float4 *>(to + 8 * (lane + 32 * k));
+                    o[0] = make_float4(f[0], f[1], f[2], f[3]);
+                    o[1] = make_float4(f[4], f[5], f[6], f[7]);
+                }
+            };
+            widen(sh.braw[slot], sh.b[0]);
+            if (WITH_Y) widen(sh.craw[slot], sh.c[0]);
+        }
+        T zr{};
+        if (WITH_Y && p.z) zr = *reinterpret_cast<const T *>(sh.z[slot][lane]);
+        {
+            Pair x[VH / 2], d[VH / 2];
+            unpack<VH>(xr, x);
+            unpack<VH>(*reinterpret_cast<const T *>(sh.dt[slot][lane]), d);
 #pragma unroll
-            for (int k = 0; k < LANES / 4; ++k) {
-                const float4 f = *reinterpret_cast<const float4 *>(from + e * LANES + 4 * k);
-                q[4 * k] = f.x; q[4 * k + 1] = f.y; q[4 * k + 2] = f.z; q[4 * k + 3] = f.w;
+            for (int e = 0; e < VH / 2; ++e) d[e] = add2(d[e], bias[e]);
+            if (p.softplus) {
+#pragma unroll
+                for (int e = 0; e < VH / 2; ++e) d[e] = softplus(d[e]);
+            }
+            if (t0 + i * kTile + my_t >= t1) {
+#pragma unroll
+                for (int e = 0; e < VH / 2; ++e) d[e] = 0;            // (a row beyond the end changes nothing)
+            }
+            const int key = SH::du_key(my_t, chunk);
+            if (32 == kTile * CHUNKS || my_t < kTile) {
+                float4 *to = &sh.du[my_t][SH::DU * chunk];
+#pragma unroll
+                for (int e = 0; e < VH / 2; ++e) {
+                    float w0, w1, u0, u1;
+                    halves(mul2(d[e], x[e]), u0, u1);
+                    halves(mul2(d[e], pair(kLog2e, kLog2e)), w0, w1);
+                    to[e ^ key] = make_float4(w0, u0, w1, u1);
+                }
+            }
+        }
+        __syncwarp();
+        const float *bv = &sh.b[0][8 * part], *cv = &sh.c[0][8 * part];
+        const uint4 *bw = &sh.braw[slot][part], *cw = &sh.craw[slot][part];
+        float2 *y = reinterpret_cast<float2 *>(&sh.y[0][y_chunk * SH::Y]) + lane % 2;
+        // y is stored once for several tokens: the next tokens' reads are not ordered behind it
+        float2 outs[kStores];
+#pragma unroll
+        for (int t = 0; t < kTile; ++t) {
+            const float4 q = sh.du[t][du_chunk * SH::DU + (entry % SH::DU ^ SH::du_key(t, du_chunk))];
+            Pair decay[2][4], b[4], cc[4];
+            if constexpr (SH::WIDE) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const Pair2 f = *reinterpret_cast<const Pair2 *>(bv + t * N + 4 * k);
+                    b[2 * k] = f.x, b[2 * k + 1] = f.y;
+                    if (WITH_Y) {
+                        const Pair2 f = *reinterpret_cast<const Pair2 *>(cv + t * N + 4 * k);
+                        cc[2 * k] = f.x, cc[2 * k + 1] = f.y;
+                    }
+                }
+            } else {
+                unpack<8>(bw[t * (N / 8)], b);
+                if (WITH_Y) unpack<8>(cw[t * (N / 8)], cc);
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const float wv = m ? q.z : q.x;
+                const Pair w = pair(wv, wv);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float e0, e1;
+                    halves(mul2(w, a[m][k]), e0, e1);
+                    decay[m][k] = pair(ex2(e0), ex2(e1));
+                }
+                if (!WITH_Y) width_sum[m] += wv;
+            }
+            float2 &out = outs[t % kStores];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const float uv = m ? q.w : q.y;
+                const Pair u = pair(uv, uv);
+                Pair sum = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    h[m][k] = fma2(decay[m][k], h[m][k], mul2(u, b[k]));
+                    if (WITH_Y) sum = k ? fma2(h[m][k], cc[k], sum) : mul2(h[m][k], cc[k]);
+                }
+                if (WITH_Y) {
+                    float lo, hi;
+                    halves(sum, lo, hi);
+                    (m ? out.y : out.x) = lo + hi;
+                }
+            }
+            if (WITH_Y && t % kStores == kStores - 1) {
+#pragma unroll
+                for (int j = 0; j < kStores; ++j) {
+                    const int tt = t - (kStores - 1) + j;
+                    y[2 * (tt * 16 + (lane / 2 % SH::Y ^ SH::y_key(tt, y_chunk)))] = outs[j];
+                }
+            }
+        }
+        __syncwarp();
+        const int t = t0 + i * kTile + my_t;
+        if (!WITH_Y || !live || t >= t1) continue;
+        Pair x[VH / 2], yv[VH / 2];
+        unpack<VH>(xr, x);
+        // a channel pair's parts, LANES of them, fill LANES / 2 entries
+        const float4 *from = &sh.y[my_t][SH::Y * chunk];
+        const int key = SH::y_key(my_t, chunk);
+#pragma unroll
+        for (int e = 0; e < VH / 2; ++e) {
+            Pair q[LANES];
+#pragma unroll
+            for (int k = 0; k < LANES / 2; ++k) {
+                const Pair2 f = *reinterpret_cast<const Pair2 *>(from + ((e * (LANES / 2) + k) ^ key));
+                q[2 * k] = f.x;
+                q[2 * k + 1] = f.y;
             }
 #pragma unroll
             for (int o = LANES / 2; o >= 1; o >>= 1)
 #pragma unroll
-                for (int k = 0; k < o; ++k) q[k] += q[k + o];
-            y[e] = fmaf(skip[e], x[e], q[0]);
+                for (int k = 0; k < o; ++k) q[k] = add2(q[k], q[k + o]);
+            yv[e] = fma2(skip[e], x[e], q[0]);
         }
         if (p.z) {
+            Pair z[VH / 2];
+            unpack<VH>(zr, z);
 #pragma unroll
-            for (int e = 0; e < V; ++e) y[e] *= silu(z[e]);
+            for (int e = 0; e < VH / 2; ++e) {                        // z / (1 + e^-z)
+                float lo, hi;
+                halves(mul2(z[e], pair(-kLog2e, -kLog2e)), lo, hi);
+                halves(add2(pair(ex2(lo), ex2(hi)), pair(1.f, 1.f)), lo, hi);
+                yv[e] = mul2(yv[e], mul2(z[e], pair(reciprocal(lo), reciprocal(hi))));
+            }
         }
         const size_t to = (size_t)t * p.channels + c;
-        if (p.out_f32) {
-            float2 *o = reinterpret_cast<float2 *>(static_cast<float *>(p.out) + to);
+        T o;
+        uint32_t *w = reinterpret_cast<uint32_t *>(&o);
 #pragma unroll
-            for (int k = 0; k < V / 2; ++k) o[k] = make_float2(y[2 * k], y[2 * k + 1]);
-        } else {
-            T o;
-            uint32_t *w = reinterpret_cast<uint32_t *>(&o);
-#pragma unroll
-            for (int k = 0; k < V / 2; ++k) w[k] = pack2(y[2 * k], y[2 * k + 1]);
-            *reinterpret_cast<T *>(static_cast<__nv_bfloat16 *>(p.out) + to) = o;
+        for (int k = 0; k < VH / 2; ++k) {
+            float lo, hi;
+            halves(yv[k], lo, hi);
+            if (p.out_f32) reinterpret_cast<float2 *>(static_cast<float *>(p.out) + to)[k] = make_float2(lo, hi);
+            else w[k] = pack2(lo, hi);
         }
-    };
-    for (int i = 0; i < SH::DEEP; ++i) ask(i);
-    prepare(0);
-    turn();
-    for (int i = 0; i < n; ++i) {
-        // x1, z1 are tile i's; after prepare(i + 1) they are x0, z0
-        const T xp = x0, zp = z0;
-        if (i + 1 < n) prepare(i + 1);
-        else x0 = x1, z0 = z1;
-        if (i > 0) finish(i - 1, xp, zp);
-        turn();
+        if (!p.out_f32) *reinterpret_cast<T *>(static_cast<__nv_bfloat16 *>(p.out) + to) = o;
     }
-    finish(n - 1, x0, z0);
+    __syncwarp();                           // what is in shared memory has been read
 }
 
-// How a call's tokens are divided among CTAs.
+// How a call's tokens are divided among warps.
 struct ScanPlan {
-    int piece;                  // tokens of a piece; 0: a CTA takes whole sequences
-    int pieces, empty;          // pieces, and further CTAs that look for sequences without tokens
-    int ctas_per_group;
+    int piece;                  // tokens of a piece; 0: a warp takes whole sequences
+    int pieces, empty;          // pieces, and further warps that look for sequences without tokens
+    int units;                  // sequences, or pieces and those further ones
+    int warps_per_group;
     float *ends, *widths, *begins;     // [pieces, channels, N], [pieces, channels], [pieces, channels, N]
 };
-constexpr int kEmptyPerCta = 64;
+constexpr int kEmptyPerWarp = 64;
 
 enum Pass { kWhole, kEnds, kOutputs };
 
 template <class SH, int PASS>
-__global__ void __launch_bounds__(kPromptThreads, 2) scan_kernel(const __grid_constant__ ScanProblem p, const __grid_constant__ ScanPlan plan) {
+__global__ void __launch_bounds__(kPromptThreads, kPromptCtas) scan_kernel(const __grid_constant__ ScanProblem p, const __grid_constant__ ScanPlan plan) {
     extern __shared__ __align__(16) unsigned char smem[];
-    typename SH::Shared &sh = *reinterpret_cast<typename SH::Shared *>(smem);
-    constexpr int N = SH::N, S = SH::S;
-    const int per_group = p.channels / p.groups, ctas = plan.ctas_per_group * p.groups;
-    const int unit = blockIdx.x / ctas, group = blockIdx.x % ctas / plan.ctas_per_group;
-    const int c0 = group * per_group + blockIdx.x % plan.ctas_per_group * SH::CH, c1 = (group + 1) * per_group;
-    // of a scanning lane: its channel and where its states lie in an array [.., channels, N]
-    const int c = c0 + threadIdx.x / SH::LANES, part = threadIdx.x % SH::LANES;
-    const bool live = threadIdx.x < 128 && c < c1;
-    const size_t at = (size_t)c * N + S * part, all = (size_t)p.channels * N;
-    Pair h[S / 2], a[S / 2];
-    auto load = [&](const float *from, Pair (&v)[S / 2]) {
+    typename SH::Shared &sh = reinterpret_cast<typename SH::Shared *>(smem)[threadIdx.x / 32];
+    constexpr int N = SH::N;
+    const int per_group = p.channels / p.groups, warps = plan.warps_per_group * p.groups, lane = threadIdx.x % 32;
+    const int w = blockIdx.x * kPromptWarps + threadIdx.x / 32, unit = w / warps, group = w % warps / plan.warps_per_group;
+    if (unit >= plan.units) return;
+    const int c0 = group * per_group + w % plan.warps_per_group * SH::V, c1 = (group + 1) * per_group;
+    // of a scanning lane: its two channels and where their states lie in an array [.., channels, N]
+    const int c = c0 + 2 * (lane / SH::LANES), part = lane % SH::LANES;
+    const bool live = c < c1;
+    const size_t at = (size_t)c * N + 8 * part, all = (size_t)p.channels * N;
+    Pair h[2][4], a[2][4];
+    auto load = [&](const float *from, Pair (&v)[2][4]) {
 #pragma unroll
-        for (int k = 0; k < S / 4; ++k) {
-            const Pair2 q = from && live ? *reinterpret_cast<const Pair2 *>(from + at + 4 * k) : Pair2{0, 0};
-            v[2 * k] = q.x;
-            v[2 * k + 1] = q.y;
-        }
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const Pair2 q = from && live ? *reinterpret_cast<const Pair2 *>(from + at + m * N + 4 * k) : Pair2{0, 0};
+                v[m][2 * k] = q.x;
+                v[m][2 * k + 1] = q.y;
+            }
     };
-    auto store = [&](float *to, const Pair (&v)[S / 2]) {
+    auto store = [&](float *to, const Pair (&v)[2][4]) {
         if (!live) return;
 #pragma unroll
-        for (int k = 0; k < S / 4; ++k) *reinterpret_cast<Pair2 *>(to + at + 4 * k) = Pair2{v[2 * k], v[2 * k + 1]};
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) *reinterpret_cast<Pair2 *>(to + at + m * N + 4 * k) = Pair2{v[m][2 * k], v[m][2 * k + 1]};
     };
     auto state_in = [&](int slot) { return p.state_in ? p.state_in + slot * all : nullptr; };
     load(p.a, a);
-    float width_sum;
+    float width_sum[2];
 
     if (PASS == kWhole) {
         const int slot = p.seqs.slot(unit);
         if (slot < 0) {
-            if (threadIdx.x == 0) raise_error(p.seqs.err, kErrInternal);
+            if (lane == 0) raise_error(p.seqs.err, kErrInternal);
             return;
         }
         load(state_in(slot), h);
-        scan_tokens<SH, true>(p, sh, p.seqs.begin(unit), p.seqs.end(unit), c0, c1, group, a, h, &width_sum);
+        scan_tokens<SH, true>(p, sh, p.seqs.begin(unit), p.seqs.end(unit), c0, c1, group, a, h, width_sum);
         if (p.state_out) store(p.state_out + slot * all, h);
         return;
     }
@@ -394,18 +449,18 @@ __global__ void __launch_bounds__(kPromptThreads, 2) scan_kernel(const __grid_co
         if (p.seqs.end(n) <= t1 || b >= t1 || slot < 0) return;
         load(b >= t0 ? state_in(slot) : nullptr, h);
         if (b >= t0 && p.state_in) store(plan.begins + unit * all, h);       // (state_out may be state_in, and is written by others)
-        scan_tokens<SH, false>(p, sh, max(b, t0), t1, c0, c1, group, a, h, &width_sum);
+        scan_tokens<SH, false>(p, sh, max(b, t0), t1, c0, c1, group, a, h, width_sum);
         store(plan.ends + unit * all, h);
-        if (live && part == 0) plan.widths[(size_t)unit * p.channels + c] = width_sum;
+        if (live && part == 0) *reinterpret_cast<float2 *>(plan.widths + (size_t)unit * p.channels + c) = make_float2(width_sum[0], width_sum[1]);
         return;
     }
     if (unit >= plan.pieces) {
-        const int first = (unit - plan.pieces) * kEmptyPerCta;
-        for (int n = first; n < min(first + kEmptyPerCta, p.seqs.n); ++n) {
+        const int first = (unit - plan.pieces) * kEmptyPerWarp;
+        for (int n = first; n < min(first + kEmptyPerWarp, p.seqs.n); ++n) {
             if (p.seqs.end(n) > p.seqs.begin(n)) continue;
             const int slot = p.seqs.slot(n);
             if (slot < 0) {
-                if (threadIdx.x == 0) raise_error(p.seqs.err, kErrInternal);
+                if (lane == 0) raise_error(p.seqs.err, kErrInternal);
                 continue;
             }
             load(state_in(slot), h);
@@ -420,72 +475,72 @@ __global__ void __launch_bounds__(kPromptThreads, 2) scan_kernel(const __grid_co
             continue;
         }
         if (slot < 0) {
-            if (threadIdx.x == 0) raise_error(p.seqs.err, kErrInternal);
+            if (lane == 0) raise_error(p.seqs.err, kErrInternal);
             continue;
         }
         if (b >= t0) {
             load(e > t1 && p.state_in ? plan.begins + unit * all : state_in(slot), h);
         } else {
 #pragma unroll
-            for (int k = 0; k < S / 2; ++k) h[k] = 0;
+            for (int k = 0; k < 8; ++k) h[k / 4][k % 4] = 0;
 #pragma unroll 4
             for (int j = b / plan.piece; j < unit; ++j) {
-                Pair end[S / 2];
+                Pair end[2][4];
                 load(plan.ends + j * all, end);
-                const float w = live ? plan.widths[(size_t)j * p.channels + c] : 0.f;
+                const float2 w = live ? *reinterpret_cast<const float2 *>(plan.widths + (size_t)j * p.channels + c) : make_float2(0.f, 0.f);
 #pragma unroll
-                for (int k = 0; k < S / 2; ++k) {
+                for (int k = 0; k < 8; ++k) {
                     float e0, e1;
-                    halves(mul2(pair(w, w), a[k]), e0, e1);
-                    h[k] = fma2(pair(ex2(e0), ex2(e1)), h[k], end[k]);
+                    const float wv = k < 4 ? w.x : w.y;
+                    halves(mul2(pair(wv, wv), a[k / 4][k % 4]), e0, e1);
+                    h[k / 4][k % 4] = fma2(pair(ex2(e0), ex2(e1)), h[k / 4][k % 4], end[k / 4][k % 4]);
                 }
             }
         }
-        scan_tokens<SH, true>(p, sh, max(b, t0), min(e, t1), c0, c1, group, a, h, &width_sum);
+        scan_tokens<SH, true>(p, sh, max(b, t0), min(e, t1), c0, c1, group, a, h, width_sum);
         if (e <= t1 && p.state_out) store(p.state_out + slot * all, h);
         t = e;
     }
 }
 
-// S: states of a lane.
-template <int N> struct ShapeOf { using T = Shape<N, N == 128 ? 8 : 4>; };
-
 template <int N>
 ScanPlan plan_scan(int n_seqs, int total, int channels, int groups, int max_len) {
-    using SH = typename ShapeOf<N>::T;
+    using SH = Shape<N>;
     ScanPlan s{};
-    s.ctas_per_group = (channels / groups + SH::CH - 1) / SH::CH;
-    const long ctas = (long)s.ctas_per_group * groups, at_once = 2L * multiprocessor_count();
+    s.warps_per_group = (channels / groups + SH::V - 1) / SH::V;
+    s.units = n_seqs;
+    const long warps = (long)s.warps_per_group * groups, at_once = (long)kPromptCtas * kPromptWarps * multiprocessor_count();
     const long longest = max_len > 0 && max_len < total ? max_len : total;
-    // Tokens that one CTA walks through, one after another: whole sequences, or pieces twice
-    const long whole = max(longest, (long)total * ctas / at_once);
-    const long halves = 2 * max(64L, (long)total * ctas / at_once);
+    // Tokens that one warp walks through, one after another: whole sequences, or pieces twice
+    const long whole = max(longest, (long)total * warps / at_once);
+    const long halves = 2 * max(64L, (long)total * warps / at_once);
     if (whole <= halves * 5 / 4) return s;
-    const long pieces = max(1L, at_once / ctas);
+    const long pieces = max(1L, at_once / warps);
     long piece = ((total + pieces - 1) / pieces + kTile - 1) / kTile * kTile;
     piece = min((long)kMaxPiece, max(64L, piece));
     s.piece = (int)piece;
-    s.pieces = (int)((total + piece - 1) / piece);
+    s.units = s.pieces = (int)((total + piece - 1) / piece);
     return s;
 }
 
 template <int N>
 cudaError_t launch(const ScanProblem &p) {
-    using SH = typename ShapeOf<N>::T;
+    using SH = Shape<N>;
     if (!p.seqs.cu || p.max_len == 1) {
-        constexpr int CH = kScanThreads / (N / 4);
+        constexpr int CH = 2 * kScanThreads / (N / 4);
         const long ctas = (long)((p.channels + CH - 1) / CH) * p.seqs.n;
         step_kernel<N><<<(unsigned)ctas, kScanThreads, 0, p.stream>>>(p);
         return cudaGetLastError();
     }
-    constexpr int smem = (int)sizeof(typename SH::Shared);
+    constexpr int smem = kPromptWarps * (int)sizeof(typename SH::Shared);
     ScanPlan s = plan_scan<N>(p.seqs.n, p.seqs.total, p.channels, p.groups, p.max_len);
-    const long ctas = (long)s.ctas_per_group * p.groups;
+    const long warps = (long)s.warps_per_group * p.groups;
     using Fn = void (*)(const ScanProblem, const ScanPlan);
     auto run = [&](Fn fn, long units) {
         const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        fn<<<(unsigned)(units * ctas), kPromptThreads, smem, p.stream>>>(p, s);
+        s.units = (int)units;
+        fn<<<(unsigned)((units * warps + kPromptWarps - 1) / kPromptWarps), kPromptThreads, smem, p.stream>>>(p, s);
         return cudaGetLastError();
     };
     if (s.piece == 0) return run(scan_kernel<SH, kWhole>, p.seqs.n);
@@ -493,7 +548,7 @@ cudaError_t launch(const ScanProblem &p) {
     s.ends = static_cast<float *>(p.workspace);
     s.begins = s.ends + states;
     s.widths = s.begins + states;
-    if (p.state_out && p.state_out != p.state_in) s.empty = (p.seqs.n + kEmptyPerCta - 1) / kEmptyPerCta;
+    if (p.state_out && p.state_out != p.state_in) s.empty = (p.seqs.n + kEmptyPerWarp - 1) / kEmptyPerWarp;
     const cudaError_t e = run(scan_kernel<SH, kEnds>, s.pieces);
     return e != cudaSuccess ? e : run(scan_kernel<SH, kOutputs>, s.pieces + s.empty);
 }
