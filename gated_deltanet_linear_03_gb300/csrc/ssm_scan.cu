@@ -45,74 +45,95 @@ __device__ __forceinline__ void store_state(float *p, const float (&h)[S]) {
 }
 
 // ---------------------------------------------------------------------------------------------- single tokens
-// A thread takes 4 states each of two channels of one sequence, and reads what it needs of a token itself.  Right for any number of
+// A thread takes 4 states each of two channels, and sequences n, n + step, ... one after another, the next one's states on their way
+// while one is worked on: the channels' parameters are read once.  It reads what it needs of a token itself.  Right for any number of
 // tokens, meant for one.
 template <int N>
-__global__ void __launch_bounds__(kScanThreads) step_kernel(const __grid_constant__ ScanProblem p) {
+__global__ void __launch_bounds__(kScanThreads) step_kernel(const __grid_constant__ ScanProblem p, int step) {
     constexpr int LANES = N / 4, CH = kScanThreads / LANES;
     const int ctas = (p.channels + 2 * CH - 1) / (2 * CH);
-    const int n = blockIdx.x / ctas, part = threadIdx.x % LANES, ch0 = blockIdx.x % ctas * 2 * CH + threadIdx.x / LANES;
-    const int slot = p.seqs.slot(n);
-    if (slot < 0) {
-        if (threadIdx.x == 0) raise_error(p.seqs.err, kErrInternal);
-        return;
-    }
+    const int part = threadIdx.x % LANES, ch0 = blockIdx.x % ctas * 2 * CH + threadIdx.x / LANES;
     const int per_group = p.channels / p.groups;
+    const size_t all = (size_t)p.channels * N;
     bool live[2];
     int c[2], bc[2];
     size_t at[2];
-    float h[2][4], a[2][4], bias[2], skip[2];
+    float a[2][4], bias[2], skip[2];
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
         live[m] = ch0 + m * CH < p.channels;             // the shuffles want whole warps
         c[m] = live[m] ? ch0 + m * CH : p.channels - 1;
-        at[m] = ((size_t)slot * p.channels + c[m]) * N + 4 * part;
+        at[m] = (size_t)c[m] * N + 4 * part;
         bc[m] = c[m] / per_group * N + 4 * part;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[m][i] = 0.f;
-        if (p.state_in) load_state(p.state_in + at[m], h[m]);
-        load4(p.a + (size_t)c[m] * N + 4 * part, a[m]);
+        load4(p.a + at[m], a[m]);
         bias[m] = p.dt_bias ? __ldg(p.dt_bias + c[m]) : 0.f;
         skip[m] = p.skip ? __ldg(p.skip + c[m]) : 0.f;
     }
-    for (int t = p.seqs.begin(n); t < p.seqs.end(n); ++t) {
-        float x[2], z[2] = {0.f, 0.f}, d[2];
-        uint2 bw[2], cw[2];
+    float next[2][4];
+    const auto begin = [&](int slot) {
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-            x[m] = __bfloat162float(p.x[t * p.x_stride + c[m]]);
-            d[m] = __bfloat162float(p.dt[t * p.dt_stride + c[m]]) + bias[m];
-            if (p.z) z[m] = __bfloat162float(p.z[t * p.z_stride + c[m]]);
-            bw[m] = *reinterpret_cast<const uint2 *>(p.b + t * p.b_stride + bc[m]);
-            cw[m] = *reinterpret_cast<const uint2 *>(p.c + t * p.c_stride + bc[m]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) next[m][i] = 0.f;
+            if (p.state_in && slot >= 0) load_state(p.state_in + slot * all + at[m], next[m]);
         }
-        if (p.softplus) halves(softplus(pair(d[0], d[1])), d[0], d[1]);
+    };
+    int n = blockIdx.x / ctas, slot = p.seqs.slot(n);
+    begin(slot);
+    for (; n < p.seqs.n; n += step) {
+        float h[2][4];
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            const float b[4] = {bf16_lo(bw[m].x), bf16_hi(bw[m].x), bf16_lo(bw[m].y), bf16_hi(bw[m].y)};
-            const float cc[4] = {bf16_lo(cw[m].x), bf16_hi(cw[m].x), bf16_lo(cw[m].y), bf16_hi(cw[m].y)};
-            const float u = d[m] * x[m], dl = d[m] * kLog2e;
-            float y = 0.f;
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                h[m][i] = fmaf(ex2(dl * a[m][i]), h[m][i], u * b[i]);
-                y = fmaf(h[m][i], cc[i], y);
+            for (int i = 0; i < 4; ++i) h[m][i] = next[m][i];
+        const int here = slot;
+        if (n + step < p.seqs.n) {
+            slot = p.seqs.slot(n + step);
+            begin(slot);
+        }
+        if (here < 0) {
+            if (threadIdx.x == 0) raise_error(p.seqs.err, kErrInternal);
+            continue;
+        }
+        for (int t = p.seqs.begin(n); t < p.seqs.end(n); ++t) {
+            float x[2], z[2] = {0.f, 0.f}, d[2];
+            uint2 bw[2], cw[2];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                x[m] = __bfloat162float(p.x[t * p.x_stride + c[m]]);
+                d[m] = __bfloat162float(p.dt[t * p.dt_stride + c[m]]) + bias[m];
+                if (p.z) z[m] = __bfloat162float(p.z[t * p.z_stride + c[m]]);
+                bw[m] = *reinterpret_cast<const uint2 *>(p.b + t * p.b_stride + bc[m]);
+                cw[m] = *reinterpret_cast<const uint2 *>(p.c + t * p.c_stride + bc[m]);
             }
+            if (p.softplus) halves(softplus(pair(d[0], d[1])), d[0], d[1]);
 #pragma unroll
-            for (int o = LANES / 2; o >= 1; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-            if (live[m] && part == 0) {
-                y = fmaf(skip[m], x[m], y);
-                if (p.z) y *= silu(z[m]);
-                const size_t to = (size_t)t * p.channels + c[m];
-                if (p.out_f32) static_cast<float *>(p.out)[to] = y;
-                else static_cast<__nv_bfloat16 *>(p.out)[to] = __float2bfloat16_rn(y);
+            for (int m = 0; m < 2; ++m) {
+                const float b[4] = {bf16_lo(bw[m].x), bf16_hi(bw[m].x), bf16_lo(bw[m].y), bf16_hi(bw[m].y)};
+                const float cc[4] = {bf16_lo(cw[m].x), bf16_hi(cw[m].x), bf16_lo(cw[m].y), bf16_hi(cw[m].y)};
+                const float u = d[m] * x[m], dl = d[m] * kLog2e;
+                float y = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    h[m][i] = fmaf(ex2(dl * a[m][i]), h[m][i], u * b[i]);
+                    y = fmaf(h[m][i], cc[i], y);
+                }
+#pragma unroll
+                for (int o = LANES / 2; o >= 1; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+                if (live[m] && part == 0) {
+                    y = fmaf(skip[m], x[m], y);
+                    if (p.z) y *= silu(z[m]);
+                    const size_t to = (size_t)t * p.channels + c[m];
+                    if (p.out_f32) static_cast<float *>(p.out)[to] = y;
+                    else static_cast<__nv_bfloat16 *>(p.out)[to] = __float2bfloat16_rn(y);
+                }
             }
         }
+        if (!p.state_out) continue;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+            if (live[m]) store_state(p.state_out + here * all + at[m], h[m]);
     }
-    if (!p.state_out) return;
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-        if (live[m]) store_state(p.state_out + at[m], h[m]);
 }
 
 // ---------------------------------------------------------------------------------------------- prompts
@@ -528,8 +549,9 @@ cudaError_t launch(const ScanProblem &p) {
     using SH = Shape<N>;
     if (!p.seqs.cu || p.max_len == 1) {
         constexpr int CH = 2 * kScanThreads / (N / 4);
-        const long ctas = (long)((p.channels + CH - 1) / CH) * p.seqs.n;
-        step_kernel<N><<<(unsigned)ctas, kScanThreads, 0, p.stream>>>(p);
+        const long ctas = (p.channels + CH - 1) / CH;
+        const int step = (int)min((long)p.seqs.n, max(1L, 7L * multiprocessor_count() / ctas));
+        step_kernel<N><<<(unsigned)(ctas * step), kScanThreads, 0, p.stream>>>(p, step);
         return cudaGetLastError();
     }
     constexpr int smem = kPromptWarps * (int)sizeof(typename SH::Shared);
