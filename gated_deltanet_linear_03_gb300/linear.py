@@ -40,7 +40,7 @@ def quantize(weight: torch.Tensor, group: int = 64, offsets: bool = True) -> Q4:
     if weight.dim() != 2 or group not in (64, 128) or weight.size(1) % group:
         raise ValueError("weight must be [n_out, k] with k a multiple of group, 64 or 128")
     n_out, k = weight.shape
-    w = weight.float().view(n_out, k // group, group)
+    w = weight.float().contiguous().view(n_out, k // group, group)
     if offsets:
         lo, hi = w.amin(dim=-1), w.amax(dim=-1)
         scale, offset = ((hi - lo) / 15).to(_BF16), lo.to(_BF16)
@@ -104,7 +104,7 @@ def _output(x, n_out, out, out_dtype, index, stream):
         code = DTYPE.get(out_dtype)
         if code is None:
             raise ValueError("out_dtype must be bf16 or fp32")
-        return (x.new_empty(shape) if code == 0 and stream is None else _empty(stream, shape, out_dtype, x.device)), code
+        return _empty(stream, shape, out_dtype, x.device), code
     code = DTYPE.get(out.dtype)
     if code is None or out.shape != shape:
         raise ValueError(f"out must be {shape}, in bf16 or fp32")
@@ -122,8 +122,13 @@ def workspace_size(rows: int, n_out: int, k: int, group: int, out_dtype=torch.bf
     return int(need)
 
 
+FEW_ROWS = 16                                             # rows that need no workspace, whatever the other sizes
+
+
 def _workspace(workspace, rows, n_out, k, group, out, index, stream):
-    """(address, bytes, what keeps the memory alive): few rows need none."""
+    """(address, bytes, what keeps the memory alive)."""
+    if workspace is None and rows <= FEW_ROWS:
+        return 0, 0, None
     if workspace is not None:
         if workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the other tensors' device")
