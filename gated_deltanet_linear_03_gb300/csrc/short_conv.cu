@@ -1,10 +1,10 @@
 // gdn_short_conv: y[t, c] = act(bias[c] + sum_j w[c, j] x[t - (W - 1) + j, c]), rows before a sequence from its state.
 //
-// A thread carries 4 channels (8 bytes) down a run of tokens with the last W - 1 inputs in registers, so
-// every input is read once, but for the W - 1 rows in front of a tile.  Tiles are cut from the packed tokens, whatever
+// A thread carries 4 channels (8 bytes) down a run of tokens with the last W - 1 inputs in registers, so that
+// every input is read once, but for the W - 1 rows in front of a run.  Runs are cut from the packed tokens, whatever
 // sequences they hold; a thread that comes to a sequence's first token takes the inputs before it from the state, and
-// writes the sequence's new state as well: its old state is read by this thread alone and before that, so that
-// state_out may be state_in.
+// writes the sequence's new state as well.  Nobody else reads that state (the tokens that need it all belong to this
+// run), so that state_out may be state_in.
 #include "layer_ops.cuh"
 
 namespace gdn {
@@ -73,25 +73,36 @@ __global__ void __launch_bounds__(kConvThreads, kConvCtas) short_conv_kernel(con
             bias[1] = pair(one[2], one[3]);
         }
     }
-    const int t0 = tile * length, t1 = min(t0 + length, p.seqs.total);
-    const __nv_bfloat16 *from = p.x + t0 * p.x_stride + c;
+    const int t0 = tile * length;
+    int t1 = min(t0 + length, p.seqs.total), begin = t0;
+    int n = p.seqs.of(t0), c0 = p.seqs.begin(n), c1 = p.seqs.end(n), slot = p.seqs.slot(n);
+    if (p.seqs.cu) {
+        // A sequence's first W - 1 tokens belong to the run that its first one lies in, which alone reads its state: this run leaves
+        // those of a sequence that began before it to the one before, and goes on over its own end for its last sequence's
+        if (c0 < t0 && t0 < c1) begin = min(max(t0, c0 + W - 1), c1);
+        int e0 = c0, e1 = c1;
+        if (length > 1) {
+            const int m = p.seqs.of(t1 - 1);
+            e0 = p.seqs.begin(m);
+            e1 = p.seqs.end(m);
+        }
+        if (e0 >= t0 && e0 < t1 && e1 > t1) t1 = max(t1, min(e1, e0 + W - 1));
+        if (begin >= t1) return;
+    }
+    const __nv_bfloat16 *from = p.x + begin * p.x_stride + c;
     uint2 x[RING];
 #pragma unroll
     for (int i = 0; i < RING; ++i) {
-        if (t0 + i < t1) x[i] = *reinterpret_cast<const uint2 *>(from);
+        if (begin + i < t1) x[i] = *reinterpret_cast<const uint2 *>(from);
         from += p.x_stride;
     }
-    int n = p.seqs.of(t0), c0 = p.seqs.begin(n), c1 = p.seqs.end(n), slot = p.seqs.slot(n);
     Pair before[W - 1][2];             // the inputs before this token, oldest first
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) {
-        const int t = t0 - (W - 1) + i;
-        uint2 row = make_uint2(0, 0);
-        if (t >= c0 && t0 < c1) row = *reinterpret_cast<const uint2 *>(p.x + t * p.x_stride + c);
-        else if (t0 > c0 && t0 < c1 && slot >= 0) row = state_row<W>(p, slot, t - c0 + W - 1, c);
-        unpack_pairs(row, before[i]);
+        const int t = begin - (W - 1) + i;
+        unpack_pairs(t >= c0 && begin < c1 ? *reinterpret_cast<const uint2 *>(p.x + t * p.x_stride + c) : make_uint2(0, 0), before[i]);
     }
-    __nv_bfloat16 *to = p.out + (size_t)t0 * p.channels + c;
+    __nv_bfloat16 *to = p.out + (size_t)begin * p.channels + c;
     const auto token = [&](const uint2 &raw, bool written) {
         Pair now[2];
         unpack_pairs(raw, now);
@@ -118,7 +129,7 @@ __global__ void __launch_bounds__(kConvThreads, kConvCtas) short_conv_kernel(con
 #pragma unroll
             for (int e = 0; e < 2; ++e) before[j][e] = j + 1 < W - 1 ? before[j + 1][e] : now[e];
     };
-    for (int base = t0; base < t1; base += RING) {
+    for (int base = begin; base < t1; base += RING) {
         if (RING > 1 && base > c0 && base + RING <= c1 && base + 2 * RING <= t1 && slot >= 0) {     // inside one sequence
 #pragma unroll
             for (int i = 0; i < RING; ++i) {
@@ -134,7 +145,7 @@ __global__ void __launch_bounds__(kConvThreads, kConvCtas) short_conv_kernel(con
             const int t = base + i;
             if (t >= t1) break;
             const uint2 now = x[i];
-            if (RING > 1 && t + RING < t1) x[i] = *reinterpret_cast<const uint2 *>(from);
+            if (t + RING < t1) x[i] = *reinterpret_cast<const uint2 *>(from);
             from += p.x_stride;
             if (t >= c1 && n + 1 < p.seqs.n) {       // the next sequence that has tokens
                 n = p.seqs.of(t);

@@ -94,6 +94,23 @@ def test_in_place_beginnings_and_pieces(ssm, lens):
     assert torch.equal(out, want) and torch.equal(state, apart)
 
 
+@pytest.mark.parametrize("width", [2, 3, 4])
+@pytest.mark.parametrize("longest,channels", [(6, 1024), (40, 4096), (300, 8192)])
+def test_in_place_wherever_sequences_begin(ssm, width, longest, channels):
+    """Many sequences, so that they begin at every distance from where the work is cut: a state that is overwritten must have been
+    read by all who need it."""
+    gen = torch.Generator().manual_seed(width)
+    lens = torch.randint(0, longest, (4000 if longest < 300 else 150,), generator=gen).tolist()
+    i = inputs(lens, channels, width, seed=longest)
+    cu = cu_of(lens)
+    y, e, s = ref.conv(i["x"][:, :64].contiguous(), i["weight"][:64], lens, None, "silu", i["past"][:, :, :64])
+    for _ in range(4):
+        state = i["past"].clone()
+        out = ssm.short_conv(i["x"], i["weight"], cu, state_in=state, state_out=state)
+        ref.check(out[:, :64], y, e)
+        assert torch.equal(state[:, :, :64].double(), s)
+
+
 def test_slices_slots_and_untouched_rows(ssm):
     """x as a slice of a projection, states in slots of a larger pool, rows that no sequence holds."""
     lens, C = [30, 1, 7], 256
