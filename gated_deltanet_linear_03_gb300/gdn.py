@@ -114,6 +114,26 @@ def bind(path: str) -> ctypes.CDLL:
     return lib
 
 
+_fast = None
+
+
+def fast_calls():
+    """The C++ part of the binding (csrc/fast_calls.cpp): the calls of :mod:`ssm` and :mod:`linear` with their checks, for the case
+    that nothing is wrong with them."""
+    global _fast
+    if _fast is None:
+        lib = load_library()
+        try:
+            from . import _fast as module
+        except ImportError as e:
+            raise RuntimeError("_fast.so not found; build it with `python -c 'import __graft_entry__ as g; g.build()'`") from e
+        module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.gdn_short_conv, lib.gdn_ssm_scan, lib.gdn_ssm_scan_workspace_size, lib.gdn_q4_linear, lib.gdn_q4_gated,
+            lib.gdn_q4_workspace_size)), GdnError)
+        _fast = module
+    return _fast
+
+
 def lib_status_string(status: int) -> str:
     try:
         return load_library().gdn_status_string(int(status)).decode()

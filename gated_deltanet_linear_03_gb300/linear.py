@@ -17,7 +17,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from .attn import _contiguous, _device, _empty, _int32, _launch, _refuse
-from .gdn import DTYPE, GDN_OK, GdnError, load_library
+from .gdn import DTYPE, GDN_OK, GdnError, fast_calls, load_library
 
 FFN_ACT = {"silu": 0, "gelu": 1}
 _BF16, _U8 = torch.bfloat16, torch.uint8
@@ -63,7 +63,8 @@ def values(w: Q4) -> torch.Tensor:
     return ((q - 8) * s if w.offsets is None else q * s + w.offsets.float()[..., None]).flatten(1)
 
 
-# As in :mod:`attn`, the checks are written for the case that nothing is wrong.
+# Calls in which nothing is wrong go by csrc/fast_calls.cpp, which checks the same; what follows makes the others, or says what is
+# wrong with them.
 def _matrix(name: str, w: Q4, k: int, index: int):
     """(codes, scales, offsets addresses, n_out, group) of a matrix whose inputs are ``k``."""
     codes, scales, offsets = w
@@ -122,13 +123,8 @@ def workspace_size(rows: int, n_out: int, k: int, group: int, out_dtype=torch.bf
     return int(need)
 
 
-FEW_ROWS = 16                                             # rows that need no workspace, whatever the other sizes
-
-
 def _workspace(workspace, rows, n_out, k, group, out, index, stream):
     """(address, bytes, what keeps the memory alive)."""
-    if workspace is None and rows <= FEW_ROWS:
-        return 0, 0, None
     if workspace is not None:
         if workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the other tensors' device")
@@ -143,6 +139,10 @@ def _workspace(workspace, rows, n_out, k, group, out, index, stream):
 def q4_linear(x: torch.Tensor, w: Q4, *, out: Optional[torch.Tensor] = None, out_dtype=torch.bfloat16,
               workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Run ``gdn_q4_linear``: ``x`` (bf16 [..., k]) times the transpose of ``w``: [..., n_out] in bf16 or fp32."""
+    if stream is None and workspace is None:
+        done = fast_calls().q4_linear(x, w, 0, out, DTYPE.get(out_dtype, -1))
+        if done is not None:
+            return done
     lib = load_library()
     dev = _device(x, "x")
     stride, rows, k = _rows(x, dev)
@@ -158,6 +158,10 @@ def q4_gated(x: torch.Tensor, gate: Q4, up: Q4, *, act: str = "silu", out: Optio
              out_dtype=torch.bfloat16, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Run ``gdn_q4_gated``: ``act(x gate^T) * (x up^T)`` for two matrices of one shape ([n_out, k], one group size, offsets
     in both or neither); ``act`` is "silu" or "gelu" (its tanh form)."""
+    if stream is None and workspace is None:
+        done = fast_calls().q4_gated(x, gate, up, FFN_ACT.get(act, -1), out, DTYPE.get(out_dtype, -1))
+        if done is not None:
+            return done
     lib = load_library()
     dev = _device(x, "x")
     stride, rows, k = _rows(x, dev)

@@ -17,14 +17,14 @@ from typing import Optional
 import torch
 
 from .attn import _contiguous, _device, _empty, _int32, _launch, _refuse
-from .gdn import DTYPE, GDN_OK, GdnError, load_library
+from .gdn import DTYPE, GDN_OK, GdnError, fast_calls, load_library
 
 CONV_ACT = {"none": 0, "silu": 1}
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
-# As in :mod:`attn`, the checks are written for the case that nothing is wrong: few attribute look-ups, no calls where a
-# tensor is what it should be.
+# Calls in which nothing is wrong go by csrc/fast_calls.cpp, which checks the same; what follows makes the others, or says what is
+# wrong with them.
 def _rows(name: str, t: torch.Tensor, shape, index: int) -> int:
     """The row stride of a bf16 [tokens, width] tensor whose rows are contiguous; ``shape`` is what it must be."""
     if t.dtype is not _BF16 or t.get_device() != index or t.dim() != 2:
@@ -37,13 +37,6 @@ def _rows(name: str, t: torch.Tensor, shape, index: int) -> int:
     if stride[1] != 1:
         raise ValueError(f"{name}: rows must be contiguous")
     return stride[0]
-
-
-def _like(x, stride, shape, dtype, stream):
-    """Contiguous memory for an output of ``x``'s shape (``stride``: the distance of its rows)."""
-    if stream is None and dtype is _BF16 and stride == shape[1] and x.is_contiguous():
-        return torch.empty_like(x)              # (the quickest of torch's ways)
-    return _empty(stream, shape, dtype, x.device)
 
 
 def _states(state_in, state_out, d0: int, d1: int, dtype, index: int):
@@ -98,6 +91,10 @@ def short_conv(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: Optional[torch
     the last tap on the token itself; ``bias``: fp32 [channels].  ``cu_seqlens``: int32 [n + 1], or None for one token a
     sequence.  ``state_in`` / ``state_out``: bf16 [slots, width - 1, channels], the inputs before the call's tokens and
     those before the next call's; None for sequences that begin, or are not continued.  They may be the same tensor."""
+    if stream is None:
+        done = fast_calls().short_conv(x, weight, cu_seqlens, bias, CONV_ACT.get(act, -1), state_in, state_out, slots, out)
+        if done is not None:
+            return done
     lib = load_library()
     dev = _device(x, "x")
     shape = x.shape
@@ -114,7 +111,7 @@ def short_conv(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: Optional[torch
     si, so, n_slots = _states(state_in, state_out, width - 1, channels, _BF16, dev)
     bp = 0 if bias is None else _parameter("bias", bias, channels, dev)
     if out is None:
-        out = _like(x, stride, shape, _BF16, stream)
+        out = _empty(stream, shape, _BF16, x.device)
     elif out.dtype is not _BF16 or out.get_device() != dev or not out.is_contiguous() or out.shape != shape:
         _contiguous("out", out, _BF16, 2, dev)
         raise ValueError("out must have the shape of x")
@@ -161,6 +158,11 @@ def scan(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch.Tensor, c:
     token a sequence.  ``state_in`` / ``state_out``: fp32 [slots, channels, n_state], None for sequences that begin, or
     are not continued; they may be the same tensor.  ``max_len``: the longest sequence as far as the host knows; it
     chooses the kernel, nothing else."""
+    if stream is None and workspace is None:
+        done = fast_calls().scan(x, dt, a, b, c, cu_seqlens, d, z, dt_bias, dt_softplus, state_in, state_out, slots, max_len, out,
+                                 DTYPE.get(out_dtype, -1))
+        if done is not None:
+            return done
     lib = load_library()
     dev = _device(x, "x")
     shape, vectors = x.shape, b.shape
@@ -189,7 +191,7 @@ def scan(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch.Tensor, c:
     if out_code is None or (out is not None and out.shape != shape):
         raise ValueError("out must have the shape of x, in bf16 or fp32")
     if out is None:
-        out = _like(x, x_stride, shape, out_dtype, stream)
+        out = _empty(stream, shape, out_dtype, x.device)
     wsp = ws_bytes = 0
     if cu_seqlens is None:
         n, cu, sl = (T, 0, 0) if slots is None else _packing(None, slots, T, dev)
