@@ -43,6 +43,7 @@ struct Tc {
 struct TcPlan {
     int ntok, m_tiles, row_tiles, cluster;
     int slice;                            // chunks of inputs of one CTA
+    bool pair;                            // two CTAs an SM
     int code_stages, x_stages, tmem_cols; // (columns: the sums, and two steps of each matrix, 128)
 };
 
@@ -88,24 +89,29 @@ __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
     if (threadIdx.x % 32 == 0) mbar_arrive(bar);
 }
 
-// The largest 15 |scale| + |offset| of a row.
+// 16 bytes of a matrix's scales or offsets; what would lie behind the last of them is zero.
+__device__ __forceinline__ uint4 eight(const __nv_bfloat16 *all, size_t at, size_t total) {
+    if (at + 8 <= total) return *reinterpret_cast<const uint4 *>(all + at);
+    uint32_t v[4] = {};
+    for (int e = 0; at + e < total; ++e) v[e / 2] |= (uint32_t)__bfloat16_as_ushort(all[at + e]) << 16 * (e % 2);
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// The largest 15 |scale| + |offset| of a row, by aligned reads: eight numbers may begin before the row or end behind it.
 template <bool OFFSETS>
-__device__ __forceinline__ float largest(const Q4Matrix &w, size_t row, int groups) {
+__device__ __forceinline__ float largest(const Q4Matrix &w, size_t row, size_t rows, int groups) {
+    const size_t first = row * groups, total = rows * groups;
     float top = 0.f;
-    const __nv_bfloat16 *s = w.scales + row * groups, *o = OFFSETS ? w.offsets + row * groups : nullptr;
-    if (groups % 8 != 0) {
-        for (int i = 0; i < groups; ++i)
-            top = fmaxf(top, 15.f * fabsf(__bfloat162float(s[i])) + (OFFSETS ? fabsf(__bfloat162float(o[i])) : 0.f));
-        return top;
-    }
-    for (int i = 0; i < groups; i += 32) {               // reads of four pieces are in flight together
+    const int before = first % 8, end = before + groups;
+    for (int i = 0; i < end; i += 32) {                  // reads of four pieces are in flight together
         uint4 vs[4], vo[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const bool there = i + 8 * q < groups;
+            const bool there = i + 8 * q < end;
+            const size_t at = first - before + i + 8 * q;
             vs[q] = vo[q] = make_uint4(0, 0, 0, 0);
-            if (there) vs[q] = *reinterpret_cast<const uint4 *>(s + i + 8 * q);
-            if (OFFSETS && there) vo[q] = *reinterpret_cast<const uint4 *>(o + i + 8 * q);
+            if (there) vs[q] = eight(w.scales, at, total);
+            if (OFFSETS && there) vo[q] = eight(w.offsets, at, total);
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -113,7 +119,10 @@ __device__ __forceinline__ float largest(const Q4Matrix &w, size_t row, int grou
             unpack8(vs[q], fs);
             unpack8(vo[q], fo);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) top = fmaxf(top, 15.f * fabsf(fs[e]) + fabsf(fo[e]));
+            for (int e = 0; e < 8; ++e) {
+                const float v = 15.f * fabsf(fs[e]) + fabsf(fo[e]);
+                if ((unsigned)(i + 8 * q + e - before) < (unsigned)groups) top = fmaxf(top, v);
+            }
         }
     }
     return top;
@@ -140,7 +149,10 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
     const int r = tid & 127, groups = p.k / p.group;
     const size_t row = min(row0 + r, p.n_out - 1);
 
-    if (warp == 8) tmem_alloc(&sm.tmem, l.tmem_cols);
+    if (warp == 8) {
+        tmem_alloc(&sm.tmem, l.tmem_cols);
+        tmem_relinquish();                  // another CTA may be on this SM, which allocates as well
+    }
     if (warp == 9 && elect_one()) {
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(&sm.code_full[i], 1);
@@ -162,7 +174,7 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
 #pragma unroll
         for (int m = 0; m < MATS; ++m) {
             // 2^e <= top < 2^(e + 1) goes to [2^-6, 2^-5); nothing, or what is not finite, stays
-            const float top = largest<OFFSETS>(m ? p.up : p.w, row, groups);
+            const float top = largest<OFFSETS>(m ? p.up : p.w, row, p.n_out, groups);
             const int e = (int)(__float_as_uint(top) >> 23) - 127;
             exponent[m] = top > 0.f && e < 128 ? max(e, -120) + 6 : 0;
         }
@@ -340,30 +352,40 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
     tc_fence_before();
     __syncthreads();
     if (tid == 0 && sm.abort) raise_error(err, kErrTimeout);
-    if (warp == 8) {
-        tmem_relinquish();
-        tmem_dealloc(tmem, l.tmem_cols);
-    }
+    if (warp == 8) tmem_dealloc(tmem, l.tmem_cols);
 }
 
-// Rows of x in fp16, scaled by 2^exponent, each 8 inputs in the order 0 4 1 5 2 6 3 7.  A warp a row.
-__global__ void __launch_bounds__(128) scale_rows_kernel(const __grid_constant__ Q4Problem p, __half *__restrict__ out, int *__restrict__ exponents) {
+// Rows of x in fp16, scaled by 2^exponent, each 8 inputs in the order 0 4 1 5 2 6 3 7.  A CTA a row: its 256 threads hold 8192 inputs;
+// of longer rows they read the rest again.
+constexpr int kScaleThreads = 256, kHeld = 4;
+__global__ void __launch_bounds__(kScaleThreads) scale_rows_kernel(const __grid_constant__ Q4Problem p, __half *__restrict__ out, int *__restrict__ exponents) {
+    __shared__ uint32_t tops[kScaleThreads / 32];
     grid_launch_dependents();
-    const int m = blockIdx.x * 4 + threadIdx.x / 32, lane = threadIdx.x % 32;
-    if (m >= p.rows) return;
+    const int m = blockIdx.x, tid = threadIdx.x, n = p.k / 8;
     const uint4 *x = reinterpret_cast<const uint4 *>(p.x + (long long)m * p.x_stride);
+    uint4 held[kHeld];
     uint32_t top = 0;
-    for (int i = lane; i < p.k / 8; i += 32) top = max(top, amax_bits(x[i]));
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int i = 0; i < kHeld; ++i) {
+        held[i] = make_uint4(0, 0, 0, 0);
+        if (tid + kScaleThreads * i < n) held[i] = x[tid + kScaleThreads * i];
+    }
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) top = max(top, amax_bits(held[i]));
+    for (int i = tid + kScaleThreads * kHeld; i < n; i += kScaleThreads) top = max(top, amax_bits(x[i]));
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (tid % 32 == 0) tops[tid / 32] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kScaleThreads / 32; ++i) top = max(top, tops[i]);
     // the largest goes to [2^14, 2^15); a row of zeros, or with what is not finite, stays as it is
     const int e = (int)(top >> 23) - 127, s = top != 0 && e < 128 ? 14 - e : 0;
     const float f0 = power_of_two(s / 2), f1 = power_of_two(s - s / 2);
-    if (lane == 0) exponents[m] = s;
+    if (tid == 0) exponents[m] = s;
     uint4 *to = reinterpret_cast<uint4 *>(out + (size_t)m * p.k);
-    for (int i = lane; i < p.k / 8; i += 32) {
+    const auto write = [&](int i, const uint4 &v) {
         float f[8];
-        unpack8(x[i], f);
+        unpack8(v, f);
         uint32_t h[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -371,21 +393,37 @@ __global__ void __launch_bounds__(128) scale_rows_kernel(const __grid_constant__
             h[k] = *reinterpret_cast<const uint32_t *>(&v);
         }
         to[i] = make_uint4(h[0], h[1], h[2], h[3]);
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+        if (tid + kScaleThreads * i < n) write(tid + kScaleThreads * i, held[i]);
+    for (int i = tid + kScaleThreads * kHeld; i < n; i += kScaleThreads) write(i, x[i]);
 }
 
 int round_up(int a, int b) { return (a + b - 1) / b * b; }
 
 size_t tc_shared(const TcPlan &l, int mats) {
     const size_t pipeline = (size_t)l.code_stages * mats * kCodeBytes + (size_t)l.x_stages * (mats == 2 ? 1 : 2) * l.ntok * 128;
-    const size_t join = l.cluster > 1 ? (size_t)mats * l.ntok * kRowsA * 4 : 0;
-    return 1024 + max(pipeline, join);
+    return 1024 + pipeline;
 }
 
-constexpr size_t kTcShared = 227 * 1024 - sizeof(TcBars) - 64;
+constexpr size_t kTcShared = 227 * 1024 - sizeof(TcBars) - 64, kTcSharedOfTwo = 112 * 1024 - sizeof(TcBars) - 64;
+
+// Stages of codes and x for this much shared memory, as many as there is room for; false: not even two of each.
+bool fit_stages(TcPlan &l, int mats, size_t room) {
+    l.code_stages = mats == 2 ? 3 : 4;
+    l.x_stages = kMaxStages;
+    while (tc_shared(l, mats) > room && l.x_stages > 2) --l.x_stages;
+    while (tc_shared(l, mats) > room && l.code_stages > 2) --l.code_stages;
+    return tc_shared(l, mats) <= room;
+}
 
 // The division that should be done first: waves of CTAs times a CTA's blocks, each as long as the product's or the unpacking's
-// part of it takes (cycles), and what a CTA takes besides.
+// part of it takes (cycles), and what a CTA takes besides.  Two CTAs on an SM take 1.35 times as long as one (97 to 65 us for 131071 x
+// 2048 and 33 rows of x), or as long as both their products.
+//
+// CTAs of a cluster, and those that need more than half of TMEM, have an SM's shared memory for themselves: no CTA of a cluster
+// ever waits for columns of TMEM that are held by a CTA which in turn waits for another of that cluster.
 TcPlan plan_tc(int rows, int n_out, int k, bool gated) {
     const int mats = gated ? 2 : 1, most = gated ? 192 : 256, sms = multiprocessor_count();
     const int chunks = (k + kChunkIn - 1) / kChunkIn, fewest = (rows + most - 1) / most;
@@ -400,15 +438,15 @@ TcPlan plan_tc(int rows, int n_out, int k, bool gated) {
             l.cluster = cluster;
             l.slice = (chunks + cluster - 1) / cluster;
             if ((long)l.slice * (cluster - 1) >= chunks) continue;            // every CTA has inputs
-            l.code_stages = gated ? 3 : 4;
-            l.x_stages = kMaxStages;
-            const size_t room = mats * l.ntok + 128 <= 256 ? 112 * 1024 : kTcShared;      // two CTAs an SM where TMEM has room for them
-            while (l.x_stages > 2 && tc_shared(l, mats) > room) --l.x_stages;
+            if (cluster > 1 && 1024 + (size_t)mats * l.ntok * kRowsA * 4 > kTcShared) continue;       // (what they join)
             l.tmem_cols = 32;
             while (l.tmem_cols < mats * l.ntok + 128) l.tmem_cols *= 2;
-            if (tc_shared(l, mats) > kTcShared) continue;
-            const double waves = ceil((double)l.row_tiles * l.m_tiles * cluster / sms);
-            const double time = waves * (l.slice * 4.0 * mats * max(2 * l.ntok + 44, 250) + 9000 + 30.0 * l.ntok * mats + (cluster > 1 ? 2000 : 0));
+            const double ctas = (double)l.row_tiles * l.m_tiles * cluster;
+            l.pair = cluster == 1 && ctas > sms && l.tmem_cols <= 256 && fit_stages(l, mats, kTcSharedOfTwo);
+            if (!l.pair && !fit_stages(l, mats, kTcShared)) continue;
+            const double products = l.slice * 4.0 * mats * (2 * l.ntok + 44), rest = 9000 + 30.0 * l.ntok * mats + (cluster > 1 ? 2000 : 0);
+            const double one = max(products, l.slice * 4.0 * mats * 250) + rest;
+            const double time = l.pair ? ceil(ctas / (2 * sms)) * max(1.35 * one, 2 * products + rest) : ceil(ctas / sms) * one;
             if (time < least) least = time, best = l;
         }
     }
@@ -419,7 +457,7 @@ template <bool GATED, bool OFFSETS>
 cudaError_t launch_tc(const Q4Problem &p, const TcPlan &l, const CUtensorMap &codes, const CUtensorMap &up, const CUtensorMap &x,
                       const int *exponents) {
     const auto fn = q4_tc_kernel<GATED, OFFSETS>;
-    const size_t smem = tc_shared(l, GATED ? 2 : 1);
+    const size_t smem = l.pair ? tc_shared(l, GATED ? 2 : 1) : kTcShared;
     static std::atomic<bool> ready[kMaxDevices];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -485,7 +523,7 @@ cudaError_t launch_q4_tc(const Q4Problem &p) {
     if (!byte_map(&codes, p.w.codes, p.n_out, p.k / 2, p.k / 2, kRowsA) || !byte_map(&x, x16, p.rows, (uint64_t)p.k * 2, (uint64_t)p.k * 2, l.ntok)) return cudaErrorInvalidValue;
     if (!p.gated) up = codes;
     else if (!byte_map(&up, p.up.codes, p.n_out, p.k / 2, p.k / 2, kRowsA)) return cudaErrorInvalidValue;
-    scale_rows_kernel<<<(unsigned)((p.rows + 3) / 4), 128, 0, p.stream>>>(p, x16, exponents);
+    scale_rows_kernel<<<(unsigned)p.rows, kScaleThreads, 0, p.stream>>>(p, x16, exponents);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if (p.gated) return p.w.offsets ? launch_tc<true, true>(p, l, codes, up, x, exponents) : launch_tc<true, false>(p, l, codes, up, x, exponents);
