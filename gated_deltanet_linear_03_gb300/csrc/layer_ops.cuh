@@ -131,8 +131,9 @@ struct ChunkScales {
     uint2 s, o;
 };
 
+// `wanted`: a bit for each that is needed; the others may be anything.
 template <bool OFFSETS>
-__device__ __forceinline__ ChunkScales chunk_scales(const Q4Matrix &w, size_t row, int groups, int first, int count, bool vector) {
+__device__ __forceinline__ ChunkScales chunk_scales(const Q4Matrix &w, size_t row, int groups, int first, int count, bool vector, int wanted = 15) {
     ChunkScales c{};
     const __nv_bfloat16 *s = w.scales + row * groups + first, *o = OFFSETS ? w.offsets + row * groups + first : nullptr;
     if (vector) {                                        // the row's groups are a multiple of the chunk's
@@ -146,10 +147,21 @@ __device__ __forceinline__ ChunkScales chunk_scales(const Q4Matrix &w, size_t ro
         }
         return c;
     }
+    if (groups % 2 == 0 && count == 4) {                 // pairs
+        if (wanted & 3 && first < groups) {
+            c.s.x = *reinterpret_cast<const uint32_t *>(s);
+            if (OFFSETS) c.o.x = *reinterpret_cast<const uint32_t *>(o);
+        }
+        if (wanted & 12 && first + 2 < groups) {
+            c.s.y = *reinterpret_cast<const uint32_t *>(s + 2);
+            if (OFFSETS) c.o.y = *reinterpret_cast<const uint32_t *>(o + 2);
+        }
+        return c;
+    }
     uint32_t v[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (i < count && first + i < groups) {
+        if (i < count && first + i < groups && wanted >> i & 1) {
             v[i] = __bfloat16_as_ushort(s[i]);
             if (OFFSETS) u[i] = __bfloat16_as_ushort(o[i]);
         }

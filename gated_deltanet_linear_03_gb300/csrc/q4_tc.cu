@@ -1,7 +1,7 @@
 // 4-bit products for many rows, on tcgen05: y[m, n] = sum_i W[n, i] x[m, i] with W = scale * code + offset.
 //
 // The weights are the product's first operand, 128 rows of W a CTA, and up to 256 rows of x its second: D[n, m] in TMEM.  Codes come by
-// TMA, 128 rows of 256 inputs a stage; 8 warps turn them into fp16 and write them into TMEM as the first operand's next 64 inputs,
+// TMA, 128 rows of 256 inputs a stage; 8 or 16 warps turn them into fp16 and write them into TMEM as the first operand's next 64 inputs,
 // a row a thread; x lies in shared memory.  So a weight is unpacked once for all rows of x of its CTA, and never goes through
 // shared memory as a number.
 //
@@ -29,29 +29,34 @@ constexpr int kRowsA = 128;               // weight rows of a CTA
 constexpr int kBlockIn = 64;              // inputs that a thread unpacks at once: 32 columns of TMEM
 constexpr int kChunkIn = 256;             // inputs of a stage of codes
 constexpr int kCodeBytes = kRowsA * kChunkIn / 2;
-constexpr int kTcThreads = 384;           // 8 warps that unpack, one each for TMA of codes and of x, one or two for the products
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 4, kMaxSlots = 4;
 
 // A step is what one wait of the thread that issues the products is for.  Its instructions between two products, a few dozen in a
-// row, take longer than a product with few columns: with one matrix a step is two blocks, which the two halves of the unpacking warps
-// share; of two matrices each has its half of the warps, its own issuing warp, and steps of one block.
-template <bool GATED>
+// row, take longer than a product with few columns: with one matrix a step is two blocks, which two groups of four unpacking warps
+// share; of two matrices each has its group of warps, its own issuing warp, and steps of one block.  What a warp does for a step
+// takes 1000 cycles, most of them waits (a barrier that is found complete 250, the store to TMEM 150).  16 warps take turns, those of
+// each of the two slots theirs; 8 are enough where two CTAs are on an SM.
+template <bool GATED, int WARPS>
 struct Tc {
     static constexpr int MATS = GATED ? 2 : 1, BLOCKS = GATED ? 1 : 2, STEP = BLOCKS * kBlockIn;
+    static constexpr int GROUPS = WARPS / 4, TURNS = WARPS / 8, PARTS = GROUPS / MATS;
+    static constexpr int THREADS = 32 * (WARPS + 4);      // one warp each for TMA of codes and of x, one or two for the products
 };
 
 struct TcPlan {
     int ntok, m_tiles, row_tiles, cluster;
     int slice;                            // chunks of inputs of one CTA
     bool pair;                            // two CTAs an SM
-    int code_stages, x_stages, tmem_cols; // (columns: the sums, and two steps of each matrix, 128)
+    int slot_bits;                        // 2^slot_bits steps of weights are in TMEM
+    int code_stages, x_stages, tmem_cols; // (columns: the sums, and the slots, 64 each)
 };
 
 struct TcBars {
-    uint64_t code_full[kMaxStages], code_empty[kMaxStages], x_full[kMaxStages], x_empty[kMaxStages], a_full[2][2], a_empty[2][2], done;
+    uint64_t code_full[kMaxStages], code_empty[kMaxStages], x_full[kMaxStages], x_empty[kMaxStages], a_full[2][kMaxSlots], a_empty[2][kMaxSlots], done;
     uint32_t tmem;
     int abort;
     float2 undo[256];                     // of each row of x: the two halves of 2^-exponent
+    float tops[4][kRowsA];                // the largest 15 |scale| + |offset| of a weight row's parts
 };
 
 // 32 lanes x 32 columns of 32 bits, a lane a thread, and the wait for them.
@@ -97,10 +102,9 @@ __device__ __forceinline__ uint4 eight(const __nv_bfloat16 *all, size_t at, size
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// The largest 15 |scale| + |offset| of a row, by aligned reads: eight numbers may begin before the row or end behind it.
+// The largest 15 |scale| + |offset| of `groups` groups, by aligned reads: eight numbers may begin before them or end behind them.
 template <bool OFFSETS>
-__device__ __forceinline__ float largest(const Q4Matrix &w, size_t row, size_t rows, int groups) {
-    const size_t first = row * groups, total = rows * groups;
+__device__ __forceinline__ float largest(const Q4Matrix &w, size_t first, int groups, size_t total) {
     float top = 0.f;
     const int before = first % 8, end = before + groups;
     for (int i = 0; i < end; i += 32) {                  // reads of four pieces are in flight together
@@ -128,12 +132,12 @@ __device__ __forceinline__ float largest(const Q4Matrix &w, size_t row, size_t r
     return top;
 }
 
-template <bool GATED, bool OFFSETS>
-__global__ void __launch_bounds__(kTcThreads, 2)
+template <bool GATED, bool OFFSETS, int WARPS>
+__global__ void __launch_bounds__(Tc<GATED, WARPS>::THREADS, WARPS == 8 ? 2 : 1)
 q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan l, const __grid_constant__ CUtensorMap code_map,
              const __grid_constant__ CUtensorMap up_map, const __grid_constant__ CUtensorMap x_map, const int *__restrict__ x_exponents,
              unsigned int *err) {
-    using T = Tc<GATED>;
+    using T = Tc<GATED, WARPS>;
     constexpr int MATS = T::MATS;
     extern __shared__ unsigned char raw[];
     __shared__ TcBars sm;
@@ -146,22 +150,24 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
     const int blocks = min(l.slice * (kChunkIn / kBlockIn), (p.k - k0) / kBlockIn);                          // at least one
     const int steps = (blocks + T::BLOCKS - 1) / T::BLOCKS, chunks = (blocks + 3) / 4;
     const int x_block = l.ntok * 128;                   // bytes of a block of x
+    const int last_slot = (1 << l.slot_bits) - 1;
+    constexpr int SLOT_COLS = 64;                       // two blocks, of one matrix or of each of two
     const int r = tid & 127, groups = p.k / p.group;
     const size_t row = min(row0 + r, p.n_out - 1);
 
-    if (warp == 8) {
+    if (warp == WARPS) {
         tmem_alloc(&sm.tmem, l.tmem_cols);
         tmem_relinquish();                  // another CTA may be on this SM, which allocates as well
     }
-    if (warp == 9 && elect_one()) {
+    if (warp == WARPS + 1 && elect_one()) {
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(&sm.code_full[i], 1);
-            mbar_init(&sm.code_empty[i], 8);
+            mbar_init(&sm.code_empty[i], WARPS);
             mbar_init(&sm.x_full[i], 1);
             mbar_init(&sm.x_empty[i], MATS);
         }
         for (int i = 0; i < 2; ++i)
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < kMaxSlots; ++k) {
                 mbar_init(&sm.a_full[i][k], GATED ? 4 : 8);
                 mbar_init(&sm.a_empty[i][k], 1);
             }
@@ -169,23 +175,27 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
         sm.abort = 0;
         fence_mbar_init();
     }
-    int exponent[MATS] = {};                    // of this thread's weight rows: W is scaled by 2^-exponent
-    if (warp < 8) {
-#pragma unroll
-        for (int m = 0; m < MATS; ++m) {
-            // 2^e <= top < 2^(e + 1) goes to [2^-6, 2^-5); nothing, or what is not finite, stays
-            const float top = largest<OFFSETS>(m ? p.up : p.w, row, p.n_out, groups);
-            const int e = (int)(__float_as_uint(top) >> 23) - 127;
-            exponent[m] = top > 0.f && e < 128 ? max(e, -120) + 6 : 0;
-        }
+    if (warp < WARPS) {                         // each group of warps a part of one matrix's groups
+        const int m = warp / 4 / T::PARTS, part = warp / 4 % T::PARTS, each = (groups + T::PARTS - 1) / T::PARTS, g0 = min(part * each, groups);
+        sm.tops[warp / 4][r] = largest<OFFSETS>(m ? p.up : p.w, row * groups + g0, min(each, groups - g0), (size_t)p.n_out * groups);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    int exponent[MATS];                         // of this thread's weight rows: W is scaled by 2^-exponent
+#pragma unroll
+    for (int m = 0; m < MATS; ++m) {
+        float top = sm.tops[m * T::PARTS][r];
+#pragma unroll
+        for (int i = 1; i < T::PARTS; ++i) top = fmaxf(top, sm.tops[m * T::PARTS + i][r]);
+        // 2^e <= top < 2^(e + 1) goes to [2^-6, 2^-5); nothing, or what is not finite, stays
+        const int e = (int)(__float_as_uint(top) >> 23) - 127;
+        exponent[m] = top > 0.f && e < 128 ? max(e, -120) + 6 : 0;
+    }
     const uint32_t tmem = sm.tmem, a_cols = tmem + MATS * l.ntok;
     volatile int *abort = &sm.abort;
 
-    if (warp == 8) {
+    if (warp == WARPS) {
         if (elect_one()) {
             int s = 0, phase = 1;               // (the first round finds every stage free)
             for (int c = 0; c < chunks; ++c) {
@@ -198,7 +208,7 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
                 if (++s == l.code_stages) s = 0, phase ^= 1;
             }
         }
-    } else if (warp == 9) {
+    } else if (warp == WARPS + 1) {
         if (elect_one()) {
             grid_dependency_wait();             // the kernel before this one scales x
             int s = 0, phase = 1;
@@ -212,20 +222,26 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
                 if (++s == l.x_stages) s = 0, phase ^= 1;
             }
         }
-    } else if (warp >= 10) {
-        const int which = warp - 10;
+    } else if (warp > WARPS) {
+        const int which = warp - WARPS - 2;
         if (which < MATS && elect_one()) {
-            const uint32_t id = idesc_f16_f32(kRowsA, l.ntok, false, false), d = tmem + which * l.ntok, a = a_cols + 64 * which;
+            const uint32_t id = idesc_f16_f32(kRowsA, l.ntok, false, false), d = tmem + which * l.ntok, a = a_cols + 32 * which;
             const uint64_t first = smem_desc(smem_u32(xs), 16, 1024, kLayoutSwizzle128B);
             int s = 0, phase = 0;
             uint64_t xd = first;
+            bool x_here = false, a_here = false;    // asked for a step ahead: the answer takes 200 cycles
             for (int t = 0; t < steps; ++t) {
-                const int slot = t & 1;
-                mbar_poll(&sm.x_full[s], phase, abort);
-                mbar_poll(&sm.a_full[which][slot], (t >> 1) & 1, abort);
+                const int slot = t & last_slot;
+                if (!x_here) mbar_poll(&sm.x_full[s], phase, abort);
+                if (!a_here) mbar_poll(&sm.a_full[which][slot], (t >> l.slot_bits) & 1, abort);
                 if (*abort) break;
                 tc_fence_after();
-                const uint32_t as = a + T::BLOCKS * 32 * slot;
+                const int next = s + 1 == l.x_stages ? 0 : s + 1;
+                if (t + 1 < steps) {
+                    x_here = mbar_test_wait(&sm.x_full[next], next ? phase : phase ^ 1);
+                    a_here = mbar_test_wait(&sm.a_full[which][(t + 1) & last_slot], ((t + 1) >> l.slot_bits) & 1);
+                }
+                const uint32_t as = a + SLOT_COLS * slot;
                 if (t == 0) mma_tmem_a(d, as, xd, id, 0);
                 else mma_tmem_a(d, as, xd, id, 1);
 #pragma unroll
@@ -237,29 +253,34 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
                 mma_commit(&sm.a_empty[which][slot]);
                 mma_commit(&sm.x_empty[s]);
                 xd += T::BLOCKS * (x_block >> 4);
-                if (++s == l.x_stages) s = 0, phase ^= 1, xd = first;
+                if ((s = next) == 0) phase ^= 1, xd = first;
             }
             mma_commit(&sm.done);
         }
     } else {
-        // Unpacking: warps 0 .. 3 and 4 .. 7 take a step's two blocks, or each one of the two matrices
-        const int half = warp / 4, mine = GATED ? half : 0, f = exponent[mine];
+        // Unpacking: two groups of four warps take a step's two blocks, or each one of the two matrices
+        const int half = warp / 4 % 2, turn = warp / 8, mine = GATED ? half : 0, f = exponent[mine];
         const int count = kChunkIn / p.group;
         const bool vector = groups % count == 0;
-        const uint32_t to = a_cols + ((uint32_t)(warp % 4) << 21) + (GATED ? 64 * half : 32 * half);        // this warp's lanes of TMEM
+        const uint32_t to = a_cols + ((uint32_t)(warp % 4) << 21) + 32 * half;        // this warp's lanes of TMEM
         const Q4Matrix &w = mine ? p.up : p.w;
         const float f0 = power_of_two(-f / 2), f1 = power_of_two(-f - -f / 2);
-        ChunkScales next = chunk_scales<OFFSETS>(w, row, groups, chunk0 * count, count, vector);
+        int wanted = 0;                         // of a chunk's scales, for this warp's blocks
+#pragma unroll
+        for (int i = 0; i < 4 / T::BLOCKS; ++i)
+            if (T::TURNS == 1 || i % 2 == turn) wanted |= 1 << (T::BLOCKS * i + (GATED ? 0 : half)) * count / 4;
+        ChunkScales next = chunk_scales<OFFSETS>(w, row, groups, chunk0 * count, count, vector, wanted);
         bool gone = false;
         int s = 0, phase = 0;
         for (int c = 0; c < chunks && !gone; ++c) {
             const ChunkScales cur = next;
-            if (c + 1 < chunks) next = chunk_scales<OFFSETS>(w, row, groups, (chunk0 + c + 1) * count, count, vector);
+            if (c + 1 < chunks) next = chunk_scales<OFFSETS>(w, row, groups, (chunk0 + c + 1) * count, count, vector, wanted);
             warp_poll(&sm.code_full[s], phase, abort);
             const unsigned char *line = codes + (size_t)(s * MATS + mine) * kCodeBytes + r * 128;
 #pragma unroll
             for (int i = 0; i < 4 / T::BLOCKS; ++i) {
-                const int t = 4 / T::BLOCKS * c + i, j = T::BLOCKS * i + (GATED ? 0 : half), slot = i & 1;
+                if (T::TURNS > 1 && i % 2 != turn) continue;
+                const int t = 4 / T::BLOCKS * c + i, j = T::BLOCKS * i + (GATED ? 0 : half), slot = t & last_slot;
                 if (t >= steps) break;
                 uint32_t v[32];
                 {
@@ -280,12 +301,12 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
                         }
                     }
                 }
-                if (t >= 2) {
-                    warp_poll(&sm.a_empty[mine][slot], (t / 2 - 1) & 1, abort);
+                if (t > last_slot) {
+                    warp_poll(&sm.a_empty[mine][slot], ((t >> l.slot_bits) - 1) & 1, abort);
                     tc_fence_after();
                 }
                 if (gone = __any_sync(0xffffffffu, *abort)) break;
-                tmem_st_row(to + T::BLOCKS * 32 * slot, v);     // (a block beyond the inputs is not multiplied)
+                tmem_st_row(to + SLOT_COLS * slot, v);     // (a block beyond the inputs is not multiplied)
                 tc_fence_before();
                 warp_arrive(&sm.a_full[mine][slot]);
             }
@@ -293,16 +314,16 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
             if (++s == l.code_stages) s = 0, phase ^= 1;
         }
         grid_dependency_wait();
-        for (int m = tid; m < l.ntok; m += 256) {
+        for (int m = tid; m < l.ntok; m += 32 * WARPS) {
             const int e = m0 + m < p.rows ? -x_exponents[m0 + m] : 0;
             sm.undo[m] = make_float2(power_of_two(e / 2), power_of_two(e - e / 2));
         }
-        asm volatile("barrier.sync 1, 256;" ::: "memory");
+        asm volatile("barrier.sync 1, %0;" ::"n"(32 * WARPS) : "memory");
         warp_poll(&sm.done, 0, abort);
         tc_fence_after();
     }
 
-    // Outputs.  Warps 0 .. 3 take the first half of the columns (rows of x), 4 .. 7 the second
+    // Outputs.  Groups of four warps take eight columns (rows of x) in turn
     __syncwarp();
     const bool good = !__any_sync(0xffffffffu, *abort);
     const int n = row0 + r, m_end = min(l.ntok, p.rows - m0);
@@ -319,9 +340,8 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
         if (n < p.n_out) out[(size_t)m * p.n_out] = __float2bfloat16_rn(y);
     };
     float *part = reinterpret_cast<float *>(base);            // [matrix][column][row]: the pipeline is done with this memory
-    if (warp < 8 && good) {
-        const int half = l.ntok / 2;
-        for (int col = warp / 4 * half; col < (warp / 4 + 1) * half; col += 8) {
+    if (warp < WARPS && good) {
+        for (int col = 8 * (warp / 4); col < l.ntok; col += 8 * T::GROUPS) {
             float y[8], z[8];
             tmem_ld8x2(tmem + col + lanes, tmem + (MATS - 1) * l.ntok + col + lanes, y, z);
 #pragma unroll
@@ -337,8 +357,8 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
     }
     if (l.cluster > 1) {
         cluster_sync();
-        if (warp < 8 && good) {
-            for (int col = 2 * rank + warp / 4; col < m_end; col += 2 * l.cluster) {
+        if (warp < WARPS && good) {
+            for (int col = T::GROUPS * rank + warp / 4; col < m_end; col += T::GROUPS * l.cluster) {
                 float y = 0.f, z = 0.f;
                 for (int q = 0; q < l.cluster; ++q) {
                     y += ld_dsmem_f32(part + col * kRowsA + r, q);
@@ -352,7 +372,7 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
     tc_fence_before();
     __syncthreads();
     if (tid == 0 && sm.abort) raise_error(err, kErrTimeout);
-    if (warp == 8) tmem_dealloc(tmem, l.tmem_cols);
+    if (warp == WARPS) tmem_dealloc(tmem, l.tmem_cols);
 }
 
 // Rows of x in fp16, scaled by 2^exponent, each 8 inputs in the order 0 4 1 5 2 6 3 7.  A CTA a row: its 256 threads hold 8192 inputs;
@@ -439,11 +459,17 @@ TcPlan plan_tc(int rows, int n_out, int k, bool gated) {
             l.slice = (chunks + cluster - 1) / cluster;
             if ((long)l.slice * (cluster - 1) >= chunks) continue;            // every CTA has inputs
             if (cluster > 1 && 1024 + (size_t)mats * l.ntok * kRowsA * 4 > kTcShared) continue;       // (what they join)
-            l.tmem_cols = 32;
-            while (l.tmem_cols < mats * l.ntok + 128) l.tmem_cols *= 2;
+            const auto columns = [&](int bits) {
+                int c = 32;
+                while (c < mats * l.ntok + (64 << bits)) c *= 2;
+                return c;
+            };
+            l.slot_bits = 1;
+            l.tmem_cols = columns(1);
             const double ctas = (double)l.row_tiles * l.m_tiles * cluster;
             l.pair = cluster == 1 && ctas > sms && l.tmem_cols <= 256 && fit_stages(l, mats, kTcSharedOfTwo);
             if (!l.pair && !fit_stages(l, mats, kTcShared)) continue;
+            if (!l.pair && columns(2) <= 512) l.slot_bits = 2, l.tmem_cols = columns(2);
             const double products = l.slice * 4.0 * mats * (2 * l.ntok + 44), rest = 9000 + 30.0 * l.ntok * mats + (cluster > 1 ? 2000 : 0);
             const double one = max(products, l.slice * 4.0 * mats * 250) + rest;
             const double time = l.pair ? ceil(ctas / (2 * sms)) * max(1.35 * one, 2 * products + rest) : ceil(ctas / sms) * one;
@@ -453,10 +479,10 @@ TcPlan plan_tc(int rows, int n_out, int k, bool gated) {
     return best;
 }
 
-template <bool GATED, bool OFFSETS>
+template <bool GATED, bool OFFSETS, int WARPS>
 cudaError_t launch_tc(const Q4Problem &p, const TcPlan &l, const CUtensorMap &codes, const CUtensorMap &up, const CUtensorMap &x,
                       const int *exponents) {
-    const auto fn = q4_tc_kernel<GATED, OFFSETS>;
+    const auto fn = q4_tc_kernel<GATED, OFFSETS, WARPS>;
     const size_t smem = l.pair ? tc_shared(l, GATED ? 2 : 1) : kTcShared;
     static std::atomic<bool> ready[kMaxDevices];
     int dev = 0;
@@ -469,7 +495,7 @@ cudaError_t launch_tc(const Q4Problem &p, const TcPlan &l, const CUtensorMap &co
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((long)l.row_tiles * l.m_tiles * l.cluster));
-    cfg.blockDim = dim3(kTcThreads);
+    cfg.blockDim = dim3(Tc<GATED, WARPS>::THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = p.stream;
     cudaLaunchAttribute attr[2]{};
@@ -526,8 +552,10 @@ cudaError_t launch_q4_tc(const Q4Problem &p) {
     scale_rows_kernel<<<(unsigned)p.rows, kScaleThreads, 0, p.stream>>>(p, x16, exponents);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    if (p.gated) return p.w.offsets ? launch_tc<true, true>(p, l, codes, up, x, exponents) : launch_tc<true, false>(p, l, codes, up, x, exponents);
-    return p.w.offsets ? launch_tc<false, true>(p, l, codes, up, x, exponents) : launch_tc<false, false>(p, l, codes, up, x, exponents);
+    using Fn = cudaError_t (*)(const Q4Problem &, const TcPlan &, const CUtensorMap &, const CUtensorMap &, const CUtensorMap &, const int *);
+    static const Fn fns[2][2][2] = {{{launch_tc<false, false, 16>, launch_tc<false, false, 8>}, {launch_tc<false, true, 16>, launch_tc<false, true, 8>}},
+                                    {{launch_tc<true, false, 16>, launch_tc<true, false, 8>}, {launch_tc<true, true, 16>, launch_tc<true, true, 8>}}};
+    return fns[p.gated][p.w.offsets != nullptr][l.pair](p, l, codes, up, x, exponents);
 }
 
 }  // namespace gdn
