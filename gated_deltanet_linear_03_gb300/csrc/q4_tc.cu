@@ -155,17 +155,43 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
     const int r = tid & 127, groups = p.k / p.group;
     const size_t row = min(row0 + r, p.n_out - 1);
 
+    const auto load_codes = [&](int c, int s) {
+        mbar_arrive_expect_tx(&sm.code_full[s], MATS * kCodeBytes);
+        unsigned char *to = codes + (size_t)s * MATS * kCodeBytes;
+        tma_load_2d(to, &code_map, &sm.code_full[s], (k0 + c * kChunkIn) / 2, row0);
+        if (GATED) tma_load_2d(to + kCodeBytes, &up_map, &sm.code_full[s], (k0 + c * kChunkIn) / 2, row0);
+    };
+    const auto load_x = [&](int t, int s) {
+        const int n = min(T::BLOCKS, blocks - t * T::BLOCKS);
+        mbar_arrive_expect_tx(&sm.x_full[s], n * x_block);
+        for (int i = 0; i < n; ++i)                     // (the map counts bytes)
+            tma_load_2d(xs + (size_t)(s * T::BLOCKS + i) * x_block, &x_map, &sm.x_full[s], 2 * (k0 + t * T::STEP + i * kBlockIn), m0);
+    };
+
+    // The first loads are on their way before the scales have been looked over
     if (warp == WARPS) {
-        tmem_alloc(&sm.tmem, l.tmem_cols);
-        tmem_relinquish();                  // another CTA may be on this SM, which allocates as well
-    }
-    if (warp == WARPS + 1 && elect_one()) {
-        for (int i = 0; i < kMaxStages; ++i) {
-            mbar_init(&sm.code_full[i], 1);
-            mbar_init(&sm.code_empty[i], WARPS);
-            mbar_init(&sm.x_full[i], 1);
-            mbar_init(&sm.x_empty[i], MATS);
+        if (elect_one()) {
+            for (int i = 0; i < kMaxStages; ++i) {
+                mbar_init(&sm.code_full[i], 1);
+                mbar_init(&sm.code_empty[i], WARPS);
+            }
+            fence_mbar_init();
+            for (int c = 0; c < min(l.code_stages, chunks); ++c) load_codes(c, c);
         }
+    } else if (warp == WARPS + 1) {
+        if (elect_one()) {
+            for (int i = 0; i < kMaxStages; ++i) {
+                mbar_init(&sm.x_full[i], 1);
+                mbar_init(&sm.x_empty[i], MATS);
+            }
+            fence_mbar_init();
+            grid_dependency_wait();                     // the kernel before this one scales x
+            for (int t = 0; t < min(l.x_stages, steps); ++t) load_x(t, t);
+        }
+    } else if (warp == WARPS + 2) {
+        tmem_alloc(&sm.tmem, l.tmem_cols);
+        tmem_relinquish();                              // another CTA may be on this SM, which allocates as well
+    } else if (warp == WARPS + 3 && elect_one()) {
         for (int i = 0; i < 2; ++i)
             for (int k = 0; k < kMaxSlots; ++k) {
                 mbar_init(&sm.a_full[i][k], GATED ? 4 : 8);
@@ -197,28 +223,21 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
 
     if (warp == WARPS) {
         if (elect_one()) {
-            int s = 0, phase = 1;               // (the first round finds every stage free)
-            for (int c = 0; c < chunks; ++c) {
+            int s = 0, phase = 0;
+            for (int c = l.code_stages; c < chunks; ++c) {
                 mbar_poll(&sm.code_empty[s], phase, abort);
                 if (*abort) break;
-                mbar_arrive_expect_tx(&sm.code_full[s], MATS * kCodeBytes);
-                unsigned char *to = codes + (size_t)s * MATS * kCodeBytes;
-                tma_load_2d(to, &code_map, &sm.code_full[s], (k0 + c * kChunkIn) / 2, row0);
-                if (GATED) tma_load_2d(to + kCodeBytes, &up_map, &sm.code_full[s], (k0 + c * kChunkIn) / 2, row0);
+                load_codes(c, s);
                 if (++s == l.code_stages) s = 0, phase ^= 1;
             }
         }
     } else if (warp == WARPS + 1) {
         if (elect_one()) {
-            grid_dependency_wait();             // the kernel before this one scales x
-            int s = 0, phase = 1;
-            for (int t = 0; t < steps; ++t) {
+            int s = 0, phase = 0;
+            for (int t = l.x_stages; t < steps; ++t) {
                 mbar_poll(&sm.x_empty[s], phase, abort);
                 if (*abort) break;
-                const int n = min(T::BLOCKS, blocks - t * T::BLOCKS);
-                mbar_arrive_expect_tx(&sm.x_full[s], n * x_block);
-                for (int i = 0; i < n; ++i)     // (the map counts bytes)
-                    tma_load_2d(xs + (size_t)(s * T::BLOCKS + i) * x_block, &x_map, &sm.x_full[s], 2 * (k0 + t * T::STEP + i * kBlockIn), m0);
+                load_x(t, s);
                 if (++s == l.x_stages) s = 0, phase ^= 1;
             }
         }
@@ -359,11 +378,15 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
         cluster_sync();
         if (warp < WARPS && good) {
             for (int col = T::GROUPS * rank + warp / 4; col < m_end; col += T::GROUPS * l.cluster) {
-                float y = 0.f, z = 0.f;
-                for (int q = 0; q < l.cluster; ++q) {
-                    y += ld_dsmem_f32(part + col * kRowsA + r, q);
-                    if (GATED) z += ld_dsmem_f32(part + (l.ntok + col) * kRowsA + r, q);
+                float ys[8] = {}, zs[8] = {}, y = 0.f, z = 0.f;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    if (q >= l.cluster) continue;
+                    ys[q] = ld_dsmem_f32(part + col * kRowsA + r, q);
+                    if (GATED) zs[q] = ld_dsmem_f32(part + (l.ntok + col) * kRowsA + r, q);
                 }
+#pragma unroll
+                for (int q = 0; q < 8; ++q) y += ys[q], z += zs[q];
                 write(col, y, z);
             }
         }
@@ -372,7 +395,7 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
     tc_fence_before();
     __syncthreads();
     if (tid == 0 && sm.abort) raise_error(err, kErrTimeout);
-    if (warp == WARPS) tmem_dealloc(tmem, l.tmem_cols);
+    if (warp == WARPS + 2) tmem_dealloc(tmem, l.tmem_cols);
 }
 
 // Rows of x in fp16, scaled by 2^exponent, each 8 inputs in the order 0 4 1 5 2 6 3 7.  A CTA a row: its 256 threads hold 8192 inputs;
