@@ -310,14 +310,25 @@ cudaError_t by_rows(const Q4Problem &p) {
 
 }  // namespace
 
-// Many rows and bf16 outputs: the kernel that multiplies on tcgen05, whose weights are rounded to fp16.
-static bool many_rows(int rows, int out_f32) { return rows > 16 && !out_f32; }
+// bf16 outputs: the kernel that multiplies on tcgen05, whose weights are rounded to fp16, or the one above for 3 to 16 rows of small
+// matrices.  The one above does not share a tile's inputs among CTAs and unpacks for every 8 rows; the other takes 7 us for nothing.
+//     n_out x k       3, 16 rows: above         on tcgen05
+//     300 x 512        3.8,  4.2 us              7.1,  7.2 us
+//     500 x 1024       4.9,  5.4                 6.9,  7.4
+//     12352 x 2048    12.0, 14.8                13.3, 13.4
+//     131071 x 2048   70.8, 90.4                61.5, 62.3
+//     4096 x 4096     12.9, 14.7                 9.8, 10.3
+//     1000 x 8192     18.0, 19.6                10.4, 10.8
+static bool on_tcgen05(int rows, int n_out, int k, int out_f32) {
+    if (rows <= 2 || out_f32) return false;
+    return rows > 16 || k >= 4096 || (rows > 8 && k >= 2048) || (long)n_out * k >= 1l << 25;
+}
 
-size_t q4_workspace_bytes(int rows, int n_out, int k, int out_f32) { return many_rows(rows, out_f32) ? q4_tc_workspace_bytes(rows, k) : 0; }
+size_t q4_workspace_bytes(int rows, int n_out, int k, int out_f32) { return on_tcgen05(rows, n_out, k, out_f32) ? q4_tc_workspace_bytes(rows, k) : 0; }
 
 cudaError_t launch_q4(const Q4Problem &p) {
     if (q4_vec_takes(p.rows, p.k)) return launch_q4_vec(p);
-    if (many_rows(p.rows, p.out_f32)) return launch_q4_tc(p);
+    if (on_tcgen05(p.rows, p.n_out, p.k, p.out_f32)) return launch_q4_tc(p);
     return p.gated ? by_rows<true>(p) : by_rows<false>(p);
 }
 

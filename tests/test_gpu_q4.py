@@ -6,7 +6,6 @@ import layer_helpers as ref
 from layer_helpers import BF, F32
 
 pytestmark = pytest.mark.gpu
-FEW = 16                 # rows of x up to which codes enter the products exactly
 
 
 @pytest.fixture(scope="module")
@@ -25,6 +24,11 @@ def matrix(linear, n_out, k, group, offsets, seed):
     return linear.Q4(codes, scales, offs)
 
 
+def rounds(linear, x, w):
+    """Calls that need a workspace round the weights to fp16; in the others codes enter the products as they are."""
+    return linear.workspace_size(x.shape[0], w.codes.shape[0], x.shape[1], x.shape[1] // w.scales.shape[1]) > 0
+
+
 def rows_of(rows, k, seed):
     g = torch.Generator(device="cuda").manual_seed(seed)
     return torch.randn(rows, k, generator=g, device="cuda").to(BF)
@@ -36,14 +40,14 @@ def rows_of(rows, k, seed):
 def test_sizes(linear, rows, n_out, k, group, offsets):
     w, x = matrix(linear, n_out, k, group, offsets, seed=k), rows_of(rows, k, seed=rows)
     ref.check(linear.q4_linear(x, w, out_dtype=F32), *ref.q4_product(x, w))
-    ref.check(linear.q4_linear(x, w), *ref.q4_product(x, w, rounded=rows > FEW))
+    ref.check(linear.q4_linear(x, w), *ref.q4_product(x, w, rounded=rounds(linear, x, w)))
 
 
 @pytest.mark.parametrize("rows", [1, 3, 8, 12, 16, 24, 32, 40, 64, 100, 509])
 @pytest.mark.parametrize("n_out,k", [(4100, 4096), (520, 192), (96, 8192)])
 def test_rows(linear, rows, n_out, k):
     w, x = matrix(linear, n_out, k, 64, True, seed=n_out), rows_of(rows, k, seed=rows)
-    ref.check(linear.q4_linear(x, w), *ref.q4_product(x, w, rounded=rows > FEW))
+    ref.check(linear.q4_linear(x, w), *ref.q4_product(x, w, rounded=rounds(linear, x, w)))
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
@@ -54,14 +58,14 @@ def test_gated(linear, rows, n_out, k, group, offsets, act):
     gate, up = (matrix(linear, n_out, k, group, offsets, seed=s) for s in (1, 2))
     x = rows_of(rows, k, seed=rows)
     ref.check(linear.q4_gated(x, gate, up, act=act, out_dtype=F32), *ref.gated(x, gate, up, act))
-    ref.check(linear.q4_gated(x, gate, up, act=act), *ref.gated(x, gate, up, act, rounded=rows > FEW))
+    ref.check(linear.q4_gated(x, gate, up, act=act), *ref.gated(x, gate, up, act, rounded=rounds(linear, x, gate)))
 
 
 @pytest.mark.parametrize("rows,k", [(1, 16384), (40, 16384), (64, 12288), (3, 65536), (70, 65536)])
 def test_long_rows(linear, rows, k):
     w, x = matrix(linear, 40, k, 128, True, seed=1), rows_of(rows, k, seed=2)
     ref.check(linear.q4_linear(x, w, out_dtype=F32), *ref.q4_product(x, w))
-    ref.check(linear.q4_linear(x, w), *ref.q4_product(x, w, rounded=rows > FEW))
+    ref.check(linear.q4_linear(x, w), *ref.q4_product(x, w, rounded=rounds(linear, x, w)))
 
 
 def test_a_vocabulary(linear):
@@ -133,7 +137,7 @@ def test_weights_of_very_different_sizes(linear, rows):
     f = 10.0 ** torch.linspace(-30, 30, 200, device="cuda")[:, None] * 10.0 ** (-6 * torch.rand(200, 16, device="cuda"))
     w = linear.Q4(w.codes, (w.scales * f).to(BF), (w.offsets * f).to(BF))
     ref.check(linear.q4_linear(x, w, out_dtype=F32), *ref.q4_product(x, w))
-    ref.check(linear.q4_linear(x, w), *ref.q4_product(x, w, rounded=rows > FEW))
+    ref.check(linear.q4_linear(x, w), *ref.q4_product(x, w, rounded=rounds(linear, x, w)))
 
 
 def test_rows_of_zeros(linear):
