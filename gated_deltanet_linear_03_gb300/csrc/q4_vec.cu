@@ -11,8 +11,13 @@
 // Codes are halves as they lie in a word: a code in the low mantissa bits of a half is c 2^-24, in the next four 16 c 2^-24.
 // So a word's four pairs (i, i + 4) cost four ANDs and one shift.  The tensor cores multiply such subnormals exactly, but line up a
 // product by its exponents as if it began with a one, so that up to 10 of a sum's last bits are lost (3e-6 of the result).  For
-// fp32 outputs each pair is therefore put under the exponent of 1024, which is taken off again: c and 16 c as normal numbers.  x goes to fp16, its row scaled by a power of two to [2^14, 2^15), which keeps all bits of a bf16
-// number down to 2^-28 of the row's largest, with every other pair divided by 16; it is put into the pairs' order once.
+// fp32 outputs each pair is therefore put under the exponent of 1024, which is taken off again: c and 16 c as normal numbers.
+// x goes to fp16, its row scaled by a power of two to [2^14, 2^15), which keeps all bits of a bf16 number down to 2^-28 of the row's
+// largest (some down to 2^-36), with every other pair divided by 16; it is put into the pairs' order once.
+//
+// Measured (device times, weights from memory): 131071 x 2048 with offsets, one row, bf16 outputs 29.4 us, 5.2 TB/s, 0.76 of the copy
+// rate; fp32 outputs 38.4 us, where the subtractions make the issue slots (0.64 busy) the limit.  12352 x 2048 7.3 us, gated 2 x 5632 x
+// 2048 7.4: launch, the first loads' latency and an uneven last round, 193 CTAs on 152 SMs; the bytes alone are 2 us.
 #include "layer_ops.cuh"
 #include "sm100.cuh"
 
@@ -73,7 +78,7 @@ struct VecMaps {
 
 template <int M, bool GATED, bool OFFSETS, bool SCALE_TMA, bool EXACT>
 __global__ void __launch_bounds__(kThreads, 2)
-q4_vec_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ VecMaps maps, int kw, unsigned int *err) {
+q4_vec_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ VecMaps maps, int kw, int each, unsigned int *err) {
     constexpr int OUT = GATED ? kRows / 2 : kRows;                     // outputs of a turn
     constexpr int kSlices = kSlicesOf<M>;
     extern __shared__ __align__(128) unsigned char raw[];
@@ -83,7 +88,7 @@ q4_vec_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ VecMa
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const int ks = warp % kw, together = kWarps / kw;                  // the warp's part of the inputs; turns of a CTA at once
     const int groups = p.k / p.group, shift = p.group == 128 ? 1 : 0;
-    const int slice0 = ks * kSlices, slices = min(kSlices, (p.k + kSlice - 1) / kSlice - slice0);
+    const int slice0 = ks * each, slices = min(each, (p.k + kSlice - 1) / kSlice - slice0);
     const int step = gridDim.x * together, turns = (p.n_out + OUT - 1) / OUT;
 
     constexpr int MATS = GATED ? 2 : 1;
@@ -310,7 +315,13 @@ bool scale_map(CUtensorMap *m, const void *at, uint64_t rows, uint64_t entries, 
 template <int M, bool GATED>
 cudaError_t launch(const Q4Problem &p) {
     int kw = 1;
-    while (kw * kSlicesOf<M> * kSlice < p.k) kw *= 2;
+    const int slices = (p.k + kSlice - 1) / kSlice;
+    while (kw * kSlicesOf<M> < slices) kw *= 2;
+    // More warps to a row's inputs where the outputs would leave half of the SMs idle (1000 x 2048: 5.2 us with a warp a row, 3.75 with
+    // 4; 1000 x 8192: 5.6 with 4, 4.4 with 8; 12352 x 2048, which fills them: 7.3 with one, 8.0 with 2)
+    const long turns = (p.n_out + (GATED ? kRows / 2 : kRows) - 1) / (GATED ? kRows / 2 : kRows);
+    while (kw < kWarps && kw < slices && turns * kw * 2 <= (long)kWarps * multiprocessor_count()) kw *= 2;
+    const int each = (slices + kw - 1) / kw;
     constexpr int OUT = GATED ? kRows / 2 : kRows;
     const int together = kWarps / kw;
     const long ctas = ((long)(p.n_out + OUT - 1) / OUT + together - 1) / together;
@@ -323,7 +334,7 @@ cudaError_t launch(const Q4Problem &p) {
         if (!scale_map(&maps.scales[m], w.scales, p.n_out, p.k / p.group, OUT)) return cudaErrorInvalidValue;
         if (w.offsets && !scale_map(&maps.offsets[m], w.offsets, p.n_out, p.k / p.group, OUT)) return cudaErrorInvalidValue;
     }
-    using Fn = void (*)(const Q4Problem, const VecMaps, int, unsigned int *);
+    using Fn = void (*)(const Q4Problem, const VecMaps, int, int, unsigned int *);
     static const Fn fns[2][2][2] = {{{q4_vec_kernel<M, GATED, false, false, false>, q4_vec_kernel<M, GATED, false, false, true>},
                                      {q4_vec_kernel<M, GATED, false, true, false>, q4_vec_kernel<M, GATED, false, true, true>}},
                                     {{q4_vec_kernel<M, GATED, true, false, false>, q4_vec_kernel<M, GATED, true, false, true>},
@@ -340,7 +351,7 @@ cudaError_t launch(const Q4Problem &p) {
         if (e != cudaSuccess) return e;
         if (dev < kMaxDevices) ready[dev][offsets][tensors][exact].store(true, std::memory_order_relaxed);
     }
-    fn<<<(unsigned)min(ctas, 2L * multiprocessor_count()), kThreads, smem, p.stream>>>(p, maps, kw, error_word());
+    fn<<<(unsigned)min(ctas, 2L * multiprocessor_count()), kThreads, smem, p.stream>>>(p, maps, kw, each, error_word());
     return cudaGetLastError();
 }
 
