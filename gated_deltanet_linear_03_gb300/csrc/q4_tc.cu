@@ -14,6 +14,11 @@
 // Sums are fp32; the powers of two are undone at the end.
 //
 // CTAs of a cluster share the inputs of one tile and join through distributed shared memory, in a fixed order.
+//
+// Bound by the products for many rows (with x as second operand of N rows a product of 16 inputs takes N / 2 + 11 cycles, at least 41), by
+// a CTA's beginning and end for few: launch, scales and first codes 3 us, last barrier, join and outputs 3 us.  Measured on a GB300:
+// 4096 x 4096 with 33 rows 10.8 us, 128 rows 13.3, 512 rows 23.8 (720 TFLOP/s); 131071 x 2048 with 33 rows 66 us, 100 rows 78 (690); gated
+// 2 x 6000 x 2048 with 509 rows 27.8 us (900 TFLOP/s; tensor pipe 0.47 active over the whole time).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

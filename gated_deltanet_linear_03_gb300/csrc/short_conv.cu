@@ -5,6 +5,10 @@
 // sequences they hold; a thread that comes to a sequence's first token takes the inputs before it from the state, and
 // writes the sequence's new state as well.  Nobody else reads that state (the tokens that need it all belong to this
 // run), so that state_out may be state_in.
+//
+// Bound by memory: 4 bytes a token and channel.  Six tokens' inputs are on their way while one is worked on, eight CTAs an SM, 6 KB an
+// SM and CTA.  Measured on a GB300: packed prompts of 12545 tokens x 8192 channels, width 4, with bias and SiLU, 71.2 us: 5.8 TB/s, 0.85
+// of the copy rate (issue slots 0.48 busy, exponentials 0.33).  One token x 8192 channels 2.4 us, which is a launch.
 #include "layer_ops.cuh"
 
 namespace gdn {
@@ -170,7 +174,8 @@ __global__ void __launch_bounds__(kConvThreads, kConvCtas) short_conv_kernel(con
 template <int W>
 cudaError_t launch(const ConvProblem &p) {
     const int piece_ctas = (p.channels / 4 + kConvThreads - 1) / kConvThreads;
-    // Few tokens: one a thread.  Many: as many CTAs as are on the SMs at once, each down an equal run of tokens
+    // Few tokens: one a thread.  Many: as many CTAs as are on the SMs at once, each down an equal run of tokens.  61 tokens x 8192
+    // channels take 3.7 us as few, 6.4 as many; 500 take 21.5 and 16.6; 3000 in prompts 86.6 and 24.0
     const long pieces = (long)p.channels / 4 * p.seqs.total;
     const bool many = pieces >= (long)kConvCtas * kConvThreads * kRing * multiprocessor_count();
     const int runs = max(1, kConvCtas * multiprocessor_count() / piece_ctas);

@@ -2,6 +2,16 @@
 //     h[n] = exp(D a[c, n]) h[n] + D x B[n],   y = (sum_n h[n] C[n] + skip x) z / (1 + e^-z),   D = softplus(dt + bias).
 //
 // A channel's states lie in the registers of N / S neighbouring lanes, S each, for as long as its sequence lasts.
+//
+// A prompt is bound by instructions: N exponentials a token and channel (32 a cycle and SM) and four multiplications or sums beside
+// each, in packed pairs, which take two of a scheduler's slots.  A warp works on its own, 8 states of 2 channels a lane: B and C of a
+// token serve 16 products a lane, and the step widths, gates and stores of 8 tokens are prepared by all lanes at once.  Where there
+// are too few sequences and channels for the GPU, the tokens are cut into pieces, and a first pass carries only the states (at 2/3 of
+// the cost of a whole one) to the pieces' beginnings.
+//
+// Measured on a GB300, 4096 channels x 16 states: 64 sequences of 128 tokens 148 us in one pass, 0.39 of the exponentials' rate; 8192 tokens
+// of one sequence 256 us (107 for the ends, 153 for the outputs: issue slots 0.61 busy, exponentials 0.59 and 0.47; the bytes are 40 us).  7
+// sequences, 6465 tokens x 1536 channels x 64 states 246 us.  One token: 61 sequences x 4096 x 16 9.1 us, 3.8 TB/s; one sequence 2.1.
 #include "layer_ops.cuh"
 #include "sm100.cuh"
 
@@ -532,7 +542,9 @@ ScanPlan plan_scan(int n_seqs, int total, int channels, int groups, int max_len)
     s.units = n_seqs;
     const long warps = (long)s.warps_per_group * groups, at_once = (long)kPromptCtas * kPromptWarps * multiprocessor_count();
     const long longest = max_len > 0 && max_len < total ? max_len : total;
-    // Tokens that one warp walks through, one after another: whole sequences, or pieces twice
+    // Tokens that one warp walks through, one after another: whole sequences, or pieces twice.  Measured, 4096 channels x 16 states,
+    // whole and in pieces: 16 x 512 tokens 176 and 211 us, 32 x 500 288 and 349, 4 x 2000 238 and 248, 1 x 100 14.5 and 17.7; but 1 x 600 72
+    // and 34, 1 x 8192 967 and 255; 7 x 60 .. 4000 of 1536 x 64 461 and 246
     const long whole = max(longest, (long)total * warps / at_once);
     const long halves = 2 * max(64L, (long)total * warps / at_once);
     if (whole <= halves * 5 / 4) return s;
