@@ -162,7 +162,7 @@ int multiprocessor_count() { return sm_count(); }
 
 extern "C" {
 
-int gdn_version(void) { return 210; }
+int gdn_version(void) { return 220; }
 
 const char *gdn_status_string(gdn_status s) {
     switch (s) {

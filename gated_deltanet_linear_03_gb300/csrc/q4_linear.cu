@@ -14,7 +14,7 @@
 //
 // Bound by latencies, of barriers above all (a wait that finds its phase complete takes some 250 cycles, and a stage has three), not by
 // the codes: 12352 x 2048 with 3 rows 12.0 us, 1.2 TB/s; with 16 14.8.  fp32 outputs of many rows, which have to keep groups apart, pay
-// for every 64 rows again: 4096 x 4096 with 33 rows 32 us, 131071 x 2048 with 33 rows 192.
+// for every 32 rows again: 4096 x 4096 with 33 rows 22.7 us, 512 rows 103 (167 TFLOP/s); 131071 x 2048 with 33 rows 203.
 //
 // A fragment's order of inputs is free as long as both operands keep it: lane (g, t) takes inputs 16 t .. 16 t + 15 of a block of 64,
 // for weight rows g and g + 8 (of two matrices, rows g of each) and for row g of x: 8 bytes of codes and 32 bytes of x in a row.
@@ -62,8 +62,8 @@ struct FewBars {
     int abort;
 };
 
-template <int NT, bool GATED, bool OFFSETS, bool EXACT>
-__global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1)
+template <int NT, int FIT, bool GATED, bool OFFSETS, bool EXACT>
+__global__ void __launch_bounds__(kThreads, FIT)
 q4_few_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ FewPlan l, const __grid_constant__ CUtensorMap code_map,
               const __grid_constant__ CUtensorMap up_map, const __grid_constant__ CUtensorMap x_map, unsigned int *err) {
     constexpr int COLS = 8 * NT, X_BOX = COLS * 128, X_BYTES = 4 * X_BOX;
@@ -261,9 +261,9 @@ size_t few_shared(int cols, const FewPlan &l) {
     return 1024 + l.stages * (stage + 16 * cols) + (size_t)2 * (kWarps / l.w) * cols * (16 * l.w + 4) * 4;
 }
 
-template <int NT, bool GATED>
+template <int NT, int FIT, bool GATED>
 cudaError_t launch(const Q4Problem &p) {
-    constexpr int COLS = 8 * NT, FIT = NT <= 2 ? 2 : 1;
+    constexpr int COLS = 8 * NT;
     const int sms = multiprocessor_count();
     FewPlan l{};
     l.m_blocks = (p.rows + COLS - 1) / COLS;
@@ -286,8 +286,9 @@ cudaError_t launch(const Q4Problem &p) {
     else if (!byte_map(&up, p.up.codes, p.n_out, p.k / 2, p.k / 2, box_rows)) return cudaErrorInvalidValue;
 
     using Fn = void (*)(const Q4Problem, const FewPlan, const CUtensorMap, const CUtensorMap, const CUtensorMap, unsigned int *);
-    static const Fn fns[2][2] = {{q4_few_kernel<NT, GATED, false, false>, q4_few_kernel<NT, GATED, false, true>},
-                                 {q4_few_kernel<NT, GATED, true, false>, q4_few_kernel<NT, GATED, true, true>}};
+    constexpr bool ONLY = NT > 2;                    // more than 16 rows come with fp32 outputs only
+    static const Fn fns[2][2] = {{q4_few_kernel<NT, FIT, GATED, false, ONLY>, q4_few_kernel<NT, FIT, GATED, false, true>},
+                                 {q4_few_kernel<NT, FIT, GATED, true, ONLY>, q4_few_kernel<NT, FIT, GATED, true, true>}};
     const int offsets = p.w.offsets != nullptr, exact = p.out_f32;
     static std::atomic<bool> ready[kMaxDevices][2][2];
     int dev = 0;
@@ -303,13 +304,14 @@ cudaError_t launch(const Q4Problem &p) {
     return cudaGetLastError();
 }
 
-// A CTA takes 8, 16, 32 or 64 rows of x.
+// A CTA takes 8, 16 or 32 rows of x.  With 32 rows two CTAs fit on an SM at 96 registers a thread instead of 168, which pays where there
+// is work for them: 4096 x 4096, 512 rows, 103 us instead of 142, 15540 x 3968, 143 rows, 141 instead of 185; but 24 rows 19.6 instead of
+// 17.4 and 12352 x 1344, 59 rows, 35.9 instead of 33.8.
 template <bool GATED>
 cudaError_t by_rows(const Q4Problem &p) {
-    if (p.rows > 32) return launch<8, GATED>(p);
-    if (p.rows > 16) return launch<4, GATED>(p);
-    if (p.rows > 8) return launch<2, GATED>(p);
-    return launch<1, GATED>(p);
+    if (p.rows > 16) return (long)p.rows * p.n_out >= 1l << 20 ? launch<4, 2, GATED>(p) : launch<4, 1, GATED>(p);
+    if (p.rows > 8) return launch<2, 2, GATED>(p);
+    return launch<1, 2, GATED>(p);
 }
 
 }  // namespace

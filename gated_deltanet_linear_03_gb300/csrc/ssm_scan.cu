@@ -11,7 +11,7 @@
 //
 // Measured on a GB300, 4096 channels x 16 states: 64 sequences of 128 tokens 148 us in one pass, 0.39 of the exponentials' rate; 8192 tokens
 // of one sequence 256 us (107 for the ends, 153 for the outputs: issue slots 0.61 busy, exponentials 0.59 and 0.47; the bytes are 40 us).  7
-// sequences, 6465 tokens x 1536 channels x 64 states 246 us.  One token: 61 sequences x 4096 x 16 9.1 us, 3.8 TB/s; one sequence 2.1.
+// sequences, 6465 tokens x 1536 channels x 64 states 246 us.  One token: 61 sequences x 4096 x 16 9.6 us, 3.6 TB/s; one sequence 2.3.
 #include "layer_ops.cuh"
 #include "sm100.cuh"
 
