@@ -16,8 +16,8 @@
 // largest (some down to 2^-36), with every other pair divided by 16; it is put into the pairs' order once.
 //
 // Measured (device times, weights from memory): 131071 x 2048 with offsets, one row, bf16 outputs 29.4 us, 5.2 TB/s, 0.76 of the copy
-// rate; fp32 outputs 38.4 us, where the subtractions make the issue slots (0.64 busy) the limit.  12352 x 2048 7.3 us, gated 2 x 5632 x
-// 2048 7.4: launch, the first loads' latency and an uneven last round, 193 CTAs on 152 SMs; the bytes alone are 2 us.
+// rate; fp32 outputs 38.4 us, where the subtractions make the issue slots (0.64 busy) the limit.  12352 x 2048 7.1 us, gated 2 x 5632 x
+// 2048 6.6: launch, the first loads' latency, and 1544 turns of 8 rows on 608 schedulers; the bytes alone are 2 us.
 #include "layer_ops.cuh"
 #include "sm100.cuh"
 
@@ -88,15 +88,18 @@ q4_vec_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ VecMa
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
     const int ks = warp % kw, together = kWarps / kw;                  // the warp's part of the inputs; turns of a CTA at once
     const int groups = p.k / p.group, shift = p.group == 128 ? 1 : 0;
-    const int slice0 = ks * each, slices = min(each, (p.k + kSlice - 1) / kSlice - slice0);
     const int step = gridDim.x * together, turns = (p.n_out + OUT - 1) / OUT;
+    // Warps on their own take turns that are gridDim.x apart, so that all SMs get as many, but for one (2 x 5632 x 2048 7.6 -> 6.6 us).
+    // Warps that meet go through the same number of turns, of which the last may be beyond the matrix
+    int turn = kw > 1 ? blockIdx.x * together + warp / kw : blockIdx.x + gridDim.x * warp;
+    const int rounds = kw > 1 ? (turns + step - 1) / step : turn < turns ? (turns - turn + step - 1) / step : 0;
+    const int slice0 = ks * each, slices = rounds ? min(each, (p.k + kSlice - 1) / kSlice - slice0) : 0;
 
     constexpr int MATS = GATED ? 2 : 1;
     Stage<MATS> *ring = reinterpret_cast<Stage<MATS> *>(raw) + warp * kDeep;
     volatile int *abort = &gave_up;
-    int turn = blockIdx.x * together + warp / kw, buffer = 0;
-    // every warp of a CTA goes through the same number of turns: its last ones may be beyond the matrix
-    const int rounds = (turns + step - 1) / step, total = rounds * max(slices, 0);
+    const int total = rounds * max(slices, 0);
+    int buffer = 0;
     if (lane == 0) {
         for (int i = 0; i < kDeep; ++i) mbar_init(&full[warp][i], 1);
         if (warp == 0) gave_up = 0;
@@ -319,12 +322,10 @@ cudaError_t launch(const Q4Problem &p) {
     while (kw * kSlicesOf<M> < slices) kw *= 2;
     // More warps to a row's inputs where the outputs would leave half of the SMs idle (1000 x 2048: 5.2 us with a warp a row, 3.75 with
     // 4; 1000 x 8192: 5.6 with 4, 4.4 with 8; 12352 x 2048, which fills them: 7.3 with one, 8.0 with 2)
-    const long turns = (p.n_out + (GATED ? kRows / 2 : kRows) - 1) / (GATED ? kRows / 2 : kRows);
+    constexpr int OUT = GATED ? kRows / 2 : kRows;
+    const long turns = ((long)p.n_out + OUT - 1) / OUT;
     while (kw < kWarps && kw < slices && turns * kw * 2 <= (long)kWarps * multiprocessor_count()) kw *= 2;
     const int each = (slices + kw - 1) / kw;
-    constexpr int OUT = GATED ? kRows / 2 : kRows;
-    const int together = kWarps / kw;
-    const long ctas = ((long)(p.n_out + OUT - 1) / OUT + together - 1) / together;
     const bool tensors = scale_tensors(p);
     VecMaps maps{};
     for (int m = 0; m < (GATED ? 2 : 1); ++m) {
@@ -351,6 +352,7 @@ cudaError_t launch(const Q4Problem &p) {
         if (e != cudaSuccess) return e;
         if (dev < kMaxDevices) ready[dev][offsets][tensors][exact].store(true, std::memory_order_relaxed);
     }
+    const long ctas = kw > 1 ? (turns * kw + kWarps - 1) / kWarps : turns;
     fn<<<(unsigned)min(ctas, 2L * multiprocessor_count()), kThreads, smem, p.stream>>>(p, maps, kw, each, error_word());
     return cudaGetLastError();
 }

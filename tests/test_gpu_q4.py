@@ -181,3 +181,41 @@ def test_streams_and_graphs(linear):
     graph.replay()
     y, e = ref.q4_product(keep, w, rounded=False)
     ref.check(out, y, e)
+
+
+def test_calls_at_once(linear):
+    """Calls of every kind on two streams at the same time, which share the SMs and their tensor memory, give what they give alone."""
+    made = []
+    for seed, (rows, n_out, k) in enumerate([(33, 4096, 4096), (100, 20000, 1024), (500, 3000, 2048), (1, 9000, 2048), (9, 700, 8192),
+                                             (20, 520, 6144)]):
+        w, up, x = matrix(linear, n_out, k, 64, True, seed), matrix(linear, n_out, k, 64, True, seed + 50), rows_of(rows, k, seed)
+        made += [lambda x=x, w=w: linear.q4_linear(x, w), lambda x=x, w=w, up=up: linear.q4_gated(x, w, up),
+                 lambda x=x, w=w: linear.q4_linear(x, w, out_dtype=F32)]
+    want = [f() for f in made]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for turn in range(6):
+        got = [None] * len(made)
+        for i in range(len(made)):                    # the two streams meet in another pairing every time
+            for s, j in ((0, i), (1, (5 * i + turn) % len(made))):
+                with torch.cuda.stream(streams[s]):
+                    out = made[j]()
+                    if s == 0:
+                        got[i] = out
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("rows,n_out,k", [(1, 1, 64), (2, 9, 1536), (1, 2431, 1024), (1, 2433, 2048), (2, 5000, 8192), (1, 40, 16384), (3, 40, 4096),
+                                          (9, 129, 2048), (16, 260, 6144)])
+def test_divisions_of_few_rows(linear, rows, n_out, k):
+    """Sizes around those at which warps share a row's inputs, CTAs get a second turn, or the call goes to another kernel."""
+    gate, up, x = matrix(linear, n_out, k, 64, True, 31), matrix(linear, n_out, k, 64, True, 32), rows_of(rows, k, 33)
+    ref.check(linear.q4_linear(x, gate), *ref.q4_product(x, gate, rounded=rounds(linear, x, gate)))
+    ref.check(linear.q4_linear(x, gate, out_dtype=F32), *ref.q4_product(x, gate))
+    ref.check(linear.q4_gated(x, gate, up), *ref.gated(x, gate, up, "silu", rounded=rounds(linear, x, gate)))
+
+
+def test_no_rows(linear):
+    w = matrix(linear, 40, 256, 64, True, 1)
+    assert linear.q4_linear(rows_of(0, 256, 1), w).shape == (0, 40) and linear.q4_gated(rows_of(0, 256, 1), w, w).shape == (0, 40)
