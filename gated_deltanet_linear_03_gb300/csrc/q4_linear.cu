@@ -1,12 +1,12 @@
 // gdn_q4_linear and gdn_q4_gated: products of activations with weights of 4 bits,
 //     y[m, n] = sum_G ( s[n, G] sum_{i in G} c[n, i] x[m, i]  +  o[n, G] sum_{i in G} x[m, i] ),
-// G over groups of 64 or 128 inputs; o = -8 s where the matrix has no offsets.  This is the kernel for a few rows and for fp32
-// outputs; one or two rows go to q4_vec.cu, many to q4_tc.cu.
+// G over groups of 64 or 128 inputs; o = -8 s where the matrix has no offsets.  This is the kernel for small products and for fp32
+// outputs; one or two rows go to q4_vec.cu, large products to q4_tc.cu.
 //
 // The inner sums go to the tensor cores (mma.sync, 16 weight rows by 8 rows of x by 16 inputs): a code is an integer below 16,
 // exact in bf16, so the products are exact and the sums fp32, and scale and offset meet them once a group instead of once a
-// weight.  With outputs in bf16 the codes enter as 128 + c, which saves the subtraction and is taken back with the offset
-// (2^-16 of the sums' terms); with fp32 outputs as c.
+// weight.  With outputs in bf16 and up to 16 rows the codes enter as 128 + c, which saves the subtraction and is taken back with the offset
+// (2^-16 of the sums' terms); otherwise as c.
 //
 // Codes and x come by TMA, stages of 16 w weight rows (w = 1, 2, 4 or 8) and all rows of x by 256 inputs, which one thread asks for
 // several stages ahead, across tiles: what reads memory is never waiting for what computes.  Eight warps compute, w along the rows by
@@ -286,7 +286,7 @@ cudaError_t launch(const Q4Problem &p) {
     else if (!byte_map(&up, p.up.codes, p.n_out, p.k / 2, p.k / 2, box_rows)) return cudaErrorInvalidValue;
 
     using Fn = void (*)(const Q4Problem, const FewPlan, const CUtensorMap, const CUtensorMap, const CUtensorMap, unsigned int *);
-    constexpr bool ONLY = NT > 2;                    // more than 16 rows come with fp32 outputs only
+    constexpr bool ONLY = NT > 2;                    // more than 16 rows are mostly fp32 outputs: that form for both
     static const Fn fns[2][2] = {{q4_few_kernel<NT, FIT, GATED, false, ONLY>, q4_few_kernel<NT, FIT, GATED, false, true>},
                                  {q4_few_kernel<NT, FIT, GATED, true, ONLY>, q4_few_kernel<NT, FIT, GATED, true, true>}};
     const int offsets = p.w.offsets != nullptr, exact = p.out_f32;
@@ -316,18 +316,24 @@ cudaError_t by_rows(const Q4Problem &p) {
 
 }  // namespace
 
-// bf16 outputs: the kernel that multiplies on tcgen05, whose weights are rounded to fp16, or the one above for 3 to 16 rows of small
-// matrices.  The one above does not share a tile's inputs among CTAs and unpacks for every 8 rows; the other takes 7 us for nothing.
-//     n_out x k       3, 16 rows: above         on tcgen05
-//     300 x 512        3.8,  4.2 us              7.1,  7.2 us
-//     500 x 1024       4.9,  5.4                 6.9,  7.4
-//     12352 x 2048    12.0, 14.8                13.3, 13.4
-//     131071 x 2048   70.8, 90.4                61.5, 62.3
-//     4096 x 4096     12.9, 14.7                 9.8, 10.3
-//     1000 x 8192     18.0, 19.6                10.4, 10.8
+// bf16 outputs: the kernel that multiplies on tcgen05, whose weights are rounded to fp16, or the one above for small products.  The one
+// above does not share a tile's inputs among CTAs and unpacks for every 8 to 32 rows; the other takes 7 us for nothing.
+//     n_out x k        above                     on tcgen05
+//     300 x 512        3, 16 rows  3.8,  4.2 us   7.1,  7.2 us
+//     500 x 1024                   4.9,  5.4      6.9,  7.4
+//     12352 x 2048                12.0, 14.8     13.3, 13.4
+//     131071 x 2048               70.8, 90.4     61.5, 62.3
+//     4096 x 4096                 12.9, 14.7      9.8, 10.3
+//     1000 x 8192                 18.0, 19.6     10.4, 10.8
+//     400 x 512        100 rows    5.4            7.4
+//     200 x 512        500 rows    6.3            8.9
+//     112 x 1152       139 rows    7.5            9.9
+//     300 x 1792       207 rows    9.1            9.2
+//     1208 x 1984      318 rows   30.9           11.6
 static bool on_tcgen05(int rows, int n_out, int k, int out_f32) {
     if (rows <= 2 || out_f32) return false;
-    return rows > 16 || k >= 4096 || (rows > 8 && k >= 2048) || (long)n_out * k >= 1l << 25;
+    if (rows > 16) return k >= 1536 || (long)rows * n_out >= 1l << 17;
+    return k >= 4096 || (rows > 8 && k >= 2048) || (long)n_out * k >= 1l << 25;
 }
 
 size_t q4_workspace_bytes(int rows, int n_out, int k, int out_f32) { return on_tcgen05(rows, n_out, k, out_f32) ? q4_tc_workspace_bytes(rows, k) : 0; }

@@ -597,7 +597,7 @@ GDN_API gdn_status gdn_ssm_scan(int n_seqs, int total_tokens, int channels, int 
  *   scales, offsets    bf16 [n_out, k / group]; offsets may be NULL
  *   out                [rows, n_out], dtype out_dtype
  *
- *   workspace          at least gdn_q4_workspace_size() bytes for the same sizes (0 for small products of few rows, and for fp32 outputs),
+ *   workspace          at least gdn_q4_workspace_size() bytes for the same sizes (0 for small products, and for fp32 outputs),
  *                      256-byte aligned; contents do not matter
  *
  * Products and sums are fp32; out is rounded once.  Calls that need no workspace take codes as they are into the products,

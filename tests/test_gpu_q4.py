@@ -36,7 +36,8 @@ def rows_of(rows, k, seed):
 
 @pytest.mark.parametrize("group,offsets", [(64, True), (64, False), (128, True), (128, False)])
 @pytest.mark.parametrize("rows,n_out,k", [(1, 1, 128), (1, 17, 256), (2, 1000, 2048), (7, 16, 1152), (9, 333, 640), (16, 50, 4096),
-                                          (17, 129, 512), (33, 2047, 1024), (65, 200, 384), (130, 300, 2176)])
+                                          (17, 129, 512), (33, 2047, 1024), (65, 200, 384), (130, 300, 2176), (40, 200, 1664), (150, 1001, 384),
+                                          (600, 250, 128)])
 def test_sizes(linear, rows, n_out, k, group, offsets):
     w, x = matrix(linear, n_out, k, group, offsets, seed=k), rows_of(rows, k, seed=rows)
     ref.check(linear.q4_linear(x, w, out_dtype=F32), *ref.q4_product(x, w))
@@ -53,7 +54,7 @@ def test_rows(linear, rows, n_out, k):
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 @pytest.mark.parametrize("group,offsets", [(64, True), (128, False)])
 @pytest.mark.parametrize("rows,n_out,k", [(1, 1, 128), (1, 5632, 2048), (5, 77, 256), (13, 1001, 384), (30, 40, 2048), (64, 513, 1024),
-                                          (200, 260, 640)])
+                                          (200, 260, 640), (64, 513, 1664), (200, 1000, 640), (90, 100, 2048), (300, 450, 128)])
 def test_gated(linear, rows, n_out, k, group, offsets, act):
     gate, up = (matrix(linear, n_out, k, group, offsets, seed=s) for s in (1, 2))
     x = rows_of(rows, k, seed=rows)
@@ -108,9 +109,10 @@ def test_slices_shapes_and_outputs(linear):
     assert linear.q4_linear(x[:0], w).shape == (0, 96)
 
 
+@pytest.mark.parametrize("k", [512, 2048])
 @pytest.mark.parametrize("rows", [1, 20, 64, 300])
-def test_not_finite_rows_stay_alone(linear, rows):
-    w, x = matrix(linear, 200, 512, 64, True, seed=9), rows_of(rows, 512, seed=10)
+def test_not_finite_rows_stay_alone(linear, rows, k):
+    w, x = matrix(linear, 200, k, 64, True, seed=9), rows_of(rows, k, seed=10)
     want = linear.q4_linear(x, w)
     x[rows // 2, 100] = float("nan")
     if rows > 4:
@@ -122,32 +124,34 @@ def test_not_finite_rows_stay_alone(linear, rows):
     assert torch.equal(out[rest], want[rest])
 
 
-def test_large_and_small_values(linear):
+@pytest.mark.parametrize("k", [512, 2048])
+def test_large_and_small_values(linear, k):
     """Activations up to 1e30 and down to 1e-30 in one call: every row keeps its own precision."""
-    w, x = matrix(linear, 300, 512, 64, True, seed=11), rows_of(40, 512, seed=12).float()
+    w, x = matrix(linear, 300, k, 64, True, seed=11), rows_of(40, k, seed=12).float()
     x = (x * 10.0 ** torch.linspace(-30, 30, 40, device="cuda")[:, None]).to(BF)
     ref.check(linear.q4_linear(x, w, out_dtype=F32), *ref.q4_product(x, w))
-    ref.check(linear.q4_linear(x, w), *ref.q4_product(x, w, rounded=True))
+    ref.check(linear.q4_linear(x, w), *ref.q4_product(x, w, rounded=rounds(linear, x, w)))
 
 
-@pytest.mark.parametrize("rows", [3, 50])
-def test_weights_of_very_different_sizes(linear, rows):
+@pytest.mark.parametrize("rows,k", [(3, 1024), (50, 1024), (50, 2048)])
+def test_weights_of_very_different_sizes(linear, rows, k):
     """Rows of weights up to 1e30 and down to 1e-30, and groups in a row a million times smaller than others."""
-    w, x = matrix(linear, 200, 1024, 64, True, seed=21), rows_of(rows, 1024, seed=22)
-    f = 10.0 ** torch.linspace(-30, 30, 200, device="cuda")[:, None] * 10.0 ** (-6 * torch.rand(200, 16, device="cuda"))
+    w, x = matrix(linear, 200, k, 64, True, seed=21), rows_of(rows, k, seed=22)
+    f = 10.0 ** torch.linspace(-30, 30, 200, device="cuda")[:, None] * 10.0 ** (-6 * torch.rand(200, k // 64, device="cuda"))
     w = linear.Q4(w.codes, (w.scales * f).to(BF), (w.offsets * f).to(BF))
     ref.check(linear.q4_linear(x, w, out_dtype=F32), *ref.q4_product(x, w))
     ref.check(linear.q4_linear(x, w), *ref.q4_product(x, w, rounded=rounds(linear, x, w)))
 
 
-def test_rows_of_zeros(linear):
-    w, x = matrix(linear, 200, 512, 64, True, seed=23), rows_of(40, 512, seed=24)
+@pytest.mark.parametrize("k", [512, 2048])
+def test_rows_of_zeros(linear, k):
+    w, x = matrix(linear, 200, k, 64, True, seed=23), rows_of(40, k, seed=24)
     x[3] = 0
     zero = linear.Q4(w.codes, w.scales.clone(), w.offsets.clone())
     zero.scales[7], zero.offsets[7] = 0, 0
     out = linear.q4_linear(x, zero)
     assert (out[3] == 0).all() and (out[:, 7] == 0).all()
-    ref.check(out, *ref.q4_product(x, zero, rounded=True))
+    ref.check(out, *ref.q4_product(x, zero, rounded=rounds(linear, x, zero)))
 
 
 @pytest.mark.parametrize("offsets", [True, False])
@@ -166,9 +170,10 @@ def test_quantize(linear, offsets, group):
     assert (linear.values(zero) == 0).all()
 
 
-def test_streams_and_graphs(linear):
-    w, x = matrix(linear, 1000, 2048, 64, True, seed=13), rows_of(3, 2048, seed=14)
-    y, e = ref.q4_product(x, w, rounded=False)
+@pytest.mark.parametrize("rows", [1, 3, 40])
+def test_streams_and_graphs(linear, rows):
+    w, x = matrix(linear, 1000, 2048, 64, True, seed=13), rows_of(rows, 2048, seed=14)
+    y, e = ref.q4_product(x, w, rounded=rounds(linear, x, w))
     other = torch.cuda.Stream()
     other.wait_stream(torch.cuda.current_stream())
     out = linear.q4_linear(x, w, stream=other)
@@ -177,10 +182,11 @@ def test_streams_and_graphs(linear):
     graph, keep = torch.cuda.CUDAGraph(), x.clone()
     with torch.cuda.graph(graph):
         out = linear.q4_linear(keep, w)
-    keep.copy_(rows_of(3, 2048, seed=15))
-    graph.replay()
-    y, e = ref.q4_product(keep, w, rounded=False)
-    ref.check(out, y, e)
+    for seed in (15, 16):
+        keep.copy_(rows_of(rows, 2048, seed=seed))
+        graph.replay()
+        y, e = ref.q4_product(keep, w, rounded=rounds(linear, keep, w))
+        ref.check(out, y, e)
 
 
 def test_calls_at_once(linear):

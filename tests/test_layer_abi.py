@@ -88,6 +88,9 @@ def q4(lib, gated, **kw):
     return lib.gdn_q4_linear(*first, P(a["out"]), a["odt"], P(a["ws"]), a["wsb"], None)
 
 
+MANY = dict(rows=100, k=2048, xs=2048)                # a call that needs a workspace
+
+
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("kw,status", [
     (dict(rows=-1), INVALID), (dict(n=0), INVALID), (dict(k=0), INVALID), (dict(k=96), UNSUPPORTED), (dict(group=32), UNSUPPORTED),
@@ -96,8 +99,8 @@ def q4(lib, gated, **kw):
     (dict(scales=None), INVALID), (dict(out=None), INVALID), (dict(xs=248), INVALID), (dict(xs=260), ALIGNMENT),
     (dict(x=at(0) + 8), ALIGNMENT), (dict(codes=at(1) + 8), ALIGNMENT), (dict(scales=at(2) + 2), ALIGNMENT),
     (dict(offsets=at(3) + 2), ALIGNMENT), (dict(out=at(7) + 2), ALIGNMENT), (dict(out=at(0)), INVALID), (dict(out=at(2) + 16), INVALID),
-    (dict(rows=100, ws=None), WORKSPACE), (dict(rows=100, wsb=100 * 256 * 2), WORKSPACE), (dict(rows=100, ws=at(8) + 16), ALIGNMENT),
-    (dict(rows=100, ws=at(1)), INVALID)])
+    (dict(MANY, ws=None), WORKSPACE), (dict(MANY, wsb=100 * 2048 * 2), WORKSPACE), (dict(MANY, ws=at(8) + 16), ALIGNMENT),
+    (dict(MANY, ws=at(1)), INVALID)])
 def test_q4_refuses(lib, gated, kw, status):
     assert q4(lib, gated, **kw) == status
     assert q4(lib, gated, rows=0) == OK
@@ -107,7 +110,8 @@ def test_q4_workspace(lib):
     st = ctypes.c_int(-1)
     size = lambda *a: (lib.gdn_q4_workspace_size(*a, st), st.value)  # noqa: E731
     assert size(1, 40, 256, 64, 0) == (0, OK) and size(1000, 40, 256, 64, 1) == (0, OK)
-    assert size(100, 40, 256, 64, 0)[0] >= 100 * 256 * 2
+    assert size(100, 40, 256, 64, 0) == (0, OK) and size(1000, 40, 2048, 64, 1) == (0, OK)
+    assert size(100, 40, 2048, 64, 0)[0] >= 100 * 2048 * 2 and size(1000, 400, 256, 64, 0)[0] >= 1000 * 256 * 2
     for bad, status in (((-1, 40, 256, 64, 0), INVALID), ((1, 40, 250, 64, 0), UNSUPPORTED), ((1, 40, 256, 64, 2), UNSUPPORTED)):
         assert size(*bad) == (0, status)
 
