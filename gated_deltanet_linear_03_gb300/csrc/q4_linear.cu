@@ -333,7 +333,7 @@ cudaError_t by_rows(const Q4Problem &p) {
 static bool on_tcgen05(int rows, int n_out, int k, int out_f32) {
     if (rows <= 2 || out_f32) return false;
     if (rows > 16) return k >= 1536 || (long)rows * n_out >= 1l << 17;
-    return k >= 4096 || (rows > 8 && k >= 2048) || (long)n_out * k >= 1l << 25;
+    return k >= 3328 || (rows > 8 && k >= 2048) || (long)n_out * k >= 1l << 25;
 }
 
 size_t q4_workspace_bytes(int rows, int n_out, int k, int out_f32) { return on_tcgen05(rows, n_out, k, out_f32) ? q4_tc_workspace_bytes(rows, k) : 0; }

@@ -8,7 +8,7 @@
 // Both operands are fp16, each row scaled by a power of two:
 //   x    the row's largest magnitude goes to [2^14, 2^15).  A bf16 number keeps all its bits down to 2^-32 of that.  A first kernel
 //        does this, and puts each 8 inputs in the order 0 4 1 5 2 6 3 7, in which a code word's pairs come out.
-//   W    by the row's largest 15 |scale| + |offset|, which goes to [2^-6, 2^-5); an element is rounded once, to fp16: by 2^-11 of itself
+//   W    by the row's largest 15 |scale| + |offset| at the CTA's inputs, which goes to [2^-6, 2^-5); an element is rounded once, to fp16: by 2^-11 of itself
 //        and 2^-19 of the row's largest at most.  A code c in the low mantissa bits of a half is c 2^-24 (a subnormal, which the
 //        arithmetic takes as any other number), so one AND and one fused product-sum with (scale 2^24, offset) make two weights.
 // Sums are fp32; the powers of two are undone at the end.
@@ -17,7 +17,7 @@
 //
 // Bound by the products for many rows (with x as second operand of N rows a product of 16 inputs takes N / 2 + 11 cycles, at least 41), by
 // a CTA's beginning and end for few: launch, scales and first codes 3 us, last barrier, join and outputs 3 us.  Measured on a GB300:
-// 4096 x 4096 with 33 rows 10.8 us, 128 rows 13.3, 512 rows 23.8 (720 TFLOP/s); 131071 x 2048 with 33 rows 66 us, 100 rows 78 (690); gated
+// 4096 x 4096 with 33 rows 11.0 us, 128 rows 13.6, 512 rows 23.8 (720 TFLOP/s); 131071 x 2048 with 33 rows 66 us, 100 rows 78 (690); gated
 // 2 x 6000 x 2048 with 509 rows 27.8 us (900 TFLOP/s; tensor pipe 0.47 active over the whole time).
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -206,14 +206,15 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
         sm.abort = 0;
         fence_mbar_init();
     }
-    if (warp < WARPS) {                         // each group of warps a part of one matrix's groups
-        const int m = warp / 4 / T::PARTS, part = warp / 4 % T::PARTS, each = (groups + T::PARTS - 1) / T::PARTS, g0 = min(part * each, groups);
-        sm.tops[warp / 4][r] = largest<OFFSETS>(m ? p.up : p.w, row * groups + g0, min(each, groups - g0), (size_t)p.n_out * groups);
+    if (warp < WARPS) {                         // each group of warps a part of what this CTA needs of one matrix's groups
+        const int begin = k0 / p.group, end = min(groups, begin + l.slice * kChunkIn / p.group), each = (end - begin + T::PARTS - 1) / T::PARTS;
+        const int m = warp / 4 / T::PARTS, g0 = min(begin + warp / 4 % T::PARTS * each, end);
+        sm.tops[warp / 4][r] = largest<OFFSETS>(m ? p.up : p.w, row * groups + g0, min(each, end - g0), (size_t)p.n_out * groups);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    int exponent[MATS];                         // of this thread's weight rows: W is scaled by 2^-exponent
+    int exponent[MATS];                         // of this thread's weight rows, at this CTA's inputs: W is scaled by 2^-exponent
 #pragma unroll
     for (int m = 0; m < MATS; ++m) {
         float top = sm.tops[m * T::PARTS][r];
@@ -356,11 +357,13 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
     const int e1 = exponent[MATS - 1];
     const float2 undo1 = make_float2(power_of_two(e1 / 2), power_of_two(e1 - e1 / 2));
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + (size_t)m0 * p.n_out + n;
-    auto write = [&](int m, float y, float z) {
-        // the halves of a power have its sign, so that nothing overflows in between that does not in the end
+    // the halves of a power have its sign, so that nothing overflows in between that does not in the end
+    const auto undone = [&](int m, float v, const float2 &of_row) {
         const float2 u = sm.undo[m];
-        y = y * (undo0.x * u.x) * (undo0.y * u.y);
-        if constexpr (GATED) y = ffn_act_fast(y, p.gelu) * (z * (undo1.x * u.x) * (undo1.y * u.y));
+        return v * (of_row.x * u.x) * (of_row.y * u.y);
+    };
+    const auto write = [&](int m, float y, float z) {
+        if constexpr (GATED) y = ffn_act_fast(y, p.gelu) * z;
         if (n < p.n_out) out[(size_t)m * p.n_out] = __float2bfloat16_rn(y);
     };
     float *part = reinterpret_cast<float *>(base);            // [matrix][column][row]: the pipeline is done with this memory
@@ -370,11 +373,14 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
             tmem_ld8x2(tmem + col + lanes, tmem + (MATS - 1) * l.ntok + col + lanes, y, z);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
+                const int m = col + i;
+                if (m >= m_end) continue;
+                const float v = undone(m, y[i], undo0), w = GATED ? undone(m, z[i], undo1) : 0.f;
                 if (l.cluster > 1) {
-                    part[(col + i) * kRowsA + r] = y[i];
-                    if (GATED) part[(l.ntok + col + i) * kRowsA + r] = z[i];
-                } else if (col + i < m_end) {
-                    write(col + i, y[i], z[i]);
+                    part[m * kRowsA + r] = v;
+                    if (GATED) part[(l.ntok + m) * kRowsA + r] = w;
+                } else {
+                    write(m, v, w);
                 }
             }
         }
