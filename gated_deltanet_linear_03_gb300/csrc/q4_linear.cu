@@ -10,7 +10,8 @@
 //
 // Codes and x come by TMA, stages of 16 w weight rows (w = 1, 2, 4 or 8) and all rows of x by 256 inputs, which one thread asks for
 // several stages ahead, across tiles: what reads memory is never waiting for what computes.  Eight warps compute, w along the rows by
-// 8 / w along the inputs; a ninth asks; a tenth sums x over blocks of 64 inputs.  Partial sums meet in shared memory in a fixed order.
+// 8 / w along the inputs; a ninth asks; a tenth sums x over blocks of 64 inputs.  Partial sums meet in shared memory in a fixed order; where there are few tiles, those of up to 8
+// CTAs of a cluster that share a tile's inputs (608 x 7424, 31 rows, fp32: 25.7 to 9.9 us).
 //
 // Bound by latencies, of barriers above all (a wait that finds its phase complete takes some 250 cycles, and a stage has three), not by
 // the codes: 12352 x 2048 with 3 rows 12.0 us, 1.2 TB/s; with 16 14.8.  fp32 outputs of many rows, which have to keep groups apart, pay
@@ -54,6 +55,7 @@ __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&v)[4]) {
 
 struct FewPlan {
     int w, m_blocks, row_tiles, stages;
+    int cluster, slice;                   // CTAs that share a tile's inputs (then each has one tile), and a CTA's chunks of them
     int codes_bytes;                      // of a stage
 };
 
@@ -75,7 +77,9 @@ q4_few_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ FewPl
     float *part = sums + l.stages * 4 * COLS;                                            // [2][8 / w][COLS][16 w + 4]
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const int w = l.w, kw = kWarps / w, rows = 16 * w, out_rows = GATED ? rows / 2 : rows;
-    const int chunks = (p.k + kChunkIn - 1) / kChunkIn, units = l.row_tiles * l.m_blocks;
+    const int units = l.row_tiles * l.m_blocks, rank = l.cluster > 1 ? (int)cluster_ctarank() : 0;
+    const int first = blockIdx.x / l.cluster, step = gridDim.x / l.cluster;
+    const int c0 = rank * l.slice, c1 = min(c0 + l.slice, (p.k + kChunkIn - 1) / kChunkIn);
     volatile int *abort = &sm.abort;
 
     if (threadIdx.x == 0) {
@@ -91,13 +95,28 @@ q4_few_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ FewPl
     }
     __syncthreads();
 
+    // Output i of a tile, neighbours for neighbouring threads: where its sums are in a part, and its end
+    const int stride = rows + 4;
+    const auto place = [&](int i) {
+        const int r = i & (out_rows - 1);
+        return i / out_rows * stride + (GATED ? r / 8 * 16 + r % 8 : r);
+    };
+    const auto write = [&](int n0, int m0, int i, float y, float z) {
+        const int n = n0 + (i & (out_rows - 1)), m = m0 + i / out_rows;
+        if (GATED) y = ffn_act(y, p.gelu) * z;
+        if (n >= p.n_out) return;
+        const size_t to = (size_t)m * p.n_out + n;
+        if (p.out_f32) static_cast<float *>(p.out)[to] = y;
+        else static_cast<__nv_bfloat16 *>(p.out)[to] = __float2bfloat16_rn(y);
+    };
+
     int s = 0, phase = 0;
     const auto advance = [&] { if (++s == l.stages) s = 0, phase ^= 1; };
     if (warp == kWarps) {
         if (elect_one()) {
-            for (int u = blockIdx.x; u < units && !*abort; u += gridDim.x) {
+            for (int u = first; u < units && !*abort; u += step) {
                 const int n0 = u / l.m_blocks * out_rows, m0 = u % l.m_blocks * COLS;
-                for (int c = 0; c < chunks; ++c) {
+                for (int c = c0; c < c1; ++c) {
                     mbar_poll(&sm.empty[s], phase ^ 1, abort);
                     if (*abort) break;
                     unsigned char *to = base + (size_t)s * stage_bytes;
@@ -115,8 +134,8 @@ q4_few_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ FewPl
         // sums of x over blocks of 64 inputs: a lane a block of a row, the four blocks at different banks
         const int j = lane % 4;
         bool gone = false;
-        for (int u = blockIdx.x; u < units && !gone; u += gridDim.x)
-            for (int c = 0; c < chunks; ++c) {
+        for (int u = first; u < units && !gone; u += step)
+            for (int c = c0; c < c1; ++c) {
                 mbar_poll(&sm.full[s], phase, abort);
                 if (gone = __any_sync(0xffffffffu, *abort)) break;
                 const unsigned char *x = base + (size_t)s * stage_bytes + l.codes_bytes + j * X_BOX;
@@ -146,11 +165,10 @@ q4_few_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ FewPl
         const Q4Matrix &second = GATED ? p.up : p.w;
         // where this lane's codes are in a stage: rows g and g + 8 of its 16, or row g of its 8 of either matrix
         const int line0 = (GATED ? 8 * rg + g : 16 * rg + g) * 128, line1 = GATED ? l.codes_bytes / 2 + line0 : line0 + 8 * 128;
-        const int stride = rows + 4;
         size_t r0 = 0, r1 = 0;
         ChunkScales next0, next1;
         const auto ask = [&](int u, int c) {      // the scales of unit u's chunk c (a row beyond the matrix repeats its last one)
-            if (c == 0) {
+            if (c == c0) {
                 const int n = u / l.m_blocks * out_rows + (GATED ? 8 : 16) * rg + g;
                 r0 = min(n, p.n_out - 1);
                 r1 = GATED ? r0 : min(n + 8, p.n_out - 1);
@@ -160,17 +178,17 @@ q4_few_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ FewPl
         };
         int buffer = 0, joins = 0;
         bool gone = false;
-        if ((int)blockIdx.x < units) ask(blockIdx.x, 0);
-        for (int u = blockIdx.x; u < units && !gone; u += gridDim.x) {
+        if (first < units) ask(first, c0);
+        for (int u = first; u < units && !gone; u += step) {
             float acc[NT][4];
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-            for (int c = 0; c < chunks; ++c) {
+            for (int c = c0; c < c1; ++c) {
                 const ChunkScales cur0 = next0, cur1 = next1;
-                if (c + 1 < chunks) ask(u, c + 1);
-                else if (u + (int)gridDim.x < units) ask(u + gridDim.x, 0);
+                if (c + 1 < c1) ask(u, c + 1);
+                else if (u + step < units) ask(u + step, c0);
                 mbar_poll(&sm.full[s], phase, abort);
                 mbar_poll(&sm.summed[s], phase, abort);
                 if (gone = __any_sync(0xffffffffu, *abort)) break;
@@ -229,6 +247,7 @@ q4_few_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ FewPl
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     mine[(ks * COLS + 8 * i + 2 * t + (e & 1)) * stride + 16 * rg + g + (e & 2) * 4] = acc[i][e];
+            if (l.cluster > 1) break;
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.joined[buffer]);
             mbar_poll(&sm.joined[buffer], joins >> 1 & 1, abort);
@@ -236,21 +255,42 @@ q4_few_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ FewPl
             ++joins;
             const int n0 = u / l.m_blocks * out_rows, m0 = u % l.m_blocks * COLS, m_rows = min(COLS, p.rows - m0);
             for (int i = threadIdx.x; i < out_rows * m_rows; i += 32 * kWarps) {
-                const int r = i & (out_rows - 1), m = i / out_rows, n = n0 + r;        // neighbours write neighbouring outputs
-                const int from = GATED ? r / 8 * 16 + r % 8 : r;
+                const float *at = mine + place(i);
                 float y = 0.f, z = 0.f;
                 for (int k = 0; k < kw; ++k) {
-                    y += mine[(k * COLS + m) * stride + from];
-                    if (GATED) z += mine[(k * COLS + m) * stride + from + 8];
+                    y += at[k * COLS * stride];
+                    if (GATED) z += at[k * COLS * stride + 8];
                 }
-                if (GATED) y = ffn_act(y, p.gelu) * z;
-                if (n >= p.n_out) continue;
-                const size_t to = (size_t)(m0 + m) * p.n_out + n;
-                if (p.out_f32) static_cast<float *>(p.out)[to] = y;
-                else static_cast<__nv_bfloat16 *>(p.out)[to] = __float2bfloat16_rn(y);
+                write(n0, m0, i, y, z);
             }
             buffer ^= 1;
         }
+    }
+    if (l.cluster > 1) {
+        __syncwarp();
+        cluster_sync();
+        if (warp < kWarps && !*abort) {
+            const int n0 = first / l.m_blocks * out_rows, m0 = first % l.m_blocks * COLS, m_rows = min(COLS, p.rows - m0);
+            for (int i = threadIdx.x + 32 * kWarps * rank; i < out_rows * m_rows; i += 32 * kWarps * l.cluster) {
+                const float *at = part + place(i);
+                float y = 0.f, z = 0.f;
+                for (int k = 0; k < kw; ++k) {
+                    float ys[8], zs[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        ys[q] = q < l.cluster ? ld_dsmem_f32(at + k * COLS * stride, q) : 0.f;
+                        if (GATED) zs[q] = q < l.cluster ? ld_dsmem_f32(at + k * COLS * stride + 8, q) : 0.f;
+                    }
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        y += ys[q];
+                        if (GATED) z += zs[q];
+                    }
+                }
+                write(n0, m0, i, y, z);
+            }
+        }
+        cluster_sync();                    // a CTA's sums are read before it is gone
     }
     __syncthreads();
     if (threadIdx.x == 0 && sm.abort) raise_error(err, kErrTimeout);
@@ -267,12 +307,19 @@ cudaError_t launch(const Q4Problem &p) {
     const int sms = multiprocessor_count();
     FewPlan l{};
     l.m_blocks = (p.rows + COLS - 1) / COLS;
-    // rows of a tile: as few rounds as possible of tiles that cost their rows and a little
+    // Rows of a tile, and CTAs that share its inputs where that fills the GPU: as few rounds as possible of tiles that cost their rows
+    // and a little, for each chunk of inputs.  A join costs as much as four such units.
+    const int chunks = (p.k + kChunkIn - 1) / kChunkIn;
     double least = 1e300;
     for (int w = 8; w >= 1; w /= 2) {
         const long tiles = (p.n_out + (GATED ? 8 : 16) * w - 1) / ((GATED ? 8 : 16) * w);
-        const double cost = ceil((double)tiles * l.m_blocks / (sms * FIT)) * (w + 0.7);
-        if (cost < least) least = cost, l.w = w, l.row_tiles = (int)tiles;
+        for (int cluster = 1; cluster <= 8 && cluster <= chunks; cluster *= 2) {
+            const int slice = (chunks + cluster - 1) / cluster;
+            const double ctas = (double)tiles * l.m_blocks * cluster;
+            if (cluster > 1 && (ctas > 0.85 * sms * FIT || (long)slice * (cluster - 1) >= chunks)) continue;
+            const double cost = ceil(ctas / (sms * FIT)) * (w + 0.7) * slice + (cluster > 1 ? 4 : 0);
+            if (cost < least) least = cost, l.w = w, l.row_tiles = (int)tiles, l.cluster = cluster, l.slice = slice;
+        }
     }
     l.codes_bytes = 16 * l.w * 128;
     constexpr size_t kShared = (FIT == 2 ? 112 : 226) * 1024 - sizeof(FewBars);
@@ -300,8 +347,18 @@ cudaError_t launch(const Q4Problem &p) {
         if (dev < kMaxDevices) ready[dev][offsets][exact].store(true, std::memory_order_relaxed);
     }
     const long units = (long)l.row_tiles * l.m_blocks;
-    fns[offsets][exact]<<<(unsigned)min(units, (long)sms * FIT), kThreads, few_shared(COLS, l), p.stream>>>(p, l, codes, up, x, error_word());
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(l.cluster > 1 ? units * l.cluster : min(units, (long)sms * FIT)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = few_shared(COLS, l);
+    cfg.stream = p.stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = l.cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = l.cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, fns[offsets][exact], p, l, codes, up, x, error_word());
 }
 
 // A CTA takes 8, 16 or 32 rows of x.  With 32 rows two CTAs fit on an SM at 96 registers a thread instead of 168, which pays where there
@@ -317,30 +374,32 @@ cudaError_t by_rows(const Q4Problem &p) {
 }  // namespace
 
 // bf16 outputs: the kernel that multiplies on tcgen05, whose weights are rounded to fp16, or the one above for small products.  The one
-// above does not share a tile's inputs among CTAs and unpacks for every 8 to 32 rows; the other takes 7 us for nothing.
+// above unpacks for every 8 to 32 rows; the other takes 7 us for nothing.
 //     n_out x k        above                     on tcgen05
-//     300 x 512        3, 16 rows  3.8,  4.2 us   7.1,  7.2 us
-//     500 x 1024                   4.9,  5.4      6.9,  7.4
-//     12352 x 2048                12.0, 14.8     13.3, 13.4
-//     131071 x 2048               70.8, 90.4     61.5, 62.3
-//     4096 x 4096                 12.9, 14.7      9.8, 10.3
-//     1000 x 8192                 18.0, 19.6     10.4, 10.8
+//     300 x 512        3, 16 rows  3.9,  4.3 us   7.1,  7.2 us
+//     1000 x 8192                  7.5,  9.0     10.4, 10.7
+//     4096 x 4096                  7.9,  8.9     10.1, 10.7
+//     12000 x 4096                16.8, 21.7     20.4, 20.6
+//     12352 x 2048                12.4, 15.2     13.3, 13.5
+//     131071 x 2048               72.8, 93.9     62.2, 62.9
+//     2 x 14000 x 2048            25.5, 29.8     18.2, 18.7
 //     400 x 512        100 rows    5.4            7.4
 //     200 x 512        500 rows    6.3            8.9
-//     112 x 1152       139 rows    7.5            9.9
-//     300 x 1792       207 rows    9.1            9.2
+//     266 x 8192       67 rows     9.8           11.9
 //     1208 x 1984      318 rows   30.9           11.6
-static bool on_tcgen05(int rows, int n_out, int k, int out_f32) {
+//     1000 x 2048      64 rows    12.8            9.1
+static bool on_tcgen05(int rows, int n_out, int k, int matrices, int out_f32) {
     if (rows <= 2 || out_f32) return false;
-    if (rows > 16) return k >= 1536 || (long)rows * n_out >= 1l << 17;
-    return k >= 3328 || (rows > 8 && k >= 2048) || (long)n_out * k >= 1l << 25;
+    if (rows <= 16) return (double)n_out * matrices * k >= (rows > 8 ? 20e6 : 50e6);
+    return (long)rows * n_out >= (k < 1536 ? 1l << 17 : 3l << 13) || (k >= 1536 && n_out > 512);
 }
 
-size_t q4_workspace_bytes(int rows, int n_out, int k, int out_f32) { return on_tcgen05(rows, n_out, k, out_f32) ? q4_tc_workspace_bytes(rows, k) : 0; }
+// (of either call, that with one matrix and that with two)
+size_t q4_workspace_bytes(int rows, int n_out, int k, int out_f32) { return on_tcgen05(rows, n_out, k, 2, out_f32) ? q4_tc_workspace_bytes(rows, k) : 0; }
 
 cudaError_t launch_q4(const Q4Problem &p) {
     if (q4_vec_takes(p.rows, p.k)) return launch_q4_vec(p);
-    if (on_tcgen05(p.rows, p.n_out, p.k, p.out_f32)) return launch_q4_tc(p);
+    if (on_tcgen05(p.rows, p.n_out, p.k, p.gated ? 2 : 1, p.out_f32)) return launch_q4_tc(p);
     return p.gated ? by_rows<true>(p) : by_rows<false>(p);
 }
 

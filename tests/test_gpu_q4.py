@@ -25,7 +25,7 @@ def matrix(linear, n_out, k, group, offsets, seed):
 
 
 def rounds(linear, x, w):
-    """Calls that need a workspace round the weights to fp16; in the others codes enter the products as they are."""
+    """Calls that need a workspace may round the weights to fp16; in the others codes enter the products as they are."""
     return linear.workspace_size(x.shape[0], w.codes.shape[0], x.shape[1], x.shape[1] // w.scales.shape[1]) > 0
 
 

@@ -88,7 +88,7 @@ def q4(lib, gated, **kw):
     return lib.gdn_q4_linear(*first, P(a["out"]), a["odt"], P(a["ws"]), a["wsb"], None)
 
 
-MANY = dict(rows=100, k=2048, xs=2048)                # a call that needs a workspace
+MANY = dict(rows=100, n=4000, k=2048, xs=2048)                # a call that needs a workspace
 
 
 @pytest.mark.parametrize("gated", [False, True])
@@ -110,8 +110,8 @@ def test_q4_workspace(lib):
     st = ctypes.c_int(-1)
     size = lambda *a: (lib.gdn_q4_workspace_size(*a, st), st.value)  # noqa: E731
     assert size(1, 40, 256, 64, 0) == (0, OK) and size(1000, 40, 256, 64, 1) == (0, OK)
-    assert size(100, 40, 256, 64, 0) == (0, OK) and size(1000, 40, 2048, 64, 1) == (0, OK)
-    assert size(100, 40, 2048, 64, 0)[0] >= 100 * 2048 * 2 and size(1000, 400, 256, 64, 0)[0] >= 1000 * 256 * 2
+    assert size(100, 40, 256, 64, 0) == (0, OK) and size(1000, 4000, 2048, 64, 1) == (0, OK)
+    assert size(100, 4000, 2048, 64, 0)[0] >= 100 * 2048 * 2 and size(1000, 400, 256, 64, 0)[0] >= 1000 * 256 * 2
     for bad, status in (((-1, 40, 256, 64, 0), INVALID), ((1, 40, 250, 64, 0), UNSUPPORTED), ((1, 40, 256, 64, 2), UNSUPPORTED)):
         assert size(*bad) == (0, status)
 
