@@ -15,7 +15,7 @@
 //
 // Bound by latencies, of barriers above all (a wait that finds its phase complete takes some 250 cycles, and a stage has three), not by
 // the codes: 12352 x 2048 with 3 rows 12.0 us, 1.2 TB/s; with 16 14.8.  fp32 outputs of many rows, which have to keep groups apart, pay
-// for every 32 rows again: 4096 x 4096 with 33 rows 22.7 us, 512 rows 103 (167 TFLOP/s); 131071 x 2048 with 33 rows 203.
+// for every 32 rows again: 4096 x 4096 with 33 rows 23 us, 512 rows 105 (165 TFLOP/s); 131071 x 2048 with 33 rows 205.
 //
 // A fragment's order of inputs is free as long as both operands keep it: lane (g, t) takes inputs 16 t .. 16 t + 15 of a block of 64,
 // for weight rows g and g + 8 (of two matrices, rows g of each) and for row g of x: 8 bytes of codes and 32 bytes of x in a row.
