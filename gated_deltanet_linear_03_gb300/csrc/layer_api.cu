@@ -73,7 +73,7 @@ gdn_status q4(int rows, int n_out, int k, int group, const void *x, long long x_
     for (const void *p : ptrs)
         if (!aligned(p)) return GDN_ERR_ALIGNMENT;
     const size_t codes = (size_t)n_out * (k / 2), scales = (size_t)n_out * (k / group) * 2;
-    const size_t need = gdn::q4_workspace_bytes(rows, n_out, k, out_dtype == GDN_DTYPE_F32);
+    const size_t need = gdn::q4_workspace_bytes(rows, n_out, k, group, out_dtype == GDN_DTYPE_F32);
     if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return GDN_ERR_ALIGNMENT;
     const Range outs[] = {{out, (size_t)rows * n_out * (out_dtype == GDN_DTYPE_F32 ? 4 : 2)}, {workspace, need}};
@@ -209,7 +209,7 @@ size_t gdn_q4_workspace_size(int rows, int n_out, int k, int group, int out_dtyp
     gdn_status st = check_q4_shape(rows, n_out, k, group);
     if (st == GDN_OK && out_dtype != GDN_DTYPE_BF16 && out_dtype != GDN_DTYPE_F32) st = GDN_ERR_UNSUPPORTED;
     if (status) *status = st;
-    return st == GDN_OK ? gdn::q4_workspace_bytes(rows, n_out, k, out_dtype == GDN_DTYPE_F32) : 0;
+    return st == GDN_OK ? gdn::q4_workspace_bytes(rows, n_out, k, group, out_dtype == GDN_DTYPE_F32) : 0;
 }
 
 gdn_status gdn_q4_linear(int rows, int n_out, int k, int group, const void *x, long long x_stride, const void *codes,

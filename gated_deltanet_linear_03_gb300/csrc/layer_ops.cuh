@@ -113,13 +113,13 @@ struct Q4Problem {
     cudaStream_t stream;
 };
 cudaError_t launch_q4(const Q4Problem &p);
-size_t q4_workspace_bytes(int rows, int n_out, int k, int out_f32);
+size_t q4_workspace_bytes(int rows, int n_out, int k, int group, int out_f32);
 // the kernel for one or two rows
 bool q4_vec_takes(int rows, int k);
 cudaError_t launch_q4_vec(const Q4Problem &p);
 // the kernel for many rows
 cudaError_t launch_q4_tc(const Q4Problem &p);
-size_t q4_tc_workspace_bytes(int rows, int k);
+size_t q4_tc_workspace_bytes(int rows, int k, int group);
 // [rows, bytes of a row, `pitch` bytes apart] read in boxes of box_bytes of box_rows rows, 128-byte swizzled or not; the second
 // form: of 128 bytes, swizzled.
 bool box_map(CUtensorMap *m, const void *at, uint64_t rows, uint64_t row_bytes, uint64_t pitch, uint32_t box_bytes, uint32_t box_rows,

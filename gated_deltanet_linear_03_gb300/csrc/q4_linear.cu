@@ -395,7 +395,9 @@ static bool on_tcgen05(int rows, int n_out, int k, int matrices, int out_f32) {
 }
 
 // (of either call, that with one matrix and that with two)
-size_t q4_workspace_bytes(int rows, int n_out, int k, int out_f32) { return on_tcgen05(rows, n_out, k, 2, out_f32) ? q4_tc_workspace_bytes(rows, k) : 0; }
+size_t q4_workspace_bytes(int rows, int n_out, int k, int group, int out_f32) {
+    return on_tcgen05(rows, n_out, k, 2, out_f32) ? q4_tc_workspace_bytes(rows, k, group) : 0;
+}
 
 cudaError_t launch_q4(const Q4Problem &p) {
     if (q4_vec_takes(p.rows, p.k)) return launch_q4_vec(p);

@@ -5,12 +5,20 @@
 // a row a thread; x lies in shared memory.  So a weight is unpacked once for all rows of x of its CTA, and never goes through
 // shared memory as a number.
 //
-// Both operands are fp16, each row scaled by a power of two:
+// Both operands are fp16, each row scaled by a power of two, and nothing of a weight is lost:
+//     W = scale (code - 8) + (offset + 8 scale),
+// of which the first part has 8 + 3 significant bits, as many as a half, and the second is the same for all inputs of a group: it
+// meets the group's sum of x.  These sums and second parts are two halves each (22 bits), so that a group is four inputs more:
+//     (hi, hi, lo, lo) of the second part by (hi, lo, hi, lo) of the sum,  16 groups to a block of 64 inputs.
+// Without offsets the second part is zero and the blocks are not there; with them they are 1/16 or 1/32 of the work.
 //   x    the row's largest magnitude goes to [2^14, 2^15).  A bf16 number keeps all its bits down to 2^-32 of that.  A first kernel
-//        does this, and puts each 8 inputs in the order 0 4 1 5 2 6 3 7, in which a code word's pairs come out.
-//   W    by the row's largest 15 |scale| + |offset| at the CTA's inputs, which goes to [2^-6, 2^-5); an element is rounded once, to fp16: by 2^-11 of itself
-//        and 2^-19 of the row's largest at most.  A code c in the low mantissa bits of a half is c 2^-24 (a subnormal, which the
-//        arithmetic takes as any other number), so one AND and one fused product-sum with (scale 2^24, offset) make two weights.
+//        does this, puts each 8 inputs in the order 0 4 1 5 2 6 3 7, in which a code word's pairs come out, and adds the groups' means
+//        (a sum would leave fp16; the second parts are multiplied by the group's size instead).
+//   W    by the row's largest 15 |scale| + |offset| at the CTA's inputs, which goes to [2^-2, 2^-1): first parts are exact for scales down to
+//        2^-15 of that, below lose 2^-22 of it at most.  A code c in bits 4 to 7 of a half is c 2^-20 (a subnormal, which the
+//        arithmetic takes as any other number), so a shift, an AND and one fused product-sum with (scale 2^20, -8 scale) make two
+//        weights.  Codes taken from bits 0 to 3 as well save three shifts in four pairs, but leave 2^-18 (131071 x 2048, 33 rows:
+//        74.5 us instead of 75); codes under the exponent of 1024 leave 2^-24 (84).
 // Sums are fp32; the powers of two are undone at the end.
 //
 // CTAs of a cluster share the inputs of one tile and join through distributed shared memory, in a fixed order.
@@ -35,6 +43,7 @@ constexpr int kBlockIn = 64;              // inputs that a thread unpacks at onc
 constexpr int kChunkIn = 256;             // inputs of a stage of codes
 constexpr int kCodeBytes = kRowsA * kChunkIn / 2;
 constexpr int kMaxStages = 4, kMaxSlots = 4;
+constexpr int kPerGroup = 4, kBlockGroups = kBlockIn / kPerGroup;      // inputs that a group's offset stands for; groups of a block of them
 
 // A step is what one wait of the thread that issues the products is for.  Its instructions between two products, a few dozen in a
 // row, take longer than a product with few columns: with one matrix a step is two blocks, which two groups of four unpacking warps
@@ -61,7 +70,7 @@ struct TcBars {
     uint32_t tmem;
     int abort;
     float2 undo[256];                     // of each row of x: the two halves of 2^-exponent
-    float tops[4][kRowsA];                // the largest 15 |scale| + |offset| of a weight row's parts
+    float tops[4][kRowsA];                // largest() of a weight row's parts
 };
 
 // 32 lanes x 32 columns of 32 bits, a lane a thread, and the wait for them.
@@ -107,7 +116,7 @@ __device__ __forceinline__ uint4 eight(const __nv_bfloat16 *all, size_t at, size
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
-// The largest 15 |scale| + |offset| of `groups` groups, by aligned reads: eight numbers may begin before them or end behind them.
+// The largest 15/16 |scale| + 1/16 |offset| of `groups` groups (which is finite where they are), by aligned reads: eight numbers may begin before them or end behind them.
 template <bool OFFSETS>
 __device__ __forceinline__ float largest(const Q4Matrix &w, size_t first, int groups, size_t total) {
     float top = 0.f;
@@ -129,7 +138,7 @@ __device__ __forceinline__ float largest(const Q4Matrix &w, size_t first, int gr
             unpack8(vo[q], fo);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float v = 15.f * fabsf(fs[e]) + fabsf(fo[e]);
+                const float v = 0.9375f * fabsf(fs[e]) + 0.0625f * fabsf(fo[e]);
                 if ((unsigned)(i + 8 * q + e - before) < (unsigned)groups) top = fmaxf(top, v);
             }
         }
@@ -153,11 +162,16 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
     const int row0 = unit / l.m_tiles * kRowsA, m0 = unit % l.m_tiles * l.ntok;
     const int chunk0 = rank * l.slice, k0 = chunk0 * kChunkIn;
     const int blocks = min(l.slice * (kChunkIn / kBlockIn), (p.k - k0) / kBlockIn);                          // at least one
-    const int steps = (blocks + T::BLOCKS - 1) / T::BLOCKS, chunks = (blocks + 3) / 4;
+    const int chunks = (blocks + 3) / 4;
+    // groups of these inputs; the blocks of their second parts, which come first, while the codes are on their way
+    const int groups = p.k / p.group, group0 = k0 / p.group, group_end = group0 + blocks * kBlockIn / p.group;
+    const int extra = OFFSETS ? (group_end - group0 + kBlockGroups - 1) / kBlockGroups : 0;
+    const int extra_steps = (extra + T::BLOCKS - 1) / T::BLOCKS, steps = extra_steps + (blocks + T::BLOCKS - 1) / T::BLOCKS;
+    const auto blocks_of = [&](int t) { return min(T::BLOCKS, t < extra_steps ? extra - t * T::BLOCKS : blocks - (t - extra_steps) * T::BLOCKS); };
     const int x_block = l.ntok * 128;                   // bytes of a block of x
     const int last_slot = (1 << l.slot_bits) - 1;
     constexpr int SLOT_COLS = 64;                       // two blocks, of one matrix or of each of two
-    const int r = tid & 127, groups = p.k / p.group;
+    const int r = tid & 127;
     const size_t row = min(row0 + r, p.n_out - 1);
 
     const auto load_codes = [&](int c, int s) {
@@ -167,10 +181,10 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
         if (GATED) tma_load_2d(to + kCodeBytes, &up_map, &sm.code_full[s], (k0 + c * kChunkIn) / 2, row0);
     };
     const auto load_x = [&](int t, int s) {
-        const int n = min(T::BLOCKS, blocks - t * T::BLOCKS);
+        const int n = blocks_of(t), at = t < extra_steps ? p.k + kPerGroup * group0 + t * T::STEP : k0 + (t - extra_steps) * T::STEP;
         mbar_arrive_expect_tx(&sm.x_full[s], n * x_block);
-        for (int i = 0; i < n; ++i)                     // (the map counts bytes)
-            tma_load_2d(xs + (size_t)(s * T::BLOCKS + i) * x_block, &x_map, &sm.x_full[s], 2 * (k0 + t * T::STEP + i * kBlockIn), m0);
+        for (int i = 0; i < n; ++i)                     // (the map counts bytes; a CTA's first group is even)
+            tma_load_2d(xs + (size_t)(s * T::BLOCKS + i) * x_block, &x_map, &sm.x_full[s], 2 * (at + i * kBlockIn), m0);
     };
 
     // The first loads are on their way before the scales have been looked over
@@ -207,9 +221,9 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
         fence_mbar_init();
     }
     if (warp < WARPS) {                         // each group of warps a part of what this CTA needs of one matrix's groups
-        const int begin = k0 / p.group, end = min(groups, begin + l.slice * kChunkIn / p.group), each = (end - begin + T::PARTS - 1) / T::PARTS;
-        const int m = warp / 4 / T::PARTS, g0 = min(begin + warp / 4 % T::PARTS * each, end);
-        sm.tops[warp / 4][r] = largest<OFFSETS>(m ? p.up : p.w, row * groups + g0, min(each, end - g0), (size_t)p.n_out * groups);
+        const int each = (group_end - group0 + T::PARTS - 1) / T::PARTS;
+        const int m = warp / 4 / T::PARTS, g0 = min(group0 + warp / 4 % T::PARTS * each, group_end);
+        sm.tops[warp / 4][r] = largest<OFFSETS>(m ? p.up : p.w, row * groups + g0, min(each, group_end - g0), (size_t)p.n_out * groups);
     }
     tc_fence_before();
     __syncthreads();
@@ -220,9 +234,9 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
         float top = sm.tops[m * T::PARTS][r];
 #pragma unroll
         for (int i = 1; i < T::PARTS; ++i) top = fmaxf(top, sm.tops[m * T::PARTS + i][r]);
-        // 2^e <= top < 2^(e + 1) goes to [2^-6, 2^-5); nothing, or what is not finite, stays
+        // 2^e <= top < 2^(e + 1), a sixteenth, goes to [2^-6, 2^-5); nothing, or what is not finite, stays
         const int e = (int)(__float_as_uint(top) >> 23) - 127;
-        exponent[m] = top > 0.f && e < 128 ? max(e, -120) + 6 : 0;
+        exponent[m] = top > 0.f && e < 128 ? e + 6 : 0;
     }
     const uint32_t tmem = sm.tmem, a_cols = tmem + MATS * l.ntok;
     volatile int *abort = &sm.abort;
@@ -271,7 +285,7 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
                 else mma_tmem_a(d, as, xd, id, 1);
 #pragma unroll
                 for (int i = 1; i < 4; ++i) mma_tmem_a(d, as + 8 * i, xd + 2 * i, id, 1);
-                if (T::BLOCKS == 2 && 2 * t + 1 < blocks) {
+                if (T::BLOCKS == 2 && blocks_of(t) == 2) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) mma_tmem_a(d, as + 32 + 8 * i, xd + (x_block >> 4) + 2 * i, id, 1);
                 }
@@ -290,12 +304,55 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
         const uint32_t to = a_cols + ((uint32_t)(warp % 4) << 21) + 32 * half;        // this warp's lanes of TMEM
         const Q4Matrix &w = mine ? p.up : p.w;
         const float f0 = power_of_two(-f / 2), f1 = power_of_two(-f - -f / 2);
+        bool gone = false;
+        // Weights of a step go to its slot once the products have read what was there
+        const auto give = [&](int t, const uint32_t (&v)[32]) {
+            const int slot = t & last_slot;
+            if (t > last_slot) {
+                warp_poll(&sm.a_empty[mine][slot], ((t >> l.slot_bits) - 1) & 1, abort);
+                tc_fence_after();
+            }
+            if (gone = __any_sync(0xffffffffu, *abort)) return;
+            tmem_st_row(to + SLOT_COLS * slot, v);         // (a block beyond the last is not multiplied)
+            tc_fence_before();
+            warp_arrive(&sm.a_full[mine][slot]);
+        };
         int wanted = 0;                         // of a chunk's scales, for this warp's blocks
 #pragma unroll
         for (int i = 0; i < 4 / T::BLOCKS; ++i)
-            if (T::TURNS == 1 || i % 2 == turn) wanted |= 1 << (T::BLOCKS * i + (GATED ? 0 : half)) * count / 4;
+            if (T::TURNS == 1 || (extra_steps + i) % 2 == turn) wanted |= 1 << (T::BLOCKS * i + (GATED ? 0 : half)) * count / 4;
         ChunkScales next = chunk_scales<OFFSETS>(w, row, groups, chunk0 * count, count, vector, wanted);
-        bool gone = false;
+        if constexpr (OFFSETS) {
+            for (int t = T::TURNS > 1 ? turn : 0; t < extra_steps && !gone; t += T::TURNS) {
+                const int first = group0 + (T::BLOCKS * t + (GATED ? 0 : half)) * kBlockGroups;
+                ChunkScales of[kBlockGroups / 4];           // four groups each; every lane's lie in another line, so few reads
+                if (groups % 8 == 0 && group0 % 8 == 0) {
+#pragma unroll
+                    for (int q = 0; q < kBlockGroups / 4; q += 2) {
+                        const bool there = first + 4 * q < groups;
+                        const uint4 zero = make_uint4(0, 0, 0, 0);
+                        const uint4 a = there ? *reinterpret_cast<const uint4 *>(w.scales + row * groups + first + 4 * q) : zero;
+                        const uint4 b = there ? *reinterpret_cast<const uint4 *>(w.offsets + row * groups + first + 4 * q) : zero;
+                        of[q] = {make_uint2(a.x, a.y), make_uint2(b.x, b.y)};
+                        of[q + 1] = {make_uint2(a.z, a.w), make_uint2(b.z, b.w)};
+                    }
+                } else {
+                    const bool fours = groups % 4 == 0 && group0 % 4 == 0;
+#pragma unroll
+                    for (int q = 0; q < kBlockGroups / 4; ++q) of[q] = chunk_scales<true>(w, row, groups, first + 4 * q, 4, fours);
+                }
+                uint32_t v[32];
+#pragma unroll
+                for (int q = 0; q < kBlockGroups; ++q) {
+                    const bool there = first + q < group_end;
+                    const float sc = nth_bf16(of[q / 4].s, q % 4) * f0 * f1, o = nth_bf16(of[q / 4].o, q % 4) * f0 * f1;
+                    const float both = there ? fmaf(8.f, sc, o) * (float)p.group : 0.f, hi = __half2float(__float2half_rn(both));
+                    v[2 * q] = f16_twice(hi);
+                    v[2 * q + 1] = f16_twice(both - hi);
+                }
+                give(t, v);
+            }
+        }
         int s = 0, phase = 0;
         for (int c = 0; c < chunks && !gone; ++c) {
             const ChunkScales cur = next;
@@ -304,36 +361,29 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
             const unsigned char *line = codes + (size_t)(s * MATS + mine) * kCodeBytes + r * 128;
 #pragma unroll
             for (int i = 0; i < 4 / T::BLOCKS; ++i) {
-                if (T::TURNS > 1 && i % 2 != turn) continue;
-                const int t = 4 / T::BLOCKS * c + i, j = T::BLOCKS * i + (GATED ? 0 : half), slot = t & last_slot;
+                const int t = extra_steps + 4 / T::BLOCKS * c + i, j = T::BLOCKS * i + (GATED ? 0 : half);
+                if (T::TURNS > 1 && t % 2 != turn) continue;
                 if (t >= steps) break;
                 uint32_t v[32];
                 {
                     const float sc = nth_bf16(cur.s, count == 4 ? j : j / 2) * f0 * f1;
-                    const float of = OFFSETS ? nth_bf16(cur.o, count == 4 ? j : j / 2) * f0 * f1 : -8.f * sc;
-                    const uint32_t s0 = f16_twice(sc * 16777216.f), s1 = f16_twice(sc * 1048576.f), o2 = f16_twice(of);
+                    const uint32_t s0 = f16_twice(sc * 1048576.f), o2 = f16_twice(-8.f * sc);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint4 q = *reinterpret_cast<const uint4 *>(line + (((2 * j + h) ^ (r & 7)) << 4));
                         const uint32_t words[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const uint32_t a = words[e], b = a >> 8;
-                            v[16 * h + 4 * e] = fma_f16x2(a & 0x000f000fu, s0, o2);
-                            v[16 * h + 4 * e + 1] = fma_f16x2(a & 0x00f000f0u, s1, o2);
-                            v[16 * h + 4 * e + 2] = fma_f16x2(b & 0x000f000fu, s0, o2);
-                            v[16 * h + 4 * e + 3] = fma_f16x2(b & 0x00f000f0u, s1, o2);
+                            const uint32_t a = words[e];
+                            v[16 * h + 4 * e + 0] = fma_f16x2((a << 4) & 0x00f000f0u, s0, o2);
+                            v[16 * h + 4 * e + 1] = fma_f16x2((a) & 0x00f000f0u, s0, o2);
+                            v[16 * h + 4 * e + 2] = fma_f16x2((a >> 4) & 0x00f000f0u, s0, o2);
+                            v[16 * h + 4 * e + 3] = fma_f16x2((a >> 8) & 0x00f000f0u, s0, o2);
                         }
                     }
                 }
-                if (t > last_slot) {
-                    warp_poll(&sm.a_empty[mine][slot], ((t >> l.slot_bits) - 1) & 1, abort);
-                    tc_fence_after();
-                }
-                if (gone = __any_sync(0xffffffffu, *abort)) break;
-                tmem_st_row(to + SLOT_COLS * slot, v);     // (a block beyond the inputs is not multiplied)
-                tc_fence_before();
-                warp_arrive(&sm.a_full[mine][slot]);
+                give(t, v);
+                if (gone) break;
             }
             if (!gone) warp_arrive(&sm.code_empty[s]);
             if (++s == l.code_stages) s = 0, phase ^= 1;
@@ -409,10 +459,11 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
     if (warp == WARPS + 2) tmem_dealloc(tmem, l.tmem_cols);
 }
 
-// Rows of x in fp16, scaled by 2^exponent, each 8 inputs in the order 0 4 1 5 2 6 3 7.  A CTA a row: its 256 threads hold 8192 inputs;
-// of longer rows they read the rest again.
+// Rows of x in fp16, scaled by 2^exponent, each 8 inputs in the order 0 4 1 5 2 6 3 7, and, where `means` is set, behind them two halves
+// twice for the mean of every group.  A CTA a row: its 256 threads hold 8192 inputs; of longer rows they read the rest again.
 constexpr int kScaleThreads = 256, kHeld = 4;
-__global__ void __launch_bounds__(kScaleThreads) scale_rows_kernel(const __grid_constant__ Q4Problem p, __half *__restrict__ out, int *__restrict__ exponents) {
+__global__ void __launch_bounds__(kScaleThreads) scale_rows_kernel(const __grid_constant__ Q4Problem p, __half *__restrict__ out, int pitch, bool means,
+                                                                   int *__restrict__ exponents) {
     __shared__ uint32_t tops[kScaleThreads / 32];
     grid_launch_dependents();
     const int m = blockIdx.x, tid = threadIdx.x, n = p.k / 8;
@@ -436,22 +487,34 @@ __global__ void __launch_bounds__(kScaleThreads) scale_rows_kernel(const __grid_
     const int e = (int)(top >> 23) - 127, s = top != 0 && e < 128 ? 14 - e : 0;
     const float f0 = power_of_two(s / 2), f1 = power_of_two(s - s / 2);
     if (tid == 0) exponents[m] = s;
-    uint4 *to = reinterpret_cast<uint4 *>(out + (size_t)m * p.k);
-    const auto write = [&](int i, const uint4 &v) {
+    uint4 *to = reinterpret_cast<uint4 *>(out + (size_t)m * pitch);
+    uint2 *mean_to = reinterpret_cast<uint2 *>(out + (size_t)m * pitch + p.k);
+    const int lanes = p.group / 8;                       // that have a group's inputs: 8 or 16, neighbours
+    const auto write = [&](int i, const uint4 &v) {      // (a whole warp, whose threads beyond the row have zeros)
         float f[8];
         unpack8(v, f);
         uint32_t h[4];
 #pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = f[k] * f0 * f1;
+#pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const __half2 v = __floats2half2_rn(f[k] * f0 * f1, f[k + 4] * f0 * f1);
+            const __half2 v = __floats2half2_rn(f[k], f[k + 4]);
             h[k] = *reinterpret_cast<const uint32_t *>(&v);
         }
-        to[i] = make_uint4(h[0], h[1], h[2], h[3]);
+        if (i < n) to[i] = make_uint4(h[0], h[1], h[2], h[3]);
+        if (!means) return;
+        float sum = ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+        for (int o = 1; o < lanes; o *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        sum *= lanes == 8 ? 1.f / 64 : 1.f / 128;
+        const __half hi = __float2half_rn(sum);
+        const __half2 both = __halves2half2(hi, __float2half_rn(sum - __half2float(hi)));
+        const uint32_t w = *reinterpret_cast<const uint32_t *>(&both);
+        if (i < n && i % lanes == 0) mean_to[i / lanes] = make_uint2(w, w);
     };
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-        if (tid + kScaleThreads * i < n) write(tid + kScaleThreads * i, held[i]);
-    for (int i = tid + kScaleThreads * kHeld; i < n; i += kScaleThreads) write(i, x[i]);
+    for (int i = 0; i < kHeld; ++i) write(tid + kScaleThreads * i, held[i]);
+    for (int first = kScaleThreads * kHeld; first < n; first += kScaleThreads)
+        write(first + tid, first + tid < n ? x[first + tid] : make_uint4(0, 0, 0, 0));
 }
 
 int round_up(int a, int b) { return (a + b - 1) / b * b; }
@@ -505,7 +568,7 @@ int clusters_at_once(int size) {
 //
 // CTAs of a cluster, and those that need more than half of TMEM, have an SM's shared memory for themselves: no CTA of a cluster
 // ever waits for columns of TMEM that are held by a CTA which in turn waits for another of that cluster.
-TcPlan plan_tc(int rows, int n_out, int k, bool gated) {
+TcPlan plan_tc(int rows, int n_out, int k, int group, bool offsets, bool gated) {
     const int mats = gated ? 2 : 1, most = gated ? 192 : 256, sms = multiprocessor_count();
     const int chunks = (k + kChunkIn - 1) / kChunkIn, fewest = (rows + most - 1) / most;
     TcPlan best{};
@@ -531,8 +594,9 @@ TcPlan plan_tc(int rows, int n_out, int k, bool gated) {
             l.pair = cluster == 1 && ctas > sms && l.tmem_cols <= 256 && fit_stages(l, mats, kTcSharedOfTwo);
             if (!l.pair && !fit_stages(l, mats, kTcShared)) continue;
             if (!l.pair && columns(2) <= 512) l.slot_bits = 2, l.tmem_cols = columns(2);
-            const double products = l.slice * 4.0 * mats * (2 * l.ntok + 44), rest = 9000 + 30.0 * l.ntok * mats + (cluster > 1 ? 2000 : 0);
-            const double one = max(products, l.slice * 4.0 * mats * 250) + rest;
+            const int blocks = 4 * l.slice + (offsets ? (l.slice * kChunkIn / group + kBlockGroups - 1) / kBlockGroups : 0);
+            const double products = blocks * mats * (2.0 * l.ntok + 44), rest = 9000 + 30.0 * l.ntok * mats + (cluster > 1 ? 2000 : 0);
+            const double one = max(products, blocks * mats * 250.0) + rest;
             const double time = l.pair ? ceil(ctas / (2 * sms)) * max(1.35 * one, 2 * products + rest)
                                        : ceil(ctas / (cluster > 1 ? cluster * clusters_at_once(cluster) : sms)) * one;
             if (time < least) least = time, best = l;
@@ -601,23 +665,29 @@ bool byte_map(CUtensorMap *m, const void *at, uint64_t rows, uint64_t row_bytes,
     return box_map(m, at, rows, row_bytes, pitch, 128, box_rows, true);
 }
 
-size_t q4_tc_workspace_bytes(int rows, int k) { return exponent_bytes(rows) + (size_t)rows * k * 2; }
+// A row of x as halves, with its groups' means.
+static int row_pitch(int k, int group) { return k + (kPerGroup * (k / group) + 7) / 8 * 8; }
+
+size_t q4_tc_workspace_bytes(int rows, int k, int group) { return exponent_bytes(rows) + (size_t)rows * row_pitch(k, group) * 2; }
 
 cudaError_t launch_q4_tc(const Q4Problem &p) {
     int *exponents = static_cast<int *>(p.workspace);
     __half *x16 = reinterpret_cast<__half *>(static_cast<uint8_t *>(p.workspace) + exponent_bytes(p.rows));
-    const TcPlan l = plan_tc(p.rows, p.n_out, p.k, p.gated);
+    const bool offsets = p.w.offsets != nullptr;
+    const int pitch = row_pitch(p.k, p.group), used = offsets ? p.k + kPerGroup * (p.k / p.group) : p.k;
+    const TcPlan l = plan_tc(p.rows, p.n_out, p.k, p.group, offsets, p.gated);
     CUtensorMap codes, up, x;
-    if (!byte_map(&codes, p.w.codes, p.n_out, p.k / 2, p.k / 2, kRowsA) || !byte_map(&x, x16, p.rows, (uint64_t)p.k * 2, (uint64_t)p.k * 2, l.ntok)) return cudaErrorInvalidValue;
+    if (!byte_map(&codes, p.w.codes, p.n_out, p.k / 2, p.k / 2, kRowsA) || !byte_map(&x, x16, p.rows, 2 * (uint64_t)used, 2 * (uint64_t)pitch, l.ntok))
+        return cudaErrorInvalidValue;
     if (!p.gated) up = codes;
     else if (!byte_map(&up, p.up.codes, p.n_out, p.k / 2, p.k / 2, kRowsA)) return cudaErrorInvalidValue;
-    scale_rows_kernel<<<(unsigned)p.rows, kScaleThreads, 0, p.stream>>>(p, x16, exponents);
+    scale_rows_kernel<<<(unsigned)p.rows, kScaleThreads, 0, p.stream>>>(p, x16, pitch, offsets, exponents);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     using Fn = cudaError_t (*)(const Q4Problem &, const TcPlan &, const CUtensorMap &, const CUtensorMap &, const CUtensorMap &, const int *);
     static const Fn fns[2][2][2] = {{{launch_tc<false, false, 16>, launch_tc<false, false, 8>}, {launch_tc<false, true, 16>, launch_tc<false, true, 8>}},
                                     {{launch_tc<true, false, 16>, launch_tc<true, false, 8>}, {launch_tc<true, true, 16>, launch_tc<true, true, 8>}}};
-    return fns[p.gated][p.w.offsets != nullptr][l.pair](p, l, codes, up, x, exponents);
+    return fns[p.gated][offsets][l.pair](p, l, codes, up, x, exponents);
 }
 
 }  // namespace gdn

@@ -602,9 +602,10 @@ GDN_API gdn_status gdn_ssm_scan(int n_seqs, int total_tokens, int channels, int 
  *
  * Products and sums are fp32; out is rounded once.  Calls that need no workspace take codes as they are into the products,
  * and scales and offsets meet the sums group by group; with one or two rows, a row of x loses what is below 2^-36 of its
- * largest.  Calls that need one may round the weights to fp16, by 2^-11 of themselves and 2^-19 of their row's largest
- * 15 |scale| + |offset| at most, and a row of x then loses what is below 2^-40 of its largest.  A row of x with an infinity or NaN
- * gives outputs that are not finite, and no other row does.
+ * largest.  Calls that need one take scale * (code - 8) into the products, exactly for scales down to 2^-15 of their row's
+ * largest 15 |scale| + |offset| (below that 2^-22 of it may be lost), and the rest of a group's weights to 2^-22; a row of x then
+ * loses what is below 2^-40 of its largest.  A row of x with an infinity or NaN gives outputs that are not finite, and no other row
+ * does.
  */
 GDN_API size_t gdn_q4_workspace_size(int rows, int n_out, int k, int group, int out_dtype, gdn_status *status);
 
