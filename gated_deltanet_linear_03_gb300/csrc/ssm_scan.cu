@@ -19,14 +19,22 @@ namespace gdn {
 namespace {
 
 constexpr int kScanThreads = 128;
-// log(1 + e^v) = max(v, 0) + log(1 + e), e = e^-|v|, without a branch and to a few units in the last place however small e is.
-// The exponential's argument is corrected for its rounding; log(1 + e) = 2 artanh(q) with q = e / (2 + e) <= 1/3, by a
+// The larger of v and 0; a NaN stays one.
+__device__ __forceinline__ float positive(float v) {
+    float r;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// log(1 + e^v) = max(v, 0) + log(1 + e), e = e^-|v|, without a branch and to a few units in the last place, down to e = 2^-126;
+// a smaller e is zero.  |v| counts as 104 at most, where e is zero: so nothing is infinite in between, and v = -inf, which masks a
+// token, or the lowest number gives 0.  The exponential's argument is corrected for its rounding; log(1 + e) = 2 artanh(q) with q = e / (2 + e) <= 1/3, by a
 // polynomial for artanh(q) / q in q^2 on [0, 1/9] whose largest relative error is least (Remez's exchange, 4e-9).
 __device__ __forceinline__ Pair softplus(Pair v) {
     const auto both = [](float x) { return pair(x, x); };
     float v0, v1, t0, t1;
     halves(v, v0, v1);
-    const Pair m = pair(-fabsf(v0), -fabsf(v1)), t = mul2(m, both(kLog2e));
+    const Pair m = pair(-fminf(fabsf(v0), 104.f), -fminf(fabsf(v1), 104.f)), t = mul2(m, both(kLog2e));
     const Pair r = fma2(m, both(1.925963033500e-8f), fma2(m, both(kLog2e), t ^ 0x8000000080000000ull));       // what t lacks of m log2 e
     halves(t, t0, t1);
     Pair e = pair(ex2(t0), ex2(t1));
@@ -37,7 +45,7 @@ __device__ __forceinline__ Pair softplus(Pair v) {
     s = fma2(q2, s, both(0.20012455f));
     s = fma2(q2, s, both(0.33333157f));
     s = fma2(q2, s, both(1.f));
-    return fma2(add2(q, q), s, pair(fmaxf(v0, 0.f), fmaxf(v1, 0.f)));
+    return fma2(add2(q, q), s, pair(positive(v0), positive(v1)));
 }
 
 template <int S>

@@ -1,0 +1,97 @@
+"""gdn_ssm_scan at the ends of its inputs' ranges: step widths of zero and without end, decays that leave fp32, and plans that only
+long or narrow inputs reach."""
+import pytest
+import torch
+
+import layer_helpers as ref
+from layer_helpers import BF, F32, i32
+from test_gpu_ssm_scan import JOINED, both, cu_of, inputs
+
+pytestmark = pytest.mark.gpu
+LOW, HIGH = torch.finfo(BF).min, torch.finfo(BF).max
+
+
+@pytest.fixture(scope="module")
+def ssm():
+    from gated_deltanet_linear_03_gb300 import ssm as s
+    return s
+
+
+def scan(ssm, i, lens, cu="given", **kw):
+    state = torch.full_like(i["past"], 7.0)
+    out = ssm.scan(i["x"], i["dt"], i["a"], i["b"], i["c"], cu_of(lens) if cu else None, d=i["d"], z=i["z"], dt_bias=i["bias"],
+                   state_in=i["past"], state_out=state, max_len=max(lens), out_dtype=F32, **kw)
+    return out, state
+
+
+# single tokens, one pass, pieces
+PLANS = [([1, 1, 1], None), ([45, 9, 1], "given"), ([1800, 700, 3], "given")]
+
+
+@pytest.mark.parametrize("lens,cu", PLANS)
+@pytest.mark.parametrize("low", [float("-inf"), LOW, -2.4e38, -1e30, -1000.0, -104.0, -100.0, -88.0])
+@pytest.mark.parametrize("where", ["dt", "bias"])
+def test_tokens_without_a_step(ssm, lens, cu, low, where):
+    """dt of -inf or the lowest number: a width of zero, which leaves the state as it is (a padded token)."""
+    i = inputs(lens, 64, 16, seed=21)
+    if where == "dt":
+        i["dt"][::3] = low
+    else:
+        i["bias"][::3] = low
+    both(ssm, i, lens, cu=cu)
+
+
+@pytest.mark.parametrize("lens,cu", PLANS)
+@pytest.mark.parametrize("n_state", [16, 128])
+def test_widths_as_large_as_numbers_are(ssm, lens, cu, n_state):
+    """dt of bf16's largest number: the width is that number, everything before is forgotten."""
+    i = inputs(lens, 32, n_state, seed=22)
+    i["a"].clamp_max_(-0.01)
+    for row in (0, 8, 17, 1000):
+        if row < sum(lens):
+            i["dt"][row], i["x"][row] = HIGH, (1e-37 * torch.randn(32, device="cuda")).to(BF)
+    both(ssm, i, lens, cu=cu)
+
+
+@pytest.mark.parametrize("lens,cu", PLANS)
+@pytest.mark.parametrize("what", ["dt", "bias", "x"])
+def test_nan_and_infinity_are_kept(ssm, lens, cu, what):
+    """A NaN (or a width of +inf) is seen in the outputs and the state of its channel, and in no other channel."""
+    i = inputs(lens, 32, 16, seed=23)
+    want, _ = scan(ssm, i, lens, cu)
+    for value in (float("nan"), float("inf")):
+        j = {k: v.clone() for k, v in i.items()}
+        if what == "bias":
+            j["bias"][5] = value
+        else:
+            j[what][0, 5] = value
+        out, state = scan(ssm, j, lens, cu)
+        assert not torch.isfinite(out[0, 5]) and not torch.isfinite(state[0, 5]).all() or lens[0] > 1
+        if value != value:
+            assert torch.isnan(out[:lens[0], 5]).all() and torch.isnan(state[0, 5]).all()
+        else:
+            assert not torch.isfinite(out[0, 5])
+        rest = [c for c in range(32) if c != 5]
+        assert torch.equal(out[:, rest], want[:, rest]) and torch.isfinite(state[:, rest]).all()
+
+
+@pytest.mark.parametrize("n_state,channels,groups,lens", [(16, 64, 4, [3000, 1, 900]), (64, 96, 2, [60, 2600, 300, 0, 7]), (128, 48, 3, [1500, 40]),
+                                                          (32, 1536, 4, [1, 1999, 3])])
+def test_groups_in_pieces(ssm, n_state, channels, groups, lens):
+    i = inputs(lens, channels, n_state, groups, seed=27)
+    both(ssm, i, lens)
+
+
+def test_a_narrow_long_sequence(ssm):
+    """More than a hundred pieces of one sequence, each of which begins with what all before it leave."""
+    both(ssm, inputs([12000], 128, 16, seed=28), [12000])
+
+
+def test_outputs_are_rounded_once_to_bf16(ssm):
+    lens = [500, 33]
+    i = inputs(lens, 64, 16, seed=30)
+    out, state = scan(ssm, i, lens)
+    kept = torch.empty_like(state)
+    half = ssm.scan(i["x"], i["dt"], i["a"], i["b"], i["c"], cu_of(lens), d=i["d"], z=i["z"], dt_bias=i["bias"], state_in=i["past"], state_out=kept,
+                    max_len=max(lens))
+    assert torch.equal(half, out.to(BF)) and torch.equal(kept, state)
