@@ -161,7 +161,6 @@ constexpr int kPromptWarps = 4, kPromptThreads = 32 * kPromptWarps;      // of a
 constexpr int kPromptCtas = 3;              // CTAs an SM
 constexpr int kMaxPiece = 2048;             // tokens of a piece of a scan in pieces
 constexpr int kTile = 8;                    // tokens of a turn
-constexpr int kStores = 8;
 
 template <int N_>
 struct Shape {
@@ -296,10 +295,6 @@ __device__ __forceinline__ void scan_tokens(const ScanProblem &p, typename SH::S
 #pragma unroll
                 for (int e = 0; e < VH / 2; ++e) d[e] = softplus(d[e]);
             }
-            if (t0 + i * kTile + my_t >= t1) {
-#pragma unroll
-                for (int e = 0; e < VH / 2; ++e) d[e] = 0;            // (a row beyond the end changes nothing)
-            }
             const int key = SH::du_key(my_t, chunk);
             if (32 == kTile * CHUNKS || my_t < kTile) {
                 float4 *to = &sh.du[my_t][SH::DU * chunk];
@@ -316,10 +311,7 @@ __device__ __forceinline__ void scan_tokens(const ScanProblem &p, typename SH::S
         const float *bv = &sh.b[0][8 * part], *cv = &sh.c[0][8 * part];
         const uint4 *bw = &sh.braw[slot][part], *cw = &sh.craw[slot][part];
         float2 *y = reinterpret_cast<float2 *>(&sh.y[0][y_chunk * SH::Y]) + lane % 2;
-        // y is stored once for several tokens: the next tokens' reads are not ordered behind it
-        float2 outs[kStores];
-#pragma unroll
-        for (int t = 0; t < kTile; ++t) {
+        const auto token = [&](int t, float2 &out) {
             const float4 q = sh.du[t][du_chunk * SH::DU + (entry % SH::DU ^ SH::du_key(t, du_chunk))];
             Pair decay[2][4], b[4], cc[4];
             if constexpr (SH::WIDE) {
@@ -348,7 +340,6 @@ __device__ __forceinline__ void scan_tokens(const ScanProblem &p, typename SH::S
                 }
                 if (!WITH_Y) width_sum[m] += wv;
             }
-            float2 &out = outs[t % kStores];
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 const float uv = m ? q.w : q.y;
@@ -365,12 +356,24 @@ __device__ __forceinline__ void scan_tokens(const ScanProblem &p, typename SH::S
                     (m ? out.y : out.x) = lo + hi;
                 }
             }
-            if (WITH_Y && t % kStores == kStores - 1) {
+        };
+        const auto store = [&](int t, const float2 &out) { y[2 * (t * 16 + (lane / 2 % SH::Y ^ SH::y_key(t, y_chunk)))] = out; };
+        const int left = t1 - (t0 + i * kTile);
+        if (left >= kTile) {
+            // y is stored once for all tokens: the next tokens' reads are not ordered behind it
+            float2 outs[kTile];
 #pragma unroll
-                for (int j = 0; j < kStores; ++j) {
-                    const int tt = t - (kStores - 1) + j;
-                    y[2 * (tt * 16 + (lane / 2 % SH::Y ^ SH::y_key(tt, y_chunk)))] = outs[j];
-                }
+            for (int t = 0; t < kTile; ++t) token(t, outs[t]);
+            if (WITH_Y) {
+#pragma unroll
+                for (int t = 0; t < kTile; ++t) store(t, outs[t]);
+            }
+        } else {                            // the last tile: no step may be taken for a row beyond the end (0 a is not 0 for every a)
+#pragma unroll 1
+            for (int t = 0; t < left; ++t) {
+                float2 out;
+                token(t, out);
+                if (WITH_Y) store(t, out);
             }
         }
         __syncwarp();

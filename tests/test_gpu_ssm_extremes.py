@@ -75,6 +75,19 @@ def test_nan_and_infinity_are_kept(ssm, lens, cu, what):
         assert torch.equal(out[:, rest], want[:, rest]) and torch.isfinite(state[:, rest]).all()
 
 
+@pytest.mark.parametrize("lens,cu", PLANS + [([41], "given"), ([8], "given"), ([1801], "given")])
+@pytest.mark.parametrize("n_state", [16, 64, 128])
+def test_a_decay_without_end(ssm, lens, cu, n_state):
+    """a = -inf forgets everything at every token, as a = -1e30 does, whatever the lengths."""
+    i = inputs(lens, 32, n_state, seed=24)
+    i["a"][::4, 1], i["a"][1::4] = -1e30, -1e30
+    want = scan(ssm, i, lens, cu)
+    i["a"][::4, 1], i["a"][1::4] = float("-inf"), float("-inf")
+    got = scan(ssm, i, lens, cu)
+    assert torch.isfinite(want[0]).all() and torch.isfinite(want[1]).all()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 @pytest.mark.parametrize("n_state,channels,groups,lens", [(16, 64, 4, [3000, 1, 900]), (64, 96, 2, [60, 2600, 300, 0, 7]), (128, 48, 3, [1500, 40]),
                                                           (32, 1536, 4, [1, 1999, 3])])
 def test_groups_in_pieces(ssm, n_state, channels, groups, lens):
