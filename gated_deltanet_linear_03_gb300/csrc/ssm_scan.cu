@@ -532,10 +532,15 @@ __global__ void __launch_bounds__(kPromptThreads, kPromptCtas) scan_kernel(const
                 const float2 w = live ? *reinterpret_cast<const float2 *>(plan.widths + (size_t)j * p.channels + c) : make_float2(0.f, 0.f);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
+                    // e^(a sum of widths) may leave fp32 where what a state becomes does not (and zero stays zero): by three
+                    // factors, none of which leaves it, as 2^378 makes infinity, and 2^-378 zero, of any number
                     float e0, e1;
                     const float wv = k < 4 ? w.x : w.y;
                     halves(mul2(pair(wv, wv), a[k / 4][k % 4]), e0, e1);
-                    h[k / 4][k % 4] = fma2(pair(ex2(e0), ex2(e1)), h[k / 4][k % 4], end[k / 4][k % 4]);
+                    const auto third = [](float e) { return ex2(fminf(fmaxf(e, -378.f), 378.f) * (1.f / 3)); };
+                    const Pair f = pair(third(e0), third(e1));
+                    Pair &v = h[k / 4][k % 4];
+                    v = add2(mul2(mul2(mul2(v, f), f), f), end[k / 4][k % 4]);
                 }
             }
         }

@@ -88,6 +88,40 @@ def test_a_decay_without_end(ssm, lens, cu, n_state):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_growth_behind_zeros_in_pieces(ssm):
+    """A state of zero stays zero however much a piece's tokens would have let it grow."""
+    lens, C = [3000], 64
+    i = inputs(lens, C, 16, seed=25)
+    i["a"] = torch.full_like(i["a"], 1.0)
+    i["past"].zero_()
+    i["dt"] = torch.full_like(i["dt"], 0.25)
+    i["x"][:2960] = 0
+    kw = dict(dt_softplus=False, d=i["d"], z=i["z"], max_len=3000, out_dtype=F32)
+    state = torch.empty_like(i["past"])
+    out = ssm.scan(i["x"], i["dt"], i["a"], i["b"], i["c"], cu_of(lens), state_in=i["past"], state_out=state, **kw)
+    y, e, h, he = ref.scan(i["x"], i["dt"], i["a"], i["b"], i["c"], lens, i["d"], i["z"], None, False, i["past"])
+    assert (out[:2960] == 0).all()
+    # no piece begins with a state but those of the last 40 tokens, which decay over 64 tokens at most (widths of 1/4: exact sums)
+    ref.check(out, y, e + 2.0 ** -19 * y.abs())
+    ref.check(state, h, he + 2.0 ** -19 * h.abs())
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_growth_and_decay_beyond_fp32_in_pieces(ssm, sign):
+    """From 1e-30 by e^120, which fp32 does not hold as a factor, to what it holds; and back."""
+    lens, C = [3000], 64
+    i = inputs(lens, C, 16, seed=26)
+    i["a"] = torch.full_like(i["a"], sign)
+    i["past"] = i["past"] * (1e-30 if sign > 0 else 1e22)
+    i["dt"] = torch.full_like(i["dt"], 0.0400390625)            # exact in bf16; sums of 3000 in fp32 are off by 2^-24 of 120 each at most
+    i["x"].zero_()
+    state = torch.empty_like(i["past"])
+    ssm.scan(i["x"], i["dt"], i["a"], i["b"], i["c"], cu_of(lens), state_in=i["past"], state_out=state, dt_softplus=False, max_len=3000)
+    h = i["past"].double() * torch.exp(torch.tensor(sign * 3000 * 0.0400390625, dtype=torch.float64))
+    # 3000 factors, each good to 2^-21 (its exponential and the product), or fewer by pieces whose exponents are rounded as often
+    assert ((state.double() - h).abs() <= 3000 * 2.0 ** -21 * h.abs()).all()
+
+
 @pytest.mark.parametrize("n_state,channels,groups,lens", [(16, 64, 4, [3000, 1, 900]), (64, 96, 2, [60, 2600, 300, 0, 7]), (128, 48, 3, [1500, 40]),
                                                           (32, 1536, 4, [1, 1999, 3])])
 def test_groups_in_pieces(ssm, n_state, channels, groups, lens):
