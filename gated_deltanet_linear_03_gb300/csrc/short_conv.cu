@@ -53,8 +53,8 @@ __global__ void __launch_bounds__(kConvThreads, kConvCtas) short_conv_kernel(con
         for (int n = first; n < min(first + kEmptyPerCta, p.seqs.n); ++n) {
             const int c0 = p.seqs.begin(n), slot = p.seqs.slot(n);
             if (p.seqs.end(n) > c0) continue;
-            if (slot >= 0) keep_state<W>(p, slot, c0, c0, c);
-            else raise_error(p.seqs.err, kErrInternal);
+            if (slot < 0) raise_error(p.seqs.err, kErrInternal);
+            else if (p.state_out && p.state_out != p.state_in) keep_state<W>(p, slot, c0, c0, c);
         }
         return;
     }
@@ -181,8 +181,9 @@ cudaError_t launch(const ConvProblem &p) {
     const int runs = max(1, kConvCtas * multiprocessor_count() / piece_ctas);
     const int length = many ? max(kRing, (p.seqs.total + runs - 1) / runs) : 1;
     const int tiles = (p.seqs.total + length - 1) / length;
-    // sequences without tokens have nobody who keeps their state, unless it stays where it is
-    const int empty = p.seqs.cu && p.state_out && p.state_out != p.state_in ? (p.seqs.n + kEmptyPerCta - 1) / kEmptyPerCta : 0;
+    // sequences without tokens have nobody who keeps their state, unless it stays where it is, or looks at their slot
+    const bool looked_at = (p.state_out && p.state_out != p.state_in) || p.seqs.slots;
+    const int empty = p.seqs.cu && looked_at ? (p.seqs.n + kEmptyPerCta - 1) / kEmptyPerCta : 0;
     const long ctas = (long)(tiles + empty) * piece_ctas;
     if (ctas == 0) return cudaSuccess;
     (many ? short_conv_kernel<W, kRing> : short_conv_kernel<W, 1>)<<<(unsigned)ctas, kConvThreads, 0, p.stream>>>(p, piece_ctas, tiles, length);

@@ -505,6 +505,7 @@ __global__ void __launch_bounds__(kPromptThreads, kPromptCtas) scan_kernel(const
                 if (lane == 0) raise_error(p.seqs.err, kErrInternal);
                 continue;
             }
+            if (!p.state_out || p.state_out == p.state_in) continue;
             load(state_in(slot), h);
             store(p.state_out + slot * all, h);
         }
@@ -598,7 +599,8 @@ cudaError_t launch(const ScanProblem &p) {
     s.ends = static_cast<float *>(p.workspace);
     s.begins = s.ends + states;
     s.widths = s.begins + states;
-    if (p.state_out && p.state_out != p.state_in) s.empty = (p.seqs.n + kEmptyPerWarp - 1) / kEmptyPerWarp;
+    // sequences without tokens have nobody who keeps their state, unless it stays where it is, or looks at their slot
+    if ((p.state_out && p.state_out != p.state_in) || p.seqs.slots) s.empty = (p.seqs.n + kEmptyPerWarp - 1) / kEmptyPerWarp;
     const cudaError_t e = run(scan_kernel<SH, kEnds>, s.pieces);
     return e != cudaSuccess ? e : run(scan_kernel<SH, kOutputs>, s.pieces + s.empty);
 }

@@ -134,6 +134,29 @@ def test_a_narrow_long_sequence(ssm):
     both(ssm, inputs([12000], 128, 16, seed=28), [12000])
 
 
+@pytest.mark.parametrize("lens", [[3, 0, 2], [0, 0, 0], [1200, 0, 900], [0, 5]])
+def test_a_slot_outside_the_pool_of_a_sequence_without_tokens(ssm, lens):
+    """Recorded like any other, also where states stay in place."""
+    from gated_deltanet_linear_03_gb300 import gdn
+    i = inputs(lens, 64, 16, seed=29)
+    n = len(lens)
+    slots = [k if lens[k] or k != lens.index(0) else n for k in range(n)]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w, conv = torch.randn(64, 4, generator=g, device="cuda"), torch.randn(n, 3, 64, generator=g, device="cuda").to(BF)
+    for in_place in (True, False):
+        assert gdn.device_error() == 0
+        state = i["past"].clone()
+        ssm.scan(i["x"], i["dt"], i["a"], i["b"], i["c"], cu_of(lens), state_in=state, state_out=state if in_place else state.clone(),
+                 slots=i32(slots), max_len=max(lens))
+        assert gdn.device_error() == 6
+        past = conv.clone()
+        ssm.short_conv(i["x"], w, cu_of(lens), state_in=past, state_out=past if in_place else past.clone(), slots=i32(slots))
+        assert gdn.device_error() == 6
+        if in_place:
+            rest = [k for k in range(n) if not lens[k]]
+            assert torch.equal(past[rest], conv[rest]) and torch.equal(state[rest], i["past"][rest])
+
+
 def test_outputs_are_rounded_once_to_bf16(ssm):
     lens = [500, 33]
     i = inputs(lens, 64, 16, seed=30)
