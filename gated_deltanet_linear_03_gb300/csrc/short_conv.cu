@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kConvThreads, kConvCtas) short_conv_kernel(con
         }
     }
     const int t0 = tile * length;
-    int t1 = min(t0 + length, p.seqs.total), begin = t0;
+    int t1 = t0 + min(length, p.seqs.total - t0), begin = t0;      // (t0 + length may pass 2^31)
     int n = p.seqs.of(t0), c0 = p.seqs.begin(n), c1 = p.seqs.end(n), slot = p.seqs.slot(n);
     if (p.seqs.cu) {
         // A sequence's first W - 1 tokens belong to the run that its first one lies in, which alone reads its state: this run leaves
