@@ -5,8 +5,7 @@
 //
 // The inner sums go to the tensor cores (mma.sync, 16 weight rows by 8 rows of x by 16 inputs): a code is an integer below 16,
 // exact in bf16, so the products are exact and the sums fp32, and scale and offset meet them once a group instead of once a
-// weight.  With outputs in bf16 and up to 16 rows the codes enter as 128 + c, which saves the subtraction and is taken back with the offset
-// (2^-16 of the sums' terms); otherwise as c.
+// weight.
 //
 // Codes and x come by TMA, stages of 16 w weight rows (w = 1, 2, 4 or 8) and all rows of x by 256 inputs, which one thread asks for
 // several stages ahead, across tiles: what reads memory is never waiting for what computes.  Eight warps compute, w along the rows by
@@ -39,7 +38,6 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
 }
 
 // The eight codes of a word as four bf16 pairs of neighbours.  Under the exponent of 128 a code is 128 + c exactly.
-template <bool EXACT>
 __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&v)[4]) {
     const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
     const uint32_t lo = __byte_perm(even, odd, 0x5140), hi = __byte_perm(even, odd, 0x7362);
@@ -47,10 +45,8 @@ __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&v)[4]) {
     v[1] = __byte_perm(lo, 0x43434343u, 0x4342);
     v[2] = __byte_perm(hi, 0x43434343u, 0x4140);
     v[3] = __byte_perm(hi, 0x43434343u, 0x4342);
-    if (EXACT) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) asm("sub.bf16x2 %0, %1, %2;" : "=r"(v[i]) : "r"(v[i]), "r"(0x43004300u));
-    }
+    for (int i = 0; i < 4; ++i) asm("sub.bf16x2 %0, %1, %2;" : "=r"(v[i]) : "r"(v[i]), "r"(0x43004300u));
 }
 
 struct FewPlan {
@@ -64,7 +60,7 @@ struct FewBars {
     int abort;
 };
 
-template <int NT, int FIT, bool GATED, bool OFFSETS, bool EXACT>
+template <int NT, int FIT, bool GATED, bool OFFSETS>
 __global__ void __launch_bounds__(kThreads, FIT)
 q4_few_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ FewPlan l, const __grid_constant__ CUtensorMap code_map,
               const __grid_constant__ CUtensorMap up_map, const __grid_constant__ CUtensorMap x_map, unsigned int *err) {
@@ -201,8 +197,8 @@ q4_few_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ FewPl
                     uint32_t v0[4], v1[4], a[4][4];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        code_pairs<EXACT>(h ? q0.y : q0.x, v0);
-                        code_pairs<EXACT>(h ? q1.y : q1.x, v1);
+                        code_pairs(h ? q0.y : q0.x, v0);
+                        code_pairs(h ? q1.y : q1.x, v1);
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             a[2 * h + i][0] = v0[2 * i];
@@ -213,9 +209,7 @@ q4_few_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ FewPl
                     }
                     const int which = count == 4 ? j : j / 2;
                     const float s0 = nth_bf16(cur0.s, which), s1 = nth_bf16(cur1.s, which);
-                    constexpr float BIAS = EXACT ? 0.f : 128.f;
-                    const float o0 = OFFSETS ? fmaf(-BIAS, s0, nth_bf16(cur0.o, which)) : -(BIAS + 8.f) * s0;
-                    const float o1 = OFFSETS ? fmaf(-BIAS, s1, nth_bf16(cur1.o, which)) : -(BIAS + 8.f) * s1;
+                    const float o0 = OFFSETS ? nth_bf16(cur0.o, which) : -8.f * s0, o1 = OFFSETS ? nth_bf16(cur1.o, which) : -8.f * s1;
                     const unsigned char *x = stage + l.codes_bytes + j * X_BOX + g * 128;
                     const float *xsum = sums + (s * 4 + j) * COLS + 2 * t;
 #pragma unroll
@@ -333,18 +327,16 @@ cudaError_t launch(const Q4Problem &p) {
     else if (!byte_map(&up, p.up.codes, p.n_out, p.k / 2, p.k / 2, box_rows)) return cudaErrorInvalidValue;
 
     using Fn = void (*)(const Q4Problem, const FewPlan, const CUtensorMap, const CUtensorMap, const CUtensorMap, unsigned int *);
-    constexpr bool ONLY = NT > 2;                    // more than 16 rows are mostly fp32 outputs: that form for both
-    static const Fn fns[2][2] = {{q4_few_kernel<NT, FIT, GATED, false, ONLY>, q4_few_kernel<NT, FIT, GATED, false, true>},
-                                 {q4_few_kernel<NT, FIT, GATED, true, ONLY>, q4_few_kernel<NT, FIT, GATED, true, true>}};
-    const int offsets = p.w.offsets != nullptr, exact = p.out_f32;
-    static std::atomic<bool> ready[kMaxDevices][2][2];
+    const int offsets = p.w.offsets != nullptr;
+    const Fn fn = offsets ? q4_few_kernel<NT, FIT, GATED, true> : q4_few_kernel<NT, FIT, GATED, false>;
+    static std::atomic<bool> ready[kMaxDevices][2];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev >= kMaxDevices || !ready[dev][offsets][exact].load(std::memory_order_relaxed)) {
-        e = cudaFuncSetAttribute(fns[offsets][exact], cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kShared);
+    if (dev >= kMaxDevices || !ready[dev][offsets].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kShared);
         if (e != cudaSuccess) return e;
-        if (dev < kMaxDevices) ready[dev][offsets][exact].store(true, std::memory_order_relaxed);
+        if (dev < kMaxDevices) ready[dev][offsets].store(true, std::memory_order_relaxed);
     }
     const long units = (long)l.row_tiles * l.m_blocks;
     cudaLaunchConfig_t cfg{};
@@ -358,7 +350,7 @@ cudaError_t launch(const Q4Problem &p) {
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = l.cluster > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, fns[offsets][exact], p, l, codes, up, x, error_word());
+    return cudaLaunchKernelEx(&cfg, fn, p, l, codes, up, x, error_word());
 }
 
 // A CTA takes 8, 16 or 32 rows of x.  With 32 rows two CTAs fit on an SM at 96 registers a thread instead of 168, which pays where there
