@@ -37,16 +37,20 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The eight codes of a word as four bf16 pairs of neighbours.  Under the exponent of 128 a code is 128 + c exactly.
+// The products enter their sums as 2^-10 of themselves, so that a group's sum of codes times x (below 2^10 of x's largest) and its sum
+// of x stay in range for every x; the outputs get it back.
+constexpr float kShrunk = 0x1p-10f, kGrown = 0x1p10f;
+
+// The eight codes of a word as four bf16 pairs of neighbours, times 2^-10.  Under the exponent of 2^-3 a code is 2^-3 + c 2^-10 exactly.
 __device__ __forceinline__ void code_pairs(uint32_t w, uint32_t (&v)[4]) {
     const uint32_t even = w & 0x0f0f0f0fu, odd = (w >> 4) & 0x0f0f0f0fu;
     const uint32_t lo = __byte_perm(even, odd, 0x5140), hi = __byte_perm(even, odd, 0x7362);
-    v[0] = __byte_perm(lo, 0x43434343u, 0x4140);
-    v[1] = __byte_perm(lo, 0x43434343u, 0x4342);
-    v[2] = __byte_perm(hi, 0x43434343u, 0x4140);
-    v[3] = __byte_perm(hi, 0x43434343u, 0x4342);
+    v[0] = __byte_perm(lo, 0x3e3e3e3eu, 0x4140);
+    v[1] = __byte_perm(lo, 0x3e3e3e3eu, 0x4342);
+    v[2] = __byte_perm(hi, 0x3e3e3e3eu, 0x4140);
+    v[3] = __byte_perm(hi, 0x3e3e3e3eu, 0x4342);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) asm("sub.bf16x2 %0, %1, %2;" : "=r"(v[i]) : "r"(v[i]), "r"(0x43004300u));
+    for (int i = 0; i < 4; ++i) asm("sub.bf16x2 %0, %1, %2;" : "=r"(v[i]) : "r"(v[i]), "r"(0x3e003e00u));
 }
 
 struct FewPlan {
@@ -99,6 +103,7 @@ q4_few_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ FewPl
     };
     const auto write = [&](int n0, int m0, int i, float y, float z) {
         const int n = n0 + (i & (out_rows - 1)), m = m0 + i / out_rows;
+        y *= kGrown, z *= kGrown;
         if (GATED) y = ffn_act(y, p.gelu) * z;
         if (n >= p.n_out) return;
         const size_t to = (size_t)m * p.n_out + n;
@@ -143,7 +148,10 @@ q4_few_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ FewPl
                     for (int q = 0; q < 8; ++q) {
                         float f[8];
                         unpack8(*reinterpret_cast<const uint4 *>(x + m * 128 + ((((q + 2 * j) & 7) ^ (m & 7)) << 4)), f);
-                        sum += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
+                        float a = f[0] * kShrunk, b = f[1] * kShrunk;
+#pragma unroll
+                        for (int e = 2; e < 8; e += 2) a = fmaf(f[e], kShrunk, a), b = fmaf(f[e + 1], kShrunk, b);
+                        sum += a + b;
                     }
                     sums[(s * 4 + j) * COLS + m] = sum;
                 }

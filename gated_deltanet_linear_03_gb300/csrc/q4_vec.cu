@@ -49,6 +49,10 @@ __device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
 }
 __device__ __forceinline__ float power_of_two(int e) { return __int_as_float((e + 127) << 23); }      // -126 .. 127
 
+// What a code of one is in the sums of products.  Codes as normal numbers get it with the scale: a sum of 64 of x's scaled numbers
+// times codes, 2^25 at most, by a scale would leave fp32 where scales are large.
+constexpr float kCodeUnit = 0x1p-24f;
+
 // Two codes of a word, of which MASK leaves their bits.
 template <bool EXACT>
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, uint32_t mask) {
@@ -175,7 +179,7 @@ q4_vec_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ VecMa
             }
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            xsum[m][i] = EXACT ? sum : sum * 5.9604644775390625e-8f;      // 2^-24, as the codes have it
+            xsum[m][i] = sum * kCodeUnit;
         }
     }
 
@@ -240,7 +244,7 @@ q4_vec_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ VecMa
 #pragma unroll
                     for (int m = 0; m < M; ++m) {
                         const float v = g & 1 ? d[m][2 * e + 1] : d[m][2 * e];
-                        acc[r + e][m] = fmaf(s, v, fmaf(o, xsum[m][i], acc[r + e][m]));
+                        acc[r + e][m] = fmaf(EXACT ? s * kCodeUnit : s, v, fmaf(o, xsum[m][i], acc[r + e][m]));
                     }
                 }
             }
@@ -290,7 +294,7 @@ q4_vec_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ VecMa
 #pragma unroll
         for (int m = 0; m < M; ++m) {
             // the scalings undone, by halves of one sign, so that nothing overflows in between that does not in the end
-            const int e = (EXACT ? 0 : 24) - exponent[m];
+            const int e = 24 - exponent[m];
             float y = v[m] * power_of_two(e / 2) * power_of_two(e - e / 2);
             int n = turn * OUT + r;
             if constexpr (GATED) {
