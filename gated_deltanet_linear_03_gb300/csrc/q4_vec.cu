@@ -8,12 +8,14 @@
 // of x all but one of a product's eight columns would be empty anyhow.  So no operand goes through shared memory, a weight costs
 // about 1.5 instructions, and scale and offset meet each group's sum in one lane of its four.
 //
-// Codes are halves as they lie in a word: a code in the low mantissa bits of a half is c 2^-24, in the next four 16 c 2^-24.
-// So a word's four pairs (i, i + 4) cost four ANDs and one shift.  The tensor cores multiply such subnormals exactly, but line up a
-// product by its exponents as if it began with a one, so that up to 10 of a sum's last bits are lost (3e-6 of the result).  For
-// fp32 outputs each pair is therefore put under the exponent of 1024, which is taken off again: c and 16 c as normal numbers.
-// x goes to fp16, its row scaled by a power of two to [2^14, 2^15), which keeps all bits of a bf16 number down to 2^-28 of the row's
-// largest (some down to 2^-36), with every other pair divided by 16; it is put into the pairs' order once.
+// Codes are halves almost as they lie in a word: a code in bits 4 to 7 of a half is c 2^-20, so a word's four pairs (i, i + 4) cost
+// four ANDs and three shifts.  The tensor cores multiply such subnormals exactly, but line up a product by its exponents as if it
+// began with a one, so that up to 6 of a sum's last bits are lost: no more than fp32 sums of another order differ by (12352 x 2048: of
+// the bf16 outputs 1.6e-4 are not the nearest to the exact ones, with fp32 outputs rounded as many; codes in bits 0 to 3 as
+// well save two shifts, but lose 10 bits: 1.9e-3).  For fp32 outputs each pair is put under the exponent of 1024, which is taken off
+// again: c and 16 c as normal numbers.  x goes to fp16, its row scaled by a power of two to [2^14, 2^15), which keeps all bits of a
+// bf16 number down to 2^-28 of the row's largest (some down to 2^-36), for fp32 outputs with every other pair divided by 16; it is
+// put into the pairs' order once.
 //
 // Measured (device times, weights from memory): 131071 x 2048 with offsets, one row, bf16 outputs 29.4 us, 5.2 TB/s, 0.76 of the copy
 // rate; fp32 outputs 38.4 us, where the subtractions make the issue slots (0.64 busy) the limit.  12352 x 2048 7.1 us, gated 2 x 5632 x
@@ -51,7 +53,8 @@ __device__ __forceinline__ float power_of_two(int e) { return __int_as_float((e 
 
 // What a code of one is in the sums of products.  Codes as normal numbers get it with the scale: a sum of 64 of x's scaled numbers
 // times codes, 2^25 at most, by a scale would leave fp32 where scales are large.
-constexpr float kCodeUnit = 0x1p-24f;
+template <bool EXACT>
+constexpr float kCodeUnit = EXACT ? 0x1p-24f : 0x1p-20f;
 
 // Two codes of a word, of which MASK leaves their bits.
 template <bool EXACT>
@@ -131,6 +134,7 @@ q4_vec_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ VecMa
     };
     for (int i = 0; i < kDeep; ++i) ask(i);
     // x at this lane's inputs as halves in the order of the codes' pairs, and its sum over the lane's group, both scaled
+    constexpr float ODD = EXACT ? 0.0625f : 1.f;            // pairs 1 and 3 of normal numbers are 16 times their codes
     uint32_t x[M][kSlices][8];
     float xsum[M][kSlices];
     int exponent[M];
@@ -173,13 +177,13 @@ q4_vec_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ VecMa
                 for (int q = 0; q < 8; ++q) f[q] = f[q] * f0 * f1;
                 sum += ((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7]));
                 x[m][i][4 * h] = f16_pair(f[0], f[4]);
-                x[m][i][4 * h + 1] = f16_pair(f[1] * 0.0625f, f[5] * 0.0625f);
+                x[m][i][4 * h + 1] = f16_pair(f[1] * ODD, f[5] * ODD);
                 x[m][i][4 * h + 2] = f16_pair(f[2], f[6]);
-                x[m][i][4 * h + 3] = f16_pair(f[3] * 0.0625f, f[7] * 0.0625f);
+                x[m][i][4 * h + 3] = f16_pair(f[3] * ODD, f[7] * ODD);
             }
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            xsum[m][i] = sum * kCodeUnit;
+            xsum[m][i] = sum * kCodeUnit<EXACT>;
         }
     }
 
@@ -225,9 +229,10 @@ q4_vec_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ VecMa
                 for (int h = 0; h < 2; ++h) {
                     const uint32_t a = h ? qa.y : qa.x, b = h ? qb.y : qb.x;
                     const uint32_t a8 = a >> 8, b8 = b >> 8;
-                    constexpr uint32_t LO = 0x000f000fu, HI = 0x00f000f0u;
-                    const uint32_t v[8] = {code_pair<EXACT>(a, LO), code_pair<EXACT>(b, LO), code_pair<EXACT>(a, HI), code_pair<EXACT>(b, HI),
-                                           code_pair<EXACT>(a8, LO), code_pair<EXACT>(b8, LO), code_pair<EXACT>(a8, HI), code_pair<EXACT>(b8, HI)};
+                    constexpr uint32_t HI = 0x00f000f0u, LO = EXACT ? 0x000f000fu : HI;
+                    const uint32_t a0 = EXACT ? a : a << 4, b0 = EXACT ? b : b << 4, a4 = EXACT ? a8 : a >> 4, b4 = EXACT ? b8 : b >> 4;
+                    const uint32_t v[8] = {code_pair<EXACT>(a0, LO), code_pair<EXACT>(b0, LO), code_pair<EXACT>(a, HI), code_pair<EXACT>(b, HI),
+                                           code_pair<EXACT>(a4, LO), code_pair<EXACT>(b4, LO), code_pair<EXACT>(a8, HI), code_pair<EXACT>(b8, HI)};
 #pragma unroll
                     for (int m = 0; m < M; ++m) {
                         const uint32_t *xm = &x[m][i][4 * h];
@@ -244,7 +249,7 @@ q4_vec_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ VecMa
 #pragma unroll
                     for (int m = 0; m < M; ++m) {
                         const float v = g & 1 ? d[m][2 * e + 1] : d[m][2 * e];
-                        acc[r + e][m] = fmaf(EXACT ? s * kCodeUnit : s, v, fmaf(o, xsum[m][i], acc[r + e][m]));
+                        acc[r + e][m] = fmaf(EXACT ? s * kCodeUnit<EXACT> : s, v, fmaf(o, xsum[m][i], acc[r + e][m]));
                     }
                 }
             }
@@ -294,7 +299,7 @@ q4_vec_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ VecMa
 #pragma unroll
         for (int m = 0; m < M; ++m) {
             // the scalings undone, by halves of one sign, so that nothing overflows in between that does not in the end
-            const int e = 24 - exponent[m];
+            const int e = (EXACT ? 24 : 20) - exponent[m];
             float y = v[m] * power_of_two(e / 2) * power_of_two(e - e / 2);
             int n = turn * OUT + r;
             if constexpr (GATED) {
