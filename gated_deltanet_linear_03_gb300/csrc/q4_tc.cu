@@ -149,7 +149,7 @@ __device__ __forceinline__ float largest(const Q4Matrix &w, size_t first, int gr
 template <bool GATED, bool OFFSETS, int WARPS>
 __global__ void __launch_bounds__(Tc<GATED, WARPS>::THREADS, WARPS == 8 ? 2 : 1)
 q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan l, const __grid_constant__ CUtensorMap code_map,
-             const __grid_constant__ CUtensorMap up_map, const __grid_constant__ CUtensorMap x_map, const int *__restrict__ x_exponents,
+             const __grid_constant__ CUtensorMap up_map, const __grid_constant__ CUtensorMap x_map, const int *x_exponents,
              unsigned int *err) {
     using T = Tc<GATED, WARPS>;
     constexpr int MATS = T::MATS;
@@ -390,7 +390,8 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
         }
         grid_dependency_wait();
         for (int m = tid; m < l.ntok; m += 32 * WARPS) {
-            const int e = m0 + m < p.rows ? -x_exponents[m0 + m] : 0;
+            // (the kernel before this one writes them while this one runs: no read-only load, none that may move before the wait)
+            const int e = m0 + m < p.rows ? -*const_cast<const volatile int *>(x_exponents + m0 + m) : 0;
             sm.undo[m] = make_float2(power_of_two(e / 2), power_of_two(e - e / 2));
         }
         asm volatile("barrier.sync 1, %0;" ::"n"(32 * WARPS) : "memory");
