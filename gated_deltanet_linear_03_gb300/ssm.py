@@ -120,11 +120,23 @@ def short_conv(x: torch.Tensor, weight: torch.Tensor, cu_seqlens: Optional[torch
     return out
 
 
-@functools.lru_cache(maxsize=4096)
 def scan_workspace_size(n_seqs: int, total_tokens: int, channels: int, n_state: int, groups: int, max_len: int = 0) -> int:
-    """Bytes of workspace that :func:`scan` needs for this problem (``gdn_ssm_scan_workspace_size``)."""
+    """Bytes of workspace that :func:`scan` needs for this problem on the current device
+    (``gdn_ssm_scan_workspace_size``), by whose multiprocessors the scan is divided."""
+    return _workspace_size(torch.cuda.current_device() if torch.cuda.is_available() else -1, n_seqs, total_tokens, channels, n_state,
+                           groups, max_len)
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_size(index: int, *sizes: int) -> int:
+    """:func:`scan_workspace_size` on CUDA device ``index`` (-1: there is none)."""
     st = ctypes.c_int(0)
-    need = load_library().gdn_ssm_scan_workspace_size(*map(_int32, (n_seqs, total_tokens, channels, n_state, groups, max_len)), st)
+    size = load_library().gdn_ssm_scan_workspace_size
+    if index < 0 or torch._C._cuda_getDevice() == index:
+        need = size(*map(_int32, sizes), st)
+    else:
+        with torch.cuda.device(index):
+            need = size(*map(_int32, sizes), st)
     if st.value != GDN_OK:
         raise GdnError(st.value, "gdn_ssm_scan_workspace_size")
     return int(need)
@@ -200,7 +212,7 @@ def scan(x: torch.Tensor, dt: torch.Tensor, a: torch.Tensor, b: torch.Tensor, c:
         n, cu, sl = _packing(cu_seqlens, slots, T, dev)
         max_len = min(_int32(max_len), T)
         if workspace is None:
-            ws_bytes = scan_workspace_size(n, T, channels, n_state, groups, max_len)
+            ws_bytes = _workspace_size(dev, n, T, channels, n_state, groups, max_len)
             if ws_bytes:
                 workspace = _empty(stream, ws_bytes, torch.uint8, x.device)
                 wsp = workspace.data_ptr()
