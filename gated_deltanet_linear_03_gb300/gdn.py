@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -117,16 +118,29 @@ def bind(path: str) -> ctypes.CDLL:
 _fast = None
 
 
+class _NoFastCalls:
+    """In the place of the C++ part where that is not built: takes no call, so that the modules' own code makes them all."""
+
+    @staticmethod
+    def _none(*args):
+        return None
+
+    short_conv = scan = q4_linear = q4_gated = _none
+
+
 def fast_calls():
     """The C++ part of the binding (csrc/fast_calls.cpp): the calls of :mod:`ssm` and :mod:`linear` with their checks, for the case
-    that nothing is wrong with them."""
+    that nothing is wrong with them.  Without it these calls cost three times as long on the host."""
     global _fast
     if _fast is None:
         lib = load_library()
         try:
             from . import _fast as module
         except ImportError as e:
-            raise RuntimeError("_fast.so not found; build it with `python -c 'import __graft_entry__ as g; g.build()'`") from e
+            warnings.warn(f"_fast.so cannot be loaded ({e}): calls take longer on the host; build it with "
+                          "`python -c 'import __graft_entry__ as g; g.build()'`", RuntimeWarning)
+            _fast = _NoFastCalls
+            return _fast
         module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
             lib.gdn_short_conv, lib.gdn_ssm_scan, lib.gdn_ssm_scan_workspace_size, lib.gdn_q4_linear, lib.gdn_q4_gated,
             lib.gdn_q4_workspace_size)), GdnError)
