@@ -8,9 +8,10 @@ when a source or header is newer than the library.
 the installed torch); g++ compiles it beside the kernels.
 
 ``build(debug=True)`` makes the bounds-checking variant ``libgdn_debug.so``
-(``-DGDN_DEBUG_BOUNDS``: every computed global address and tensor-copy
-coordinate is checked before use; see csrc/gdn_internal.cuh).  It has the same
-ABI and is built only on request.
+(``-DGDN_DEBUG_BOUNDS``: the recurrence's kernels, chunked.cu, scan.cu and
+decode.cu, check every computed global address and tensor-copy coordinate before
+use; see csrc/gdn_internal.cuh).  It has the same ABI and is built only on
+request.
 """
 from __future__ import annotations
 

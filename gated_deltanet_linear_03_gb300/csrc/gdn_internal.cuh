@@ -57,7 +57,8 @@ __device__ __forceinline__ void raise_error(unsigned int *err, unsigned int bit)
 }
 
 // Bounds-checking build (compiled with -DGDN_DEBUG_BOUNDS, as libgdn_debug.so): before every global access
-// whose address a kernel computes, and before every tensor-copy request, GDN_INB(last, extent, err) checks
+// whose address a kernel of the recurrence (chunked.cu, scan.cu, decode.cu) computes, and before every tensor-copy
+// request of theirs, GDN_INB(last, extent, err) checks
 // the highest element index the access touches against the extent of its buffer (in elements, or rows for a
 // tensor copy).  An access out of range is skipped and kErrBounds is recorded in the device error word; a
 // skipped tensor load leaves its barrier incomplete, so the kernel's bounded wait then ends it with
