@@ -13,8 +13,8 @@
 // CTAs of a cluster that share a tile's inputs (608 x 7424, 31 rows, fp32: 25.7 to 9.9 us).
 //
 // Bound by latencies, of barriers above all (a wait that finds its phase complete takes some 250 cycles, and a stage has three), not by
-// the codes: 12352 x 2048 with 3 rows 12.0 us, 1.2 TB/s; with 16 14.8.  fp32 outputs of many rows, which have to keep groups apart, pay
-// for every 32 rows again: 4096 x 4096 with 33 rows 23 us, 512 rows 105 (165 TFLOP/s); 131071 x 2048 with 33 rows 205.
+// the codes: 12352 x 2048 with 3 rows 12.7 us, 1.1 TB/s; with 16 and fp32 outputs 15.4.  fp32 outputs of many rows, which have to keep
+// groups apart, pay for every 32 rows again: 4096 x 4096 with 33 rows 21 us, 512 rows 109 (158 TFLOP/s); 131071 x 2048 with 33 rows 220.
 //
 // A fragment's order of inputs is free as long as both operands keep it: lane (g, t) takes inputs 16 t .. 16 t + 15 of a block of 64,
 // for weight rows g and g + 8 (of two matrices, rows g of each) and for row g of x: 8 bytes of codes and 32 bytes of x in a row.
@@ -362,8 +362,8 @@ cudaError_t launch(const Q4Problem &p) {
 }
 
 // A CTA takes 8, 16 or 32 rows of x.  With 32 rows two CTAs fit on an SM at 96 registers a thread instead of 168, which pays where there
-// is work for them: 4096 x 4096, 512 rows, 103 us instead of 142, 15540 x 3968, 143 rows, 141 instead of 185; but 24 rows 19.6 instead of
-// 17.4 and 12352 x 1344, 59 rows, 35.9 instead of 33.8.
+// is work for them: 4096 x 4096, 512 rows, 109 us instead of 154, 15540 x 3968, 143 rows, 155 instead of 176; but 12352 x 1344, 59 rows, 38.8
+// instead of 36.3, and 4096 x 4096, 24 rows, 12.5 and 12.3.
 template <bool GATED>
 cudaError_t by_rows(const Q4Problem &p) {
     if (p.rows > 16) return (long)p.rows * p.n_out >= 1l << 20 ? launch<4, 2, GATED>(p) : launch<4, 1, GATED>(p);
@@ -373,21 +373,21 @@ cudaError_t by_rows(const Q4Problem &p) {
 
 }  // namespace
 
-// bf16 outputs: the kernel that multiplies on tcgen05, whose weights are rounded to fp16, or the one above for small products.  The one
-// above unpacks for every 8 to 32 rows; the other takes 7 us for nothing.
+// bf16 outputs: the kernel that multiplies on tcgen05, or the one above for small products.  The one above unpacks for every 8 to 32
+// rows; the other takes 7 us for nothing.  With offsets in groups of 64:
 //     n_out x k        above                     on tcgen05
-//     300 x 512        3, 16 rows  3.9,  4.3 us   7.1,  7.2 us
-//     1000 x 8192                  7.5,  9.0     10.4, 10.7
-//     4096 x 4096                  7.9,  8.9     10.1, 10.7
-//     12000 x 4096                16.8, 21.7     20.4, 20.6
-//     12352 x 2048                12.4, 15.2     13.3, 13.5
-//     131071 x 2048               72.8, 93.9     62.2, 62.9
-//     2 x 14000 x 2048            25.5, 29.8     18.2, 18.7
-//     400 x 512        100 rows    5.4            7.4
-//     200 x 512        500 rows    6.3            8.9
-//     266 x 8192       67 rows     9.8           11.9
-//     1208 x 1984      318 rows   30.9           11.6
-//     1000 x 2048      64 rows    12.8            9.1
+//     300 x 512        3, 16 rows  3.9,  4.2 us   7.7,  8.0 us
+//     1000 x 8192                  7.7,  9.4     12.0, 12.4
+//     4096 x 4096                  8.0,  9.5     12.0, 12.6
+//     12000 x 4096                17.8, 22.8     24.7, 24.9
+//     12352 x 2048                12.7, 15.3     14.1, 14.3
+//     131071 x 2048               73.7, 95.2     66.0, 67.0
+//     2 x 14000 x 2048            25.9, 30.5     20.5, 21.1
+//     400 x 512        100 rows    5.9            8.3
+//     200 x 512        500 rows    6.7           10.2
+//     266 x 8192       67 rows    10.0           13.1
+//     1208 x 1984      318 rows   33.3           13.7
+//     1000 x 2048      64 rows    12.9           10.2
 static bool on_tcgen05(int rows, int n_out, int k, int matrices, int out_f32) {
     if (rows <= 2 || out_f32) return false;
     if (rows <= 16) return (double)n_out * matrices * k >= (rows > 8 ? 20e6 : 50e6);

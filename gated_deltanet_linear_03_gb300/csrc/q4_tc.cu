@@ -17,16 +17,18 @@
 //   W    by the row's largest 15 |scale| + |offset| at the CTA's inputs, which goes to [2^-2, 2^-1): first parts are exact for scales down to
 //        2^-15 of that, below lose 2^-22 of it at most.  A code c in bits 4 to 7 of a half is c 2^-20 (a subnormal, which the
 //        arithmetic takes as any other number), so a shift, an AND and one fused product-sum with (scale 2^20, -8 scale) make two
-//        weights.  Codes taken from bits 0 to 3 as well save three shifts in four pairs, but leave 2^-18 (131071 x 2048, 33 rows:
-//        74.5 us instead of 75); codes under the exponent of 1024 leave 2^-24 (84).
-// Sums are fp32; the powers of two are undone at the end.
+//        weights.  Codes taken from bits 0 to 3 as well save two shifts in four pairs, but leave 2^-18 (131071 x 2048, 33 rows, with
+//        caches flushed: 76 us instead of 77); codes under the exponent of 1024 leave 2^-24 (84).
+// Sums are fp32, in TMEM, where an addition cuts what does not fit: with 2048 inputs 6e-4 of the bf16 outputs are not the nearest to the
+// exact ones, twice as many as by sums that round.  The powers of two are undone at the end.
 //
 // CTAs of a cluster share the inputs of one tile and join through distributed shared memory, in a fixed order.
 //
 // Bound by the products for many rows (with x as second operand of N rows a product of 16 inputs takes N / 2 + 11 cycles, at least 41), by
 // a CTA's beginning and end for few: launch, scales and first codes 3 us, last barrier, join and outputs 3 us.  Measured on a GB300:
-// 4096 x 4096 with 33 rows 11.0 us, 128 rows 13.6, 512 rows 23.8 (720 TFLOP/s); 131071 x 2048 with 33 rows 66 us, 100 rows 78 (690); gated
-// 2 x 6000 x 2048 with 509 rows 27.8 us (900 TFLOP/s; tensor pipe 0.47 active over the whole time).
+// 4096 x 4096 without offsets, 33 rows 11.0 us, 128 rows 13.8, 512 rows 23.8 (720 TFLOP/s), with offsets in groups of 64 13.2, 16.1 and 29.7;
+// with offsets 131071 x 2048, 33 rows 71 us, 100 rows 84 (640); gated 2 x 6000 x 2048, 509 rows, 30.5 us (820 TFLOP/s; tensor pipe 0.46 active
+// over the whole time).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -553,7 +555,7 @@ bool fit_stages(TcPlan &l, int mats, size_t room) {
 }
 
 // Clusters of 2, 4 or 8 CTAs with an SM each that are on the GPU at once.  They lie within the GPU's processing clusters of SMs, some of
-// whose SMs are left over: those of 8 do not fit 19 times (759 x 7808, 122 rows, 29.5 us with 18 of them, 16.8 with fewer).
+// whose SMs are left over: those of 8 do not fit 19 times (759 x 7808, 122 rows, 26.1 us with 18 of them, 15.1 with fewer).
 int clusters_at_once(int size) {
     static std::atomic<int> known[kMaxDevices][9];
     int dev = 0, n = 0;
@@ -580,7 +582,7 @@ int clusters_at_once(int size) {
 }
 
 // The division that should be done first: waves of CTAs times a CTA's blocks, each as long as the product's or the unpacking's
-// part of it takes (cycles), and what a CTA takes besides.  Two CTAs on an SM take 1.35 times as long as one (97 to 65 us for 131071 x
+// part of it takes (cycles), and what a CTA takes besides.  Two CTAs on an SM take 1.35 times as long as one (97 to 71 us for 131071 x
 // 2048 and 33 rows of x), or as long as both their products.
 //
 // CTAs of a cluster, and those that need more than half of TMEM, have an SM's shared memory for themselves: no CTA of a cluster

@@ -17,9 +17,9 @@
 // bf16 number down to 2^-28 of the row's largest (some down to 2^-36), for fp32 outputs with every other pair divided by 16; it is
 // put into the pairs' order once.
 //
-// Measured (device times, weights from memory): 131071 x 2048 with offsets, one row, bf16 outputs 29.4 us, 5.2 TB/s, 0.76 of the copy
-// rate; fp32 outputs 38.4 us, where the subtractions make the issue slots (0.64 busy) the limit.  12352 x 2048 7.1 us, gated 2 x 5632 x
-// 2048 6.6: launch, the first loads' latency, and 1544 turns of 8 rows on 608 schedulers; the bytes alone are 2 us.
+// Measured (device times, weights from memory): 131071 x 2048 with offsets, one row, bf16 outputs 32.4 us, 4.7 TB/s, 0.69 of the copy
+// rate (29.8 with codes in bits 0 to 3); fp32 outputs 39.3 us, where the subtractions make the issue slots (0.63 busy) the limit.
+// 12352 x 2048 7.6 us, gated 2 x 5632 x 2048 7.1: launch, the first loads' latency, and 1544 turns of 8 rows on 608 schedulers; the bytes alone are 2 us.
 #include "layer_ops.cuh"
 #include "sm100.cuh"
 

@@ -9,9 +9,9 @@
 // are too few sequences and channels for the GPU, the tokens are cut into pieces, and a first pass carries only the states (at 2/3 of
 // the cost of a whole one) to the pieces' beginnings.
 //
-// Measured on a GB300, 4096 channels x 16 states: 64 sequences of 128 tokens 148 us in one pass, 0.39 of the exponentials' rate; 8192 tokens
-// of one sequence 256 us (107 for the ends, 153 for the outputs: issue slots 0.61 busy, exponentials 0.59 and 0.47; the bytes are 40 us).  7
-// sequences, 6465 tokens x 1536 channels x 64 states 246 us.  One token: 61 sequences x 4096 x 16 9.6 us, 3.6 TB/s; one sequence 2.3.
+// Measured on a GB300, 4096 channels x 16 states: 64 sequences of 128 tokens 155 us in one pass, 0.37 of the exponentials' rate; 8192 tokens
+// of one sequence 263 us (107 for the ends, 156 for the outputs: issue slots 0.63 and 0.59 busy, exponentials 0.58 and 0.45; the bytes are
+// 40 us).  7 sequences, 6465 tokens x 1536 channels x 64 states 251 us.  One token: 61 sequences x 4096 x 16 9.5 us, 3.6 TB/s; one sequence 2.1.
 #include "layer_ops.cuh"
 #include "sm100.cuh"
 
@@ -560,8 +560,8 @@ ScanPlan plan_scan(int n_seqs, int total, int channels, int groups, int max_len)
     const long warps = (long)s.warps_per_group * groups, at_once = (long)kPromptCtas * kPromptWarps * multiprocessor_count();
     const long longest = max_len > 0 && max_len < total ? max_len : total;
     // Tokens that one warp walks through, one after another: whole sequences, or pieces twice.  Measured, 4096 channels x 16 states,
-    // whole and in pieces: 16 x 512 tokens 176 and 211 us, 32 x 500 288 and 349, 4 x 2000 238 and 248, 1 x 100 14.5 and 17.7; but 1 x 600 72
-    // and 34, 1 x 8192 967 and 255; 7 x 60 .. 4000 of 1536 x 64 461 and 246
+    // whole and in pieces: 16 x 512 tokens 187 and 217 us, 32 x 500 301 and 360, 1 x 100 15.7 and 18.5; but 4 x 2000 263 and 254, 1 x 600
+    // 80 and 35, 1 x 8192 1065 and 263; 7 x 60 .. 4000 of 1536 x 64 464 and 251
     const long whole = max(longest, (long)total * warps / at_once);
     const long halves = 2 * max(64L, (long)total * warps / at_once);
     if (whole <= halves * 5 / 4) return s;

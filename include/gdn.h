@@ -602,7 +602,8 @@ GDN_API gdn_status gdn_ssm_scan(int n_seqs, int total_tokens, int channels, int 
  *
  * Products and sums are fp32; out is rounded once.  Calls that need no workspace take codes as they are into the products,
  * and scales and offsets meet the sums group by group; with one or two rows, a row of x loses what is below 2^-36 of its
- * largest.  Calls that need one take scale * (code - 8) into the products, exactly for scales down to 2^-15 of their row's
+ * largest, and with bf16 outputs besides a group's sum up to 6 of its last bits.  With three rows and more such a call's products
+ * of codes and x enter the sums as 2^-10 of themselves: what that takes below 2^-126 loses bits.  Calls that need a workspace take scale * (code - 8) into the products, exactly for scales down to 2^-15 of their row's
  * largest 15 |scale| + |offset| (below that 2^-22 of it may be lost), and the rest of a group's weights to 2^-22; a row of x then
  * loses what is below 2^-40 of its largest.  A row of x with an infinity or NaN gives outputs that are not finite, and no other row
  * does.
