@@ -393,10 +393,11 @@ q4_tc_kernel(const __grid_constant__ Q4Problem p, const __grid_constant__ TcPlan
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const uint32_t a = words[e];
-                            v[16 * h + 4 * e + 0] = fma_f16x2((a << 4) & 0x00f000f0u, s0, o2);
-                            v[16 * h + 4 * e + 1] = fma_f16x2((a) & 0x00f000f0u, s0, o2);
-                            v[16 * h + 4 * e + 2] = fma_f16x2((a >> 4) & 0x00f000f0u, s0, o2);
-                            v[16 * h + 4 * e + 3] = fma_f16x2((a >> 8) & 0x00f000f0u, s0, o2);
+                            constexpr uint32_t CODES = 0x00f000f0u;
+                            v[16 * h + 4 * e] = fma_f16x2(a << 4 & CODES, s0, o2);
+                            v[16 * h + 4 * e + 1] = fma_f16x2(a & CODES, s0, o2);
+                            v[16 * h + 4 * e + 2] = fma_f16x2(a >> 4 & CODES, s0, o2);
+                            v[16 * h + 4 * e + 3] = fma_f16x2(a >> 8 & CODES, s0, o2);
                         }
                     }
                 }

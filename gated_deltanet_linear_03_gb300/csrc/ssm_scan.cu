@@ -9,9 +9,9 @@
 // are too few sequences and channels for the GPU, the tokens are cut into pieces, and a first pass carries only the states (at 2/3 of
 // the cost of a whole one) to the pieces' beginnings.
 //
-// Measured on a GB300, 4096 channels x 16 states: 64 sequences of 128 tokens 155 us in one pass, 0.37 of the exponentials' rate; 8192 tokens
-// of one sequence 263 us (107 for the ends, 156 for the outputs: issue slots 0.63 and 0.59 busy, exponentials 0.58 and 0.45; the bytes are
-// 40 us).  7 sequences, 6465 tokens x 1536 channels x 64 states 251 us.  One token: 61 sequences x 4096 x 16 9.5 us, 3.6 TB/s; one sequence 2.1.
+// Measured on a GB300, 4096 channels x 16 states: 64 sequences of 128 tokens 152 us in one pass, 0.38 of the exponentials' rate; 8192 tokens
+// of one sequence 259 us (107 for the ends, 152 for the outputs: issue slots 0.63 and 0.61 busy, exponentials 0.58 and 0.46; the bytes are
+// 40 us).  7 sequences, 6465 tokens x 1536 channels x 64 states 247 us.  One token: 61 sequences x 4096 x 16 9.5 us, 3.6 TB/s; one sequence 2.1.
 #include "layer_ops.cuh"
 #include "sm100.cuh"
 
@@ -25,6 +25,10 @@ __device__ __forceinline__ float positive(float v) {
     asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(v));
     return r;
 }
+
+// a without infinities: the lowest number forgets as much at every step, and leaves the state as it is at a step of zero, which 0 a of
+// an infinite a does not.
+__device__ __forceinline__ float finite(float a) { return fabsf(a) == INFINITY ? copysignf(3.402823466e38f, a) : a; }
 
 // log(1 + e^v) = max(v, 0) + log(1 + e), e = e^-|v|, without a branch and to a few units in the last place, down to e = 2^-126;
 // a smaller e is zero.  |v| counts as 104 at most, where e is zero: so nothing is infinite in between, and v = -inf, which masks a
@@ -84,6 +88,8 @@ __global__ void __launch_bounds__(kScanThreads) step_kernel(const __grid_constan
         at[m] = (size_t)c[m] * N + 4 * part;
         bc[m] = c[m] / per_group * N + 4 * part;
         load4(p.a + at[m], a[m]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[m][i] = finite(a[m][i]);
         bias[m] = p.dt_bias ? __ldg(p.dt_bias + c[m]) : 0.f;
         skip[m] = p.skip ? __ldg(p.skip + c[m]) : 0.f;
     }
@@ -295,6 +301,10 @@ __device__ __forceinline__ void scan_tokens(const ScanProblem &p, typename SH::S
 #pragma unroll
                 for (int e = 0; e < VH / 2; ++e) d[e] = softplus(d[e]);
             }
+            if (t0 + i * kTile + my_t >= t1) {
+#pragma unroll
+                for (int e = 0; e < VH / 2; ++e) d[e] = 0;            // (a row beyond the end changes nothing)
+            }
             const int key = SH::du_key(my_t, chunk);
             if (32 == kTile * CHUNKS || my_t < kTile) {
                 float4 *to = &sh.du[my_t][SH::DU * chunk];
@@ -311,7 +321,11 @@ __device__ __forceinline__ void scan_tokens(const ScanProblem &p, typename SH::S
         const float *bv = &sh.b[0][8 * part], *cv = &sh.c[0][8 * part];
         const uint4 *bw = &sh.braw[slot][part], *cw = &sh.craw[slot][part];
         float2 *y = reinterpret_cast<float2 *>(&sh.y[0][y_chunk * SH::Y]) + lane % 2;
-        const auto token = [&](int t, float2 &out) {
+        // y is stored once for all tokens: the next tokens' reads are not ordered behind it
+        float2 outs[kTile];
+#pragma unroll
+        for (int t = 0; t < kTile; ++t) {
+            float2 &out = outs[t];
             const float4 q = sh.du[t][du_chunk * SH::DU + (entry % SH::DU ^ SH::du_key(t, du_chunk))];
             Pair decay[2][4], b[4], cc[4];
             if constexpr (SH::WIDE) {
@@ -356,25 +370,10 @@ __device__ __forceinline__ void scan_tokens(const ScanProblem &p, typename SH::S
                     (m ? out.y : out.x) = lo + hi;
                 }
             }
-        };
-        const auto store = [&](int t, const float2 &out) { y[2 * (t * 16 + (lane / 2 % SH::Y ^ SH::y_key(t, y_chunk)))] = out; };
-        const int left = t1 - (t0 + i * kTile);
-        if (left >= kTile) {
-            // y is stored once for all tokens: the next tokens' reads are not ordered behind it
-            float2 outs[kTile];
+        }
+        if (WITH_Y) {
 #pragma unroll
-            for (int t = 0; t < kTile; ++t) token(t, outs[t]);
-            if (WITH_Y) {
-#pragma unroll
-                for (int t = 0; t < kTile; ++t) store(t, outs[t]);
-            }
-        } else {                            // the last tile: no step may be taken for a row beyond the end (0 a is not 0 for every a)
-#pragma unroll 1
-            for (int t = 0; t < left; ++t) {
-                float2 out;
-                token(t, out);
-                if (WITH_Y) store(t, out);
-            }
+            for (int t = 0; t < kTile; ++t) y[2 * (t * 16 + (lane / 2 % SH::Y ^ SH::y_key(t, y_chunk)))] = outs[t];
         }
         __syncwarp();
         const int t = t0 + i * kTile + my_t;
@@ -470,6 +469,12 @@ __global__ void __launch_bounds__(kPromptThreads, kPromptCtas) scan_kernel(const
     };
     auto state_in = [&](int slot) { return p.state_in ? p.state_in + slot * all : nullptr; };
     load(p.a, a);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        float lo, hi;
+        halves(a[k / 4][k % 4], lo, hi);
+        a[k / 4][k % 4] = pair(finite(lo), finite(hi));
+    }
     float width_sum[2];
 
     if (PASS == kWhole) {
@@ -560,8 +565,8 @@ ScanPlan plan_scan(int n_seqs, int total, int channels, int groups, int max_len)
     const long warps = (long)s.warps_per_group * groups, at_once = (long)kPromptCtas * kPromptWarps * multiprocessor_count();
     const long longest = max_len > 0 && max_len < total ? max_len : total;
     // Tokens that one warp walks through, one after another: whole sequences, or pieces twice.  Measured, 4096 channels x 16 states,
-    // whole and in pieces: 16 x 512 tokens 187 and 217 us, 32 x 500 301 and 360, 1 x 100 15.7 and 18.5; but 4 x 2000 263 and 254, 1 x 600
-    // 80 and 35, 1 x 8192 1065 and 263; 7 x 60 .. 4000 of 1536 x 64 464 and 251
+    // whole and in pieces: 16 x 512 tokens 180 and 216 us, 32 x 500 293 and 355, 4 x 2000 244 and 253, 1 x 100 14.8 and 17.5; but 1 x 600
+    // 74 and 35, 1 x 8192 990 and 259; 7 x 60 .. 4000 of 1536 x 64 456 and 247
     const long whole = max(longest, (long)total * warps / at_once);
     const long halves = 2 * max(64L, (long)total * warps / at_once);
     if (whole <= halves * 5 / 4) return s;

@@ -562,7 +562,8 @@ GDN_API gdn_status gdn_short_conv(int n_seqs, int total_tokens, int channels, in
  *                      least channels); z may be NULL
  *   b, c               bf16 [T, groups, n_state], tokens b_stride, c_stride elements apart (multiples of 8, at least
  *                      groups * n_state)
- *   a                  fp32 [channels, n_state], usually negative
+ *   a                  fp32 [channels, n_state], usually negative.  An infinite one counts as the largest finite number of its
+ *                      sign: -inf forgets at every step but one of width zero
  *   dt_bias, skip      fp32 [channels], may be NULL
  *   dt_softplus        1 or 0
  *   state_in/out       fp32 [n_slots, channels, n_state]

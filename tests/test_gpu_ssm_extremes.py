@@ -88,6 +88,31 @@ def test_a_decay_without_end(ssm, lens, cu, n_state):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("lens,cu", PLANS)
+@pytest.mark.parametrize("low", [float("-inf"), LOW, -100.0])
+def test_a_decay_without_end_and_no_step(ssm, lens, cu, low):
+    """A token whose width is zero leaves the state as it is, for a = -inf too."""
+    i = inputs(lens, 32, 16, seed=31)
+    i["a"][:, 3] = -1e30
+    i["dt"][::2] = low
+    want = scan(ssm, i, lens, cu)
+    i["a"][:, 3] = float("-inf")
+    got = scan(ssm, i, lens, cu)
+    assert torch.isfinite(want[0]).all() and torch.isfinite(want[1]).all()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("lens,cu", PLANS)
+def test_a_that_is_not_a_number_is_seen(ssm, lens, cu):
+    i = inputs(lens, 32, 16, seed=32)
+    want = scan(ssm, i, lens, cu)
+    i["a"][7, 2] = float("nan")
+    got = scan(ssm, i, lens, cu)
+    rest = [c for c in range(32) if c != 7]
+    assert torch.isnan(got[0][:, 7]).all() and torch.isnan(got[1][:, 7, 2]).all()
+    assert torch.equal(got[0][:, rest], want[0][:, rest]) and torch.equal(got[1][:, rest], want[1][:, rest])
+
+
 def test_growth_behind_zeros_in_pieces(ssm):
     """A state of zero stays zero however much a piece's tokens would have let it grow."""
     lens, C = [3000], 64
